@@ -39,6 +39,19 @@ __global__ __launch_bounds__(256) void k_count_bad(const float* __restrict__ a, 
     if ((threadIdx.x & 63) == 0 && c) atomicAdd(out, c);
 }
 
+// Non-finite elements of a [rows x cols] matrix with leading dimension ld, one
+// workgroup per row at a time; the exponent mask fits the element type.
+template <class U>
+__global__ __launch_bounds__(256) void k_count_bad_rows(const U* __restrict__ a, int64_t rows, int64_t cols, int64_t ld,
+                                                        uint32_t emask, unsigned long long* __restrict__ out)
+{
+    unsigned long long c = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t j = threadIdx.x; j < cols; j += 256) c += ((uint32_t)a[r * ld + j] & emask) == emask ? 1ull : 0ull;
+    for (int off = 32; off > 0; off >>= 1) c += __shfl_xor(c, off);
+    if ((threadIdx.x & 63) == 0 && c) atomicAdd(out, c);
+}
+
 std::mutex g_mu;
 std::vector<unsigned long long*> g_addr;   // per device
 
@@ -65,6 +78,36 @@ bool values_check_on()
     return e != nullptr && std::strcmp(e, "1") == 0;
 }
 
+vq_status read_count(unsigned long long* cnt, bool sign_clear, const char* call, const char* what, hipStream_t st)
+{
+    unsigned long long bad = 0;
+    VQ_HIP(hipMemcpyAsync(&bad, cnt, sizeof(bad), hipMemcpyDeviceToHost, st));
+    VQ_HIP(hipStreamSynchronize(st));
+    if (bad)
+        return fail(VQ_ERR_INVALID, std::string(call) + ": VQ_CHECK: " + what + " holds " + std::to_string(bad) +
+                                        (sign_clear ? " non-finite or negative values" : " non-finite values"));
+    return VQ_OK;
+}
+
+vq_status check_matrix(const void* a, int64_t rows, int64_t cols, int64_t ld, int dtype, const char* call,
+                       const char* what, hipStream_t st)
+{
+    if (!values_check_on() || a == nullptr || rows <= 0 || cols <= 0) return VQ_OK;
+    unsigned long long* cnt = nullptr;
+    if (vq_status s = counter_address(&cnt); s != VQ_OK) return s;
+    hipLaunchKernelGGL(k_zero_u64, dim3(1), dim3(64), 0, st, cnt);
+    VQ_LAUNCHED("k_zero_u64");
+    const unsigned grid = (unsigned)std::min<int64_t>(rows, 4096);
+    if (dtype == VQ_F32)
+        hipLaunchKernelGGL(k_count_bad_rows<uint32_t>, dim3(grid), dim3(256), 0, st, static_cast<const uint32_t*>(a), rows,
+                           cols, ld, 0x7f800000u, cnt);
+    else
+        hipLaunchKernelGGL(k_count_bad_rows<uint16_t>, dim3(grid), dim3(256), 0, st, static_cast<const uint16_t*>(a), rows,
+                           cols, ld, dtype == VQ_BF16 ? 0x7f80u : 0x7c00u, cnt);
+    VQ_LAUNCHED("k_count_bad_rows");
+    return read_count(cnt, false, call, what, st);
+}
+
 vq_status check_values(const float* a, int64_t n, bool sign_clear, const char* call, const char* what,
                        hipStream_t st)
 {
@@ -76,13 +119,7 @@ vq_status check_values(const float* a, int64_t n, bool sign_clear, const char* c
     const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 4096);
     hipLaunchKernelGGL(k_count_bad, dim3(grid), dim3(256), 0, st, a, n, sign_clear ? 1 : 0, cnt);
     VQ_LAUNCHED("k_count_bad");
-    unsigned long long bad = 0;
-    VQ_HIP(hipMemcpyAsync(&bad, cnt, sizeof(bad), hipMemcpyDeviceToHost, st));
-    VQ_HIP(hipStreamSynchronize(st));
-    if (bad)
-        return fail(VQ_ERR_INVALID, std::string(call) + ": VQ_CHECK: " + what + " holds " + std::to_string(bad) +
-                                        (sign_clear ? " non-finite or negative values" : " non-finite values"));
-    return VQ_OK;
+    return read_count(cnt, sign_clear, call, what, st);
 }
 
 }  // namespace vq

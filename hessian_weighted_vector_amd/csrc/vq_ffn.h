@@ -1,0 +1,239 @@
+// Shared by the feed-forward kernels (dense products, few-token products,
+// products from the compressed form): 16-bit element types, activations and
+// the epilogue that every forward product ends in.  Not part of the ABI.
+#pragma once
+
+#include "vq_internal.h"
+
+namespace vq {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// 16-bit element types: storage E, vectors of four and eight, and the
+// 16 x 16 x 32 matrix instruction with float32 accumulation.  Stores round to
+// nearest even once, from float32.
+struct Bf16 {
+    typedef __bf16 E;
+    typedef __bf16 V4 __attribute__((ext_vector_type(4)));
+    typedef __bf16 V8 __attribute__((ext_vector_type(8)));
+    static __device__ inline f32x4 mfma(V8 a, V8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+    static __device__ inline V4 lds_tr(__attribute__((address_space(3))) V4* p) { return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(p); }
+};
+struct F16 {
+    typedef _Float16 E;
+    typedef _Float16 V4 __attribute__((ext_vector_type(4)));
+    typedef _Float16 V8 __attribute__((ext_vector_type(8)));
+    static __device__ inline f32x4 mfma(V8 a, V8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ inline V4 lds_tr(__attribute__((address_space(3))) V4* p)
+    {
+        typedef short S4 __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)p));
+    }
+};
+
+// ---- activations --------------------------------------------------------
+// Dense products: the result is rounded to 16 bits, so the exponential and the
+// reciprocal are the hardware's (a few float32 ulp).  The tanh form of GELU is
+// z * logistic(2 v), which needs no tanh and loses nothing for negative z.
+__device__ inline float logistic_fast(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kGeluC = 0.79788456080286536f;       // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// erfc(z / -sqrt 2) / 2 = the normal distribution function, without the
+// cancellation of 1 + erf in the lower tail.
+__device__ inline float normal_cdf(float z) { return 0.5f * erfcf(-kSqrtHalf * z); }
+
+// z * logistic, with the limit 0 where z is so negative that the logistic is 0.
+__device__ inline float act_fast(int act, float z)
+{
+    switch (act) {
+    case VQ_ACT_RELU: return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z);   // NaN stays NaN
+    case VQ_ACT_SILU: return z * logistic_fast(z);
+    case VQ_ACT_GELU: return z * normal_cdf(z);
+    case VQ_ACT_GELU_TANH: return z * logistic_fast(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    case VQ_ACT_SIGMOID: return logistic_fast(z);
+    default: return z;
+    }
+}
+
+// The same in full float32 accuracy (float32 results).
+__device__ inline float act_full(int act, float z)
+{
+    switch (act) {
+    case VQ_ACT_RELU: return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z);
+    case VQ_ACT_SILU: return z / (1.0f + expf(-z));
+    case VQ_ACT_GELU: return z * normal_cdf(z);
+    case VQ_ACT_GELU_TANH: return z / (1.0f + expf(-2.0f * kGeluC * (z + kGeluA * z * z * z)));
+    case VQ_ACT_SIGMOID: return 1.0f / (1.0f + expf(-z));
+    default: return z;
+    }
+}
+
+// act(z) and act'(z).  ReLU's derivative at 0 is 0.
+__device__ inline void act_grad(int act, float z, float& a, float& da)
+{
+    switch (act) {
+    case VQ_ACT_RELU: a = z > 0.0f ? z : 0.0f; da = z > 0.0f ? 1.0f : 0.0f; break;
+    case VQ_ACT_SILU: {
+        const float s = logistic_fast(z);
+        a = z * s;
+        da = s * (1.0f + z * (1.0f - s));
+        break;
+    }
+    case VQ_ACT_GELU: {
+        const float c = normal_cdf(z);
+        a = z * c;
+        da = c + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+        break;
+    }
+    case VQ_ACT_GELU_TANH: {
+        const float s = logistic_fast(2.0f * kGeluC * (z + kGeluA * z * z * z));
+        a = z * s;
+        // (1 - s) is 0 long before z^2 reaches the bound, which keeps 0 * inf away
+        da = s + z * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * fminf(z * z, 1e6f));
+        break;
+    }
+    case VQ_ACT_SIGMOID: {
+        const float s = logistic_fast(z);
+        a = s;
+        da = s * (1.0f - s);
+        break;
+    }
+    default: a = z; da = 1.0f;
+    }
+}
+
+// ---- epilogue -----------------------------------------------------------
+// Output element (token t, feature m) from float32 sums:
+//   one product:  Z = s + bias, Y = act(Z) + R
+//   gated pair:   G = s0 + bias0, U = s1 + bias1, Y = act(G) * U
+// Z (or G and U) are also stored where the caller keeps them.  Each stored
+// value is rounded once, from float32; the activation reads the unrounded sums.
+struct Epilogue {
+    int act;
+    int vec;                 // every row can be read and written eight features at a time
+    const void* bias[2];     // nullable
+    const void* R;           // nullable
+    void* Y;
+    void* Z[2];              // nullable
+    int64_t ldr, ldy, ldz;
+};
+
+// Reads or writes features m .. m+7 of row t (those below M), as one 16-byte
+// access where `vec` allows.
+template <class T>
+__device__ inline void store8(void* base, int64_t ld, int64_t t, int m, int M, bool vec, const float (&v)[8])
+{
+    typename T::E* o = static_cast<typename T::E*>(base) + t * ld + m;
+    if (vec && m + 8 <= M) {
+        typename T::V8 w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = (typename T::E)v[i];
+        *reinterpret_cast<typename T::V8*>(o) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (m + i < M) o[i] = (typename T::E)v[i];
+    }
+}
+
+template <class T>
+__device__ inline void load8(const void* base, int64_t ld, int64_t t, int m, int M, bool vec, float (&v)[8])
+{
+    const typename T::E* p = static_cast<const typename T::E*>(base) + t * ld + m;
+    if (vec && m + 8 <= M) {
+        const typename T::V8 w = *reinterpret_cast<const typename T::V8*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = m + i < M ? (float)p[i] : 0.0f;
+    }
+}
+
+// Features m .. m+7 of token t (those below M).
+template <class T>
+__device__ inline void epilogue_one(const Epilogue& e, int64_t t, int m, int M, float (&z)[8])
+{
+    const bool vec = e.vec;
+    if (e.bias[0]) {
+        float b[8];
+        load8<T>(e.bias[0], 0, 0, m, M, vec, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += b[i];
+    }
+    if (e.Z[0]) store8<T>(e.Z[0], e.ldz, t, m, M, vec, z);
+    if (e.act != VQ_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = act_fast(e.act, z[i]);
+    }
+    if (e.R) {
+        float r[8];
+        load8<T>(e.R, e.ldr, t, m, M, vec, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += r[i];
+    }
+    store8<T>(e.Y, e.ldy, t, m, M, vec, z);
+}
+
+template <class T>
+__device__ inline void epilogue_pair(const Epilogue& e, int64_t t, int m, int M, float (&g)[8], float (&u)[8])
+{
+    const bool vec = e.vec;
+    float b[8];
+    if (e.bias[0]) {
+        load8<T>(e.bias[0], 0, 0, m, M, vec, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] += b[i];
+    }
+    if (e.bias[1]) {
+        load8<T>(e.bias[1], 0, 0, m, M, vec, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += b[i];
+    }
+    if (e.Z[0]) {
+        store8<T>(e.Z[0], e.ldz, t, m, M, vec, g);
+        store8<T>(e.Z[1], e.ldz, t, m, M, vec, u);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = act_fast(e.act, g[i]) * u[i];
+    store8<T>(e.Y, e.ldy, t, m, M, vec, g);
+}
+
+// Whether rows at p with leading dimension ld can be accessed 16 bytes at a time.
+inline bool vec8_ok(const void* p, int64_t ld) { return p == nullptr || (aligned16(p) && ld % 8 == 0); }
+
+// ---- the tiled product --------------------------------------------------
+// out[q, p] = sum over segments and k of P[p, k] Q[q, k] (p contiguous in the
+// output).  An operand is k-contiguous (element (r, k) at r * ld + k) or
+// k-strided (element (r, k) at k * ld + r).  Operands that reach the kernel
+// have 16-byte aligned rows (base, ld) and a multiple of eight elements along
+// their contiguous axis.
+enum GemmKind {
+    GEMM_LINEAR,    // both k-contiguous; linear epilogue
+    GEMM_GATED,     // both k-contiguous; P is a pair, gated epilogue
+    GEMM_DX,        // P k-strided, Q k-contiguous; two segments where gated
+    GEMM_DW         // both k-strided; two outputs (Q[0], Q[1]) where gated
+};
+
+struct GemmArgs {
+    GemmKind kind;
+    int dtype;
+    int np, nq;                 // features (of each matrix of a pair), output rows
+    int nseg, nbatch;           // segments summed; outputs in one launch
+    int64_t kP, kQ;             // valid k of each operand (kP = kQ up to zero padding)
+    const void* P[2];
+    const void* Q[2];
+    int64_t ldp, ldq;
+    int wp, wq;                 // valid elements along a k-strided operand's rows
+    Epilogue epi;
+    void* Y2;                   // second output (nbatch = 2)
+};
+
+size_t gemm_workspace(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int nbatch);
+vq_status gemm_launch(const GemmArgs& a, void* ws, size_t ws_bytes, hipStream_t st);
+
+}  // namespace vq

@@ -1,0 +1,531 @@
+// The dense feed-forward calls: the product with bias, activation and residual
+// (vq_linear), the gated pair of projections (vq_gated), and their backward
+// passes.  The products run in vq_gemm.hip; here are the elementwise kernels
+// around them and the entry points.
+//
+//   k_pack        a copy with 16-byte aligned rows, zero padded to a multiple
+//                 of eight, for operands that are not (odd sizes, odd strides)
+//   k_grad        dZ = dY act'(Z), or dG = dH U act'(G) and dU = dH act(G), and
+//                 the bias gradients' partial column sums, in one pass
+//   k_bias_sum    the bias gradients from the partial sums, in a fixed order
+//   k_zero_rows   gradients of zero tokens
+//
+// The gradients of the pre-activations are rounded to the tensors' 16-bit type
+// once, since the matrix cores read them in it: one rounding of 2^-9 (bf16) or
+// 2^-12 (fp16) per product term, independent over the sum.  The bias gradients
+// are summed from the unrounded values.
+#include "vq_ffn.h"
+
+#include <algorithm>
+
+namespace vq {
+namespace {
+
+constexpr int64_t kMaxLd = 1 << 21;      // tile offsets stay below 2^31 bytes
+constexpr int64_t kMaxSize = 1 << 20;    // M and N
+constexpr int64_t kMaxTokens = 1 << 28;
+
+// Hands out workspace slices; with no base it only counts.  Every call counts
+// first and compares with the caller's bytes.
+struct Arena {
+    char* base;
+    size_t used = 0;
+    void* take(size_t bytes)
+    {
+        char* p = base + used;
+        used += align_up(bytes);
+        return base ? p : nullptr;
+    }
+};
+
+inline int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+// Whether the tiled product's 16-byte loads can read the matrix as it is.
+bool loads_ok(const Mat& m) { return aligned16(m.p) && m.ld % 8 == 0 && m.cols % 8 == 0 && m.ld <= kMaxLd; }
+
+__global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ s, int64_t rows, int cols, int64_t ld,
+                                              int64_t ldp, uint16_t* __restrict__ o)
+{
+    const int64_t per = ldp / 8;
+    const int64_t n = rows * per;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+        const int64_t r = e / per;
+        const int c = (int)(e - r * per) * 8;
+        const uint16_t* p = s + r * ld + c;
+        alignas(16) uint16_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i] : (uint16_t)0;
+        *reinterpret_cast<uint4*>(o + r * ldp + c) = *reinterpret_cast<const uint4*>(v);
+    }
+}
+
+__global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int64_t rows, int64_t cols, int64_t ld)
+{
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < rows * cols; e += (int64_t)gridDim.x * 256)
+        o[e / cols * ld + e % cols] = 0;
+}
+
+// A wave takes 8 rows of 512 columns (eight a lane), a workgroup 32 rows; the
+// four waves' column sums join in LDS.  GATED: D0 = dG, D1 = dU.  D0 may be
+// null (bias gradient alone).  D0 and D1 have zero-padded rows of ldd.
+constexpr int kGradRows = 32;
+template <class T, bool GATED>
+__global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const void* dY, int64_t ldy, const void* Z0,
+                                              const void* Z1, int64_t ldz, bool vec, typename T::E* D0,
+                                              typename T::E* D1, int64_t ldd, float* part0, float* part1)
+{
+    __shared__ float sums[GATED ? 2 : 1][4][512];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int m = blockIdx.x * 512 + lane * 8;
+    const int64_t t0 = (int64_t)blockIdx.y * kGradRows + wave * (kGradRows / 4);
+    float c0[8] = {}, c1[8] = {};
+    if (m < M) {
+#pragma unroll 2
+        for (int r = 0; r < kGradRows / 4; ++r) {
+            const int64_t t = t0 + r;
+            if (t >= nt) break;
+            float dy[8], z[8], u[8];
+            load8<T>(dY, ldy, t, m, M, vec, dy);
+            if (GATED || act != VQ_ACT_NONE) load8<T>(Z0, ldz, t, m, M, vec, z);
+            if (GATED) load8<T>(Z1, ldz, t, m, M, vec, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float a, da;
+                if (GATED) {
+                    act_grad(act, z[i], a, da);
+                    z[i] = dy[i] * u[i] * da;
+                    u[i] = dy[i] * a;
+                    c1[i] += u[i];
+                } else if (act != VQ_ACT_NONE) {
+                    act_grad(act, z[i], a, da);
+                    z[i] = dy[i] * da;
+                } else {
+                    z[i] = dy[i];
+                }
+                c0[i] += z[i];
+            }
+            // columns past M (loaded as zero) give zeros: the padding
+            if (D0) store8<T>(D0, ldd, t, m, (int)ldd, true, z);
+            if (GATED) store8<T>(D1, ldd, t, m, (int)ldd, true, u);
+        }
+    }
+    if (!part0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        sums[0][wave][lane * 8 + i] = c0[i];
+        if (GATED) sums[GATED ? 1 : 0][wave][lane * 8 + i] = c1[i];
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < 512; k += 256) {
+        const int col = blockIdx.x * 512 + k;
+        if (col >= M) break;
+        part0[(int64_t)blockIdx.y * M + col] = sums[0][0][k] + sums[0][1][k] + sums[0][2][k] + sums[0][3][k];
+        if (GATED) {
+            constexpr int b = GATED ? 1 : 0;
+            part1[(int64_t)blockIdx.y * M + col] = sums[b][0][k] + sums[b][1][k] + sums[b][2][k] + sums[b][3][k];
+        }
+    }
+}
+
+// db = sum of `n` partial rows: 16 columns and 16 row slices a workgroup, the
+// slices added in order.
+template <class T>
+__global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part0, const float* __restrict__ part1,
+                                                  int64_t n, int M, typename T::E* db0, typename T::E* db1)
+{
+    __shared__ float sh[16][17];
+    const float* part = blockIdx.y ? part1 : part0;
+    typename T::E* db = blockIdx.y ? db1 : db0;
+    if (db == nullptr) return;
+    const int c = threadIdx.x & 15, sl = threadIdx.x >> 4;
+    const int m = blockIdx.x * 16 + c;
+    float s = 0.0f;
+    if (m < M)
+        for (int64_t r = sl; r < n; r += 16) s += part[r * M + m];
+    sh[sl][c] = s;
+    __syncthreads();
+    if (sl == 0 && m < M) {
+        for (int k = 1; k < 16; ++k) s += sh[k][c];
+        db[m] = (typename T::E)s;
+    }
+}
+
+// A packed copy in the workspace takes the matrix's place.  run = false only counts.
+vq_status pack(Mat& m, Arena& ws, bool run, hipStream_t st)
+{
+    const int64_t ldp = round8(m.cols);
+    void* o = ws.take((size_t)m.rows * ldp * 2);
+    if (run) {
+        hipLaunchKernelGGL(k_pack, dim3((unsigned)std::min<int64_t>((m.rows * (ldp / 8) + 255) / 256, 65536)), dim3(256), 0,
+                           st, static_cast<const uint16_t*>(m.p), m.rows, (int)m.cols, m.ld, ldp,
+                           static_cast<uint16_t*>(o));
+        VQ_LAUNCHED("k_pack");
+        m.p = o;
+    }
+    m.ld = ldp;
+    m.cols = ldp;
+    return VQ_OK;
+}
+
+vq_status zero_matrix(void* o, int64_t rows, int64_t cols, int64_t ld, hipStream_t st)
+{
+    if (!o || rows * cols == 0) return VQ_OK;
+    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)std::min<int64_t>((rows * cols + 255) / 256, 65536)), dim3(256), 0, st,
+                       static_cast<uint16_t*>(o), rows, cols, ld);
+    VQ_LAUNCHED("k_zero_rows");
+    return VQ_OK;
+}
+
+// Forward product(s): nm = 1 (linear) or 2 (gated).
+struct Forward {
+    int64_t T, M, N;
+    int dtype, nm;
+    const void* X; int64_t ldx;
+    const void* W[2]; int64_t ldw;
+    Epilogue epi;
+};
+
+vq_status forward(const Forward& f, Arena& ws, bool run, hipStream_t st)
+{
+    if (f.T == 0) return VQ_OK;
+    Mat x{f.X, f.T, f.N, f.ldx};
+    Mat w[2] = {{f.W[0], f.M, f.N, f.ldw}, {f.W[1], f.M, f.N, f.ldw}};
+    if (!loads_ok(x)) VQ_TRY(pack(x, ws, run, st));
+    // a pair shares one leading dimension: both are packed or neither
+    if (!loads_ok(w[0]) || (f.nm > 1 && !loads_ok(w[1])))
+        for (int i = 0; i < f.nm; ++i) VQ_TRY(pack(w[i], ws, run, st));
+    GemmArgs g{};
+    g.kind = f.nm > 1 ? GEMM_GATED : GEMM_LINEAR;
+    g.dtype = f.dtype;
+    g.np = (int)f.M; g.nq = (int)f.T;
+    g.nseg = 1; g.nbatch = 1;
+    g.kP = w[0].cols; g.kQ = x.cols;
+    for (int i = 0; i < f.nm; ++i) { g.P[i] = w[i].p; }
+    g.Q[0] = x.p;
+    g.ldp = w[0].ld; g.ldq = x.ld;
+    g.epi = f.epi;
+    const size_t gb = gemm_workspace(g.kind, g.np, g.nq, f.N, 1, 1);
+    void* gw = ws.take(gb);
+    return run ? gemm_launch(g, gw, gb, st) : VQ_OK;
+}
+
+struct Backward {
+    int64_t T, M, N;
+    int dtype, act, nm;
+    const void* dY; int64_t lddy;
+    const void* X; int64_t ldx;
+    const void* W[2]; int64_t ldw;
+    const void* Z[2]; int64_t ldz;
+    void* dX; int64_t lddx;
+    void* dW[2]; int64_t lddw;
+    void* db[2];
+};
+
+template <class T>
+vq_status grad_launch(const Backward& b, void* const (&D)[2], int64_t ldd, float* const (&part)[2], hipStream_t st)
+{
+    typedef typename T::E E;
+    const dim3 grid((unsigned)((b.M + 511) / 512), (unsigned)((b.T + kGradRows - 1) / kGradRows));
+    const bool vec = vec8_ok(b.dY, b.lddy) && vec8_ok(b.Z[0], b.ldz) && vec8_ok(b.Z[1], b.ldz);
+    if (b.nm > 1)
+        hipLaunchKernelGGL((k_grad<T, true>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], b.Z[1],
+                           b.ldz, vec, (E*)D[0], (E*)D[1], ldd, part[0], part[1]);
+    else
+        hipLaunchKernelGGL((k_grad<T, false>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], b.Z[1],
+                           b.ldz, vec, (E*)D[0], (E*)nullptr, ldd, part[0], part[1]);
+    VQ_LAUNCHED("k_grad");
+    if (part[0]) {
+        hipLaunchKernelGGL((k_bias_sum<T>), dim3((unsigned)((b.M + 15) / 16), b.nm), dim3(256), 0, st, part[0], part[1],
+                           (int64_t)grid.y, (int)b.M, (E*)b.db[0], (E*)b.db[1]);
+        VQ_LAUNCHED("k_bias_sum");
+    }
+    return VQ_OK;
+}
+
+vq_status backward(const Backward& b, Arena& ws, bool run, hipStream_t st)
+{
+    const bool want_dw = b.dW[0] || b.dW[1], want_db = b.db[0] || b.db[1];
+    if (b.T == 0) {
+        if (run)
+            for (int i = 0; i < b.nm; ++i) {
+                VQ_TRY(zero_matrix(b.dW[i], b.M, b.N, b.lddw, st));
+                VQ_TRY(zero_matrix(b.db[i], 1, b.M, b.M, st));
+            }
+        return VQ_OK;
+    }
+    // gradients of the pre-activations: the caller's dY itself where it is one
+    Mat d[2] = {{b.dY, b.T, b.M, b.lddy}, {nullptr, b.T, b.M, b.lddy}};
+    const bool own_d = (b.dX || want_dw) && (b.nm > 1 || b.act != VQ_ACT_NONE || !loads_ok(d[0]));
+    void* D[2] = {nullptr, nullptr};
+    const int64_t ldd = round8(b.M);
+    if (own_d || (b.nm > 1 && want_db))
+        for (int i = 0; i < b.nm; ++i) {
+            D[i] = ws.take((size_t)b.T * ldd * 2);
+            d[i] = {D[i], b.T, ldd, ldd};
+        }
+    float* part[2] = {nullptr, nullptr};
+    if (want_db)
+        for (int i = 0; i < b.nm; ++i)
+            part[i] = static_cast<float*>(ws.take((size_t)((b.T + kGradRows - 1) / kGradRows) * b.M * sizeof(float)));
+    Mat x{b.X, b.T, b.N, b.ldx};
+    Mat w[2] = {{b.W[0], b.M, b.N, b.ldw}, {b.W[1], b.M, b.N, b.ldw}};
+    const size_t gx = b.dX ? gemm_workspace(GEMM_DX, b.N, b.T, b.M, b.nm, 1) : 0;
+    const int nb = b.dW[0] && b.dW[1] ? 2 : 1;
+    const size_t gw = want_dw ? gemm_workspace(GEMM_DW, b.N, b.M, b.T, 1, nb) : 0;
+    void* part_ws = ws.take(std::max(gx, gw));       // the two products run one after the other
+    if (want_dw && !loads_ok(x)) VQ_TRY(pack(x, ws, run, st));
+    if (b.dX && (!loads_ok(w[0]) || (b.nm > 1 && !loads_ok(w[1]))))
+        for (int i = 0; i < b.nm; ++i) VQ_TRY(pack(w[i], ws, run, st));
+    if (!run) return VQ_OK;
+
+    if (D[0] || want_db)
+        VQ_TRY(b.dtype == VQ_BF16 ? grad_launch<Bf16>(b, D, ldd, part, st) : grad_launch<F16>(b, D, ldd, part, st));
+    GemmArgs g{};
+    g.dtype = b.dtype;
+    g.np = (int)b.N;
+    if (b.dX) {
+        g.kind = GEMM_DX;
+        g.nq = (int)b.T;
+        g.nseg = b.nm; g.nbatch = 1;
+        for (int i = 0; i < b.nm; ++i) { g.P[i] = w[i].p; g.Q[i] = d[i].p; }
+        g.ldp = w[0].ld; g.ldq = d[0].ld;
+        g.kP = b.M; g.kQ = d[0].cols;
+        g.wp = (int)w[0].cols;
+        g.epi.Y = b.dX; g.epi.ldy = b.lddx;
+        VQ_TRY(gemm_launch(g, part_ws, gx, st));
+    }
+    if (want_dw) {
+        const int first = b.dW[0] ? 0 : 1;
+        g.kind = GEMM_DW;
+        g.nq = (int)b.M;
+        g.nseg = 1; g.nbatch = nb;
+        g.P[0] = g.P[1] = x.p;
+        g.Q[0] = d[first].p; g.Q[1] = d[1].p;
+        g.ldp = x.ld; g.ldq = d[0].ld;
+        g.kP = g.kQ = b.T;
+        g.wp = (int)x.cols; g.wq = (int)d[0].cols;
+        g.epi.Y = b.dW[first]; g.epi.ldy = b.lddw;
+        g.Y2 = b.dW[1];
+        VQ_TRY(gemm_launch(g, part_ws, gw, st));
+    }
+    return VQ_OK;
+}
+
+// ---- argument checks ------------------------------------------------------
+vq_status check_sizes(const std::string& call, int64_t T, int64_t M, int64_t N, int dtype, int act)
+{
+    VQ_CHECK(T >= 0 && T <= kMaxTokens, call + ": T must be in [0, 2^28]");
+    VQ_CHECK(M >= 1 && M <= kMaxSize && N >= 1 && N <= kMaxSize, call + ": M and N must be in [1, 2^20]");
+    VQ_CHECK(dtype == VQ_BF16 || dtype == VQ_F16, call + ": dtype must be VQ_BF16 or VQ_F16");
+    VQ_CHECK(act >= VQ_ACT_NONE && act <= VQ_ACT_SIGMOID, call + ": unknown activation");
+    return VQ_OK;
+}
+
+vq_status check_ld(const std::string& call, const char* what, const void* p, int64_t ld, int64_t cols)
+{
+    VQ_CHECK(p == nullptr || ld >= cols, call + ": leading dimension of " + what + " is below its row length");
+    VQ_CHECK(p == nullptr || ld <= ((int64_t)1 << 40), call + ": leading dimension of " + what + " is too large");
+    VQ_CHECK((reinterpret_cast<uintptr_t>(p) & 1u) == 0, call + ": " + what + " is not aligned to its elements");
+    return VQ_OK;
+}
+
+#define VQ_MATRIX(a, rows, cols, ld, call, what) \
+    VQ_TRY(check_matrix((a), (rows), (cols), (ld), dtype, (call), (what), as_stream(stream)))
+
+}  // namespace
+}  // namespace vq
+
+using namespace vq;
+
+extern "C" {
+
+size_t vq_linear_workspace_bytes(int64_t T, int64_t M, int64_t N, const void* X, int64_t ldx, const void* W, int64_t ldw)
+{
+    if (check_sizes("vq_linear", T, M, N, VQ_BF16, 0) != VQ_OK) return 0;
+    Forward f{T, M, N, VQ_BF16, 1, X, ldx, {W, nullptr}, ldw, {}};
+    Arena ws{nullptr};
+    return forward(f, ws, false, nullptr) == VQ_OK ? ws.used : 0;
+}
+
+vq_status vq_linear(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* X, int64_t ldx, const void* W,
+                    int64_t ldw, const void* bias, const void* R, int64_t ldr, void* Y, int64_t ldy, void* Z, int64_t ldz,
+                    void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_linear";
+    VQ_TRY(check_sizes(call, T, M, N, dtype, act));
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(X && W && Y, "vq_linear: null pointer");
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "W", W, ldw, N));
+    VQ_TRY(check_ld(call, "bias", bias, M, M));
+    VQ_TRY(check_ld(call, "R", R, ldr, M));
+    VQ_TRY(check_ld(call, "Y", Y, ldy, M));
+    VQ_TRY(check_ld(call, "Z", Z, ldz, M));
+    VQ_CHECK(Y != X && Y != W && Y != Z && (!Z || (Z != X && Z != W && Z != R)), "vq_linear: outputs may not alias inputs");
+    VQ_CHECK(Y != R || ldy == ldr, "vq_linear: Y in place of R needs R's leading dimension");
+    VQ_TRY(check_device());
+    VQ_MATRIX(X, T, N, ldx, call, "X");
+    VQ_MATRIX(W, M, N, ldw, call, "W");
+    VQ_MATRIX(bias, 1, M, M, call, "bias");
+    VQ_MATRIX(R, T, M, ldr, call, "R");
+    Forward f{T, M, N, dtype, 1, X, ldx, {W, nullptr}, ldw, {act, 0, {bias, nullptr}, R, Y, {Z, nullptr}, ldr, ldy, ldz}};
+    Arena a{nullptr};
+    VQ_TRY(forward(f, a, false, as_stream(stream)));
+    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_linear: workspace too small");
+    TimedRegion tr("linear", 0, as_stream(stream));
+    Arena w{static_cast<char*>(ws)};
+    return forward(f, w, true, as_stream(stream));
+}
+
+size_t vq_gated_workspace_bytes(int64_t T, int64_t M, int64_t N, const void* X, int64_t ldx, const void* Wg,
+                                const void* Wu, int64_t ldw)
+{
+    if (check_sizes("vq_gated", T, M, N, VQ_BF16, 0) != VQ_OK) return 0;
+    Forward f{T, M, N, VQ_BF16, 2, X, ldx, {Wg, Wu}, ldw, {}};
+    Arena ws{nullptr};
+    return forward(f, ws, false, nullptr) == VQ_OK ? ws.used : 0;
+}
+
+vq_status vq_gated(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* X, int64_t ldx, const void* Wg,
+                   const void* Wu, int64_t ldw, const void* bg, const void* bu, void* H, int64_t ldh, void* G, void* U,
+                   int64_t ldz, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_gated";
+    VQ_TRY(check_sizes(call, T, M, N, dtype, act));
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(X && Wg && Wu && H, "vq_gated: null pointer");
+    VQ_CHECK((G == nullptr) == (U == nullptr), "vq_gated: G and U come together");
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "Wg", Wg, ldw, N));
+    VQ_TRY(check_ld(call, "Wu", Wu, ldw, N));
+    VQ_TRY(check_ld(call, "bg", bg, M, M));
+    VQ_TRY(check_ld(call, "bu", bu, M, M));
+    VQ_TRY(check_ld(call, "H", H, ldh, M));
+    VQ_TRY(check_ld(call, "G", G, ldz, M));
+    VQ_TRY(check_ld(call, "U", U, ldz, M));
+    for (const void* o : {(const void*)H, (const void*)G, (const void*)U})
+        VQ_CHECK(!o || (o != X && o != Wg && o != Wu), "vq_gated: outputs may not alias inputs");
+    VQ_CHECK(H != G && H != U && (!G || G != U), "vq_gated: outputs may not alias each other");
+    VQ_TRY(check_device());
+    VQ_MATRIX(X, T, N, ldx, call, "X");
+    VQ_MATRIX(Wg, M, N, ldw, call, "Wg");
+    VQ_MATRIX(Wu, M, N, ldw, call, "Wu");
+    VQ_MATRIX(bg, 1, M, M, call, "bg");
+    VQ_MATRIX(bu, 1, M, M, call, "bu");
+    Forward f{T, M, N, dtype, 2, X, ldx, {Wg, Wu}, ldw, {act, 0, {bg, bu}, nullptr, H, {G, U}, 0, ldh, ldz}};
+    Arena a{nullptr};
+    VQ_TRY(forward(f, a, false, as_stream(stream)));
+    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_gated: workspace too small");
+    TimedRegion tr("gated", 0, as_stream(stream));
+    Arena w{static_cast<char*>(ws)};
+    return forward(f, w, true, as_stream(stream));
+}
+
+size_t vq_linear_backward_workspace_bytes(int64_t T, int64_t M, int64_t N, int act, const void* dY, int64_t lddy,
+                                          const void* X, int64_t ldx, const void* W, int64_t ldw, int want_dx, int want_dw,
+                                          int want_db)
+{
+    if (check_sizes("vq_linear_backward", T, M, N, VQ_BF16, act) != VQ_OK) return 0;
+    void* const on = reinterpret_cast<void*>(uintptr_t(16));      // counted, never used
+    Backward b{T, M, N, VQ_BF16, act, 1, dY, lddy, X, ldx, {W, nullptr}, ldw, {nullptr, nullptr}, 0,
+               want_dx ? on : nullptr, N, {want_dw ? on : nullptr, nullptr}, N, {want_db ? on : nullptr, nullptr}};
+    Arena ws{nullptr};
+    return backward(b, ws, false, nullptr) == VQ_OK ? ws.used : 0;
+}
+
+vq_status vq_linear_backward(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* dY, int64_t lddy,
+                             const void* X, int64_t ldx, const void* W, int64_t ldw, const void* Z, int64_t ldz, void* dX,
+                             int64_t lddx, void* dW, int64_t lddw, void* db, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_linear_backward";
+    VQ_TRY(check_sizes(call, T, M, N, dtype, act));
+    VQ_CHECK(T == 0 || dY, "vq_linear_backward: dY is null");
+    VQ_CHECK(T == 0 || !dX || W, "vq_linear_backward: dX needs W");
+    VQ_CHECK(T == 0 || !dW || X, "vq_linear_backward: dW needs X");
+    VQ_CHECK(T == 0 || act == VQ_ACT_NONE || Z, "vq_linear_backward: the activation's gradient needs Z");
+    VQ_TRY(check_ld(call, "dY", dY, lddy, M));
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "W", W, ldw, N));
+    VQ_TRY(check_ld(call, "Z", Z, ldz, M));
+    VQ_TRY(check_ld(call, "dX", dX, lddx, N));
+    VQ_TRY(check_ld(call, "dW", dW, lddw, N));
+    VQ_TRY(check_ld(call, "db", db, M, M));
+    for (const void* o : {(const void*)dX, (const void*)dW, (const void*)db})
+        VQ_CHECK(!o || (o != dY && o != X && o != W && o != Z), "vq_linear_backward: outputs may not alias inputs");
+    if (T > 0 || dW || db) VQ_TRY(check_device());
+    VQ_MATRIX(dY, T, M, lddy, call, "dY");
+    if (dW) VQ_MATRIX(X, T, N, ldx, call, "X");
+    if (dX) VQ_MATRIX(W, M, N, ldw, call, "W");
+    if (act != VQ_ACT_NONE) VQ_MATRIX(Z, T, M, ldz, call, "Z");
+    Backward b{T, M, N, dtype, act, 1, dY, lddy, X, ldx, {W, nullptr}, ldw, {act != VQ_ACT_NONE ? Z : nullptr, nullptr}, ldz,
+               dX, lddx, {dW, nullptr}, lddw, {db, nullptr}};
+    Arena a{nullptr};
+    VQ_TRY(backward(b, a, false, as_stream(stream)));
+    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_linear_backward: workspace too small");
+    TimedRegion tr("linear_backward", 0, as_stream(stream));
+    Arena w{static_cast<char*>(ws)};
+    return backward(b, w, true, as_stream(stream));
+}
+
+size_t vq_gated_backward_workspace_bytes(int64_t T, int64_t M, int64_t N, int act, const void* dH, int64_t lddh,
+                                         const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
+                                         int want_dx, int want_dw, int want_db)
+{
+    if (check_sizes("vq_gated_backward", T, M, N, VQ_BF16, act) != VQ_OK) return 0;
+    void* const on = reinterpret_cast<void*>(uintptr_t(16));      // counted, never used
+    void* const w = want_dw ? on : nullptr;
+    void* const db = want_db ? on : nullptr;
+    Backward b{T, M, N, VQ_BF16, act, 2, dH, lddh, X, ldx, {Wg, Wu}, ldw, {nullptr, nullptr}, 0,
+               want_dx ? on : nullptr, N, {w, w}, N, {db, db}};
+    Arena ws{nullptr};
+    return backward(b, ws, false, nullptr) == VQ_OK ? ws.used : 0;
+}
+
+vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* dH, int64_t lddh,
+                            const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, const void* G,
+                            const void* U, int64_t ldz, void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw,
+                            void* dbg, void* dbu, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_gated_backward";
+    VQ_TRY(check_sizes(call, T, M, N, dtype, act));
+    VQ_CHECK(T == 0 || (dH && G && U), "vq_gated_backward: null pointer");
+    VQ_CHECK(T == 0 || !dX || (Wg && Wu), "vq_gated_backward: dX needs Wg and Wu");
+    VQ_CHECK(T == 0 || !(dWg || dWu) || X, "vq_gated_backward: dWg and dWu need X");
+    VQ_CHECK((dWg == nullptr) == (dWu == nullptr) && (!dWg || dWg != dWu), "vq_gated_backward: dWg and dWu come together, apart");
+    VQ_CHECK((dbg == nullptr) == (dbu == nullptr) && (!dbg || dbg != dbu), "vq_gated_backward: dbg and dbu come together, apart");
+    VQ_TRY(check_ld(call, "dH", dH, lddh, M));
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "Wg", Wg, ldw, N));
+    VQ_TRY(check_ld(call, "Wu", Wu, ldw, N));
+    VQ_TRY(check_ld(call, "G", G, ldz, M));
+    VQ_TRY(check_ld(call, "U", U, ldz, M));
+    VQ_TRY(check_ld(call, "dX", dX, lddx, N));
+    VQ_TRY(check_ld(call, "dWg", dWg, lddw, N));
+    VQ_TRY(check_ld(call, "dWu", dWu, lddw, N));
+    VQ_TRY(check_ld(call, "dbg", dbg, M, M));
+    VQ_TRY(check_ld(call, "dbu", dbu, M, M));
+    for (const void* o : {(const void*)dX, (const void*)dWg, (const void*)dWu, (const void*)dbg, (const void*)dbu})
+        VQ_CHECK(!o || (o != dH && o != X && o != Wg && o != Wu && o != G && o != U),
+                 "vq_gated_backward: outputs may not alias inputs");
+    if (T > 0 || dWg || dbg) VQ_TRY(check_device());
+    VQ_MATRIX(dH, T, M, lddh, call, "dH");
+    if (dWg) VQ_MATRIX(X, T, N, ldx, call, "X");
+    if (dX) VQ_MATRIX(Wg, M, N, ldw, call, "Wg");
+    if (dX) VQ_MATRIX(Wu, M, N, ldw, call, "Wu");
+    VQ_MATRIX(G, T, M, ldz, call, "G");
+    VQ_MATRIX(U, T, M, ldz, call, "U");
+    Backward b{T, M, N, dtype, act, 2, dH, lddh, X, ldx, {Wg, Wu}, ldw, {G, U}, ldz, dX, lddx, {dWg, dWu}, lddw, {dbg, dbu}};
+    Arena a{nullptr};
+    VQ_TRY(backward(b, a, false, as_stream(stream)));
+    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_gated_backward: workspace too small");
+    TimedRegion tr("gated_backward", 0, as_stream(stream));
+    Arena w{static_cast<char*>(ws)};
+    return backward(b, w, true, as_stream(stream));
+}
+
+}  // extern "C"

@@ -89,23 +89,6 @@ vq_status check_K(int K, int64_t n_sub)
     return VQ_OK;
 }
 
-namespace {
-
-#define VQ_WS(cond, msg)                                            \
-    do {                                                          \
-        if (!(cond)) return ::vq::fail(VQ_ERR_WORKSPACE, (msg));  \
-    } while (0)
-
-#define VQ_TRY(expr)                          \
-    do {                                      \
-        vq_status vq_s_ = (expr);             \
-        if (vq_s_ != VQ_OK) return vq_s_;     \
-    } while (0)
-
-// VQ_CHECK=1 mode: finite values (weights: also non-negative) in an input.
-#define VQ_VALUES(a, n, weights, call, what) \
-    VQ_TRY(::vq::check_values((a), (n), (weights), (call), (what), as_stream(stream)))
-
 // The current device must be a gfx950; checked once per device.
 vq_status check_device()
 {
@@ -120,6 +103,8 @@ vq_status check_device()
     ok_dev = dev;
     return VQ_OK;
 }
+
+namespace {
 
 int64_t nnz_of(int64_t M, int64_t N, double p) { return (int64_t)std::floor(p * (double)(M * N)); }
 

@@ -34,6 +34,21 @@ vq_status hip_fail(hipError_t e, const char* what);
         if (vq_e_ != hipSuccess) return ::vq::hip_fail(vq_e_, name); \
     } while (0)
 
+#define VQ_WS(cond, msg)                                            \
+    do {                                                          \
+        if (!(cond)) return ::vq::fail(VQ_ERR_WORKSPACE, (msg));  \
+    } while (0)
+
+#define VQ_TRY(expr)                          \
+    do {                                      \
+        vq_status vq_s_ = (expr);             \
+        if (vq_s_ != VQ_OK) return vq_s_;     \
+    } while (0)
+
+// VQ_CHECK=1 mode: finite values (weights: also non-negative) in an input.
+#define VQ_VALUES(a, n, weights, call, what) \
+    VQ_TRY(::vq::check_values((a), (n), (weights), (call), (what), as_stream(stream)))
+
 // ---- workspace ----------------------------------------------------------
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -70,6 +85,7 @@ size_t ws_hfactor(int64_t N);
 // Argument checks shared by the entry points.
 vq_status check_shape(int64_t M, int64_t N, int d);
 vq_status check_K(int K, int64_t n_sub);
+vq_status check_device();   // the current device must be a gfx950
 
 // Input value checks (environment VQ_CHECK=1): counts the non-finite values of
 // a[0..n) (with sign_clear, also those with the sign bit set) on the device and
@@ -78,6 +94,11 @@ vq_status check_K(int K, int64_t n_sub);
 bool values_check_on();
 vq_status check_values(const float* a, int64_t n, bool sign_clear, const char* call, const char* what,
                        hipStream_t st);
+
+// The same for a [rows x cols] matrix of 16-bit elements (VQ_BF16 or VQ_F16) with
+// leading dimension ld, or of float32 (VQ_F32).
+vq_status check_matrix(const void* a, int64_t rows, int64_t cols, int64_t ld, int dtype, const char* call,
+                       const char* what, hipStream_t st);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

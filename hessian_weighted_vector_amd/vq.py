@@ -97,6 +97,16 @@ SIGNATURES = {
                             ctypes.POINTER(GroupedOutputs), _P, _SZ, _P]),
     "vq_bits_per_weight_grouped": (_D, [ctypes.POINTER(GroupedParams)]),
     "vq_bits_per_weight": (_D, [_I64, _I64, _I, _I, _I, _I64, _I, _I]),
+    "vq_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _I64, _P, _I64]),
+    "vq_linear": (_I, [_I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "vq_linear_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I]),
+    "vq_linear_backward": (_I, [_I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                _P, _P, _SZ, _P]),
+    "vq_gated_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _I64, _P, _P, _I64]),
+    "vq_gated": (_I, [_I64, _I64, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "vq_gated_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I]),
+    "vq_gated_backward": (_I, [_I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64,
+                               _P, _P, _I64, _P, _P, _P, _SZ, _P]),
     "vq_timing_enable": (None, [_I]),
     "vq_timing_count": (_I, []),
     "vq_timing_get": (_I, [_I, ctypes.c_char_p, _I, ctypes.POINTER(_I), ctypes.POINTER(_I64),
@@ -461,3 +471,165 @@ def fit(W, h, d, K1, iters1, K2=0, iters2=0, outlier_frac=0.0, binorm=False, mas
         o["C2"] = None
         o["idx2"] = None
     return o
+
+
+# ---- dense feed-forward calls ------------------------------------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _act(act):
+    try:
+        return ACTIVATIONS[act]
+    except KeyError:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTIVATIONS), act)) from None
+
+
+def _half(t, name):
+    """The library's code of a 16-bit tensor's type."""
+    code = _DTYPES.get(t.dtype)
+    if code is None or code > 1:
+        raise TypeError("%s must be torch.bfloat16 or torch.float16, got %s" % (name, t.dtype))
+    return code
+
+
+def _matrix(t, rows, cols, dtype, name):
+    """(pointer, leading dimension) of a [rows x cols] tensor with unit column stride; None passes."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU" % name)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must be [%d x %d], got %s" % (name, rows, cols, list(t.shape)))
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    if rows > 1 and s0 < cols:
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return t.data_ptr(), s0 if rows > 1 else max(s0, cols)
+
+
+def _vector(t, n, dtype, name):
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s must be [%d], got %s" % (name, n, list(t.shape)))
+    return _ptr(t)
+
+
+def _scratch(need, ws, device):
+    """(pointer, bytes, tensor) of a workspace of at least `need` bytes."""
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return _ptr(ws), ws.numel(), ws
+
+
+def _dims(X, W):
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be matrices")
+    return X.shape[0], W.shape[0], W.shape[1]
+
+
+def linear(X, W, bias=None, residual=None, act="none", want_pre=False, out=None, ws=None):
+    """Y = act(X W^T + bias) + residual: X [T, N], W [M, N], bfloat16 or float16 (one type).
+
+    With want_pre returns (Y, Z), Z = X W^T + bias (linear_backward's `pre`).
+    Rows may be strided.  `out` may be the residual itself.
+    """
+    T, M, N = _dims(X, W)
+    dt, a = _half(X, "X"), _act(act)
+    x, ldx = _matrix(X, T, N, X.dtype, "X")
+    w, ldw = _matrix(W, M, N, X.dtype, "W")
+    b = _vector(bias, M, X.dtype, "bias")
+    r, ldr = _matrix(residual, T, M, X.dtype, "residual")
+    Y = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    Z = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
+    y, ldy = _matrix(Y, T, M, X.dtype, "out")
+    z, ldz = _matrix(Z, T, M, X.dtype, "pre")
+    lib = load()
+    p, n, ws = _scratch(lib.vq_linear_workspace_bytes(T, M, N, x, ldx, w, ldw), ws, X.device)
+    _check(lib.vq_linear(T, M, N, dt, a, x, ldx, w, ldw, b, r, ldr, y, ldy, z, ldz, p, n, _stream()))
+    return (Y, Z) if want_pre else Y
+
+
+def linear_backward(dY, X, W, pre=None, act="none", want_dx=True, want_dw=True, want_db=False, ws=None):
+    """(dX, dW, db) of linear for the incoming gradient dY [T, M]; None where not wanted.
+
+    `pre` is the Z that linear returned (needed unless act is "none").  The
+    residual's gradient is dY itself.
+    """
+    T, M, N = _dims(X, W)
+    dt, a = _half(X, "X"), _act(act)
+    if a != 0 and pre is None:
+        raise ValueError("pre is needed for the activation's gradient")
+    g, ldg = _matrix(dY, T, M, X.dtype, "dY")
+    x, ldx = _matrix(X, T, N, X.dtype, "X")
+    w, ldw = _matrix(W, M, N, X.dtype, "W")
+    z, ldz = _matrix(pre, T, M, X.dtype, "pre")
+    dX = torch.empty((T, N), dtype=X.dtype, device=X.device) if want_dx else None
+    dW = torch.empty((M, N), dtype=X.dtype, device=X.device) if want_dw else None
+    db = torch.empty(M, dtype=X.dtype, device=X.device) if want_db else None
+    lib = load()
+    p, n, ws = _scratch(lib.vq_linear_backward_workspace_bytes(T, M, N, a, g, ldg, x, ldx, w, ldw, want_dx, want_dw,
+                                                               want_db), ws, X.device)
+    _check(lib.vq_linear_backward(T, M, N, dt, a, g, ldg, x, ldx, w, ldw, z, ldz, _ptr(dX), N, _ptr(dW), N, _ptr(db),
+                                  p, n, _stream()))
+    return dX, dW, db
+
+
+def gated(X, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", want_pre=False, out=None, ws=None):
+    """H = act(G) * U, G = X W_gate^T + bias_gate, U = X W_up^T + bias_up, in one kernel.
+
+    X [T, N], W_gate and W_up [M, N], bfloat16 or float16.  With want_pre
+    returns (H, G, U), which gated_backward takes.
+    """
+    T, M, N = _dims(X, W_gate)
+    dt, a = _half(X, "X"), _act(act)
+    x, ldx = _matrix(X, T, N, X.dtype, "X")
+    wg, ldw = _matrix(W_gate, M, N, X.dtype, "W_gate")
+    wu, ldu = _matrix(W_up, M, N, X.dtype, "W_up")
+    if ldw != ldu:
+        raise ValueError("W_gate and W_up must have the same row stride")
+    bg = _vector(bias_gate, M, X.dtype, "bias_gate")
+    bu = _vector(bias_up, M, X.dtype, "bias_up")
+    H = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    h, ldh = _matrix(H, T, M, X.dtype, "out")
+    G = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
+    U = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
+    lib = load()
+    p, n, ws = _scratch(lib.vq_gated_workspace_bytes(T, M, N, x, ldx, wg, wu, ldw), ws, X.device)
+    _check(lib.vq_gated(T, M, N, dt, a, x, ldx, wg, wu, ldw, bg, bu, h, ldh, _ptr(G), _ptr(U), M, p, n, _stream()))
+    return (H, G, U) if want_pre else H
+
+
+def gated_backward(dH, X, W_gate, W_up, G, U, act="silu", want_dx=True, want_dw=True, want_db=False, ws=None):
+    """(dX, dW_gate, dW_up, db_gate, db_up) of gated; None where not wanted."""
+    T, M, N = _dims(X, W_gate)
+    dt, a = _half(X, "X"), _act(act)
+    dh, lddh = _matrix(dH, T, M, X.dtype, "dH")
+    x, ldx = _matrix(X, T, N, X.dtype, "X")
+    wg, ldw = _matrix(W_gate, M, N, X.dtype, "W_gate")
+    wu, ldu = _matrix(W_up, M, N, X.dtype, "W_up")
+    g, ldz = _matrix(G, T, M, X.dtype, "G")
+    u, ldz2 = _matrix(U, T, M, X.dtype, "U")
+    if ldw != ldu or ldz != ldz2:
+        raise ValueError("W_gate and W_up, and G and U, must have the same row stride")
+
+    def new(on, *shape):
+        return torch.empty(shape, dtype=X.dtype, device=X.device) if on else None
+
+    dX, dWg, dWu = new(want_dx, T, N), new(want_dw, M, N), new(want_dw, M, N)
+    dbg, dbu = new(want_db, M), new(want_db, M)
+    lib = load()
+    p, n, ws = _scratch(lib.vq_gated_backward_workspace_bytes(T, M, N, a, dh, lddh, x, ldx, wg, wu, ldw, want_dx,
+                                                              want_dw, want_db), ws, X.device)
+    _check(lib.vq_gated_backward(T, M, N, dt, a, dh, lddh, x, ldx, wg, wu, ldw, g, u, ldz, _ptr(dX), N, _ptr(dWg),
+                                 _ptr(dWu), N, _ptr(dbg), _ptr(dbu), p, n, _stream()))
+    return dX, dWg, dWu, dbg, dbu

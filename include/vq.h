@@ -64,6 +64,17 @@ typedef enum {
     VQ_ERR_UNSUPPORTED = 5  /* no gfx950 device current */
 } vq_status;
 
+/* 16-bit element types of the dense feed-forward calls. */
+typedef enum { VQ_BF16 = 0, VQ_F16 = 1, VQ_F32 = 2 } vq_dtype;
+
+/* Activations of the feed-forward calls.  VQ_ACT_GELU is z Phi(z) with the
+ * normal distribution function, VQ_ACT_GELU_TANH its tanh approximation
+ * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum {
+    VQ_ACT_NONE = 0, VQ_ACT_RELU = 1, VQ_ACT_SILU = 2, VQ_ACT_GELU = 3, VQ_ACT_GELU_TANH = 4,
+    VQ_ACT_SIGMOID = 5
+} vq_act;
+
 /* Library version string (static storage). */
 const char* vq_version(void);
 
@@ -401,6 +412,67 @@ vq_status vq_fit_grouped(const vq_grouped_params* p, const vq_grouped_inputs* in
  * scales (bi-normalization) and one int32 per outlier column, over M*N. */
 double vq_bits_per_weight_grouped(const vq_grouped_params* p);
 
+
+/* Dense feed-forward calls: the layers that the quantized matrices belong to,
+ * with their gradients, on 16-bit tensors (dtype VQ_BF16 or VQ_F16; every
+ * tensor of a call has the same type).  T tokens, M output and N input
+ * features.  Matrices are row-major with a leading dimension in elements (the
+ * distance between rows, at least the row length); vectors (biases) are
+ * contiguous.  Any size, stride and element-aligned address is accepted; rows
+ * that are 16-byte aligned and a multiple of eight elements long are read in
+ * place, others are first copied into the workspace.  1 <= M, N <= 2^20,
+ * 0 <= T <= 2^28; T = 0 is a no-op (the backward calls write zero gradients of
+ * weights and biases).  Products and sums are float32 on the matrix cores;
+ * each stored value is rounded once from float32.  Results are bitwise
+ * reproducible for fixed arguments (the sums' split depends on sizes and
+ * alignment, never on timing).  Outputs may not overlap inputs, except Y = R
+ * (same address and leading dimension).  Non-finite inputs spread into the
+ * outputs whose sums they enter and no others.  The workspace queries take the
+ * same sizes, addresses and leading dimensions as the call (addresses for
+ * their alignment alone) and return 0 for sizes that the call rejects. */
+
+/* Y = act(X W^T + bias) + R:  X [T x N], W [M x N], bias [M] (nullable), R [T x M]
+ * (nullable), Y [T x M].  Z (nullable) [T x M] receives X W^T + bias, which
+ * the backward call needs when act is not VQ_ACT_NONE. */
+size_t vq_linear_workspace_bytes(int64_t T, int64_t M, int64_t N, const void* X, int64_t ldx, const void* W, int64_t ldw);
+vq_status vq_linear(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* X, int64_t ldx,
+                    const void* W, int64_t ldw, const void* bias, const void* R, int64_t ldr,
+                    void* Y, int64_t ldy, void* Z, int64_t ldz, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of vq_linear:  dZ = dY act'(Z),  dX = dZ W,  dW = dZ^T X,
+ * db = column sums of dZ (R's gradient is dY).  Each of dX [T x N],
+ * dW [M x N], db [M] may be NULL; W is read for dX, X for dW, Z where act is
+ * not VQ_ACT_NONE.  dZ enters the products rounded to the tensors' type; db is
+ * summed before that rounding. */
+size_t vq_linear_backward_workspace_bytes(int64_t T, int64_t M, int64_t N, int act, const void* dY, int64_t lddy,
+                                          const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                          int want_dx, int want_dw, int want_db);
+vq_status vq_linear_backward(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* dY, int64_t lddy,
+                             const void* X, int64_t ldx, const void* W, int64_t ldw, const void* Z, int64_t ldz,
+                             void* dX, int64_t lddx, void* dW, int64_t lddw, void* db,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* H = act(G) * U with G = X Wg^T + bg and U = X Wu^T + bu, in one kernel:  Wg, Wu
+ * [M x N] with one leading dimension, bg, bu [M] (nullable), H [T x M].  G and
+ * U [T x M] (both or neither NULL) receive the pre-activations for the
+ * backward call; H is formed from their unrounded values. */
+size_t vq_gated_workspace_bytes(int64_t T, int64_t M, int64_t N, const void* X, int64_t ldx, const void* Wg,
+                                const void* Wu, int64_t ldw);
+vq_status vq_gated(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* X, int64_t ldx,
+                   const void* Wg, const void* Wu, int64_t ldw, const void* bg, const void* bu,
+                   void* H, int64_t ldh, void* G, void* U, int64_t ldz, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of vq_gated:  dG = dH U act'(G),  dU = dH act(G),
+ * dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,  dbg, dbu = column sums of
+ * dG, dU.  dX may be NULL, dWg and dWu both, dbg and dbu both. */
+size_t vq_gated_backward_workspace_bytes(int64_t T, int64_t M, int64_t N, int act, const void* dH, int64_t lddh,
+                                         const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
+                                         int want_dx, int want_dw, int want_db);
+vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act, const void* dH, int64_t lddh,
+                            const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
+                            const void* G, const void* U, int64_t ldz, void* dX, int64_t lddx,
+                            void* dWg, void* dWu, int64_t lddw, void* dbg, void* dbu,
+                            void* ws, size_t ws_bytes, void* stream);
 
 /* Bits per weight of the stored result (host arithmetic; VPTQ page,
  * "End-to-End Quantization Pipeline", compression ratio: index bits plus

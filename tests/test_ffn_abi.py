@@ -1,0 +1,104 @@
+"""Refusals of the feed-forward calls without a GPU: every case fails validation on the host."""
+import math
+
+import pytest
+import torch
+
+import ffn_reference as ref
+from hessian_weighted_vector_amd import vq
+
+FAKE = 0x10000            # never dereferenced
+BF16, F16, F32 = 0, 1, 2
+
+
+def linear(T=4, M=8, N=16, dt=BF16, act=0, X=FAKE, ldx=16, W=FAKE + 4096, ldw=16, b=None, R=None, ldr=8,
+           Y=FAKE + 8192, ldy=8, Z=None, ldz=8, ws=None, n=0):
+    lib = vq.load()
+    return lib.vq_linear(T, M, N, dt, act, X, ldx, W, ldw, b, R, ldr, Y, ldy, Z, ldz, ws, n, None), \
+        lib.vq_last_error().decode()
+
+
+@pytest.mark.parametrize("change,msg", [
+    (dict(T=-1), "T must"), (dict(M=0), "M and N"), (dict(N=0), "M and N"), (dict(N=(1 << 20) + 1, ldx=1 << 21, ldw=1 << 21), "M and N"),
+    (dict(dt=F32), "dtype"), (dict(dt=-1), "dtype"), (dict(act=6), "activation"), (dict(act=-1), "activation"),
+    (dict(X=None), "null"), (dict(W=None), "null"), (dict(Y=None), "null"),
+    (dict(ldx=15), "leading dimension of X"), (dict(ldw=15), "leading dimension of W"),
+    (dict(ldy=7), "leading dimension of Y"), (dict(R=FAKE + 64, ldr=7), "leading dimension of R"),
+    (dict(Z=FAKE + 64, ldz=7), "leading dimension of Z"), (dict(X=FAKE + 1), "aligned"),
+    (dict(Y=FAKE), "alias"), (dict(Z=FAKE + 8192), "alias"), (dict(Z=FAKE), "alias"),
+    (dict(R=FAKE + 8192, ldr=16), "in place"),
+])
+def test_linear_refuses(change, msg):
+    st, text = linear(**change)
+    assert st == vq.VQ_ERR_INVALID
+    assert msg in text and text.startswith("vq_linear")
+
+
+def test_gated_and_backward_refuse():
+    lib = vq.load()
+    A, B, C, D = FAKE, FAKE + 4096, FAKE + 8192, FAKE + 16384
+
+    def gated(T=4, M=8, N=16, dt=BF16, act=2, X=A, Wg=B, Wu=C, ldw=16, H=D, ldh=8, G=None, U=None):
+        return lib.vq_gated(T, M, N, dt, act, X, 16, Wg, Wu, ldw, None, None, H, ldh, G, U, 8, None, 0, None)
+
+    for kw in (dict(Wu=None), dict(G=D + 4096), dict(ldw=8), dict(H=B), dict(G=D, U=D + 4096), dict(G=D + 64, U=D + 64),
+               dict(dt=F32), dict(act=9), dict(T=-2)):
+        assert gated(**kw) == vq.VQ_ERR_INVALID, kw
+        assert lib.vq_last_error().decode().startswith("vq_gated:"), kw
+
+    def lback(T=4, act=2, dY=A, X=B, W=C, Z=D, dX=D + 4096, dW=D + 8192, db=None, lddx=16):
+        return lib.vq_linear_backward(T, 8, 16, F16, act, dY, 8, X, 16, W, 16, Z, 8, dX, lddx, dW, 16, db, None, 0, None)
+
+    for kw in (dict(dY=None), dict(Z=None), dict(X=None), dict(W=None), dict(dX=A), dict(dW=B), dict(lddx=15), dict(act=-1)):
+        assert lback(**kw) == vq.VQ_ERR_INVALID, kw
+        assert lib.vq_last_error().decode().startswith("vq_linear_backward:"), kw
+
+    def gback(dH=A, X=B, Wg=C, Wu=C + 2048, G=D, U=D + 2048, dX=D + 4096, dWg=D + 8192, dWu=D + 12288, dbg=None, dbu=None):
+        return lib.vq_gated_backward(4, 8, 16, BF16, 2, dH, 8, X, 16, Wg, Wu, 16, G, U, 8, dX, 16, dWg, dWu, 16, dbg, dbu,
+                                     None, 0, None)
+
+    for kw in (dict(dH=None), dict(G=None), dict(U=None), dict(Wg=None), dict(X=None), dict(dWu=None), dict(dWu=D + 8192),
+               dict(dbg=D + 32768), dict(dX=A), dict(dWg=B)):
+        assert gback(**kw) == vq.VQ_ERR_INVALID, kw
+        assert lib.vq_last_error().decode().startswith("vq_gated_backward:"), kw
+
+
+def test_workspace_queries():
+    lib = vq.load()
+    # sizes that the calls reject
+    assert lib.vq_linear_workspace_bytes(4, 0, 16, FAKE, 16, FAKE, 16) == 0
+    assert lib.vq_gated_workspace_bytes(-1, 8, 16, FAKE, 16, FAKE, FAKE, 16) == 0
+    # rows that are not 16-byte aligned are copied: the query depends on stride and address
+    a = lib.vq_linear_workspace_bytes(512, 512, 512, FAKE, 512, FAKE, 512)
+    b = lib.vq_linear_workspace_bytes(512, 512, 512, FAKE, 513, FAKE, 512)
+    c = lib.vq_linear_workspace_bytes(512, 512, 512, FAKE + 2, 512, FAKE, 512)
+    assert b - a == c - a == 512 * 512 * 2
+    # the gradients of the pre-activations live in the workspace
+    n = lib.vq_gated_backward_workspace_bytes(64, 96, 32, 2, FAKE, 96, FAKE, 32, FAKE, FAKE, 32, 1, 1, 0)
+    assert n >= 2 * 64 * 96 * 2
+
+
+def test_python_checks():
+    X = torch.zeros((4, 16), dtype=torch.bfloat16)
+    W = torch.zeros((8, 16), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        vq.linear(X, W)
+    with pytest.raises(TypeError, match="bfloat16 or torch.float16"):
+        vq.linear(X.float(), W.float())
+    with pytest.raises(ValueError, match="act must be one of"):
+        vq.linear(X, W, act="tanh")
+    with pytest.raises(ValueError, match="matrices"):
+        vq.linear(X[0], W)
+    with pytest.raises(ValueError, match="pre is needed"):
+        vq.linear_backward(X, X, W, act="silu")
+
+
+def test_reference_derivatives_against_differences():
+    """The reference's act_grad is the derivative of its act (float64 central differences)."""
+    z = torch.linspace(-6, 6, 241, dtype=torch.float64) + 0.0123
+    h = 1e-6
+    for name in ref.ACTS:
+        fd = (ref.act(name, z + h) - ref.act(name, z - h)) / (2 * h)
+        assert torch.allclose(ref.act_grad(name, z), fd, rtol=0, atol=1e-8), name
+        assert float(ref.act_grad(name, z).abs().max()) <= ref.LIPSCHITZ
+    assert math.isclose(float(ref.act("gelu", torch.tensor(1.0, dtype=torch.float64))), 0.8413447460685429, rel_tol=1e-12)
