@@ -1,0 +1,600 @@
+// Feed-forward calls that read the compressed matrices, for few tokens:
+//   vq_qlinear  Y = act(X W^T + bias) + R
+//   vq_qgated   H = act(X Wg^T + bg) * (X Wu^T + bu), both matrices in one launch
+// with W = decoded codebook rows, scaled, with the sparse correction; W is
+// never written.
+//
+// The product runs on the matrix cores with exact operands.  A lane's share of
+// a 16 x 16 x 32 instruction is eight consecutive k of one row, which is one
+// sub-vector of d = 8 (two of d = 4; a shorter one padded with zeros): the lane
+// gathers its centroid row, adds the residual row, multiplies by the column
+// scales and splits the float32 values into bf16 terms hi + lo (+ lowest),
+// each the rounding of what the terms before leave.  The tokens are split
+// alike (bf16 tokens are one term, fp16 two, float32 three), and the products
+// of terms down to 2^-18 (16-bit results) or 2^-27 (float32 results) of the
+// leading one are summed in float32.  Sixteen tokens cost the gathers of one.
+//
+// What bounds it is the gathers: each sub-vector is one L1 miss into L2, and a
+// CU keeps about 64 of them in flight.  Neighbouring lanes fetch the two halves
+// of one centroid row in one instruction (one request, not two) and swap them.
+// Indices are read 16 bytes (eight sub-vectors) a lane.
+//
+// A workgroup owns 16 rows; its waves take blocks of 32 sub-vectors in turn and
+// their sums are added in wave order.  Where the rows alone leave CUs idle the
+// blocks are split over workgroups too, and a second kernel adds the parts in
+// order.  The sparse correction adds sum_e delta_e x[col_e] per row, delta
+// being the exact value less the decoded weight, made once per matrix.
+#include "vq_ffn.h"
+
+#include <algorithm>
+#include <cstring>
+#include <string>
+
+namespace vq {
+namespace {
+
+typedef Bf16::V8 V8;
+
+constexpr int kQRows = 16;
+constexpr int kC2Floats = 2048;            // residual codebooks up to 8 KB are held in LDS
+constexpr int kQTokens = 32;               // tokens per launch
+
+struct QMat {
+    const float* C1;
+    const uint16_t* idx1;
+    const float* C2;
+    const uint16_t* idx2;
+    const float* rs;
+    const float* cs;
+    const int32_t* row_ptr;
+    const int32_t* col;
+    const float* delta;
+    int K1, K2;
+};
+
+struct QArgs {
+    QMat q[2];
+    int64_t M, N, nb;
+    int d, T, splits;
+    const void* X;
+    int64_t ldx;
+    int dtype, act;
+    const void* bias[2];
+    const void* R;
+    int64_t ldr;
+    void* Y;
+    int64_t ldy;
+    float* part;               // [splits][matrices][T][M], or null
+};
+
+template <int XT> struct XType;
+template <> struct XType<VQ_BF16> { typedef __bf16 E; static constexpr int kTerms = 1, kWTerms = 2; };
+template <> struct XType<VQ_F16> { typedef _Float16 E; static constexpr int kTerms = 2, kWTerms = 2; };
+template <> struct XType<VQ_F32> { typedef float E; static constexpr int kTerms = 3, kWTerms = 3; };
+
+__device__ inline int swap_pair(int v) { return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true); }
+__device__ inline float swap_pair(float v) { return __int_as_float(swap_pair(__float_as_int(v))); }
+
+// v = t[0] + t[1] + ... in bf16 terms, each rounded to nearest.
+template <int NTERM>
+__device__ inline void split(const float (&v)[8], V8 (&t)[NTERM])
+{
+    float rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < NTERM; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            t[k][i] = (__bf16)rest[i];
+            if (k + 1 < NTERM) rest[i] = rest[i] - (float)t[k][i];
+        }
+}
+
+// Eight consecutive values at an element-aligned address (the hardware takes
+// unaligned vector loads).
+template <class E, int N>
+__device__ inline void load_n(const E* p, float (&v)[8])
+{
+    E e[N];
+    __builtin_memcpy(e, p, sizeof(E) * N);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = (float)e[i];
+}
+
+// Tokens' terms for the chunk of columns at `col` (n of them valid).
+template <int XT>
+__device__ inline void load_tokens(const QArgs& a, int t, int64_t col, int n, V8 (&x)[XType<XT>::kTerms])
+{
+    typedef typename XType<XT>::E E;
+    float v[8] = {};
+    if (t < a.T && n > 0) {
+        const E* p = static_cast<const E*>(a.X) + t * a.ldx + col;
+        if (n == 8) {
+            load_n<E, 8>(p, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) v[i] = (float)p[i];
+        }
+    }
+    split<XType<XT>::kTerms>(v, x);
+}
+
+template <class E> __device__ inline float load_x(const void* p, int64_t i) { return (float)static_cast<const E*>(p)[i]; }
+
+__device__ inline float load_any(const void* p, int64_t i, int dtype)
+{
+    return dtype == VQ_F32 ? load_x<float>(p, i) : dtype == VQ_BF16 ? load_x<__bf16>(p, i) : load_x<_Float16>(p, i);
+}
+
+__device__ inline void store_any(void* p, int64_t i, int dtype, float v)
+{
+    if (dtype == VQ_F32) static_cast<float*>(p)[i] = v;
+    else if (dtype == VQ_BF16) static_cast<__bf16*>(p)[i] = (__bf16)v;
+    else static_cast<_Float16*>(p)[i] = (_Float16)v;
+}
+
+// Eight indices from sub-vector s of a row (nb in the row), below K; past the row's end 0.
+__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, int K, int (&k)[8])
+{
+    uint16_t v[8] = {};
+    if (s + 8 <= nb) {
+        __builtin_memcpy(v, row + s, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s + i < nb) v[i] = row[s + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = v[i] < K ? v[i] : K - 1;
+}
+
+// D = 8 or 4: sub-vectors of that length in 16-byte aligned codebooks.  D = 0: any
+// d, one sub-vector per chunk of eight k slots.
+template <int D, int XT, int NT, int NM>
+__global__ __launch_bounds__(512) void k_qffn(const QArgs a)
+{
+    constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
+    constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
+    extern __shared__ __align__(16) float lds[];
+    const int d = D ? D : a.d;
+    const int nwaves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.x * kQRows;
+    const int64_t row = row0 + r < a.M ? row0 + r : a.M - 1;
+
+    // residual codebooks
+    int c2_at[2] = {-1, -1}, used = 0;
+    for (int m = 0; m < NM; ++m)
+        if (a.q[m].C2 && a.q[m].K2 * d <= kC2Floats) {
+            c2_at[m] = used;
+            for (int i = threadIdx.x; i < a.q[m].K2 * d; i += blockDim.x) lds[used + i] = a.q[m].C2[i];
+            used += (a.q[m].K2 * d + 3) & ~3;
+        }
+    __syncthreads();
+
+    f32x4 acc[NM][NT];
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int nkb = (int)((a.nb + 31) / 32);
+    const int kb0 = (int)((int64_t)nkb * blockIdx.y / a.splits), kb1 = (int)((int64_t)nkb * (blockIdx.y + 1) / a.splits);
+    for (int kb = kb0 + wave; kb < kb1; kb += nwaves) {
+        const int64_t s = (int64_t)kb * 32 + g * 8;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const QMat& q = a.q[m];
+            int k1[8], k2[8];
+            load_indices(q.idx1 + row * a.nb, s, a.nb, q.K1, k1);
+            if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, q.K2, k2);
+            const float* c2 = c2_at[m] >= 0 ? lds + c2_at[m] : q.C2;
+            // gathers first: all of the block's rows are requested before any is used
+            constexpr int G = D == 0 ? 1 : 8;
+            f32x4 ga[G], gb[G];
+            if (D == 8) {
+                const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const int other = swap_pair(k1[j]);
+                    const int odd = lane & 1;
+                    ga[j] = C[2 * (odd ? other : k1[j]) + odd];
+                    gb[j] = C[2 * (odd ? k1[j] : other) + odd];
+                }
+            } else if (D == 4) {
+                const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
+#pragma unroll
+                for (int j = 0; j < G; ++j) ga[j] = C[k1[j]];
+            }
+#pragma unroll
+            for (int j = 0; j < 8 / U; ++j) {
+                float w[8] = {};
+                const int64_t sv = s + j * U;
+                const int64_t col = sv * d;
+                const int left = (int)(a.nb - sv < U ? (a.nb - sv < 0 ? 0 : a.nb - sv) : U) * d;    // valid columns
+                if (D == 8) {
+                    const int odd = lane & 1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float other = swap_pair(odd ? ga[j][i] : gb[j][i]);
+                        w[i] = odd ? other : ga[j][i];
+                        w[4 + i] = odd ? gb[j][i] : other;
+                    }
+                } else if (D == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = ga[(j * 2) % G][i];
+                        w[4 + i] = ga[(j * 2 + 1) % G][i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < d) w[i] = q.C1[(int64_t)k1[j] * d + i];
+                }
+                if (q.C2) {
+                    if (D) {
+                        constexpr int H = D == 8 ? 0 : 1;          // second half: the same row or the next index
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + (int64_t)k2[j * U + h * H] * D + (D == 8 ? h * 4 : 0));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[h * 4 + i] += v[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < d) w[i] += c2[(int64_t)k2[j] * d + i];
+                    }
+                }
+                if (q.cs) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < left) w[i] *= q.cs[col + i];
+                }
+                V8 wt[WTERMS];
+                split<WTERMS>(w, wt);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    V8 xt[XTERMS];
+                    load_tokens<XT>(a, n * 16 + r, col, left, xt);
+#pragma unroll
+                    for (int p = 0; p < WTERMS; ++p)
+#pragma unroll
+                        for (int t = 0; t < XTERMS; ++t)
+                            if (p + t < WTERMS) acc[m][n] = Bf16::mfma(wt[p], xt[t], acc[m][n]);
+                }
+            }
+        }
+    }
+
+    // sums over the waves, in wave order; the sparse corrections beside them
+    float* red = lds + used;                                   // [nwaves][NM][NT][64] of four rows
+    float* corr = red + nwaves * NM * NT * 256;                // [NM][NT * 16][16]
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<f32x4*>(red + (((wave * NM + m) * NT + n) * 64 + lane) * 4) = acc[m][n];
+    int tl = 1;                                                // lanes across tokens
+    while (tl < a.T) tl *= 2;
+    for (int job = wave; job < NM * kQRows; job += nwaves) {
+        const int m = job / kQRows, rr = job % kQRows;
+        const QMat& q = a.q[m];
+        const int t = lane & (tl - 1);
+        float c = 0.0f;
+        if (q.row_ptr && blockIdx.y == 0 && row0 + rr < a.M && t < a.T) {
+            const int e1 = q.row_ptr[row0 + rr + 1];
+            for (int e = q.row_ptr[row0 + rr] + lane / tl; e < e1; e += 64 / tl) {
+                const int j = q.col[e];
+                if ((uint32_t)j < (uint64_t)a.N)
+                    c = fmaf(q.delta[e], load_x<typename XType<XT>::E>(a.X, t * a.ldx + j), c);
+            }
+        }
+        for (int o = 32; o >= tl; o >>= 1) c += __shfl_xor(c, o, 64);
+        if (lane < tl && lane < NT * 16) corr[(m * NT * 16 + lane) * kQRows + rr] = c;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 256; i += blockDim.x) {
+        // item i of the accumulators: fragment n, lane l, element e -> token, row
+        const int n = i >> 8, l = (i >> 2) & 63, e = i & 3;
+        const int t = n * 16 + (l & 15), rr = (l >> 4) * 4 + e;
+        const int64_t out_row = row0 + rr;
+        if (t >= a.T || out_row >= a.M) continue;
+        float z[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            float v = 0.0f;
+            for (int w = 0; w < nwaves; ++w) v += red[((w * NM + m) * NT + n) * 256 + (i & 255)];
+            if (a.q[m].rs) v *= a.q[m].rs[out_row];
+            z[m] = v + corr[(m * NT * 16 + t) * kQRows + rr];
+            if (a.part) a.part[(((int64_t)blockIdx.y * NM + m) * a.T + t) * a.M + out_row] = z[m];
+            else if (a.bias[m]) z[m] += load_any(a.bias[m], out_row, XT);
+        }
+        if (a.part) continue;
+        float y = act_full(a.act, z[0]);
+        if (NM > 1) y *= z[NM - 1];
+        if (a.R) y += load_any(a.R, t * a.ldr + out_row, XT);
+        store_any(a.Y, t * a.ldy + out_row, XT, y);
+    }
+}
+
+// Adds the parts in order and applies the epilogue.
+template <int NM>
+__global__ __launch_bounds__(256) void k_qffn_finish(const QArgs a)
+{
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t n = (int64_t)a.T * a.M;
+    if (e >= n) return;
+    const int64_t t = e / a.M, row = e - t * a.M;
+    float z[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        float v = 0.0f;
+        for (int s = 0; s < a.splits; ++s) v += a.part[((int64_t)s * NM + m) * n + e];
+        z[m] = a.bias[m] ? v + load_any(a.bias[m], row, a.dtype) : v;
+    }
+    float y = act_full(a.act, z[0]);
+    if (NM > 1) y *= z[NM - 1];
+    if (a.R) y += load_any(a.R, t * a.ldr + row, a.dtype);
+    store_any(a.Y, t * a.ldy + row, a.dtype, y);
+}
+
+// delta_e = val_e - decoded weight at e (each step rounded as the
+// reconstruction rounds it, then the difference).
+__global__ __launch_bounds__(256) void k_sparse_delta(int64_t M, int64_t N, int64_t nb, int d, const float* __restrict__ C1,
+                                                      int K1, const uint16_t* __restrict__ idx1,
+                                                      const float* __restrict__ C2, int K2,
+                                                      const uint16_t* __restrict__ idx2, const float* __restrict__ rs,
+                                                      const float* __restrict__ cs, const int32_t* __restrict__ row_ptr,
+                                                      const int32_t* __restrict__ col, const float* __restrict__ val,
+                                                      float* __restrict__ delta)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (i >= M) return;
+    const int e1 = row_ptr[i + 1];
+    for (int e = row_ptr[i] + lane; e < e1; e += 64) {
+        const int64_t j = col[e];
+        float w = 0.0f;
+        if (j >= 0 && j < N) {
+            const int64_t s = j / d;
+            const int t = (int)(j - s * d);
+            const int k1 = idx1[i * nb + s];
+            w = C1[(int64_t)(k1 < K1 ? k1 : K1 - 1) * d + t];
+            if (C2) {
+                const int k2 = idx2[i * nb + s];
+                w = w + C2[(int64_t)(k2 < K2 ? k2 : K2 - 1) * d + t];
+            }
+            if (cs) w = w * cs[j];
+            if (rs) w = w * rs[i];
+        }
+        delta[e] = val[e] - w;
+    }
+}
+
+// ---- plan ---------------------------------------------------------------
+struct QPlan {
+    int waves, splits;
+    int64_t groups;
+};
+
+// Row groups first; where they leave fewer than two workgroups a CU, the blocks
+// of 32 sub-vectors are split over up to 16 workgroups (one block a wave at
+// least).
+QPlan q_plan(int64_t M, int64_t nb)
+{
+    QPlan p;
+    p.groups = (M + kQRows - 1) / kQRows;
+    const int64_t nkb = (nb + 31) / 32;
+    p.waves = nkb >= 4 ? 8 : 4;
+    p.splits = 1;
+    while (p.splits < 16 && p.groups * p.splits < 512 && nkb >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+    return p;
+}
+
+size_t q_workspace(int64_t M, int64_t nb, int64_t T, int nm)
+{
+    const QPlan p = q_plan(M, nb);
+    const int64_t t = T < kQTokens ? T : kQTokens;
+    return p.splits > 1 ? align_up((size_t)p.splits * nm * t * M * sizeof(float)) : 0;
+}
+
+template <int D, int XT, int NT, int NM>
+vq_status q_launch(const QArgs& a, const QPlan& p, hipStream_t st)
+{
+    size_t lds = 0;
+    for (int m = 0; m < NM; ++m)
+        if (a.q[m].C2 && a.q[m].K2 * a.d <= kC2Floats) lds += (a.q[m].K2 * a.d + 3) & ~3;
+    lds = (lds + (size_t)p.waves * NM * NT * 256 + (size_t)NM * NT * 16 * kQRows) * sizeof(float);
+    hipLaunchKernelGGL((k_qffn<D, XT, NT, NM>), dim3((unsigned)p.groups, p.splits), dim3(p.waves * 64), lds, st, a);
+    VQ_LAUNCHED("k_qffn");
+    return VQ_OK;
+}
+
+template <int D, int XT, int NT>
+vq_status q_matrices(const QArgs& a, const QPlan& p, int nm, hipStream_t st)
+{
+    return nm == 2 ? q_launch<D, XT, NT, 2>(a, p, st) : q_launch<D, XT, NT, 1>(a, p, st);
+}
+
+template <int D, int XT>
+vq_status q_tokens(const QArgs& a, const QPlan& p, int nm, hipStream_t st)
+{
+    return a.T > 16 ? q_matrices<D, XT, 2>(a, p, nm, st) : q_matrices<D, XT, 1>(a, p, nm, st);
+}
+
+template <int D>
+vq_status q_type(const QArgs& a, const QPlan& p, int nm, hipStream_t st)
+{
+    switch (a.dtype) {
+    case VQ_BF16: return q_tokens<D, VQ_BF16>(a, p, nm, st);
+    case VQ_F16: return q_tokens<D, VQ_F16>(a, p, nm, st);
+    default: return q_tokens<D, VQ_F32>(a, p, nm, st);
+    }
+}
+
+vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
+{
+    const QPlan p = q_plan(a.M, a.nb);
+    a.splits = p.splits;
+    a.part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
+    bool vec = a.d == 8 || a.d == 4;
+    for (int m = 0; m < nm; ++m) vec = vec && aligned16(a.q[m].C1) && (!a.q[m].C2 || aligned16(a.q[m].C2));
+    const size_t e = a.dtype == VQ_F32 ? 4 : 2;
+    const char* X = static_cast<const char*>(a.X);
+    const char* R = static_cast<const char*>(a.R);
+    char* Y = static_cast<char*>(a.Y);
+    for (int64_t t0 = 0; t0 < T; t0 += kQTokens) {
+        a.T = (int)(T - t0 < kQTokens ? T - t0 : kQTokens);
+        a.X = X + t0 * a.ldx * e;
+        a.R = R ? R + t0 * a.ldr * e : nullptr;
+        a.Y = Y + t0 * a.ldy * e;
+        VQ_TRY(vec && a.d == 8 ? q_type<8>(a, p, nm, st) : vec ? q_type<4>(a, p, nm, st) : q_type<0>(a, p, nm, st));
+        if (a.part) {
+            const dim3 grid(grid_for((int64_t)a.T * a.M, 256));
+            if (nm == 2) hipLaunchKernelGGL(k_qffn_finish<2>, grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL(k_qffn_finish<1>, grid, dim3(256), 0, st, a);
+            VQ_LAUNCHED("k_qffn_finish");
+        }
+    }
+    return VQ_OK;
+}
+
+vq_status check_qmatrix(const std::string& call, const vq_qmatrix* Q)
+{
+    VQ_CHECK(Q != nullptr, call + ": matrix is null");
+    VQ_TRY(check_shape(Q->M, Q->N, Q->d));
+    const int64_t n_sub = Q->M * Q->N / Q->d;
+    VQ_TRY(check_K(Q->K1, n_sub));
+    VQ_CHECK(Q->C1 && Q->idx1, call + ": null pointer");
+    if (Q->C2) {
+        VQ_TRY(check_K(Q->K2, n_sub));
+        VQ_CHECK(Q->idx2 != nullptr, call + ": idx2 is null");
+    }
+    return VQ_OK;
+}
+
+vq_status check_call(const std::string& call, const vq_qmatrix* Q, int64_t T, int dtype, int act, const void* X, int64_t ldx,
+                     const void* Y, int64_t ldy)
+{
+    VQ_TRY(check_qmatrix(call, Q));
+    VQ_CHECK(!Q->row_ptr || (Q->col && Q->delta), call + ": the sparse part needs col and delta");
+    VQ_CHECK(T >= 0 && T <= (1 << 28), call + ": T must be in [0, 2^28]");
+    VQ_CHECK(dtype >= VQ_BF16 && dtype <= VQ_F32, call + ": dtype must be VQ_BF16, VQ_F16 or VQ_F32");
+    VQ_CHECK(act >= VQ_ACT_NONE && act <= VQ_ACT_SIGMOID, call + ": unknown activation");
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(X && Y, call + ": null pointer");
+    VQ_CHECK(ldx >= Q->N && ldx <= ((int64_t)1 << 40), call + ": leading dimension of X is out of range");
+    VQ_CHECK(ldy >= Q->M && ldy <= ((int64_t)1 << 40), call + ": leading dimension of the output is out of range");
+    const uintptr_t mis = dtype == VQ_F32 ? 3 : 1;
+    VQ_CHECK(((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y)) & mis) == 0,
+             call + ": a tensor is not aligned to its elements");
+    VQ_CHECK(X != Y, call + ": the output may not alias X");
+    return VQ_OK;
+}
+
+vq_status check_qvalues(const char* call, const vq_qmatrix* Q, hipStream_t stream)
+{
+    VQ_VALUES(Q->C1, (int64_t)Q->K1 * Q->d, false, call, "C1");
+    VQ_VALUES(Q->C2, (int64_t)Q->K2 * Q->d, false, call, "C2");
+    VQ_VALUES(Q->rscale, Q->M, false, call, "rscale");
+    VQ_VALUES(Q->cscale, Q->N, false, call, "cscale");
+    return VQ_OK;
+}
+
+QMat device_matrix(const vq_qmatrix* Q)
+{
+    return {Q->C1, Q->idx1, Q->C2, Q->idx2, Q->rscale, Q->cscale, Q->row_ptr, Q->col, Q->delta, Q->K1, Q->C2 ? Q->K2 : 0};
+}
+
+}  // namespace
+}  // namespace vq
+
+using namespace vq;
+
+extern "C" {
+
+vq_status vq_sparse_delta(const vq_qmatrix* Q, const float* val, float* delta, void* stream)
+{
+    const char* call = "vq_sparse_delta";
+    VQ_TRY(check_qmatrix(call, Q));
+    VQ_CHECK(Q->row_ptr && Q->col && val && delta, "vq_sparse_delta: null pointer");
+    VQ_TRY(check_device());
+    VQ_TRY(check_qvalues(call, Q, as_stream(stream)));
+    hipLaunchKernelGGL(k_sparse_delta, dim3(grid_for(Q->M, 4)), dim3(256), 0, as_stream(stream), Q->M, Q->N, Q->N / Q->d, Q->d,
+                       Q->C1, Q->K1, Q->idx1, Q->C2, Q->K2, Q->idx2, Q->rscale, Q->cscale, Q->row_ptr, Q->col, val, delta);
+    VQ_LAUNCHED("k_sparse_delta");
+    return VQ_OK;
+}
+
+size_t vq_qlinear_workspace_bytes(int64_t M, int64_t N, int d, int64_t T)
+{
+    if (T <= 0 || check_shape(M, N, d) != VQ_OK) return 0;
+    return q_workspace(M, N / d, T, 1);
+}
+
+vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const void* X, int64_t ldx, const void* bias,
+                     const void* R, int64_t ldr, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_qlinear";
+    VQ_TRY(check_call(call, Q, T, dtype, act, X, ldx, Y, ldy));
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(!R || ldr >= Q->M, "vq_qlinear: leading dimension of R is below its row length");
+    VQ_CHECK(Y != R || ldy == ldr, "vq_qlinear: Y in place of R needs R's leading dimension");
+    const size_t need = q_workspace(Q->M, Q->N / Q->d, T, 1);
+    VQ_WS(need == 0 || (ws && ws_bytes >= need), "vq_qlinear: workspace too small");
+    VQ_TRY(check_device());
+    VQ_TRY(check_qvalues(call, Q, as_stream(stream)));
+    VQ_TRY(check_matrix(X, T, Q->N, ldx, dtype, call, "X", as_stream(stream)));
+    VQ_TRY(check_matrix(bias, 1, Q->M, Q->M, dtype, call, "bias", as_stream(stream)));
+    VQ_TRY(check_matrix(R, T, Q->M, ldr, dtype, call, "R", as_stream(stream)));
+    QArgs a{};
+    a.q[0] = device_matrix(Q);
+    a.M = Q->M; a.N = Q->N; a.nb = Q->N / Q->d; a.d = Q->d;
+    a.X = X; a.ldx = ldx;
+    a.dtype = dtype; a.act = act;
+    a.bias[0] = bias;
+    a.R = R; a.ldr = ldr;
+    a.Y = Y; a.ldy = ldy;
+    TimedRegion tr("qlinear", Q->K1, as_stream(stream));
+    return q_run(a, T, 1, ws, as_stream(stream));
+}
+
+size_t vq_qgated_workspace_bytes(int64_t M, int64_t N, int d, int64_t T)
+{
+    if (T <= 0 || check_shape(M, N, d) != VQ_OK) return 0;
+    return q_workspace(M, N / d, T, 2);
+}
+
+vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int dtype, int act, const void* X, int64_t ldx,
+                    const void* bg, const void* bu, void* H, int64_t ldh, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_qgated";
+    VQ_TRY(check_call(call, Qg, T, dtype, act, X, ldx, H, ldh));
+    VQ_TRY(check_call(call, Qu, T, dtype, act, X, ldx, H, ldh));
+    VQ_CHECK(Qg->M == Qu->M && Qg->N == Qu->N && Qg->d == Qu->d, "vq_qgated: the matrices differ in M, N or d");
+    if (T == 0) return VQ_OK;
+    const size_t need = q_workspace(Qg->M, Qg->N / Qg->d, T, 2);
+    VQ_WS(need == 0 || (ws && ws_bytes >= need), "vq_qgated: workspace too small");
+    VQ_TRY(check_device());
+    VQ_TRY(check_qvalues(call, Qg, as_stream(stream)));
+    VQ_TRY(check_qvalues(call, Qu, as_stream(stream)));
+    VQ_TRY(check_matrix(X, T, Qg->N, ldx, dtype, call, "X", as_stream(stream)));
+    VQ_TRY(check_matrix(bg, 1, Qg->M, Qg->M, dtype, call, "bg", as_stream(stream)));
+    VQ_TRY(check_matrix(bu, 1, Qg->M, Qg->M, dtype, call, "bu", as_stream(stream)));
+    QArgs a{};
+    a.q[0] = device_matrix(Qg);
+    a.q[1] = device_matrix(Qu);
+    a.M = Qg->M; a.N = Qg->N; a.nb = Qg->N / Qg->d; a.d = Qg->d;
+    a.X = X; a.ldx = ldx;
+    a.dtype = dtype; a.act = act;
+    a.bias[0] = bg; a.bias[1] = bu;
+    a.Y = H; a.ldy = ldh;
+    TimedRegion tr("qgated", Qg->K1, as_stream(stream));
+    return q_run(a, T, 2, ws, as_stream(stream));
+}
+
+}  // extern "C"

@@ -62,6 +62,11 @@ class GroupedOutputs(ctypes.Structure):
                 ("mask", _P), ("W_hat", _P), ("J_hist", _P), ("bpw", _P)]
 
 
+class QMatrixStruct(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("d", _I), ("K1", _I), ("K2", _I), ("C1", _P), ("idx1", _P), ("C2", _P),
+                ("idx2", _P), ("rscale", _P), ("cscale", _P), ("row_ptr", _P), ("col", _P), ("delta", _P)]
+
+
 # name -> (restype, argtypes); every symbol declared in include/vq.h
 SIGNATURES = {
     "vq_version": (ctypes.c_char_p, []),
@@ -107,6 +112,11 @@ SIGNATURES = {
     "vq_gated_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I]),
     "vq_gated_backward": (_I, [_I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64,
                                _P, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "vq_sparse_delta": (_I, [_P, _P, _P, _P]),
+    "vq_qlinear_workspace_bytes": (_SZ, [_I64, _I64, _I, _I64]),
+    "vq_qlinear": (_I, [_P, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "vq_qgated_workspace_bytes": (_SZ, [_I64, _I64, _I, _I64]),
+    "vq_qgated": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P, _P, _P, _I64, _P, _SZ, _P]),
     "vq_timing_enable": (None, [_I]),
     "vq_timing_count": (_I, []),
     "vq_timing_get": (_I, [_I, ctypes.c_char_p, _I, ctypes.POINTER(_I), ctypes.POINTER(_I64),
@@ -633,3 +643,99 @@ def gated_backward(dH, X, W_gate, W_up, G, U, act="silu", want_dx=True, want_dw=
     _check(lib.vq_gated_backward(T, M, N, dt, a, dh, lddh, x, ldx, wg, wu, ldw, g, u, ldz, _ptr(dX), N, _ptr(dWg),
                                  _ptr(dWu), N, _ptr(dbg), _ptr(dbu), p, n, _stream()))
     return dX, dWg, dWu, dbg, dbu
+
+
+# ---- feed-forward calls on compressed matrices --------------------------------
+
+class QMatrix:
+    """A compressed matrix as a serving program keeps it.
+
+    Takes the arrays of a fit (codebooks, indices, scales, sparse correction)
+    and makes the sparse part's differences to the decoded weights once, on the
+    current stream.  Holds references to the arrays; call refresh() after
+    changing any of them in place.
+    """
+
+    def __init__(self, M, N, d, C1, idx1, C2=None, idx2=None, rscale=None, cscale=None, row_ptr=None, col=None, val=None):
+        n_sub = M * N // d if d else 0
+        for t, dt, n, name in ((C1, torch.float32, None, "C1"), (C2, torch.float32, None, "C2"),
+                               (idx1, torch.uint16, n_sub, "idx1"), (idx2, torch.uint16, n_sub, "idx2"),
+                               (rscale, torch.float32, M, "rscale"), (cscale, torch.float32, N, "cscale"),
+                               (row_ptr, torch.int32, M + 1, "row_ptr"), (col, torch.int32, None, "col"),
+                               (val, torch.float32, None, "val")):
+            _dtype(t, dt, name)
+            if t is not None and n is not None and t.numel() != n:
+                raise ValueError("%s must have %d elements, got %d" % (name, n, t.numel()))
+        for t, name in ((C1, "C1"), (C2, "C2")):
+            if t is not None and (t.dim() != 2 or t.shape[1] != d):
+                raise ValueError("%s must be [K x %d], got %s" % (name, d, list(t.shape)))
+        if (C2 is None) != (idx2 is None):
+            raise ValueError("C2 and idx2 come together")
+        sparse = row_ptr is not None and col is not None and col.numel() > 0
+        if sparse and (val is None or val.numel() != col.numel()):
+            raise ValueError("val must have as many elements as col")
+        self.M, self.N, self.d = int(M), int(N), int(d)
+        self.val = val if sparse else None
+        self.delta = torch.empty_like(val) if sparse else None
+        self._keep = (C1, idx1, C2, idx2, rscale, cscale, row_ptr, col)
+        self._struct = QMatrixStruct(M, N, d, C1.shape[0], 0 if C2 is None else C2.shape[0], _ptr(C1), _ptr(idx1),
+                                     _ptr(C2), _ptr(idx2), _ptr(rscale), _ptr(cscale), _ptr(row_ptr) if sparse else None,
+                                     _ptr(col) if sparse else None, _ptr(self.delta))
+        self._ref = ctypes.addressof(self._struct)
+        self.device = C1.device
+        self.refresh()
+
+    @classmethod
+    def from_fit(cls, out, M, N, d):
+        """From the dict that fit returns."""
+        return cls(M, N, d, out["C1"], out["idx1"], out["C2"], out["idx2"], out.get("rscale"), out.get("cscale"),
+                   out["row_ptr"], out["col"], out["val"])
+
+    def refresh(self):
+        """Makes the sparse differences again (current stream)."""
+        if self.delta is not None:
+            _check(load().vq_sparse_delta(self._ref, _ptr(self.val), _ptr(self.delta), _stream()))
+
+
+def _any_dtype(t, name):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be torch.bfloat16, torch.float16 or torch.float32, got %s" % (name, t.dtype))
+    return code
+
+
+def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
+    """Y = act(X W^T + bias) + residual with W = the QMatrix Q, never decoded to memory.
+
+    X [T, N] of bfloat16, float16 or float32; the other tensors have its type.
+    """
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    T, M, N = X.shape[0], Q.M, Q.N
+    dt, a = _any_dtype(X, "X"), _act(act)
+    x, ldx = _matrix(X, T, N, X.dtype, "X")
+    b = _vector(bias, M, X.dtype, "bias")
+    r, ldr = _matrix(residual, T, M, X.dtype, "residual")
+    Y = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    y, ldy = _matrix(Y, T, M, X.dtype, "out")
+    lib = load()
+    p, n, ws = _scratch(lib.vq_qlinear_workspace_bytes(M, N, Q.d, T), ws, X.device)
+    _check(lib.vq_qlinear(Q._ref, T, dt, a, x, ldx, b, r, ldr, y, ldy, p, n, _stream()))
+    return Y
+
+
+def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, ws=None):
+    """H = act(X Wg^T + bias_gate) * (X Wu^T + bias_up) with both compressed matrices in one launch."""
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    T, M, N = X.shape[0], Q_gate.M, Q_gate.N
+    dt, a = _any_dtype(X, "X"), _act(act)
+    x, ldx = _matrix(X, T, N, X.dtype, "X")
+    bg = _vector(bias_gate, M, X.dtype, "bias_gate")
+    bu = _vector(bias_up, M, X.dtype, "bias_up")
+    H = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    h, ldh = _matrix(H, T, M, X.dtype, "out")
+    lib = load()
+    p, n, ws = _scratch(lib.vq_qgated_workspace_bytes(M, N, Q_gate.d, T), ws, X.device)
+    _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
+    return H

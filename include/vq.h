@@ -474,6 +474,49 @@ vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act,
                             void* dWg, void* dWu, int64_t lddw, void* dbg, void* dbu,
                             void* ws, size_t ws_bytes, void* stream);
 
+/* Feed-forward calls on compressed matrices (VPTQ page, "End-to-End
+ * Quantization Pipeline": the centroids are looked up inside the product, the
+ * full matrix is never written), for few tokens.  The matrix is the one that
+ * vq_reconstruct writes for the same arrays: decoded codebook rows, scaled,
+ * with the sparse positions overwritten.  The sparse part enters as delta
+ * [nnz] = val - (decoded, scaled weight), which vq_sparse_delta writes once
+ * per matrix (and again after any of its arrays changed).  C2, idx2, rscale,
+ * cscale and the sparse part (row_ptr, col, delta) may be NULL.  Indices at or
+ * above K read the codebook's last row; sparse columns outside [0, N) are
+ * skipped.  Columns must be distinct within a row. */
+typedef struct {
+    int64_t M, N;
+    int d;
+    int K1, K2;
+    const float* C1; const uint16_t* idx1;
+    const float* C2; const uint16_t* idx2;
+    const float* rscale; const float* cscale;
+    const int32_t* row_ptr; const int32_t* col; const float* delta;
+} vq_qmatrix;
+
+/* delta[e] = val[e] - decoded weight at entry e (Q->delta is not read). */
+vq_status vq_sparse_delta(const vq_qmatrix* Q, const float* val, float* delta, void* stream);
+
+/* Y = act(X W^T + bias) + R and H = act(X Wg^T + bg) * (X Wu^T + bu) with the
+ * compressed matrices; Qg and Qu have the same M, N and d.  X [T x N], bias, bg,
+ * bu [M] (nullable), R [T x M] (nullable), Y, H [T x M], all of one type
+ * (VQ_BF16, VQ_F16 or VQ_F32), rows with leading dimensions in elements.  T = 0
+ * is a no-op; Y may be R itself (same address and leading dimension), other
+ * overlaps are not allowed.  Float32 sums; before the epilogue, with
+ * S[t,i] = sum_j |W[i,j] x[t,j]| + sum_e |delta_e x[t,col_e]| over the decoded,
+ * scaled W, each sum is within ((N + nnz_i + 64) * 2^-23 + eps) * S of exact,
+ * eps = 2^-16 for the 16-bit types (the decoded weights enter as two bf16 terms)
+ * and 2^-22 for float32 (three terms).  Bitwise reproducible for fixed
+ * arguments.  Every 32 tokens are one pass over the matrix. */
+size_t vq_qlinear_workspace_bytes(int64_t M, int64_t N, int d, int64_t T);
+vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const void* X, int64_t ldx,
+                     const void* bias, const void* R, int64_t ldr, void* Y, int64_t ldy,
+                     void* ws, size_t ws_bytes, void* stream);
+size_t vq_qgated_workspace_bytes(int64_t M, int64_t N, int d, int64_t T);
+vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int dtype, int act,
+                    const void* X, int64_t ldx, const void* bg, const void* bu, void* H, int64_t ldh,
+                    void* ws, size_t ws_bytes, void* stream);
+
 /* Bits per weight of the stored result (host arithmetic; VPTQ page,
  * "End-to-End Quantization Pipeline", compression ratio: index bits plus
  * codebook bits, extended by the sparse part and the scales):

@@ -102,3 +102,72 @@ def test_reference_derivatives_against_differences():
         assert torch.allclose(ref.act_grad(name, z), fd, rtol=0, atol=1e-8), name
         assert float(ref.act_grad(name, z).abs().max()) <= ref.LIPSCHITZ
     assert math.isclose(float(ref.act("gelu", torch.tensor(1.0, dtype=torch.float64))), 0.8413447460685429, rel_tol=1e-12)
+
+
+def qmatrix(**change):
+    f = dict(M=32, N=64, d=8, K1=16, K2=0, C1=FAKE, idx1=FAKE + 4096, C2=None, idx2=None, rscale=None, cscale=None,
+             row_ptr=None, col=None, delta=None)
+    f.update(change)
+    return vq.QMatrixStruct(*[f[k] for k, _ in vq.QMatrixStruct._fields_])
+
+
+@pytest.mark.parametrize("change,msg", [
+    (dict(M=0), "positive"), (dict(N=60), "multiple"), (dict(d=9), "d must"), (dict(K1=0), "K must"),
+    (dict(K1=257), "exceeds"), (dict(C1=None), "null"), (dict(idx1=None), "null"),
+    (dict(C2=FAKE, K2=4), "idx2"), (dict(C2=FAKE, idx2=FAKE, K2=0), "K must"),
+    (dict(row_ptr=FAKE), "col and delta"), (dict(row_ptr=FAKE, col=FAKE), "col and delta"),
+])
+def test_compressed_calls_refuse_bad_matrices(change, msg):
+    import ctypes
+    lib = vq.load()
+    good, bad = qmatrix(), qmatrix(**change)
+    X, Y = FAKE + 8192, FAKE + 16384
+    assert lib.vq_qlinear(ctypes.byref(bad), 1, F32, 0, X, 64, None, None, 0, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+    assert msg in lib.vq_last_error().decode()
+    for a, b in ((bad, good), (good, bad)):
+        assert lib.vq_qgated(ctypes.byref(a), ctypes.byref(b), 1, F32, 0, X, 64, None, None, Y, 32, None, 0,
+                             None) == vq.VQ_ERR_INVALID
+
+
+def test_compressed_calls_refuse_bad_arguments():
+    import ctypes
+    lib = vq.load()
+    X, Y = FAKE + 8192, FAKE + 16384
+
+    def qlin(T=1, dt=F32, act=0, X=X, ldx=64, R=None, ldr=32, Y=Y, ldy=32):
+        st = lib.vq_qlinear(ctypes.byref(qmatrix()), T, dt, act, X, ldx, None, R, ldr, Y, ldy, None, 0, None)
+        return st, lib.vq_last_error().decode()
+
+    for kw, msg in ((dict(T=-1), "T must"), (dict(dt=3), "dtype"), (dict(act=7), "activation"), (dict(X=None), "null"),
+                    (dict(Y=None), "null"), (dict(ldx=63), "leading dimension of X"), (dict(ldy=31), "output"),
+                    (dict(R=FAKE, ldr=31), "R"), (dict(Y=X), "alias"), (dict(X=X + 2), "aligned"),
+                    (dict(R=Y, ldr=64), "in place")):
+        st, text = qlin(**kw)
+        assert st == vq.VQ_ERR_INVALID and msg in text, (kw, text)
+    assert lib.vq_qlinear(None, 1, F32, 0, X, 64, None, None, 0, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+    assert lib.vq_qgated(ctypes.byref(qmatrix()), ctypes.byref(qmatrix(M=48)), 1, F32, 0, X, 64, None, None, Y, 48, None, 0,
+                         None) == vq.VQ_ERR_INVALID
+    assert "differ" in lib.vq_last_error().decode()
+    assert lib.vq_sparse_delta(ctypes.byref(qmatrix()), FAKE, FAKE, None) == vq.VQ_ERR_INVALID
+    # rows split over workgroups need their parts' workspace
+    need = lib.vq_qlinear_workspace_bytes(32, 65536, 8, 4)
+    assert need >= 2 * 4 * 32 * 4
+    big = qmatrix(N=65536)
+    assert lib.vq_qlinear(ctypes.byref(big), 4, F32, 0, X, 65536, None, None, 0, Y, 32, FAKE, need - 1,
+                          None) == vq.VQ_ERR_WORKSPACE
+    assert lib.vq_qlinear_workspace_bytes(32, 60, 8, 4) == 0
+
+
+def test_qmatrix_checks():
+    C1 = torch.zeros((16, 8))
+    idx = torch.zeros(32 * 8, dtype=torch.uint16)
+    with pytest.raises(ValueError, match="idx1 must have 256"):
+        vq.QMatrix(32, 64, 8, C1, idx[:-1])
+    with pytest.raises(TypeError, match="idx1 must be"):
+        vq.QMatrix(32, 64, 8, C1, idx.to(torch.int32))
+    with pytest.raises(ValueError, match="C1 must be"):
+        vq.QMatrix(32, 64, 8, C1[:, :4], idx)
+    with pytest.raises(ValueError, match="come together"):
+        vq.QMatrix(32, 64, 8, C1, idx, C2=C1)
+    with pytest.raises(ValueError, match="GPU"):
+        vq.QMatrix(32, 64, 8, C1, idx)
