@@ -13,6 +13,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // 16 x 16 x 32 matrix instruction with float32 accumulation.  Stores round to
 // nearest even once, from float32.
 struct Bf16 {
+    static constexpr int kDtype = VQ_BF16;
     typedef __bf16 E;
     typedef __bf16 V4 __attribute__((ext_vector_type(4)));
     typedef __bf16 V8 __attribute__((ext_vector_type(8)));
@@ -20,6 +21,7 @@ struct Bf16 {
     static __device__ inline V4 lds_tr(__attribute__((address_space(3))) V4* p) { return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(p); }
 };
 struct F16 {
+    static constexpr int kDtype = VQ_F16;
     typedef _Float16 E;
     typedef _Float16 V4 __attribute__((ext_vector_type(4)));
     typedef _Float16 V8 __attribute__((ext_vector_type(8)));
@@ -154,6 +156,22 @@ __device__ inline void load8(const void* base, int64_t ld, int64_t t, int m, int
     }
 }
 
+// The same at any element-aligned address (the hardware takes unaligned vector loads).
+template <class T>
+__device__ inline void load8_any(const void* base, int64_t ld, int64_t t, int m, int M, float (&v)[8])
+{
+    const typename T::E* p = static_cast<const typename T::E*>(base) + t * ld + m;
+    if (m + 8 <= M) {
+        typename T::V8 w;
+        __builtin_memcpy(&w, p, 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = m + i < M ? (float)p[i] : 0.0f;
+    }
+}
+
 // Features m .. m+7 of token t (those below M).
 template <class T>
 __device__ inline void epilogue_one(const Epilogue& e, int64_t t, int m, int M, float (&z)[8])
@@ -206,6 +224,12 @@ __device__ inline void epilogue_pair(const Epilogue& e, int64_t t, int m, int M,
 // Whether rows at p with leading dimension ld can be accessed 16 bytes at a time.
 inline bool vec8_ok(const void* p, int64_t ld) { return p == nullptr || (aligned16(p) && ld % 8 == 0); }
 
+inline void set_vec(Epilogue& e)
+{
+    e.vec = vec8_ok(e.Y, e.ldy) && vec8_ok(e.R, e.ldr) && vec8_ok(e.Z[0], e.ldz) && vec8_ok(e.Z[1], e.ldz) &&
+            vec8_ok(e.bias[0], 0) && vec8_ok(e.bias[1], 0);
+}
+
 // ---- the tiled product --------------------------------------------------
 // out[q, p] = sum over segments and k of P[p, k] Q[q, k] (p contiguous in the
 // output).  An operand is k-contiguous (element (r, k) at r * ld + k) or
@@ -235,5 +259,22 @@ struct GemmArgs {
 
 size_t gemm_workspace(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int nbatch);
 vq_status gemm_launch(const GemmArgs& a, void* ws, size_t ws_bytes, hipStream_t st);
+
+// Adds float32 parts [splits][matrices][nq][pitch] in order and applies the epilogue.
+vq_status finish_parts(int dtype, bool pair, const float* part, int splits, int np, int nq, int pitch, const Epilogue& e,
+                       hipStream_t st);
+
+// ---- few tokens -----------------------------------------------------------
+// The forward products for up to 32 tokens, any strides and alignment.
+struct FewArgs {
+    int64_t T, M, K;
+    int dtype, nm;
+    const void* X; int64_t ldx;
+    const void* W[2]; int64_t ldw;
+    Epilogue epi;
+};
+bool few_tokens(int64_t T);
+size_t few_workspace(int64_t T, int64_t M, int64_t K, int nm);
+vq_status few_product(const FewArgs& f, void* ws, hipStream_t st);
 
 }  // namespace vq

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int
 constexpr int kGradRows = 32;
 template <class T, bool GATED>
 __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const void* dY, int64_t ldy, const void* Z0,
-                                              const void* Z1, int64_t ldz, bool vec, typename T::E* D0,
+                                              const void* Z1, int64_t ldz, typename T::E* D0,
                                               typename T::E* D1, int64_t ldd, float* part0, float* part1)
 {
     __shared__ float sums[GATED ? 2 : 1][4][512];
@@ -90,9 +90,9 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
             const int64_t t = t0 + r;
             if (t >= nt) break;
             float dy[8], z[8], u[8];
-            load8<T>(dY, ldy, t, m, M, vec, dy);
-            if (GATED || act != VQ_ACT_NONE) load8<T>(Z0, ldz, t, m, M, vec, z);
-            if (GATED) load8<T>(Z1, ldz, t, m, M, vec, u);
+            load8_any<T>(dY, ldy, t, m, M, dy);
+            if (GATED || act != VQ_ACT_NONE) load8_any<T>(Z0, ldz, t, m, M, z);
+            if (GATED) load8_any<T>(Z1, ldz, t, m, M, u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float a, da;
@@ -193,6 +193,11 @@ struct Forward {
 vq_status forward(const Forward& f, Arena& ws, bool run, hipStream_t st)
 {
     if (f.T == 0) return VQ_OK;
+    if (few_tokens(f.T)) {
+        void* part = ws.take(few_workspace(f.T, f.M, f.N, f.nm));
+        if (!run) return VQ_OK;
+        return few_product({f.T, f.M, f.N, f.dtype, f.nm, f.X, f.ldx, {f.W[0], f.W[1]}, f.ldw, f.epi}, part, st);
+    }
     Mat x{f.X, f.T, f.N, f.ldx};
     Mat w[2] = {{f.W[0], f.M, f.N, f.ldw}, {f.W[1], f.M, f.N, f.ldw}};
     if (!loads_ok(x)) VQ_TRY(pack(x, ws, run, st));
@@ -231,13 +236,12 @@ vq_status grad_launch(const Backward& b, void* const (&D)[2], int64_t ldd, float
 {
     typedef typename T::E E;
     const dim3 grid((unsigned)((b.M + 511) / 512), (unsigned)((b.T + kGradRows - 1) / kGradRows));
-    const bool vec = vec8_ok(b.dY, b.lddy) && vec8_ok(b.Z[0], b.ldz) && vec8_ok(b.Z[1], b.ldz);
     if (b.nm > 1)
         hipLaunchKernelGGL((k_grad<T, true>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], b.Z[1],
-                           b.ldz, vec, (E*)D[0], (E*)D[1], ldd, part[0], part[1]);
+                           b.ldz, (E*)D[0], (E*)D[1], ldd, part[0], part[1]);
     else
         hipLaunchKernelGGL((k_grad<T, false>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], b.Z[1],
-                           b.ldz, vec, (E*)D[0], (E*)nullptr, ldd, part[0], part[1]);
+                           b.ldz, (E*)D[0], (E*)nullptr, ldd, part[0], part[1]);
     VQ_LAUNCHED("k_grad");
     if (part[0]) {
         hipLaunchKernelGGL((k_bias_sum<T>), dim3((unsigned)((b.M + 15) / 16), b.nm), dim3(256), 0, st, part[0], part[1],

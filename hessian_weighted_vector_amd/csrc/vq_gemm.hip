@@ -274,10 +274,17 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     }
 }
 
-// Sums the splits' partial tiles in order and applies the epilogue; eight
-// features a thread.
+// Adds the parts in order and applies the epilogue; eight features a thread.
+// Not a pair: blockIdx.y is the output (Y[0] or Y[1]).
+struct Finish {
+    const float* part;         // [splits][outputs][nq][pitch]
+    int splits, np, nq, pitch;
+    Epilogue epi;
+    void* Y2;
+};
+
 template <class T, bool PAIR>
-__global__ __launch_bounds__(256) void k_gemm_finish(const Tile a, int nbatch)
+__global__ __launch_bounds__(256) void k_gemm_finish(const Finish a)
 {
     const int64_t per = a.pitch / 8;
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -286,7 +293,7 @@ __global__ __launch_bounds__(256) void k_gemm_finish(const Tile a, int nbatch)
     const int p = (int)(e - q * per) * 8;
     const int64_t plane = (int64_t)a.nq * a.pitch;
     const int b = blockIdx.y;
-    const int nout = PAIR ? 2 : nbatch;
+    const int nout = PAIR ? 2 : gridDim.y;
     const float* o = a.part + q * a.pitch + p + b * plane;
     float s[8] = {}, u[8] = {};
     for (int z = 0; z < a.splits; ++z) {
@@ -310,6 +317,16 @@ __global__ __launch_bounds__(256) void k_gemm_finish(const Tile a, int nbatch)
         if (b) ep.Y = a.Y2;
         epilogue_one<T>(ep, q, p, a.np, s);
     }
+}
+
+template <class T>
+vq_status launch_finish(const Finish& f, bool pair, int nbatch, hipStream_t st)
+{
+    const dim3 grid(grid_for((int64_t)f.nq * (f.pitch / 8), 256), pair ? 1 : nbatch);
+    if (pair) hipLaunchKernelGGL((k_gemm_finish<T, true>), grid, dim3(256), 0, st, f);
+    else hipLaunchKernelGGL((k_gemm_finish<T, false>), grid, dim3(256), 0, st, f);
+    VQ_LAUNCHED("k_gemm_finish");
+    return VQ_OK;
 }
 
 // ---- plan ---------------------------------------------------------------
@@ -371,11 +388,7 @@ vq_status launch_shape(const Tile& t, const Plan& p, int nbatch, hipStream_t st)
     }
     hipLaunchKernelGGL(kern, dim3(p.ntp * p.ntq, p.splits, nbatch), dim3(kThreads), lds, st, t);
     VQ_LAUNCHED("k_gemm");
-    if (p.splits > 1) {
-        hipLaunchKernelGGL((k_gemm_finish<T, PAIR>), dim3(grid_for((int64_t)t.nq * (t.pitch / 8), 256), PAIR ? 1 : nbatch), dim3(256), 0, st,
-                           t, nbatch);
-        VQ_LAUNCHED("k_gemm_finish");
-    }
+    if (p.splits > 1) VQ_TRY(launch_finish<T>({t.part, t.splits, t.np, t.nq, t.pitch, t.epi, t.Y2}, PAIR, nbatch, st));
     return VQ_OK;
 }
 
@@ -399,6 +412,13 @@ vq_status launch_type(GemmKind kind, const Tile& t, const Plan& p, int nbatch, h
 
 }  // namespace
 
+vq_status finish_parts(int dtype, bool pair, const float* part, int splits, int np, int nq, int pitch, const Epilogue& e,
+                       hipStream_t st)
+{
+    const Finish f{part, splits, np, nq, pitch, e, nullptr};
+    return dtype == VQ_BF16 ? launch_finish<Bf16>(f, pair, 1, st) : launch_finish<F16>(f, pair, 1, st);
+}
+
 size_t gemm_workspace(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int nbatch)
 {
     return make_plan(kind, np, nq, K, nseg, nbatch).part_bytes;
@@ -420,9 +440,8 @@ vq_status gemm_launch(const GemmArgs& g, void* ws, size_t ws_bytes, hipStream_t 
     t.seg_steps = p.seg_steps; t.steps = p.steps;
     t.splits = p.splits; t.pitch = p.pitch;
     t.epi = g.epi; t.Y2 = g.Y2;
-    t.epi.vec = vec8_ok(g.epi.Y, g.epi.ldy) && vec8_ok(g.Y2, g.epi.ldy) && vec8_ok(g.epi.R, g.epi.ldr) &&
-                vec8_ok(g.epi.Z[0], g.epi.ldz) && vec8_ok(g.epi.Z[1], g.epi.ldz) && vec8_ok(g.epi.bias[0], 0) &&
-                vec8_ok(g.epi.bias[1], 0);
+    set_vec(t.epi);
+    t.epi.vec = t.epi.vec && vec8_ok(g.Y2, g.epi.ldy);
     if (p.splits > 1) {
         Carver cv(ws, ws_bytes);
         t.part = cv.take<float>(p.part_bytes / sizeof(float));

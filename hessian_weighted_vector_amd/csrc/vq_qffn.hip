@@ -91,34 +91,26 @@ __device__ inline void split(const float (&v)[8], V8 (&t)[NTERM])
         }
 }
 
-// Eight consecutive values at an element-aligned address (the hardware takes
-// unaligned vector loads).
-template <class E, int N>
-__device__ inline void load_n(const E* p, float (&v)[8])
+// Raw tokens of one chunk as loaded, and their terms.  Loads are unconditional
+// (addresses are clamped into the tensor) so that a block's loads can all be in
+// flight; the hardware takes vector loads at any element-aligned address.
+template <int XT> struct RawTokens { typename XType<XT>::E e[8]; };
+
+template <int XT>
+__device__ inline RawTokens<XT> load_tokens(const typename XType<XT>::E* row, int64_t col)
 {
-    E e[N];
-    __builtin_memcpy(e, p, sizeof(E) * N);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = (float)e[i];
+    RawTokens<XT> v;
+    __builtin_memcpy(v.e, row + col, sizeof(v.e));
+    return v;
 }
 
-// Tokens' terms for the chunk of columns at `col` (n of them valid).
 template <int XT>
-__device__ inline void load_tokens(const QArgs& a, int t, int64_t col, int n, V8 (&x)[XType<XT>::kTerms])
+__device__ inline void token_terms(const RawTokens<XT>& v, V8 (&x)[XType<XT>::kTerms])
 {
-    typedef typename XType<XT>::E E;
-    float v[8] = {};
-    if (t < a.T && n > 0) {
-        const E* p = static_cast<const E*>(a.X) + t * a.ldx + col;
-        if (n == 8) {
-            load_n<E, 8>(p, v);
-        } else {
+    float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) v[i] = (float)p[i];
-        }
-    }
-    split<XType<XT>::kTerms>(v, x);
+    for (int i = 0; i < 8; ++i) f[i] = (float)v.e[i];
+    split<XType<XT>::kTerms>(f, x);
 }
 
 template <class E> __device__ inline float load_x(const void* p, int64_t i) { return (float)static_cast<const E*>(p)[i]; }
@@ -135,25 +127,39 @@ __device__ inline void store_any(void* p, int64_t i, int dtype, float v)
     else static_cast<_Float16*>(p)[i] = (_Float16)v;
 }
 
-// Eight indices from sub-vector s of a row (nb in the row), below K; past the row's end 0.
-__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, int K, int (&k)[8])
+// C indices from sub-vector s of a row of nb, two to a register; past the row's end 0.
+template <int C>
+__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, uint32_t (&k)[C / 2])
 {
-    uint16_t v[8] = {};
-    if (s + 8 <= nb) {
-        __builtin_memcpy(v, row + s, 16);
+    if (s + C <= nb) {
+        __builtin_memcpy(k, row + s, C * 2);
     } else {
+        uint16_t v[C] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < C; ++i)
             if (s + i < nb) v[i] = row[s + i];
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = v[i] < K ? v[i] : K - 1;
+        for (int i = 0; i < C / 2; ++i) k[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
+    }
 }
 
-// D = 8 or 4: sub-vectors of that length in 16-byte aligned codebooks.  D = 0: any
-// d, one sub-vector per chunk of eight k slots.
+// Index j of them, at most K - 1.
+template <int C2>
+__device__ inline int index_of(const uint32_t (&k)[C2], int j, int K)
+{
+    const int v = (int)((k[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+    return v < K ? v : K - 1;
+}
+
+// Chunks of eight k slots whose loads a wave has in flight together (registers
+// set it), and the sub-vectors of a row that a wave takes in one step.
+constexpr int chunks_of(int xt, int nt) { return xt == VQ_F32 || nt > 1 ? 2 : 4; }
+constexpr int block_of(int d, int xt, int nt) { return 4 * chunks_of(xt, nt) * (d == 4 ? 2 : 1); }
+
+// D = 8 or 4: sub-vectors of that length in 16-byte aligned codebooks (4: an even
+// number of them in a row).  D = 0: any d, one sub-vector per chunk of eight k slots.
 template <int D, int XT, int NT, int NM>
-__global__ __launch_bounds__(512) void k_qffn(const QArgs a)
+__global__ __launch_bounds__(512, 4) void k_qffn(const QArgs a)
 {
     constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
     constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
@@ -181,85 +187,139 @@ __global__ __launch_bounds__(512) void k_qffn(const QArgs a)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int nkb = (int)((a.nb + 31) / 32);
+    typedef typename XType<XT>::E E;
+    const E* xrow[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)         // tokens past the last read the last: their sums are not stored
+        xrow[n] = static_cast<const E*>(a.X) + (n * 16 + r < a.T ? n * 16 + r : a.T - 1) * a.ldx;
+
+    constexpr int H = chunks_of(XT, NT), B = block_of(D, XT, NT);
+    const int nkb = (int)((a.nb + B - 1) / B);
     const int kb0 = (int)((int64_t)nkb * blockIdx.y / a.splits), kb1 = (int)((int64_t)nkb * (blockIdx.y + 1) / a.splits);
+    uint32_t i1[NM][H * U / 2], i2[NM][H * U / 2];
+    const auto load_block = [&](int kb) {
+        const int64_t s = (int64_t)kb * B + g * (H * U);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            load_indices<H * U>(a.q[m].idx1 + row * a.nb, s, a.nb, i1[m]);
+            if (a.q[m].C2) load_indices<H * U>(a.q[m].idx2 + row * a.nb, s, a.nb, i2[m]);
+        }
+    };
+    if (kb0 + wave < kb1) load_block(kb0 + wave);
+#pragma unroll 1
     for (int kb = kb0 + wave; kb < kb1; kb += nwaves) {
-        const int64_t s = (int64_t)kb * 32 + g * 8;
+        const int64_t s = (int64_t)kb * B + g * (H * U);
+        // columns of chunk j; past the row's end the last chunk's, with zero tokens
+        const auto column = [&](int j) {
+            const int64_t sv = s + j * U, top = a.nb - U;
+            return (sv < top ? sv : top) * d;
+        };
+        RawTokens<XT> x[NT][H];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                if (D) {
+                    x[n][j] = load_tokens<XT>(xrow[n], column(j));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[n][j].e[i] = xrow[n][column(j) + (i < d ? i : d - 1)];
+                }
+            }
+        if ((int64_t)kb * B + B > a.nb) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    if (s + j * U >= a.nb) x[n][j] = RawTokens<XT>{};
+        }
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             const QMat& q = a.q[m];
-            int k1[8], k2[8];
-            load_indices(q.idx1 + row * a.nb, s, a.nb, q.K1, k1);
-            if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, q.K2, k2);
-            const float* c2 = c2_at[m] >= 0 ? lds + c2_at[m] : q.C2;
-            // gathers first: all of the block's rows are requested before any is used
-            constexpr int G = D == 0 ? 1 : 8;
-            f32x4 ga[G], gb[G];
+            float w[H][8];
             if (D == 8) {
                 const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
+                const int odd = lane & 1;
+                f32x4 ga[H], gb[H];
 #pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    const int other = swap_pair(k1[j]);
-                    const int odd = lane & 1;
-                    ga[j] = C[2 * (odd ? other : k1[j]) + odd];
-                    gb[j] = C[2 * (odd ? k1[j] : other) + odd];
+                for (int j = 0; j < H; ++j) {
+                    const int mine = index_of(i1[m], j, q.K1), other = swap_pair(mine);
+                    ga[j] = C[2 * (odd ? other : mine) + odd];
+                    gb[j] = C[2 * (odd ? mine : other) + odd];
                 }
-            } else if (D == 4) {
-                const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
 #pragma unroll
-                for (int j = 0; j < G; ++j) ga[j] = C[k1[j]];
-            }
-#pragma unroll
-            for (int j = 0; j < 8 / U; ++j) {
-                float w[8] = {};
-                const int64_t sv = s + j * U;
-                const int64_t col = sv * d;
-                const int left = (int)(a.nb - sv < U ? (a.nb - sv < 0 ? 0 : a.nb - sv) : U) * d;    // valid columns
-                if (D == 8) {
-                    const int odd = lane & 1;
+                for (int j = 0; j < H; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float other = swap_pair(odd ? ga[j][i] : gb[j][i]);
-                        w[i] = odd ? other : ga[j][i];
-                        w[4 + i] = odd ? gb[j][i] : other;
+                        w[j][i] = odd ? other : ga[j][i];
+                        w[j][4 + i] = odd ? gb[j][i] : other;
                     }
-                } else if (D == 4) {
+            } else if (D == 4) {
+                const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = ga[(j * 2) % G][i];
-                        w[4 + i] = ga[(j * 2 + 1) % G][i];
+                for (int j = 0; j < H; ++j)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const f32x4 v = C[index_of(i1[m], j * 2 + u, q.K1)];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[j][u * 4 + i] = v[i];
                     }
-                } else {
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < d) w[i] = q.C1[(int64_t)k1[j] * d + i];
+                for (int j = 0; j < H; ++j) {
+                    const float* c = q.C1 + (int64_t)index_of(i1[m], j, q.K1) * d;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float v = c[i < d ? i : d - 1];
+                        w[j][i] = i < d ? v : 0.0f;
+                    }
                 }
-                if (q.C2) {
+            }
+            if (q.C2) {
+                const float* c2 = c2_at[m] >= 0 ? lds + c2_at[m] : q.C2;
+#pragma unroll
+                for (int j = 0; j < H; ++j)
                     if (D) {
-                        constexpr int H = D == 8 ? 0 : 1;          // second half: the same row or the next index
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + (int64_t)k2[j * U + h * H] * D + (D == 8 ? h * 4 : 0));
+                        for (int u = 0; u < 2; ++u) {        // halves of one row, or two rows
+                            const int k = index_of(i2[m], j * U + (D == 4 ? u : 0), q.K2);
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + k * D + (D == 8 ? u * 4 : 0));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) w[h * 4 + i] += v[i];
+                            for (int i = 0; i < 4; ++i) w[j][u * 4 + i] += v[i];
                         }
                     } else {
+                        const float* c = c2 + index_of(i2[m], j, q.K2) * d;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < d) w[i] += c2[(int64_t)k2[j] * d + i];
+                        for (int i = 0; i < 8; ++i) {
+                            const float v = c[i < d ? i : d - 1];
+                            w[j][i] += i < d ? v : 0.0f;
+                        }
                     }
-                }
-                if (q.cs) {
+            }
+            if (q.cs) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < left) w[i] *= q.cs[col + i];
+                for (int j = 0; j < H; ++j) {
+                    float c[8];
+                    if (D) {
+                        __builtin_memcpy(c, q.cs + column(j), sizeof(c));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) c[i] = q.cs[column(j) + (i < d ? i : d - 1)];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[j][i] *= c[i];
                 }
+            }
+            if (m == NM - 1 && kb + nwaves < kb1) load_block(kb + nwaves);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
                 V8 wt[WTERMS];
-                split<WTERMS>(w, wt);
+                split<WTERMS>(w[j], wt);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     V8 xt[XTERMS];
-                    load_tokens<XT>(a, n * 16 + r, col, left, xt);
+                    token_terms<XT>(x[n][j], xt);
 #pragma unroll
                     for (int p = 0; p < WTERMS; ++p)
 #pragma unroll
@@ -381,9 +441,8 @@ struct QPlan {
     int64_t groups;
 };
 
-// Row groups first; where they leave fewer than two workgroups a CU, the blocks
-// of 32 sub-vectors are split over up to 16 workgroups (one block a wave at
-// least).
+// Row groups first; where they leave fewer than two workgroups a CU, each row's
+// sub-vectors are split over up to 16 workgroups (at least 32 a wave).
 QPlan q_plan(int64_t M, int64_t nb)
 {
     QPlan p;
@@ -441,7 +500,7 @@ vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
     const QPlan p = q_plan(a.M, a.nb);
     a.splits = p.splits;
     a.part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
-    bool vec = a.d == 8 || a.d == 4;
+    bool vec = a.d == 8 || (a.d == 4 && a.nb % 2 == 0);          // chunks of eight columns
     for (int m = 0; m < nm; ++m) vec = vec && aligned16(a.q[m].C1) && (!a.q[m].C2 || aligned16(a.q[m].C2));
     const size_t e = a.dtype == VQ_F32 ? 4 : 2;
     const char* X = static_cast<const char*>(a.X);
