@@ -19,7 +19,6 @@ namespace vq {
 namespace {
 
 constexpr int kRows = 16;
-constexpr int kFewWaves = 8;
 
 struct Few {
     const char* W[2];
@@ -55,13 +54,14 @@ __device__ inline typename T::V8 chunk_tail(const typename T::E* row, int64_t co
 }
 
 template <class T, int NT, bool PAIR, int H>
-__global__ __launch_bounds__(kFewWaves * 64) void k_few(const Few a)
+__global__ __launch_bounds__(1024) void k_few(const Few a)
 {
     typedef typename T::E E;
     typedef typename T::V8 V8;
     constexpr int NM = PAIR ? 2 : 1;
     constexpr int B = 32 * H;
-    __shared__ float red[kFewWaves * NM * NT * 256];
+    extern __shared__ __align__(16) float red[];                 // [waves][NM][NT][64] of four features
+    const int nwaves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
     const int m0 = blockIdx.x * kRows;
@@ -105,13 +105,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(const Few a)
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll 1
-        for (; kb + kFewWaves < f1; kb += kFewWaves) {
+        for (; kb + nwaves < f1; kb += nwaves) {
             // a chunk's registers are refilled for the next block as soon as they are used
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 multiply(j);
                 __builtin_amdgcn_sched_barrier(0);
-                load(kb + kFewWaves, j);
+                load(kb + nwaves, j);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(const Few a)
     // columns past the last whole block: steps of 32, dealt to the waves of the last split
     if (blockIdx.y == a.splits - 1) {
         const int steps = (int)((a.K - (int64_t)nfull * B + 31) / 32);
-        for (int s = wave; s < steps; s += kFewWaves) {
+        for (int s = wave; s < steps; s += nwaves) {
             const int64_t c = (int64_t)nfull * B + s * 32 + g * 8;
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(const Few a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < kFewWaves; ++k)
+            for (int k = 0; k < nwaves; ++k)
                 v += *reinterpret_cast<const f32x4*>(
                     red + (((k * NM + m) * NT + (t >> 4)) * 64 + (f * 2 + h) * 16 + (t & 15)) * 4);
 #pragma unroll
@@ -167,22 +167,33 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(const Few a)
     }
 }
 
-// At least two workgroups a CU while every wave of every split keeps a block.
-int few_splits(int64_t M, int64_t K)
+// Sixteen waves a workgroup where the rows give less than two workgroups of
+// eight a CU; the columns are split over workgroups where they give less than
+// one of sixteen and every wave of every split keeps a block.
+struct FewPlan { int waves, splits; };
+FewPlan few_plan(int64_t M, int64_t K)
 {
     const int64_t groups = (M + kRows - 1) / kRows, blocks = K / 256;
-    int s = 1;
-    while (s < 16 && groups * s < 512 && blocks >= (int64_t)kFewWaves * s * 2) s *= 2;
-    return s;
+    FewPlan p{groups < 512 && blocks >= 16 ? 16 : 8, 1};
+    while (p.splits < 16 && groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+    return p;
+}
+
+template <class T, int NT, bool PAIR, int H>
+vq_status few_kernel(const Few& a, int waves, hipStream_t st)
+{
+    const dim3 grid((unsigned)((a.M + kRows - 1) / kRows), (unsigned)a.splits);
+    const size_t lds = (size_t)waves * (PAIR ? 2 : 1) * NT * 256 * sizeof(float);
+    hipLaunchKernelGGL((k_few<T, NT, PAIR, H>), grid, dim3(waves * 64), lds, st, a);
+    VQ_LAUNCHED("k_few");
+    return VQ_OK;
 }
 
 template <class T, int NT>
-vq_status few_launch(const Few& a, bool pair, hipStream_t st)
+vq_status few_launch(const Few& a, int waves, bool pair, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.M + kRows - 1) / kRows), (unsigned)a.splits);
-    if (pair) hipLaunchKernelGGL((k_few<T, NT, true, 4>), grid, dim3(kFewWaves * 64), 0, st, a);
-    else hipLaunchKernelGGL((k_few<T, NT, false, NT == 1 ? 8 : 4>), grid, dim3(kFewWaves * 64), 0, st, a);
-    VQ_LAUNCHED("k_few");
+    if (pair) VQ_TRY((few_kernel<T, NT, true, 4>(a, waves, st)));
+    else VQ_TRY((few_kernel<T, NT, false, NT == 1 ? 8 : 4>(a, waves, st)));
     if (a.splits > 1) VQ_TRY(finish_parts(T::kDtype, pair, a.part, a.splits, a.M, a.T, a.pitch, a.epi, st));
     return VQ_OK;
 }
@@ -193,7 +204,7 @@ bool few_tokens(int64_t T) { return T <= 32; }
 
 size_t few_workspace(int64_t T, int64_t M, int64_t K, int nm)
 {
-    const int s = few_splits(M, K);
+    const int s = few_plan(M, K).splits;
     return s > 1 ? align_up((size_t)s * nm * T * ((M + 7) / 8 * 8) * sizeof(float)) : 0;
 }
 
@@ -204,14 +215,15 @@ vq_status few_product(const FewArgs& f, void* ws, hipStream_t st)
     a.X = static_cast<const char*>(f.X);
     a.ldw = f.ldw; a.ldx = f.ldx; a.K = f.K;
     a.M = (int)f.M; a.T = (int)f.T;
-    a.splits = few_splits(f.M, f.K);
+    const FewPlan p = few_plan(f.M, f.K);
+    a.splits = p.splits;
     a.pitch = (int)((f.M + 7) / 8 * 8);
     a.part = a.splits > 1 ? static_cast<float*>(ws) : nullptr;
     a.epi = f.epi;
     set_vec(a.epi);
     const bool pair = f.nm > 1;
-    if (f.dtype == VQ_BF16) return f.T > 16 ? few_launch<Bf16, 2>(a, pair, st) : few_launch<Bf16, 1>(a, pair, st);
-    return f.T > 16 ? few_launch<F16, 2>(a, pair, st) : few_launch<F16, 1>(a, pair, st);
+    if (f.dtype == VQ_BF16) return f.T > 16 ? few_launch<Bf16, 2>(a, p.waves, pair, st) : few_launch<Bf16, 1>(a, p.waves, pair, st);
+    return f.T > 16 ? few_launch<F16, 2>(a, p.waves, pair, st) : few_launch<F16, 1>(a, p.waves, pair, st);
 }
 
 }  // namespace vq

@@ -17,16 +17,16 @@ struct Bf16 {
     typedef __bf16 E;
     typedef __bf16 V4 __attribute__((ext_vector_type(4)));
     typedef __bf16 V8 __attribute__((ext_vector_type(8)));
-    static __device__ inline f32x4 mfma(V8 a, V8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-    static __device__ inline V4 lds_tr(__attribute__((address_space(3))) V4* p) { return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(p); }
+    static __device__ __forceinline__ f32x4 mfma(V8 a, V8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ V4 lds_tr(__attribute__((address_space(3))) V4* p) { return __builtin_amdgcn_ds_read_tr16_b64_v4bf16(p); }
 };
 struct F16 {
     static constexpr int kDtype = VQ_F16;
     typedef _Float16 E;
     typedef _Float16 V4 __attribute__((ext_vector_type(4)));
     typedef _Float16 V8 __attribute__((ext_vector_type(8)));
-    static __device__ inline f32x4 mfma(V8 a, V8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-    static __device__ inline V4 lds_tr(__attribute__((address_space(3))) V4* p)
+    static __device__ __forceinline__ f32x4 mfma(V8 a, V8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ V4 lds_tr(__attribute__((address_space(3))) V4* p)
     {
         typedef short S4 __attribute__((ext_vector_type(4)));
         return __builtin_bit_cast(V4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) S4*)p));

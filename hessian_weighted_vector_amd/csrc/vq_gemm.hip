@@ -31,15 +31,14 @@ constexpr int kWaves = 8;
 constexpr int kWP = 2, kWQ = 4;       // the waves' grid over the tile
 constexpr int kBK = 64;               // k per step
 constexpr uint32_t kOob = 0xC0000000u;     // past every resource's end
-constexpr int64_t kMaxRecords = 0x7fffffff;
 
 // Kernel arguments (one copy in the kernel's argument segment).
 struct Tile {
     const char* P[2];
     const char* Q[2];
     float* part;               // [splits][outputs][nq][pitch] partial sums, or null
-    int64_t ldp, ldq;
-    int64_t kP, kQ;
+    int ldp, ldq;
+    int kP, kQ;
     int np, nq, wp, wq;
     int ntp, ntq;              // tiles
     int seg_steps;             // K steps per segment
@@ -50,12 +49,11 @@ struct Tile {
     void* Y2;
 };
 
-typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(3))) char* lds_ptr;
 
-__device__ inline __amdgpu_buffer_rsrc_t resource(const char* base, int64_t bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* base, int bytes)
 {
-    const int64_t n = bytes < 0 ? 0 : (bytes > kMaxRecords ? kMaxRecords : bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, (int)n, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bytes, 0x00020000);
 }
 
 // Per-lane part of an operand's load addresses and its per-step resource.
@@ -67,48 +65,53 @@ struct Slice {
     static constexpr int kChunks = R / 8;                // 16-byte chunks of a k row (TR)
     static constexpr int kRowsPerLoad = TR ? 512 / R : 8;
 
-    static __device__ inline int swizzle(int row)
+    static __device__ __forceinline__ int swizzle(int row)
     {
         return TR ? (2 * ((row & 3) | ((row >> 1) & 4))) & (kChunks - 1) : row & 7;
     }
 };
 
-// Loads `n` of the slice's wave loads (every kWaves-th from `wave`) into lds.
-// k0: first k of the step within its segment.
+// Issues this wave's loads (every kWaves-th of the slice) of the step that
+// starts at k0 of its segment.  Everything past the matrix, a k0 past K
+// included, arrives as zeros.  Offsets and sizes fit 32 bits: a slice spans at
+// most 256 rows of 2^21 elements.
 template <int R, bool TR, bool PAIR>
-__device__ inline void load_slice(const char* b0, const char* b1, int64_t ld, int row0, int nrows, int width, int64_t k0,
-                                  int64_t K, char* lds, int wave, int lane)
+__device__ __forceinline__ void load_slice(const char* b0, const char* b1, int ld, int row0, int nrows, int width, int k0, int K,
+                                  lds_ptr lds, int wave, int lane)
 {
     typedef Slice<R, TR> S;
+    typedef __attribute__((address_space(3))) void* dst;
     if (!TR) {
         const int rl = lane >> 3;
         const int chunk = (lane & 7) ^ rl;
         uint32_t v = (uint32_t)(rl * ld * 2 + chunk * 16);
         if (k0 + chunk * 8 >= K) v = kOob;
         const int64_t off = (int64_t)row0 * ld * 2;
-        const int64_t bytes = ((int64_t)(nrows - row0 - 1) * ld + K) * 2;
+        const int rows = PAIR ? R / 2 : R;
+        const int bytes = (((nrows - row0 < rows ? nrows - row0 : rows) - 1) * ld + K) * 2;
         const __amdgpu_buffer_rsrc_t r0 = resource(b0 + off, bytes);
         const __amdgpu_buffer_rsrc_t r1 = PAIR ? resource(b1 + off, bytes) : r0;
 #pragma unroll
         for (int j = 0; j < S::kLoads / kWaves; ++j) {
             const int inst = j * kWaves + wave;
             const bool second = PAIR && j >= S::kLoads / kWaves / 2;
-            const int rows = (PAIR && second) ? inst * 8 - R / 2 : inst * 8;
-            const uint32_t so = (uint32_t)(rows * ld * 2 + k0 * 2);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? r1 : r0, (lds_ptr)(lds + inst * 1024), 16, v, so, 0, 0);
+            const uint32_t so = (uint32_t)((second ? inst * 8 - R / 2 : inst * 8) * ld * 2 + k0 * 2);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? r1 : r0, (dst)(lds + inst * 1024), 16, v, so, 0, 0);
         }
     } else {
+        // a wave's loads are a multiple of 16 k rows apart, which the swizzle does not see
+        static_assert(kWaves * S::kRowsPerLoad % 16 == 0, "the loads of a wave share their swizzle");
         const int rl = lane / S::kChunks;
-        const __amdgpu_buffer_rsrc_t r0 =
-            resource(b0 + (k0 * ld + row0) * 2, ((K - k0 - 1) * ld + (width - row0)) * 2);
+        const int chunk = (lane % S::kChunks) ^ S::swizzle(wave * S::kRowsPerLoad + rl);
+        const uint32_t v = (uint32_t)(rl * ld * 2 + chunk * 16);
+        const int rows = K - k0 < kBK ? K - k0 : kBK;
+        const int bytes = rows <= 0 ? 0 : ((rows - 1) * ld + (width - row0)) * 2;
+        const __amdgpu_buffer_rsrc_t r0 = resource(b0 + ((int64_t)k0 * ld + row0) * 2, bytes);
 #pragma unroll
         for (int j = 0; j < S::kLoads / kWaves; ++j) {
             const int inst = j * kWaves + wave;
-            const int row = inst * S::kRowsPerLoad + rl;
-            const int chunk = (lane % S::kChunks) ^ S::swizzle(row);
-            const uint32_t v = (uint32_t)(rl * ld * 2 + chunk * 16);
             const uint32_t so = (uint32_t)(inst * S::kRowsPerLoad * ld * 2);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (lds_ptr)(lds + inst * 1024), 16, v, so, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (dst)(lds + inst * 1024), 16, v, so, 0, 0);
         }
     }
 }
@@ -116,17 +119,17 @@ __device__ inline void load_slice(const char* b0, const char* b1, int64_t ld, in
 // Fragment (16 rows from r0, k = kk*32 .. +31): lane l holds row r0 + l%16,
 // k = kk*32 + 8*(l/16) .. +7.
 template <class T, int R, bool TR>
-__device__ inline typename T::V8 fragment(char* lds, int r0, int kk, int lane)
+__device__ __forceinline__ typename T::V8 fragment(lds_ptr lds, int r0, int kk, int lane)
 {
     typedef Slice<R, TR> S;
     const int i = lane & 15, g = lane >> 4;
     if (!TR) {
         const int row = r0 + i;
-        return *reinterpret_cast<const typename T::V8*>(lds + row * 128 + ((kk * 4 + g) ^ S::swizzle(row)) * 16);
+        return *(const __attribute__((address_space(3))) typename T::V8*)(lds + row * 128 + ((kk * 4 + g) ^ S::swizzle(row)) * 16);
     } else {
         const int row = kk * 32 + g * 8 + (i >> 2);          // second half: row + 4, same swizzle
         const int chunk = (r0 / 8 + ((i & 3) >> 1)) ^ S::swizzle(row);
-        char* p = lds + row * (R * 2) + chunk * 16 + (i & 1) * 8;
+        lds_ptr p = lds + row * (R * 2) + chunk * 16 + (i & 1) * 8;
         typedef __attribute__((address_space(3))) typename T::V4* tr_ptr;
         const typename T::V4 a = T::lds_tr((tr_ptr)p);
         const typename T::V4 b = T::lds_tr((tr_ptr)(p + 4 * R * 2));
@@ -150,71 +153,119 @@ __device__ inline void pick_tile(int id, int n, int ntp, int ntq, int& tp, int& 
     tq = band * G + in % gq;
 }
 
-// Floats per row of the epilogue's LDS tile: the pad spreads a column's rows over the banks.
-constexpr int epilogue_pitch(int fp) { return fp * 16 + 4; }
+// s_waitcnt with the given outstanding vector-memory and LDS counts.
+constexpr int wait_imm(int vm, int lgkm) { return (vm & 15) | (vm >> 4) << 14 | 7 << 4 | lgkm << 8; }
+
+template <class T, bool TRP, bool TRQ, int FP, int FQ, bool PAIR>
+struct Main {
+    static constexpr int BP = kWP * FP * 16, BQ = kWQ * FQ * 16;
+    static constexpr int kBuf = (BP + BQ) * kBK * 2;
+    static constexpr int kLoads = kBuf / 1024 / kWaves;          // a wave's loads per step
+    typedef typename T::V8 V8;
+    struct Frags { V8 p[FP], q[FQ]; };
+
+    // First row (of the tile) of fragment i of wave row wp: in a pair the first
+    // half of the fragments is the gate's, the second the same features of up.
+    static __device__ __forceinline__ int prow(int wp, int i)
+    {
+        return PAIR ? (i < FP / 2 ? wp * (FP / 2) + i : FP + wp * (FP / 2) + i - FP / 2) * 16 : (wp * FP + i) * 16;
+    }
+
+    // Steps s0 .. s1-1 into acc.  A step is two halves of k = 32.  While the
+    // matrix cores work on one half, the next half's fragments are read from LDS,
+    // so a wave waits for LDS only at the start.  One barrier a step, between the
+    // halves: behind it the next step's slices are complete (each wave has waited
+    // for its own loads) and this step's buffer is free (its last fragments are
+    // in registers), so the loads of the step after next go out.
+    static __device__ __forceinline__ void run(const Tile& a, int p0, int q0, int batch, int s0, int s1, int wave, int lane,
+                                               lds_ptr pb0, lds_ptr pb1, lds_ptr qb0, lds_ptr qb1, f32x4 (&acc)[FP][FQ])
+    {
+        const int wp = wave / kWQ, wq = wave % kWQ;
+        const auto issue = [&](int s, lds_ptr pb, lds_ptr qb) __attribute__((always_inline)) {
+            // a step past the last stays in the last segment, past its K
+            const int seg = s >= a.seg_steps && a.steps > a.seg_steps ? 1 : 0;
+            const int k0 = (s - seg * a.seg_steps) * kBK;
+            load_slice<BP, TRP, PAIR>(PAIR ? a.P[0] : a.P[seg], a.P[1], a.ldp, p0, a.np, a.wp, k0, a.kP, pb, wave, lane);
+            load_slice<BQ, TRQ, false>(a.Q[seg + batch], nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, qb, wave, lane);
+        };
+        const auto read = [&](Frags& f, lds_ptr pb, lds_ptr qb, int kk) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) f.q[j] = fragment<T, BQ, TRQ>(qb, (wq * FQ + j) * 16, kk, lane);
+#pragma unroll
+            for (int i = 0; i < FP; ++i) f.p[i] = fragment<T, BP, TRP>(pb, prow(wp, i), kk, lane);
+        };
+        const auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) acc[i][j] = T::mfma(f.p[i], f.q[j], acc[i][j]);
+        };
+        Frags f0, f1;
+        // Loads and reads spread over the products of a half.
+        constexpr int kReads = FP * (TRP ? 2 : 1) + FQ * (TRQ ? 2 : 1), kMfma = FP * FQ;
+        const auto spread = [](int loads) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kMfma; ++i) {
+                const int r0 = kReads * i * 4 / (kMfma * 3), r1 = kReads * (i + 1) * 4 / (kMfma * 3);
+#pragma unroll
+                for (int r = r0; r < r1 && r < kReads; ++r) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (loads * (i + 1) / kMfma > loads * i / kMfma) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+        };
+        const auto step = [&](int s, lds_ptr pc, lds_ptr qc, lds_ptr pn, lds_ptr qn) __attribute__((always_inline)) {
+            read(f1, pc, qc, 1);
+            multiply(f0);
+            spread(0);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+            asm volatile("s_barrier" ::: "memory");
+            read(f0, pn, qn, 0);
+            issue(s + 2, pc, qc);
+            multiply(f1);
+            spread(kLoads);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        issue(s0, pb0, qb0);
+        issue(s0 + 1, pb1, qb1);
+        __builtin_amdgcn_s_waitcnt(wait_imm(kLoads, 0));
+        asm volatile("s_barrier" ::: "memory");
+        read(f0, pb0, qb0, 0);
+        // loads past s1 go out too (nothing uses them): the body stays one block
+#pragma unroll 1
+        for (int s = s0;; s += 2) {
+            step(s, pb0, qb0, pb1, qb1);
+            if (s + 1 >= s1) break;
+            step(s + 1, pb1, qb1, pb0, qb0);
+            if (s + 2 >= s1) break;
+        }
+    }
+};
 
 template <class T, bool TRP, bool TRQ, int FP, int FQ, bool PAIR>
 __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const Tile a)
 {
-    constexpr int BP = kWP * FP * 16, BQ = kWQ * FQ * 16;
-    constexpr int kBuf = (BP + BQ) * kBK * 2;
-    extern __shared__ __align__(1024) char lds[];
+    typedef Main<T, TRP, TRQ, FP, FQ, PAIR> L;
+    // four arrays, not one: the compiler then knows that a fragment is never read
+    // from a buffer that is being filled, and does not wait for those loads
+    __shared__ __align__(1024) char pb0[L::BP * kBK * 2], pb1[L::BP * kBK * 2], qb0[L::BQ * kBK * 2], qb1[L::BQ * kBK * 2];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ntiles = a.ntp * a.ntq;
+    const int wp = wave / kWQ, wq = wave % kWQ;
     const int split = blockIdx.y;
     const int batch = blockIdx.z;
     int tp, tq;
-    pick_tile(blockIdx.x, ntiles, a.ntp, a.ntq, tp, tq);
-    const int p0 = tp * (PAIR ? BP / 2 : BP), q0 = tq * BQ;
+    pick_tile(blockIdx.x, a.ntp * a.ntq, a.ntp, a.ntq, tp, tq);
+    const int p0 = tp * (PAIR ? L::BP / 2 : L::BP), q0 = tq * L::BQ;
     const int s0 = (int)((int64_t)a.steps * split / a.splits), s1 = (int)((int64_t)a.steps * (split + 1) / a.splits);
-
-    const auto issue = [&](int s, int buf) {
-        const int seg = s >= a.seg_steps ? 1 : 0;
-        const int64_t k0 = (int64_t)(s - seg * a.seg_steps) * kBK;
-        char* d = lds + buf * kBuf;
-        load_slice<BP, TRP, PAIR>(PAIR ? a.P[0] : a.P[seg], a.P[1], a.ldp, p0, a.np, a.wp, k0, a.kP, d, wave, lane);
-        load_slice<BQ, TRQ, false>(a.Q[seg + batch], nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, d + BP * kBK * 2, wave,
-                                   lane);
-    };
 
     f32x4 acc[FP][FQ];
 #pragma unroll
     for (int i = 0; i < FP; ++i)
 #pragma unroll
         for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // rows of the tile that fragment i of this wave covers; in a pair the first
-    // half of the fragments is the gate's, the second the same features of up
-    const int wp = wave / kWQ, wq = wave % kWQ;
-    const auto prow = [&](int i) {
-        return PAIR ? (i < FP / 2 ? wp * (FP / 2) + i : FP + wp * (FP / 2) + i - FP / 2) * 16 : (wp * FP + i) * 16;
-    };
-
-    issue(s0, 0);
-    for (int s = s0; s < s1; ++s) {
-        const int buf = (s - s0) & 1;
-        // this wave's loads of the step have landed, its reads of the other buffer are done
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        char* lp = lds + buf * kBuf;
-        char* lq = lp + BP * kBK * 2;
-        typename T::V8 fp[FP][2], fq[FQ][2];
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-            for (int i = 0; i < FP; ++i) fp[i][kk] = fragment<T, BP, TRP>(lp, prow(i), kk, lane);
-#pragma unroll
-            for (int j = 0; j < FQ; ++j) fq[j][kk] = fragment<T, BQ, TRQ>(lq, (wq * FQ + j) * 16, kk, lane);
-        }
-        if (s + 1 < s1) issue(s + 1, buf ^ 1);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int i = 0; i < FP; ++i)
-#pragma unroll
-                for (int j = 0; j < FQ; ++j) acc[i][j] = T::mfma(fp[i][kk], fq[j][kk], acc[i][j]);
-    }
+    L::run(a, p0, q0, batch, s0, s1, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
 
     // lane l: output row l%16 of fragment j, features 4*(l/16) .. +3 of fragment i
     const int q_l = lane & 15, p_l = (lane >> 4) * 4;
@@ -233,6 +284,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
                 if (PAIR) *reinterpret_cast<f32x4*>(o + plane + (int64_t)q * a.pitch + p) = acc[i + NI][j];
             }
         }
+        __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));          // no load into LDS outlives the workgroup
         return;
     }
 
@@ -241,30 +293,39 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     // and a row's lanes write whole cache lines.
     Epilogue e = a.epi;
     if (batch) e.Y = a.Y2;
-    constexpr int kPitch = epilogue_pitch(FP);
+    constexpr int kRow = FP * 16;                   // floats per row of the tile
     constexpr int kLanes = NI * 2;                  // lanes per row
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    float* w = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
+    static_assert(2 * 32 * kRow * 4 <= L::BP * kBK * 2 && L::BP == L::BQ, "two waves' tiles fit one operand buffer");
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));     // the last loads into LDS too
+    asm volatile("s_barrier" ::: "memory");
+    char* const bufs[4] = {pb0, pb1, qb0, qb1};
+    char* w = (wave & 4 ? (wave & 2 ? bufs[3] : bufs[2]) : (wave & 2 ? bufs[1] : bufs[0])) + (wave & 1) * 32 * kRow * 4;
+    // 16-byte chunk c of row r sits in slot c ^ (r & 7)
+    const auto at = [&](int row, int chunk) { return reinterpret_cast<f32x4*>(w + row * kRow * 4 + (chunk ^ (row & 7)) * 16); };
 #pragma unroll
     for (int h = 0; h < FQ / 2; ++h) {
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj)
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
-                *reinterpret_cast<f32x4*>(w + (jj * 16 + q_l) * kPitch + i * 16 + p_l) = acc[i][h * 2 + jj];
+            for (int i = 0; i < FP; ++i) *at(jj * 16 + q_l, i * 4 + (lane >> 4)) = acc[i][h * 2 + jj];
 #pragma unroll 1
         for (int r = 0; r < 32; r += 64 / kLanes) {
-            const int row = r + lane / kLanes, c = (lane % kLanes) * 8;
+            const int row = r + lane / kLanes, c = (lane % kLanes) * 2;
             const int q = q0 + (wq * FQ + h * 2) * 16 + row;
-            const int p = p0 + wp * NI * 16 + c;
+            const int p = p0 + wp * NI * 16 + c * 4;
             if (q < a.nq && p < a.np) {
+                const auto take = [&](int chunk, float (&v)[8]) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const f32x4 t = *at(row, chunk + k);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[k * 4 + i] = t[i];
+                    }
+                };
                 float v[8], u[8];
-                const float* src = w + row * kPitch + c;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = src[i];
+                take(c, v);
                 if (PAIR) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = src[NI * 16 + i];
+                    take(NI * 4 + c, u);
                     epilogue_pair<T>(e, q, p, a.np, v, u);
                 } else {
                     epilogue_one<T>(e, q, p, a.np, v);
@@ -374,19 +435,7 @@ Plan make_plan(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int n
 template <class T, bool TRP, bool TRQ, bool PAIR, int FP, int FQ>
 vq_status launch_shape(const Tile& t, const Plan& p, int nbatch, hipStream_t st)
 {
-    constexpr size_t slices = 2 * (size_t)(kWP * FP + kWQ * FQ) * 16 * kBK * 2;
-    constexpr size_t turned = (size_t)kWaves * 32 * epilogue_pitch(FP) * sizeof(float);
-    constexpr size_t lds = slices > turned ? slices : turned;
-    const auto kern = k_gemm<T, TRP, TRQ, FP, FQ, PAIR>;
-    static thread_local int set_dev = -1;
-    int dev = 0;
-    VQ_HIP(hipGetDevice(&dev));
-    if (lds > 65536 && set_dev != dev) {
-        VQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)lds));
-        set_dev = dev;
-    }
-    hipLaunchKernelGGL(kern, dim3(p.ntp * p.ntq, p.splits, nbatch), dim3(kThreads), lds, st, t);
+    hipLaunchKernelGGL((k_gemm<T, TRP, TRQ, FP, FQ, PAIR>), dim3(p.ntp * p.ntq, p.splits, nbatch), dim3(kThreads), 0, st, t);
     VQ_LAUNCHED("k_gemm");
     if (p.splits > 1) VQ_TRY(launch_finish<T>({t.part, t.splits, t.np, t.nq, t.pitch, t.epi, t.Y2}, PAIR, nbatch, st));
     return VQ_OK;
@@ -433,8 +482,8 @@ vq_status gemm_launch(const GemmArgs& g, void* ws, size_t ws_bytes, hipStream_t 
         t.P[i] = static_cast<const char*>(g.P[i]);
         t.Q[i] = static_cast<const char*>(g.Q[i]);
     }
-    t.ldp = g.ldp; t.ldq = g.ldq;
-    t.kP = g.kP; t.kQ = g.kQ;
+    t.ldp = (int)g.ldp; t.ldq = (int)g.ldq;
+    t.kP = (int)g.kP; t.kQ = (int)g.kQ;
     t.np = g.np; t.nq = g.nq; t.wp = g.wp; t.wq = g.wq;
     t.ntp = p.ntp; t.ntq = p.ntq;
     t.seg_steps = p.seg_steps; t.steps = p.steps;

@@ -159,7 +159,7 @@ constexpr int block_of(int d, int xt, int nt) { return 4 * chunks_of(xt, nt) * (
 // D = 8 or 4: sub-vectors of that length in 16-byte aligned codebooks (4: an even
 // number of them in a row).  D = 0: any d, one sub-vector per chunk of eight k slots.
 template <int D, int XT, int NT, int NM>
-__global__ __launch_bounds__(512, 4) void k_qffn(const QArgs a)
+__global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
 {
     constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
     constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
@@ -441,16 +441,17 @@ struct QPlan {
     int64_t groups;
 };
 
-// Row groups first; where they leave fewer than two workgroups a CU, each row's
-// sub-vectors are split over up to 16 workgroups (at least 32 a wave).
+// Sixteen waves a workgroup where the row groups give less than two workgroups of
+// eight a CU; each row's sub-vectors are split over up to 16 workgroups where
+// they give less than one of sixteen (at least 32 sub-vectors a wave).
 QPlan q_plan(int64_t M, int64_t nb)
 {
     QPlan p;
     p.groups = (M + kQRows - 1) / kQRows;
     const int64_t nkb = (nb + 31) / 32;
-    p.waves = nkb >= 4 ? 8 : 4;
+    p.waves = nkb >= 16 && p.groups < 512 ? 16 : nkb >= 4 ? 8 : 4;
     p.splits = 1;
-    while (p.splits < 16 && p.groups * p.splits < 512 && nkb >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+    while (p.splits < 16 && p.groups * p.splits < 256 && nkb >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
     return p;
 }
 

@@ -7,6 +7,7 @@ a non-zero status.  There is no fallback: if libvq.so is missing or no
 gfx950 device is present the call fails.
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -161,7 +162,8 @@ def _ptr(t):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    # the raw handle of the current device's current stream, without a Stream object
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype(t, dt, name):
@@ -512,14 +514,16 @@ def _matrix(t, rows, cols, dtype, name):
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
         raise ValueError("%s must be on the GPU" % name)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError("%s must be [%d x %d], got %s" % (name, rows, cols, list(t.shape)))
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError("%s must have contiguous rows" % name)
-    if rows > 1 and s0 < cols:
-        raise ValueError("%s must have rows that do not overlap" % name)
-    return t.data_ptr(), s0 if rows > 1 else max(s0, cols)
+    if s0 < cols:
+        if rows > 1:
+            raise ValueError("%s must have rows that do not overlap" % name)
+        s0 = cols
+    return t.data_ptr(), s0
 
 
 def _vector(t, n, dtype, name):
@@ -539,6 +543,37 @@ def _scratch(need, ws, device):
             return None, 0, None
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     return _ptr(ws), ws.numel(), ws
+
+
+# Workspace sizes by sizes, leading dimensions and alignments (an address stands for its last four bits).
+@functools.lru_cache(maxsize=4096)
+def _linear_need(T, M, N, x, ldx, w, ldw):
+    return load().vq_linear_workspace_bytes(T, M, N, x, ldx, w, ldw)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_need(T, M, N, x, ldx, wg, wu, ldw):
+    return load().vq_gated_workspace_bytes(T, M, N, x, ldx, wg, wu, ldw)
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_backward_need(*args):
+    return load().vq_linear_backward_workspace_bytes(*args)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_backward_need(*args):
+    return load().vq_gated_backward_workspace_bytes(*args)
+
+
+@functools.lru_cache(maxsize=4096)
+def _qlinear_need(M, N, d, T):
+    return load().vq_qlinear_workspace_bytes(M, N, d, T)
+
+
+@functools.lru_cache(maxsize=4096)
+def _qgated_need(M, N, d, T):
+    return load().vq_qgated_workspace_bytes(M, N, d, T)
 
 
 def _dims(X, W):
@@ -564,7 +599,7 @@ def linear(X, W, bias=None, residual=None, act="none", want_pre=False, out=None,
     y, ldy = _matrix(Y, T, M, X.dtype, "out")
     z, ldz = _matrix(Z, T, M, X.dtype, "pre")
     lib = load()
-    p, n, ws = _scratch(lib.vq_linear_workspace_bytes(T, M, N, x, ldx, w, ldw), ws, X.device)
+    p, n, ws = _scratch(_linear_need(T, M, N, x & 15, ldx, w & 15, ldw), ws, X.device)
     _check(lib.vq_linear(T, M, N, dt, a, x, ldx, w, ldw, b, r, ldr, y, ldy, z, ldz, p, n, _stream()))
     return (Y, Z) if want_pre else Y
 
@@ -587,8 +622,8 @@ def linear_backward(dY, X, W, pre=None, act="none", want_dx=True, want_dw=True, 
     dW = torch.empty((M, N), dtype=X.dtype, device=X.device) if want_dw else None
     db = torch.empty(M, dtype=X.dtype, device=X.device) if want_db else None
     lib = load()
-    p, n, ws = _scratch(lib.vq_linear_backward_workspace_bytes(T, M, N, a, g, ldg, x, ldx, w, ldw, want_dx, want_dw,
-                                                               want_db), ws, X.device)
+    p, n, ws = _scratch(_linear_backward_need(T, M, N, a, g & 15, ldg, x & 15, ldx, w & 15, ldw, want_dx, want_dw, want_db),
+                        ws, X.device)
     _check(lib.vq_linear_backward(T, M, N, dt, a, g, ldg, x, ldx, w, ldw, z, ldz, _ptr(dX), N, _ptr(dW), N, _ptr(db),
                                   p, n, _stream()))
     return dX, dW, db
@@ -614,7 +649,7 @@ def gated(X, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", want_pre=Fa
     G = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
     U = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
     lib = load()
-    p, n, ws = _scratch(lib.vq_gated_workspace_bytes(T, M, N, x, ldx, wg, wu, ldw), ws, X.device)
+    p, n, ws = _scratch(_gated_need(T, M, N, x & 15, ldx, wg & 15, wu & 15, ldw), ws, X.device)
     _check(lib.vq_gated(T, M, N, dt, a, x, ldx, wg, wu, ldw, bg, bu, h, ldh, _ptr(G), _ptr(U), M, p, n, _stream()))
     return (H, G, U) if want_pre else H
 
@@ -638,8 +673,8 @@ def gated_backward(dH, X, W_gate, W_up, G, U, act="silu", want_dx=True, want_dw=
     dX, dWg, dWu = new(want_dx, T, N), new(want_dw, M, N), new(want_dw, M, N)
     dbg, dbu = new(want_db, M), new(want_db, M)
     lib = load()
-    p, n, ws = _scratch(lib.vq_gated_backward_workspace_bytes(T, M, N, a, dh, lddh, x, ldx, wg, wu, ldw, want_dx,
-                                                              want_dw, want_db), ws, X.device)
+    p, n, ws = _scratch(_gated_backward_need(T, M, N, a, dh & 15, lddh, x & 15, ldx, wg & 15, wu & 15, ldw, want_dx, want_dw,
+                                             want_db), ws, X.device)
     _check(lib.vq_gated_backward(T, M, N, dt, a, dh, lddh, x, ldx, wg, wu, ldw, g, u, ldz, _ptr(dX), N, _ptr(dWg),
                                  _ptr(dWu), N, _ptr(dbg), _ptr(dbu), p, n, _stream()))
     return dX, dWg, dWu, dbg, dbu
@@ -719,7 +754,7 @@ def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
     Y = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
     y, ldy = _matrix(Y, T, M, X.dtype, "out")
     lib = load()
-    p, n, ws = _scratch(lib.vq_qlinear_workspace_bytes(M, N, Q.d, T), ws, X.device)
+    p, n, ws = _scratch(_qlinear_need(M, N, Q.d, T), ws, X.device)
     _check(lib.vq_qlinear(Q._ref, T, dt, a, x, ldx, b, r, ldr, y, ldy, p, n, _stream()))
     return Y
 
@@ -736,6 +771,6 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     H = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
     h, ldh = _matrix(H, T, M, X.dtype, "out")
     lib = load()
-    p, n, ws = _scratch(lib.vq_qgated_workspace_bytes(M, N, Q_gate.d, T), ws, X.device)
+    p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X.device)
     _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
     return H
