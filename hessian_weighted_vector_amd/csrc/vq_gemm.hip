@@ -116,25 +116,28 @@ __device__ __forceinline__ void load_slice(const char* b0, const char* b1, int l
     }
 }
 
-// Fragment (16 rows from r0, k = kk*32 .. +31): lane l holds row r0 + l%16,
-// k = kk*32 + 8*(l/16) .. +7.
-template <class T, int R, bool TR>
-__device__ __forceinline__ typename T::V8 fragment(lds_ptr lds, int r0, int kk, int lane)
+// Fragment i (of the wave's rows from r0) of half kk: lane l holds row r0 + 16 i + l%16,
+// k = kk*32 + 8*(l/16) .. +7.  lane_base is the lane's byte offset for i = kk = 0; the
+// swizzles make the other fragments' offsets an exclusive or away from it.
+template <int R, bool TR>
+__device__ __forceinline__ uint32_t lane_base(int r0, int lane)
 {
     typedef Slice<R, TR> S;
     const int i = lane & 15, g = lane >> 4;
-    if (!TR) {
-        const int row = r0 + i;
-        return *(const __attribute__((address_space(3))) typename T::V8*)(lds + row * 128 + ((kk * 4 + g) ^ S::swizzle(row)) * 16);
-    } else {
-        const int row = kk * 32 + g * 8 + (i >> 2);          // second half: row + 4, same swizzle
-        const int chunk = (r0 / 8 + ((i & 3) >> 1)) ^ S::swizzle(row);
-        lds_ptr p = lds + row * (R * 2) + chunk * 16 + (i & 1) * 8;
-        typedef __attribute__((address_space(3))) typename T::V4* tr_ptr;
-        const typename T::V4 a = T::lds_tr((tr_ptr)p);
-        const typename T::V4 b = T::lds_tr((tr_ptr)(p + 4 * R * 2));
-        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
+    if (!TR) return (uint32_t)((r0 + i) * 128 + ((g ^ S::swizzle(i)) * 16));
+    const int row = g * 8 + (i >> 2);                     // the read's second half: row + 4, same swizzle
+    return (uint32_t)(row * (R * 2) + (((r0 / 8 + ((i & 3) >> 1)) ^ S::swizzle(row)) * 16) + (i & 1) * 8);
+}
+
+template <class T, int R, bool TR>
+__device__ __forceinline__ typename T::V8 fragment(lds_ptr lds, uint32_t base, int i, int kk)
+{
+    if (!TR) return *(const __attribute__((address_space(3))) typename T::V8*)(lds + (base ^ (kk * 64)) + i * 2048);
+    lds_ptr p = lds + (base ^ (i * 32)) + kk * 32 * R * 2;
+    typedef __attribute__((address_space(3))) typename T::V4* tr_ptr;
+    const typename T::V4 a = T::lds_tr((tr_ptr)p);
+    const typename T::V4 b = T::lds_tr((tr_ptr)(p + 4 * R * 2));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // Work item -> tile.  Consecutive workgroup ids go to the eight dies in turn;
@@ -164,14 +167,12 @@ struct Main {
     typedef typename T::V8 V8;
     struct Frags { V8 p[FP], q[FQ]; };
 
-    // First row (of the tile) of fragment i of wave row wp: in a pair the first
-    // half of the fragments is the gate's, the second the same features of up.
-    static __device__ __forceinline__ int prow(int wp, int i)
-    {
-        return PAIR ? (i < FP / 2 ? wp * (FP / 2) + i : FP + wp * (FP / 2) + i - FP / 2) * 16 : (wp * FP + i) * 16;
-    }
+    // Fragment i of P starts at row (i + skip(i)) * 16 of the wave's first: in a
+    // pair the first half of the fragments is the gate's, the second the same
+    // features of up, half a tile further.
+    static __device__ __forceinline__ int skip(int i) { return PAIR && i >= FP / 2 ? FP / 2 : 0; }
 
-    // Steps s0 .. s1-1 into acc.  A step is two halves of k = 32.  While the
+    // Steps s0 .. s1-1 (an even count) into acc.  A step is two halves of k = 32.  While the
     // matrix cores work on one half, the next half's fragments are read from LDS,
     // so a wave waits for LDS only at the start.  One barrier a step, between the
     // halves: behind it the next step's slices are complete (each wave has waited
@@ -181,18 +182,29 @@ struct Main {
                                                lds_ptr pb0, lds_ptr pb1, lds_ptr qb0, lds_ptr qb1, f32x4 (&acc)[FP][FQ])
     {
         const int wp = wave / kWQ, wq = wave % kWQ;
+        // pointers in registers: one read in the loop would be awaited with the fragments
+        const char* const P0 = a.P[0];
+        const char* const P1 = a.P[1];
+        const char* const Q0 = batch ? a.Q[1] : a.Q[0];
+        const char* const Q1 = a.Q[1];
         const auto issue = [&](int s, lds_ptr pb, lds_ptr qb) __attribute__((always_inline)) {
             // a step past the last stays in the last segment, past its K
-            const int seg = s >= a.seg_steps && a.steps > a.seg_steps ? 1 : 0;
-            const int k0 = (s - seg * a.seg_steps) * kBK;
-            load_slice<BP, TRP, PAIR>(PAIR ? a.P[0] : a.P[seg], a.P[1], a.ldp, p0, a.np, a.wp, k0, a.kP, pb, wave, lane);
-            load_slice<BQ, TRQ, false>(a.Q[seg + batch], nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, qb, wave, lane);
+            int l = lane;
+            if (TRP || TRQ) asm volatile("" : "+v"(l));          // formed anew: registers
+            const bool second = s >= a.seg_steps && a.steps > a.seg_steps;
+            const int k0 = (second ? s - a.seg_steps : s) * kBK;
+            load_slice<BP, TRP, PAIR>(!PAIR && second ? P1 : P0, P1, a.ldp, p0, a.np, a.wp, k0, a.kP, pb, wave, l);
+            load_slice<BQ, TRQ, false>(second ? Q1 : Q0, nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, qb, wave, l);
         };
+        uint32_t pbase = lane_base<BP, TRP>(wp * (PAIR ? FP / 2 : FP) * 16, lane);
+        uint32_t qbase = lane_base<BQ, TRQ>(wq * FQ * 16, lane);
         const auto read = [&](Frags& f, lds_ptr pb, lds_ptr qb, int kk) __attribute__((always_inline)) {
+            // the offsets are formed anew each time: kept, they would take the registers of the sums
+            asm volatile("" : "+v"(pbase), "+v"(qbase));
 #pragma unroll
-            for (int j = 0; j < FQ; ++j) f.q[j] = fragment<T, BQ, TRQ>(qb, (wq * FQ + j) * 16, kk, lane);
+            for (int j = 0; j < FQ; ++j) f.q[j] = fragment<T, BQ, TRQ>(qb, qbase, j, kk);
 #pragma unroll
-            for (int i = 0; i < FP; ++i) f.p[i] = fragment<T, BP, TRP>(pb, prow(wp, i), kk, lane);
+            for (int i = 0; i < FP; ++i) f.p[i] = fragment<T, BP, TRP>(pb, pbase, i + skip(i), kk);
         };
         const auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
 #pragma unroll
@@ -206,7 +218,7 @@ struct Main {
         const auto spread = [](int loads) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < kMfma; ++i) {
-                const int r0 = kReads * i * 4 / (kMfma * 3), r1 = kReads * (i + 1) * 4 / (kMfma * 3);
+                const int r0 = kReads * i * 1 / (kMfma * 1), r1 = kReads * (i + 1) * 1 / (kMfma * 1);
 #pragma unroll
                 for (int r = r0; r < r1 && r < kReads; ++r) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -231,13 +243,11 @@ struct Main {
         __builtin_amdgcn_s_waitcnt(wait_imm(kLoads, 0));
         asm volatile("s_barrier" ::: "memory");
         read(f0, pb0, qb0, 0);
-        // loads past s1 go out too (nothing uses them): the body stays one block
+        // loads past s1 go out too (zeros past the matrix): the body stays one block
 #pragma unroll 1
-        for (int s = s0;; s += 2) {
+        for (int s = s0; s < s1; s += 2) {
             step(s, pb0, qb0, pb1, qb1);
-            if (s + 1 >= s1) break;
             step(s + 1, pb1, qb1, pb0, qb0);
-            if (s + 2 >= s1) break;
         }
     }
 };
@@ -258,7 +268,9 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     int tp, tq;
     pick_tile(blockIdx.x, a.ntp * a.ntq, a.ntp, a.ntq, tp, tq);
     const int p0 = tp * (PAIR ? L::BP / 2 : L::BP), q0 = tq * L::BQ;
-    const int s0 = (int)((int64_t)a.steps * split / a.splits), s1 = (int)((int64_t)a.steps * (split + 1) / a.splits);
+    // splits in pairs of steps, as the loop takes them; past the last step come zeros
+    const int pairs = (a.steps + 1) / 2;
+    const int s0 = 2 * (int)((int64_t)pairs * split / a.splits), s1 = 2 * (int)((int64_t)pairs * (split + 1) / a.splits);
 
     f32x4 acc[FP][FQ];
 #pragma unroll
@@ -413,7 +425,7 @@ Plan make_plan(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int n
         p.steps = p.seg_steps * nseg;
         p.pitch = (int)((np + 7) / 8 * 8);
         const int64_t tiles = (int64_t)p.ntp * p.ntq * nbatch;
-        for (int sp = 1; sp <= 16 && sp <= p.steps; ++sp) {
+        for (int sp = 1; sp <= 16 && 2 * sp <= p.steps + 1; ++sp) {
             // rounds of the chip, each as long as its share of K steps; a step of
             // the large tile costs four of the small one at twice the tiles per CU
             const double slots = p.fp == 8 ? 256.0 : 512.0;
