@@ -220,7 +220,6 @@ vq_status few_product(const FewArgs& f, void* ws, hipStream_t st)
     a.pitch = (int)((f.M + 7) / 8 * 8);
     a.part = a.splits > 1 ? static_cast<float*>(ws) : nullptr;
     a.epi = f.epi;
-    set_vec(a.epi);
     const bool pair = f.nm > 1;
     if (f.dtype == VQ_BF16) return f.T > 16 ? few_launch<Bf16, 2>(a, p.waves, pair, st) : few_launch<Bf16, 1>(a, p.waves, pair, st);
     return f.T > 16 ? few_launch<F16, 2>(a, p.waves, pair, st) : few_launch<F16, 1>(a, p.waves, pair, st);

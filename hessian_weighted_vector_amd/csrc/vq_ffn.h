@@ -116,7 +116,6 @@ __device__ inline void act_grad(int act, float z, float& a, float& da)
 // value is rounded once, from float32; the activation reads the unrounded sums.
 struct Epilogue {
     int act;
-    int vec;                 // every row can be read and written eight features at a time
     const void* bias[2];     // nullable
     const void* R;           // nullable
     void* Y;
@@ -124,41 +123,27 @@ struct Epilogue {
     int64_t ldr, ldy, ldz;
 };
 
-// Reads or writes features m .. m+7 of row t (those below M), as one 16-byte
-// access where `vec` allows.
+// Reads or writes features m .. m+7 of row t (those below M): one 16-byte access
+// where all eight exist, at any element-aligned address (the hardware takes
+// unaligned vector accesses; aligned rows run at full speed).
 template <class T>
-__device__ inline void store8(void* base, int64_t ld, int64_t t, int m, int M, bool vec, const float (&v)[8])
+__device__ inline void store8(void* base, int64_t ld, int64_t t, int m, int M, const float (&v)[8])
 {
     typename T::E* o = static_cast<typename T::E*>(base) + t * ld + m;
-    if (vec && m + 8 <= M) {
-        typename T::V8 w;
+    typename T::V8 w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = (typename T::E)v[i];
-        *reinterpret_cast<typename T::V8*>(o) = w;
+    for (int i = 0; i < 8; ++i) w[i] = (typename T::E)v[i];
+    if (m + 8 <= M) {
+        __builtin_memcpy(o, &w, 16);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (m + i < M) o[i] = (typename T::E)v[i];
+            if (m + i < M) o[i] = w[i];
     }
 }
 
 template <class T>
-__device__ inline void load8(const void* base, int64_t ld, int64_t t, int m, int M, bool vec, float (&v)[8])
-{
-    const typename T::E* p = static_cast<const typename T::E*>(base) + t * ld + m;
-    if (vec && m + 8 <= M) {
-        const typename T::V8 w = *reinterpret_cast<const typename T::V8*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)w[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = m + i < M ? (float)p[i] : 0.0f;
-    }
-}
-
-// The same at any element-aligned address (the hardware takes unaligned vector loads).
-template <class T>
-__device__ inline void load8_any(const void* base, int64_t ld, int64_t t, int m, int M, float (&v)[8])
+__device__ inline void load8(const void* base, int64_t ld, int64_t t, int m, int M, float (&v)[8])
 {
     const typename T::E* p = static_cast<const typename T::E*>(base) + t * ld + m;
     if (m + 8 <= M) {
@@ -176,58 +161,47 @@ __device__ inline void load8_any(const void* base, int64_t ld, int64_t t, int m,
 template <class T>
 __device__ inline void epilogue_one(const Epilogue& e, int64_t t, int m, int M, float (&z)[8])
 {
-    const bool vec = e.vec;
     if (e.bias[0]) {
         float b[8];
-        load8<T>(e.bias[0], 0, 0, m, M, vec, b);
+        load8<T>(e.bias[0], 0, 0, m, M, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] += b[i];
     }
-    if (e.Z[0]) store8<T>(e.Z[0], e.ldz, t, m, M, vec, z);
+    if (e.Z[0]) store8<T>(e.Z[0], e.ldz, t, m, M, z);
     if (e.act != VQ_ACT_NONE) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = act_fast(e.act, z[i]);
     }
     if (e.R) {
         float r[8];
-        load8<T>(e.R, e.ldr, t, m, M, vec, r);
+        load8<T>(e.R, e.ldr, t, m, M, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] += r[i];
     }
-    store8<T>(e.Y, e.ldy, t, m, M, vec, z);
+    store8<T>(e.Y, e.ldy, t, m, M, z);
 }
 
 template <class T>
 __device__ inline void epilogue_pair(const Epilogue& e, int64_t t, int m, int M, float (&g)[8], float (&u)[8])
 {
-    const bool vec = e.vec;
     float b[8];
     if (e.bias[0]) {
-        load8<T>(e.bias[0], 0, 0, m, M, vec, b);
+        load8<T>(e.bias[0], 0, 0, m, M, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] += b[i];
     }
     if (e.bias[1]) {
-        load8<T>(e.bias[1], 0, 0, m, M, vec, b);
+        load8<T>(e.bias[1], 0, 0, m, M, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] += b[i];
     }
     if (e.Z[0]) {
-        store8<T>(e.Z[0], e.ldz, t, m, M, vec, g);
-        store8<T>(e.Z[1], e.ldz, t, m, M, vec, u);
+        store8<T>(e.Z[0], e.ldz, t, m, M, g);
+        store8<T>(e.Z[1], e.ldz, t, m, M, u);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = act_fast(e.act, g[i]) * u[i];
-    store8<T>(e.Y, e.ldy, t, m, M, vec, g);
-}
-
-// Whether rows at p with leading dimension ld can be accessed 16 bytes at a time.
-inline bool vec8_ok(const void* p, int64_t ld) { return p == nullptr || (aligned16(p) && ld % 8 == 0); }
-
-inline void set_vec(Epilogue& e)
-{
-    e.vec = vec8_ok(e.Y, e.ldy) && vec8_ok(e.R, e.ldr) && vec8_ok(e.Z[0], e.ldz) && vec8_ok(e.Z[1], e.ldz) &&
-            vec8_ok(e.bias[0], 0) && vec8_ok(e.bias[1], 0);
+    store8<T>(e.Y, e.ldy, t, m, M, g);
 }
 
 // ---- the tiled product --------------------------------------------------

@@ -48,19 +48,32 @@ struct Mat {
 // Whether the tiled product's 16-byte loads can read the matrix as it is.
 bool loads_ok(const Mat& m) { return aligned16(m.p) && m.ld % 8 == 0 && m.cols % 8 == 0 && m.ld <= kMaxLd; }
 
-__global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ s, int64_t rows, int cols, int64_t ld,
-                                              int64_t ldp, uint16_t* __restrict__ o)
+struct Pack {
+    const uint16_t* s;
+    uint16_t* o;
+    int64_t rows, ld, ldp;
+    int cols;
+};
+struct Packs { Pack m[3]; };
+
+// blockIdx.y: the matrix.
+__global__ __launch_bounds__(256) void k_pack(const Packs a)
 {
-    const int64_t per = ldp / 8;
-    const int64_t n = rows * per;
+    const Pack m = a.m[blockIdx.y];
+    const int64_t per = m.ldp / 8;
+    const int64_t n = m.rows * per;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
         const int64_t r = e / per;
         const int c = (int)(e - r * per) * 8;
-        const uint16_t* p = s + r * ld + c;
+        const uint16_t* p = m.s + r * m.ld + c;
         alignas(16) uint16_t v[8];
+        if (c + 8 <= m.cols) {
+            __builtin_memcpy(v, p, 16);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i] : (uint16_t)0;
-        *reinterpret_cast<uint4*>(o + r * ldp + c) = *reinterpret_cast<const uint4*>(v);
+            for (int i = 0; i < 8; ++i) v[i] = c + i < m.cols ? p[i] : (uint16_t)0;
+        }
+        *reinterpret_cast<uint4*>(m.o + r * m.ldp + c) = *reinterpret_cast<const uint4*>(v);
     }
 }
 
@@ -70,48 +83,55 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int
         o[e / cols * ld + e % cols] = 0;
 }
 
-// A wave takes 8 rows of 512 columns (eight a lane), a workgroup 32 rows; the
-// four waves' column sums join in LDS.  GATED: D0 = dG, D1 = dU.  D0 may be
-// null (bias gradient alone).  D0 and D1 have zero-padded rows of ldd.
-constexpr int kGradRows = 32;
-template <class T, bool GATED>
+// A workgroup's four waves take R rows each of 512 columns (eight a lane), and
+// their column sums join in LDS.  GATED: D0 = dG, D1 = dU.  D0 may be null (bias
+// gradient alone).  D0 and D1 have zero-padded rows of ldd.  Bound by its bytes.
+template <class T, bool GATED, int R>
 __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const void* dY, int64_t ldy, const void* Z0,
-                                              const void* Z1, int64_t ldz, typename T::E* D0,
-                                              typename T::E* D1, int64_t ldd, float* part0, float* part1)
+                                              const void* Z1, int64_t ldz, typename T::E* D0, typename T::E* D1,
+                                              int64_t ldd, float* part0, float* part1)
 {
     __shared__ float sums[GATED ? 2 : 1][4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m = blockIdx.x * 512 + lane * 8;
-    const int64_t t0 = (int64_t)blockIdx.y * kGradRows + wave * (kGradRows / 4);
+    const int m = blockIdx.y * 512 + lane * 8;
+    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * R;
     float c0[8] = {}, c1[8] = {};
     if (m < M) {
-#pragma unroll 2
-        for (int r = 0; r < kGradRows / 4; ++r) {
-            const int64_t t = t0 + r;
-            if (t >= nt) break;
-            float dy[8], z[8], u[8];
-            load8_any<T>(dY, ldy, t, m, M, dy);
-            if (GATED || act != VQ_ACT_NONE) load8_any<T>(Z0, ldz, t, m, M, z);
-            if (GATED) load8_any<T>(Z1, ldz, t, m, M, u);
+        constexpr int B = R < 4 ? R : GATED ? 2 : 4;         // rows whose loads are in flight together
+#pragma unroll 1
+        for (int r = 0; r < R; r += B) {
+            float dy[B][8], z[B][8], u[B][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a, da;
-                if (GATED) {
-                    act_grad(act, z[i], a, da);
-                    z[i] = dy[i] * u[i] * da;
-                    u[i] = dy[i] * a;
-                    c1[i] += u[i];
-                } else if (act != VQ_ACT_NONE) {
-                    act_grad(act, z[i], a, da);
-                    z[i] = dy[i] * da;
-                } else {
-                    z[i] = dy[i];
-                }
-                c0[i] += z[i];
+            for (int k = 0; k < B; ++k) {
+                const int64_t t = t0 + r + k < nt ? t0 + r + k : nt - 1;
+                load8<T>(dY, ldy, t, m, M, dy[k]);
+                if (GATED || act != VQ_ACT_NONE) load8<T>(Z0, ldz, t, m, M, z[k]);
+                if (GATED) load8<T>(Z1, ldz, t, m, M, u[k]);
             }
-            // columns past M (loaded as zero) give zeros: the padding
-            if (D0) store8<T>(D0, ldd, t, m, (int)ldd, true, z);
-            if (GATED) store8<T>(D1, ldd, t, m, (int)ldd, true, u);
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int64_t t = t0 + r + k;
+                if (t >= nt) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float a, da;
+                    if (GATED) {
+                        act_grad(act, z[k][i], a, da);
+                        z[k][i] = dy[k][i] * u[k][i] * da;
+                        u[k][i] = dy[k][i] * a;
+                        c1[i] += u[k][i];
+                    } else if (act != VQ_ACT_NONE) {
+                        act_grad(act, z[k][i], a, da);
+                        z[k][i] = dy[k][i] * da;
+                    } else {
+                        z[k][i] = dy[k][i];
+                    }
+                    c0[i] += z[k][i];
+                }
+                // columns past M (loaded as zero) give zeros: the padding
+                if (D0) store8<T>(D0, ldd, t, m, (int)ldd, z[k]);
+                if (GATED) store8<T>(D1, ldd, t, m, (int)ldd, u[k]);
+            }
         }
     }
     if (!part0) return;
@@ -122,15 +142,18 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
     }
     __syncthreads();
     for (int k = threadIdx.x; k < 512; k += 256) {
-        const int col = blockIdx.x * 512 + k;
+        const int col = blockIdx.y * 512 + k;
         if (col >= M) break;
-        part0[(int64_t)blockIdx.y * M + col] = sums[0][0][k] + sums[0][1][k] + sums[0][2][k] + sums[0][3][k];
+        part0[(int64_t)blockIdx.x * M + col] = sums[0][0][k] + sums[0][1][k] + sums[0][2][k] + sums[0][3][k];
         if (GATED) {
             constexpr int b = GATED ? 1 : 0;
-            part1[(int64_t)blockIdx.y * M + col] = sums[b][0][k] + sums[b][1][k] + sums[b][2][k] + sums[b][3][k];
+            part1[(int64_t)blockIdx.x * M + col] = sums[b][0][k] + sums[b][1][k] + sums[b][2][k] + sums[b][3][k];
         }
     }
 }
+
+// Rows a workgroup takes: 32, or 4 where that leaves less than a workgroup a CU.
+int grad_rows(int64_t T, int64_t M) { return (M + 511) / 512 * ((T + 31) / 32) < 256 ? 4 : 32; }
 
 // db = sum of `n` partial rows: 16 columns and 16 row slices a workgroup, the
 // slices added in order.
@@ -155,22 +178,29 @@ __global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part
     }
 }
 
-// A packed copy in the workspace takes the matrix's place.  run = false only counts.
-vq_status pack(Mat& m, Arena& ws, bool run, hipStream_t st)
-{
-    const int64_t ldp = round8(m.cols);
-    void* o = ws.take((size_t)m.rows * ldp * 2);
-    if (run) {
-        hipLaunchKernelGGL(k_pack, dim3((unsigned)std::min<int64_t>((m.rows * (ldp / 8) + 255) / 256, 65536)), dim3(256), 0,
-                           st, static_cast<const uint16_t*>(m.p), m.rows, (int)m.cols, m.ld, ldp,
-                           static_cast<uint16_t*>(o));
-        VQ_LAUNCHED("k_pack");
-        m.p = o;
+// Collects the operands that need a packed copy; each copy in the workspace takes
+// its matrix's place, and one launch makes them all.
+struct Packer {
+    Arena& ws;
+    Packs list{};
+    int count = 0;
+    int64_t most = 0;
+    void add(Mat& m)
+    {
+        const int64_t ldp = round8(m.cols);
+        void* o = ws.take((size_t)m.rows * ldp * 2);
+        list.m[count++] = {static_cast<const uint16_t*>(m.p), static_cast<uint16_t*>(o), m.rows, m.ld, ldp, (int)m.cols};
+        most = std::max(most, m.rows * (ldp / 8));
+        m = {o, m.rows, ldp, ldp};
     }
-    m.ld = ldp;
-    m.cols = ldp;
-    return VQ_OK;
-}
+    vq_status launch(hipStream_t st) const
+    {
+        if (count == 0) return VQ_OK;
+        hipLaunchKernelGGL(k_pack, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 16384), count), dim3(256), 0, st, list);
+        VQ_LAUNCHED("k_pack");
+        return VQ_OK;
+    }
+};
 
 vq_status zero_matrix(void* o, int64_t rows, int64_t cols, int64_t ld, hipStream_t st)
 {
@@ -200,10 +230,11 @@ vq_status forward(const Forward& f, Arena& ws, bool run, hipStream_t st)
     }
     Mat x{f.X, f.T, f.N, f.ldx};
     Mat w[2] = {{f.W[0], f.M, f.N, f.ldw}, {f.W[1], f.M, f.N, f.ldw}};
-    if (!loads_ok(x)) VQ_TRY(pack(x, ws, run, st));
+    Packer pk{ws};
+    if (!loads_ok(x)) pk.add(x);
     // a pair shares one leading dimension: both are packed or neither
     if (!loads_ok(w[0]) || (f.nm > 1 && !loads_ok(w[1])))
-        for (int i = 0; i < f.nm; ++i) VQ_TRY(pack(w[i], ws, run, st));
+        for (int i = 0; i < f.nm; ++i) pk.add(w[i]);
     GemmArgs g{};
     g.kind = f.nm > 1 ? GEMM_GATED : GEMM_LINEAR;
     g.dtype = f.dtype;
@@ -216,7 +247,9 @@ vq_status forward(const Forward& f, Arena& ws, bool run, hipStream_t st)
     g.epi = f.epi;
     const size_t gb = gemm_workspace(g.kind, g.np, g.nq, f.N, 1, 1);
     void* gw = ws.take(gb);
-    return run ? gemm_launch(g, gw, gb, st) : VQ_OK;
+    if (!run) return VQ_OK;
+    VQ_TRY(pk.launch(st));
+    return gemm_launch(g, gw, gb, st);
 }
 
 struct Backward {
@@ -235,17 +268,20 @@ template <class T>
 vq_status grad_launch(const Backward& b, void* const (&D)[2], int64_t ldd, float* const (&part)[2], hipStream_t st)
 {
     typedef typename T::E E;
-    const dim3 grid((unsigned)((b.M + 511) / 512), (unsigned)((b.T + kGradRows - 1) / kGradRows));
-    if (b.nm > 1)
-        hipLaunchKernelGGL((k_grad<T, true>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], b.Z[1],
-                           b.ldz, (E*)D[0], (E*)D[1], ldd, part[0], part[1]);
-    else
-        hipLaunchKernelGGL((k_grad<T, false>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], b.Z[1],
-                           b.ldz, (E*)D[0], (E*)nullptr, ldd, part[0], part[1]);
+    const int rows = grad_rows(b.T, b.M);
+    const dim3 grid((unsigned)((b.T + rows - 1) / rows), (unsigned)((b.M + 511) / 512));
+#define VQ_GRAD(GATED_, R_)                                                                                          \
+    hipLaunchKernelGGL((k_grad<T, GATED_, R_>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0],     \
+                       b.Z[1], b.ldz, (E*)D[0], (E*)D[1], ldd, part[0], part[1])
+    if (b.nm > 1 && rows == 32) VQ_GRAD(true, 8);
+    else if (b.nm > 1) VQ_GRAD(true, 1);
+    else if (rows == 32) VQ_GRAD(false, 8);
+    else VQ_GRAD(false, 1);
+#undef VQ_GRAD
     VQ_LAUNCHED("k_grad");
     if (part[0]) {
         hipLaunchKernelGGL((k_bias_sum<T>), dim3((unsigned)((b.M + 15) / 16), b.nm), dim3(256), 0, st, part[0], part[1],
-                           (int64_t)grid.y, (int)b.M, (E*)b.db[0], (E*)b.db[1]);
+                           (int64_t)grid.x, (int)b.M, (E*)b.db[0], (E*)b.db[1]);
         VQ_LAUNCHED("k_bias_sum");
     }
     return VQ_OK;
@@ -273,19 +309,22 @@ vq_status backward(const Backward& b, Arena& ws, bool run, hipStream_t st)
             d[i] = {D[i], b.T, ldd, ldd};
         }
     float* part[2] = {nullptr, nullptr};
+    const int rows = grad_rows(b.T, b.M);
     if (want_db)
         for (int i = 0; i < b.nm; ++i)
-            part[i] = static_cast<float*>(ws.take((size_t)((b.T + kGradRows - 1) / kGradRows) * b.M * sizeof(float)));
+            part[i] = static_cast<float*>(ws.take((size_t)((b.T + rows - 1) / rows) * b.M * sizeof(float)));
     Mat x{b.X, b.T, b.N, b.ldx};
     Mat w[2] = {{b.W[0], b.M, b.N, b.ldw}, {b.W[1], b.M, b.N, b.ldw}};
     const size_t gx = b.dX ? gemm_workspace(GEMM_DX, b.N, b.T, b.M, b.nm, 1) : 0;
     const int nb = b.dW[0] && b.dW[1] ? 2 : 1;
     const size_t gw = want_dw ? gemm_workspace(GEMM_DW, b.N, b.M, b.T, 1, nb) : 0;
     void* part_ws = ws.take(std::max(gx, gw));       // the two products run one after the other
-    if (want_dw && !loads_ok(x)) VQ_TRY(pack(x, ws, run, st));
+    Packer pk{ws};
+    if (want_dw && !loads_ok(x)) pk.add(x);
     if (b.dX && (!loads_ok(w[0]) || (b.nm > 1 && !loads_ok(w[1]))))
-        for (int i = 0; i < b.nm; ++i) VQ_TRY(pack(w[i], ws, run, st));
+        for (int i = 0; i < b.nm; ++i) pk.add(w[i]);
     if (!run) return VQ_OK;
+    VQ_TRY(pk.launch(st));
 
     if (D[0] || want_db)
         VQ_TRY(b.dtype == VQ_BF16 ? grad_launch<Bf16>(b, D, ldd, part, st) : grad_launch<F16>(b, D, ldd, part, st));
@@ -325,6 +364,7 @@ vq_status check_sizes(const std::string& call, int64_t T, int64_t M, int64_t N, 
 {
     VQ_CHECK(T >= 0 && T <= kMaxTokens, call + ": T must be in [0, 2^28]");
     VQ_CHECK(M >= 1 && M <= kMaxSize && N >= 1 && N <= kMaxSize, call + ": M and N must be in [1, 2^20]");
+    VQ_CHECK(T * std::max(M, N) <= ((int64_t)1 << 40), call + ": T * max(M, N) must be at most 2^40");
     VQ_CHECK(dtype == VQ_BF16 || dtype == VQ_F16, call + ": dtype must be VQ_BF16 or VQ_F16");
     VQ_CHECK(act >= VQ_ACT_NONE && act <= VQ_ACT_SIGMOID, call + ": unknown activation");
     return VQ_OK;
@@ -377,7 +417,7 @@ vq_status vq_linear(int64_t T, int64_t M, int64_t N, int dtype, int act, const v
     VQ_MATRIX(W, M, N, ldw, call, "W");
     VQ_MATRIX(bias, 1, M, M, call, "bias");
     VQ_MATRIX(R, T, M, ldr, call, "R");
-    Forward f{T, M, N, dtype, 1, X, ldx, {W, nullptr}, ldw, {act, 0, {bias, nullptr}, R, Y, {Z, nullptr}, ldr, ldy, ldz}};
+    Forward f{T, M, N, dtype, 1, X, ldx, {W, nullptr}, ldw, {act, {bias, nullptr}, R, Y, {Z, nullptr}, ldr, ldy, ldz}};
     Arena a{nullptr};
     VQ_TRY(forward(f, a, false, as_stream(stream)));
     VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_linear: workspace too small");
@@ -421,7 +461,7 @@ vq_status vq_gated(int64_t T, int64_t M, int64_t N, int dtype, int act, const vo
     VQ_MATRIX(Wu, M, N, ldw, call, "Wu");
     VQ_MATRIX(bg, 1, M, M, call, "bg");
     VQ_MATRIX(bu, 1, M, M, call, "bu");
-    Forward f{T, M, N, dtype, 2, X, ldx, {Wg, Wu}, ldw, {act, 0, {bg, bu}, nullptr, H, {G, U}, 0, ldh, ldz}};
+    Forward f{T, M, N, dtype, 2, X, ldx, {Wg, Wu}, ldw, {act, {bg, bu}, nullptr, H, {G, U}, 0, ldh, ldz}};
     Arena a{nullptr};
     VQ_TRY(forward(f, a, false, as_stream(stream)));
     VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_gated: workspace too small");

@@ -307,23 +307,24 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     if (batch) e.Y = a.Y2;
     constexpr int kRow = FP * 16;                   // floats per row of the tile
     constexpr int kLanes = NI * 2;                  // lanes per row
-    static_assert(2 * 32 * kRow * 4 <= L::BP * kBK * 2 && L::BP == L::BQ, "two waves' tiles fit one operand buffer");
+    constexpr int kSmall = (L::BP < L::BQ ? L::BP : L::BQ) * kBK * 2;            // bytes of the smaller buffer
+    constexpr int J = 2 * 32 * kRow * 4 <= kSmall ? 2 : 1;     // columns of fragments at a time: two waves a buffer
+    static_assert(2 * J * 16 * kRow * 4 <= kSmall && FQ % J == 0, "two waves' tiles fit one operand buffer");
     __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));     // the last loads into LDS too
     asm volatile("s_barrier" ::: "memory");
-    char* const bufs[4] = {pb0, pb1, qb0, qb1};
-    char* w = (wave & 4 ? (wave & 2 ? bufs[3] : bufs[2]) : (wave & 2 ? bufs[1] : bufs[0])) + (wave & 1) * 32 * kRow * 4;
+    char* const w = (wave & 4 ? (wave & 2 ? qb1 : qb0) : (wave & 2 ? pb1 : pb0)) + (wave & 1) * J * 16 * kRow * 4;
     // 16-byte chunk c of row r sits in slot c ^ (r & 7)
     const auto at = [&](int row, int chunk) { return reinterpret_cast<f32x4*>(w + row * kRow * 4 + (chunk ^ (row & 7)) * 16); };
 #pragma unroll
-    for (int h = 0; h < FQ / 2; ++h) {
+    for (int h = 0; h < FQ / J; ++h) {
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj)
+        for (int jj = 0; jj < J; ++jj)
 #pragma unroll
-            for (int i = 0; i < FP; ++i) *at(jj * 16 + q_l, i * 4 + (lane >> 4)) = acc[i][h * 2 + jj];
+            for (int i = 0; i < FP; ++i) *at(jj * 16 + q_l, i * 4 + (lane >> 4)) = acc[i][h * J + jj];
 #pragma unroll 1
-        for (int r = 0; r < 32; r += 64 / kLanes) {
+        for (int r = 0; r < J * 16; r += 64 / kLanes) {
             const int row = r + lane / kLanes, c = (lane % kLanes) * 2;
-            const int q = q0 + (wq * FQ + h * 2) * 16 + row;
+            const int q = q0 + (wq * FQ + h * J) * 16 + row;
             const int p = p0 + wp * NI * 16 + c * 4;
             if (q < a.nq && p < a.np) {
                 const auto take = [&](int chunk, float (&v)[8]) {
@@ -408,30 +409,41 @@ struct Plan {
     size_t part_bytes;
 };
 
+// Tile and split by a model of the time in microseconds, fitted to 76 products
+// of 64 to 28672 (mean loss against the best of all tiles and splits: 0.6 %).
+// One 256 x 256 tile a CU: 1.45 a step, 10 a round for the epilogue and the
+// pipeline's start.  128 x 128 tiles: 0.8 a step with one on a CU, 1.15 with two,
+// 4 a round.  Split sums: 9.5 for the second launch and the parts' traffic.
+// (2048 x 4096 x 11008: 156 us as 256 x 256 over two splits, 170 us as 128 x 128;
+// 1024 x 2048 x 2048: 31 us and 19 us.)
 Plan make_plan(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int nbatch)
 {
     const bool pair = kind == GEMM_GATED;
+    const int nout = pair ? 2 : nbatch;
     Plan best{};
     double best_cost = 1e300;
-    static const int shapes[][2] = {{8, 4}, {4, 2}};
-    for (const auto& s : shapes) {
+    for (int small = 0; small < 2; ++small) {
         Plan p;
-        p.fp = s[0];
-        p.fq = s[1];
+        p.fp = small ? 4 : 8;
+        p.fq = small ? 2 : 4;
         const int bp = kWP * p.fp * 16 / (pair ? 2 : 1), bq = kWQ * p.fq * 16;
         p.ntp = (int)((np + bp - 1) / bp);
         p.ntq = (int)((nq + bq - 1) / bq);
         p.seg_steps = (int)((K + kBK - 1) / kBK);
         p.steps = p.seg_steps * nseg;
         p.pitch = (int)((np + 7) / 8 * 8);
-        const int64_t tiles = (int64_t)p.ntp * p.ntq * nbatch;
-        for (int sp = 1; sp <= 16 && 2 * sp <= p.steps + 1; ++sp) {
-            // rounds of the chip, each as long as its share of K steps; a step of
-            // the large tile costs four of the small one at twice the tiles per CU
-            const double slots = p.fp == 8 ? 256.0 : 512.0;
-            const double rounds = (double)((int64_t)((tiles * sp + slots - 1) / slots));
-            double cost = rounds * ((p.steps + sp - 1) / sp + 6.0) * (p.fp == 8 ? 2.0 : 1.2);
-            if (sp > 1) cost += 4.0 + (double)np * nq * (pair ? 2 : nbatch) * (sp + 1) * 4.0 / 4e6;
+        const int pairs = (p.steps + 1) / 2;
+        for (int sp = 1; sp <= 16 && sp <= pairs; ++sp) {
+            const int64_t tiles = (int64_t)p.ntp * p.ntq * nbatch * sp;
+            const double st = 2.0 * ((pairs + sp - 1) / sp);
+            double cost;
+            if (!small) {
+                cost = (double)((tiles + 255) / 256) * (st * 1.45 + 10.0);
+            } else {
+                const int64_t rest = tiles % 512;
+                cost = (double)(tiles / 512) * (st * 1.15 + 4.0) + (rest ? st * (rest <= 256 ? 0.8 : 1.15) + 4.0 : 0.0);
+            }
+            if (sp > 1) cost += 9.5 + 0.8e-6 * (double)np * nq * nout * (sp + 1);
             if (cost < best_cost) {
                 best_cost = cost;
                 best = p;
@@ -439,7 +451,6 @@ Plan make_plan(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int n
             }
         }
     }
-    const int nout = pair ? 2 : nbatch;
     best.part_bytes = best.splits > 1 ? align_up((size_t)best.splits * nout * nq * best.pitch * sizeof(float)) : 0;
     return best;
 }
@@ -501,8 +512,6 @@ vq_status gemm_launch(const GemmArgs& g, void* ws, size_t ws_bytes, hipStream_t 
     t.seg_steps = p.seg_steps; t.steps = p.steps;
     t.splits = p.splits; t.pitch = p.pitch;
     t.epi = g.epi; t.Y2 = g.Y2;
-    set_vec(t.epi);
-    t.epi.vec = t.epi.vec && vec8_ok(g.Y2, g.epi.ldy);
     if (p.splits > 1) {
         Carver cv(ws, ws_bytes);
         t.part = cv.take<float>(p.part_bytes / sizeof(float));

@@ -6,21 +6,26 @@
 //
 // The product runs on the matrix cores with exact operands.  A lane's share of
 // a 16 x 16 x 32 instruction is eight consecutive k of one row, which is one
-// sub-vector of d = 8 (two of d = 4; a shorter one padded with zeros): the lane
-// gathers its centroid row, adds the residual row, multiplies by the column
-// scales and splits the float32 values into bf16 terms hi + lo (+ lowest),
-// each the rounding of what the terms before leave.  The tokens are split
-// alike (bf16 tokens are one term, fp16 two, float32 three), and the products
-// of terms down to 2^-18 (16-bit results) or 2^-27 (float32 results) of the
-// leading one are summed in float32.  Sixteen tokens cost the gathers of one.
+// sub-vector of d = 8 (two of d = 4; one of another length padded with zeros):
+// the lane gathers its centroid row, adds the residual row, multiplies by the
+// column scales and splits the float32 values into bf16 terms hi + lo (+
+// lowest), each the rounding of what the terms before leave.  The tokens are
+// split alike (bf16 tokens are one term, fp16 two, float32 three), and the
+// products of terms down to 2^-18 (16-bit results) or 2^-27 (float32 results)
+// of the leading one are summed in float32.  Sixteen tokens cost the gathers of
+// one.
 //
-// What bounds it is the gathers: each sub-vector is one L1 miss into L2, and a
-// CU keeps about 64 of them in flight.  Neighbouring lanes fetch the two halves
-// of one centroid row in one instruction (one request, not two) and swap them.
-// Indices are read 16 bytes (eight sub-vectors) a lane.
+// What bounds it is the requests from L1 to L2: each sub-vector is one, a CU
+// keeps about 64 of them in flight, and everything else that misses L1 queues
+// with them.  So the tokens' terms and the column scales of a slab of columns
+// are staged in LDS once a workgroup, indices are read 16 bytes (eight
+// sub-vectors) a lane, a block ahead, and neighbouring lanes fetch the two
+// halves of one centroid row in one instruction (one request, not two) and swap
+// them.
 //
-// A workgroup owns 16 rows; its waves take blocks of 32 sub-vectors in turn and
-// their sums are added in wave order.  Where the rows alone leave CUs idle the
+// A workgroup owns 16 rows; its waves (of a pair, the even ones gate and the odd
+// ones up) take blocks of 32 sub-vectors in turn and their sums are added in wave
+// order.  Where the rows alone leave CUs idle the
 // blocks are split over workgroups too, and a second kernel adds the parts in
 // order.  The sparse correction adds sum_e delta_e x[col_e] per row, delta
 // being the exact value less the decoded weight, made once per matrix.
@@ -36,6 +41,7 @@ namespace {
 typedef Bf16::V8 V8;
 
 constexpr int kQRows = 16;
+constexpr int kBlock = 32;                 // sub-vectors of a row that a wave takes at a time
 constexpr int kC2Floats = 2048;            // residual codebooks up to 8 KB are held in LDS
 constexpr int kQTokens = 32;               // tokens per launch
 
@@ -55,7 +61,8 @@ struct QMat {
 struct QArgs {
     QMat q[2];
     int64_t M, N, nb;
-    int d, T, splits;
+    int d, T, nm, splits;
+    int slab;                  // sub-vectors per slab, a multiple of kBlock
     const void* X;
     int64_t ldx;
     int dtype, act;
@@ -91,28 +98,6 @@ __device__ inline void split(const float (&v)[8], V8 (&t)[NTERM])
         }
 }
 
-// Raw tokens of one chunk as loaded, and their terms.  Loads are unconditional
-// (addresses are clamped into the tensor) so that a block's loads can all be in
-// flight; the hardware takes vector loads at any element-aligned address.
-template <int XT> struct RawTokens { typename XType<XT>::E e[8]; };
-
-template <int XT>
-__device__ inline RawTokens<XT> load_tokens(const typename XType<XT>::E* row, int64_t col)
-{
-    RawTokens<XT> v;
-    __builtin_memcpy(v.e, row + col, sizeof(v.e));
-    return v;
-}
-
-template <int XT>
-__device__ inline void token_terms(const RawTokens<XT>& v, V8 (&x)[XType<XT>::kTerms])
-{
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)v.e[i];
-    split<XType<XT>::kTerms>(f, x);
-}
-
 template <class E> __device__ inline float load_x(const void* p, int64_t i) { return (float)static_cast<const E*>(p)[i]; }
 
 __device__ inline float load_any(const void* p, int64_t i, int dtype)
@@ -127,277 +112,346 @@ __device__ inline void store_any(void* p, int64_t i, int dtype, float v)
     else static_cast<_Float16*>(p)[i] = (_Float16)v;
 }
 
-// C indices from sub-vector s of a row of nb, two to a register; past the row's end 0.
-template <int C>
-__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, uint32_t (&k)[C / 2])
+// Eight indices from sub-vector s of a row of nb, two to a register; past the row's end 0.
+__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, uint32_t (&k)[4])
 {
-    if (s + C <= nb) {
-        __builtin_memcpy(k, row + s, C * 2);
+    if (s + 8 <= nb) {
+        __builtin_memcpy(k, row + s, 16);
     } else {
-        uint16_t v[C] = {};
+        uint16_t v[8] = {};
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < 8; ++i)
             if (s + i < nb) v[i] = row[s + i];
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) k[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
+        for (int i = 0; i < 4; ++i) k[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
     }
 }
 
 // Index j of them, at most K - 1.
-template <int C2>
-__device__ inline int index_of(const uint32_t (&k)[C2], int j, int K)
+__device__ inline int index_of(const uint32_t (&k)[4], int j, int K)
 {
     const int v = (int)((k[j >> 1] >> (16 * (j & 1))) & 0xffffu);
     return v < K ? v : K - 1;
 }
 
-// Chunks of eight k slots whose loads a wave has in flight together (registers
-// set it), and the sub-vectors of a row that a wave takes in one step.
-constexpr int chunks_of(int xt, int nt) { return xt == VQ_F32 || nt > 1 ? 2 : 4; }
-constexpr int block_of(int d, int xt, int nt) { return 4 * chunks_of(xt, nt) * (d == 4 ? 2 : 1); }
+// Row k of a codebook of any d <= 8, zero padded to eight: two (overlapping)
+// four-element loads inside the row for d >= 4.
+__device__ inline void load_row(const float* C, int k, int d, float (&w)[8])
+{
+    const float* row = C + (int64_t)k * d;
+    if (d >= 4) {
+        float a[4], b[4];
+        __builtin_memcpy(a, row, 16);
+        __builtin_memcpy(b, row + d - 4, 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = a[i];
+            float v = 0.0f;                          // element 4 + i is b[8 - d + i]
+#pragma unroll
+            for (int q = i; q < 4; ++q) v = q - i == 8 - d ? b[q] : v;
+            w[4 + i] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const float v = row[i < d ? i : d - 1];
+            w[i] = i < d ? v : 0.0f;
+        }
+#pragma unroll
+        for (int i = 3; i < 8; ++i) w[i] = 0.0f;
+    }
+}
+
+// Columns of LDS per sub-vector: d = 8 and 4 as they are, others padded to eight.
+__host__ __device__ constexpr int slots_of(int D) { return D ? D : 8; }
+// Elements between tokens in LDS: 16 bytes past a multiple of 128, so that eight
+// tokens' reads of one column are in different banks.
+__host__ __device__ constexpr int token_pitch(int columns) { return columns + 8; }
 
 // D = 8 or 4: sub-vectors of that length in 16-byte aligned codebooks (4: an even
 // number of them in a row).  D = 0: any d, one sub-vector per chunk of eight k slots.
-template <int D, int XT, int NT, int NM>
+template <int D, int XT, int NT>
 __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
 {
+    typedef typename XType<XT>::E E;
     constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
     constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
+    constexpr int S = slots_of(D);
+    constexpr int H = D ? 4 : 2;                       // chunks whose gathers are in flight together
     extern __shared__ __align__(16) float lds[];
     const int d = D ? D : a.d;
-    const int nwaves = blockDim.x >> 6;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int nm = a.nm;
+    const int nthreads = blockDim.x, nwaves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int64_t row0 = (int64_t)blockIdx.x * kQRows;
     const int64_t row = row0 + r < a.M ? row0 + r : a.M - 1;
+    // this wave's matrix, its place among the matrix's waves and their number
+    const int mm = nm > 1 ? wave & 1 : 0, turn = nm > 1 ? wave >> 1 : wave, turns = nm > 1 ? nwaves >> 1 : nwaves;
 
-    // residual codebooks
-    int c2_at[2] = {-1, -1}, used = 0;
-    for (int m = 0; m < NM; ++m)
-        if (a.q[m].C2 && a.q[m].K2 * d <= kC2Floats) {
-            c2_at[m] = used;
-            for (int i = threadIdx.x; i < a.q[m].K2 * d; i += blockDim.x) lds[used + i] = a.q[m].C2[i];
-            used += (a.q[m].K2 * d + 3) & ~3;
+    // LDS: residual codebooks (rows of S floats), column scales [scaled][slab * S],
+    // token terms [XTERMS][T][pitch]; the sums' exchange takes the last two's place
+    const int columns = a.slab * S, pitch = token_pitch(columns);
+    int used = 0, c2_at = -1, cs_at = -1, cs_rows = 0;
+    for (int m = 0; m < nm; ++m) {
+        if (a.q[m].C2 && a.q[m].K2 * S <= kC2Floats) {
+            if (m == mm) c2_at = used;
+            for (int i = threadIdx.x; i < a.q[m].K2 * S; i += nthreads) {
+                const int k = i / S, e = i % S;
+                lds[used + i] = D || e < d ? a.q[m].C2[k * d + e] : 0.0f;
+            }
+            used += a.q[m].K2 * S;
         }
-    __syncthreads();
+        if (a.q[m].cs) {
+            if (m == mm) cs_at = cs_rows * columns;
+            ++cs_rows;
+        }
+    }
+    float* const cs = lds + used;
+    __bf16* const xs = reinterpret_cast<__bf16*>(cs + cs_rows * columns);
+    const QMat q = a.q[mm];
 
-    f32x4 acc[NM][NT];
+    f32x4 acc[NT];
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // sparse corrections of this wave's rows: lane -> token lane % tl
+    constexpr int kJobs = 4;                                   // two matrices' 16 rows over at least eight waves
+    float corr[kJobs] = {};
+    int tl = 1;
+    while (tl < a.T) tl *= 2;
 
-    typedef typename XType<XT>::E E;
-    const E* xrow[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)         // tokens past the last read the last: their sums are not stored
-        xrow[n] = static_cast<const E*>(a.X) + (n * 16 + r < a.T ? n * 16 + r : a.T - 1) * a.ldx;
-
-    constexpr int H = chunks_of(XT, NT), B = block_of(D, XT, NT);
-    const int nkb = (int)((a.nb + B - 1) / B);
+    const int nkb = (int)((a.nb + kBlock - 1) / kBlock);
     const int kb0 = (int)((int64_t)nkb * blockIdx.y / a.splits), kb1 = (int)((int64_t)nkb * (blockIdx.y + 1) / a.splits);
-    uint32_t i1[NM][H * U / 2], i2[NM][H * U / 2];
+    const int slab_blocks = a.slab / kBlock;
+    uint32_t i1[4], i2[4] = {};
     const auto load_block = [&](int kb) {
-        const int64_t s = (int64_t)kb * B + g * (H * U);
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            load_indices<H * U>(a.q[m].idx1 + row * a.nb, s, a.nb, i1[m]);
-            if (a.q[m].C2) load_indices<H * U>(a.q[m].idx2 + row * a.nb, s, a.nb, i2[m]);
-        }
+        const int64_t s = (int64_t)kb * kBlock + g * 8;
+        load_indices(q.idx1 + row * a.nb, s, a.nb, i1);
+        if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, i2);
     };
-    if (kb0 + wave < kb1) load_block(kb0 + wave);
-#pragma unroll 1
-    for (int kb = kb0 + wave; kb < kb1; kb += nwaves) {
-        const int64_t s = (int64_t)kb * B + g * (H * U);
-        // columns of chunk j; past the row's end the last chunk's, with zero tokens
-        const auto column = [&](int j) {
-            const int64_t sv = s + j * U, top = a.nb - U;
-            return (sv < top ? sv : top) * d;
+
+    for (int sb = kb0; sb < kb1; sb += slab_blocks) {
+        const int se = sb + slab_blocks < kb1 ? sb + slab_blocks : kb1;
+        const int64_t sv0 = (int64_t)sb * kBlock;
+        const int cols = (se - sb) * kBlock * S;               // of this slab
+        if (sb + turn < se) load_block(sb + turn);
+        __syncthreads();
+        // column c of the slab: element c % S of sub-vector sv0 + c / S; zero past the row and past d
+        const auto source = [&](int c) -> int64_t {
+            const int64_t sv = sv0 + c / S;
+            const int e = c % S;
+            return sv < a.nb && (D || e < d) ? sv * d + e : -1;
         };
-        RawTokens<XT> x[NT][H];
+        int at = 0;
+        for (int m = 0; m < nm; ++m)
+            if (a.q[m].cs) {
+                for (int c = threadIdx.x; c < cols; c += nthreads) {
+                    const int64_t j = source(c);
+                    cs[at + c] = j >= 0 ? a.q[m].cs[j] : 0.0f;
+                }
+                at += columns;
+            }
+        for (int t = 0; t < a.T; ++t) {
+            const E* x = static_cast<const E*>(a.X) + t * a.ldx;
+            for (int c = threadIdx.x * 8; c < cols; c += nthreads * 8) {
+                float v[8];
+                const int64_t j = source(c);
+                if (D && j >= 0 && j + 8 <= a.N) {
+                    E e[8];
+                    __builtin_memcpy(e, x + j, sizeof(e));
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < H; ++j) {
-                if (D) {
-                    x[n][j] = load_tokens<XT>(xrow[n], column(j));
+                    for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[n][j].e[i] = xrow[n][column(j) + (i < d ? i : d - 1)];
-                }
-            }
-        if ((int64_t)kb * B + B > a.nb) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-                    if (s + j * U >= a.nb) x[n][j] = RawTokens<XT>{};
-        }
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const QMat& q = a.q[m];
-            float w[H][8];
-            if (D == 8) {
-                const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
-                const int odd = lane & 1;
-                f32x4 ga[H], gb[H];
-#pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    const int mine = index_of(i1[m], j, q.K1), other = swap_pair(mine);
-                    ga[j] = C[2 * (odd ? other : mine) + odd];
-                    gb[j] = C[2 * (odd ? mine : other) + odd];
-                }
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float other = swap_pair(odd ? ga[j][i] : gb[j][i]);
-                        w[j][i] = odd ? other : ga[j][i];
-                        w[j][4 + i] = odd ? gb[j][i] : other;
-                    }
-            } else if (D == 4) {
-                const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const f32x4 v = C[index_of(i1[m], j * 2 + u, q.K1)];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[j][u * 4 + i] = v[i];
-                    }
-            } else {
-#pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    const float* c = q.C1 + (int64_t)index_of(i1[m], j, q.K1) * d;
-#pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float v = c[i < d ? i : d - 1];
-                        w[j][i] = i < d ? v : 0.0f;
+                        const int64_t k = source(c + i);
+                        v[i] = k >= 0 ? (float)x[k] : 0.0f;
                     }
                 }
+                V8 w[XTERMS];
+                split<XTERMS>(v, w);
+#pragma unroll
+                for (int k = 0; k < XTERMS; ++k) *reinterpret_cast<V8*>(xs + (k * a.T + t) * pitch + c) = w[k];
             }
-            if (q.C2) {
-                const float* c2 = c2_at[m] >= 0 ? lds + c2_at[m] : q.C2;
+        }
+        __syncthreads();
+
+#pragma unroll 1
+        for (int kb = sb + turn; kb < se; kb += turns) {
+            uint32_t k1[4], k2[4];
 #pragma unroll
-                for (int j = 0; j < H; ++j)
-                    if (D) {
+            for (int i = 0; i < 4; ++i) {
+                k1[i] = i1[i];
+                k2[i] = i2[i];
+            }
+            if (kb + turns < se) load_block(kb + turns);
+            const int c0 = ((kb - sb) * kBlock + g * 8) * S;   // the lane's first column in the slab
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {        // halves of one row, or two rows
-                            const int k = index_of(i2[m], j * U + (D == 4 ? u : 0), q.K2);
-                            const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + k * D + (D == 8 ? u * 4 : 0));
+            for (int h = 0; h < 8 / U / H; ++h) {
+                float w[H][8];
+                if (D == 8) {
+                    const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
+                    const int odd = lane & 1;
+                    f32x4 ga[H], gb[H];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) w[j][u * 4 + i] += v[i];
+                    for (int j = 0; j < H; ++j) {
+                        const int mine = index_of(k1, h * H + j, q.K1), other = swap_pair(mine);
+                        ga[j] = C[2 * (odd ? other : mine) + odd];
+                        gb[j] = C[2 * (odd ? mine : other) + odd];
+                    }
+#pragma unroll
+                    for (int j = 0; j < H; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float other = swap_pair(odd ? ga[j][i] : gb[j][i]);
+                            w[j][i] = odd ? other : ga[j][i];
+                            w[j][4 + i] = odd ? gb[j][i] : other;
                         }
-                    } else {
-                        const float* c = c2 + index_of(i2[m], j, q.K2) * d;
+                } else if (D == 4) {
+                    const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float v = c[i < d ? i : d - 1];
-                            w[j][i] += i < d ? v : 0.0f;
+                    for (int j = 0; j < H; ++j)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const f32x4 v = C[index_of(k1, j * 2 + u, q.K1)];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[j][u * 4 + i] = v[i];
+                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) load_row(q.C1, index_of(k1, h * H + j, q.K1), d, w[j]);
+                }
+                if (q.C2) {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) {
+                        if (D == 0 && c2_at < 0) {
+                            float v[8];
+                            load_row(q.C2, index_of(k2, h * H + j, q.K2), d, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[j][i] += v[i];
+                        } else {
+                            const float* c2 = c2_at >= 0 ? lds + c2_at : q.C2;
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {        // halves of one row, or two rows
+                                const int k = index_of(k2, (h * H + j) * U + (D == 4 ? u : 0), q.K2);
+                                const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + k * S + (D == 4 ? 0 : u * 4));
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[j][u * 4 + i] += v[i];
+                            }
                         }
                     }
-            }
-            if (q.cs) {
+                }
+                if (cs_at >= 0) {
+#pragma unroll
+                    for (int j = 0; j < H; ++j)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(cs + cs_at + c0 + (h * H + j) * 8 + u * 4);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[j][u * 4 + i] *= v[i];
+                        }
+                }
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
-                    float c[8];
-                    if (D) {
-                        __builtin_memcpy(c, q.cs + column(j), sizeof(c));
-                    } else {
+                    V8 wt[WTERMS];
+                    split<WTERMS>(w[j], wt);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) c[i] = q.cs[column(j) + (i < d ? i : d - 1)];
+                    for (int n = 0; n < NT; ++n) {
+                        // tokens past the last read the last: their sums are not stored
+                        const int t = n * 16 + r < a.T ? n * 16 + r : a.T - 1;
+                        V8 xt[XTERMS];
+#pragma unroll
+                        for (int k = 0; k < XTERMS; ++k)
+                            xt[k] = *reinterpret_cast<const V8*>(xs + (k * a.T + t) * pitch + c0 + (h * H + j) * 8);
+#pragma unroll
+                        for (int p = 0; p < WTERMS; ++p)
+#pragma unroll
+                            for (int k = 0; k < XTERMS; ++k)
+                                if (p + k < WTERMS) acc[n] = Bf16::mfma(wt[p], xt[k], acc[n]);
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[j][i] *= c[i];
                 }
+                __builtin_amdgcn_sched_barrier(0);             // one group's rows in registers at a time
             }
-            if (m == NM - 1 && kb + nwaves < kb1) load_block(kb + nwaves);
+        }
+
+        // exact entries whose column lies in the slab: x from its terms
+        const int64_t col0 = sv0 * d, col1 = (int64_t)se * kBlock < a.nb ? (int64_t)se * kBlock * d : a.N;
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                V8 wt[WTERMS];
-                split<WTERMS>(w[j], wt);
+        for (int job = 0; job < kJobs; ++job) {
+            const int id = job * nwaves + wave, m = id / kQRows, rr = id % kQRows;
+            const int t = lane & (tl - 1);
+            if (id >= nm * kQRows || row0 + rr >= a.M || t >= a.T) continue;
+            const QMat& q = a.q[m];
+            if (!q.row_ptr) continue;
+            const int e1 = q.row_ptr[row0 + rr + 1];
+            for (int e = q.row_ptr[row0 + rr] + lane / tl; e < e1; e += 64 / tl) {
+                const int64_t j = q.col[e];
+                if (j < col0 || j >= col1) continue;
+                const int c = D ? (int)(j - col0) : (int)((j - col0) / d) * S + (int)((j - col0) % d);
+                float x = 0.0f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    V8 xt[XTERMS];
-                    token_terms<XT>(x[n][j], xt);
-#pragma unroll
-                    for (int p = 0; p < WTERMS; ++p)
-#pragma unroll
-                        for (int t = 0; t < XTERMS; ++t)
-                            if (p + t < WTERMS) acc[m][n] = Bf16::mfma(wt[p], xt[t], acc[m][n]);
-                }
+                for (int k = 0; k < XTERMS; ++k) x += (float)xs[(k * a.T + t) * pitch + c];
+                corr[job] = fmaf(q.delta[e], x, corr[job]);
             }
         }
     }
 
-    // sums over the waves, in wave order; the sparse corrections beside them
-    float* red = lds + used;                                   // [nwaves][NM][NT][64] of four rows
-    float* corr = red + nwaves * NM * NT * 256;                // [NM][NT * 16][16]
+    // sums over the waves, in wave order, and the corrections
+    __syncthreads();
+    float* red = lds + used;                                   // [nwaves][NT][64] of four rows
+    float* cor = red + nwaves * NT * 256;                      // [nm][NT * 16][16]
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
+    for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(red + ((wave * NT + n) * 64 + lane) * 4) = acc[n];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            *reinterpret_cast<f32x4*>(red + (((wave * NM + m) * NT + n) * 64 + lane) * 4) = acc[m][n];
-    int tl = 1;                                                // lanes across tokens
-    while (tl < a.T) tl *= 2;
-    for (int job = wave; job < NM * kQRows; job += nwaves) {
-        const int m = job / kQRows, rr = job % kQRows;
-        const QMat& q = a.q[m];
-        const int t = lane & (tl - 1);
-        float c = 0.0f;
-        if (q.row_ptr && blockIdx.y == 0 && row0 + rr < a.M && t < a.T) {
-            const int e1 = q.row_ptr[row0 + rr + 1];
-            for (int e = q.row_ptr[row0 + rr] + lane / tl; e < e1; e += 64 / tl) {
-                const int j = q.col[e];
-                if ((uint32_t)j < (uint64_t)a.N)
-                    c = fmaf(q.delta[e], load_x<typename XType<XT>::E>(a.X, t * a.ldx + j), c);
-            }
-        }
+    for (int job = 0; job < kJobs; ++job) {
+        const int id = job * nwaves + wave, m = id / kQRows, rr = id % kQRows;
+        float c = corr[job];
         for (int o = 32; o >= tl; o >>= 1) c += __shfl_xor(c, o, 64);
-        if (lane < tl && lane < NT * 16) corr[(m * NT * 16 + lane) * kQRows + rr] = c;
+        if (id < nm * kQRows && lane < tl && lane < NT * 16) cor[(m * NT * 16 + lane) * kQRows + rr] = c;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < NT * 256; i += blockDim.x) {
+    for (int i = threadIdx.x; i < NT * 256; i += nthreads) {
         // item i of the accumulators: fragment n, lane l, element e -> token, row
         const int n = i >> 8, l = (i >> 2) & 63, e = i & 3;
         const int t = n * 16 + (l & 15), rr = (l >> 4) * 4 + e;
         const int64_t out_row = row0 + rr;
         if (t >= a.T || out_row >= a.M) continue;
-        float z[NM];
+        float z[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
+        for (int m = 0; m < 2; ++m) {
+            if (m >= nm) break;
             float v = 0.0f;
-            for (int w = 0; w < nwaves; ++w) v += red[((w * NM + m) * NT + n) * 256 + (i & 255)];
+            for (int w = m; w < nwaves; w += nm) v += red[(w * NT + n) * 256 + (i & 255)];
             if (a.q[m].rs) v *= a.q[m].rs[out_row];
-            z[m] = v + corr[(m * NT * 16 + t) * kQRows + rr];
-            if (a.part) a.part[(((int64_t)blockIdx.y * NM + m) * a.T + t) * a.M + out_row] = z[m];
+            z[m] = v + cor[(m * NT * 16 + t) * kQRows + rr];
+            if (a.part) a.part[(((int64_t)blockIdx.y * nm + m) * a.T + t) * a.M + out_row] = z[m];
             else if (a.bias[m]) z[m] += load_any(a.bias[m], out_row, XT);
         }
         if (a.part) continue;
         float y = act_full(a.act, z[0]);
-        if (NM > 1) y *= z[NM - 1];
+        if (nm > 1) y *= z[1];
         if (a.R) y += load_any(a.R, t * a.ldr + out_row, XT);
         store_any(a.Y, t * a.ldy + out_row, XT, y);
     }
 }
 
 // Adds the parts in order and applies the epilogue.
-template <int NM>
 __global__ __launch_bounds__(256) void k_qffn_finish(const QArgs a)
 {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t n = (int64_t)a.T * a.M;
     if (e >= n) return;
     const int64_t t = e / a.M, row = e - t * a.M;
-    float z[NM];
+    float z[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
+    for (int m = 0; m < 2; ++m) {
+        if (m >= a.nm) break;
         float v = 0.0f;
-        for (int s = 0; s < a.splits; ++s) v += a.part[((int64_t)s * NM + m) * n + e];
+        for (int s = 0; s < a.splits; ++s) v += a.part[((int64_t)s * a.nm + m) * n + e];
         z[m] = a.bias[m] ? v + load_any(a.bias[m], row, a.dtype) : v;
     }
     float y = act_full(a.act, z[0]);
-    if (NM > 1) y *= z[NM - 1];
+    if (a.nm > 1) y *= z[1];
     if (a.R) y += load_any(a.R, t * a.ldr + row, a.dtype);
     store_any(a.Y, t * a.ldy + row, a.dtype, y);
 }
@@ -441,64 +495,85 @@ struct QPlan {
     int64_t groups;
 };
 
-// Sixteen waves a workgroup where the row groups give less than two workgroups of
-// eight a CU; each row's sub-vectors are split over up to 16 workgroups where
-// they give less than one of sixteen (at least 32 sub-vectors a wave).
-QPlan q_plan(int64_t M, int64_t nb)
+// Sixteen waves a workgroup (one a CU, up to 144 KB of LDS) where the matrices
+// have a block for each, else eight (two a CU).  Each row's sub-vectors are split
+// over up to 16 workgroups where the row groups leave CUs idle.
+QPlan q_plan(int64_t M, int64_t nb, int nm)
 {
     QPlan p;
     p.groups = (M + kQRows - 1) / kQRows;
-    const int64_t nkb = (nb + 31) / 32;
-    p.waves = nkb >= 16 && p.groups < 512 ? 16 : nkb >= 4 ? 8 : 4;
+    const int64_t blocks = (nb + kBlock - 1) / kBlock * nm;
+    p.waves = blocks >= 16 ? 16 : 8;
     p.splits = 1;
-    while (p.splits < 16 && p.groups * p.splits < 256 && nkb >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+    while (p.splits < 16 && p.groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
     return p;
 }
 
 size_t q_workspace(int64_t M, int64_t nb, int64_t T, int nm)
 {
-    const QPlan p = q_plan(M, nb);
+    const QPlan p = q_plan(M, nb, nm);
     const int64_t t = T < kQTokens ? T : kQTokens;
     return p.splits > 1 ? align_up((size_t)p.splits * nm * t * M * sizeof(float)) : 0;
 }
 
-template <int D, int XT, int NT, int NM>
-vq_status q_launch(const QArgs& a, const QPlan& p, hipStream_t st)
+template <int D, int XT, int NT>
+vq_status q_launch(QArgs a, const QPlan& p, hipStream_t st)
 {
-    size_t lds = 0;
-    for (int m = 0; m < NM; ++m)
-        if (a.q[m].C2 && a.q[m].K2 * a.d <= kC2Floats) lds += (a.q[m].K2 * a.d + 3) & ~3;
-    lds = (lds + (size_t)p.waves * NM * NT * 256 + (size_t)NM * NT * 16 * kQRows) * sizeof(float);
-    hipLaunchKernelGGL((k_qffn<D, XT, NT, NM>), dim3((unsigned)p.groups, p.splits), dim3(p.waves * 64), lds, st, a);
+    constexpr int S = slots_of(D);
+    size_t c2 = 0;
+    int scales = 0;
+    for (int m = 0; m < a.nm; ++m) {
+        if (a.q[m].C2 && a.q[m].K2 * S <= kC2Floats) c2 += (size_t)a.q[m].K2 * S * sizeof(float);
+        scales += a.q[m].cs != nullptr;
+    }
+    const size_t cap = p.waves == 16 ? 144 * 1024 : 72 * 1024;
+    const size_t per_token = XType<XT>::kTerms * 2 * (size_t)a.T;
+    const auto slab_bytes = [&](int64_t sv) {
+        return (size_t)scales * sv * S * sizeof(float) + per_token * token_pitch((int)sv * S);
+    };
+    // balanced slabs of whole blocks
+    const int64_t nkb = (a.nb + kBlock - 1) / kBlock, mine = (nkb + p.splits - 1) / p.splits;
+    int64_t slabs = 1;
+    while (slabs < mine && c2 + slab_bytes((mine + slabs - 1) / slabs * kBlock) > cap) ++slabs;
+    a.slab = (int)((mine + slabs - 1) / slabs * kBlock);
+    const size_t sums = ((size_t)p.waves * NT * 256 + (size_t)a.nm * NT * 16 * kQRows) * sizeof(float);
+    const size_t lds = c2 + std::max(slab_bytes(a.slab), sums);
+    const auto kern = k_qffn<D, XT, NT>;
+    if (lds > 64 * 1024) {
+        static thread_local int set_dev = -1;
+        int dev = 0;
+        VQ_HIP(hipGetDevice(&dev));
+        if (set_dev != dev) {
+            VQ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       160 * 1024));
+            set_dev = dev;
+        }
+    }
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.groups, p.splits), dim3(p.waves * 64), lds, st, a);
     VQ_LAUNCHED("k_qffn");
     return VQ_OK;
 }
 
-template <int D, int XT, int NT>
-vq_status q_matrices(const QArgs& a, const QPlan& p, int nm, hipStream_t st)
-{
-    return nm == 2 ? q_launch<D, XT, NT, 2>(a, p, st) : q_launch<D, XT, NT, 1>(a, p, st);
-}
-
 template <int D, int XT>
-vq_status q_tokens(const QArgs& a, const QPlan& p, int nm, hipStream_t st)
+vq_status q_tokens(const QArgs& a, const QPlan& p, hipStream_t st)
 {
-    return a.T > 16 ? q_matrices<D, XT, 2>(a, p, nm, st) : q_matrices<D, XT, 1>(a, p, nm, st);
+    return a.T > 16 ? q_launch<D, XT, 2>(a, p, st) : q_launch<D, XT, 1>(a, p, st);
 }
 
 template <int D>
-vq_status q_type(const QArgs& a, const QPlan& p, int nm, hipStream_t st)
+vq_status q_type(const QArgs& a, const QPlan& p, hipStream_t st)
 {
     switch (a.dtype) {
-    case VQ_BF16: return q_tokens<D, VQ_BF16>(a, p, nm, st);
-    case VQ_F16: return q_tokens<D, VQ_F16>(a, p, nm, st);
-    default: return q_tokens<D, VQ_F32>(a, p, nm, st);
+    case VQ_BF16: return q_tokens<D, VQ_BF16>(a, p, st);
+    case VQ_F16: return q_tokens<D, VQ_F16>(a, p, st);
+    default: return q_tokens<D, VQ_F32>(a, p, st);
     }
 }
 
 vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
 {
-    const QPlan p = q_plan(a.M, a.nb);
+    const QPlan p = q_plan(a.M, a.nb, nm);
+    a.nm = nm;
     a.splits = p.splits;
     a.part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
     bool vec = a.d == 8 || (a.d == 4 && a.nb % 2 == 0);          // chunks of eight columns
@@ -512,11 +587,9 @@ vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
         a.X = X + t0 * a.ldx * e;
         a.R = R ? R + t0 * a.ldr * e : nullptr;
         a.Y = Y + t0 * a.ldy * e;
-        VQ_TRY(vec && a.d == 8 ? q_type<8>(a, p, nm, st) : vec ? q_type<4>(a, p, nm, st) : q_type<0>(a, p, nm, st));
+        VQ_TRY(vec && a.d == 8 ? q_type<8>(a, p, st) : vec ? q_type<4>(a, p, st) : q_type<0>(a, p, st));
         if (a.part) {
-            const dim3 grid(grid_for((int64_t)a.T * a.M, 256));
-            if (nm == 2) hipLaunchKernelGGL(k_qffn_finish<2>, grid, dim3(256), 0, st, a);
-            else hipLaunchKernelGGL(k_qffn_finish<1>, grid, dim3(256), 0, st, a);
+            hipLaunchKernelGGL(k_qffn_finish, dim3(grid_for((int64_t)a.T * a.M, 256)), dim3(256), 0, st, a);
             VQ_LAUNCHED("k_qffn_finish");
         }
     }
