@@ -245,29 +245,42 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
         int at = 0;
         for (int m = 0; m < nm; ++m)
             if (a.q[m].cs) {
+#pragma unroll 4
                 for (int c = threadIdx.x; c < cols; c += nthreads) {
                     const int64_t j = source(c);
-                    cs[at + c] = j >= 0 ? a.q[m].cs[j] : 0.0f;
+                    const float v = a.q[m].cs[j >= 0 ? j : 0];
+                    cs[at + c] = j >= 0 ? v : 0.0f;
                 }
                 at += columns;
             }
-        for (int t = 0; t < a.T; ++t) {
-            const E* x = static_cast<const E*>(a.X) + t * a.ldx;
-            for (int c = threadIdx.x * 8; c < cols; c += nthreads * 8) {
-                float v[8];
-                const int64_t j = source(c);
-                if (D && j >= 0 && j + 8 <= a.N) {
-                    E e[8];
-                    __builtin_memcpy(e, x + j, sizeof(e));
+        // chunks of eight columns of all tokens, four a thread in flight
+        const int per = cols / 8, total = per * a.T;
+        for (int i0 = threadIdx.x; i0 < total; i0 += nthreads * 4) {
+            E e[4][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = (float)e[i];
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * nthreads < total ? i0 + u * nthreads : total - 1;
+                const int t = i / per, c = (i - t * per) * 8;
+                const E* x = static_cast<const E*>(a.X) + t * a.ldx;
+                if (D) {
+                    const int64_t j = sv0 * d + c;
+                    __builtin_memcpy(e[u], x + (j + 8 <= a.N ? j : a.N - 8), sizeof(e[u]));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t k = source(c + i);
-                        v[i] = k >= 0 ? (float)x[k] : 0.0f;
+                    for (int k = 0; k < 8; ++k) {
+                        const int64_t j = source(c + k);
+                        e[u][k] = x[j >= 0 ? j : 0];
                     }
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * nthreads;
+                if (i >= total) break;
+                const int t = i / per, c = (i - t * per) * 8;
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = source(c + k) >= 0 ? (float)e[u][k] : 0.0f;
                 V8 w[XTERMS];
                 split<XTERMS>(v, w);
 #pragma unroll
@@ -495,15 +508,18 @@ struct QPlan {
     int64_t groups;
 };
 
-// Sixteen waves a workgroup (one a CU, up to 144 KB of LDS) where the matrices
-// have a block for each, else eight (two a CU).  Each row's sub-vectors are split
-// over up to 16 workgroups where the row groups leave CUs idle.
+// Sixteen waves a workgroup (one a CU, up to 144 KB of LDS) where the matrices have
+// four blocks for each, or a block for each and the row groups give less than two
+// workgroups a CU; else eight (two a CU: one gathers while the other stages or
+// sums).  8192 x 2048 pair, one token: 43 us with sixteen, 36 us with eight;
+// 11008 x 4096 pair, eight tokens: 121 us and 137 us.  Each row's sub-vectors are
+// split over up to 16 workgroups where the row groups leave CUs idle.
 QPlan q_plan(int64_t M, int64_t nb, int nm)
 {
     QPlan p;
     p.groups = (M + kQRows - 1) / kQRows;
     const int64_t blocks = (nb + kBlock - 1) / kBlock * nm;
-    p.waves = blocks >= 16 ? 16 : 8;
+    p.waves = blocks >= 64 || (blocks >= 16 && p.groups < 512) ? 16 : 8;
     p.splits = 1;
     while (p.splits < 16 && p.groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
     return p;
