@@ -71,50 +71,56 @@ struct Slice {
     }
 };
 
-// Issues this wave's loads (every kWaves-th of the slice) of the step that
-// starts at k0 of its segment.  Everything past the matrix, a k0 past K
-// included, arrives as zeros.  Offsets and sizes fit 32 bits: a slice spans at
-// most 256 rows of 2^21 elements.
+// A wave's loads (every kWaves-th of the slice) of the step that starts at k0 of
+// its segment.  Everything past the matrix, a k0 past K included, arrives as
+// zeros.  Offsets and sizes fit 32 bits: a slice spans at most 256 rows of 2^21
+// elements.
 template <int R, bool TR, bool PAIR>
-__device__ __forceinline__ void load_slice(const char* b0, const char* b1, int ld, int row0, int nrows, int width, int k0, int K,
-                                  lds_ptr lds, int wave, int lane)
-{
+struct Loader {
     typedef Slice<R, TR> S;
-    typedef __attribute__((address_space(3))) void* dst;
-    if (!TR) {
-        const int rl = lane >> 3;
-        const int chunk = (lane & 7) ^ rl;
-        uint32_t v = (uint32_t)(rl * ld * 2 + chunk * 16);
-        if (k0 + chunk * 8 >= K) v = kOob;
-        const int64_t off = (int64_t)row0 * ld * 2;
-        const int rows = PAIR ? R / 2 : R;
-        const int bytes = (((nrows - row0 < rows ? nrows - row0 : rows) - 1) * ld + K) * 2;
-        const __amdgpu_buffer_rsrc_t r0 = resource(b0 + off, bytes);
-        const __amdgpu_buffer_rsrc_t r1 = PAIR ? resource(b1 + off, bytes) : r0;
-#pragma unroll
-        for (int j = 0; j < S::kLoads / kWaves; ++j) {
-            const int inst = j * kWaves + wave;
-            const bool second = PAIR && j >= S::kLoads / kWaves / 2;
-            const uint32_t so = (uint32_t)((second ? inst * 8 - R / 2 : inst * 8) * ld * 2 + k0 * 2);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? r1 : r0, (dst)(lds + inst * 1024), 16, v, so, 0, 0);
-        }
-    } else {
-        // a wave's loads are a multiple of 16 k rows apart, which the swizzle does not see
-        static_assert(kWaves * S::kRowsPerLoad % 16 == 0, "the loads of a wave share their swizzle");
-        const int rl = lane / S::kChunks;
-        const int chunk = (lane % S::kChunks) ^ S::swizzle(wave * S::kRowsPerLoad + rl);
-        const uint32_t v = (uint32_t)(rl * ld * 2 + chunk * 16);
-        const int rows = K - k0 < kBK ? K - k0 : kBK;
-        const int bytes = rows <= 0 ? 0 : ((rows - 1) * ld + (width - row0)) * 2;
-        const __amdgpu_buffer_rsrc_t r0 = resource(b0 + ((int64_t)k0 * ld + row0) * 2, bytes);
-#pragma unroll
-        for (int j = 0; j < S::kLoads / kWaves; ++j) {
-            const int inst = j * kWaves + wave;
-            const uint32_t so = (uint32_t)(inst * S::kRowsPerLoad * ld * 2);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, (dst)(lds + inst * 1024), 16, v, so, 0, 0);
+    static constexpr int kCount = S::kLoads / kWaves;
+    const char* b0;            // the matrix from the slice on (of a pair, both)
+    const char* b1;
+    int bytes;                 // to the slice's end
+    uint32_t v;                // lane's offset
+    int so, stride;            // the wave's first load, and from one to the next
+
+    __device__ __forceinline__ Loader(const char* m0, const char* m1, int ld, int row0, int nrows, int width, int k0, int K,
+                                      int wave, unsigned lane)
+    {
+        if (!TR) {
+            const unsigned rl = lane >> 3, chunk = (lane & 7) ^ rl;
+            v = rl * ld * 2 + chunk * 16;
+            if (k0 + (int)chunk * 8 >= K) v = kOob;
+            const int64_t off = (int64_t)row0 * ld * 2;
+            const int rows = PAIR ? R / 2 : R;
+            bytes = (((nrows - row0 < rows ? nrows - row0 : rows) - 1) * ld + K) * 2;
+            b0 = m0 + off;
+            b1 = PAIR ? m1 + off : b0;
+            so = wave * 16 * ld + k0 * 2;
+            stride = kWaves * 16 * ld;
+        } else {
+            // a wave's loads are a multiple of 16 k rows apart, which the swizzle does not see
+            static_assert(kWaves * S::kRowsPerLoad % 16 == 0, "the loads of a wave share their swizzle");
+            const unsigned rl = lane / S::kChunks;
+            const unsigned chunk = (lane % S::kChunks) ^ S::swizzle(wave * S::kRowsPerLoad + rl);
+            v = rl * ld * 2 + chunk * 16;
+            const int rows = K - k0 < kBK ? K - k0 : kBK;
+            bytes = rows <= 0 ? 0 : ((rows - 1) * ld + (width - row0)) * 2;
+            b0 = b1 = m0 + ((int64_t)k0 * ld + row0) * 2;
+            so = wave * S::kRowsPerLoad * 2 * ld;
+            stride = kWaves * S::kRowsPerLoad * 2 * ld;
         }
     }
-}
+    // Load j into its place in the slice; the second half of a pair's rows come from the second matrix.
+    __device__ __forceinline__ void issue(lds_ptr slice, int wave, int j) const
+    {
+        typedef __attribute__((address_space(3))) void* dst;
+        const bool second = PAIR && j >= kCount / 2;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(second ? b1 : b0, bytes), (dst)(slice + (j * kWaves + wave) * 1024), 16, v,
+                                                 so + (second ? j - kCount / 2 : j) * stride, 0, 0);
+    }
+};
 
 // Fragment i (of the wave's rows from r0) of half kk: lane l holds row r0 + 16 i + l%16,
 // k = kk*32 + 8*(l/16) .. +7.  lane_base is the lane's byte offset for i = kk = 0; the
@@ -187,62 +193,66 @@ struct Main {
         const char* const P1 = a.P[1];
         const char* const Q0 = batch ? a.Q[1] : a.Q[0];
         const char* const Q1 = a.Q[1];
-        const auto issue = [&](int s, lds_ptr pb, lds_ptr qb) __attribute__((always_inline)) {
-            // a step past the last stays in the last segment, past its K
-            int l = lane;
-            if (TRP || TRQ) asm volatile("" : "+v"(l));          // formed anew: registers
-            const bool second = s >= a.seg_steps && a.steps > a.seg_steps;
-            const int k0 = (second ? s - a.seg_steps : s) * kBK;
-            load_slice<BP, TRP, PAIR>(!PAIR && second ? P1 : P0, P1, a.ldp, p0, a.np, a.wp, k0, a.kP, pb, wave, l);
-            load_slice<BQ, TRQ, false>(second ? Q1 : Q0, nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, qb, wave, l);
-        };
+        typedef Loader<BP, TRP, PAIR> LoadP;
+        typedef Loader<BQ, TRQ, false> LoadQ;
+        static_assert(LoadP::kCount + LoadQ::kCount == FP && kLoads == FP, "one load beside each row of products");
         uint32_t pbase = lane_base<BP, TRP>(wp * (PAIR ? FP / 2 : FP) * 16, lane);
         uint32_t qbase = lane_base<BQ, TRQ>(wq * FQ * 16, lane);
-        const auto read = [&](Frags& f, lds_ptr pb, lds_ptr qb, int kk) __attribute__((always_inline)) {
-            // the offsets are formed anew each time: kept, they would take the registers of the sums
-            asm volatile("" : "+v"(pbase), "+v"(qbase));
-#pragma unroll
-            for (int j = 0; j < FQ; ++j) f.q[j] = fragment<T, BQ, TRQ>(qb, qbase, j, kk);
-#pragma unroll
-            for (int i = 0; i < FP; ++i) f.p[i] = fragment<T, BP, TRP>(pb, pbase, i + skip(i), kk);
+        // Piece i of a half's fragments: one of P and one of Q while there are any.
+        const auto read = [&](Frags& f, lds_ptr pb, lds_ptr qb, int kk, int i) __attribute__((always_inline)) {
+            if (i < FQ) f.q[i] = fragment<T, BQ, TRQ>(qb, qbase, i, kk);
+            f.p[i] = fragment<T, BP, TRP>(pb, pbase, i + skip(i), kk);
         };
-        const auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
+        const auto multiply = [&](const Frags& f, int i) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
-#pragma unroll
-                for (int j = 0; j < FQ; ++j) acc[i][j] = T::mfma(f.p[i], f.q[j], acc[i][j]);
+            for (int j = 0; j < FQ; ++j) acc[i][j] = T::mfma(f.p[i], f.q[j], acc[i][j]);
         };
+        // the lane's offsets are formed anew in each half: kept, they would take the registers of the sums
+        const auto renew = [&] __attribute__((always_inline)) { asm volatile("" : "+v"(pbase), "+v"(qbase)); };
         Frags f0, f1;
-        // Loads and reads spread over the products of a half.
-        constexpr int kReads = FP * (TRP ? 2 : 1) + FQ * (TRQ ? 2 : 1), kMfma = FP * FQ;
-        const auto spread = [](int loads) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < kMfma; ++i) {
-                const int r0 = kReads * i * 1 / (kMfma * 1), r1 = kReads * (i + 1) * 1 / (kMfma * 1);
-#pragma unroll
-                for (int r = r0; r < r1 && r < kReads; ++r) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                if (loads * (i + 1) / kMfma > loads * i / kMfma) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            }
-        };
         const auto step = [&](int s, lds_ptr pc, lds_ptr qc, lds_ptr pn, lds_ptr qn) __attribute__((always_inline)) {
-            read(f1, pc, qc, 1);
-            multiply(f0);
-            spread(0);
-            __builtin_amdgcn_sched_barrier(0);
+            renew();
+            unsigned l = lane;
+            if (TRP || TRQ) asm volatile("" : "+v"(l));
+            // a step past the last stays in the last segment, past its K
+            const bool second = s + 2 >= a.seg_steps && a.steps > a.seg_steps;
+            const int k0 = (second ? s + 2 - a.seg_steps : s + 2) * kBK;
+            const LoadP lp(!PAIR && second ? P1 : P0, P1, a.ldp, p0, a.np, a.wp, k0, a.kP, wave, l);
+            const LoadQ lq(second ? Q1 : Q0, nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, wave, l);
+#pragma unroll
+            for (int i = 0; i < FP; ++i) {
+                read(f1, pc, qc, 1, i);
+                multiply(f0, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
             __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
             asm volatile("s_barrier" ::: "memory");
-            read(f0, pn, qn, 0);
-            issue(s + 2, pc, qc);
-            multiply(f1);
-            spread(kLoads);
-            __builtin_amdgcn_sched_barrier(0);
+            renew();
+#pragma unroll
+            for (int i = 0; i < FP; ++i) {
+                read(f0, pn, qn, 0, i);
+                if (i < LoadP::kCount) lp.issue(pc, wave, i);
+                else lq.issue(qc, wave, i - LoadP::kCount);
+                multiply(f1, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        const auto issue = [&](int s, lds_ptr pb, lds_ptr qb) __attribute__((always_inline)) {
+            const bool second = s >= a.seg_steps && a.steps > a.seg_steps;
+            const int k0 = (second ? s - a.seg_steps : s) * kBK;
+            const LoadP lp(!PAIR && second ? P1 : P0, P1, a.ldp, p0, a.np, a.wp, k0, a.kP, wave, lane);
+            const LoadQ lq(second ? Q1 : Q0, nullptr, a.ldq, q0, a.nq, a.wq, k0, a.kQ, wave, lane);
+#pragma unroll
+            for (int j = 0; j < LoadP::kCount; ++j) lp.issue(pb, wave, j);
+#pragma unroll
+            for (int j = 0; j < LoadQ::kCount; ++j) lq.issue(qb, wave, j);
         };
         issue(s0, pb0, qb0);
         issue(s0 + 1, pb1, qb1);
         __builtin_amdgcn_s_waitcnt(wait_imm(kLoads, 0));
         asm volatile("s_barrier" ::: "memory");
-        read(f0, pb0, qb0, 0);
+#pragma unroll
+        for (int i = 0; i < FP; ++i) read(f0, pb0, qb0, 0, i);
         // loads past s1 go out too (zeros past the matrix): the body stays one block
 #pragma unroll 1
         for (int s = s0; s < s1; s += 2) {
