@@ -48,17 +48,25 @@ constexpr float kGeluA = 0.044715f;
 // cancellation of 1 + erf in the lower tail.
 __device__ inline float normal_cdf(float z) { return 0.5f * erfcf(-kSqrtHalf * z); }
 
-// z * logistic, with the limit 0 where z is so negative that the logistic is 0.
-__device__ inline float act_fast(int act, float z)
+// act of eight values; the choice is made once for all.  z * logistic tends to 0
+// where the logistic is 0; NaN stays NaN.
+__device__ inline void activate(int act, float (&z)[8])
 {
-    switch (act) {
-    case VQ_ACT_RELU: return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z);   // NaN stays NaN
-    case VQ_ACT_SILU: return z * logistic_fast(z);
-    case VQ_ACT_GELU: return z * normal_cdf(z);
-    case VQ_ACT_GELU_TANH: return z * logistic_fast(2.0f * kGeluC * (z + kGeluA * z * z * z));
-    case VQ_ACT_SIGMOID: return logistic_fast(z);
-    default: return z;
+#define VQ_EACH(EXPR)                                 \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i)     \
+    {                                                 \
+        const float v = z[i];                         \
+        z[i] = (EXPR);                                \
     }
+    switch (act) {
+    case VQ_ACT_RELU: VQ_EACH(v > 0.0f ? v : (v <= 0.0f ? 0.0f : v)) break;
+    case VQ_ACT_SILU: VQ_EACH(v * logistic_fast(v)) break;
+    case VQ_ACT_GELU: VQ_EACH(v * normal_cdf(v)) break;
+    case VQ_ACT_GELU_TANH: VQ_EACH(v * logistic_fast(2.0f * kGeluC * (v + kGeluA * v * v * v))) break;
+    case VQ_ACT_SIGMOID: VQ_EACH(logistic_fast(v)) break;
+    default: break;
+    }
+#undef VQ_EACH
 }
 
 // The same in full float32 accuracy (float32 results).
@@ -74,38 +82,33 @@ __device__ inline float act_full(int act, float z)
     }
 }
 
-// act(z) and act'(z).  ReLU's derivative at 0 is 0.
-__device__ inline void act_grad(int act, float z, float& a, float& da)
+// z -> act'(z) and, where wanted, a = act(z), of eight values.  ReLU's derivative at
+// 0 is 0.
+template <bool VALUE>
+__device__ inline void act_grad(int act, float (&z)[8], float (&a)[8])
 {
+#define VQ_EACH(BODY)                                 \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i)     \
+    {                                                 \
+        const float v = z[i];                         \
+        float val, der;                               \
+        BODY;                                         \
+        z[i] = der;                                   \
+        if (VALUE) a[i] = val;                        \
+    }
     switch (act) {
-    case VQ_ACT_RELU: a = z > 0.0f ? z : 0.0f; da = z > 0.0f ? 1.0f : 0.0f; break;
-    case VQ_ACT_SILU: {
-        const float s = logistic_fast(z);
-        a = z * s;
-        da = s * (1.0f + z * (1.0f - s));
+    case VQ_ACT_RELU: VQ_EACH(val = v > 0.0f ? v : 0.0f; der = v > 0.0f ? 1.0f : 0.0f) break;
+    case VQ_ACT_SILU: VQ_EACH(const float s = logistic_fast(v); val = v * s; der = s * (1.0f + v * (1.0f - s))) break;
+    case VQ_ACT_GELU: VQ_EACH(const float c = normal_cdf(v); val = v * c; der = c + v * kInvSqrt2Pi * __expf(-0.5f * v * v)) break;
+    case VQ_ACT_GELU_TANH:
+        // (1 - s) is 0 long before v^2 reaches the bound, which keeps 0 * inf away
+        VQ_EACH(const float q = v * v; const float s = logistic_fast(2.0f * kGeluC * v * (1.0f + kGeluA * q)); val = v * s;
+                der = s + val * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * fminf(q, 1e6f)))
         break;
+    case VQ_ACT_SIGMOID: VQ_EACH(const float s = logistic_fast(v); val = s; der = s * (1.0f - s)) break;
+    default: VQ_EACH(val = v; der = 1.0f)
     }
-    case VQ_ACT_GELU: {
-        const float c = normal_cdf(z);
-        a = z * c;
-        da = c + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
-        break;
-    }
-    case VQ_ACT_GELU_TANH: {
-        const float s = logistic_fast(2.0f * kGeluC * (z + kGeluA * z * z * z));
-        a = z * s;
-        // (1 - s) is 0 long before z^2 reaches the bound, which keeps 0 * inf away
-        da = s + z * s * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * fminf(z * z, 1e6f));
-        break;
-    }
-    case VQ_ACT_SIGMOID: {
-        const float s = logistic_fast(z);
-        a = s;
-        da = s * (1.0f - s);
-        break;
-    }
-    default: a = z; da = 1.0f;
-    }
+#undef VQ_EACH
 }
 
 // ---- epilogue -----------------------------------------------------------
@@ -168,10 +171,7 @@ __device__ inline void epilogue_one(const Epilogue& e, int64_t t, int m, int M, 
         for (int i = 0; i < 8; ++i) z[i] += b[i];
     }
     if (e.Z[0]) store8<T>(e.Z[0], e.ldz, t, m, M, z);
-    if (e.act != VQ_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = act_fast(e.act, z[i]);
-    }
+    activate(e.act, z);
     if (e.R) {
         float r[8];
         load8<T>(e.R, e.ldr, t, m, M, r);
@@ -199,8 +199,9 @@ __device__ inline void epilogue_pair(const Epilogue& e, int64_t t, int m, int M,
         store8<T>(e.Z[0], e.ldz, t, m, M, g);
         store8<T>(e.Z[1], e.ldz, t, m, M, u);
     }
+    activate(e.act, g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = act_fast(e.act, g[i]) * u[i];
+    for (int i = 0; i < 8; ++i) g[i] *= u[i];
     store8<T>(e.Y, e.ldy, t, m, M, g);
 }
 

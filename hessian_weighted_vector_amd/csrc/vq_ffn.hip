@@ -97,7 +97,7 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
     const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * R;
     float c0[8] = {}, c1[8] = {};
     if (m < M) {
-        constexpr int B = R < 4 ? R : GATED ? 2 : 4;         // rows whose loads are in flight together
+        constexpr int B = R < 2 ? R : 2;                     // rows whose loads are in flight together
 #pragma unroll 1
         for (int r = 0; r < R; r += B) {
             float dy[B][8], z[B][8], u[B][8];
@@ -112,21 +112,22 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
             for (int k = 0; k < B; ++k) {
                 const int64_t t = t0 + r + k;
                 if (t >= nt) break;
+                float a[8];
+                if (GATED || act != VQ_ACT_NONE) {
+                    act_grad<GATED>(act, z[k], a);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        z[k][i] *= GATED ? dy[k][i] * u[k][i] : dy[k][i];
+                        if (GATED) u[k][i] = dy[k][i] * a[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[k][i] = dy[k][i];
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float a, da;
-                    if (GATED) {
-                        act_grad(act, z[k][i], a, da);
-                        z[k][i] = dy[k][i] * u[k][i] * da;
-                        u[k][i] = dy[k][i] * a;
-                        c1[i] += u[k][i];
-                    } else if (act != VQ_ACT_NONE) {
-                        act_grad(act, z[k][i], a, da);
-                        z[k][i] = dy[k][i] * da;
-                    } else {
-                        z[k][i] = dy[k][i];
-                    }
                     c0[i] += z[k][i];
+                    if (GATED) c1[i] += u[k][i];
                 }
                 // columns past M (loaded as zero) give zeros: the padding
                 if (D0) store8<T>(D0, ldd, t, m, (int)ldd, z[k]);

@@ -508,18 +508,21 @@ struct QPlan {
     int64_t groups;
 };
 
-// Sixteen waves a workgroup (one a CU, up to 144 KB of LDS) where the matrices have
-// four blocks for each, or a block for each and the row groups give less than two
-// workgroups a CU; else eight (two a CU: one gathers while the other stages or
-// sums).  8192 x 2048 pair, one token: 43 us with sixteen, 36 us with eight;
-// 11008 x 4096 pair, eight tokens: 121 us and 137 us.  Each row's sub-vectors are
-// split over up to 16 workgroups where the row groups leave CUs idle.
-QPlan q_plan(int64_t M, int64_t nb, int nm)
+constexpr size_t kLdsTwo = 72 * 1024, kLdsOne = 144 * 1024;      // a workgroup's LDS with two or one on a CU
+
+// Eight waves a workgroup, two on a CU (one gathers while the other stages or
+// sums), where the row groups fill them and a row's tokens and scales fit their
+// LDS in one slab, or where there is no block for each of sixteen; else sixteen.
+// Pair of 8192 x 2048, one token: 36 us with eight, 43 us with sixteen; of 11008 x
+// 4096, one token 93 and 104 us, but eight tokens (two slabs) 137 and 125 us.
+// Each row's sub-vectors are split over up to 16 workgroups where the row groups
+// leave CUs idle.  slab: LDS bytes of a whole row's staging.
+QPlan q_plan(int64_t M, int64_t nb, int nm, size_t slab)
 {
     QPlan p;
     p.groups = (M + kQRows - 1) / kQRows;
     const int64_t blocks = (nb + kBlock - 1) / kBlock * nm;
-    p.waves = blocks >= 64 || (blocks >= 16 && p.groups < 512) ? 16 : 8;
+    p.waves = blocks < 16 || (p.groups >= 512 && slab <= kLdsTwo) ? 8 : 16;
     p.splits = 1;
     while (p.splits < 16 && p.groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
     return p;
@@ -527,13 +530,13 @@ QPlan q_plan(int64_t M, int64_t nb, int nm)
 
 size_t q_workspace(int64_t M, int64_t nb, int64_t T, int nm)
 {
-    const QPlan p = q_plan(M, nb, nm);
+    const QPlan p = q_plan(M, nb, nm, 0);          // a split needs few row groups, where the slab does not count
     const int64_t t = T < kQTokens ? T : kQTokens;
     return p.splits > 1 ? align_up((size_t)p.splits * nm * t * M * sizeof(float)) : 0;
 }
 
 template <int D, int XT, int NT>
-vq_status q_launch(QArgs a, const QPlan& p, hipStream_t st)
+vq_status q_launch(QArgs a, hipStream_t st)
 {
     constexpr int S = slots_of(D);
     size_t c2 = 0;
@@ -542,13 +545,15 @@ vq_status q_launch(QArgs a, const QPlan& p, hipStream_t st)
         if (a.q[m].C2 && a.q[m].K2 * S <= kC2Floats) c2 += (size_t)a.q[m].K2 * S * sizeof(float);
         scales += a.q[m].cs != nullptr;
     }
-    const size_t cap = p.waves == 16 ? 144 * 1024 : 72 * 1024;
     const size_t per_token = XType<XT>::kTerms * 2 * (size_t)a.T;
     const auto slab_bytes = [&](int64_t sv) {
-        return (size_t)scales * sv * S * sizeof(float) + per_token * token_pitch((int)sv * S);
+        return (size_t)scales * sv * S * sizeof(float) + per_token * token_pitch((int)(sv * S));
     };
+    const int64_t nkb = (a.nb + kBlock - 1) / kBlock;
+    const QPlan p = q_plan(a.M, a.nb, a.nm, c2 + slab_bytes(nkb * kBlock));
     // balanced slabs of whole blocks
-    const int64_t nkb = (a.nb + kBlock - 1) / kBlock, mine = (nkb + p.splits - 1) / p.splits;
+    const size_t cap = p.waves == 16 ? kLdsOne : kLdsTwo;
+    const int64_t mine = (nkb + p.splits - 1) / p.splits;
     int64_t slabs = 1;
     while (slabs < mine && c2 + slab_bytes((mine + slabs - 1) / slabs * kBlock) > cap) ++slabs;
     a.slab = (int)((mine + slabs - 1) / slabs * kBlock);
@@ -571,27 +576,26 @@ vq_status q_launch(QArgs a, const QPlan& p, hipStream_t st)
 }
 
 template <int D, int XT>
-vq_status q_tokens(const QArgs& a, const QPlan& p, hipStream_t st)
+vq_status q_tokens(const QArgs& a, hipStream_t st)
 {
-    return a.T > 16 ? q_launch<D, XT, 2>(a, p, st) : q_launch<D, XT, 1>(a, p, st);
+    return a.T > 16 ? q_launch<D, XT, 2>(a, st) : q_launch<D, XT, 1>(a, st);
 }
 
 template <int D>
-vq_status q_type(const QArgs& a, const QPlan& p, hipStream_t st)
+vq_status q_type(const QArgs& a, hipStream_t st)
 {
     switch (a.dtype) {
-    case VQ_BF16: return q_tokens<D, VQ_BF16>(a, p, st);
-    case VQ_F16: return q_tokens<D, VQ_F16>(a, p, st);
-    default: return q_tokens<D, VQ_F32>(a, p, st);
+    case VQ_BF16: return q_tokens<D, VQ_BF16>(a, st);
+    case VQ_F16: return q_tokens<D, VQ_F16>(a, st);
+    default: return q_tokens<D, VQ_F32>(a, st);
     }
 }
 
 vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
 {
-    const QPlan p = q_plan(a.M, a.nb, nm);
     a.nm = nm;
-    a.splits = p.splits;
-    a.part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
+    a.splits = q_plan(a.M, a.nb, nm, 0).splits;
+    a.part = a.splits > 1 ? static_cast<float*>(ws) : nullptr;
     bool vec = a.d == 8 || (a.d == 4 && a.nb % 2 == 0);          // chunks of eight columns
     for (int m = 0; m < nm; ++m) vec = vec && aligned16(a.q[m].C1) && (!a.q[m].C2 || aligned16(a.q[m].C2));
     const size_t e = a.dtype == VQ_F32 ? 4 : 2;
@@ -603,7 +607,7 @@ vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
         a.X = X + t0 * a.ldx * e;
         a.R = R ? R + t0 * a.ldr * e : nullptr;
         a.Y = Y + t0 * a.ldy * e;
-        VQ_TRY(vec && a.d == 8 ? q_type<8>(a, p, st) : vec ? q_type<4>(a, p, st) : q_type<0>(a, p, st));
+        VQ_TRY(vec && a.d == 8 ? q_type<8>(a, st) : vec ? q_type<4>(a, st) : q_type<0>(a, st));
         if (a.part) {
             hipLaunchKernelGGL(k_qffn_finish, dim3(grid_for((int64_t)a.T * a.M, 256)), dim3(256), 0, st, a);
             VQ_LAUNCHED("k_qffn_finish");
