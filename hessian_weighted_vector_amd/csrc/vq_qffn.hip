@@ -112,9 +112,11 @@ __device__ inline void store_any(void* p, int64_t i, int dtype, float v)
     else static_cast<_Float16*>(p)[i] = (_Float16)v;
 }
 
-// Eight indices from sub-vector s of a row of nb, two to a register; past the row's end 0.
-__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, uint32_t (&k)[4])
+// Eight indices from sub-vector s of a row of nb, two to a register, at most top (two
+// copies of K - 1); past the row's end 0.
+__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, uint32_t top, uint32_t (&k)[4])
 {
+    typedef uint16_t U2 __attribute__((ext_vector_type(2)));
     if (s + 8 <= nb) {
         __builtin_memcpy(k, row + s, 16);
     } else {
@@ -125,20 +127,19 @@ __device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) k[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        k[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(U2, k[i]), __builtin_bit_cast(U2, top)));
 }
 
-// Index j of them, at most K - 1.
-__device__ inline int index_of(const uint32_t (&k)[4], int j, int K)
-{
-    const int v = (int)((k[j >> 1] >> (16 * (j & 1))) & 0xffffu);
-    return v < K ? v : K - 1;
-}
+// Index j of them.
+__device__ inline uint32_t index_of(const uint32_t (&k)[4], int j) { return j & 1 ? k[j >> 1] >> 16 : k[j >> 1] & 0xffffu; }
 
 // Row k of a codebook of any d <= 8, zero padded to eight: two (overlapping)
 // four-element loads inside the row for d >= 4.
-__device__ inline void load_row(const float* C, int k, int d, float (&w)[8])
+__device__ inline void load_row(const float* C, uint32_t k, int d, float (&w)[8])
 {
-    const float* row = C + (int64_t)k * d;
+    const float* row = C + k * (uint32_t)d;
     if (d >= 4) {
         float a[4], b[4];
         __builtin_memcpy(a, row, 16);
@@ -177,7 +178,9 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
     constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
     constexpr int S = slots_of(D);
-    constexpr int H = D ? 4 : 2;                       // chunks whose gathers are in flight together
+    // Chunks whose gathers are in flight together: as many as their rows and the terms
+    // leave registers for.  4096 x 11008, one float32 token: 44.9 us with two, 48.6 with four.
+    constexpr int H = D && XT == VQ_BF16 && NT == 1 ? 4 : 2;
     extern __shared__ __align__(16) float lds[];
     const int d = D ? D : a.d;
     const int nm = a.nm;
@@ -192,21 +195,18 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     // LDS: residual codebooks (rows of S floats), column scales [scaled][slab * S],
     // token terms [XTERMS][T][pitch]; the sums' exchange takes the last two's place
     const int columns = a.slab * S, pitch = token_pitch(columns);
-    int used = 0, c2_at = -1, cs_at = -1, cs_rows = 0;
-    for (int m = 0; m < nm; ++m) {
+    int used = 0, cs_rows = 0;
+    int c2_of[2] = {-1, -1}, cs_of[2] = {-1, -1};
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if (m >= nm) break;
         if (a.q[m].C2 && a.q[m].K2 * S <= kC2Floats) {
-            if (m == mm) c2_at = used;
-            for (int i = threadIdx.x; i < a.q[m].K2 * S; i += nthreads) {
-                const int k = i / S, e = i % S;
-                lds[used + i] = D || e < d ? a.q[m].C2[k * d + e] : 0.0f;
-            }
+            c2_of[m] = used;
             used += a.q[m].K2 * S;
         }
-        if (a.q[m].cs) {
-            if (m == mm) cs_at = cs_rows * columns;
-            ++cs_rows;
-        }
+        if (a.q[m].cs) cs_of[m] = cs_rows++ * columns;
     }
+    const int c2_at = c2_of[mm], cs_at = cs_of[mm];
     float* const cs = lds + used;
     __bf16* const xs = reinterpret_cast<__bf16*>(cs + cs_rows * columns);
     const QMat q = a.q[mm];
@@ -223,64 +223,114 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     const int nkb = (int)((a.nb + kBlock - 1) / kBlock);
     const int kb0 = (int)((int64_t)nkb * blockIdx.y / a.splits), kb1 = (int)((int64_t)nkb * (blockIdx.y + 1) / a.splits);
     const int slab_blocks = a.slab / kBlock;
+    const uint32_t top1 = (uint32_t)(q.K1 - 1) * 0x10001u, top2 = q.C2 ? (uint32_t)(q.K2 - 1) * 0x10001u : 0;
     uint32_t i1[4], i2[4] = {};
     const auto load_block = [&](int kb) {
         const int64_t s = (int64_t)kb * kBlock + g * 8;
-        load_indices(q.idx1 + row * a.nb, s, a.nb, i1);
-        if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, i2);
+        load_indices(q.idx1 + row * a.nb, s, a.nb, top1, i1);
+        if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, top2, i2);
     };
+
+    const int item = threadIdx.x;
+    int e0[kJobs], e1[kJobs];
+#pragma unroll
+    for (int job = 0; job < kJobs; ++job) {
+        const int id = job * nwaves + wave, m = id / kQRows;
+        const int64_t i = row0 + id % kQRows;
+        const int32_t* rp = id < nm * kQRows && i < a.M ? a.q[m & 1].row_ptr : nullptr;
+        e0[job] = rp ? rp[i] : 0;
+        e1[job] = rp ? rp[i + 1] : 0;
+    }
+    f32x4 c2_v[2];                                             // D: at most one quad a thread
+    if (D) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (c2_of[m] >= 0 && item < a.q[m].K2 * S / 4) c2_v[m] = reinterpret_cast<const f32x4*>(a.q[m].C2)[item];
+    }
 
     for (int sb = kb0; sb < kb1; sb += slab_blocks) {
         const int se = sb + slab_blocks < kb1 ? sb + slab_blocks : kb1;
         const int64_t sv0 = (int64_t)sb * kBlock;
         const int cols = (se - sb) * kBlock * S;               // of this slab
         if (sb + turn < se) load_block(sb + turn);
-        __syncthreads();
-        // column c of the slab: element c % S of sub-vector sv0 + c / S; zero past the row and past d
-        const auto source = [&](int c) -> int64_t {
-            const int64_t sv = sv0 + c / S;
-            const int e = c % S;
-            return sv < a.nb && (D || e < d) ? sv * d + e : -1;
-        };
-        int at = 0;
-        for (int m = 0; m < nm; ++m)
-            if (a.q[m].cs) {
-#pragma unroll 4
-                for (int c = threadIdx.x; c < cols; c += nthreads) {
-                    const int64_t j = source(c);
-                    const float v = a.q[m].cs[j >= 0 ? j : 0];
-                    cs[at + c] = j >= 0 ? v : 0.0f;
+        if (sb != kb0) __syncthreads();
+        if (D) {
+            // quads of column scales and chunks of eight columns of the tokens, two
+            // of each a thread in flight; columns past the row are zeros
+            const int quads = cs_rows ? cols / 4 : 0, per = cols / 8, total = per * a.T;
+            constexpr int kFlight = 2;
+            const int most = quads > total ? quads : total;
+            for (int i0 = item; i0 < most; i0 += nthreads * kFlight) {
+                E e[kFlight][8];
+                f32x4 c[2][kFlight];
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    const int i = i0 + u * nthreads;
+                    const int ix = i < total ? i : total - 1, t = ix / per;
+                    const int64_t j = sv0 * d + (ix - t * per) * 8;
+                    __builtin_memcpy(e[u], static_cast<const E*>(a.X) + t * a.ldx + (j < a.N ? j : a.N - 8), sizeof(e[u]));
+                    const int64_t jc = sv0 * d + (i < quads ? i : 0) * 4;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        if (cs_of[m] >= 0) __builtin_memcpy(&c[m][u], a.q[m].cs + (jc < a.N ? jc : a.N - 4), 16);
                 }
-                at += columns;
-            }
-        // chunks of eight columns of all tokens, four a thread in flight
-        const int per = cols / 8, total = per * a.T;
-        for (int i0 = threadIdx.x; i0 < total; i0 += nthreads * 4) {
-            E e[4][8];
+                if (sb == kb0 && i0 == item) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * nthreads < total ? i0 + u * nthreads : total - 1;
-                const int t = i / per, c = (i - t * per) * 8;
-                const E* x = static_cast<const E*>(a.X) + t * a.ldx;
-                if (D) {
-                    const int64_t j = sv0 * d + c;
-                    __builtin_memcpy(e[u], x + (j + 8 <= a.N ? j : a.N - 8), sizeof(e[u]));
-                } else {
+                    for (int m = 0; m < 2; ++m)
+                        if (c2_of[m] >= 0 && item < a.q[m].K2 * S / 4) reinterpret_cast<f32x4*>(lds + c2_of[m])[item] = c2_v[m];
+                }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int64_t j = source(c + k);
-                        e[u][k] = x[j >= 0 ? j : 0];
+                for (int u = 0; u < kFlight; ++u) {
+                    const int i = i0 + u * nthreads;
+                    if (i < total) {
+                        const int t = i / per, cx = (i - t * per) * 8;
+                        const bool in = sv0 * d + cx < a.N;
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = in ? (float)e[u][k] : 0.0f;
+                        V8 w[XTERMS];
+                        split<XTERMS>(v, w);
+#pragma unroll
+                        for (int k = 0; k < XTERMS; ++k) *reinterpret_cast<V8*>(xs + (k * a.T + t) * pitch + cx) = w[k];
+                    }
+                    if (i < quads) {
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+                            if (cs_of[m] >= 0) {
+                                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                                *reinterpret_cast<f32x4*>(cs + cs_of[m] + i * 4) = sv0 * d + i * 4 < a.N ? c[m][u] : zero;
+                            }
                     }
                 }
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * nthreads;
-                if (i >= total) break;
+        } else {
+            // column c of the slab: element c % 8 of sub-vector sv0 + c / 8; zero past the row and past d
+            const auto source = [&](int c) -> int64_t {
+                const int64_t sv = sv0 + c / S;
+                const int e = c % S;
+                return sv < a.nb && e < d ? sv * d + e : -1;
+            };
+            for (int m = 0; m < nm; ++m) {
+                if (c2_of[m] >= 0 && sb == kb0)
+                    for (int i = item; i < a.q[m].K2 * S; i += nthreads)
+                        lds[c2_of[m] + i] = i % S < d ? a.q[m].C2[i / S * d + i % S] : 0.0f;
+                if (cs_of[m] >= 0)
+                    for (int c = item; c < cols; c += nthreads) {
+                        const int64_t j = source(c);
+                        cs[cs_of[m] + c] = j >= 0 ? a.q[m].cs[j] : 0.0f;
+                    }
+            }
+            const int per = cols / 8, total = per * a.T;
+            for (int i = item; i < total; i += nthreads) {
                 const int t = i / per, c = (i - t * per) * 8;
+                const E* x = static_cast<const E*>(a.X) + t * a.ldx;
                 float v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = source(c + k) >= 0 ? (float)e[u][k] : 0.0f;
+                for (int k = 0; k < 8; ++k) {
+                    const int64_t j = source(c + k);
+                    const float f = (float)x[j >= 0 ? j : 0];
+                    v[k] = j >= 0 ? f : 0.0f;
+                }
                 V8 w[XTERMS];
                 split<XTERMS>(v, w);
 #pragma unroll
@@ -308,7 +358,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                     f32x4 ga[H], gb[H];
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
-                        const int mine = index_of(k1, h * H + j, q.K1), other = swap_pair(mine);
+                        const int mine = index_of(k1, h * H + j), other = swap_pair(mine);
                         ga[j] = C[2 * (odd ? other : mine) + odd];
                         gb[j] = C[2 * (odd ? mine : other) + odd];
                     }
@@ -326,27 +376,27 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                     for (int j = 0; j < H; ++j)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const f32x4 v = C[index_of(k1, j * 2 + u, q.K1)];
+                            const f32x4 v = C[index_of(k1, (h * H + j) * 2 + u)];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) w[j][u * 4 + i] = v[i];
                         }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < H; ++j) load_row(q.C1, index_of(k1, h * H + j, q.K1), d, w[j]);
+                    for (int j = 0; j < H; ++j) load_row(q.C1, index_of(k1, h * H + j), d, w[j]);
                 }
                 if (q.C2) {
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         if (D == 0 && c2_at < 0) {
                             float v[8];
-                            load_row(q.C2, index_of(k2, h * H + j, q.K2), d, v);
+                            load_row(q.C2, index_of(k2, h * H + j), d, v);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) w[j][i] += v[i];
                         } else {
                             const float* c2 = c2_at >= 0 ? lds + c2_at : q.C2;
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {        // halves of one row, or two rows
-                                const int k = index_of(k2, (h * H + j) * U + (D == 4 ? u : 0), q.K2);
+                                const int k = index_of(k2, (h * H + j) * U + (D == 4 ? u : 0));
                                 const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + k * S + (D == 4 ? 0 : u * 4));
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) w[j][u * 4 + i] += v[i];
@@ -391,22 +441,47 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
         const int64_t col0 = sv0 * d, col1 = (int64_t)se * kBlock < a.nb ? (int64_t)se * kBlock * d : a.N;
 #pragma unroll
         for (int job = 0; job < kJobs; ++job) {
-            const int id = job * nwaves + wave, m = id / kQRows, rr = id % kQRows;
-            const int t = lane & (tl - 1);
-            if (id >= nm * kQRows || row0 + rr >= a.M || t >= a.T) continue;
-            const QMat& q = a.q[m];
-            if (!q.row_ptr) continue;
-            const int e1 = q.row_ptr[row0 + rr + 1];
-            for (int e = q.row_ptr[row0 + rr] + lane / tl; e < e1; e += 64 / tl) {
-                const int64_t j = q.col[e];
-                if (j < col0 || j >= col1) continue;
-                const int c = D ? (int)(j - col0) : (int)((j - col0) / d) * S + (int)((j - col0) % d);
-                float x = 0.0f;
+            if (e0[job] >= e1[job]) continue;
+            const QMat& q = a.q[(job * nwaves + wave) / kQRows];
+            const int t = lane & (tl - 1), step = 64 / tl;
+            const int tx = t < a.T ? t : a.T - 1;
+            for (int e = e0[job] + lane / tl; e < e1[job]; e += step * 4) {
+                int j[4];
+                float v[4];
 #pragma unroll
-                for (int k = 0; k < XTERMS; ++k) x += (float)xs[(k * a.T + t) * pitch + c];
-                corr[job] = fmaf(q.delta[e], x, corr[job]);
+                for (int u = 0; u < 4; ++u) {              // four entries in flight
+                    const int k = e + u * step < e1[job] ? e + u * step : e1[job] - 1;
+                    j[u] = q.col[k];
+                    v[u] = q.delta[k];
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (e + u * step >= e1[job] || j[u] < col0 || j[u] >= col1) continue;
+                    const int cl = (int)(j[u] - col0);
+                    const int c = D ? cl : cl / d * S + cl % d;
+                    float x = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < XTERMS; ++k) x += (float)xs[(k * a.T + tx) * pitch + c];
+                    corr[job] = fmaf(v[u], x, corr[job]);
+                }
             }
         }
+    }
+
+    // Item threadIdx.x of the sums is fragment n, lane l, element e -> token, row; what
+    // its end needs is loaded ahead of the exchange.
+    const int item_t = (item >> 8) * 16 + ((item >> 2) & 15), item_r = ((item >> 6) & 3) * 4 + (item & 3);
+    const int64_t out_row = row0 + item_r;
+    const bool stores = item < NT * 256 && item_t < a.T && out_row < a.M;
+    float rs_v[2] = {1.0f, 1.0f}, bias_v[2] = {0.0f, 0.0f}, res_v = 0.0f;
+    if (stores) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (m >= nm) break;
+            if (a.q[m].rs) rs_v[m] = a.q[m].rs[out_row];
+            if (a.bias[m]) bias_v[m] = load_any(a.bias[m], out_row, XT);
+        }
+        if (a.R) res_v = load_any(a.R, item_t * a.ldr + out_row, XT);
     }
 
     // sums over the waves, in wave order, and the corrections
@@ -423,29 +498,30 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
         if (id < nm * kQRows && lane < tl && lane < NT * 16) cor[(m * NT * 16 + lane) * kQRows + rr] = c;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < NT * 256; i += nthreads) {
-        // item i of the accumulators: fragment n, lane l, element e -> token, row
-        const int n = i >> 8, l = (i >> 2) & 63, e = i & 3;
-        const int t = n * 16 + (l & 15), rr = (l >> 4) * 4 + e;
-        const int64_t out_row = row0 + rr;
-        if (t >= a.T || out_row >= a.M) continue;
-        float z[2] = {0.0f, 0.0f};
+    if (!stores) return;
+    float z[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            if (m >= nm) break;
-            float v = 0.0f;
-            for (int w = m; w < nwaves; w += nm) v += red[(w * NT + n) * 256 + (i & 255)];
-            if (a.q[m].rs) v *= a.q[m].rs[out_row];
-            z[m] = v + cor[(m * NT * 16 + t) * kQRows + rr];
-            if (a.part) a.part[(((int64_t)blockIdx.y * nm + m) * a.T + t) * a.M + out_row] = z[m];
-            else if (a.bias[m]) z[m] += load_any(a.bias[m], out_row, XT);
+    for (int m = 0; m < 2; ++m) {
+        if (m >= nm) break;
+        const float* p = red + m * NT * 256 + (item >> 8) * 256 + (item & 255);
+        float v = 0.0f;
+        for (int w = 0; w < turns; w += 4) {                   // 4, 8 or 16 waves a matrix
+            float f[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) f[u] = p[(w + u) * nm * NT * 256];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v += f[u];
         }
-        if (a.part) continue;
-        float y = act_full(a.act, z[0]);
-        if (nm > 1) y *= z[1];
-        if (a.R) y += load_any(a.R, t * a.ldr + out_row, XT);
-        store_any(a.Y, t * a.ldy + out_row, XT, y);
+        if (a.q[m].rs) v *= rs_v[m];
+        z[m] = v + cor[(m * NT * 16 + item_t) * kQRows + item_r];
+        if (a.part) a.part[(((int64_t)blockIdx.y * nm + m) * a.T + item_t) * a.M + out_row] = z[m];
+        z[m] += bias_v[m];
     }
+    if (a.part) return;
+    float y = act_full(a.act, z[0]);
+    if (nm > 1) y *= z[1];
+    if (a.R) y += res_v;
+    store_any(a.Y, item_t * a.ldy + out_row, XT, y);
 }
 
 // Adds the parts in order and applies the epilogue.
