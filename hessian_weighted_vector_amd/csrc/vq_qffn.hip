@@ -259,7 +259,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
             // of each a thread in flight; columns past the row are zeros
             const int quads = cs_rows ? cols / 4 : 0, per = cols / 8, total = per * a.T;
             constexpr int kFlight = 2;
-            const int most = quads > total ? quads : total;
+            const int most = max(max(quads, total), nthreads);    // every thread passes once
             for (int i0 = item; i0 < most; i0 += nthreads * kFlight) {
                 E e[kFlight][8];
                 f32x4 c[2][kFlight];

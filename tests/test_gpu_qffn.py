@@ -188,6 +188,23 @@ def test_matrices_of_a_pair_may_differ():
               y.abs() * e1 + z1.abs() * ey + ey * e1 + 2.0 ** -23 * (y * z1).abs(), torch.float32)
 
 
+@pytest.mark.parametrize("d,K2,N", [(8, 256, 64), (8, 256, 2048), (4, 512, 8), (4, 512, 1024), (5, 250, 40)])
+@pytest.mark.parametrize("T", [1, 3])
+def test_residual_codebook_larger_than_the_row(d, K2, N, T):
+    """The residual codebook fills its whole place in LDS; the row has fewer quads to stage."""
+    say("residual codebook of", K2, "rows, d =", d, "N =", N, "T =", T)
+    g = np.random.default_rng([81, d, N, T])
+    p, q = (make_matrix(g, 400, N, d, 40, K2, False, 2) for _ in range(2))
+    P, Q = on_gpu(p), on_gpu(q)
+    for dtype in DT.values():
+        X = tokens(g, T, N, dtype)
+        (z0, e0), (z1, e1) = sums(p, X, dtype), sums(q, X, dtype)
+        check("qlinear", vq.qlinear(P, X), z0, e0, dtype)
+        y, ey = activated("silu", z0, e0)
+        check("qgated", vq.qgated(P, Q, X), y * z1,
+              y.abs() * e1 + z1.abs() * ey + ey * e1 + 2.0 ** -23 * (y * z1).abs(), dtype)
+
+
 def test_no_tokens_reproducible_and_refresh():
     say("T = 0, reproducible, refresh")
     g = np.random.default_rng([80])
