@@ -579,36 +579,41 @@ __global__ __launch_bounds__(256) void k_sparse_delta(int64_t M, int64_t N, int6
 }
 
 // ---- plan ---------------------------------------------------------------
-struct QPlan {
-    int waves, splits;
-    int64_t groups;
-};
-
 constexpr size_t kLdsTwo = 72 * 1024, kLdsOne = 144 * 1024;      // a workgroup's LDS with two or one on a CU
 
-// Eight waves a workgroup, two on a CU (one gathers while the other stages or
-// sums), where the row groups fill them and a row's tokens and scales fit their
-// LDS in one slab, or where there is no block for each of sixteen; else sixteen.
-// Pair of 8192 x 2048, one token: 36 us with eight, 43 us with sixteen; of 11008 x
-// 4096, one token 93 and 104 us, but eight tokens (two slabs) 137 and 125 us.
-// Each row's sub-vectors are split over up to 16 workgroups where the row groups
-// leave CUs idle.  slab: LDS bytes of a whole row's staging.
-QPlan q_plan(int64_t M, int64_t nb, int nm, size_t slab)
+int64_t q_groups(int64_t M) { return (M + kQRows - 1) / kQRows; }
+int64_t q_blocks(int64_t nb) { return (nb + kBlock - 1) / kBlock; }
+
+// Each row's blocks are split over up to 16 workgroups while the workgroups stay
+// one a CU and have four blocks or more.  179 x 15720, one token: 18 us over 8 or
+// 16, 41 us over one, 25 us over 32; 512 x 4096, pair: 19 us over 4, 29 us over
+// one; 256 x 1024: 11.5 us over one, 13.8 us over two.
+int q_splits(int64_t M, int64_t nb)
 {
-    QPlan p;
-    p.groups = (M + kQRows - 1) / kQRows;
-    const int64_t blocks = (nb + kBlock - 1) / kBlock * nm;
-    p.waves = blocks < 16 || (p.groups >= 512 && slab <= kLdsTwo) ? 8 : 16;
-    p.splits = 1;
-    while (p.splits < 16 && p.groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
-    return p;
+    int s = 1;
+    while (s < 16 && q_groups(M) * s * 2 <= 256 && q_blocks(nb) >= s * 8) s *= 2;
+    return s;
+}
+
+// Eight waves a workgroup where its tokens and scales fit in half a CU's LDS at
+// once, so that two share a CU and one gathers while the other stages or sums;
+// else sixteen.  Pair of 8192 x 2048, one token: 36 us with eight, 43 us with
+// sixteen; of 11008 x 4096, one token 93 and 104 us, but eight tokens (two slabs)
+// 137 and 125 us.  Many tokens' exact entries are shared among sixteen where the
+// rows leave one workgroup a CU: pair of 64 x 4096, 24 tokens, 37 and 23 us;
+// without exact entries 19.1 and 20.3 us (512 x 4096).  lds: bytes staged at once.
+int q_waves(const QArgs& a, size_t lds)
+{
+    if (q_blocks(a.nb) * a.nm < 16) return 8;
+    const bool sparse = a.q[0].row_ptr || (a.nm > 1 && a.q[1].row_ptr);
+    return lds > kLdsTwo || (sparse && a.T > 8 && q_groups(a.M) * a.splits < 512) ? 16 : 8;
 }
 
 size_t q_workspace(int64_t M, int64_t nb, int64_t T, int nm)
 {
-    const QPlan p = q_plan(M, nb, nm, 0);          // a split needs few row groups, where the slab does not count
+    const int splits = q_splits(M, nb);
     const int64_t t = T < kQTokens ? T : kQTokens;
-    return p.splits > 1 ? align_up((size_t)p.splits * nm * t * M * sizeof(float)) : 0;
+    return splits > 1 ? align_up((size_t)splits * nm * t * M * sizeof(float)) : 0;
 }
 
 template <int D, int XT, int NT>
@@ -625,15 +630,14 @@ vq_status q_launch(QArgs a, hipStream_t st)
     const auto slab_bytes = [&](int64_t sv) {
         return (size_t)scales * sv * S * sizeof(float) + per_token * token_pitch((int)(sv * S));
     };
-    const int64_t nkb = (a.nb + kBlock - 1) / kBlock;
-    const QPlan p = q_plan(a.M, a.nb, a.nm, c2 + slab_bytes(nkb * kBlock));
+    const int64_t mine = (q_blocks(a.nb) + a.splits - 1) / a.splits;
+    const int waves = q_waves(a, c2 + slab_bytes(mine * kBlock));
     // balanced slabs of whole blocks
-    const size_t cap = p.waves == 16 ? kLdsOne : kLdsTwo;
-    const int64_t mine = (nkb + p.splits - 1) / p.splits;
+    const size_t cap = waves == 16 ? kLdsOne : kLdsTwo;
     int64_t slabs = 1;
     while (slabs < mine && c2 + slab_bytes((mine + slabs - 1) / slabs * kBlock) > cap) ++slabs;
     a.slab = (int)((mine + slabs - 1) / slabs * kBlock);
-    const size_t sums = ((size_t)p.waves * NT * 256 + (size_t)a.nm * NT * 16 * kQRows) * sizeof(float);
+    const size_t sums = ((size_t)waves * NT * 256 + (size_t)a.nm * NT * 16 * kQRows) * sizeof(float);
     const size_t lds = c2 + std::max(slab_bytes(a.slab), sums);
     const auto kern = k_qffn<D, XT, NT>;
     if (lds > 64 * 1024) {
@@ -646,7 +650,7 @@ vq_status q_launch(QArgs a, hipStream_t st)
             set_dev = dev;
         }
     }
-    hipLaunchKernelGGL(kern, dim3((unsigned)p.groups, p.splits), dim3(p.waves * 64), lds, st, a);
+    hipLaunchKernelGGL(kern, dim3((unsigned)q_groups(a.M), a.splits), dim3(waves * 64), lds, st, a);
     VQ_LAUNCHED("k_qffn");
     return VQ_OK;
 }
@@ -670,7 +674,7 @@ vq_status q_type(const QArgs& a, hipStream_t st)
 vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
 {
     a.nm = nm;
-    a.splits = q_plan(a.M, a.nb, nm, 0).splits;
+    a.splits = q_splits(a.M, a.nb);
     a.part = a.splits > 1 ? static_cast<float*>(ws) : nullptr;
     bool vec = a.d == 8 || (a.d == 4 && a.nb % 2 == 0);          // chunks of eight columns
     for (int m = 0; m < nm; ++m) vec = vec && aligned16(a.q[m].C1) && (!a.q[m].C2 || aligned16(a.q[m].C2));
