@@ -235,6 +235,17 @@ struct GemmArgs {
 size_t gemm_workspace(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int nbatch);
 vq_status gemm_launch(const GemmArgs& a, void* ws, size_t ws_bytes, hipStream_t st);
 
+// A product's sizes: K is the smaller of its operands' valid k.
+struct GemmSize {
+    GemmKind kind;
+    int64_t np, nq, K;
+    int nseg, nbatch;
+};
+
+// A GEMM_DX and a GEMM_DW product, in one launch where that is faster.
+size_t gemm_two_workspace(const GemmSize& x, const GemmSize& w);
+vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, void* ws, size_t ws_bytes, hipStream_t st);
+
 // Adds float32 parts [splits][matrices][nq][pitch] in order and applies the epilogue.
 vq_status finish_parts(int dtype, bool pair, const float* part, int splits, int np, int nq, int pitch, const Epilogue& e,
                        hipStream_t st);

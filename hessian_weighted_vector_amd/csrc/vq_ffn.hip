@@ -316,10 +316,13 @@ vq_status backward(const Backward& b, Arena& ws, bool run, hipStream_t st)
             part[i] = static_cast<float*>(ws.take((size_t)((b.T + rows - 1) / rows) * b.M * sizeof(float)));
     Mat x{b.X, b.T, b.N, b.ldx};
     Mat w[2] = {{b.W[0], b.M, b.N, b.ldw}, {b.W[1], b.M, b.N, b.ldw}};
-    const size_t gx = b.dX ? gemm_workspace(GEMM_DX, b.N, b.T, b.M, b.nm, 1) : 0;
     const int nb = b.dW[0] && b.dW[1] ? 2 : 1;
-    const size_t gw = want_dw ? gemm_workspace(GEMM_DW, b.N, b.M, b.T, 1, nb) : 0;
-    void* part_ws = ws.take(std::max(gx, gw));       // the two products run one after the other
+    const GemmSize sx{GEMM_DX, b.N, b.T, b.M, b.nm, 1}, sw{GEMM_DW, b.N, b.M, b.T, 1, nb};
+    const size_t parts = b.dX && want_dw ? gemm_two_workspace(sx, sw)
+                         : b.dX          ? gemm_workspace(sx.kind, sx.np, sx.nq, sx.K, sx.nseg, sx.nbatch)
+                         : want_dw       ? gemm_workspace(sw.kind, sw.np, sw.nq, sw.K, sw.nseg, sw.nbatch)
+                                         : 0;
+    void* part_ws = ws.take(parts);
     Packer pk{ws};
     if (want_dw && !loads_ok(x)) pk.add(x);
     if (b.dX && (!loads_ok(w[0]) || (b.nm > 1 && !loads_ok(w[1]))))
@@ -329,35 +332,35 @@ vq_status backward(const Backward& b, Arena& ws, bool run, hipStream_t st)
 
     if (D[0] || want_db)
         VQ_TRY(b.dtype == VQ_BF16 ? grad_launch<Bf16>(b, D, ldd, part, st) : grad_launch<F16>(b, D, ldd, part, st));
-    GemmArgs g{};
-    g.dtype = b.dtype;
-    g.np = (int)b.N;
+    GemmArgs gx{}, gw{};
+    gx.dtype = gw.dtype = b.dtype;
+    gx.np = gw.np = (int)b.N;
     if (b.dX) {
-        g.kind = GEMM_DX;
-        g.nq = (int)b.T;
-        g.nseg = b.nm; g.nbatch = 1;
-        for (int i = 0; i < b.nm; ++i) { g.P[i] = w[i].p; g.Q[i] = d[i].p; }
-        g.ldp = w[0].ld; g.ldq = d[0].ld;
-        g.kP = b.M; g.kQ = d[0].cols;
-        g.wp = (int)w[0].cols;
-        g.epi.Y = b.dX; g.epi.ldy = b.lddx;
-        VQ_TRY(gemm_launch(g, part_ws, gx, st));
+        gx.kind = GEMM_DX;
+        gx.nq = (int)b.T;
+        gx.nseg = b.nm; gx.nbatch = 1;
+        for (int i = 0; i < b.nm; ++i) { gx.P[i] = w[i].p; gx.Q[i] = d[i].p; }
+        gx.ldp = w[0].ld; gx.ldq = d[0].ld;
+        gx.kP = b.M; gx.kQ = d[0].cols;
+        gx.wp = (int)w[0].cols;
+        gx.epi.Y = b.dX; gx.epi.ldy = b.lddx;
     }
     if (want_dw) {
         const int first = b.dW[0] ? 0 : 1;
-        g.kind = GEMM_DW;
-        g.nq = (int)b.M;
-        g.nseg = 1; g.nbatch = nb;
-        g.P[0] = g.P[1] = x.p;
-        g.Q[0] = d[first].p; g.Q[1] = d[1].p;
-        g.ldp = x.ld; g.ldq = d[0].ld;
-        g.kP = g.kQ = b.T;
-        g.wp = (int)x.cols; g.wq = (int)d[0].cols;
-        g.epi.Y = b.dW[first]; g.epi.ldy = b.lddw;
-        g.Y2 = b.dW[1];
-        VQ_TRY(gemm_launch(g, part_ws, gw, st));
+        gw.kind = GEMM_DW;
+        gw.nq = (int)b.M;
+        gw.nseg = 1; gw.nbatch = nb;
+        gw.P[0] = gw.P[1] = x.p;
+        gw.Q[0] = d[first].p; gw.Q[1] = d[1].p;
+        gw.ldp = x.ld; gw.ldq = d[0].ld;
+        gw.kP = gw.kQ = b.T;
+        gw.wp = (int)x.cols; gw.wq = (int)d[0].cols;
+        gw.epi.Y = b.dW[first]; gw.epi.ldy = b.lddw;
+        gw.Y2 = b.dW[1];
     }
-    return VQ_OK;
+    if (b.dX && want_dw) return gemm_two_launch(gx, gw, part_ws, parts, st);
+    if (b.dX) return gemm_launch(gx, part_ws, parts, st);
+    return want_dw ? gemm_launch(gw, part_ws, parts, st) : VQ_OK;
 }
 
 // ---- argument checks ------------------------------------------------------

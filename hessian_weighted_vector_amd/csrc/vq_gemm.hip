@@ -23,6 +23,8 @@
 // pointed past the resource's end.
 #include "vq_ffn.h"
 
+#include <algorithm>
+
 namespace vq {
 namespace {
 
@@ -262,21 +264,17 @@ struct Main {
     }
 };
 
+// One tile of one split of output `batch` of nbatch, from operands to stored outputs or parts.
 template <class T, bool TRP, bool TRQ, int FP, int FQ, bool PAIR>
-__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const Tile a)
+__device__ __forceinline__ void tile_product(const Tile& a, int id, int split, int batch, int nbatch, char* pb0, char* pb1,
+                                             char* qb0, char* qb1)
 {
     typedef Main<T, TRP, TRQ, FP, FQ, PAIR> L;
-    // four arrays, not one: the compiler then knows that a fragment is never read
-    // from a buffer that is being filled, and does not wait for those loads
-    __shared__ __align__(1024) char pb0[L::BP * kBK * 2], pb1[L::BP * kBK * 2], qb0[L::BQ * kBK * 2], qb1[L::BQ * kBK * 2];
-
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / kWQ, wq = wave % kWQ;
-    const int split = blockIdx.y;
-    const int batch = blockIdx.z;
     int tp, tq;
-    pick_tile(blockIdx.x, a.ntp * a.ntq, a.ntp, a.ntq, tp, tq);
+    pick_tile(id, a.ntp * a.ntq, a.ntp, a.ntq, tp, tq);
     const int p0 = tp * (PAIR ? L::BP / 2 : L::BP), q0 = tq * L::BQ;
     // splits in pairs of steps, as the loop takes them; past the last step come zeros
     const int pairs = (a.steps + 1) / 2;
@@ -294,7 +292,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     constexpr int NI = PAIR ? FP / 2 : FP;
     if (a.part) {
         const int64_t plane = (int64_t)a.nq * a.pitch;
-        float* o = a.part + ((int64_t)split * (PAIR ? 2 : gridDim.z) + batch) * plane;
+        float* o = a.part + ((int64_t)split * (PAIR ? 2 : nbatch) + batch) * plane;
 #pragma unroll
         for (int j = 0; j < FQ; ++j) {
             const int q = q0 + (wq * FQ + j) * 16 + q_l;
@@ -358,6 +356,44 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     }
 }
 
+// The tile's operands in LDS, double buffered.  Four arrays, not one: the compiler
+// then knows that a fragment is never read from a buffer that is being filled, and
+// does not wait for those loads.
+#define VQ_TILE_BUFFERS(L) \
+    __shared__ __align__(1024) char pb0[L::BP * kBK * 2], pb1[L::BP * kBK * 2], qb0[L::BQ * kBK * 2], qb1[L::BQ * kBK * 2]
+
+template <class T, bool TRP, bool TRQ, int FP, int FQ, bool PAIR>
+__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const Tile a)
+{
+    typedef Main<T, TRP, TRQ, FP, FQ, PAIR> L;
+    VQ_TILE_BUFFERS(L);
+    tile_product<T, TRP, TRQ, FP, FQ, PAIR>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, pb0, pb1, qb0, qb1);
+}
+
+// dX and dW of a backward pass in one launch: the tiles of one fill the CUs that the
+// other's last round would leave idle.
+struct Two {
+    Tile x, w;
+    int nx, nw;                // workgroups
+    int w_first, w_batch;      // whether dW's come first; its outputs
+};
+
+template <class T, int FP, int FQ>
+__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm_two(const Two a)
+{
+    typedef Main<T, true, true, FP, FQ, false> L;
+    VQ_TILE_BUFFERS(L);
+    const int id = blockIdx.x, first = a.w_first ? a.nw : a.nx;
+    const int at = id < first ? id : id - first;
+    if ((id < first) != (a.w_first != 0)) {
+        const int tiles = a.x.ntp * a.x.ntq;
+        tile_product<T, true, false, FP, FQ, false>(a.x, at % tiles, at / tiles, 0, 1, pb0, pb1, qb0, qb1);
+    } else {
+        const int tiles = a.w.ntp * a.w.ntq, batch = at / (tiles * a.w.splits), in = at - batch * tiles * a.w.splits;
+        tile_product<T, true, true, FP, FQ, false>(a.w, in % tiles, in / tiles, batch, a.w_batch, pb0, pb1, qb0, qb1);
+    }
+}
+
 // Adds the parts in order and applies the epilogue; eight features a thread.
 // Not a pair: blockIdx.y is the output (Y[0] or Y[1]).
 struct Finish {
@@ -417,6 +453,7 @@ vq_status launch_finish(const Finish& f, bool pair, int nbatch, hipStream_t st)
 struct Plan {
     int fp, fq, ntp, ntq, splits, steps, seg_steps, pitch;
     size_t part_bytes;
+    double cost;               // microseconds by the model (of two in one launch: of a tile)
 };
 
 // Tile and split by a model of the time in microseconds, fitted to 76 products
@@ -426,43 +463,120 @@ struct Plan {
 // 4 a round.  Split sums: 9.5 for the second launch and the parts' traffic.
 // (2048 x 4096 x 11008: 156 us as 256 x 256 over two splits, 170 us as 128 x 128;
 // 1024 x 2048 x 2048: 31 us and 19 us.)
+Plan make_shape(GemmKind kind, int small, int64_t np, int64_t nq, int64_t K, int nseg)
+{
+    Plan p{};
+    p.fp = small ? 4 : 8;
+    p.fq = small ? 2 : 4;
+    const int bp = kWP * p.fp * 16 / (kind == GEMM_GATED ? 2 : 1), bq = kWQ * p.fq * 16;
+    p.ntp = (int)((np + bp - 1) / bp);
+    p.ntq = (int)((nq + bq - 1) / bq);
+    p.seg_steps = (int)((K + kBK - 1) / kBK);
+    p.steps = p.seg_steps * nseg;
+    p.pitch = (int)((np + 7) / 8 * 8);
+    return p;
+}
+
+size_t part_bytes(const Plan& p, int64_t nq, int nout)
+{
+    return p.splits > 1 ? align_up((size_t)p.splits * nout * nq * p.pitch * sizeof(float)) : 0;
+}
+
 Plan make_plan(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int nbatch)
 {
-    const bool pair = kind == GEMM_GATED;
-    const int nout = pair ? 2 : nbatch;
+    const int nout = kind == GEMM_GATED ? 2 : nbatch;
     Plan best{};
-    double best_cost = 1e300;
+    best.cost = 1e300;
     for (int small = 0; small < 2; ++small) {
-        Plan p;
-        p.fp = small ? 4 : 8;
-        p.fq = small ? 2 : 4;
-        const int bp = kWP * p.fp * 16 / (pair ? 2 : 1), bq = kWQ * p.fq * 16;
-        p.ntp = (int)((np + bp - 1) / bp);
-        p.ntq = (int)((nq + bq - 1) / bq);
-        p.seg_steps = (int)((K + kBK - 1) / kBK);
-        p.steps = p.seg_steps * nseg;
-        p.pitch = (int)((np + 7) / 8 * 8);
+        Plan p = make_shape(kind, small, np, nq, K, nseg);
         const int pairs = (p.steps + 1) / 2;
         for (int sp = 1; sp <= 16 && sp <= pairs; ++sp) {
             const int64_t tiles = (int64_t)p.ntp * p.ntq * nbatch * sp;
             const double st = 2.0 * ((pairs + sp - 1) / sp);
-            double cost;
             if (!small) {
-                cost = (double)((tiles + 255) / 256) * (st * 1.45 + 10.0);
+                p.cost = (double)((tiles + 255) / 256) * (st * 1.45 + 10.0);
             } else {
                 const int64_t rest = tiles % 512;
-                cost = (double)(tiles / 512) * (st * 1.15 + 4.0) + (rest ? st * (rest <= 256 ? 0.8 : 1.15) + 4.0 : 0.0);
+                p.cost = (double)(tiles / 512) * (st * 1.15 + 4.0) + (rest ? st * (rest <= 256 ? 0.8 : 1.15) + 4.0 : 0.0);
             }
-            if (sp > 1) cost += 9.5 + 0.8e-6 * (double)np * nq * nout * (sp + 1);
-            if (cost < best_cost) {
-                best_cost = cost;
+            if (sp > 1) p.cost += 9.5 + 0.8e-6 * (double)np * nq * nout * (sp + 1);
+            if (p.cost < best.cost) {
                 best = p;
                 best.splits = sp;
             }
         }
     }
-    best.part_bytes = best.splits > 1 ? align_up((size_t)best.splits * nout * nq * best.pitch * sizeof(float)) : 0;
+    best.part_bytes = part_bytes(best, nq, nout);
     return best;
+}
+
+// Time until nl tiles of l microseconds and then ns of s <= l are done, each taken by
+// the first free of `slots` places.
+double fill_time(int64_t nl, double l, int64_t ns, double s, int slots)
+{
+    const int64_t rounds = nl / slots, late = nl % slots;       // `late` places start later by l
+    const double t0 = (double)rounds * l;
+    const double level = t0 + ((double)late * l + (double)ns * s) / slots;     // were tiles divisible
+    double best = 1e300;
+    for (int c = 0; c < 2; ++c) {                               // the last tile ends a place of either kind
+        const double start = t0 + c * l;
+        for (int64_t k = std::max<int64_t>(0, (int64_t)((level - start) / s)), n = 0; n < 4; ++k, ++n) {
+            const double t = start + (double)k * s + 1e-9;
+            const int64_t room = (int64_t)((t - t0) / s) * (slots - late) +
+                                 (t >= t0 + l ? (int64_t)((t - t0 - l) / s) * late : 0);
+            if (room >= ns && t < best) best = t;
+        }
+    }
+    if (late && best < t0 + l) best = t0 + l;
+    return best;
+}
+
+double split_cost(const Plan& p, int64_t np, int64_t nq, int nout)
+{
+    return p.splits > 1 ? 9.5 + 0.8e-6 * (double)np * nq * nout * (p.splits + 1) : 0.0;
+}
+
+// dX and dW together or apart, by the same model; apart costs 3 for its second launch.
+// Fills both plans; whether together.
+bool make_plans(const GemmSize& x, const GemmSize& w, Plan& px, Plan& pw)
+{
+    px = make_plan(x.kind, x.np, x.nq, x.K, x.nseg, x.nbatch);
+    pw = make_plan(w.kind, w.np, w.nq, w.K, w.nseg, w.nbatch);
+    double best = px.cost + pw.cost + 3.0;
+    bool two = false;
+    static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    for (int small = 0; small < 2; ++small) {
+        Plan a = make_shape(x.kind, small, x.np, x.nq, x.K, x.nseg);
+        Plan b = make_shape(w.kind, small, w.np, w.nq, w.K, w.nseg);
+        const int64_t ta = (int64_t)a.ntp * a.ntq, tb = (int64_t)b.ntp * b.ntq * w.nbatch;
+        const int slots = small ? 512 : 256;
+        for (int sa : kSplits) {
+            if (sa > (a.steps + 1) / 2 || (sa > 1 && ta * sa > 2 * slots)) break;
+            a.splits = sa;
+            const double fa = split_cost(a, x.np, x.nq, 1);
+            for (int sb : kSplits) {
+                if (sb > (b.steps + 1) / 2 || (sb > 1 && tb * sb > 2 * slots)) break;
+                b.splits = sb;
+                const double per = small ? (ta * sa + tb * sb <= 256 ? 0.8 : 1.15) : 1.45, round = small ? 4.0 : 10.0;
+                const double ca = 2.0 * (((a.steps + 1) / 2 + sa - 1) / sa) * per + round;
+                const double cb = 2.0 * (((b.steps + 1) / 2 + sb - 1) / sb) * per + round;
+                const double t = (ca >= cb ? fill_time(ta * sa, ca, tb * sb, cb, slots) : fill_time(tb * sb, cb, ta * sa, ca, slots)) +
+                                 fa + split_cost(b, w.np, w.nq, w.nbatch);
+                if (t < best) {
+                    best = t;
+                    two = true;
+                    a.cost = ca; b.cost = cb;
+                    px = a;
+                    pw = b;
+                }
+            }
+        }
+    }
+    if (two) {
+        px.part_bytes = part_bytes(px, x.nq, 1);
+        pw.part_bytes = part_bytes(pw, w.nq, w.nbatch);
+    }
+    return two;
 }
 
 template <class T, bool TRP, bool TRQ, bool PAIR, int FP, int FQ>
@@ -506,11 +620,12 @@ size_t gemm_workspace(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg
     return make_plan(kind, np, nq, K, nseg, nbatch).part_bytes;
 }
 
-vq_status gemm_launch(const GemmArgs& g, void* ws, size_t ws_bytes, hipStream_t st)
+namespace {
+
+// The kernel's arguments; parts from cv.
+bool make_tile(const GemmArgs& g, const Plan& p, Carver& cv, Tile& t)
 {
-    const int64_t K = g.kP < g.kQ ? g.kP : g.kQ;
-    const Plan p = make_plan(g.kind, g.np, g.nq, K, g.nseg, g.nbatch);
-    Tile t{};
+    t = Tile{};
     for (int i = 0; i < 2; ++i) {
         t.P[i] = static_cast<const char*>(g.P[i]);
         t.Q[i] = static_cast<const char*>(g.Q[i]);
@@ -522,12 +637,58 @@ vq_status gemm_launch(const GemmArgs& g, void* ws, size_t ws_bytes, hipStream_t 
     t.seg_steps = p.seg_steps; t.steps = p.steps;
     t.splits = p.splits; t.pitch = p.pitch;
     t.epi = g.epi; t.Y2 = g.Y2;
-    if (p.splits > 1) {
-        Carver cv(ws, ws_bytes);
-        t.part = cv.take<float>(p.part_bytes / sizeof(float));
-        if (!cv.ok) return fail(VQ_ERR_WORKSPACE, "matrix product: workspace too small");
-    }
+    if (p.splits > 1) t.part = cv.take<float>(p.part_bytes / sizeof(float));
+    return cv.ok;
+}
+
+GemmSize size_of(const GemmArgs& g) { return {g.kind, g.np, g.nq, std::min(g.kP, g.kQ), g.nseg, g.nbatch}; }
+
+template <class T>
+vq_status launch_two(const Two& a, const Plan& px, const Plan& pw, hipStream_t st)
+{
+    if (px.fp == 8) hipLaunchKernelGGL((k_gemm_two<T, 8, 4>), dim3(a.nx + a.nw), dim3(kThreads), 0, st, a);
+    else hipLaunchKernelGGL((k_gemm_two<T, 4, 2>), dim3(a.nx + a.nw), dim3(kThreads), 0, st, a);
+    VQ_LAUNCHED("k_gemm_two");
+    if (px.splits > 1) VQ_TRY(launch_finish<T>({a.x.part, px.splits, a.x.np, a.x.nq, a.x.pitch, a.x.epi, nullptr}, false, 1, st));
+    if (pw.splits > 1)
+        VQ_TRY(launch_finish<T>({a.w.part, pw.splits, a.w.np, a.w.nq, a.w.pitch, a.w.epi, a.w.Y2}, false, a.w_batch, st));
+    return VQ_OK;
+}
+
+}  // namespace
+
+vq_status gemm_launch(const GemmArgs& g, void* ws, size_t ws_bytes, hipStream_t st)
+{
+    const GemmSize z = size_of(g);
+    const Plan p = make_plan(z.kind, z.np, z.nq, z.K, z.nseg, z.nbatch);
+    Carver cv(ws, ws_bytes);
+    Tile t;
+    if (!make_tile(g, p, cv, t)) return fail(VQ_ERR_WORKSPACE, "matrix product: workspace too small");
     return g.dtype == VQ_BF16 ? launch_type<Bf16>(g.kind, t, p, g.nbatch, st) : launch_type<F16>(g.kind, t, p, g.nbatch, st);
+}
+
+size_t gemm_two_workspace(const GemmSize& x, const GemmSize& w)
+{
+    Plan px, pw;
+    return make_plans(x, w, px, pw) ? px.part_bytes + pw.part_bytes : std::max(px.part_bytes, pw.part_bytes);
+}
+
+vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, void* ws, size_t ws_bytes, hipStream_t st)
+{
+    Plan px, pw;
+    if (!make_plans(size_of(x), size_of(w), px, pw)) {          // one after the other, parts in the same place
+        VQ_TRY(gemm_launch(x, ws, ws_bytes, st));
+        return gemm_launch(w, ws, ws_bytes, st);
+    }
+    Carver cv(ws, ws_bytes);
+    Two a{};
+    if (!make_tile(x, px, cv, a.x) || !make_tile(w, pw, cv, a.w))
+        return fail(VQ_ERR_WORKSPACE, "matrix product: workspace too small");
+    a.nx = px.ntp * px.ntq * px.splits;
+    a.nw = pw.ntp * pw.ntq * pw.splits * w.nbatch;
+    a.w_batch = w.nbatch;
+    a.w_first = pw.cost > px.cost;
+    return x.dtype == VQ_BF16 ? launch_two<Bf16>(a, px, pw, st) : launch_two<F16>(a, px, pw, st);
 }
 
 }  // namespace vq
