@@ -192,10 +192,12 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     // this wave's matrix, its place among the matrix's waves and their number
     const int mm = nm > 1 ? wave & 1 : 0, turn = nm > 1 ? wave >> 1 : wave, turns = nm > 1 ? nwaves >> 1 : nwaves;
 
-    // LDS: residual codebooks (rows of S floats), column scales [scaled][slab * S],
-    // token terms [XTERMS][T][pitch]; the sums' exchange takes the last two's place
+    // LDS: corrections [nm][NT * 16][16], residual codebooks (rows of S floats), column
+    // scales [scaled][slab * S], token terms [XTERMS][T][pitch]; the sums' exchange takes
+    // the last two's place
     const int columns = a.slab * S, pitch = token_pitch(columns);
-    int used = 0, cs_rows = 0;
+    float* const cor = lds;
+    int used = nm * NT * 16 * kQRows, cs_rows = 0;
     int c2_of[2] = {-1, -1}, cs_of[2] = {-1, -1};
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -214,9 +216,9 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // sparse corrections of this wave's rows: lane -> token lane % tl
+    // sparse corrections: a wave's lanes are tl token places, over which the rest share the entries
+    const bool sparse = a.q[0].row_ptr || (nm > 1 && a.q[1].row_ptr);
     constexpr int kJobs = 4;                                   // two matrices' 16 rows over at least eight waves
-    float corr[kJobs] = {};
     int tl = 1;
     while (tl < a.T) tl *= 2;
 
@@ -232,14 +234,16 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     };
 
     const int item = threadIdx.x;
-    int e0[kJobs], e1[kJobs];
-#pragma unroll
-    for (int job = 0; job < kJobs; ++job) {
-        const int id = job * nwaves + wave, m = id / kQRows;
+    // lane j < kJobs: where the entries of the wave's job j (row nwaves * j + wave of both matrices) begin and end
+    int ends[2] = {0, 0};
+    if (sparse && lane < kJobs) {
+        const int id = lane * nwaves + wave;
         const int64_t i = row0 + id % kQRows;
-        const int32_t* rp = id < nm * kQRows && i < a.M ? a.q[m & 1].row_ptr : nullptr;
-        e0[job] = rp ? rp[i] : 0;
-        e1[job] = rp ? rp[i + 1] : 0;
+        const int32_t* rp = id < nm * kQRows && i < a.M ? (id < kQRows ? a.q[0].row_ptr : a.q[1].row_ptr) : nullptr;
+        if (rp) {
+            ends[0] = rp[i];
+            ends[1] = rp[i + 1];
+        }
     }
     f32x4 c2_v[2];                                             // D: at most one quad a thread
     if (D) {
@@ -348,9 +352,9 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                 k2[i] = i2[i];
             }
             if (kb + turns < se) load_block(kb + turns);
-            const int c0 = ((kb - sb) * kBlock + g * 8) * S;   // the lane's first column in the slab
-#pragma unroll
-            for (int h = 0; h < 8 / U / H; ++h) {
+            int c0 = ((kb - sb) * kBlock + g * 8) * S;         // the lane's first column in the slab
+#pragma unroll 1
+            for (int h = 0; h < 8 / U / H; ++h) {              // one copy of the body: the code stays in its cache
                 float w[H][8];
                 if (D == 8) {
                     const f32x4* C = reinterpret_cast<const f32x4*>(q.C1);
@@ -358,7 +362,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                     f32x4 ga[H], gb[H];
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
-                        const int mine = index_of(k1, h * H + j), other = swap_pair(mine);
+                        const int mine = index_of(k1, j), other = swap_pair(mine);
                         ga[j] = C[2 * (odd ? other : mine) + odd];
                         gb[j] = C[2 * (odd ? mine : other) + odd];
                     }
@@ -376,27 +380,27 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                     for (int j = 0; j < H; ++j)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const f32x4 v = C[index_of(k1, (h * H + j) * 2 + u)];
+                            const f32x4 v = C[index_of(k1, j * 2 + u)];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) w[j][u * 4 + i] = v[i];
                         }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < H; ++j) load_row(q.C1, index_of(k1, h * H + j), d, w[j]);
+                    for (int j = 0; j < H; ++j) load_row(q.C1, index_of(k1, j), d, w[j]);
                 }
                 if (q.C2) {
 #pragma unroll
                     for (int j = 0; j < H; ++j) {
                         if (D == 0 && c2_at < 0) {
                             float v[8];
-                            load_row(q.C2, index_of(k2, h * H + j), d, v);
+                            load_row(q.C2, index_of(k2, j), d, v);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) w[j][i] += v[i];
                         } else {
                             const float* c2 = c2_at >= 0 ? lds + c2_at : q.C2;
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {        // halves of one row, or two rows
-                                const int k = index_of(k2, (h * H + j) * U + (D == 4 ? u : 0));
+                                const int k = index_of(k2, j * U + (D == 4 ? u : 0));
                                 const f32x4 v = *reinterpret_cast<const f32x4*>(c2 + k * S + (D == 4 ? 0 : u * 4));
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) w[j][u * 4 + i] += v[i];
@@ -409,7 +413,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                     for (int j = 0; j < H; ++j)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const f32x4 v = *reinterpret_cast<const f32x4*>(cs + cs_at + c0 + (h * H + j) * 8 + u * 4);
+                            const f32x4 v = *reinterpret_cast<const f32x4*>(cs + cs_at + c0 + j * 8 + u * 4);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) w[j][u * 4 + i] *= v[i];
                         }
@@ -425,7 +429,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                         V8 xt[XTERMS];
 #pragma unroll
                         for (int k = 0; k < XTERMS; ++k)
-                            xt[k] = *reinterpret_cast<const V8*>(xs + (k * a.T + t) * pitch + c0 + (h * H + j) * 8);
+                            xt[k] = *reinterpret_cast<const V8*>(xs + (k * a.T + t) * pitch + c0 + j * 8);
 #pragma unroll
                         for (int p = 0; p < WTERMS; ++p)
 #pragma unroll
@@ -433,37 +437,52 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                                 if (p + k < WTERMS) acc[n] = Bf16::mfma(wt[p], xt[k], acc[n]);
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);             // one group's rows in registers at a time
+                c0 += H * 8;
+#pragma unroll
+                for (int i = 0; i + U * H / 2 < 4; ++i) {
+                    k1[i] = k1[i + U * H / 2];
+                    k2[i] = k2[i + U * H / 2];
+                }
             }
         }
 
         // exact entries whose column lies in the slab: x from its terms
-        const int64_t col0 = sv0 * d, col1 = (int64_t)se * kBlock < a.nb ? (int64_t)se * kBlock * d : a.N;
+        if (sparse) {
+            const int64_t col0 = sv0 * d, col1 = (int64_t)se * kBlock < a.nb ? (int64_t)se * kBlock * d : a.N;
+            const int t = lane & (tl - 1), tx = t < a.T ? t : a.T - 1;
+#pragma unroll 1
+            for (int job = 0; job < kJobs; ++job) {
+                const int id = job * nwaves + wave;
+                if (id >= nm * kQRows) break;
+                const int e0 = __builtin_amdgcn_readlane(ends[0], job), e1 = __builtin_amdgcn_readlane(ends[1], job);
+                const int32_t* const col = id < kQRows ? a.q[0].col : a.q[1].col;
+                const float* const delta = id < kQRows ? a.q[0].delta : a.q[1].delta;
+                const int step = 64 / tl;
+                float c = 0.0f;
+#pragma unroll 1
+                for (int e = e0 + lane / tl; e < e1; e += step * 4) {
+                    int j[4];
+                    float v[4];
 #pragma unroll
-        for (int job = 0; job < kJobs; ++job) {
-            if (e0[job] >= e1[job]) continue;
-            const QMat& q = a.q[(job * nwaves + wave) / kQRows];
-            const int t = lane & (tl - 1), step = 64 / tl;
-            const int tx = t < a.T ? t : a.T - 1;
-            for (int e = e0[job] + lane / tl; e < e1[job]; e += step * 4) {
-                int j[4];
-                float v[4];
+                    for (int u = 0; u < 4; ++u) {              // four entries in flight
+                        const int k = e + u * step < e1 ? e + u * step : e1 - 1;
+                        j[u] = col[k];
+                        v[u] = delta[k];
+                    }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {              // four entries in flight
-                    const int k = e + u * step < e1[job] ? e + u * step : e1[job] - 1;
-                    j[u] = q.col[k];
-                    v[u] = q.delta[k];
+                    for (int u = 0; u < 4; ++u) {
+                        if (e + u * step >= e1 || j[u] < col0 || j[u] >= col1) continue;
+                        const int cl = (int)(j[u] - col0);
+                        const int at = D ? cl : cl / d * S + cl % d;
+                        float x = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < XTERMS; ++k) x += (float)xs[(k * a.T + tx) * pitch + at];
+                        c = fmaf(v[u], x, c);
+                    }
                 }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (e + u * step >= e1[job] || j[u] < col0 || j[u] >= col1) continue;
-                    const int cl = (int)(j[u] - col0);
-                    const int c = D ? cl : cl / d * S + cl % d;
-                    float x = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < XTERMS; ++k) x += (float)xs[(k * a.T + tx) * pitch + c];
-                    corr[job] = fmaf(v[u], x, corr[job]);
-                }
+                for (int o = 32; o >= tl; o >>= 1) c += __shfl_xor(c, o, 64);
+                float* const place = cor + (id / kQRows * NT * 16 + lane) * kQRows + id % kQRows;
+                if (lane < tl && lane < NT * 16) *place = sb == kb0 ? c : *place + c;
             }
         }
     }
@@ -487,16 +506,8 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     // sums over the waves, in wave order, and the corrections
     __syncthreads();
     float* red = lds + used;                                   // [nwaves][NT][64] of four rows
-    float* cor = red + nwaves * NT * 256;                      // [nm][NT * 16][16]
 #pragma unroll
     for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(red + ((wave * NT + n) * 64 + lane) * 4) = acc[n];
-#pragma unroll
-    for (int job = 0; job < kJobs; ++job) {
-        const int id = job * nwaves + wave, m = id / kQRows, rr = id % kQRows;
-        float c = corr[job];
-        for (int o = 32; o >= tl; o >>= 1) c += __shfl_xor(c, o, 64);
-        if (id < nm * kQRows && lane < tl && lane < NT * 16) cor[(m * NT * 16 + lane) * kQRows + rr] = c;
-    }
     __syncthreads();
     if (!stores) return;
     float z[2] = {0.0f, 0.0f};
@@ -513,7 +524,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
             for (int u = 0; u < 4; ++u) v += f[u];
         }
         if (a.q[m].rs) v *= rs_v[m];
-        z[m] = v + cor[(m * NT * 16 + item_t) * kQRows + item_r];
+        z[m] = sparse ? v + cor[(m * NT * 16 + item_t) * kQRows + item_r] : v;
         if (a.part) a.part[(((int64_t)blockIdx.y * nm + m) * a.T + item_t) * a.M + out_row] = z[m];
         z[m] += bias_v[m];
     }
@@ -620,7 +631,7 @@ template <int D, int XT, int NT>
 vq_status q_launch(QArgs a, hipStream_t st)
 {
     constexpr int S = slots_of(D);
-    size_t c2 = 0;
+    size_t c2 = (size_t)a.nm * NT * 16 * kQRows * sizeof(float);   // the corrections and the residual codebooks
     int scales = 0;
     for (int m = 0; m < a.nm; ++m) {
         if (a.q[m].C2 && a.q[m].K2 * S <= kC2Floats) c2 += (size_t)a.q[m].K2 * S * sizeof(float);
@@ -637,7 +648,7 @@ vq_status q_launch(QArgs a, hipStream_t st)
     int64_t slabs = 1;
     while (slabs < mine && c2 + slab_bytes((mine + slabs - 1) / slabs * kBlock) > cap) ++slabs;
     a.slab = (int)((mine + slabs - 1) / slabs * kBlock);
-    const size_t sums = ((size_t)waves * NT * 256 + (size_t)a.nm * NT * 16 * kQRows) * sizeof(float);
+    const size_t sums = (size_t)waves * NT * 256 * sizeof(float);
     const size_t lds = c2 + std::max(slab_bytes(a.slab), sums);
     const auto kern = k_qffn<D, XT, NT>;
     if (lds > 64 * 1024) {
