@@ -82,20 +82,33 @@ template <> struct XType<VQ_F32> { typedef float E; static constexpr int kTerms 
 __device__ inline int swap_pair(int v) { return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true); }
 __device__ inline float swap_pair(float v) { return __int_as_float(swap_pair(__float_as_int(v))); }
 
-// v = t[0] + t[1] + ... in bf16 terms, each rounded to nearest.
+// v = t[0] + t[1] + ... in bf16 terms, each rounded to nearest.  What a term leaves
+// is exact, and formed by the two-element dot product, (t0, t1) . (-1, 0) + v0, which
+// takes the packed terms as they are: 12 instructions a term and chunk, not 20.
 template <int NTERM>
 __device__ inline void split(const float (&v)[8], V8 (&t)[NTERM])
 {
+    typedef __bf16 V2 __attribute__((ext_vector_type(2)));
+    // -1 in the low and in the high half, in registers: as a constant of the instruction
+    // the compiler writes -1.0 for either, which is read as the high half's
+    uint32_t low = 0x0000bf80u, high = 0xbf800000u;
+    asm("" : "+s"(low), "+s"(high));
+    const V2 first = __builtin_bit_cast(V2, low), second = __builtin_bit_cast(V2, high);
     float rest[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) rest[i] = v[i];
 #pragma unroll
-    for (int k = 0; k < NTERM; ++k)
+    for (int k = 0; k < NTERM; ++k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            t[k][i] = (__bf16)rest[i];
-            if (k + 1 < NTERM) rest[i] = rest[i] - (float)t[k][i];
+        for (int i = 0; i < 8; ++i) t[k][i] = (__bf16)rest[i];
+        if (k + 1 == NTERM) break;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const V2 p = {t[k][i], t[k][i + 1]};
+            rest[i] = __builtin_amdgcn_fdot2_f32_bf16(p, first, rest[i], false);
+            rest[i + 1] = __builtin_amdgcn_fdot2_f32_bf16(p, second, rest[i + 1], false);
         }
+    }
 }
 
 template <class E> __device__ inline float load_x(const void* p, int64_t i) { return (float)static_cast<const E*>(p)[i]; }
@@ -178,9 +191,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
     constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
     constexpr int S = slots_of(D);
-    // Chunks whose gathers are in flight together: as many as their rows and the terms
-    // leave registers for.  4096 x 11008, one float32 token: 44.9 us with two, 48.6 with four.
-    constexpr int H = D && XT == VQ_BF16 && NT == 1 ? 4 : 2;
+    constexpr int H = 2;                               // chunks whose gathers are in flight together
     extern __shared__ __align__(16) float lds[];
     const int d = D ? D : a.d;
     const int nm = a.nm;
