@@ -227,11 +227,13 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // sparse corrections: a wave's lanes are tl token places, over which the rest share the entries
+    // Sparse corrections: a wave has one, two or four rows (16 of each matrix over its
+    // waves) and gives each as many lanes; a row's lanes are tp tokens, times entries.
     const bool sparse = a.q[0].row_ptr || (nm > 1 && a.q[1].row_ptr);
-    constexpr int kJobs = 4;                                   // two matrices' 16 rows over at least eight waves
-    int tl = 1;
-    while (tl < a.T) tl *= 2;
+    const int own = nm * kQRows / nwaves, per_row = 64 / own;
+    int tp = 1;
+    while (tp < a.T && tp < per_row) tp *= 2;
+    const int sparse_id = lane / per_row * nwaves + wave;      // matrix * 16 + row
 
     const int nkb = (int)((a.nb + kBlock - 1) / kBlock);
     const int kb0 = (int)((int64_t)nkb * blockIdx.y / a.splits), kb1 = (int)((int64_t)nkb * (blockIdx.y + 1) / a.splits);
@@ -245,15 +247,13 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     };
 
     const int item = threadIdx.x;
-    // lane j < kJobs: where the entries of the wave's job j (row nwaves * j + wave of both matrices) begin and end
-    int ends[2] = {0, 0};
-    if (sparse && lane < kJobs) {
-        const int id = lane * nwaves + wave;
-        const int64_t i = row0 + id % kQRows;
-        const int32_t* rp = id < nm * kQRows && i < a.M ? (id < kQRows ? a.q[0].row_ptr : a.q[1].row_ptr) : nullptr;
-        if (rp) {
-            ends[0] = rp[i];
-            ends[1] = rp[i + 1];
+    int e0 = 0, e1 = 0;                                        // the lane's row's entries
+    if (sparse) {
+        const int64_t i = row0 + sparse_id % kQRows;
+        const int32_t* rp = sparse_id < kQRows ? a.q[0].row_ptr : a.q[1].row_ptr;
+        if (rp && i < a.M) {
+            e0 = rp[i];
+            e1 = rp[i + 1];
         }
     }
     f32x4 c2_v[2];                                             // D: at most one quad a thread
@@ -460,18 +460,15 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
         // exact entries whose column lies in the slab: x from its terms
         if (sparse) {
             const int64_t col0 = sv0 * d, col1 = (int64_t)se * kBlock < a.nb ? (int64_t)se * kBlock * d : a.N;
-            const int t = lane & (tl - 1), tx = t < a.T ? t : a.T - 1;
+            const int32_t* const col = sparse_id < kQRows ? a.q[0].col : a.q[1].col;
+            const float* const delta = sparse_id < kQRows ? a.q[0].delta : a.q[1].delta;
+            const int place = lane % per_row, step = per_row / tp;
 #pragma unroll 1
-            for (int job = 0; job < kJobs; ++job) {
-                const int id = job * nwaves + wave;
-                if (id >= nm * kQRows) break;
-                const int e0 = __builtin_amdgcn_readlane(ends[0], job), e1 = __builtin_amdgcn_readlane(ends[1], job);
-                const int32_t* const col = id < kQRows ? a.q[0].col : a.q[1].col;
-                const float* const delta = id < kQRows ? a.q[0].delta : a.q[1].delta;
-                const int step = 64 / tl;
+            for (int t0 = 0; t0 < a.T; t0 += tp) {
+                const int t = t0 + (place & (tp - 1)), tx = t < a.T ? t : a.T - 1;
                 float c = 0.0f;
 #pragma unroll 1
-                for (int e = e0 + lane / tl; e < e1; e += step * 4) {
+                for (int e = e0 + place / tp; e < e1; e += step * 4) {
                     int j[4];
                     float v[4];
 #pragma unroll
@@ -491,9 +488,9 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                         c = fmaf(v[u], x, c);
                     }
                 }
-                for (int o = 32; o >= tl; o >>= 1) c += __shfl_xor(c, o, 64);
-                float* const place = cor + (id / kQRows * NT * 16 + lane) * kQRows + id % kQRows;
-                if (lane < tl && lane < NT * 16) *place = sb == kb0 ? c : *place + c;
+                for (int o = per_row / 2; o >= tp; o >>= 1) c += __shfl_xor(c, o, 64);
+                float* const sum = cor + (sparse_id / kQRows * NT * 16 + t) * kQRows + sparse_id % kQRows;
+                if (place < tp && t < a.T) *sum = sb == kb0 ? c : *sum + c;
             }
         }
     }
