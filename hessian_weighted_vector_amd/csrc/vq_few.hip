@@ -12,7 +12,9 @@
 // workgroups to keep the memory busy, the columns are split over workgroups and
 // the tiled product's second kernel adds the parts.
 //
-// Bound by the weights' bytes.  Loads are at any element-aligned address.
+// Bound by the weights' bytes.  Loads are at any element-aligned address.  One
+// token: 4096 x 11008 bf16 in 17.5 us (5.2 TB/s; a large read reaches 6.2), a pair
+// of 8192 x 2048 fp16 in 12.8 us (5.2 TB/s).
 #include "vq_ffn.h"
 
 namespace vq {
@@ -168,8 +170,12 @@ __global__ __launch_bounds__(1024) void k_few(const Few a)
 }
 
 // Sixteen waves a workgroup where the rows give less than two workgroups of
-// eight a CU; the columns are split over workgroups where they give less than
-// one of sixteen and every wave of every split keeps a block.
+// eight a CU: pair of 4096 x 8192, 27 us with sixteen and 33 with eight; 2048 x
+// 8192, 16 tokens, 13.5 and 17; the other way round 4096 x 8192, one token, 19 and
+// 15.  With more rows eight: 8192 x 8192, 25 and 34 us.  The columns are split
+// over workgroups where the rows give less than one of sixteen and every wave of
+// every split keeps a block: 1024 x 16384, 13-16 us over four, 20 over one; 1024
+// x 4096, one: 8.9 us, and 12.7 over two with their second launch.
 struct FewPlan { int waves, splits; };
 FewPlan few_plan(int64_t M, int64_t K)
 {
@@ -200,7 +206,12 @@ vq_status few_launch(const Few& a, int waves, bool pair, hipStream_t st)
 
 }  // namespace
 
-bool few_tokens(int64_t T) { return T <= 32; }
+// Up to 32 tokens, while the weights' elements times the tokens stay below 6e8: past
+// that the tiled product, which reads the tokens once a tile, is faster.  One token by
+// 8192 x 8192: 25 us here and 26 us tiled, eight 29 and 26, 32 45 and 28; 4096 x 4096,
+// 32 tokens: 14 and 16; pair of 28672 x 8192, one token: 169 and 161, eight 186 and 161;
+// pair of 8192 x 8192, one 40 and 43, 16 48 and 45.
+bool few_tokens(int64_t T, int64_t M, int64_t K, int nm) { return T <= 32 && (double)T * (double)M * (double)K * nm < 6e8; }
 
 size_t few_workspace(int64_t T, int64_t M, int64_t K, int nm)
 {

@@ -251,7 +251,7 @@ vq_status finish_parts(int dtype, bool pair, const float* part, int splits, int 
                        hipStream_t st);
 
 // ---- few tokens -----------------------------------------------------------
-// The forward products for up to 32 tokens, any strides and alignment.
+// The forward products for up to 32 tokens, any strides and alignment; whether that is the faster way.
 struct FewArgs {
     int64_t T, M, K;
     int dtype, nm;
@@ -259,7 +259,7 @@ struct FewArgs {
     const void* W[2]; int64_t ldw;
     Epilogue epi;
 };
-bool few_tokens(int64_t T);
+bool few_tokens(int64_t T, int64_t M, int64_t K, int nm);
 size_t few_workspace(int64_t T, int64_t M, int64_t K, int nm);
 vq_status few_product(const FewArgs& f, void* ws, hipStream_t st);
 

@@ -15,13 +15,17 @@
 // of the leading one are summed in float32.  Sixteen tokens cost the gathers of
 // one.
 //
-// What bounds it is the requests from L1 to L2: each sub-vector is one, a CU
-// keeps about 64 of them in flight, and everything else that misses L1 queues
-// with them.  So the tokens' terms and the column scales of a slab of columns
-// are staged in LDS once a workgroup, indices are read 16 bytes (eight
-// sub-vectors) a lane, a block ahead, and neighbouring lanes fetch the two
+// What bounds it is the requests from L1 to L2: each sub-vector is one, to a
+// random line, and at 0.42 a clock and CU the L2 channels of a die (16 for 32 CUs)
+// take 0.84 of one each a clock.  So the tokens' terms and the column scales of a
+// slab of columns are staged in LDS once a workgroup, indices are read 16 bytes
+// (eight sub-vectors) a lane, a block ahead, and neighbouring lanes fetch the two
 // halves of one centroid row in one instruction (one request, not two) and swap
-// them.
+// them.  4096 x 11008, one float32 token, all parts: 36 us, of which the gathers
+// alone (no residual, scales or exact entries) take 31; a pair of 8192 x 2048, one
+// token, 30 us; of 11008 x 4096, eight tokens, 94 us.  The body has one copy:
+// unrolled over a block's groups it was 28 KB of code and its sums went through
+// scratch memory, 14 to 20 % slower.
 //
 // A workgroup owns 16 rows; its waves (of a pair, the even ones gate and the odd
 // ones up) take blocks of 32 sub-vectors in turn and their sums are added in wave
@@ -604,9 +608,9 @@ int64_t q_groups(int64_t M) { return (M + kQRows - 1) / kQRows; }
 int64_t q_blocks(int64_t nb) { return (nb + kBlock - 1) / kBlock; }
 
 // Each row's blocks are split over up to 16 workgroups while the workgroups stay
-// one a CU and have four blocks or more.  179 x 15720, one token: 18 us over 8 or
-// 16, 41 us over one, 25 us over 32; 512 x 4096, pair: 19 us over 4, 29 us over
-// one; 256 x 1024: 11.5 us over one, 13.8 us over two.
+// one a CU and have four blocks or more.  179 x 15720, one token: 17 us over 8 or
+// 16, 37 us over one, 22 us over 32; 512 x 4096, pair: 17 us over 4, 31 us over
+// one; 256 x 1024: 10 us over one, 13 us over two.
 int q_splits(int64_t M, int64_t nb)
 {
     int s = 1;
@@ -616,11 +620,11 @@ int q_splits(int64_t M, int64_t nb)
 
 // Eight waves a workgroup where its tokens and scales fit in half a CU's LDS at
 // once, so that two share a CU and one gathers while the other stages or sums;
-// else sixteen.  Pair of 8192 x 2048, one token: 36 us with eight, 43 us with
-// sixteen; of 11008 x 4096, one token 93 and 104 us, but eight tokens (two slabs)
-// 137 and 125 us.  Many tokens' exact entries are shared among sixteen where the
-// rows leave one workgroup a CU: pair of 64 x 4096, 24 tokens, 37 and 23 us;
-// without exact entries 19.1 and 20.3 us (512 x 4096).  lds: bytes staged at once.
+// else sixteen.  Pair of 8192 x 2048, one token: 31 us with eight, 39 us with
+// sixteen; of 11008 x 4096, one token 74 and 87 us, but 16 tokens (more slabs)
+// 145 and 124 us.  Many tokens' exact entries are shared among sixteen where the
+// rows leave one workgroup a CU: pair of 512 x 4096, 24 tokens, 31 and 26 us;
+// without exact entries 19.0 and 19.6 us.  lds: bytes staged at once.
 int q_waves(const QArgs& a, size_t lds)
 {
     if (q_blocks(a.nb) * a.nm < 16) return 8;

@@ -165,6 +165,17 @@ def test_split_sums_and_many_tiles():
                   ref.linear_backward(dY, X, Wg, None, "none", dtype)[:2])
 
 
+def test_few_tokens_of_a_large_matrix():
+    """Enough weights for the tiled product to be taken for few tokens; unaligned rows keep the other."""
+    say("few tokens, large matrix")
+    g = torch.Generator().manual_seed(21)
+    X = tensor(g, (20, 4096), torch.bfloat16)
+    W = [tensor(g, (8192, 4096), torch.bfloat16, 0.02) for _ in range(2)]
+    for Wg, Wu in (W, [torch.cat([w, w[:, :1]], 1)[:, :4096] for w in W]):
+        check("linear", (vq.linear(X, Wg, act="silu"),), ref.linear(X, Wg, None, None, "silu", torch.bfloat16)[:1])
+        check("gated", (vq.gated(X, Wg, Wu),), ref.gated(X, Wg, Wu, None, None, "silu", torch.bfloat16)[:1])
+
+
 def test_residual_in_place_and_reproducible():
     say("in place")
     g = torch.Generator().manual_seed(5)
