@@ -21,8 +21,8 @@
 // slab of columns are staged in LDS once a workgroup, indices are read 16 bytes
 // (eight sub-vectors) a lane, a block ahead, and neighbouring lanes fetch the two
 // halves of one centroid row in one instruction (one request, not two) and swap
-// them.  4096 x 11008, one float32 token, all parts: 36 us, of which the gathers
-// alone (no residual, scales or exact entries) take 31; a pair of 8192 x 2048, one
+// them.  4096 x 11008, one float32 token, all parts: 36 to 40 us; without residual,
+// scales and exact entries 33, the gathers alone; a pair of 8192 x 2048, one
 // token, 30 us; of 11008 x 4096, eight tokens, 94 us.  The body has one copy:
 // unrolled over a block's groups it was 28 KB of code and its sums went through
 // scratch memory, 14 to 20 % slower.

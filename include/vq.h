@@ -530,7 +530,9 @@ double vq_bits_per_weight(int64_t M, int64_t N, int d, int K1, int K2, int64_t n
  * recorded on that call's stream; vq_timing_enable(0) stops recording.
  * Records are keyed by (step name, K); names: "assign_search" (the matrix-core
  * search kernel alone), "assign" (the whole vq_assign), "update", "objective",
- * "select", "binorm", "residual", "reconstruct", "init".  vq_timing_count()
+ * "select", "binorm", "residual", "reconstruct", "init", "linear",
+ * "linear_backward", "gated", "gated_backward", "qlinear", "qgated" (the whole
+ * call; K is 0 for these).  vq_timing_count()
  * waits for the recorded events and returns the number of records;
  * vq_timing_get(i, ...) fills record i (name into a caller buffer of
  * name_len bytes): launches, total, min and max milliseconds.  Returns 0 on
