@@ -242,9 +242,19 @@ struct GemmSize {
     int nseg, nbatch;
 };
 
-// A GEMM_DX and a GEMM_DW product, in one launch where that is faster.
+// Bias gradients: db = the sum of n partial rows of M, for up to two outputs.
+struct BiasSum {
+    const float* part[2];
+    void* db[2];
+    int64_t n;
+    int M, outputs;
+};
+vq_status bias_sum_launch(int dtype, const BiasSum& b, hipStream_t st);
+
+// A GEMM_DX and a GEMM_DW product and the bias gradients (outputs may be 0), in one
+// launch where that is faster.
 size_t gemm_two_workspace(const GemmSize& x, const GemmSize& w);
-vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, void* ws, size_t ws_bytes, hipStream_t st);
+vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, const BiasSum& b, void* ws, size_t ws_bytes, hipStream_t st);
 
 // Adds float32 parts [splits][matrices][nq][pitch] in order and applies the epilogue.
 vq_status finish_parts(int dtype, bool pair, const float* part, int splits, int np, int nq, int pitch, const Epilogue& e,

@@ -7,7 +7,7 @@
 //                 of eight, for operands that are not (odd sizes, odd strides)
 //   k_grad        dZ = dY act'(Z), or dG = dH U act'(G) and dU = dH act(G), and
 //                 the bias gradients' partial column sums, in one pass
-//   k_bias_sum    the bias gradients from the partial sums, in a fixed order
+//                 (the copies above ride in its launch)
 //   k_zero_rows   gradients of zero tokens
 //
 // The gradients of the pre-activations are rounded to the tensors' 16-bit type
@@ -54,15 +54,18 @@ struct Pack {
     int64_t rows, ld, ldp;
     int cols;
 };
-struct Packs { Pack m[3]; };
+struct Packs {
+    Pack m[3];
+    int count = 0;
+    int blocks = 0;            // a matrix's
+};
 
-// blockIdx.y: the matrix.
-__global__ __launch_bounds__(256) void k_pack(const Packs a)
+// Block `block` of `blocks` of the copy of m.
+__device__ __forceinline__ void pack_rows(const Pack& m, int block, int blocks)
 {
-    const Pack m = a.m[blockIdx.y];
     const int64_t per = m.ldp / 8;
     const int64_t n = m.rows * per;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    for (int64_t e = (int64_t)block * 256 + threadIdx.x; e < n; e += (int64_t)blocks * 256) {
         const int64_t r = e / per;
         const int c = (int)(e - r * per) * 8;
         const uint16_t* p = m.s + r * m.ld + c;
@@ -76,6 +79,9 @@ __global__ __launch_bounds__(256) void k_pack(const Packs a)
         *reinterpret_cast<uint4*>(m.o + r * m.ldp + c) = *reinterpret_cast<const uint4*>(v);
     }
 }
+
+// blockIdx.y: the matrix.
+__global__ __launch_bounds__(256) void k_pack(const Packs a) { pack_rows(a.m[blockIdx.y], blockIdx.x, gridDim.x); }
 
 __global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int64_t rows, int64_t cols, int64_t ld)
 {
@@ -91,8 +97,13 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int
 template <class T, bool GATED, int R>
 __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const void* dY, int64_t ldy, const void* Z0,
                                               const void* Z1, int64_t ldz, typename T::E* D0, typename T::E* D1,
-                                              int64_t ldd, float* part0, float* part1)
+                                              int64_t ldd, float* part0, float* part1, const Packs packs)
 {
+    if (blockIdx.y >= (M + 511) / 512) {                     // the operands' copies, in the same launch
+        const int id = (blockIdx.y - (M + 511) / 512) * gridDim.x + blockIdx.x;
+        if (id < packs.blocks * packs.count) pack_rows(packs.m[id / packs.blocks], id % packs.blocks, packs.blocks);
+        return;
+    }
     __shared__ float sums[GATED ? 2 : 1][4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int m = blockIdx.y * 512 + lane * 8;
@@ -160,48 +171,25 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
 // partial sums' bytes); 512 x 8192: 18 and 16 us.
 int grad_rows(int64_t T, int64_t M) { return (M + 511) / 512 * ((T + 31) / 32) < 256 ? 4 : 32; }
 
-// db = sum of `n` partial rows: 16 columns and 16 row slices a workgroup, the
-// slices added in order.
-template <class T>
-__global__ __launch_bounds__(256) void k_bias_sum(const float* __restrict__ part0, const float* __restrict__ part1,
-                                                  int64_t n, int M, typename T::E* db0, typename T::E* db1)
-{
-    __shared__ float sh[16][17];
-    const float* part = blockIdx.y ? part1 : part0;
-    typename T::E* db = blockIdx.y ? db1 : db0;
-    if (db == nullptr) return;
-    const int c = threadIdx.x & 15, sl = threadIdx.x >> 4;
-    const int m = blockIdx.x * 16 + c;
-    float s = 0.0f;
-    if (m < M)
-        for (int64_t r = sl; r < n; r += 16) s += part[r * M + m];
-    sh[sl][c] = s;
-    __syncthreads();
-    if (sl == 0 && m < M) {
-        for (int k = 1; k < 16; ++k) s += sh[k][c];
-        db[m] = (typename T::E)s;
-    }
-}
-
 // Collects the operands that need a packed copy; each copy in the workspace takes
 // its matrix's place, and one launch makes them all.
 struct Packer {
     Arena& ws;
     Packs list{};
-    int count = 0;
     int64_t most = 0;
     void add(Mat& m)
     {
         const int64_t ldp = round8(m.cols);
         void* o = ws.take((size_t)m.rows * ldp * 2);
-        list.m[count++] = {static_cast<const uint16_t*>(m.p), static_cast<uint16_t*>(o), m.rows, m.ld, ldp, (int)m.cols};
+        list.m[list.count++] = {static_cast<const uint16_t*>(m.p), static_cast<uint16_t*>(o), m.rows, m.ld, ldp, (int)m.cols};
         most = std::max(most, m.rows * (ldp / 8));
+        list.blocks = (int)std::min<int64_t>((most + 255) / 256, 16384);
         m = {o, m.rows, ldp, ldp};
     }
     vq_status launch(hipStream_t st) const
     {
-        if (count == 0) return VQ_OK;
-        hipLaunchKernelGGL(k_pack, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 16384), count), dim3(256), 0, st, list);
+        if (list.count == 0) return VQ_OK;
+        hipLaunchKernelGGL(k_pack, dim3((unsigned)list.blocks, list.count), dim3(256), 0, st, list);
         VQ_LAUNCHED("k_pack");
         return VQ_OK;
     }
@@ -272,25 +260,22 @@ struct Backward {
 };
 
 template <class T>
-vq_status grad_launch(const Backward& b, void* const (&D)[2], int64_t ldd, float* const (&part)[2], hipStream_t st)
+vq_status grad_launch(const Backward& b, void* const (&D)[2], int64_t ldd, float* const (&part)[2], const Packs& packs,
+                      hipStream_t st)
 {
     typedef typename T::E E;
     const int rows = grad_rows(b.T, b.M);
-    const dim3 grid((unsigned)((b.T + rows - 1) / rows), (unsigned)((b.M + 511) / 512));
+    const int64_t gx = (b.T + rows - 1) / rows, copies = ((int64_t)packs.blocks * packs.count + gx - 1) / gx;
+    const dim3 grid((unsigned)gx, (unsigned)((b.M + 511) / 512 + copies));
 #define VQ_GRAD(GATED_, R_)                                                                                          \
     hipLaunchKernelGGL((k_grad<T, GATED_, R_>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0],     \
-                       b.Z[1], b.ldz, (E*)D[0], (E*)D[1], ldd, part[0], part[1])
+                       b.Z[1], b.ldz, (E*)D[0], (E*)D[1], ldd, part[0], part[1], packs)
     if (b.nm > 1 && rows == 32) VQ_GRAD(true, 8);
     else if (b.nm > 1) VQ_GRAD(true, 1);
     else if (rows == 32) VQ_GRAD(false, 8);
     else VQ_GRAD(false, 1);
 #undef VQ_GRAD
     VQ_LAUNCHED("k_grad");
-    if (part[0]) {
-        hipLaunchKernelGGL((k_bias_sum<T>), dim3((unsigned)((b.M + 15) / 16), b.nm), dim3(256), 0, st, part[0], part[1],
-                           (int64_t)grid.x, (int)b.M, (E*)b.db[0], (E*)b.db[1]);
-        VQ_LAUNCHED("k_bias_sum");
-    }
     return VQ_OK;
 }
 
@@ -334,10 +319,17 @@ vq_status backward(const Backward& b, Arena& ws, bool run, hipStream_t st)
     if (b.dX && (!loads_ok(w[0]) || (b.nm > 1 && !loads_ok(w[1]))))
         for (int i = 0; i < b.nm; ++i) pk.add(w[i]);
     if (!run) return VQ_OK;
-    VQ_TRY(pk.launch(st));
-
-    if (D[0] || want_db)
-        VQ_TRY(b.dtype == VQ_BF16 ? grad_launch<Bf16>(b, D, ldd, part, st) : grad_launch<F16>(b, D, ldd, part, st));
+    if (D[0] || want_db) {
+        // one grid row of copies or more: a grid has fewer than 2^16 of them
+        const bool ride = (b.M + 511) / 512 + (int64_t)pk.list.blocks * pk.list.count / ((b.T + rows - 1) / rows) < 65000;
+        if (!ride) VQ_TRY(pk.launch(st));
+        const Packs packs = ride ? pk.list : Packs{};
+        VQ_TRY(b.dtype == VQ_BF16 ? grad_launch<Bf16>(b, D, ldd, part, packs, st) : grad_launch<F16>(b, D, ldd, part, packs, st));
+    } else {
+        VQ_TRY(pk.launch(st));
+    }
+    BiasSum bs{{part[0], part[1]}, {b.db[0], b.db[1]}, (b.T + rows - 1) / rows, (int)b.M, want_db ? b.nm : 0};
+    if (!(b.dX && want_dw)) VQ_TRY(bias_sum_launch(b.dtype, bs, st));
     GemmArgs gx{}, gw{};
     gx.dtype = gw.dtype = b.dtype;
     gx.np = gw.np = (int)b.N;
@@ -364,7 +356,7 @@ vq_status backward(const Backward& b, Arena& ws, bool run, hipStream_t st)
         gw.epi.Y = b.dW[first]; gw.epi.ldy = b.lddw;
         gw.Y2 = b.dW[1];
     }
-    if (b.dX && want_dw) return gemm_two_launch(gx, gw, part_ws, parts, st);
+    if (b.dX && want_dw) return gemm_two_launch(gx, gw, bs, part_ws, parts, st);
     if (b.dX) return gemm_launch(gx, part_ws, parts, st);
     return want_dw ? gemm_launch(gw, part_ws, parts, st) : VQ_OK;
 }

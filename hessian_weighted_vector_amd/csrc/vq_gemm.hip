@@ -378,10 +378,42 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm(const 
     tile_product<T, TRP, TRQ, FP, FQ, PAIR>(a, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z, pb0, pb1, qb0, qb1);
 }
 
+// Sums of the partial rows in 64 columns: a wave every eighth row, the waves' sums in
+// wave order.  sh: 8 * 64 floats.
+constexpr int kBiasColumns = 64;
+template <class T>
+__device__ __forceinline__ void bias_columns(const BiasSum& b, int id, float* sh)
+{
+    const int blocks = (b.M + kBiasColumns - 1) / kBiasColumns, o = id / blocks;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = (id - o * blocks) * kBiasColumns + lane;
+    const float* part = o ? b.part[1] : b.part[0];
+    float s = 0.0f;
+    if (m < b.M) {
+#pragma unroll 8
+        for (int64_t r = wave; r < b.n; r += kWaves) s += part[r * b.M + m];
+    }
+    sh[wave * 64 + lane] = s;
+    __syncthreads();
+    if (wave == 0 && m < b.M) {
+        for (int k = 1; k < kWaves; ++k) s += sh[k * 64 + lane];
+        static_cast<typename T::E*>(o ? b.db[1] : b.db[0])[m] = (typename T::E)s;
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_bias_sum(const BiasSum b)
+{
+    __shared__ float sh[kWaves * 64];
+    bias_columns<T>(b, blockIdx.x, sh);
+}
+
+int bias_blocks(const BiasSum& b) { return (b.M + kBiasColumns - 1) / kBiasColumns * b.outputs; }
+
 // dX and dW of a backward pass in one launch: the tiles of one fill the CUs that the
-// other's last round would leave idle.
+// other's last round would leave idle, and the bias gradients come last.
 struct Two {
     Tile x, w;
+    BiasSum bias;
     int nx, nw;                // workgroups
     int w_first, w_batch;      // whether dW's come first; its outputs
 };
@@ -392,6 +424,10 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_gemm_two(co
     typedef Main<T, true, true, FP, FQ, false> L;
     VQ_TILE_BUFFERS(L);
     const int id = blockIdx.x, first = a.w_first ? a.nw : a.nx;
+    if (id >= a.nx + a.nw) {
+        bias_columns<T>(a.bias, id - a.nx - a.nw, reinterpret_cast<float*>(pb0));
+        return;
+    }
     const int at = id < first ? id : id - first;
     if ((id < first) != (a.w_first != 0)) {
         const int tiles = a.x.ntp * a.x.ntq;
@@ -654,8 +690,9 @@ GemmSize size_of(const GemmArgs& g) { return {g.kind, g.np, g.nq, std::min(g.kP,
 template <class T>
 vq_status launch_two(const Two& a, const Plan& px, const Plan& pw, hipStream_t st)
 {
-    if (px.fp == 8) hipLaunchKernelGGL((k_gemm_two<T, 8, 4>), dim3(a.nx + a.nw), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((k_gemm_two<T, 4, 2>), dim3(a.nx + a.nw), dim3(kThreads), 0, st, a);
+    const int blocks = a.nx + a.nw + bias_blocks(a.bias);
+    if (px.fp == 8) hipLaunchKernelGGL((k_gemm_two<T, 8, 4>), dim3(blocks), dim3(kThreads), 0, st, a);
+    else hipLaunchKernelGGL((k_gemm_two<T, 4, 2>), dim3(blocks), dim3(kThreads), 0, st, a);
     VQ_LAUNCHED("k_gemm_two");
     if (px.splits > 1) VQ_TRY(launch_finish<T>({a.x.part, px.splits, a.x.np, a.x.nq, a.x.pitch, a.x.epi, nullptr}, false, 1, st));
     if (pw.splits > 1)
@@ -681,10 +718,20 @@ size_t gemm_two_workspace(const GemmSize& x, const GemmSize& w)
     return make_plans(x, w, px, pw) ? px.part_bytes + pw.part_bytes : std::max(px.part_bytes, pw.part_bytes);
 }
 
-vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, void* ws, size_t ws_bytes, hipStream_t st)
+vq_status bias_sum_launch(int dtype, const BiasSum& b, hipStream_t st)
+{
+    if (b.outputs == 0) return VQ_OK;
+    if (dtype == VQ_BF16) hipLaunchKernelGGL((k_bias_sum<Bf16>), dim3(bias_blocks(b)), dim3(kThreads), 0, st, b);
+    else hipLaunchKernelGGL((k_bias_sum<F16>), dim3(bias_blocks(b)), dim3(kThreads), 0, st, b);
+    VQ_LAUNCHED("k_bias_sum");
+    return VQ_OK;
+}
+
+vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, const BiasSum& b, void* ws, size_t ws_bytes, hipStream_t st)
 {
     Plan px, pw;
     if (!make_plans(size_of(x), size_of(w), px, pw)) {          // one after the other, parts in the same place
+        VQ_TRY(bias_sum_launch(x.dtype, b, st));
         VQ_TRY(gemm_launch(x, ws, ws_bytes, st));
         return gemm_launch(w, ws, ws_bytes, st);
     }
@@ -696,6 +743,7 @@ vq_status gemm_two_launch(const GemmArgs& x, const GemmArgs& w, void* ws, size_t
     a.nw = pw.ntp * pw.ntq * pw.splits * w.nbatch;
     a.w_batch = w.nbatch;
     a.w_first = pw.cost > px.cost;
+    a.bias = b;
     return x.dtype == VQ_BF16 ? launch_two<Bf16>(a, px, pw, st) : launch_two<F16>(a, px, pw, st);
 }
 
