@@ -163,7 +163,7 @@ def _ptr(t):
 
 def _stream():
     # the raw handle of the current device's current stream, without a Stream object
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype(t, dt, name):
@@ -594,8 +594,8 @@ def linear(X, W, bias=None, residual=None, act="none", want_pre=False, out=None,
     w, ldw = _matrix(W, M, N, X.dtype, "W")
     b = _vector(bias, M, X.dtype, "bias")
     r, ldr = _matrix(residual, T, M, X.dtype, "residual")
-    Y = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
-    Z = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
+    Y = out if out is not None else X.new_empty((T, M))
+    Z = X.new_empty((T, M)) if want_pre else None
     y, ldy = _matrix(Y, T, M, X.dtype, "out")
     z, ldz = _matrix(Z, T, M, X.dtype, "pre")
     lib = load()
@@ -618,9 +618,9 @@ def linear_backward(dY, X, W, pre=None, act="none", want_dx=True, want_dw=True, 
     x, ldx = _matrix(X, T, N, X.dtype, "X")
     w, ldw = _matrix(W, M, N, X.dtype, "W")
     z, ldz = _matrix(pre, T, M, X.dtype, "pre")
-    dX = torch.empty((T, N), dtype=X.dtype, device=X.device) if want_dx else None
-    dW = torch.empty((M, N), dtype=X.dtype, device=X.device) if want_dw else None
-    db = torch.empty(M, dtype=X.dtype, device=X.device) if want_db else None
+    dX = X.new_empty((T, N)) if want_dx else None
+    dW = X.new_empty((M, N)) if want_dw else None
+    db = X.new_empty(M) if want_db else None
     lib = load()
     p, n, ws = _scratch(_linear_backward_need(T, M, N, a, g & 15, ldg, x & 15, ldx, w & 15, ldw, want_dx, want_dw, want_db),
                         ws, X.device)
@@ -644,10 +644,10 @@ def gated(X, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", want_pre=Fa
         raise ValueError("W_gate and W_up must have the same row stride")
     bg = _vector(bias_gate, M, X.dtype, "bias_gate")
     bu = _vector(bias_up, M, X.dtype, "bias_up")
-    H = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    H = out if out is not None else X.new_empty((T, M))
     h, ldh = _matrix(H, T, M, X.dtype, "out")
-    G = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
-    U = torch.empty((T, M), dtype=X.dtype, device=X.device) if want_pre else None
+    G = X.new_empty((T, M)) if want_pre else None
+    U = X.new_empty((T, M)) if want_pre else None
     lib = load()
     p, n, ws = _scratch(_gated_need(T, M, N, x & 15, ldx, wg & 15, wu & 15, ldw), ws, X.device)
     _check(lib.vq_gated(T, M, N, dt, a, x, ldx, wg, wu, ldw, bg, bu, h, ldh, _ptr(G), _ptr(U), M, p, n, _stream()))
@@ -668,7 +668,7 @@ def gated_backward(dH, X, W_gate, W_up, G, U, act="silu", want_dx=True, want_dw=
         raise ValueError("W_gate and W_up, and G and U, must have the same row stride")
 
     def new(on, *shape):
-        return torch.empty(shape, dtype=X.dtype, device=X.device) if on else None
+        return X.new_empty(shape) if on else None
 
     dX, dWg, dWu = new(want_dx, T, N), new(want_dw, M, N), new(want_dw, M, N)
     dbg, dbu = new(want_db, M), new(want_db, M)
@@ -751,7 +751,7 @@ def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
     x, ldx = _matrix(X, T, N, X.dtype, "X")
     b = _vector(bias, M, X.dtype, "bias")
     r, ldr = _matrix(residual, T, M, X.dtype, "residual")
-    Y = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    Y = out if out is not None else X.new_empty((T, M))
     y, ldy = _matrix(Y, T, M, X.dtype, "out")
     lib = load()
     p, n, ws = _scratch(_qlinear_need(M, N, Q.d, T), ws, X.device)
@@ -768,7 +768,7 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     x, ldx = _matrix(X, T, N, X.dtype, "X")
     bg = _vector(bias_gate, M, X.dtype, "bias_gate")
     bu = _vector(bias_up, M, X.dtype, "bias_up")
-    H = out if out is not None else torch.empty((T, M), dtype=X.dtype, device=X.device)
+    H = out if out is not None else X.new_empty((T, M))
     h, ldh = _matrix(H, T, M, X.dtype, "out")
     lib = load()
     p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X.device)
