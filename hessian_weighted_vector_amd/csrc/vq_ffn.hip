@@ -106,8 +106,10 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
     }
     __shared__ float sums[GATED ? 2 : 1][4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m = blockIdx.y * 512 + lane * 8;
-    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * R;
+    // neighbouring workgroups take neighbouring columns
+    const int ncol = (M + 511) / 512, wid = blockIdx.y * gridDim.x + blockIdx.x, by = wid % ncol, bx = wid / ncol;
+    const int m = by * 512 + lane * 8;
+    const int64_t t0 = ((int64_t)bx * 4 + wave) * R;
     float c0[8] = {}, c1[8] = {};
     if (m < M) {
         constexpr int B = R < 2 ? R : 2;                     // rows whose loads are in flight together
@@ -156,12 +158,12 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
     }
     __syncthreads();
     for (int k = threadIdx.x; k < 512; k += 256) {
-        const int col = blockIdx.y * 512 + k;
+        const int col = by * 512 + k;
         if (col >= M) break;
-        part0[(int64_t)blockIdx.x * M + col] = sums[0][0][k] + sums[0][1][k] + sums[0][2][k] + sums[0][3][k];
+        part0[(int64_t)bx * M + col] = sums[0][0][k] + sums[0][1][k] + sums[0][2][k] + sums[0][3][k];
         if (GATED) {
             constexpr int b = GATED ? 1 : 0;
-            part1[(int64_t)blockIdx.x * M + col] = sums[b][0][k] + sums[b][1][k] + sums[b][2][k] + sums[b][3][k];
+            part1[(int64_t)bx * M + col] = sums[b][0][k] + sums[b][1][k] + sums[b][2][k] + sums[b][3][k];
         }
     }
 }

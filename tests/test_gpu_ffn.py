@@ -176,6 +176,26 @@ def test_few_tokens_of_a_large_matrix():
         check("gated", (vq.gated(X, Wg, Wu),), ref.gated(X, Wg, Wu, None, None, "silu", torch.bfloat16)[:1])
 
 
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: first and last rows, and gradients over all of them."""
+    say("large offsets")
+    T, M, N = 270000, 8192, 64
+    g = torch.Generator(device="cuda").manual_seed(22)
+    X = torch.randn((T, N), generator=g, device="cuda").bfloat16()
+    W = (0.1 * torch.randn((M, N), generator=g, device="cuda")).bfloat16()
+    Y, Z = vq.linear(X, W, act="relu", want_pre=True)
+    rows = torch.tensor([0, 1, 262143, 262144, T - 2, T - 1])
+    check("rows", (Y[rows], Z[rows]), ref.linear(X[rows], W, None, None, "relu", torch.bfloat16))
+    # dY is zero but in those rows: the gradients are theirs alone
+    Y.zero_()
+    Y[rows] = torch.randn((len(rows), M), generator=g, device="cuda").bfloat16()
+    dX, dW, _ = vq.linear_backward(Y, X, W, Z, "relu")
+    want = ref.linear_backward(Y[rows], X[rows], W, Z[rows], "relu", torch.bfloat16)
+    check("dX", (dX[rows],), want[:1])
+    check("dW", (dW,), want[1:2])
+    assert int((dX != 0).any(1).sum()) == len(rows)
+
+
 def test_residual_in_place_and_reproducible():
     say("in place")
     g = torch.Generator().manual_seed(5)
