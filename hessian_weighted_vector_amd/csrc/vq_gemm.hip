@@ -460,7 +460,8 @@ __global__ __launch_bounds__(256) void k_gemm_finish(const Finish a)
     const int nout = PAIR ? 2 : gridDim.y;
     const float* o = a.part + q * a.pitch + p + b * plane;
     float s[8] = {}, u[8] = {};
-    for (int z = 0; z < a.splits; ++z) {
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) {                      // four parts in flight
         const float* oz = o + (int64_t)z * nout * plane;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

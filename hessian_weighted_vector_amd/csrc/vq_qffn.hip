@@ -559,6 +559,7 @@ __global__ __launch_bounds__(256) void k_qffn_finish(const QArgs a)
     for (int m = 0; m < 2; ++m) {
         if (m >= a.nm) break;
         float v = 0.0f;
+#pragma unroll 4
         for (int s = 0; s < a.splits; ++s) v += a.part[((int64_t)s * a.nm + m) * n + e];
         z[m] = a.bias[m] ? v + load_any(a.bias[m], row, a.dtype) : v;
     }
