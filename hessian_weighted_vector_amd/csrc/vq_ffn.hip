@@ -92,8 +92,10 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int
 // A workgroup's four waves take R rows each of 512 columns (eight a lane), and
 // their column sums join in LDS.  GATED: D0 = dG, D1 = dU.  D0 may be null (bias
 // gradient alone).  D0 and D1 have zero-padded rows of ldd.  Bound by its bytes:
-// 4096 x 8192, act'(Z) from bf16, 201 MB in 49 us (4.1 TB/s; a large copy reaches
-// 4.9); gated 2048 x 11008, 225 MB in 55 us.
+// 4096 x 8192, act'(Z) from bf16, 201 MB in 48 us (4.2 TB/s; a large copy reaches
+// 4.9); gated 2048 x 11008, 225 MB in 55 us.  Four rows in flight took 69 us there.
+// Neighbouring workgroups take neighbouring columns: whole rows come from memory
+// together (a backward call of 4096 x 8192 x 2048 279 us without, 268 with).
 template <class T, bool GATED, int R>
 __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const void* dY, int64_t ldy, const void* Z0,
                                               const void* Z1, int64_t ldz, typename T::E* D0, typename T::E* D1,
@@ -106,7 +108,6 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
     }
     __shared__ float sums[GATED ? 2 : 1][4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // neighbouring workgroups take neighbouring columns
     const int ncol = (M + 511) / 512, wid = blockIdx.y * gridDim.x + blockIdx.x, by = wid % ncol, bx = wid / ncol;
     const int m = by * 512 + lane * 8;
     const int64_t t0 = ((int64_t)bx * 4 + wave) * R;
