@@ -126,6 +126,30 @@ struct Epilogue {
     int64_t ldr, ldy, ldz;
 };
 
+// Eight 16-bit elements at any element's address.  A 16-byte load runs at full rate
+// from any multiple of four bytes and at less than half from others, so it starts at
+// the word that holds the first element, and the last element comes by itself.
+struct Words {
+    uint32_t q[4];
+    uint16_t last;
+    __device__ __forceinline__ void load(const void* p)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        __builtin_memcpy(q, __builtin_assume_aligned(reinterpret_cast<const void*>(at & ~(uintptr_t)3), 4), 16);
+        last = *reinterpret_cast<const uint16_t*>(at + 14);
+    }
+    // The elements; p as loaded from, or less by whole words.
+    __device__ __forceinline__ uint4 get(const void* p) const
+    {
+        const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(p) & 2;
+        return {__builtin_amdgcn_alignbyte(q[1], q[0], s), __builtin_amdgcn_alignbyte(q[2], q[1], s),
+                __builtin_amdgcn_alignbyte(q[3], q[2], s), __builtin_amdgcn_alignbyte(last, q[3], s)};
+    }
+};
+
+// Whether some of a matrix's rows begin at an odd element.
+inline bool odd_rows(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 2) || (ld & 1); }
+
 // Reads or writes features m .. m+7 of row t (those below M): one 16-byte access
 // where all eight exist, at any element-aligned address (the hardware takes
 // unaligned vector accesses; aligned rows run at full speed).
@@ -145,13 +169,20 @@ __device__ inline void store8(void* base, int64_t ld, int64_t t, int m, int M, c
     }
 }
 
-template <class T>
+template <class T, bool ODD = false>
 __device__ inline void load8(const void* base, int64_t ld, int64_t t, int m, int M, float (&v)[8])
 {
     const typename T::E* p = static_cast<const typename T::E*>(base) + t * ld + m;
     if (m + 8 <= M) {
         typename T::V8 w;
-        __builtin_memcpy(&w, p, 16);
+        if (ODD) {
+            Words a;
+            a.load(p);
+            const uint4 u = a.get(p);
+            __builtin_memcpy(&w, &u, 16);
+        } else {
+            __builtin_memcpy(&w, p, 16);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)w[i];
     } else {

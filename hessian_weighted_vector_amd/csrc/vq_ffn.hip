@@ -53,6 +53,7 @@ struct Pack {
     uint16_t* o;
     int64_t rows, ld, ldp;
     int cols;
+    int odd;                   // some rows begin at an odd element
 };
 struct Packs {
     Pack m[3];
@@ -71,7 +72,14 @@ __device__ __forceinline__ void pack_rows(const Pack& m, int block, int blocks)
         const uint16_t* p = m.s + r * m.ld + c;
         alignas(16) uint16_t v[8];
         if (c + 8 <= m.cols) {
-            __builtin_memcpy(v, p, 16);
+            if (m.odd) {
+                Words w;
+                w.load(p);
+                const uint4 u = w.get(p);
+                __builtin_memcpy(v, &u, 16);
+            } else {
+                __builtin_memcpy(v, p, 16);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = c + i < m.cols ? p[i] : (uint16_t)0;
@@ -96,7 +104,7 @@ __global__ __launch_bounds__(256) void k_zero_rows(uint16_t* __restrict__ o, int
 // 4.9); gated 2048 x 11008, 225 MB in 55 us.  Four rows in flight took 69 us there.
 // Neighbouring workgroups take neighbouring columns: whole rows come from memory
 // together (a backward call of 4096 x 8192 x 2048 279 us without, 268 with).
-template <class T, bool GATED, int R>
+template <class T, bool GATED, int R, bool ODD>
 __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const void* dY, int64_t ldy, const void* Z0,
                                               const void* Z1, int64_t ldz, typename T::E* D0, typename T::E* D1,
                                               int64_t ldd, float* part0, float* part1, const Packs packs)
@@ -120,9 +128,9 @@ __global__ __launch_bounds__(256) void k_grad(int64_t nt, int M, int act, const 
 #pragma unroll
             for (int k = 0; k < B; ++k) {
                 const int64_t t = t0 + r + k < nt ? t0 + r + k : nt - 1;
-                load8<T>(dY, ldy, t, m, M, dy[k]);
-                if (GATED || act != VQ_ACT_NONE) load8<T>(Z0, ldz, t, m, M, z[k]);
-                if (GATED) load8<T>(Z1, ldz, t, m, M, u[k]);
+                load8<T, ODD>(dY, ldy, t, m, M, dy[k]);
+                if (GATED || act != VQ_ACT_NONE) load8<T, ODD>(Z0, ldz, t, m, M, z[k]);
+                if (GATED) load8<T, ODD>(Z1, ldz, t, m, M, u[k]);
             }
 #pragma unroll
             for (int k = 0; k < B; ++k) {
@@ -184,7 +192,8 @@ struct Packer {
     {
         const int64_t ldp = round8(m.cols);
         void* o = ws.take((size_t)m.rows * ldp * 2);
-        list.m[list.count++] = {static_cast<const uint16_t*>(m.p), static_cast<uint16_t*>(o), m.rows, m.ld, ldp, (int)m.cols};
+        list.m[list.count++] = {static_cast<const uint16_t*>(m.p), static_cast<uint16_t*>(o), m.rows, m.ld, ldp, (int)m.cols,
+                                odd_rows(m.p, m.ld)};
         most = std::max(most, m.rows * (ldp / 8));
         list.blocks = (int)std::min<int64_t>((most + 255) / 256, 16384);
         m = {o, m.rows, ldp, ldp};
@@ -270,13 +279,20 @@ vq_status grad_launch(const Backward& b, void* const (&D)[2], int64_t ldd, float
     const int rows = grad_rows(b.T, b.M);
     const int64_t gx = (b.T + rows - 1) / rows, copies = ((int64_t)packs.blocks * packs.count + gx - 1) / gx;
     const dim3 grid((unsigned)gx, (unsigned)((b.M + 511) / 512 + copies));
-#define VQ_GRAD(GATED_, R_)                                                                                          \
-    hipLaunchKernelGGL((k_grad<T, GATED_, R_>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0],     \
+#define VQ_GRAD(GATED_, R_, ODD_)                                                                                    \
+    hipLaunchKernelGGL((k_grad<T, GATED_, R_, ODD_>), grid, dim3(256), 0, st, b.T, (int)b.M, b.act, b.dY, b.lddy, b.Z[0], \
                        b.Z[1], b.ldz, (E*)D[0], (E*)D[1], ldd, part[0], part[1], packs)
-    if (b.nm > 1 && rows == 32) VQ_GRAD(true, 8);
-    else if (b.nm > 1) VQ_GRAD(true, 1);
-    else if (rows == 32) VQ_GRAD(false, 8);
-    else VQ_GRAD(false, 1);
+#define VQ_GRAD_ROWS(GATED_, ODD_)           \
+    do {                                     \
+        if (rows == 32) VQ_GRAD(GATED_, 8, ODD_); \
+        else VQ_GRAD(GATED_, 1, ODD_);       \
+    } while (0)
+    const bool odd = odd_rows(b.dY, b.lddy) || (b.Z[0] && odd_rows(b.Z[0], b.ldz)) || (b.Z[1] && odd_rows(b.Z[1], b.ldz));
+    if (b.nm > 1 && odd) VQ_GRAD_ROWS(true, true);
+    else if (b.nm > 1) VQ_GRAD_ROWS(true, false);
+    else if (odd) VQ_GRAD_ROWS(false, true);
+    else VQ_GRAD_ROWS(false, false);
+#undef VQ_GRAD_ROWS
 #undef VQ_GRAD
     VQ_LAUNCHED("k_grad");
     return VQ_OK;
