@@ -129,28 +129,57 @@ __device__ inline void store_any(void* p, int64_t i, int dtype, float v)
     else static_cast<_Float16*>(p)[i] = (_Float16)v;
 }
 
-// Eight indices from sub-vector s of a row of nb, two to a register, at most top (two
-// copies of K - 1); past the row's end 0.
-__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, uint32_t top, uint32_t (&k)[4])
+// Eight indices from sub-vector s of a row of nb, as they are loaded ahead; past the
+// row's end 0.  odd: whether some rows begin at an odd index.
+__device__ inline void load_indices(const uint16_t* row, int64_t s, int64_t nb, bool odd, Words& k)
+{
+    if (s + 8 <= nb && !odd) {
+        __builtin_memcpy(k.q, row + s, 16);
+    } else if (s + 8 <= nb) {
+        k.load(row + s);
+    } else {
+        uint16_t v[9] = {};                            // as Words: from the word that holds the first
+        const bool from = odd && (reinterpret_cast<uintptr_t>(row) & 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t e = s + i < nb ? row[s + i] : (uint16_t)0;
+            v[i] = from ? v[i] : e;
+            v[i + 1] = from ? e : v[i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k.q[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
+        k.last = v[8];
+    }
+}
+
+// They, two to a register, at most top (two copies of K - 1).
+__device__ inline void take_indices(const Words& w, const uint16_t* row, bool odd, uint32_t top, uint32_t (&k)[4])
 {
     typedef uint16_t U2 __attribute__((ext_vector_type(2)));
-    if (s + 8 <= nb) {
-        __builtin_memcpy(k, row + s, 16);
-    } else {
-        uint16_t v[8] = {};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (s + i < nb) v[i] = row[s + i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
+    uint32_t v[4] = {w.q[0], w.q[1], w.q[2], w.q[3]};
+    if (odd) {
+        const uint4 u = w.get(row);
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        k[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(U2, k[i]), __builtin_bit_cast(U2, top)));
+        k[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(U2, v[i]), __builtin_bit_cast(U2, top)));
 }
 
 // Index j of them.
 __device__ inline uint32_t index_of(const uint32_t (&k)[4], int j) { return j & 1 ? k[j >> 1] >> 16 : k[j >> 1] & 0xffffu; }
+
+// Elements 4 .. 7 of a row of d >= 4, zeros past it, from its last four.
+__device__ inline void tail_of(const float (&last)[4], int d, float (&w)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = 0.0f;                              // element 4 + i is last[8 - d + i]
+#pragma unroll
+        for (int q = i; q < 4; ++q) v = q - i == 8 - d ? last[q] : v;
+        w[4 + i] = v;
+    }
+}
 
 // Row k of a codebook of any d <= 8, zero padded to eight: two (overlapping)
 // four-element loads inside the row for d >= 4.
@@ -162,13 +191,8 @@ __device__ inline void load_row(const float* C, uint32_t k, int d, float (&w)[8]
         __builtin_memcpy(a, row, 16);
         __builtin_memcpy(b, row + d - 4, 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = a[i];
-            float v = 0.0f;                          // element 4 + i is b[8 - d + i]
-#pragma unroll
-            for (int q = i; q < 4; ++q) v = q - i == 8 - d ? b[q] : v;
-            w[4 + i] = v;
-        }
+        for (int i = 0; i < 4; ++i) w[i] = a[i];
+        tail_of(b, d, w);
     } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -243,11 +267,17 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
     const int kb0 = (int)((int64_t)nkb * blockIdx.y / a.splits), kb1 = (int)((int64_t)nkb * (blockIdx.y + 1) / a.splits);
     const int slab_blocks = a.slab / kBlock;
     const uint32_t top1 = (uint32_t)(q.K1 - 1) * 0x10001u, top2 = q.C2 ? (uint32_t)(q.K2 - 1) * 0x10001u : 0;
-    uint32_t i1[4], i2[4] = {};
+    const bool odd1 = (reinterpret_cast<uintptr_t>(q.idx1) & 2) || (a.nb & 1);
+    const bool odd2 = (reinterpret_cast<uintptr_t>(q.idx2) & 2) || (a.nb & 1);
+    // d = 5 to 7: whether neighbouring lanes share rows (one request each, more
+    // instructions).  One token by 4096 x 11010, d = 6, K1 = 65536: 48 us shared,
+    // 52 not; two by 1133 x 14616, K1 = 197 (in L1): 28 and 26 us.
+    const bool share = D == 0 && d >= 5 && q.K1 * d > 16384;
+    Words i1, i2 = {};
     const auto load_block = [&](int kb) {
         const int64_t s = (int64_t)kb * kBlock + g * 8;
-        load_indices(q.idx1 + row * a.nb, s, a.nb, top1, i1);
-        if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, top2, i2);
+        load_indices(q.idx1 + row * a.nb, s, a.nb, odd1, i1);
+        if (q.C2) load_indices(q.idx2 + row * a.nb, s, a.nb, odd2, i2);
     };
 
     const int item = threadIdx.x;
@@ -361,11 +391,8 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
 #pragma unroll 1
         for (int kb = sb + turn; kb < se; kb += turns) {
             uint32_t k1[4], k2[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                k1[i] = i1[i];
-                k2[i] = i2[i];
-            }
+            take_indices(i1, q.idx1 + row * a.nb, odd1, top1, k1);       // blocks keep the row's parity
+            take_indices(i2, q.idx2 + row * a.nb, odd2, top2, k2);
             if (kb + turns < se) load_block(kb + turns);
             int c0 = ((kb - sb) * kBlock + g * 8) * S;         // the lane's first column in the slab
 #pragma unroll 1
@@ -399,6 +426,27 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) w[j][u * 4 + i] = v[i];
                         }
+                } else if (share) {
+                    // as with d = 8, by the row's first and last four elements
+                    const int odd = lane & 1;
+                    float ga[H][4], gb[H][4];
+#pragma unroll
+                    for (int j = 0; j < H; ++j) {
+                        const int mine = index_of(k1, j), other = swap_pair(mine);
+                        __builtin_memcpy(ga[j], q.C1 + (uint32_t)((odd ? other : mine) * d + odd * (d - 4)), 16);
+                        __builtin_memcpy(gb[j], q.C1 + (uint32_t)((odd ? mine : other) * d + odd * (d - 4)), 16);
+                    }
+#pragma unroll
+                    for (int j = 0; j < H; ++j) {
+                        float last[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float other = swap_pair(odd ? ga[j][i] : gb[j][i]);
+                            w[j][i] = odd ? other : ga[j][i];
+                            last[i] = odd ? gb[j][i] : other;
+                        }
+                        tail_of(last, d, w[j]);
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < H; ++j) load_row(q.C1, index_of(k1, j), d, w[j]);

@@ -174,6 +174,24 @@ def test_misaligned_codebooks_strided_tokens_full_rows(d):
         check("strided out", out, z, e, dtype)
 
 
+@pytest.mark.parametrize("d,nb", [(8, 34), (8, 35), (4, 70), (4, 37), (6, 33), (6, 40), (7, 8), (5, 3)])
+def test_indices_at_odd_addresses(d, nb):
+    """Index rows that begin at odd elements, by their number or by their array's address; a codebook above and below L1's size."""
+    say("odd index rows, d =", d, "nb =", nb)
+    g = np.random.default_rng([83, d, nb])
+    for K1 in (30, min(5000, 150 * nb)):
+        q = make_matrix(g, 150, d * nb, d, K1, 20, False, 2)
+        X = tokens(g, 2, d * nb, torch.float32)
+        z, e = sums(q, X, torch.float32)
+        t = {k: dev(v) if isinstance(v, np.ndarray) else v for k, v in q.items()}
+        check("as they are", vq.qlinear(vq.QMatrix(**t), X), z, e, torch.float32)
+        for k in ("idx1", "idx2"):
+            buf = torch.zeros(t[k].numel() + 1, dtype=torch.uint16, device="cuda")
+            buf[1:] = t[k]
+            t[k] = buf[1:]
+        check("shifted", vq.qlinear(vq.QMatrix(**t), X), z, e, torch.float32)
+
+
 def test_matrices_of_a_pair_may_differ():
     """One with a residual stage in memory, scales and a sparse part, one without any."""
     say("differing pair")
