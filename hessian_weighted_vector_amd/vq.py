@@ -526,6 +526,14 @@ def _matrix(t, rows, cols, dtype, name):
     return t.data_ptr(), s0
 
 
+def _output(out, X, rows, cols, name="out"):
+    """(tensor, pointer, leading dimension) of a caller's output or of a new one of X's type."""
+    if out is None:
+        out = X.new_empty((rows, cols))
+        return out, out.data_ptr(), cols
+    return (out,) + _matrix(out, rows, cols, X.dtype, name)
+
+
 def _vector(t, n, dtype, name):
     if t is None:
         return None
@@ -594,10 +602,8 @@ def linear(X, W, bias=None, residual=None, act="none", want_pre=False, out=None,
     w, ldw = _matrix(W, M, N, X.dtype, "W")
     b = _vector(bias, M, X.dtype, "bias")
     r, ldr = _matrix(residual, T, M, X.dtype, "residual")
-    Y = out if out is not None else X.new_empty((T, M))
-    Z = X.new_empty((T, M)) if want_pre else None
-    y, ldy = _matrix(Y, T, M, X.dtype, "out")
-    z, ldz = _matrix(Z, T, M, X.dtype, "pre")
+    Y, y, ldy = _output(out, X, T, M)
+    Z, z, ldz = _output(None, X, T, M) if want_pre else (None, None, 0)
     lib = load()
     p, n, ws = _scratch(_linear_need(T, M, N, x & 15, ldx, w & 15, ldw), ws, X.device)
     _check(lib.vq_linear(T, M, N, dt, a, x, ldx, w, ldw, b, r, ldr, y, ldy, z, ldz, p, n, _stream()))
@@ -644,8 +650,7 @@ def gated(X, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", want_pre=Fa
         raise ValueError("W_gate and W_up must have the same row stride")
     bg = _vector(bias_gate, M, X.dtype, "bias_gate")
     bu = _vector(bias_up, M, X.dtype, "bias_up")
-    H = out if out is not None else X.new_empty((T, M))
-    h, ldh = _matrix(H, T, M, X.dtype, "out")
+    H, h, ldh = _output(out, X, T, M)
     G = X.new_empty((T, M)) if want_pre else None
     U = X.new_empty((T, M)) if want_pre else None
     lib = load()
@@ -751,8 +756,7 @@ def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
     x, ldx = _matrix(X, T, N, X.dtype, "X")
     b = _vector(bias, M, X.dtype, "bias")
     r, ldr = _matrix(residual, T, M, X.dtype, "residual")
-    Y = out if out is not None else X.new_empty((T, M))
-    y, ldy = _matrix(Y, T, M, X.dtype, "out")
+    Y, y, ldy = _output(out, X, T, M)
     lib = load()
     p, n, ws = _scratch(_qlinear_need(M, N, Q.d, T), ws, X.device)
     _check(lib.vq_qlinear(Q._ref, T, dt, a, x, ldx, b, r, ldr, y, ldy, p, n, _stream()))
@@ -768,8 +772,7 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     x, ldx = _matrix(X, T, N, X.dtype, "X")
     bg = _vector(bias_gate, M, X.dtype, "bias_gate")
     bu = _vector(bias_up, M, X.dtype, "bias_up")
-    H = out if out is not None else X.new_empty((T, M))
-    h, ldh = _matrix(H, T, M, X.dtype, "out")
+    H, h, ldh = _output(out, X, T, M)
     lib = load()
     p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X.device)
     _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
