@@ -105,7 +105,11 @@ __device__ inline void act_grad(int act, float (&z)[8], float (&a)[8])
         VQ_EACH(const float q = v * v; const float s = logistic_fast(2.0f * kGeluC * v * (1.0f + kGeluA * q)); val = v * s;
                 der = s + val * (1.0f - s) * (2.0f * kGeluC) * (1.0f + 3.0f * kGeluA * fminf(q, 1e6f)))
         break;
-    case VQ_ACT_SIGMOID: VQ_EACH(const float s = logistic_fast(v); val = s; der = s * (1.0f - s)) break;
+    case VQ_ACT_SIGMOID:
+        // the derivative is even, and from e = exp(-|v|) nothing cancels: e / (1 + e)^2
+        VQ_EACH(const float e = __expf(-fabsf(v)); const float s = __builtin_amdgcn_rcpf(1.0f + e); val = v < 0.0f ? e * s : s;
+                der = e * s * s)
+        break;
     default: VQ_EACH(val = v; der = 1.0f)
     }
 #undef VQ_EACH

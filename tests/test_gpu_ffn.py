@@ -350,3 +350,33 @@ def test_input_check_names_the_array(monkeypatch):
         W[3, 29] = float("inf")
         with pytest.raises(vq.VQError, match="W holds 1 non-finite"):
             vq.linear(X, W)
+
+
+def exact_to_rounding(got, want, dtype, arg):
+    """Each element within its own rounding of want: u, the hardware exponential's error (2^-23 of the value for each
+    unit of its argument, and a few more), or half the smallest subnormal.  No share of any other value."""
+    off = (ref.f64(got) - want).abs()
+    bound = want.abs() * (ref.UNIT[dtype] + (8 + arg.abs()) * 2.0 ** -23) + ref.TINY[dtype]
+    say("   max error / bound = %.3g" % float((off / bound).max()))
+    return bool((off <= bound).all())
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_sigmoid_gradient_far_from_zero(dt):
+    """The derivative sigma(z) sigma(-z) to its own rounding on both sides of zero, where 1 - sigma(z) has no bits left."""
+    say("sigmoid gradient", dt)
+    dtype = DT[dt]
+    z = torch.tensor([v for a in (0.5, 4, 8, 9.5, 10, 12, 13, 14, 15, 16, 16.5, 17, 18, 20, 24) for v in (a, -a)],
+                     dtype=torch.float64)
+    n = len(z)
+    X = torch.eye(n, dtype=dtype, device="cuda")
+    W = torch.zeros((1, n), dtype=dtype, device="cuda")
+    one = torch.ones((n, 1), dtype=dtype, device="cuda")
+    Z = z.to(dtype).cuda()[:, None].contiguous()
+    want, half = torch.sigmoid(z) * torch.sigmoid(-z), torch.full((n, 1), 0.5, dtype=dtype, device="cuda")
+    # row t of dW is dZ of token t alone
+    _, dW, _ = vq.linear_backward(one, X, W, pre=Z, act="sigmoid", want_dx=False)
+    assert exact_to_rounding(dW[0], want, dtype, z)
+    _, dWg, dWu, _, _ = vq.gated_backward(one, X, W, W.clone(), Z, half, act="sigmoid", want_dx=False)
+    assert exact_to_rounding(dWg[0], 0.5 * want, dtype, z)
+    assert exact_to_rounding(dWu[0], torch.sigmoid(z), dtype, z)
