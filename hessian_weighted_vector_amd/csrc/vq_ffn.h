@@ -83,7 +83,7 @@ __device__ inline float act_full(int act, float z)
 }
 
 // z -> act'(z) and, where wanted, a = act(z), of eight values.  ReLU's derivative at
-// 0 is 0.
+// 0 is 0; NaN stays NaN in both.
 template <bool VALUE>
 __device__ inline void act_grad(int act, float (&z)[8], float (&a)[8])
 {
@@ -97,7 +97,7 @@ __device__ inline void act_grad(int act, float (&z)[8], float (&a)[8])
         if (VALUE) a[i] = val;                        \
     }
     switch (act) {
-    case VQ_ACT_RELU: VQ_EACH(val = v > 0.0f ? v : 0.0f; der = v > 0.0f ? 1.0f : 0.0f) break;
+    case VQ_ACT_RELU: VQ_EACH(val = v > 0.0f ? v : (v <= 0.0f ? 0.0f : v); der = v > 0.0f ? 1.0f : val) break;
     case VQ_ACT_SILU: VQ_EACH(const float s = logistic_fast(v); val = v * s; der = s * (1.0f + v * (1.0f - s))) break;
     case VQ_ACT_GELU: VQ_EACH(const float c = normal_cdf(v); val = v * c; der = c + v * kInvSqrt2Pi * __expf(-0.5f * v * v)) break;
     case VQ_ACT_GELU_TANH:

@@ -380,3 +380,30 @@ def test_sigmoid_gradient_far_from_zero(dt):
     _, dWg, dWu, _, _ = vq.gated_backward(one, X, W, W.clone(), Z, half, act="sigmoid", want_dx=False)
     assert exact_to_rounding(dWg[0], 0.5 * want, dtype, z)
     assert exact_to_rounding(dWu[0], torch.sigmoid(z), dtype, z)
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+def test_nan_pre_activations_reach_the_gradients(name):
+    """A NaN that the forward pass kept makes NaN of every gradient whose sums it enters, and of no other."""
+    say("NaN pre-activation", name)
+    T, M, N = 9, 40, 24
+    g = torch.Generator().manual_seed(23)
+    X, dY = tensor(g, (T, N), torch.bfloat16), tensor(g, (T, M), torch.bfloat16)
+    Wg, Wu = (tensor(g, (M, N), torch.bfloat16) for _ in range(2))
+    G, U = (tensor(g, (T, M), torch.bfloat16) for _ in range(2))
+    clean = vq.gated_backward(dY, X, Wg, Wu, G, U, act=name, want_db=True)
+    G[4, 7] = float("nan")
+    row = torch.arange(T, device="cuda")[:, None] == 4
+    col = torch.arange(M, device="cuda") == 7
+    got = vq.gated_backward(dY, X, Wg, Wu, G, U, act=name, want_db=True)
+    # with act "none" the derivative is 1 whatever G is: dG does not depend on it
+    into_g = name != "none"
+    bad = (row, col[:, None] & into_g, col[:, None], col & into_g, col)
+    for k, (o, c, b) in enumerate(zip(got, clean, bad)):
+        b = b.expand_as(o)
+        assert torch.equal(torch.isnan(o), b), (name, k)
+        assert torch.equal(o[~b].view(torch.int16), c[~b].view(torch.int16)), (name, k)
+    if name != "none":
+        dX, dW, db = vq.linear_backward(dY, X, Wg, pre=G, act=name, want_db=True)
+        for o, b in ((dX, row), (dW, col[:, None]), (db, col)):
+            assert torch.equal(torch.isnan(o), b.expand_as(o)), name
