@@ -9,6 +9,16 @@ namespace vq {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// A call's workspace: large enough, and where one is needed on a 16-byte boundary, since
+// its parts and copies are written and read 16 bytes at a time.
+inline vq_status check_workspace(const char* call, const void* ws, size_t ws_bytes, size_t need)
+{
+    if (need == 0) return VQ_OK;
+    VQ_WS(ws && ws_bytes >= need, std::string(call) + ": workspace too small");
+    VQ_CHECK(aligned16(ws), std::string(call) + ": workspace is not 16-byte aligned");
+    return VQ_OK;
+}
+
 // 16-bit element types: storage E, vectors of four and eight, and the
 // 16 x 16 x 32 matrix instruction with float32 accumulation.  Stores round to
 // nearest even once, from float32.

@@ -433,15 +433,15 @@ vq_status vq_linear(int64_t T, int64_t M, int64_t N, int dtype, int act, const v
     VQ_TRY(check_ld(call, "Z", Z, ldz, M));
     VQ_CHECK(Y != X && Y != W && Y != Z && (!Z || (Z != X && Z != W && Z != R)), "vq_linear: outputs may not alias inputs");
     VQ_CHECK(Y != R || ldy == ldr, "vq_linear: Y in place of R needs R's leading dimension");
+    Forward f{T, M, N, dtype, 1, X, ldx, {W, nullptr}, ldw, {act, {bias, nullptr}, R, Y, {Z, nullptr}, ldr, ldy, ldz}};
+    Arena a{nullptr};
+    VQ_TRY(forward(f, a, false, as_stream(stream)));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, a.used));
     VQ_TRY(check_device());
     VQ_MATRIX(X, T, N, ldx, call, "X");
     VQ_MATRIX(W, M, N, ldw, call, "W");
     VQ_MATRIX(bias, 1, M, M, call, "bias");
     VQ_MATRIX(R, T, M, ldr, call, "R");
-    Forward f{T, M, N, dtype, 1, X, ldx, {W, nullptr}, ldw, {act, {bias, nullptr}, R, Y, {Z, nullptr}, ldr, ldy, ldz}};
-    Arena a{nullptr};
-    VQ_TRY(forward(f, a, false, as_stream(stream)));
-    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_linear: workspace too small");
     TimedRegion tr("linear", 0, as_stream(stream));
     Arena w{static_cast<char*>(ws)};
     return forward(f, w, true, as_stream(stream));
@@ -476,16 +476,16 @@ vq_status vq_gated(int64_t T, int64_t M, int64_t N, int dtype, int act, const vo
     for (const void* o : {(const void*)H, (const void*)G, (const void*)U})
         VQ_CHECK(!o || (o != X && o != Wg && o != Wu), "vq_gated: outputs may not alias inputs");
     VQ_CHECK(H != G && H != U && (!G || G != U), "vq_gated: outputs may not alias each other");
+    Forward f{T, M, N, dtype, 2, X, ldx, {Wg, Wu}, ldw, {act, {bg, bu}, nullptr, H, {G, U}, 0, ldh, ldz}};
+    Arena a{nullptr};
+    VQ_TRY(forward(f, a, false, as_stream(stream)));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, a.used));
     VQ_TRY(check_device());
     VQ_MATRIX(X, T, N, ldx, call, "X");
     VQ_MATRIX(Wg, M, N, ldw, call, "Wg");
     VQ_MATRIX(Wu, M, N, ldw, call, "Wu");
     VQ_MATRIX(bg, 1, M, M, call, "bg");
     VQ_MATRIX(bu, 1, M, M, call, "bu");
-    Forward f{T, M, N, dtype, 2, X, ldx, {Wg, Wu}, ldw, {act, {bg, bu}, nullptr, H, {G, U}, 0, ldh, ldz}};
-    Arena a{nullptr};
-    VQ_TRY(forward(f, a, false, as_stream(stream)));
-    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_gated: workspace too small");
     TimedRegion tr("gated", 0, as_stream(stream));
     Arena w{static_cast<char*>(ws)};
     return forward(f, w, true, as_stream(stream));
@@ -522,16 +522,16 @@ vq_status vq_linear_backward(int64_t T, int64_t M, int64_t N, int dtype, int act
     VQ_TRY(check_ld(call, "db", db, M, M));
     for (const void* o : {(const void*)dX, (const void*)dW, (const void*)db})
         VQ_CHECK(!o || (o != dY && o != X && o != W && o != Z), "vq_linear_backward: outputs may not alias inputs");
+    Backward b{T, M, N, dtype, act, 1, dY, lddy, X, ldx, {W, nullptr}, ldw, {act != VQ_ACT_NONE ? Z : nullptr, nullptr}, ldz,
+               dX, lddx, {dW, nullptr}, lddw, {db, nullptr}};
+    Arena a{nullptr};
+    VQ_TRY(backward(b, a, false, as_stream(stream)));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, a.used));
     if (T > 0 || dW || db) VQ_TRY(check_device());
     VQ_MATRIX(dY, T, M, lddy, call, "dY");
     if (dW) VQ_MATRIX(X, T, N, ldx, call, "X");
     if (dX) VQ_MATRIX(W, M, N, ldw, call, "W");
     if (act != VQ_ACT_NONE) VQ_MATRIX(Z, T, M, ldz, call, "Z");
-    Backward b{T, M, N, dtype, act, 1, dY, lddy, X, ldx, {W, nullptr}, ldw, {act != VQ_ACT_NONE ? Z : nullptr, nullptr}, ldz,
-               dX, lddx, {dW, nullptr}, lddw, {db, nullptr}};
-    Arena a{nullptr};
-    VQ_TRY(backward(b, a, false, as_stream(stream)));
-    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_linear_backward: workspace too small");
     TimedRegion tr("linear_backward", 0, as_stream(stream));
     Arena w{static_cast<char*>(ws)};
     return backward(b, w, true, as_stream(stream));
@@ -577,6 +577,10 @@ vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act,
     for (const void* o : {(const void*)dX, (const void*)dWg, (const void*)dWu, (const void*)dbg, (const void*)dbu})
         VQ_CHECK(!o || (o != dH && o != X && o != Wg && o != Wu && o != G && o != U),
                  "vq_gated_backward: outputs may not alias inputs");
+    Backward b{T, M, N, dtype, act, 2, dH, lddh, X, ldx, {Wg, Wu}, ldw, {G, U}, ldz, dX, lddx, {dWg, dWu}, lddw, {dbg, dbu}};
+    Arena a{nullptr};
+    VQ_TRY(backward(b, a, false, as_stream(stream)));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, a.used));
     if (T > 0 || dWg || dbg) VQ_TRY(check_device());
     VQ_MATRIX(dH, T, M, lddh, call, "dH");
     if (dWg) VQ_MATRIX(X, T, N, ldx, call, "X");
@@ -584,10 +588,6 @@ vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act,
     if (dX) VQ_MATRIX(Wu, M, N, ldw, call, "Wu");
     VQ_MATRIX(G, T, M, ldz, call, "G");
     VQ_MATRIX(U, T, M, ldz, call, "U");
-    Backward b{T, M, N, dtype, act, 2, dH, lddh, X, ldx, {Wg, Wu}, ldw, {G, U}, ldz, dX, lddx, {dWg, dWu}, lddw, {dbg, dbu}};
-    Arena a{nullptr};
-    VQ_TRY(backward(b, a, false, as_stream(stream)));
-    VQ_WS(a.used == 0 || (ws && ws_bytes >= a.used), "vq_gated_backward: workspace too small");
     TimedRegion tr("gated_backward", 0, as_stream(stream));
     Arena w{static_cast<char*>(ws)};
     return backward(b, w, true, as_stream(stream));

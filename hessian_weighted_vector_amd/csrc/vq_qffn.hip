@@ -850,7 +850,7 @@ vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const v
     VQ_CHECK(!R || ldr >= Q->M, "vq_qlinear: leading dimension of R is below its row length");
     VQ_CHECK(Y != R || ldy == ldr, "vq_qlinear: Y in place of R needs R's leading dimension");
     const size_t need = q_workspace(Q->M, Q->N / Q->d, T, 1);
-    VQ_WS(need == 0 || (ws && ws_bytes >= need), "vq_qlinear: workspace too small");
+    VQ_TRY(check_workspace(call, ws, ws_bytes, need));
     VQ_TRY(check_device());
     VQ_TRY(check_qvalues(call, Q, as_stream(stream)));
     VQ_TRY(check_matrix(X, T, Q->N, ldx, dtype, call, "X", as_stream(stream)));
@@ -883,7 +883,7 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
     VQ_CHECK(Qg->M == Qu->M && Qg->N == Qu->N && Qg->d == Qu->d, "vq_qgated: the matrices differ in M, N or d");
     if (T == 0) return VQ_OK;
     const size_t need = q_workspace(Qg->M, Qg->N / Qg->d, T, 2);
-    VQ_WS(need == 0 || (ws && ws_bytes >= need), "vq_qgated: workspace too small");
+    VQ_TRY(check_workspace(call, ws, ws_bytes, need));
     VQ_TRY(check_device());
     VQ_TRY(check_qvalues(call, Qg, as_stream(stream)));
     VQ_TRY(check_qvalues(call, Qu, as_stream(stream)));

@@ -429,7 +429,9 @@ double vq_bits_per_weight_grouped(const vq_grouped_params* p);
  * (same address and leading dimension).  Non-finite inputs spread into the
  * outputs whose sums they enter and no others.  The workspace queries take the
  * same sizes, addresses and leading dimensions as the call (addresses for
- * their alignment alone) and return 0 for sizes that the call rejects. */
+ * their alignment alone) and return 0 for sizes that the call rejects.  A
+ * workspace begins at a multiple of 16 bytes; where the query returns 0 it may
+ * be NULL. */
 
 /* Y = act(X W^T + bias) + R:  X [T x N], W [M x N], bias [M] (nullable), R [T x M]
  * (nullable), Y [T x M].  Z (nullable) [T x M] receives X W^T + bias, which
@@ -507,7 +509,8 @@ vq_status vq_sparse_delta(const vq_qmatrix* Q, const float* val, float* delta, v
  * scaled W, each sum is within ((N + nnz_i + 64) * 2^-23 + eps) * S of exact,
  * eps = 2^-16 for the 16-bit types (the decoded weights enter as two bf16 terms)
  * and 2^-22 for float32 (three terms).  Bitwise reproducible for fixed
- * arguments.  Every 32 tokens are one pass over the matrix. */
+ * arguments.  Every 32 tokens are one pass over the matrix.  The workspace is
+ * as in the dense calls. */
 size_t vq_qlinear_workspace_bytes(int64_t M, int64_t N, int d, int64_t T);
 vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const void* X, int64_t ldx,
                      const void* bias, const void* R, int64_t ldr, void* Y, int64_t ldy,

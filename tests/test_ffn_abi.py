@@ -171,3 +171,33 @@ def test_qmatrix_checks():
         vq.QMatrix(32, 64, 8, C1, idx, C2=C1)
     with pytest.raises(ValueError, match="GPU"):
         vq.QMatrix(32, 64, 8, C1, idx)
+
+
+def test_workspaces_off_16_bytes_are_refused():
+    """Parts and copies in the workspace are accessed 16 bytes at a time: an odd base is an error, before any launch."""
+    import ctypes
+    lib = vq.load()
+    T = M = N = 512
+    A, B, C, D, E = (FAKE + (k << 24) for k in range(5))
+    F, G, H = (FAKE + (k << 24) for k in range(5, 8))
+    ld = 513                                  # odd rows: every operand is copied
+    n = 1 << 30
+    q = qmatrix(M=32, N=65536)                # rows split over workgroups
+
+    calls = {
+        "vq_linear": lambda ws: lib.vq_linear(T, M, N, BF16, 2, A, ld, B, ld, None, None, 0, C, M, None, 0, ws, n, None),
+        "vq_gated": lambda ws: lib.vq_gated(T, M, N, BF16, 2, A, ld, B, C, ld, None, None, D, M, None, None, 0, ws, n, None),
+        "vq_linear_backward": lambda ws: lib.vq_linear_backward(T, M, N, F16, 2, A, ld, B, ld, C, ld, D, ld, E, N, F, N, None,
+                                                                ws, n, None),
+        "vq_gated_backward": lambda ws: lib.vq_gated_backward(T, M, N, F16, 2, A, ld, B, ld, C, D, ld, E, F, ld, G, N, H, A + 64,
+                                                              N, None, None, ws, n, None),
+        "vq_qlinear": lambda ws: lib.vq_qlinear(ctypes.byref(q), 4, F32, 0, A, 65536, None, None, 0, B, 32, ws, n, None),
+        "vq_qgated": lambda ws: lib.vq_qgated(ctypes.byref(q), ctypes.byref(q), 4, F32, 0, A, 65536, None, None, B, 32, ws, n,
+                                              None),
+    }
+    for name, call in calls.items():
+        for off in (1, 2, 4, 8, 20):
+            assert call((1 << 36) + off) == vq.VQ_ERR_INVALID, (name, off)
+            text = lib.vq_last_error().decode()
+            assert text.startswith(name) and "16-byte aligned" in text, (name, off, text)
+        assert call(None) == vq.VQ_ERR_WORKSPACE, name
