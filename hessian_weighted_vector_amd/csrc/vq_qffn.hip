@@ -9,11 +9,14 @@
 // sub-vector of d = 8 (two of d = 4; one of another length padded with zeros):
 // the lane gathers its centroid row, adds the residual row, multiplies by the
 // column scales and splits the float32 values into bf16 terms hi + lo (+
-// lowest), each the rounding of what the terms before leave.  The tokens are
-// split alike (bf16 tokens are one term, fp16 two, float32 three), and the
-// products of terms down to 2^-18 (16-bit results) or 2^-27 (float32 results)
-// of the leading one are summed in float32.  Sixteen tokens cost the gathers of
-// one.
+// lowest), each the rounding of what the terms before leave; the tokens are split
+// alike (bf16 tokens are one term, fp16 two, float32 three, without a remainder).
+// Of a value v the second term is at most 2^-8 v and the third 2^-17 v; two terms
+// leave at most 2^-17 v, three nothing (24 bits).  With 16-bit tokens every
+// product of a token's and a weight's terms is summed, in float32: what is missing
+// is at most 2^-17 |w x|.  With float32 tokens the products of the second with the
+// third terms and of the third terms are left out, at most 2^-23 |w x|.  Sixteen
+// tokens cost the gathers of one.
 //
 // What bounds it is the requests from L1 to L2: each sub-vector is one, to a
 // random line, and at 0.42 a clock and CU the L2 channels of a die (16 for 32 CUs)
@@ -78,10 +81,11 @@ struct QArgs {
     float* part;               // [splits][matrices][T][M], or null
 };
 
+// kOrders: products of term p of a weight and term k of a token are summed for p + k below it.
 template <int XT> struct XType;
-template <> struct XType<VQ_BF16> { typedef __bf16 E; static constexpr int kTerms = 1, kWTerms = 2; };
-template <> struct XType<VQ_F16> { typedef _Float16 E; static constexpr int kTerms = 2, kWTerms = 2; };
-template <> struct XType<VQ_F32> { typedef float E; static constexpr int kTerms = 3, kWTerms = 3; };
+template <> struct XType<VQ_BF16> { typedef __bf16 E; static constexpr int kTerms = 1, kWTerms = 2, kOrders = 2; };
+template <> struct XType<VQ_F16> { typedef _Float16 E; static constexpr int kTerms = 2, kWTerms = 2, kOrders = 3; };
+template <> struct XType<VQ_F32> { typedef float E; static constexpr int kTerms = 3, kWTerms = 3, kOrders = 3; };
 
 __device__ inline int swap_pair(int v) { return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xf, 0xf, true); }
 __device__ inline float swap_pair(float v) { return __int_as_float(swap_pair(__float_as_int(v))); }
@@ -216,7 +220,7 @@ template <int D, int XT, int NT>
 __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
 {
     typedef typename XType<XT>::E E;
-    constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms;
+    constexpr int XTERMS = XType<XT>::kTerms, WTERMS = XType<XT>::kWTerms, ORDERS = XType<XT>::kOrders;
     constexpr int U = D == 4 ? 2 : 1;                  // sub-vectors per chunk
     constexpr int S = slots_of(D);
     constexpr int H = 2;                               // chunks whose gathers are in flight together
@@ -497,7 +501,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
                         for (int p = 0; p < WTERMS; ++p)
 #pragma unroll
                             for (int k = 0; k < XTERMS; ++k)
-                                if (p + k < WTERMS) acc[n] = Bf16::mfma(wt[p], xt[k], acc[n]);
+                                if (p + k < ORDERS) acc[n] = Bf16::mfma(wt[p], xt[k], acc[n]);
                     }
                 }
                 c0 += H * 8;

@@ -287,3 +287,41 @@ def test_input_check_names_the_array(monkeypatch):
         X[2, 63] = float("nan")
         with pytest.raises(vq.VQError, match="X holds 1 non-finite"):
             vq.qlinear(Q, X)
+
+
+def split_left(v, n):
+    """What n bfloat16 terms, each the rounding of what the ones before leave, leave of v."""
+    v = v.double()
+    for _ in range(n):
+        v = v - v.bfloat16().double()
+    return v
+
+
+@pytest.mark.parametrize("d", [8, 4, 6])
+@pytest.mark.parametrize("dt", DT)
+def test_terms_of_same_signed_values(d, dt):
+    """Weights and tokens whose bfloat16 terms leave the most, all of one sign, so that no error averages away.
+
+    A residual of minus the rounded sum leaves the difference, which the output type holds to its own
+    rounding.  Eps of the split alone: 2^-17 with 16-bit tokens, 2^-23 with float32; beside it the
+    float32 sums, N + 8 additions of at most four (bf16: two, float32: six) products of terms each,
+    2^-24 of the sum apiece, and the residual's subtraction.
+    """
+    dtype = DT[dt]
+    N, M, K = 2 * d, 16, 32
+    g = torch.Generator().manual_seed(24)
+    cand = 1 + torch.rand(1 << 16, generator=g) * 2.0 ** -6
+    worst = split_left(cand, 1).abs() + 2.0 ** 9 * split_left(cand, 2).abs()
+    w = cand[worst.topk(K * d).indices].reshape(K, d)
+    w = torch.where(split_left(w, 1) > 0, w, w - 2 * split_left(w, 1).float())     # second terms of one sign
+    x = (1 + torch.rand(1 << 16, generator=g) * 2.0 ** -6).to(dtype).float()
+    x = x[split_left(x, 1).topk(N).indices] if dtype != torch.bfloat16 else x[:N]
+    idx = torch.randint(0, K, (M * 2,), generator=g).to(torch.uint16)
+    Q = vq.QMatrix(M, N, d, w.cuda(), idx.cuda())
+    X = x.to(dtype)[None, :]
+    z = X.double() @ w.double()[idx.long()].reshape(M, N).T
+    R = -z.to(dtype)
+    terms = {"bf16": 2, "f16": 4, "f32": 6}[dt]
+    eps = (2.0 ** -23 if dt == "f32" else 2.0 ** -17) + (N + 8) * terms * 2.0 ** -24
+    say("terms", dt, d)
+    check("difference", vq.qlinear(Q, X.cuda(), residual=R.cuda()), z + R.double(), eps * z, dtype)
