@@ -208,6 +208,50 @@ __device__ inline void load_row(const float* C, uint32_t k, int d, float (&w)[8]
     }
 }
 
+// One sum from the definition, in plain float32.  Infinite values cannot be split
+// (inf - inf), and inf times a term of zero is NaN, so a sum that comes out infinite
+// or NaN is formed again by this: rare, so one lane takes a row (4096 x 11008, one
+// token with an infinity in its last column, 2.9 ms).  An infinite token value meets an
+// exact entry's whole weight, not the decoded one and the difference.  Finite calls pay
+// for the test with 0 to 1 % (fp16, 17 to 32 tokens, 3 %).
+template <class E>
+__device__ inline float defined_sum(const QMat& q, const E* x, int64_t row, int64_t nb, int d)
+{
+    const int e0 = q.row_ptr ? q.row_ptr[row] : 0, e1 = q.row_ptr ? q.row_ptr[row + 1] : 0;
+    const float rs = q.rs ? q.rs[row] : 1.0f;
+    const int64_t N = nb * d;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int64_t b = 0; b < nb; ++b) {
+        const uint32_t i1 = q.idx1[row * nb + b], i2 = q.C2 ? q.idx2[row * nb + b] : 0;
+        const float* const c1 = q.C1 + (int64_t)min(i1, (uint32_t)q.K1 - 1) * d;
+        const float* const c2 = q.C2 ? q.C2 + (int64_t)min(i2, (uint32_t)q.K2 - 1) * d : nullptr;
+#pragma unroll 1
+        for (int i = 0; i < d; ++i) {
+            const int64_t j = b * d + i;
+            float w = c2 ? c1[i] + c2[i] : c1[i];
+            if (q.cs) w *= q.cs[j];
+            w *= rs;
+            const float v = (float)x[j];
+            if (__builtin_isinf(v)) {
+#pragma unroll 1
+                for (int e = e0; e < e1; ++e)
+                    if (q.col[e] == j) w += q.delta[e];
+            }
+            s += w * v;
+        }
+        if (__builtin_isnan(s)) return s;
+    }
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+        const int64_t j = q.col[e];
+        if (j < 0 || j >= N) continue;
+        const float v = (float)x[j];
+        if (__builtin_isfinite(v)) s += q.delta[e] * v;
+    }
+    return s;
+}
+
 // Columns of LDS per sub-vector: d = 8 and 4 as they are, others padded to eight.
 __host__ __device__ constexpr int slots_of(int D) { return D ? D : 8; }
 // Elements between tokens in LDS: 16 bytes past a multiple of 128, so that eight
@@ -589,6 +633,8 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
         }
         if (a.q[m].rs) v *= rs_v[m];
         z[m] = sparse ? v + cor[(m * NT * 16 + item_t) * kQRows + item_r] : v;
+        if (__builtin_expect(!a.part && !__builtin_isfinite(z[m]), 0))
+            z[m] = defined_sum(a.q[m], static_cast<const E*>(a.X) + item_t * a.ldx, out_row, a.nb, d);
         if (a.part) a.part[(((int64_t)blockIdx.y * nm + m) * a.T + item_t) * a.M + out_row] = z[m];
         z[m] += bias_v[m];
     }
@@ -600,6 +646,7 @@ __global__ __launch_bounds__(1024) void k_qffn(const QArgs a)
 }
 
 // Adds the parts in order and applies the epilogue.
+template <int XT>
 __global__ __launch_bounds__(256) void k_qffn_finish(const QArgs a)
 {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -613,12 +660,14 @@ __global__ __launch_bounds__(256) void k_qffn_finish(const QArgs a)
         float v = 0.0f;
 #pragma unroll 4
         for (int s = 0; s < a.splits; ++s) v += a.part[((int64_t)s * a.nm + m) * n + e];
-        z[m] = a.bias[m] ? v + load_any(a.bias[m], row, a.dtype) : v;
+        if (__builtin_expect(!__builtin_isfinite(v), 0))
+            v = defined_sum(a.q[m], static_cast<const typename XType<XT>::E*>(a.X) + t * a.ldx, row, a.nb, a.d);
+        z[m] = a.bias[m] ? v + load_any(a.bias[m], row, XT) : v;
     }
     float y = act_full(a.act, z[0]);
     if (a.nm > 1) y *= z[1];
-    if (a.R) y += load_any(a.R, t * a.ldr + row, a.dtype);
-    store_any(a.Y, t * a.ldy + row, a.dtype, y);
+    if (a.R) y += load_any(a.R, t * a.ldr + row, XT);
+    store_any(a.Y, t * a.ldy + row, XT, y);
 }
 
 // delta_e = val_e - decoded weight at e (each step rounded as the
@@ -765,7 +814,10 @@ vq_status q_run(QArgs a, int64_t T, int nm, void* ws, hipStream_t st)
         a.Y = Y + t0 * a.ldy * e;
         VQ_TRY(vec && a.d == 8 ? q_type<8>(a, st) : vec ? q_type<4>(a, st) : q_type<0>(a, st));
         if (a.part) {
-            hipLaunchKernelGGL(k_qffn_finish, dim3(grid_for((int64_t)a.T * a.M, 256)), dim3(256), 0, st, a);
+            const auto finish = a.dtype == VQ_BF16 ? k_qffn_finish<VQ_BF16>
+                                : a.dtype == VQ_F16 ? k_qffn_finish<VQ_F16>
+                                                    : k_qffn_finish<VQ_F32>;
+            hipLaunchKernelGGL(finish, dim3(grid_for((int64_t)a.T * a.M, 256)), dim3(256), 0, st, a);
             VQ_LAUNCHED("k_qffn_finish");
         }
     }

@@ -509,8 +509,11 @@ vq_status vq_sparse_delta(const vq_qmatrix* Q, const float* val, float* delta, v
  * scaled W, each sum is within ((N + nnz_i + 64) * 2^-23 + eps) * S of exact,
  * eps = 2^-16 for the 16-bit types (the decoded weights enter as two bf16 terms)
  * and 2^-22 for float32 (three terms).  Bitwise reproducible for fixed
- * arguments.  Every 32 tokens are one pass over the matrix.  The workspace is
- * as in the dense calls. */
+ * arguments.  Every 32 tokens are one pass over the matrix.  An infinite or NaN
+ * token value gives what the definition gives in the outputs whose sums it
+ * enters (an exact entry by its exact value) and changes no others; a call whose
+ * sums come out infinite or NaN takes milliseconds.  Codebooks, scales and exact
+ * values are finite.  The workspace is as in the dense calls. */
 size_t vq_qlinear_workspace_bytes(int64_t M, int64_t N, int d, int64_t T);
 vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const void* X, int64_t ldx,
                      const void* bias, const void* R, int64_t ldr, void* Y, int64_t ldy,

@@ -325,3 +325,60 @@ def test_terms_of_same_signed_values(d, dt):
     eps = (2.0 ** -23 if dt == "f32" else 2.0 ** -17) + (N + 8) * terms * 2.0 ** -24
     say("terms", dt, d)
     check("difference", vq.qlinear(Q, X.cuda(), residual=R.cuda()), z + R.double(), eps * z, dtype)
+
+
+def agree(name, got, value, error, dtype):
+    """NaN and infinities where the definition has them; elsewhere within the bound."""
+    g, fin = ref.f64(got), torch.isfinite(value)
+    assert torch.equal(torch.isnan(g), torch.isnan(value)), name
+    inf = torch.isinf(value)
+    assert torch.equal(torch.isinf(g), inf) and torch.equal(g[inf], value[inf]), name
+    if bool(fin.any()):
+        check(name, g[fin], value[fin], error[fin], dtype)
+
+
+@pytest.mark.parametrize("case", [(60, 264, 8, 100, 20, True), (33, 2056, 8, 200, 300, False), (40, 260, 4, 60, 9, True),
+                                  (50, 96, 6, 40, 0, False)], ids=lambda c: "%dx%d_d%d" % c[:3])
+@pytest.mark.parametrize("dt", DT)
+def test_infinite_and_nan_tokens(case, dt):
+    """Infinite and NaN tokens give what the definition gives (at exact entries by the exact weight); other tokens keep their bits."""
+    M, N, d, K1, K2, scales = case
+    dtype = DT[dt]
+    say("non-finite tokens", case, dt)
+    g = np.random.default_rng([85, M, N, d])
+    q = [make_matrix(g, M, N, d, K1, K2, scales, 9, full_row=5) for _ in range(2)]
+    Q = [on_gpu(m) for m in q]
+    inf = float("inf")
+    X = tokens(g, 18, N, dtype)
+    clean = vq.qlinear(Q[0], X), vq.qgated(Q[0], Q[1], X, act="none")
+    exact = int(q[0]["col"][0])                       # a column that some row holds exactly
+    X[1, 3] = inf
+    X[2, N - 1] = -inf
+    X[4, exact] = inf
+    X[7, 0], X[7, 9] = inf, -inf
+    X[9, N // 2] = float("nan")
+    X[16] = float("nan")
+    X[17, exact], X[17, N - 2] = -inf, 1.0
+    if dtype == torch.float32:
+        X[11, 5] = 3.4e38                              # finite, and past the largest bfloat16 value
+    finite = torch.where(torch.isfinite(X), X, torch.zeros_like(X))
+    z = [(ref.f64(X) @ torch.from_numpy(what(m)).T, sums(m, finite, dtype)[1]) for m in q]
+    # the sum is formed again where it came out infinite: N + nnz additions, as the bound has them
+    same = [t for t in range(18) if t not in (1, 2, 4, 7, 9, 11, 16, 17)]
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    got = vq.qlinear(Q[0], X)
+    agree("qlinear", got, *z[0], dtype)
+    assert torch.equal(got[same].view(bits), clean[0][same].view(bits))
+    agree("relu", vq.qlinear(Q[0], X, act="relu"), ref.act("relu", z[0][0]), z[0][1], dtype)
+    got = vq.qgated(Q[0], Q[1], X, act="none")
+    (a, ea), (u, eu) = z
+    rows = [t for t in range(18) if t != 11]           # the square of 3.4e38 is past the type
+    agree("qgated", got[rows], (a * u)[rows], (a.abs() * eu + u.abs() * ea + ea * eu + 2.0 ** -23 * (a * u).abs())[rows], dtype)
+    assert torch.equal(got[same].view(bits), clean[1][same].view(bits))
+
+
+def what(q):
+    """The reconstruction, float64 of its float32 values."""
+    return oracle.reconstruct(M=q["M"], N=q["N"], d=q["d"], C1=q["C1"], idx1=q["idx1"], C2=q["C2"], idx2=q["idx2"],
+                              r=q["rscale"], c=q["cscale"], row_ptr=q["row_ptr"], col=q["col"],
+                              val=q["val"]).astype(np.float64)
