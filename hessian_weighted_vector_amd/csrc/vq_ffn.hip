@@ -17,6 +17,7 @@
 #include "vq_ffn.h"
 
 #include <algorithm>
+#include <initializer_list>
 
 namespace vq {
 namespace {
@@ -399,6 +400,17 @@ vq_status check_ld(const std::string& call, const char* what, const void* p, int
     return VQ_OK;
 }
 
+// No output (null ones aside) begins where an input or another output does.
+vq_status check_apart(const std::string& call, std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs)
+{
+    for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* i : inputs) VQ_CHECK(*o != i, call + ": outputs may not alias inputs");
+        for (auto p = outputs.begin(); p != o; ++p) VQ_CHECK(*o != *p, call + ": outputs may not alias each other");
+    }
+    return VQ_OK;
+}
+
 #define VQ_MATRIX(a, rows, cols, ld, call, what) \
     VQ_TRY(check_matrix((a), (rows), (cols), (ld), dtype, (call), (what), as_stream(stream)))
 
@@ -431,7 +443,8 @@ vq_status vq_linear(int64_t T, int64_t M, int64_t N, int dtype, int act, const v
     VQ_TRY(check_ld(call, "R", R, ldr, M));
     VQ_TRY(check_ld(call, "Y", Y, ldy, M));
     VQ_TRY(check_ld(call, "Z", Z, ldz, M));
-    VQ_CHECK(Y != X && Y != W && Y != Z && (!Z || (Z != X && Z != W && Z != R)), "vq_linear: outputs may not alias inputs");
+    VQ_TRY(check_apart(call, {Y, Z}, {X, W, bias}));
+    VQ_CHECK(!Z || Z != R, "vq_linear: outputs may not alias inputs");
     VQ_CHECK(Y != R || ldy == ldr, "vq_linear: Y in place of R needs R's leading dimension");
     Forward f{T, M, N, dtype, 1, X, ldx, {W, nullptr}, ldw, {act, {bias, nullptr}, R, Y, {Z, nullptr}, ldr, ldy, ldz}};
     Arena a{nullptr};
@@ -473,9 +486,7 @@ vq_status vq_gated(int64_t T, int64_t M, int64_t N, int dtype, int act, const vo
     VQ_TRY(check_ld(call, "H", H, ldh, M));
     VQ_TRY(check_ld(call, "G", G, ldz, M));
     VQ_TRY(check_ld(call, "U", U, ldz, M));
-    for (const void* o : {(const void*)H, (const void*)G, (const void*)U})
-        VQ_CHECK(!o || (o != X && o != Wg && o != Wu), "vq_gated: outputs may not alias inputs");
-    VQ_CHECK(H != G && H != U && (!G || G != U), "vq_gated: outputs may not alias each other");
+    VQ_TRY(check_apart(call, {H, G, U}, {X, Wg, Wu, bg, bu}));
     Forward f{T, M, N, dtype, 2, X, ldx, {Wg, Wu}, ldw, {act, {bg, bu}, nullptr, H, {G, U}, 0, ldh, ldz}};
     Arena a{nullptr};
     VQ_TRY(forward(f, a, false, as_stream(stream)));
@@ -520,8 +531,7 @@ vq_status vq_linear_backward(int64_t T, int64_t M, int64_t N, int dtype, int act
     VQ_TRY(check_ld(call, "dX", dX, lddx, N));
     VQ_TRY(check_ld(call, "dW", dW, lddw, N));
     VQ_TRY(check_ld(call, "db", db, M, M));
-    for (const void* o : {(const void*)dX, (const void*)dW, (const void*)db})
-        VQ_CHECK(!o || (o != dY && o != X && o != W && o != Z), "vq_linear_backward: outputs may not alias inputs");
+    VQ_TRY(check_apart(call, {dX, dW, db}, {dY, X, W, Z}));
     Backward b{T, M, N, dtype, act, 1, dY, lddy, X, ldx, {W, nullptr}, ldw, {act != VQ_ACT_NONE ? Z : nullptr, nullptr}, ldz,
                dX, lddx, {dW, nullptr}, lddw, {db, nullptr}};
     Arena a{nullptr};
@@ -561,8 +571,8 @@ vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act,
     VQ_CHECK(T == 0 || (dH && G && U), "vq_gated_backward: null pointer");
     VQ_CHECK(T == 0 || !dX || (Wg && Wu), "vq_gated_backward: dX needs Wg and Wu");
     VQ_CHECK(T == 0 || !(dWg || dWu) || X, "vq_gated_backward: dWg and dWu need X");
-    VQ_CHECK((dWg == nullptr) == (dWu == nullptr) && (!dWg || dWg != dWu), "vq_gated_backward: dWg and dWu come together, apart");
-    VQ_CHECK((dbg == nullptr) == (dbu == nullptr) && (!dbg || dbg != dbu), "vq_gated_backward: dbg and dbu come together, apart");
+    VQ_CHECK((dWg == nullptr) == (dWu == nullptr), "vq_gated_backward: dWg and dWu come together");
+    VQ_CHECK((dbg == nullptr) == (dbu == nullptr), "vq_gated_backward: dbg and dbu come together");
     VQ_TRY(check_ld(call, "dH", dH, lddh, M));
     VQ_TRY(check_ld(call, "X", X, ldx, N));
     VQ_TRY(check_ld(call, "Wg", Wg, ldw, N));
@@ -574,9 +584,7 @@ vq_status vq_gated_backward(int64_t T, int64_t M, int64_t N, int dtype, int act,
     VQ_TRY(check_ld(call, "dWu", dWu, lddw, N));
     VQ_TRY(check_ld(call, "dbg", dbg, M, M));
     VQ_TRY(check_ld(call, "dbu", dbu, M, M));
-    for (const void* o : {(const void*)dX, (const void*)dWg, (const void*)dWu, (const void*)dbg, (const void*)dbu})
-        VQ_CHECK(!o || (o != dH && o != X && o != Wg && o != Wu && o != G && o != U),
-                 "vq_gated_backward: outputs may not alias inputs");
+    VQ_TRY(check_apart(call, {dX, dWg, dWu, dbg, dbu}, {dH, X, Wg, Wu, G, U}));
     Backward b{T, M, N, dtype, act, 2, dH, lddh, X, ldx, {Wg, Wu}, ldw, {G, U}, ldz, dX, lddx, {dWg, dWu}, lddw, {dbg, dbu}};
     Arena a{nullptr};
     VQ_TRY(backward(b, a, false, as_stream(stream)));

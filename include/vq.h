@@ -425,8 +425,8 @@ double vq_bits_per_weight_grouped(const vq_grouped_params* p);
  * weights and biases).  Products and sums are float32 on the matrix cores;
  * each stored value is rounded once from float32.  Results are bitwise
  * reproducible for fixed arguments (the sums' split depends on sizes and
- * alignment, never on timing).  Outputs may not overlap inputs, except Y = R
- * (same address and leading dimension).  Non-finite inputs spread into the
+ * alignment, never on timing).  Outputs may not overlap inputs or each other,
+ * except Y = R (same address and leading dimension).  Non-finite inputs spread into the
  * outputs whose sums they enter and no others.  The workspace queries take the
  * same sizes, addresses and leading dimensions as the call (addresses for
  * their alignment alone) and return 0 for sizes that the call rejects.  A

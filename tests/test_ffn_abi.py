@@ -201,3 +201,33 @@ def test_workspaces_off_16_bytes_are_refused():
             text = lib.vq_last_error().decode()
             assert text.startswith(name) and "16-byte aligned" in text, (name, off, text)
         assert call(None) == vq.VQ_ERR_WORKSPACE, name
+
+
+def test_outputs_at_one_address_are_refused():
+    """Two outputs at one address, or an output at a bias's, would be written over each other."""
+    lib = vq.load()
+    P = [FAKE + 4096 * k for k in range(16)]
+    X, W, W2, Z, Z2, D, o1, o2, o3, o4, o5, b = P[:12]
+
+    def lback(dX=o1, dW=o2, db=o3):
+        return lib.vq_linear_backward(4, 8, 16, F16, 2, D, 8, X, 16, W, 16, Z, 8, dX, 16, dW, 16, db, None, 0, None)
+
+    def gback(dX=o1, dWg=o2, dWu=o3, dbg=o4, dbu=o5):
+        return lib.vq_gated_backward(4, 8, 16, BF16, 2, D, 8, X, 16, W, W2, 16, Z, Z2, 8, dX, 16, dWg, dWu, 16, dbg, dbu,
+                                     None, 0, None)
+
+    def refuse(st, call, kw):
+        assert st == vq.VQ_ERR_INVALID, (call, kw)
+        text = lib.vq_last_error().decode()
+        assert text.startswith(call + ":") and "alias" in text, (kw, text)
+
+    for kw in (dict(dX=o2), dict(db=o2), dict(db=o1)):
+        refuse(lback(**kw), "vq_linear_backward", kw)
+    for kw in (dict(dX=o2), dict(dX=o3), dict(dWu=o2), dict(dbu=o4), dict(dbg=o1), dict(dbu=o3)):
+        refuse(gback(**kw), "vq_gated_backward", kw)
+    refuse(lib.vq_linear(4, 8, 16, BF16, 0, X, 16, W, 16, b, None, 0, b, 8, None, 0, None, 0, None), "vq_linear", "Y is the bias")
+    refuse(lib.vq_linear(4, 8, 16, BF16, 0, X, 16, W, 16, b, None, 0, o1, 8, b, 8, None, 0, None), "vq_linear", "Z is the bias")
+    refuse(lib.vq_gated(4, 8, 16, BF16, 2, X, 16, W, W2, 16, None, b, o1, 8, o2, b, 8, None, 0, None), "vq_gated", "U is a bias")
+    # apart, the calls reach the workspace's check
+    for st in (lback(), gback()):
+        assert st == vq.VQ_ERR_WORKSPACE
