@@ -920,7 +920,7 @@ vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const v
     a.bias[0] = bias;
     a.R = R; a.ldr = ldr;
     a.Y = Y; a.ldy = ldy;
-    TimedRegion tr("qlinear", Q->K1, as_stream(stream));
+    TimedRegion tr("qlinear", 0, as_stream(stream));
     return q_run(a, T, 1, ws, as_stream(stream));
 }
 
@@ -954,7 +954,7 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
     a.dtype = dtype; a.act = act;
     a.bias[0] = bg; a.bias[1] = bu;
     a.Y = H; a.ldy = ldh;
-    TimedRegion tr("qgated", Qg->K1, as_stream(stream));
+    TimedRegion tr("qgated", 0, as_stream(stream));
     return q_run(a, T, 2, ws, as_stream(stream));
 }
 

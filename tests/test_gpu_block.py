@@ -158,3 +158,22 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for k, (o, w) in enumerate(zip(out, want)):
             assert torch.equal(o.view(torch.int16), w.view(torch.int16)), k
+
+
+def test_timing_records():
+    """Each feed-forward call has one record, keyed by its name and K = 0 whatever the codebooks' sizes."""
+    say("timing")
+    b, X, dY = make(8, 6, 64, 48, torch.bfloat16)
+    small = b.compress(*b.calibrate(X), d=8, K1=16, iters1=1, K2=8, iters2=1)
+    other = b.compress(*b.calibrate(X), d=8, K1=32, iters1=1, K2=8, iters2=1)
+    vq.timing_enable()
+    try:
+        _, kept = b.forward(X, keep=True)
+        b.backward(dY, kept)
+        small.forward(X)
+        other.forward(X)
+        records = {(name, K): n for name, K, n, *_ in vq.timing_records()}
+    finally:
+        vq.timing_enable(False)
+    assert records == {("gated", 0): 1, ("linear", 0): 1, ("linear_backward", 0): 1, ("gated_backward", 0): 1,
+                       ("qgated", 0): 2, ("qlinear", 0): 2}
