@@ -161,9 +161,12 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current device's index, and the raw handle of its current stream without a Stream object
+_device = torch._C._cuda_getDevice
+
+
 def _stream():
-    # the raw handle of the current device's current stream, without a Stream object
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch._C._cuda_getCurrentRawStream(_device())
 
 
 def _dtype(t, dt, name):
@@ -506,14 +509,28 @@ def _half(t, name):
     return code
 
 
-def _matrix(t, rows, cols, dtype, name):
-    """(pointer, leading dimension) of a [rows x cols] tensor with unit column stride; None passes."""
+def _home(X, name="X"):
+    """The index of the current GPU, where the launches go; X has to be on it."""
+    dev = X.get_device()
+    if dev < 0 or dev != _device():
+        _elsewhere(X, name)
+    return dev
+
+
+def _elsewhere(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be on the GPU" % name)
+    raise ValueError("%s must be on the current GPU %d, is on %d" % (name, _device(), t.get_device()))
+
+
+def _matrix(t, rows, cols, dtype, dev, name):
+    """(pointer, leading dimension) of a [rows x cols] tensor on GPU dev with unit column stride; None passes."""
     if t is None:
         return None, 0
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_cuda:
-        raise ValueError("%s must be on the GPU" % name)
+    if t.get_device() != dev:
+        _elsewhere(t, name)
     if t.shape != (rows, cols):
         raise ValueError("%s must be [%d x %d], got %s" % (name, rows, cols, list(t.shape)))
     s0, s1 = t.stride()
@@ -526,30 +543,34 @@ def _matrix(t, rows, cols, dtype, name):
     return t.data_ptr(), s0
 
 
-def _output(out, X, rows, cols, name="out"):
+def _output(out, X, rows, cols, dev):
     """(tensor, pointer, leading dimension) of a caller's output or of a new one of X's type."""
     if out is None:
         out = X.new_empty((rows, cols))
         return out, out.data_ptr(), cols
-    return (out,) + _matrix(out, rows, cols, X.dtype, name)
+    return (out,) + _matrix(out, rows, cols, X.dtype, dev, "out")
 
 
-def _vector(t, n, dtype, name):
+def _vector(t, n, dtype, dev, name):
     if t is None:
         return None
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError("%s must be [%d], got %s" % (name, n, list(t.shape)))
+    if t.get_device() != dev:
+        _elsewhere(t, name)
     return _ptr(t)
 
 
-def _scratch(need, ws, device):
+def _scratch(need, ws, X, dev):
     """(pointer, bytes, tensor) of a workspace of at least `need` bytes."""
     if ws is None:
         if need == 0:
             return None, 0, None
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+    elif ws.get_device() != dev:
+        _elsewhere(ws, "ws")
     return _ptr(ws), ws.numel(), ws
 
 
@@ -597,15 +618,15 @@ def linear(X, W, bias=None, residual=None, act="none", want_pre=False, out=None,
     Rows may be strided.  `out` may be the residual itself.
     """
     T, M, N = _dims(X, W)
-    dt, a = _half(X, "X"), _act(act)
-    x, ldx = _matrix(X, T, N, X.dtype, "X")
-    w, ldw = _matrix(W, M, N, X.dtype, "W")
-    b = _vector(bias, M, X.dtype, "bias")
-    r, ldr = _matrix(residual, T, M, X.dtype, "residual")
-    Y, y, ldy = _output(out, X, T, M)
-    Z, z, ldz = _output(None, X, T, M) if want_pre else (None, None, 0)
+    dt, a, dev = _half(X, "X"), _act(act), _home(X)
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    w, ldw = _matrix(W, M, N, X.dtype, dev, "W")
+    b = _vector(bias, M, X.dtype, dev, "bias")
+    r, ldr = _matrix(residual, T, M, X.dtype, dev, "residual")
+    Y, y, ldy = _output(out, X, T, M, dev)
+    Z, z, ldz = _output(None, X, T, M, dev) if want_pre else (None, None, 0)
     lib = load()
-    p, n, ws = _scratch(_linear_need(T, M, N, x & 15, ldx, w & 15, ldw), ws, X.device)
+    p, n, ws = _scratch(_linear_need(T, M, N, x & 15, ldx, w & 15, ldw), ws, X, dev)
     _check(lib.vq_linear(T, M, N, dt, a, x, ldx, w, ldw, b, r, ldr, y, ldy, z, ldz, p, n, _stream()))
     return (Y, Z) if want_pre else Y
 
@@ -620,16 +641,17 @@ def linear_backward(dY, X, W, pre=None, act="none", want_dx=True, want_dw=True, 
     dt, a = _half(X, "X"), _act(act)
     if a != 0 and pre is None:
         raise ValueError("pre is needed for the activation's gradient")
-    g, ldg = _matrix(dY, T, M, X.dtype, "dY")
-    x, ldx = _matrix(X, T, N, X.dtype, "X")
-    w, ldw = _matrix(W, M, N, X.dtype, "W")
-    z, ldz = _matrix(pre, T, M, X.dtype, "pre")
+    dev = _home(X)
+    g, ldg = _matrix(dY, T, M, X.dtype, dev, "dY")
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    w, ldw = _matrix(W, M, N, X.dtype, dev, "W")
+    z, ldz = _matrix(pre, T, M, X.dtype, dev, "pre")
     dX = X.new_empty((T, N)) if want_dx else None
     dW = X.new_empty((M, N)) if want_dw else None
     db = X.new_empty(M) if want_db else None
     lib = load()
     p, n, ws = _scratch(_linear_backward_need(T, M, N, a, g & 15, ldg, x & 15, ldx, w & 15, ldw, want_dx, want_dw, want_db),
-                        ws, X.device)
+                        ws, X, dev)
     _check(lib.vq_linear_backward(T, M, N, dt, a, g, ldg, x, ldx, w, ldw, z, ldz, _ptr(dX), N, _ptr(dW), N, _ptr(db),
                                   p, n, _stream()))
     return dX, dW, db
@@ -642,19 +664,19 @@ def gated(X, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", want_pre=Fa
     returns (H, G, U), which gated_backward takes.
     """
     T, M, N = _dims(X, W_gate)
-    dt, a = _half(X, "X"), _act(act)
-    x, ldx = _matrix(X, T, N, X.dtype, "X")
-    wg, ldw = _matrix(W_gate, M, N, X.dtype, "W_gate")
-    wu, ldu = _matrix(W_up, M, N, X.dtype, "W_up")
+    dt, a, dev = _half(X, "X"), _act(act), _home(X)
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    wg, ldw = _matrix(W_gate, M, N, X.dtype, dev, "W_gate")
+    wu, ldu = _matrix(W_up, M, N, X.dtype, dev, "W_up")
     if ldw != ldu:
         raise ValueError("W_gate and W_up must have the same row stride")
-    bg = _vector(bias_gate, M, X.dtype, "bias_gate")
-    bu = _vector(bias_up, M, X.dtype, "bias_up")
-    H, h, ldh = _output(out, X, T, M)
+    bg = _vector(bias_gate, M, X.dtype, dev, "bias_gate")
+    bu = _vector(bias_up, M, X.dtype, dev, "bias_up")
+    H, h, ldh = _output(out, X, T, M, dev)
     G = X.new_empty((T, M)) if want_pre else None
     U = X.new_empty((T, M)) if want_pre else None
     lib = load()
-    p, n, ws = _scratch(_gated_need(T, M, N, x & 15, ldx, wg & 15, wu & 15, ldw), ws, X.device)
+    p, n, ws = _scratch(_gated_need(T, M, N, x & 15, ldx, wg & 15, wu & 15, ldw), ws, X, dev)
     _check(lib.vq_gated(T, M, N, dt, a, x, ldx, wg, wu, ldw, bg, bu, h, ldh, _ptr(G), _ptr(U), M, p, n, _stream()))
     return (H, G, U) if want_pre else H
 
@@ -662,13 +684,13 @@ def gated(X, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", want_pre=Fa
 def gated_backward(dH, X, W_gate, W_up, G, U, act="silu", want_dx=True, want_dw=True, want_db=False, ws=None):
     """(dX, dW_gate, dW_up, db_gate, db_up) of gated; None where not wanted."""
     T, M, N = _dims(X, W_gate)
-    dt, a = _half(X, "X"), _act(act)
-    dh, lddh = _matrix(dH, T, M, X.dtype, "dH")
-    x, ldx = _matrix(X, T, N, X.dtype, "X")
-    wg, ldw = _matrix(W_gate, M, N, X.dtype, "W_gate")
-    wu, ldu = _matrix(W_up, M, N, X.dtype, "W_up")
-    g, ldz = _matrix(G, T, M, X.dtype, "G")
-    u, ldz2 = _matrix(U, T, M, X.dtype, "U")
+    dt, a, dev = _half(X, "X"), _act(act), _home(X)
+    dh, lddh = _matrix(dH, T, M, X.dtype, dev, "dH")
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    wg, ldw = _matrix(W_gate, M, N, X.dtype, dev, "W_gate")
+    wu, ldu = _matrix(W_up, M, N, X.dtype, dev, "W_up")
+    g, ldz = _matrix(G, T, M, X.dtype, dev, "G")
+    u, ldz2 = _matrix(U, T, M, X.dtype, dev, "U")
     if ldw != ldu or ldz != ldz2:
         raise ValueError("W_gate and W_up, and G and U, must have the same row stride")
 
@@ -679,7 +701,7 @@ def gated_backward(dH, X, W_gate, W_up, G, U, act="silu", want_dx=True, want_dw=
     dbg, dbu = new(want_db, M), new(want_db, M)
     lib = load()
     p, n, ws = _scratch(_gated_backward_need(T, M, N, a, dh & 15, lddh, x & 15, ldx, wg & 15, wu & 15, ldw, want_dx, want_dw,
-                                             want_db), ws, X.device)
+                                             want_db), ws, X, dev)
     _check(lib.vq_gated_backward(T, M, N, dt, a, dh, lddh, x, ldx, wg, wu, ldw, g, u, ldz, _ptr(dX), N, _ptr(dWg),
                                  _ptr(dWu), N, _ptr(dbg), _ptr(dbu), p, n, _stream()))
     return dX, dWg, dWu, dbg, dbu
@@ -711,6 +733,10 @@ class QMatrix:
                 raise ValueError("%s must be [K x %d], got %s" % (name, d, list(t.shape)))
         if (C2 is None) != (idx2 is None):
             raise ValueError("C2 and idx2 come together")
+        for t, name in ((C1, "C1"), (idx1, "idx1"), (C2, "C2"), (idx2, "idx2"), (rscale, "rscale"), (cscale, "cscale"),
+                        (row_ptr, "row_ptr"), (col, "col"), (val, "val")):
+            if t is not None:
+                _home(t, name)
         sparse = row_ptr is not None and col is not None and col.numel() > 0
         if sparse and (val is None or val.numel() != col.numel()):
             raise ValueError("val must have as many elements as col")
@@ -723,6 +749,7 @@ class QMatrix:
                                      _ptr(col) if sparse else None, _ptr(self.delta))
         self._ref = ctypes.addressof(self._struct)
         self.device = C1.device
+        self.index = C1.get_device()
         self.refresh()
 
     @classmethod
@@ -733,6 +760,8 @@ class QMatrix:
 
     def refresh(self):
         """Makes the sparse differences again (current stream)."""
+        if self.index != _device():
+            _elsewhere(self._keep[0], "the matrix")
         if self.delta is not None:
             _check(load().vq_sparse_delta(self._ref, _ptr(self.val), _ptr(self.delta), _stream()))
 
@@ -752,13 +781,15 @@ def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     T, M, N = X.shape[0], Q.M, Q.N
-    dt, a = _any_dtype(X, "X"), _act(act)
-    x, ldx = _matrix(X, T, N, X.dtype, "X")
-    b = _vector(bias, M, X.dtype, "bias")
-    r, ldr = _matrix(residual, T, M, X.dtype, "residual")
-    Y, y, ldy = _output(out, X, T, M)
+    dt, a, dev = _any_dtype(X, "X"), _act(act), _home(X)
+    if Q.index != dev:
+        _elsewhere(Q._keep[0], "Q")
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    b = _vector(bias, M, X.dtype, dev, "bias")
+    r, ldr = _matrix(residual, T, M, X.dtype, dev, "residual")
+    Y, y, ldy = _output(out, X, T, M, dev)
     lib = load()
-    p, n, ws = _scratch(_qlinear_need(M, N, Q.d, T), ws, X.device)
+    p, n, ws = _scratch(_qlinear_need(M, N, Q.d, T), ws, X, dev)
     _check(lib.vq_qlinear(Q._ref, T, dt, a, x, ldx, b, r, ldr, y, ldy, p, n, _stream()))
     return Y
 
@@ -768,12 +799,16 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     T, M, N = X.shape[0], Q_gate.M, Q_gate.N
-    dt, a = _any_dtype(X, "X"), _act(act)
-    x, ldx = _matrix(X, T, N, X.dtype, "X")
-    bg = _vector(bias_gate, M, X.dtype, "bias_gate")
-    bu = _vector(bias_up, M, X.dtype, "bias_up")
-    H, h, ldh = _output(out, X, T, M)
+    dt, a, dev = _any_dtype(X, "X"), _act(act), _home(X)
+    if Q_gate.index != dev:
+        _elsewhere(Q_gate._keep[0], "Q_gate")
+    if Q_up.index != dev:
+        _elsewhere(Q_up._keep[0], "Q_up")
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    bg = _vector(bias_gate, M, X.dtype, dev, "bias_gate")
+    bu = _vector(bias_up, M, X.dtype, dev, "bias_up")
+    H, h, ldh = _output(out, X, T, M, dev)
     lib = load()
-    p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X.device)
+    p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X, dev)
     _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
     return H

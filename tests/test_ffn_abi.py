@@ -231,3 +231,58 @@ def test_outputs_at_one_address_are_refused():
     # apart, the calls reach the workspace's check
     for st in (lback(), gback()):
         assert st == vq.VQ_ERR_WORKSPACE
+
+
+class Elsewhere:
+    """Stands for a bfloat16 matrix or vector on GPU `index`; never dereferenced."""
+    is_cuda = True
+
+    def __init__(self, *shape, index=1, dtype=torch.bfloat16):
+        self.shape, self.index, self.dtype = torch.Size(shape), index, dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self):
+        return (self.shape[-1], 1) if len(self.shape) == 2 else (1,)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_tensors_of_another_gpu_are_refused(monkeypatch):
+    """The launches go to the current GPU's stream: a tensor of another one is an error, not a stray access."""
+    monkeypatch.setattr(vq, "_device", lambda: 0)
+    X, W, H = Elsewhere(4, 16), Elsewhere(8, 16), Elsewhere(4, 8)
+
+    def here(*shape, **kw):
+        return Elsewhere(*shape, index=0, **kw)
+
+    for call, name in [
+            (lambda: vq.linear(X, here(8, 16)), "X"), (lambda: vq.linear(here(4, 16), W), "W"),
+            (lambda: vq.linear(here(4, 16), here(8, 16), bias=Elsewhere(8)), "bias"),
+            (lambda: vq.linear(here(4, 16), here(8, 16), out=H), "out"),
+            (lambda: vq.linear(here(4, 16), here(8, 16), out=here(4, 8), ws=Elsewhere(64, dtype=torch.uint8)), "ws"),
+            (lambda: vq.gated(here(4, 16), here(8, 16), W), "W_up"),
+            (lambda: vq.linear_backward(H, here(4, 16), here(8, 16)), "dY"),
+            (lambda: vq.gated_backward(here(4, 8), here(4, 16), here(8, 16), here(8, 16), here(4, 8), H), "U")]:
+        with pytest.raises(ValueError, match=name + " must be on the current GPU 0, is on 1"):
+            call()
+
+    f32 = dict(dtype=torch.float32)
+    with pytest.raises(ValueError, match="idx1 must be on the current GPU"):
+        vq.QMatrix(32, 64, 8, here(16, 8, **f32), Elsewhere(256, dtype=torch.uint16))
+    Q = vq.QMatrix.__new__(vq.QMatrix)
+    Q.M, Q.N, Q.d, Q._keep, Q.delta, Q.index = 32, 64, 8, (Elsewhere(16, 8, **f32),), None, 1
+    for call in (lambda: vq.qlinear(Q, here(1, 64, **f32)), lambda: vq.qgated(Q, Q, here(1, 64, **f32)), Q.refresh):
+        with pytest.raises(ValueError, match="on the current GPU 0, is on 1"):
+            call()
