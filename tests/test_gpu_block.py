@@ -177,3 +177,22 @@ def test_timing_records():
         vq.timing_enable(False)
     assert records == {("gated", 0): 1, ("linear", 0): 1, ("linear_backward", 0): 1, ("gated_backward", 0): 1,
                        ("qgated", 0): 2, ("qlinear", 0): 2}
+
+
+def test_stream_and_device_handles(monkeypatch):
+    """The raw handles are those of torch's public calls, and the calls run as well on the public ones alone."""
+    say("handles")
+    side = torch.cuda.Stream()
+    for s in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(s):
+            assert vq._stream() == s.cuda_stream == vq._public_stream(vq._device())
+    assert vq._device() == torch.cuda.current_device()
+    b, X, _ = make(9, 3, 40, 24, torch.bfloat16)
+    want = b.forward(X)
+    monkeypatch.setattr(vq, "_device", torch.cuda.current_device)
+    monkeypatch.setattr(vq, "_raw_stream", vq._public_stream)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = b.forward(X)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
