@@ -839,7 +839,7 @@ vq_status check_qmatrix(const std::string& call, const vq_qmatrix* Q)
 }
 
 vq_status check_call(const std::string& call, const vq_qmatrix* Q, int64_t T, int dtype, int act, const void* X, int64_t ldx,
-                     const void* Y, int64_t ldy)
+                     const void* Y, int64_t ldy, const void* bias, const void* R, int64_t ldr)
 {
     VQ_TRY(check_qmatrix(call, Q));
     VQ_CHECK(!Q->row_ptr || (Q->col && Q->delta), call + ": the sparse part needs col and delta");
@@ -850,10 +850,13 @@ vq_status check_call(const std::string& call, const vq_qmatrix* Q, int64_t T, in
     VQ_CHECK(X && Y, call + ": null pointer");
     VQ_CHECK(ldx >= Q->N && ldx <= ((int64_t)1 << 40), call + ": leading dimension of X is out of range");
     VQ_CHECK(ldy >= Q->M && ldy <= ((int64_t)1 << 40), call + ": leading dimension of the output is out of range");
+    VQ_CHECK(!R || (ldr >= Q->M && ldr <= ((int64_t)1 << 40)), call + ": leading dimension of R is out of range");
     const uintptr_t mis = dtype == VQ_F32 ? 3 : 1;
-    VQ_CHECK(((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y)) & mis) == 0,
-             call + ": a tensor is not aligned to its elements");
+    for (const void* p : {X, Y, bias, R})
+        VQ_CHECK((reinterpret_cast<uintptr_t>(p) & mis) == 0, call + ": a tensor is not aligned to its elements");
     VQ_CHECK(X != Y, call + ": the output may not alias X");
+    VQ_CHECK(bias != Y, call + ": the output may not alias a bias");
+    VQ_CHECK(Y != R || ldy == ldr, call + ": Y in place of R needs R's leading dimension");
     return VQ_OK;
 }
 
@@ -901,10 +904,8 @@ vq_status vq_qlinear(const vq_qmatrix* Q, int64_t T, int dtype, int act, const v
                      const void* R, int64_t ldr, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream)
 {
     const char* call = "vq_qlinear";
-    VQ_TRY(check_call(call, Q, T, dtype, act, X, ldx, Y, ldy));
+    VQ_TRY(check_call(call, Q, T, dtype, act, X, ldx, Y, ldy, bias, R, ldr));
     if (T == 0) return VQ_OK;
-    VQ_CHECK(!R || ldr >= Q->M, "vq_qlinear: leading dimension of R is below its row length");
-    VQ_CHECK(Y != R || ldy == ldr, "vq_qlinear: Y in place of R needs R's leading dimension");
     const size_t need = q_workspace(Q->M, Q->N / Q->d, T, 1);
     VQ_TRY(check_workspace(call, ws, ws_bytes, need));
     VQ_TRY(check_device());
@@ -934,8 +935,8 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
                     const void* bg, const void* bu, void* H, int64_t ldh, void* ws, size_t ws_bytes, void* stream)
 {
     const char* call = "vq_qgated";
-    VQ_TRY(check_call(call, Qg, T, dtype, act, X, ldx, H, ldh));
-    VQ_TRY(check_call(call, Qu, T, dtype, act, X, ldx, H, ldh));
+    VQ_TRY(check_call(call, Qg, T, dtype, act, X, ldx, H, ldh, bg, nullptr, 0));
+    VQ_TRY(check_call(call, Qu, T, dtype, act, X, ldx, H, ldh, bu, nullptr, 0));
     VQ_CHECK(Qg->M == Qu->M && Qg->N == Qu->N && Qg->d == Qu->d, "vq_qgated: the matrices differ in M, N or d");
     if (T == 0) return VQ_OK;
     const size_t need = q_workspace(Qg->M, Qg->N / Qg->d, T, 2);

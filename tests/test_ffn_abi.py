@@ -286,3 +286,24 @@ def test_tensors_of_another_gpu_are_refused(monkeypatch):
     for call in (lambda: vq.qlinear(Q, here(1, 64, **f32)), lambda: vq.qgated(Q, Q, here(1, 64, **f32)), Q.refresh):
         with pytest.raises(ValueError, match="on the current GPU 0, is on 1"):
             call()
+
+
+def test_compressed_calls_check_residual_and_biases():
+    """A residual or bias off its elements' boundary, a residual's row distance out of range, an output at a bias."""
+    import ctypes
+    lib = vq.load()
+    q = ctypes.byref(qmatrix())
+    X, Y, Z = FAKE + 8192, FAKE + 16384, FAKE + 32768
+    for dt, off in ((F32, 2), (F32, 1), (BF16, 1), (F16, 1)):
+        for b, R in ((Z + off, None), (None, Z + off)):
+            assert lib.vq_qlinear(q, 1, dt, 0, X, 64, b, R, 32, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+            assert "not aligned" in lib.vq_last_error().decode()
+        for bg, bu in ((Z + off, None), (None, Z + off)):
+            assert lib.vq_qgated(q, q, 1, dt, 0, X, 64, bg, bu, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+            assert "not aligned" in lib.vq_last_error().decode()
+    for ldr in (31, -1, (1 << 40) + 1):
+        assert lib.vq_qlinear(q, 1, F32, 0, X, 64, None, Z, ldr, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+        assert "leading dimension of R" in lib.vq_last_error().decode()
+    assert lib.vq_qlinear(q, 1, F32, 0, X, 64, Y, None, 0, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+    assert lib.vq_qgated(q, q, 1, F32, 0, X, 64, None, Y, Y, 32, None, 0, None) == vq.VQ_ERR_INVALID
+    assert "bias" in lib.vq_last_error().decode()
