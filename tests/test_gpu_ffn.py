@@ -407,3 +407,61 @@ def test_nan_pre_activations_reach_the_gradients(name):
         dX, dW, db = vq.linear_backward(dY, X, Wg, pre=G, act=name, want_db=True)
         for o, b in ((dX, row), (dW, col[:, None]), (db, col)):
             assert torch.equal(torch.isnan(o), b.expand_as(o)), name
+
+
+# Sizes for which the plan takes the 256 x 256 tile (mostly ragged past it: odd rows, which are
+# copied, and rows of a multiple of eight, which are not), and what else it takes with it.
+LARGE_TILES = [
+    ("linear", 4728, 1703, 130),             # 7 x 19 tiles, each over all of k
+    ("linear", 4304, 408, 4360),             # 2 x 17, sums split
+    ("gated", 870, 4890, 135),               # pair of half tiles, 39 x 4
+    ("gated", 152, 4368, 3512),              # split sums of a pair
+    ("linear_backward", 664, 736, 6104),     # dX and dW in one launch, dX first
+    ("linear_backward", 821, 569, 6124),     # dW first
+    ("linear_backward", 2870, 144, 1969),    # dW's sums split
+    ("linear_backward", 282, 3665, 1494),    # dX's
+    ("linear_backward", 4344, 4280, 136),    # both; bias sums over 32 rows a workgroup
+    ("linear_backward", 4340, 4276, 139),    # the same from odd rows
+    ("gated_backward", 576, 280, 6176),      # dX of two segments, two dW
+    ("gated_backward", 669, 313, 6033),      # dW first
+    ("gated_backward", 3664, 2984, 152),     # both split; 32 rows a workgroup in the elementwise pass
+    ("gated_backward", 3664, 2983, 151),     # the same from odd rows
+    ("gated_backward", 752, 5976, 557),      # dX split, 32 rows
+    ("gated_backward", 279, 5151, 1413),     # one after the other: dX by 128 x 128 split, dW by 256 x 256
+    ("gated_backward", 4204, 535, 3148),     # dX by 256 x 256, dW by 128 x 128
+    ("gated_backward", 440, 3506, 4487),     # both by 256 x 256, dX's sums split and both in one place of the workspace
+]
+
+
+@pytest.mark.parametrize("case", LARGE_TILES, ids=["%s_%dx%dx%d" % c for c in LARGE_TILES])
+@pytest.mark.parametrize("dt", DT)
+def test_large_tiles(case, dt):
+    op, T, M, N = case
+    dtype = DT[dt]
+    name = ref.ACTS[(T + M + N + (dt == "f16")) % len(ref.ACTS)]
+    say(op, T, M, N, dt, name)
+    g = torch.Generator().manual_seed(T + M + N)
+    X = tensor(g, (T, N), dtype)
+    W = [tensor(g, (M, N), dtype, N ** -0.5) for _ in range(2 if op.startswith("gated") else 1)]
+    b = [tensor(g, (M,), dtype) for _ in W]
+    if op == "linear":
+        R = tensor(g, (T, M), dtype)
+        check(op, vq.linear(X, W[0], bias=b[0], residual=R, act=name, want_pre=True),
+              ref.linear(X, W[0], b[0], R, name, dtype))
+        return
+    if op == "gated":
+        check(op, vq.gated(X, *W, bias_gate=b[0], bias_up=b[1], act=name, want_pre=True),
+              ref.gated(X, *W, *b, name, dtype))
+        return
+    dY = tensor(g, (T, M), dtype)
+    Z = [tensor(g, (T, M), dtype, 1.5) for _ in W]
+    if op == "linear_backward":
+        want = ref.linear_backward(dY, X, W[0], Z[0], name, dtype)
+        check(op, vq.linear_backward(dY, X, W[0], pre=Z[0], act=name, want_db=True), want)
+        check("dX alone", vq.linear_backward(dY, X, W[0], pre=Z[0], act=name, want_dw=False)[:1], want[:1])
+        check("dW alone", vq.linear_backward(dY, X, W[0], pre=Z[0], act=name, want_dx=False)[1:2], want[1:2])
+    else:
+        want = ref.gated_backward(dY, X, *W, *Z, name, dtype)
+        check(op, vq.gated_backward(dY, X, *W, *Z, act=name, want_db=True), want)
+        check("dX alone", vq.gated_backward(dY, X, *W, *Z, act=name, want_dw=False)[:1], want[:1])
+        check("dW alone", vq.gated_backward(dY, X, *W, *Z, act=name, want_dx=False)[1:3], want[1:3])
