@@ -45,8 +45,9 @@ struct F16 {
 
 // ---- activations --------------------------------------------------------
 // Dense products: the result is rounded to 16 bits, so the exponential and the
-// reciprocal are the hardware's (a few float32 ulp).  The tanh form of GELU is
-// z * logistic(2 v), which needs no tanh and loses nothing for negative z.
+// reciprocal are the hardware's (a few float32 ulp; results below about 1e-36 may be
+// 0).  The tanh form of GELU is z * logistic(2 v), which needs no tanh and loses
+// nothing for negative z.
 __device__ inline float logistic_fast(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 constexpr float kSqrtHalf = 0.70710678118654752f;
@@ -79,15 +80,25 @@ __device__ inline void activate(int act, float (&z)[8])
 #undef VQ_EACH
 }
 
-// The same in full float32 accuracy (float32 results).
+// z times the logistic function of v, to float32's smallest values: the exponential is
+// never of a positive argument, so where it is tiny the result is too, and not 0.
+__device__ inline float times_logistic(float z, float v)
+{
+    const float e = expf(-fabsf(v));
+    return (v < 0.0f ? z * e : z) / (1.0f + e);
+}
+
+// The activations in full float32 accuracy (float32 results).  An error of the exponential's
+// argument is the result's relative error, so the tanh form's argument takes three
+// roundings (z^2, multiply-add, product) and two rounded constants: 4 * 2^-24 of it.
 __device__ inline float act_full(int act, float z)
 {
     switch (act) {
     case VQ_ACT_RELU: return z > 0.0f ? z : (z <= 0.0f ? 0.0f : z);
-    case VQ_ACT_SILU: return z / (1.0f + expf(-z));
+    case VQ_ACT_SILU: return times_logistic(z, z);
     case VQ_ACT_GELU: return z * normal_cdf(z);
-    case VQ_ACT_GELU_TANH: return z / (1.0f + expf(-2.0f * kGeluC * (z + kGeluA * z * z * z)));
-    case VQ_ACT_SIGMOID: return 1.0f / (1.0f + expf(-z));
+    case VQ_ACT_GELU_TANH: return times_logistic(z, z * fmaf(2.0f * kGeluC * kGeluA, z * z, 2.0f * kGeluC));
+    case VQ_ACT_SIGMOID: return times_logistic(1.0f, z);
     default: return z;
     }
 }

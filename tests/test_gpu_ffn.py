@@ -422,6 +422,7 @@ LARGE_TILES = [
     ("linear_backward", 282, 3665, 1494),    # dX's
     ("linear_backward", 4344, 4280, 136),    # both; bias sums over 32 rows a workgroup
     ("linear_backward", 4340, 4276, 139),    # the same from odd rows
+    ("linear_backward", 4340, 4277, 139),    # and from odd rows of the pre-activations
     ("gated_backward", 576, 280, 6176),      # dX of two segments, two dW
     ("gated_backward", 669, 313, 6033),      # dW first
     ("gated_backward", 3664, 2984, 152),     # both split; 32 rows a workgroup in the elementwise pass

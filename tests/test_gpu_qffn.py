@@ -382,3 +382,30 @@ def what(q):
     return oracle.reconstruct(M=q["M"], N=q["N"], d=q["d"], C1=q["C1"], idx1=q["idx1"], C2=q["C2"], idx2=q["idx2"],
                               r=q["rscale"], c=q["cscale"], row_ptr=q["row_ptr"], col=q["col"],
                               val=q["val"]).astype(np.float64)
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+def test_activations_in_float32(name):
+    """Float32 results have float32's accuracy, far past the 16-bit results' 2^-16.
+
+    One column, a token of 1: the sum is the weight itself.  Relative bound: 8 * 2^-23 for the exponential
+    (or error function), the additions, products and the quotient, and twice 2^-23 for each unit of an
+    exponent's argument that is itself rounded: z^2 / 2 for GELU, the cubic for its tanh form, none for the
+    others.  Results below the smallest normal value may be flushed.
+    """
+    say("float32 activation", name)
+    z = torch.linspace(-20, 20, 4001)
+    n = len(z)
+    Q = vq.QMatrix(n, 1, 1, z[:, None].contiguous().cuda(), torch.arange(n, dtype=torch.int32).to(torch.uint16).cuda())
+    zz = z.double()
+    want = ref.act(name, zz)
+    if name == "gelu_tanh":
+        v = 2 * (2 / np.pi) ** 0.5 * (zz + 0.044715 * zz ** 3)
+        want, arg = zz * torch.sigmoid(v), v.abs()      # as ref.act, without its cancellation
+    else:
+        arg = zz.square() / 2 if name == "gelu" else torch.zeros_like(zz)
+    X = torch.ones((1, 1), device="cuda")
+    bound = want.abs() * (8 + 2 * arg) * 2.0 ** -23 + 2.0 ** -126
+    off = (ref.f64(vq.qlinear(Q, X, act=name))[0] - want).abs()
+    say("   max error / bound = %.3g" % float((off / bound).max()))
+    assert bool((off <= bound).all())
