@@ -33,7 +33,11 @@ class GatedBlock:
         return (Y, (X, r)) if keep else Y
 
     def backward(self, dY, kept):
-        """(dX, dWg, dWu, dWd)."""
+        """(dX, dWg, dWu, dWd).
+
+        dX is rounded to the type twice, as the block's two terms (the gated product's gradient
+        and the residual's, dY) are two tensors of it.
+        """
         X, (H, G, U) = kept
         dH, dWd, _ = vq.linear_backward(dY, H, self.Wd)
         dX, dWg, dWu, _, _ = vq.gated_backward(dH, X, self.Wg, self.Wu, G, U, act=self.act)
@@ -58,7 +62,10 @@ class GatedBlock:
 
 
 class CompressedBlock:
-    """The block from its compressed matrices, for a few tokens of any of the types."""
+    """The block from its compressed matrices, for a few tokens of any of the types.
+
+    Every 32 tokens read the matrices anew: a prompt is faster through GatedBlock.
+    """
 
     def __init__(self, gate, up, down, act="silu"):
         if (up.M, up.N) != (gate.M, gate.N) or (down.M, down.N) != (gate.N, gate.M):

@@ -228,10 +228,12 @@ vq_status few_launch(const Few& a, int waves, bool pair, hipStream_t st)
 }  // namespace
 
 // Up to 32 tokens, while the weights' elements times the tokens stay below 6e8: past
-// that the tiled product, which reads the tokens once a tile, is faster.  One token by
-// 8192 x 8192: 25 us here and 26 us tiled, eight 29 and 26, 32 45 and 28; 4096 x 4096,
-// 32 tokens: 14 and 16; pair of 28672 x 8192, one token: 169 and 161, eight 186 and 161;
-// pair of 8192 x 8192, one 40 and 43, 16 48 and 45.
+// that the tiled product, which reads the tokens once a tile, is mostly faster.  One
+// token by 8192 x 8192: 25 us here and 26 us tiled, 32 45 and 28; 4096 x 4096, 32 tokens:
+// 14 and 16; pair of 8192 x 8192, one 40 and 43.  The product of sizes does not separate
+// the two everywhere; below the threshold this way is the slower for one token by 8192 x
+// 28672 (107 us here, 91 tiled), by 16384 x 4096 (27, 25) and by pairs of 28672 x 8192 (168,
+// 161) and 16384 x 4096 (48, 43), and for eight by 8192 x 8192 (29, 26) and 11008 x 4096 (22, 21).
 bool few_tokens(int64_t T, int64_t M, int64_t K, int nm) { return T <= 32 && (double)T * (double)M * (double)K * nm < 6e8; }
 
 size_t few_workspace(int64_t T, int64_t M, int64_t K, int nm)

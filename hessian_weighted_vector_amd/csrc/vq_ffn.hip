@@ -11,9 +11,12 @@
 //   k_zero_rows   gradients of zero tokens
 //
 // The gradients of the pre-activations are rounded to the tensors' 16-bit type
-// once, since the matrix cores read them in it: one rounding of at most 2^-8 (bf16)
-// or 2^-11 (fp16) of each, independent over the products' sums.  The bias gradients
-// are summed from the unrounded values.
+// once, since the matrix cores read them in it: one rounding of each, independent over
+// the products' sums.  In bf16 it is at most 2^-8 of the value.  In fp16 it is at most
+// 2^-11 of values from 2^-14 to 65504, 2^-25 absolute below and infinite above, also
+// where dX and dW themselves would be representable: fp16 callers scale their losses
+// so that dY act'(Z), dH U act'(G) and dH act(G) stay in that range.  The bias
+// gradients are summed from the unrounded values.
 #include "vq_ffn.h"
 
 #include <algorithm>

@@ -18,17 +18,19 @@
 // third terms and of the third terms are left out, at most 2^-23 |w x|.  Sixteen
 // tokens cost the gathers of one.
 //
-// What bounds it is the requests from L1 to L2: each sub-vector is one, to a
-// random line, and at 0.42 a clock and CU the L2 channels of a die (16 for 32 CUs)
-// take 0.84 of one each a clock.  So the tokens' terms and the column scales of a
+// What bounds it is the requests from L1 to L2 that a CU keeps in flight: each
+// sub-vector is one, to a random line, L2 hits of 237 cycles, and about 65 are in flight
+// (0.28 a clock and CU; the L2 channels, 16 for a die of 32 CUs, take 0.56 of one each
+// a clock).  So the tokens' terms and the column scales of a
 // slab of columns are staged in LDS once a workgroup, indices are read 16 bytes
 // (eight sub-vectors) a lane, a block ahead, and neighbouring lanes fetch the two
 // halves of one centroid row in one instruction (one request, not two) and swap
 // them.  4096 x 11008, one float32 token, all parts: 36 to 40 us; without residual,
 // scales and exact entries 33, the gathers alone; a pair of 8192 x 2048, one
-// token, 30 us; of 11008 x 4096, eight tokens, 94 us.  The body has one copy:
+// token, 30 us; of 11008 x 4096, eight tokens, 95 us.  The body has one copy:
 // unrolled over a block's groups it was 28 KB of code and its sums went through
-// scratch memory, 14 to 20 % slower.
+// scratch memory, 14 to 20 % slower.  Seventeen to 32 float32 tokens still keep 11
+// registers there (d = 8 and 4).
 //
 // A workgroup owns 16 rows; its waves (of a pair, the even ones gate and the odd
 // ones up) take blocks of 32 sub-vectors in turn and their sums are added in wave

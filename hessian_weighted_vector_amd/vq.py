@@ -495,6 +495,8 @@ def fit(W, h, d, K1, iters1, K2=0, iters2=0, outlier_frac=0.0, binorm=False, mas
 
 
 # ---- dense feed-forward calls ------------------------------------------------
+# Outputs carry no autograd graph, also where an input requires gradients: the backward
+# passes are calls of their own (linear_backward, gated_backward).
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -782,7 +784,8 @@ def _any_dtype(t, name):
 def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
     """Y = act(X W^T + bias) + residual with W = the QMatrix Q, never decoded to memory.
 
-    X [T, N] of bfloat16, float16 or float32; the other tensors have its type.
+    X [T, N] of bfloat16, float16 or float32; the other tensors have its type.  For a few
+    tokens: every 32 read the matrix anew.
     """
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
@@ -801,7 +804,7 @@ def qlinear(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
 
 
 def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, ws=None):
-    """H = act(X Wg^T + bias_gate) * (X Wu^T + bias_up) with both compressed matrices in one launch."""
+    """H = act(X Wg^T + bias_gate) * (X Wu^T + bias_up) with both compressed matrices in one launch (tokens as in qlinear)."""
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     T, M, N = X.shape[0], Q_gate.M, Q_gate.N

@@ -444,8 +444,10 @@ vq_status vq_linear(int64_t T, int64_t M, int64_t N, int dtype, int act, const v
 /* Gradients of vq_linear:  dZ = dY act'(Z),  dX = dZ W,  dW = dZ^T X,
  * db = column sums of dZ (R's gradient is dY).  Each of dX [T x N],
  * dW [M x N], db [M] may be NULL; W is read for dX, X for dW, Z where act is
- * not VQ_ACT_NONE.  dZ enters the products rounded to the tensors' type; db is
- * summed before that rounding. */
+ * not VQ_ACT_NONE.  dZ enters the products rounded to the tensors' type: with
+ * VQ_F16 a dZ past 65504 enters as an infinity, and one below 2^-14 to 2^-25
+ * absolute, also where dX and dW would be representable.  db is summed before
+ * that rounding. */
 size_t vq_linear_backward_workspace_bytes(int64_t T, int64_t M, int64_t N, int act, const void* dY, int64_t lddy,
                                           const void* X, int64_t ldx, const void* W, int64_t ldw,
                                           int want_dx, int want_dw, int want_db);
@@ -466,7 +468,8 @@ vq_status vq_gated(int64_t T, int64_t M, int64_t N, int dtype, int act, const vo
 
 /* Gradients of vq_gated:  dG = dH U act'(G),  dU = dH act(G),
  * dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,  dbg, dbu = column sums of
- * dG, dU.  dX may be NULL, dWg and dWu both, dbg and dbu both. */
+ * dG, dU.  dX may be NULL, dWg and dWu both, dbg and dbu both.  dG and dU enter the
+ * products rounded to the tensors' type, as dZ above. */
 size_t vq_gated_backward_workspace_bytes(int64_t T, int64_t M, int64_t N, int act, const void* dH, int64_t lddh,
                                          const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
                                          int want_dx, int want_dw, int want_db);
@@ -509,7 +512,11 @@ vq_status vq_sparse_delta(const vq_qmatrix* Q, const float* val, float* delta, v
  * scaled W, each sum is within ((N + nnz_i + 64) * 2^-23 + eps) * S of exact,
  * eps = 2^-16 for the 16-bit types (the decoded weights enter as two bf16 terms)
  * and 2^-22 for float32 (three terms).  Bitwise reproducible for fixed
- * arguments.  Every 32 tokens are one pass over the matrix.  An infinite or NaN
+ * arguments.  Every 32 tokens are one pass over the matrix, so a prompt is better
+ * multiplied by a dense matrix (vq_reconstruct, vq_linear).  vq_qgemv is the same
+ * product for float32 tokens alone, without an epilogue, from the exact values
+ * rather than delta: for callers that keep no vq_qmatrix.  (4096 x 11008, 1, 8, 16 and
+ * 32 tokens: 36, 67, 134 and 271 us by vq_qgemv, 36-39, 61, 100 and 300 here.)  An infinite or NaN
  * token value gives what the definition gives in the outputs whose sums it
  * enters (an exact entry by its exact value) and changes no others; a call whose
  * sums come out infinite or NaN takes milliseconds.  Codebooks, scales and exact
