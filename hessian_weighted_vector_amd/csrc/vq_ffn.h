@@ -24,6 +24,7 @@ inline vq_status check_workspace(const char* call, const void* ws, size_t ws_byt
 // nearest even once, from float32.
 struct Bf16 {
     static constexpr int kDtype = VQ_BF16;
+    typedef f32x4 Acc;                          // four sums
     typedef __bf16 E;
     typedef __bf16 V4 __attribute__((ext_vector_type(4)));
     typedef __bf16 V8 __attribute__((ext_vector_type(8)));
@@ -32,6 +33,7 @@ struct Bf16 {
 };
 struct F16 {
     static constexpr int kDtype = VQ_F16;
+    typedef f32x4 Acc;
     typedef _Float16 E;
     typedef _Float16 V4 __attribute__((ext_vector_type(4)));
     typedef _Float16 V8 __attribute__((ext_vector_type(8)));
