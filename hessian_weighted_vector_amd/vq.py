@@ -68,6 +68,16 @@ class QMatrixStruct(ctypes.Structure):
                 ("idx2", _P), ("rscale", _P), ("cscale", _P), ("row_ptr", _P), ("col", _P), ("delta", _P)]
 
 
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("grad", _P), ("master", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
+                ("n", _I64)]
+
+
+class AdamWPlan(ctypes.Structure):
+    _fields_ = [("table", _P), ("count", _I64), ("chunks", _I64), ("param_dtype", _I), ("grad_dtype", _I),
+                ("has_master", _I), ("state_bits", _I)]
+
+
 # name -> (restype, argtypes); every symbol declared in include/vq.h
 SIGNATURES = {
     "vq_version": (ctypes.c_char_p, []),
@@ -118,6 +128,9 @@ SIGNATURES = {
     "vq_qlinear": (_I, [_P, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "vq_qgated_workspace_bytes": (_SZ, [_I64, _I64, _I, _I64]),
     "vq_qgated": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "vq_adamw_plan_bytes": (_SZ, [_P, _I64]),
+    "vq_adamw_plan": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P, _P]),
+    "vq_adamw": (_I, [_P, _D, _D, _D, _D, _D, _I64, _P, _P, _P, _P]),
     "vq_timing_enable": (None, [_I]),
     "vq_timing_count": (_I, []),
     "vq_timing_get": (_I, [_I, ctypes.c_char_p, _I, ctypes.POINTER(_I), ctypes.POINTER(_I64),
@@ -821,3 +834,143 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X, dev)
     _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
     return H
+
+
+# ---- the optimizer's step -------------------------------------------------------
+
+class AdamW:
+    """AdamW over many tensors in one launch, in place.
+
+        m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,  g = grad_scale * grad,
+        p = (1 - lr wd) p - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+
+    params: contiguous tensors of one type (bfloat16, float16 or float32); grads: of the same
+    sizes and of one type, kept by the caller and filled before each step, or given to step().
+    masters: float32 tensors that hold the values of 16-bit params.  state_bits 8 keeps the
+    moments as float8_e4m3fn codes of m and sqrt(v) with a float32 scale for each 256
+    elements.  `state` (a dict of lists m, v and, in 8 bits, m_scale, v_scale, as the
+    attribute of that name holds them) and `steps` continue an earlier run; `state` is used
+    in place.  capturable keeps the step's number (`steps`, int64) and the learning rate
+    (`lr`, float32) on the GPU: a captured step() replays as consecutive steps.
+    """
+
+    BLOCK = 256
+
+    def __init__(self, params, grads=None, masters=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits=32, state=None, steps=0, capturable=False):
+        self.params, self.masters = list(params), None if masters is None else list(masters)
+        if not self.params:
+            raise ValueError("params must not be empty")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32, got %r" % (state_bits,))
+        self.index = _home(self.params[0], "params[0]")
+        self.dtype = _any_dtype(self.params[0], "params[0]")
+        self._same(self.params, self.params[0].dtype, "params")
+        if self.masters is not None:
+            if self.dtype == 2:
+                raise ValueError("float32 params have no masters")
+            self._same(self.masters, torch.float32, "masters")
+        self.betas, self.eps, self.weight_decay = (float(betas[0]), float(betas[1])), float(eps), float(weight_decay)
+        self.state_bits = state_bits
+        dev = self.params[0].device
+        if state is None:
+            state = self._new_state(dev)
+        self.state = {k: None if state.get(k) is None else list(state[k]) for k in ("m", "v", "m_scale", "v_scale")}
+        kind = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        for k in ("m", "v"):
+            self._same(self.state[k], kind, "state[%r]" % k)
+        for k in ("m_scale", "v_scale"):
+            if state_bits == 8:
+                self._same(self.state[k], torch.float32, "state[%r]" % k, blocks=True)
+            elif self.state[k] is not None:
+                raise ValueError("32-bit moments have no scales")
+        self.capturable = bool(capturable)
+        if capturable:
+            self.steps = torch.full((1,), int(steps), dtype=torch.int64, device=dev)
+            self.lr = torch.full((1,), float(lr), device=dev)
+        else:
+            self.steps, self.lr = int(steps), float(lr)
+        self.grads = None
+        self._plan = AdamWPlan()
+        self._ref = ctypes.addressof(self._plan)
+        if grads is not None:
+            self._bind(grads)
+
+    def _new_state(self, dev):
+        """Zero moments: one buffer each, every tensor from a block's border on."""
+        starts, at = [], 0
+        for p in self.params:
+            starts.append(at)
+            at += -(-p.numel() // self.BLOCK)
+        kind = torch.float32 if self.state_bits == 32 else torch.uint8
+        out = {}
+        for k in ("m", "v"):
+            flat = torch.zeros(at * self.BLOCK, dtype=kind, device=dev)
+            flat = flat if self.state_bits == 32 else flat.view(torch.float8_e4m3fn)
+            out[k] = [flat[s * self.BLOCK:s * self.BLOCK + p.numel()].view(p.shape) for s, p in zip(starts, self.params)]
+            if self.state_bits == 8:
+                scale = torch.zeros(at, device=dev)
+                out[k + "_scale"] = [scale[s:s - (-p.numel() // self.BLOCK)] for s, p in zip(starts, self.params)]
+        return out
+
+    def _same(self, ts, dtype, name, blocks=False):
+        """Checks a list against params: type, sizes, device, contiguity."""
+        if ts is None or len(ts) != len(self.params):
+            raise ValueError("%s must have %d tensors" % (name, len(self.params)))
+        for i, (t, p) in enumerate(zip(ts, self.params)):
+            n = -(-p.numel() // self.BLOCK) if blocks else p.numel()
+            if t.dtype != dtype:
+                raise TypeError("%s[%d] must be %s, got %s" % (name, i, dtype, t.dtype))
+            if t.get_device() != self.index:
+                _elsewhere(t, "%s[%d]" % (name, i))
+            if t.numel() != n:
+                raise ValueError("%s[%d] must have %d elements, got %d" % (name, i, n, t.numel()))
+            if not t.is_contiguous():
+                raise ValueError("%s[%d] must be contiguous" % (name, i))
+
+    def _bind(self, grads):
+        """The table of these gradients' tensors on the GPU (waits for the stream)."""
+        grads = list(grads)
+        if not grads:
+            raise ValueError("grads must have %d tensors" % len(self.params))
+        code = _any_dtype(grads[0], "grads[0]")
+        self._same(grads, grads[0].dtype, "grads")
+        n = len(self.params)
+        none = [None] * n
+        s = self.state
+        rows = (AdamWTensor * n)(*[
+            AdamWTensor(p.data_ptr(), g.data_ptr(), w.data_ptr() if w is not None else None, m.data_ptr(), v.data_ptr(),
+                        ms.data_ptr() if ms is not None else None, vs.data_ptr() if vs is not None else None, p.numel())
+            for p, g, w, m, v, ms, vs in zip(self.params, grads, self.masters or none, s["m"], s["v"], s["m_scale"] or none,
+                                             s["v_scale"] or none)])
+        lib = load()
+        need = lib.vq_adamw_plan_bytes(rows, n)
+        table = torch.empty(need, dtype=torch.uint8, device=self.params[0].device)
+        plan = AdamWPlan()
+        _check(lib.vq_adamw_plan(rows, n, self.dtype, code, self.masters is not None, self.state_bits, table.data_ptr(), need,
+                                 ctypes.addressof(plan), _stream()))
+        self.grads, self._table, self._plan, self._ref, self._bound = grads, table, plan, ctypes.addressof(plan), _stream()
+
+    def step(self, grads=None, grad_scale=None):
+        """One step.  grads replace those of the last step (the table is made anew, which waits for
+        the stream); grad_scale: a float32 tensor of one element on the GPU that the gradients are
+        multiplied by."""
+        if self.index != _device():
+            _elsewhere(self.params[0], "params[0]")
+        if grads is not None:
+            self._bind(grads)
+        if self.grads is None:
+            raise ValueError("grads are needed")
+        gs = None
+        if grad_scale is not None:
+            gs = _vector(grad_scale.reshape(-1), 1, torch.float32, self.index, "grad_scale")
+        st = _stream()
+        if st != self._bound:                                 # the table's memory waits for this stream too
+            self._table.record_stream(torch.cuda.current_stream())
+        b1, b2 = self.betas
+        if self.capturable:
+            _check(load().vq_adamw(self._ref, 0.0, b1, b2, self.eps, self.weight_decay, 0, self.steps.data_ptr(),
+                                   self.lr.data_ptr(), gs, st))
+        else:
+            _check(load().vq_adamw(self._ref, self.lr, b1, b2, self.eps, self.weight_decay, self.steps + 1, None, None, gs, st))
+            self.steps += 1

@@ -64,7 +64,7 @@ typedef enum {
     VQ_ERR_UNSUPPORTED = 5  /* no gfx950 device current */
 } vq_status;
 
-/* 16-bit element types of the dense feed-forward calls. */
+/* Element types; the dense feed-forward calls take the 16-bit ones. */
 typedef enum { VQ_BF16 = 0, VQ_F16 = 1, VQ_F32 = 2 } vq_dtype;
 
 /* Activations of the feed-forward calls.  VQ_ACT_GELU is z Phi(z) with the
@@ -530,6 +530,55 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
                     const void* X, int64_t ldx, const void* bg, const void* bu, void* H, int64_t ldh,
                     void* ws, size_t ws_bytes, void* stream);
 
+/* AdamW (decoupled weight decay) over many tensors in one launch:
+ *   g = grad_scale * grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = (1 - lr wd) p - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in float32, each element once, in place.  A tensor is n consecutive elements:
+ * param (param_dtype) and grad (grad_dtype; of all tensors of a plan the same types,
+ * VQ_BF16, VQ_F16 or VQ_F32); with has_master, float32 master holds p and param
+ * (16 bits) its rounded copy, else param itself is read and rounded once when
+ * written.  Moments in 32 bits: m, v float32 [n].  In 8 bits: m, v are one e4m3 code
+ * (OCP, no infinities) an element, and each 256 consecutive elements, the last
+ * possibly fewer, have one float32 in m_scale and v_scale [ceil(n / 256)]; the
+ * moments are code_m * m_scale and (code_v * v_scale)^2.  A step writes scale =
+ * (largest of the block) / 448 and the nearest codes (ties to even) of the quotients, a
+ * root above zero as at least 2^-9; it steps with the moments as they were before that rounding.
+ * All zero codes and scales are zero moments.  A non-finite gradient spreads into its element, with 8-bit
+ * moments into its block.
+ *
+ * vq_adamw_plan writes a table of the tensors (host array) into `table`
+ * (device, vq_adamw_plan_bytes, 16-byte aligned) and the plan; it waits for the
+ * stream, so it is made outside of a capture.  The plan is valid while
+ * the tensors and the table stay where they are; several may be alive.  Tensors may not overlap, gradients
+ * may overlap each other.  n = 0 is allowed.
+ *
+ * vq_adamw is one step.  step counts from 1.  step_from (device int64, nullable)
+ * holds the number of steps done, in place of step: the call adds one to it and takes
+ * the learning rate from lr_from (device, nullable) or lr, so that a captured
+ * graph replays as consecutive steps.  grad_scale: device float32 or NULL (1). */
+typedef struct {
+    void* param;
+    const void* grad;
+    float* master;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    int64_t n;
+} vq_adamw_tensor;
+
+typedef struct {
+    void* table;
+    int64_t count, chunks;
+    int param_dtype, grad_dtype, has_master, state_bits;
+} vq_adamw_plan_t;
+
+size_t vq_adamw_plan_bytes(const vq_adamw_tensor* tensors, int64_t count);
+vq_status vq_adamw_plan(const vq_adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype, int has_master,
+                        int state_bits, void* table, size_t table_bytes, vq_adamw_plan_t* plan, void* stream);
+vq_status vq_adamw(const vq_adamw_plan_t* plan, double lr, double beta1, double beta2, double eps, double weight_decay,
+                   int64_t step, int64_t* step_from, const float* lr_from, const float* grad_scale, void* stream);
+
 /* Bits per weight of the stored result (host arithmetic; VPTQ page,
  * "End-to-End Quantization Pipeline", compression ratio: index bits plus
  * codebook bits, extended by the sparse part and the scales):
@@ -544,8 +593,8 @@ double vq_bits_per_weight(int64_t M, int64_t N, int d, int K1, int K2, int64_t n
  * Records are keyed by (step name, K); names: "assign_search" (the matrix-core
  * search kernel alone), "assign" (the whole vq_assign), "update", "objective",
  * "select", "binorm", "residual", "reconstruct", "init", "linear",
- * "linear_backward", "gated", "gated_backward", "qlinear", "qgated" (the whole
- * call; K is 0 for these).  vq_timing_count()
+ * "linear_backward", "gated", "gated_backward", "qlinear", "qgated", "adamw" (the
+ * whole call; K is 0 for these).  vq_timing_count()
  * waits for the recorded events and returns the number of records;
  * vq_timing_get(i, ...) fills record i (name into a caller buffer of
  * name_len bytes): launches, total, min and max milliseconds.  Returns 0 on
