@@ -15,7 +15,7 @@
 // Bound by the weights' bytes.  Loads are at any element-aligned address.  One
 // token: 4096 x 11008 bf16 in 17.5 us (5.2 TB/s; a large read reaches 6.2), a pair
 // of 8192 x 2048 fp16 in 12.8 us (5.2 TB/s).
-#include "vq_ffn.h"
+#include "vq_few.h"
 
 namespace vq {
 namespace {
@@ -31,48 +31,6 @@ struct Few {
     float* part;                 // [splits][matrices][T][pitch], or null
     Epilogue epi;
 };
-
-template <class T>
-__device__ inline typename T::V8 chunk(const typename T::E* row, int64_t col)
-{
-    typename T::V8 v;
-    __builtin_memcpy(&v, row + col, 16);
-    return v;
-}
-
-// The same as it is loaded ahead.  ODD: rows may begin at an odd element (8192 x 4096
-// with rows of 4097, one token: 15.6 us by words, 28.7 us by chunks; of 4098, 13.0).
-template <class T, bool ODD>
-struct Ahead {
-    typename T::V8 v;
-    __device__ __forceinline__ void load(const typename T::E* row, int64_t col) { v = chunk<T>(row, col); }
-    __device__ __forceinline__ typename T::V8 get(const typename T::E*) const { return v; }
-};
-template <class T>
-struct Ahead<T, true> {
-    Words w;
-    __device__ __forceinline__ void load(const typename T::E* row, int64_t col) { w.load(row + col); }
-    __device__ __forceinline__ typename T::V8 get(const typename T::E* row) const
-    {
-        const uint4 u = w.get(row);                              // columns are multiples of eight
-        return __builtin_bit_cast(typename T::V8, u);
-    }
-};
-
-// A chunk with columns at or past K as zeros.
-template <class T>
-__device__ inline typename T::V8 chunk_tail(const typename T::E* row, int64_t col, int64_t K)
-{
-    typename T::V8 v = {};
-    if (col + 8 <= K) {
-        v = chunk<T>(row, col);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < K) v[i] = row[col + i];
-    }
-    return v;
-}
 
 template <class T, int NT, bool PAIR, int H, bool ODD>
 __global__ __launch_bounds__(1024) void k_few(const Few a)

@@ -5,6 +5,8 @@
 
 #include "vq_internal.h"
 
+#include <initializer_list>
+
 namespace vq {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -18,6 +20,30 @@ inline vq_status check_workspace(const char* call, const void* ws, size_t ws_byt
     VQ_CHECK(aligned16(ws), std::string(call) + ": workspace is not 16-byte aligned");
     return VQ_OK;
 }
+
+constexpr int64_t kMaxSize = 1 << 20;    // of a matrix's rows and columns
+
+inline vq_status check_ld(const std::string& call, const char* what, const void* p, int64_t ld, int64_t cols)
+{
+    VQ_CHECK(p == nullptr || ld >= cols, call + ": leading dimension of " + what + " is below its row length");
+    VQ_CHECK(p == nullptr || ld <= ((int64_t)1 << 40), call + ": leading dimension of " + what + " is too large");
+    VQ_CHECK((reinterpret_cast<uintptr_t>(p) & 1u) == 0, call + ": " + what + " is not aligned to its elements");
+    return VQ_OK;
+}
+
+// No output (null ones aside) begins where an input or another output does.
+inline vq_status check_apart(const std::string& call, std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs)
+{
+    for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* i : inputs) VQ_CHECK(*o != i, call + ": outputs may not alias inputs");
+        for (auto p = outputs.begin(); p != o; ++p) VQ_CHECK(*o != *p, call + ": outputs may not alias each other");
+    }
+    return VQ_OK;
+}
+
+#define VQ_MATRIX(a, rows, cols, ld, call, what) \
+    VQ_TRY(check_matrix((a), (rows), (cols), (ld), dtype, (call), (what), as_stream(stream)))
 
 // 16-bit element types: storage E, vectors of four and eight, and the
 // 16 x 16 x 32 matrix instruction with float32 accumulation.  Stores round to
@@ -262,6 +288,49 @@ __device__ inline void epilogue_pair(const Epilogue& e, int64_t t, int m, int M,
     for (int i = 0; i < 8; ++i) g[i] *= u[i];
     store8<T>(e.Y, e.ldy, t, m, M, g);
 }
+
+// ---- operands -------------------------------------------------------------
+constexpr int64_t kMaxLd = 1 << 21;      // tile offsets stay below 2^31 bytes
+
+// Hands out workspace slices; with no base it only counts.  Every call counts
+// first and compares with the caller's bytes.
+struct Arena {
+    char* base;
+    size_t used = 0;
+    void* take(size_t bytes)
+    {
+        char* p = base + used;
+        used += align_up(bytes);
+        return base ? p : nullptr;
+    }
+};
+
+inline int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+// Whether the tiled product's 16-byte loads can read the matrix as it is.
+inline bool loads_ok(const Mat& m) { return aligned16(m.p) && m.ld % 8 == 0 && m.cols % 8 == 0 && m.ld <= kMaxLd; }
+
+struct Pack {
+    const uint16_t* s;
+    uint16_t* o;
+    int64_t rows, ld, ldp;
+    int cols;
+    int odd;                   // some rows begin at an odd element
+};
+struct Packs {
+    Pack m[3];
+    int count = 0;
+    int blocks = 0;            // a matrix's
+};
+
+// The copies in one launch; blocks of a matrix whose copy has n chunks of eight.
+vq_status pack_launch(const Packs& list, hipStream_t st);
+inline int pack_blocks(int64_t n) { return (int)((n + 255) / 256 < 16384 ? (n + 255) / 256 : 16384); }
 
 // ---- the tiled product --------------------------------------------------
 // out[q, p] = sum over segments and k of P[p, k] Q[q, k] (p contiguous in the

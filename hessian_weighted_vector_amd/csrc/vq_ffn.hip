@@ -20,50 +20,11 @@
 #include "vq_ffn.h"
 
 #include <algorithm>
-#include <initializer_list>
 
 namespace vq {
 namespace {
 
-constexpr int64_t kMaxLd = 1 << 21;      // tile offsets stay below 2^31 bytes
-constexpr int64_t kMaxSize = 1 << 20;    // M and N
 constexpr int64_t kMaxTokens = 1 << 28;
-
-// Hands out workspace slices; with no base it only counts.  Every call counts
-// first and compares with the caller's bytes.
-struct Arena {
-    char* base;
-    size_t used = 0;
-    void* take(size_t bytes)
-    {
-        char* p = base + used;
-        used += align_up(bytes);
-        return base ? p : nullptr;
-    }
-};
-
-inline int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
-
-struct Mat {
-    const void* p;
-    int64_t rows, cols, ld;
-};
-
-// Whether the tiled product's 16-byte loads can read the matrix as it is.
-bool loads_ok(const Mat& m) { return aligned16(m.p) && m.ld % 8 == 0 && m.cols % 8 == 0 && m.ld <= kMaxLd; }
-
-struct Pack {
-    const uint16_t* s;
-    uint16_t* o;
-    int64_t rows, ld, ldp;
-    int cols;
-    int odd;                   // some rows begin at an odd element
-};
-struct Packs {
-    Pack m[3];
-    int count = 0;
-    int blocks = 0;            // a matrix's
-};
 
 // Block `block` of `blocks` of the copy of m.
 __device__ __forceinline__ void pack_rows(const Pack& m, int block, int blocks)
@@ -199,15 +160,12 @@ struct Packer {
         list.m[list.count++] = {static_cast<const uint16_t*>(m.p), static_cast<uint16_t*>(o), m.rows, m.ld, ldp, (int)m.cols,
                                 odd_rows(m.p, m.ld)};
         most = std::max(most, m.rows * (ldp / 8));
-        list.blocks = (int)std::min<int64_t>((most + 255) / 256, 16384);
+        list.blocks = pack_blocks(most);
         m = {o, m.rows, ldp, ldp};
     }
     vq_status launch(hipStream_t st) const
     {
-        if (list.count == 0) return VQ_OK;
-        hipLaunchKernelGGL(k_pack, dim3((unsigned)list.blocks, list.count), dim3(256), 0, st, list);
-        VQ_LAUNCHED("k_pack");
-        return VQ_OK;
+        return pack_launch(list, st);
     }
 };
 
@@ -395,29 +353,17 @@ vq_status check_sizes(const std::string& call, int64_t T, int64_t M, int64_t N, 
     return VQ_OK;
 }
 
-vq_status check_ld(const std::string& call, const char* what, const void* p, int64_t ld, int64_t cols)
-{
-    VQ_CHECK(p == nullptr || ld >= cols, call + ": leading dimension of " + what + " is below its row length");
-    VQ_CHECK(p == nullptr || ld <= ((int64_t)1 << 40), call + ": leading dimension of " + what + " is too large");
-    VQ_CHECK((reinterpret_cast<uintptr_t>(p) & 1u) == 0, call + ": " + what + " is not aligned to its elements");
-    return VQ_OK;
-}
-
-// No output (null ones aside) begins where an input or another output does.
-vq_status check_apart(const std::string& call, std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs)
-{
-    for (auto o = outputs.begin(); o != outputs.end(); ++o) {
-        if (!*o) continue;
-        for (const void* i : inputs) VQ_CHECK(*o != i, call + ": outputs may not alias inputs");
-        for (auto p = outputs.begin(); p != o; ++p) VQ_CHECK(*o != *p, call + ": outputs may not alias each other");
-    }
-    return VQ_OK;
-}
-
-#define VQ_MATRIX(a, rows, cols, ld, call, what) \
-    VQ_TRY(check_matrix((a), (rows), (cols), (ld), dtype, (call), (what), as_stream(stream)))
 
 }  // namespace
+
+vq_status pack_launch(const Packs& list, hipStream_t st)
+{
+    if (list.count == 0) return VQ_OK;
+    hipLaunchKernelGGL(k_pack, dim3((unsigned)list.blocks, list.count), dim3(256), 0, st, list);
+    VQ_LAUNCHED("k_pack");
+    return VQ_OK;
+}
+
 }  // namespace vq
 
 using namespace vq;
