@@ -1,0 +1,956 @@
+// Softmax cross entropy over a large vocabulary, its logits never kept (vq_cross_entropy,
+// vq_cross_entropy_backward).
+//
+//   z[t, v] = x_t . w_v,  lse_t = log sum_v exp z[t, v],  loss_t = lse_t - z[t, label_t]
+//   dz[t, v] = dloss_t (exp(z[t, v] - lse_t) - [v = label_t]),  dX = dz W,  dW = dz^T X
+//
+//   k_loss_index    the tokens that are learnt, one behind the other, and their labels
+//   k_loss_gather   their rows of X, 16-byte aligned
+//   k_loss_logits   the tiled product z; a wave's tile leaves of each token the largest
+//                   logit, the sum of exponentials below it, and the label's logit
+//   k_loss_few      the same for few tokens, the vocabulary read straight from memory
+//   k_loss_join     joins those pairs (m, s) in a fixed order: lse = m + log s
+//   k_loss_grad     the tiled product z again, for one piece of the vocabulary; dz from it
+//   k_loss_two      the piece's rows of dW and its part of dX in one launch
+//   k_loss_dx       dX from the sums, in the caller's order; zeros for the other tokens
+//
+// The forward pass reads X and W once a band of tiles and writes eight bytes a token and
+// 64 or 128 words of the vocabulary; the logits stay in the accumulators.  The backward
+// pass forms them again rather than keep them (6 T V N operations, 4 of them dX and dW)
+// and takes the vocabulary in pieces whose dz stays small enough to be read back from
+// the last-level cache.  dX is summed over the pieces in float32.
+//
+// Tokens whose label is ignore_index take no part: they are left out before the products
+// (a training batch may be half prompt), so nothing that their rows of X hold reaches a
+// result.  How many are left is known on the GPU alone: the grids are those of all
+// tokens, and workgroups past the count end at once.
+//
+// The logits and the sums of exponentials are float32; dz is rounded to the tensors'
+// type once, because the matrix cores read it in it.  In fp16 it is first multiplied by
+// a power of two that brings the largest |dloss| to 2^13, and dX and dW by its inverse: so
+// probabilities down to 2^-27 keep fp16's full precision.
+#include "vq_few.h"
+#include "vq_tile.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace vq {
+namespace {
+
+constexpr int64_t kMaxLossTokens = 1 << 20;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int64_t kPieceBytes = 128 << 20;      // of dz, or of a packed piece of W
+
+// What the index kernel leaves in front of the workspace.
+struct Head {
+    int count;                   // tokens learnt
+    float scale, inverse;        // dz's power of two
+};
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// (m, s) stands for s e^m.  Where every logit was -inf, m is -inf and s 0.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
+{
+    const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
+    s = s * exp_of(m - base) + s2 * exp_of(m2 - base);
+    m = top;
+}
+
+struct Index {
+    const int64_t* labels;
+    int64_t T, V, ignore;
+    Head* head;
+    int* order;                  // token of each place
+    int* label;                  // of each place; -1: outside the vocabulary
+    // forward
+    float* loss;                 // zeroed where ignored
+    float* lse;
+    // backward
+    int* place;                  // of each token; -1: ignored
+    const float* dloss;
+    const float* lse_in;
+    float* g;                    // dloss and lse of each place
+    float* lse_at;
+    int scaled;                  // whether dz takes a power of two
+};
+
+// One workgroup; a thread takes a run of consecutive tokens.
+__global__ __launch_bounds__(1024) void k_loss_index(const Index a)
+{
+    __shared__ int sums[16];
+    __shared__ float tops[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t per = (a.T + 1023) / 1024, t0 = threadIdx.x * per, t1 = t0 + per < a.T ? t0 + per : a.T;
+    int n = 0;
+    float top = 0.0f;
+    for (int64_t t = t0; t < t1; ++t) {
+        const bool on = a.labels[t] != a.ignore;
+        n += on;
+        if (a.scaled && on) top = fmaxf(top, fabsf(a.dloss[t]));
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(upto, o);
+        if (lane >= o) upto += v;
+        top = fmaxf(top, __shfl_xor(top, o));
+    }
+    if (lane == 63) sums[wave] = upto;
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    int at = upto - n, all = 0;
+    for (int w = 0; w < 16; ++w) {
+        if (w < wave) at += sums[w];
+        all += sums[w];
+        top = fmaxf(top, tops[w]);
+    }
+    float scale = 1.0f;
+    if (a.scaled && top > 0.0f && top < INFINITY) {
+        const int e = 13 - ilogbf(top);
+        scale = ldexpf(1.0f, e < -100 ? -100 : e > 100 ? 100 : e);
+    }
+    if (threadIdx.x == 0) *a.head = Head{all, scale, 1.0f / scale};
+    for (int64_t t = t0; t < t1; ++t) {
+        const int64_t l = a.labels[t];
+        const bool on = l != a.ignore;
+        if (a.place) a.place[t] = on ? at : -1;
+        if (!on) {
+            if (a.loss) a.loss[t] = a.lse[t] = 0.0f;
+            continue;
+        }
+        const bool known = l >= 0 && l < a.V;
+        a.order[at] = (int)t;
+        a.label[at] = known ? (int)l : -1;
+        if (a.g) {
+            a.g[at] = known ? a.dloss[t] * scale : NAN;
+            a.lse_at[at] = a.lse_in[t];
+        }
+        ++at;
+    }
+}
+
+// Row `place` of the learnt tokens' matrix; columns to its pitch are zeros.
+__global__ __launch_bounds__(256) void k_loss_gather(const Head* head, const int* __restrict__ order, const Pack m)
+{
+    const int q = blockIdx.x;
+    if (q >= head->count) return;
+    const uint16_t* row = m.s + (int64_t)order[q] * m.ld;
+    uint16_t* o = m.o + (int64_t)q * m.ldp;
+    for (int c = threadIdx.x * 8; c < m.ldp; c += 256 * 8) {
+        alignas(16) uint16_t v[8];
+        if (c + 8 <= m.cols) {
+            if (m.odd) {
+                Words w;
+                w.load(row + c);
+                const uint4 u = w.get(row + c);
+                __builtin_memcpy(v, &u, 16);
+            } else {
+                __builtin_memcpy(v, row + c, 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < m.cols ? row[c + i] : (uint16_t)0;
+        }
+        *reinterpret_cast<uint4*>(o + c) = *reinterpret_cast<const uint4*>(v);
+    }
+}
+
+// The tiled product of a piece of W (rows v0 .. of the vocabulary) and the learnt tokens.
+struct Logits {
+    Tile t;                      // nq: all tokens
+    const Head* head;
+    const int* label;
+    int v0;
+    // forward
+    float2* part;                // [waves' columns of tiles][tokens]
+    int64_t pitch;               // tokens a row of it
+    float* picked;               // the labels' logits
+    // backward
+    const float* lse;
+    const float* g;
+    void* dz;                    // [places][ldz], zeros past the piece
+    int64_t ldz;
+};
+
+// The tile's sums; false where the grid's place holds none.
+template <class L>
+__device__ __forceinline__ bool logits_tile(const Tile& full, int n, int& p0, int& q0, int& tp, int wave, int lane, char* pb0,
+                                            char* pb1, char* qb0, char* qb1, f32x4 (&acc)[L::kFP][L::kFQ])
+{
+    Tile t = full;
+    t.nq = n;
+    const int ntq = (n + L::BQ - 1) / L::BQ, tiles = t.ntp * ntq;
+    if ((int)blockIdx.x >= tiles) return false;
+    int tq;
+    pick_tile(blockIdx.x, tiles, t.ntp, ntq, tp, tq);
+    p0 = tp * L::BP;
+    q0 = tq * L::BQ;
+#pragma unroll
+    for (int i = 0; i < L::kFP; ++i)
+#pragma unroll
+        for (int j = 0; j < L::kFQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    L::run(t, p0, q0, 0, 0, (t.steps + 1) / 2 * 2, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
+    return true;
+}
+
+template <class T, int FP, int FQ>
+__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_logits(const Logits a)
+{
+    typedef Main<T, false, false, FP, FQ, false> L;
+    VQ_TILE_BUFFERS(L);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave / kWQ, wq = wave % kWQ;
+    const int n = a.head->count;
+    int p0, q0, tp;
+    f32x4 acc[FP][FQ];
+    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc)) return;
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));               // no load into LDS outlives the workgroup
+
+    // lane l: token l%16 of fragment j, words 4*(l/16) .. +3 of fragment i
+    const int first = p0 + wp * FP * 16, quad = lane >> 4;
+    if (first + FP * 16 > a.t.np) {
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (first + i * 16 + quad * 4 + r >= a.t.np)
+#pragma unroll
+                    for (int j = 0; j < FQ; ++j) acc[i][j][r] = -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+        const int q = q0 + (wq * FQ + j) * 16 + (lane & 15);
+        const int want = q < n ? a.label[q] - a.v0 - first : -1;
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float base = m == -INFINITY ? 0.0f : m;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s += exp_of(acc[i][j][r] - base);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (quad == 0 && q < n) a.part[(int64_t)(tp * kWP + wp) * a.pitch + q] = make_float2(m, s);
+        if (want >= 0 && want < FP * 16 && (want >> 2 & 3) == quad) {
+            float z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) z = want == i * 16 + quad * 4 + r ? acc[i][j][r] : z;
+            a.picked[q] = z;
+        }
+    }
+}
+
+template <class T, int FP, int FQ>
+__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_grad(const Logits a)
+{
+    typedef Main<T, false, false, FP, FQ, false> L;
+    VQ_TILE_BUFFERS(L);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = a.head->count;
+    int p0, q0, tp;
+    f32x4 acc[FP][FQ];
+    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc)) return;
+    each_row<L>(acc, p0, q0, (int)a.ldz, n, wave, lane, pb0, pb1, qb0, qb1, [&](int q, int p, float (&v)[8], float (&)[8]) {
+        const float lse = a.lse[q], g = a.g[q];
+        const int want = a.label[q] - a.v0 - p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float e = exp_of(v[i] - lse);
+            v[i] = p + i < a.t.np ? (i == want ? e - 1.0f : e) * g : 0.0f;
+        }
+        store8<T>(a.dz, a.ldz, q, p, (int)a.ldz, v);
+    });
+}
+
+// Few tokens: a wave takes 16 rows of W whole, a workgroup 64, tokens as they come.
+struct FewLogits {
+    const char* W;
+    const char* X;
+    int64_t ldw, ldx, K;
+    int V, T;
+    const int64_t* labels;
+    float2* part;                // [workgroups][T]
+    float* picked;
+};
+
+template <class T, int NT, int H, bool ODD>
+__global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
+{
+    typedef typename T::E E;
+    constexpr int B = 32 * H;
+    __shared__ float2 sh[4][NT * 16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int m0 = blockIdx.x * 64 + wave * 16;
+    const int64_t row = m0 + r < a.V ? m0 + r : a.V - 1;         // rows and tokens past the last repeat it
+    const E* const w = reinterpret_cast<const E*>(a.W) + row * a.ldw;
+    const E* x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        x[n] = reinterpret_cast<const E*>(a.X) + (int64_t)(n * 16 + r < a.T ? n * 16 + r : a.T - 1) * a.ldx;
+    f32x4 acc[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int nfull = (int)(a.K / B);
+    Ahead<T, ODD> wv[H], xv[NT][H];
+    const auto load = [&](int kb, int j) {
+        const int64_t c = (int64_t)kb * B + j * 32 + g * 8;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xv[n][j].load(x[n], c);
+        wv[j].load(w, c);
+    };
+    const auto multiply = [&](int j) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] = T::mfma(wv[j].get(w), xv[n][j].get(x[n]), acc[n]);
+    };
+    if (nfull > 0) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            load(0, j);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll 1
+        for (int kb = 0; kb + 1 < nfull; ++kb) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                multiply(j);
+                __builtin_amdgcn_sched_barrier(0);
+                load(kb + 1, j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) multiply(j);
+    }
+    for (int64_t c0 = (int64_t)nfull * B; c0 < a.K; c0 += 32) {
+        const int64_t c = c0 + g * 8;
+        const typename T::V8 v = chunk_tail<T>(w, c, a.K);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] = T::mfma(v, chunk_tail<T>(x[n], c, a.K), acc[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int t = n * 16 + r;
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (m0 + g * 4 + i < a.V) m = fmaxf(m, acc[n][i]);
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (m0 + g * 4 + i < a.V) s += exp_of(acc[n][i] - base);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (g == 0) sh[wave][t] = make_float2(m, s);
+        if (t < a.T) {
+            const int64_t want = a.labels[t] - m0 - g * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (want == i && m0 + g * 4 + i < a.V) a.picked[t] = acc[n][i];
+        }
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < a.T) {
+        float m = sh[0][t].x, s = sh[0][t].y;
+#pragma unroll
+        for (int k = 1; k < 4; ++k) join(m, s, sh[k][t].x, sh[k][t].y);
+        a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(m, s);
+    }
+}
+
+// Sixteen tokens a workgroup, 64 threads a token: each joins every 64th part, then a tree.
+struct Join {
+    const float2* part;
+    int parts;
+    int64_t pitch;
+    const Head* head;            // or null: every token, ignored ones among them
+    const int* order;
+    const int64_t* labels;
+    const float* picked;
+    int64_t T, V, ignore;
+    float* loss;
+    float* lse;
+};
+
+__global__ __launch_bounds__(1024) void k_loss_join(const Join a)
+{
+    __shared__ float2 sh[64][16];
+    const int n = a.head ? a.head->count : (int)a.T;
+    const int k = threadIdx.x & 15, slice = threadIdx.x >> 4;
+    const int q = blockIdx.x * 16 + k;
+    if (blockIdx.x * 16 >= n) return;
+    float m = -INFINITY, s = 0.0f;
+    if (q < n) {
+#pragma unroll 4
+        for (int p = slice; p < a.parts; p += 64) {
+            const float2 v = a.part[(int64_t)p * a.pitch + q];
+            join(m, s, v.x, v.y);
+        }
+    }
+    sh[slice][k] = make_float2(m, s);
+    __syncthreads();
+#pragma unroll
+    for (int h = 32; h > 0; h >>= 1) {
+        if (slice < h) {
+            const float2 v = sh[slice + h][k];
+            join(m, s, v.x, v.y);
+            sh[slice][k] = make_float2(m, s);
+        }
+        __syncthreads();
+    }
+    if (slice != 0 || q >= n) return;
+    const int64_t t = a.head ? a.order[q] : q, label = a.labels[t];
+    const float lse = m + logf(s);
+    const bool on = label != a.ignore;
+    a.lse[t] = on ? lse : 0.0f;
+    a.loss[t] = !on ? 0.0f : label >= 0 && label < a.V ? lse - a.picked[q] : NAN;
+}
+
+// dX's sums and dW's rows of a piece.
+struct Grads {
+    Tile x, w;                   // nq of x, k of w: all tokens
+    const Head* head;
+    float* sums;                 // [splits of x][tokens][pitch]
+    int64_t plane;
+    int add;                     // to what the pieces before left there
+    void* dW;                    // the piece's rows
+    int64_t lddw;
+    int with_x, with_w, w_first;
+};
+
+template <class T, int FP, int FQ>
+__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_two(const Grads a)
+{
+    typedef Main<T, true, false, FP, FQ, false> LX;
+    typedef Main<T, true, true, FP, FQ, false> LW;
+    VQ_TILE_BUFFERS(LW);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = a.head->count;
+    const int ntq_x = (n + LX::BQ - 1) / LX::BQ, tiles_x = a.x.ntp * ntq_x;
+    const int nx = a.with_x ? tiles_x * a.x.splits : 0, nw = a.with_w ? a.w.ntp * a.w.ntq : 0;
+    const int id = blockIdx.x, first = a.w_first ? nw : nx;
+    if (id >= nx + nw) return;
+    const int at = id < first ? id : id - first;
+    f32x4 acc[FP][FQ];
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int tp, tq;
+    if ((id < first) != (a.w_first != 0)) {
+        Tile t = a.x;
+        t.nq = n;
+        const int split = at / tiles_x, pairs = (t.steps + 1) / 2;
+        pick_tile(at % tiles_x, tiles_x, t.ntp, ntq_x, tp, tq);
+        const int p0 = tp * LX::BP, q0 = tq * LX::BQ;
+        const int s0 = 2 * (int)((int64_t)pairs * split / t.splits), s1 = 2 * (int)((int64_t)pairs * (split + 1) / t.splits);
+        LX::run(t, p0, q0, 0, s0, s1, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
+        float* const o = a.sums + split * a.plane;
+        const int wp = wave / kWQ, wq = wave % kWQ;
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const int q = q0 + (wq * FQ + j) * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < FP; ++i) {
+                const int p = p0 + (wp * FP + i) * 16 + (lane >> 4) * 4;
+                if (q >= n || p >= t.np) continue;
+                f32x4* const at = reinterpret_cast<f32x4*>(o + (int64_t)q * t.pitch + p);
+                if (a.add) acc[i][j] += *at;
+                *at = acc[i][j];
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));           // no load into LDS outlives the workgroup
+    } else {
+        Tile t = a.w;
+        t.kP = t.kQ = n;
+        t.steps = t.seg_steps = (n + kBK - 1) / kBK;
+        pick_tile(at, nw, t.ntp, t.ntq, tp, tq);
+        const int p0 = tp * LW::BP, q0 = tq * LW::BQ;
+        LW::run(t, p0, q0, 0, 0, (t.steps + 1) / 2 * 2, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
+        const float scale = a.head->inverse;
+        each_row<LW>(acc, p0, q0, t.np, t.nq, wave, lane, pb0, pb1, qb0, qb1, [&](int q, int p, float (&v)[8], float (&)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= scale;
+            store8<T>(a.dW, a.lddw, q, p, t.np, v);
+        });
+    }
+}
+
+// A token's row of dX: the sums' parts in order, eight columns a thread.
+struct TokenGrads {
+    const float* sums;
+    int splits, pitch, N;
+    int64_t plane, T, ldx;
+    const Head* head;
+    const int* place;
+    void* dX;
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_loss_dx(const TokenGrads a)
+{
+    const int per = a.pitch / 8;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= per * a.T) return;
+    const int64_t t = e / per;
+    const int p = (int)(e - t * per) * 8, q = a.place[t];
+    float s[8] = {};
+    if (q >= 0) {
+        const float* o = a.sums + (int64_t)q * a.pitch + p;
+#pragma unroll 4
+        for (int z = 0; z < a.splits; ++z) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(o + z * a.plane + h * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[h * 4 + i] += v[i];
+            }
+        }
+        const float scale = a.head->inverse;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] *= scale;
+    }
+    store8<T>(a.dX, a.ldx, t, p, a.N, s);
+}
+
+// ---- plan -------------------------------------------------------------------
+// Tiles of 256 x 256 (one on a CU) or 128 x 128 (two), by the tiled products' model of
+// microseconds: 1.45 a step and 10 a tile, or 0.8 (alone on a CU) and 1.15 and 4.
+struct Shape {
+    int small, bp, bq;
+};
+Shape shape(int small) { return {small, small ? 128 : 256, small ? 128 : 256}; }
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+double tiles_cost(int small, int64_t tiles, double steps)
+{
+    if (!small) return (double)up(tiles, 256) * (steps * 1.45 + 10.0);
+    const int64_t rest = tiles % 512;
+    return (double)(tiles / 512) * (steps * 1.15 + 4.0) + (rest ? steps * (rest <= 256 ? 0.8 : 1.15) + 4.0 : 0.0);
+}
+
+Shape logits_shape(int64_t V, int64_t T, int64_t N)
+{
+    const double st = 2.0 * up(up(N, kBK), 2);
+    const double big = tiles_cost(0, up(V, 256) * up(T, 256), st), little = tiles_cost(1, up(V, 128) * up(T, 128), st);
+    return shape(little < big);
+}
+
+// Both gradients of a piece in one launch: the shape, and how many parts dX's sums are in.
+struct GradPlan {
+    Shape s;
+    int splits, w_first;
+};
+GradPlan grad_plan(int64_t Vp, int64_t T, int64_t N, bool with_x, bool with_w)
+{
+    GradPlan best{};
+    double least = 1e300;
+    const int64_t px = up(up(Vp, kBK), 2), pw = up(up(T, kBK), 2);
+    for (int small = 0; small < 2; ++small) {
+        const Shape s = shape(small);
+        const int64_t tx = with_x ? up(N, s.bp) * up(T, s.bq) : 0, tw = with_w ? up(N, s.bp) * up(Vp, s.bq) : 0;
+        const int slots = small ? 512 : 256;
+        for (int sx = 1; sx <= 16 && sx <= px; ++sx) {
+            const double per = small ? (tx * sx + tw <= 256 ? 0.8 : 1.15) : 1.45, round = small ? 4.0 : 10.0;
+            const double cx = tx ? 2.0 * up(px, sx) * per + round : 0.0, cw = tw ? 2.0 * pw * per + round : 0.0;
+            // the longer ones first, the shorter ones fill the last round
+            double t = std::max((cx * tx * sx + cw * tw) / slots + 0.5 * std::min(cx, cw), std::max(cx, cw));
+            t += 0.8e-6 * (double)T * N * (with_x ? sx : 0);
+            if (t < least) {
+                least = t;
+                best = {s, sx, cw > cx};
+            }
+            if (!with_x) break;
+        }
+    }
+    return best;
+}
+
+// Words of a piece: a multiple of 256, pieces of nearly one size.
+int64_t piece(int64_t V, int64_t bytes_a_word)
+{
+    const int64_t n = up(V * bytes_a_word, kPieceBytes);
+    return std::min(up(up(V, n), 256) * 256, up(V, 8) * 8);
+}
+
+Tile tile_of(const void* P, int64_t ldp, int64_t kP, int64_t np, int64_t wp, const void* Q, int64_t ldq, int64_t kQ, int64_t nq,
+             int64_t wq, const Shape& s)
+{
+    Tile t{};
+    t.P[0] = t.P[1] = static_cast<const char*>(P);
+    t.Q[0] = t.Q[1] = static_cast<const char*>(Q);
+    t.ldp = (int)ldp; t.ldq = (int)ldq;
+    t.kP = (int)kP; t.kQ = (int)kQ;
+    t.np = (int)np; t.nq = (int)nq;
+    t.wp = (int)wp; t.wq = (int)wq;
+    t.ntp = (int)up(np, s.bp); t.ntq = (int)up(nq, s.bq);
+    t.steps = t.seg_steps = (int)up(std::min(kP, kQ), kBK);
+    t.splits = 1;
+    return t;
+}
+
+struct Loss {
+    int64_t T, V, N;
+    int dtype;
+    const void* X; int64_t ldx;
+    const void* W; int64_t ldw;
+    const int64_t* labels; int64_t ignore;
+    // forward
+    float* loss;
+    float* lse;
+    // backward
+    const float* dloss;
+    const float* lse_in;
+    void* dX; int64_t lddx;
+    void* dW; int64_t lddw;
+};
+
+// The learnt tokens' order, labels and rows of X, in the workspace.
+struct Tokens {
+    Head* head;
+    int* order;
+    int* label;
+    uint16_t* x;
+    int64_t ldx;
+    void take(Arena& ws, const Loss& a)
+    {
+        ldx = round8(a.N);
+        head = static_cast<Head*>(ws.take(sizeof(Head)));
+        order = static_cast<int*>(ws.take(a.T * sizeof(int)));
+        label = static_cast<int*>(ws.take(a.T * sizeof(int)));
+        x = static_cast<uint16_t*>(ws.take(a.T * ldx * 2));
+    }
+    vq_status launch(const Loss& a, Index ix, hipStream_t st) const
+    {
+        ix.labels = a.labels;
+        ix.T = a.T; ix.V = a.V; ix.ignore = a.ignore;
+        ix.head = head; ix.order = order; ix.label = label;
+        hipLaunchKernelGGL(k_loss_index, dim3(1), dim3(1024), 0, st, ix);
+        VQ_LAUNCHED("k_loss_index");
+        const Pack p{static_cast<const uint16_t*>(a.X), x, a.T, a.ldx, ldx, (int)a.N, odd_rows(a.X, a.ldx)};
+        hipLaunchKernelGGL(k_loss_gather, dim3((unsigned)a.T), dim3(256), 0, st, head, order, p);
+        VQ_LAUNCHED("k_loss_gather");
+        return VQ_OK;
+    }
+};
+
+// Rows v0 .. v0 + n of W as the tiles read them: in place, or copied to `copy`.
+vq_status words(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, Mat& out, hipStream_t st)
+{
+    const uint16_t* p = static_cast<const uint16_t*>(a.W) + v0 * a.ldw;
+    out = {p, n, a.N, a.ldw};
+    if (!copy) return VQ_OK;
+    const int64_t ldp = round8(a.N);
+    Packs k{};
+    k.m[0] = {p, copy, n, a.ldw, ldp, (int)a.N, odd_rows(p, a.ldw)};
+    k.count = 1;
+    k.blocks = pack_blocks(n * (ldp / 8));
+    out = {copy, n, ldp, ldp};
+    return pack_launch(k, st);
+}
+
+// Whether the vocabulary is read for few tokens straight from memory.
+bool few(const Loss& a) { return a.T <= 32; }
+
+template <class T, int NT, int H>
+void few_launch(const FewLogits& f, bool odd, int groups, hipStream_t st)
+{
+    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true>), dim3(groups), dim3(256), 0, st, f);
+    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false>), dim3(groups), dim3(256), 0, st, f);
+}
+
+template <class T>
+void few_tokens_launch(const FewLogits& f, bool odd, int groups, hipStream_t st)
+{
+    if (f.T > 16) few_launch<T, 2, 4>(f, odd, groups, st);
+    else few_launch<T, 1, 8>(f, odd, groups, st);
+}
+
+template <class T>
+void logits_launch(const Logits& g, const Shape& s, bool backward, hipStream_t st)
+{
+    const dim3 grid((unsigned)(g.t.ntp * g.t.ntq));
+    if (s.small) {
+        if (backward) hipLaunchKernelGGL((k_loss_grad<T, 4, 2>), grid, dim3(kThreads), 0, st, g);
+        else hipLaunchKernelGGL((k_loss_logits<T, 4, 2>), grid, dim3(kThreads), 0, st, g);
+    } else {
+        if (backward) hipLaunchKernelGGL((k_loss_grad<T, 8, 4>), grid, dim3(kThreads), 0, st, g);
+        else hipLaunchKernelGGL((k_loss_logits<T, 8, 4>), grid, dim3(kThreads), 0, st, g);
+    }
+}
+
+vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
+{
+    if (a.T == 0) return VQ_OK;
+    Join j{};
+    j.labels = a.labels;
+    j.T = a.T; j.V = a.V; j.ignore = a.ignore;
+    j.loss = a.loss; j.lse = a.lse;
+    j.pitch = a.T;
+    if (few(a)) {
+        j.parts = (int)up(a.V, 64);
+        float2* part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
+        float* picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
+        if (!run) return VQ_OK;
+        const FewLogits f{static_cast<const char*>(a.W), static_cast<const char*>(a.X), a.ldw, a.ldx, a.N, (int)a.V, (int)a.T,
+                          a.labels, part, picked};
+        const bool odd = odd_rows(a.W, a.ldw) || odd_rows(a.X, a.ldx);
+        if (a.dtype == VQ_BF16) few_tokens_launch<Bf16>(f, odd, j.parts, st);
+        else few_tokens_launch<F16>(f, odd, j.parts, st);
+        VQ_LAUNCHED("k_loss_few");
+        j.part = part; j.picked = picked;
+    } else {
+        Tokens tk;
+        tk.take(ws, a);
+        const bool copied = !loads_ok({a.W, a.V, a.N, a.ldw});
+        const int64_t Vp = copied ? piece(a.V, 2 * round8(a.N)) : a.V;
+        uint16_t* copy = copied ? static_cast<uint16_t*>(ws.take(Vp * round8(a.N) * 2)) : nullptr;
+        const Shape s = logits_shape(Vp, a.T, a.N);
+        const int per = kWP * (int)up(Vp, s.bp);              // parts of a piece
+        j.parts = 0;
+        for (int64_t v0 = 0; v0 < a.V; v0 += Vp) j.parts += kWP * (int)up(std::min(Vp, a.V - v0), s.bp);
+        float2* part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
+        float* picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
+        if (!run) return VQ_OK;
+        Index ix{};
+        ix.loss = a.loss; ix.lse = a.lse;
+        VQ_TRY(tk.launch(a, ix, st));
+        for (int64_t v0 = 0, k = 0; v0 < a.V; v0 += Vp, ++k) {
+            const int64_t n = std::min(Vp, a.V - v0);
+            Mat w;
+            VQ_TRY(words(a, v0, n, copy, w, st));
+            Logits g{};
+            g.t = tile_of(w.p, w.ld, w.cols, n, 0, tk.x, tk.ldx, tk.ldx, a.T, 0, s);
+            g.head = tk.head; g.label = tk.label;
+            g.v0 = (int)v0;
+            g.part = part + k * per * a.T; g.pitch = a.T; g.picked = picked;
+            if (a.dtype == VQ_BF16) logits_launch<Bf16>(g, s, false, st);
+            else logits_launch<F16>(g, s, false, st);
+            VQ_LAUNCHED("k_loss_logits");
+        }
+        j.part = part; j.picked = picked;
+        j.head = tk.head; j.order = tk.order;
+    }
+    hipLaunchKernelGGL(k_loss_join, dim3((unsigned)up(a.T, 16)), dim3(1024), 0, st, j);
+    VQ_LAUNCHED("k_loss_join");
+    return VQ_OK;
+}
+
+template <class T>
+void grads_launch(const Grads& g, const GradPlan& p, hipStream_t st)
+{
+    const dim3 grid((unsigned)((g.with_x ? g.x.ntp * g.x.ntq * g.x.splits : 0) + (g.with_w ? g.w.ntp * g.w.ntq : 0)));
+    if (p.s.small) hipLaunchKernelGGL((k_loss_two<T, 4, 2>), grid, dim3(kThreads), 0, st, g);
+    else hipLaunchKernelGGL((k_loss_two<T, 8, 4>), grid, dim3(kThreads), 0, st, g);
+}
+
+__global__ __launch_bounds__(256) void k_loss_zero(uint16_t* __restrict__ o, int64_t rows, int64_t cols, int64_t ld)
+{
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < rows * cols; e += (int64_t)gridDim.x * 256)
+        o[e / cols * ld + e % cols] = 0;
+}
+
+vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
+{
+    if (!a.dX && !a.dW) return VQ_OK;
+    if (a.T == 0) {
+        if (run && a.dW) {
+            hipLaunchKernelGGL(k_loss_zero, dim3((unsigned)std::min<int64_t>(up(a.V * a.N, 256), 65536)), dim3(256), 0, st,
+                               static_cast<uint16_t*>(a.dW), a.V, a.N, a.lddw);
+            VQ_LAUNCHED("k_loss_zero");
+        }
+        return VQ_OK;
+    }
+    Tokens tk;
+    tk.take(ws, a);
+    int* place = static_cast<int*>(ws.take(a.T * sizeof(int)));
+    float* g = static_cast<float*>(ws.take(a.T * sizeof(float)));
+    float* lse = static_cast<float*>(ws.take(a.T * sizeof(float)));
+    const int64_t N8 = round8(a.N);
+    const bool copied = !loads_ok({a.W, a.V, a.N, a.ldw});
+    const int64_t Vp = piece(a.V, 2 * (copied ? std::max(a.T, N8) : a.T));
+    uint16_t* copy = copied ? static_cast<uint16_t*>(ws.take(Vp * N8 * 2)) : nullptr;
+    void* dz = ws.take(a.T * Vp * 2);
+    const GradPlan plan = grad_plan(std::min(Vp, a.V), a.T, a.N, a.dX, a.dW);
+    float* sums = a.dX ? static_cast<float*>(ws.take(plan.splits * a.T * N8 * sizeof(float))) : nullptr;
+    if (!run) return VQ_OK;
+    Index ix{};
+    ix.place = place;
+    ix.dloss = a.dloss; ix.lse_in = a.lse_in;
+    ix.g = g; ix.lse_at = lse;
+    ix.scaled = a.dtype == VQ_F16;
+    VQ_TRY(tk.launch(a, ix, st));
+    for (int64_t v0 = 0; v0 < a.V; v0 += Vp) {
+        const int64_t n = std::min(Vp, a.V - v0), n8 = round8(n);
+        Mat w;
+        VQ_TRY(words(a, v0, n, copy, w, st));
+        const Shape s = logits_shape(n, a.T, a.N);
+        Logits l{};
+        l.t = tile_of(w.p, w.ld, w.cols, n, 0, tk.x, tk.ldx, tk.ldx, a.T, 0, s);
+        l.head = tk.head; l.label = tk.label;
+        l.v0 = (int)v0;
+        l.lse = lse; l.g = g;
+        l.dz = dz; l.ldz = n8;
+        Grads b{};
+        // dX: sum over the piece's words of W[word, column] dz[token, word]
+        b.x = tile_of(w.p, w.ld, n, a.N, w.cols, dz, n8, n8, a.T, 0, plan.s);
+        b.x.pitch = (int)N8;
+        b.x.splits = std::min<int>(plan.splits, (b.x.steps + 1) / 2);
+        // dW: sum over the tokens of X[token, column] dz[token, word]
+        b.w = tile_of(tk.x, tk.ldx, a.T, a.N, tk.ldx, dz, n8, a.T, n, n8, plan.s);
+        b.head = tk.head;
+        b.sums = sums;
+        b.plane = a.T * N8;
+        b.add = v0 > 0;
+        b.dW = a.dW ? static_cast<uint16_t*>(a.dW) + v0 * a.lddw : nullptr;
+        b.lddw = a.lddw;
+        b.with_x = a.dX != nullptr; b.with_w = a.dW != nullptr;
+        b.w_first = plan.w_first;
+        if (a.dtype == VQ_BF16) {
+            logits_launch<Bf16>(l, s, true, st);
+            VQ_LAUNCHED("k_loss_grad");
+            grads_launch<Bf16>(b, plan, st);
+        } else {
+            logits_launch<F16>(l, s, true, st);
+            VQ_LAUNCHED("k_loss_grad");
+            grads_launch<F16>(b, plan, st);
+        }
+        VQ_LAUNCHED("k_loss_two");
+    }
+    if (!a.dX) return VQ_OK;
+    const TokenGrads d{sums, std::min<int>(plan.splits, (int)up(up(std::min(Vp, a.V), kBK), 2)), (int)N8, (int)a.N, a.T * N8, a.T,
+                       a.lddx, tk.head, place, a.dX};
+    const dim3 grid((unsigned)up(a.T * (N8 / 8), 256));
+    if (a.dtype == VQ_BF16) hipLaunchKernelGGL((k_loss_dx<Bf16>), grid, dim3(256), 0, st, d);
+    else hipLaunchKernelGGL((k_loss_dx<F16>), grid, dim3(256), 0, st, d);
+    VQ_LAUNCHED("k_loss_dx");
+    return VQ_OK;
+}
+
+vq_status check_sizes(const std::string& call, int64_t T, int64_t V, int64_t N, int dtype)
+{
+    VQ_CHECK(T >= 0 && T <= kMaxLossTokens, call + ": T must be in [0, 2^20]");
+    VQ_CHECK(V >= 1 && V <= kMaxSize && N >= 1 && N <= kMaxSize, call + ": V and N must be in [1, 2^20]");
+    VQ_CHECK(dtype == VQ_BF16 || dtype == VQ_F16, call + ": dtype must be VQ_BF16 or VQ_F16");
+    return VQ_OK;
+}
+
+vq_status check_vector(const std::string& call, const char* what, const void* p, size_t align)
+{
+    VQ_CHECK(reinterpret_cast<uintptr_t>(p) % align == 0, call + ": " + what + " is not aligned to its elements");
+    return VQ_OK;
+}
+
+}  // namespace
+}  // namespace vq
+
+using namespace vq;
+
+extern "C" {
+
+size_t vq_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t N, const void* W, int64_t ldw)
+{
+    if (check_sizes("vq_cross_entropy", T, V, N, VQ_BF16) != VQ_OK) return 0;
+    Loss a{};
+    a.T = T; a.V = V; a.N = N;
+    a.W = W; a.ldw = ldw;
+    Arena ws{nullptr};
+    return forward(a, ws, false, nullptr) == VQ_OK ? ws.used : 0;
+}
+
+vq_status vq_cross_entropy(int64_t T, int64_t V, int64_t N, int dtype, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                           const int64_t* labels, int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                           void* stream)
+{
+    const char* call = "vq_cross_entropy";
+    VQ_TRY(check_sizes(call, T, V, N, dtype));
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(X && W && labels && loss && lse, "vq_cross_entropy: null pointer");
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "W", W, ldw, N));
+    VQ_TRY(check_vector(call, "labels", labels, 8));
+    VQ_TRY(check_vector(call, "loss", loss, 4));
+    VQ_TRY(check_vector(call, "lse", lse, 4));
+    VQ_TRY(check_apart(call, {loss, lse}, {X, W, labels}));
+    Loss a{};
+    a.T = T; a.V = V; a.N = N; a.dtype = dtype;
+    a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
+    a.labels = labels; a.ignore = ignore_index;
+    a.loss = loss; a.lse = lse;
+    Arena count{nullptr};
+    VQ_TRY(forward(a, count, false, as_stream(stream)));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, count.used));
+    VQ_TRY(check_device());
+    VQ_MATRIX(X, T, N, ldx, call, "X");
+    VQ_MATRIX(W, V, N, ldw, call, "W");
+    TimedRegion tr("cross_entropy", 0, as_stream(stream));
+    Arena w{static_cast<char*>(ws)};
+    return forward(a, w, true, as_stream(stream));
+}
+
+size_t vq_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int64_t N, const void* W, int64_t ldw, int want_dx,
+                                                 int want_dw)
+{
+    if (check_sizes("vq_cross_entropy_backward", T, V, N, VQ_BF16) != VQ_OK) return 0;
+    void* const on = reinterpret_cast<void*>(uintptr_t(16));      // counted, never used
+    Loss a{};
+    a.T = T; a.V = V; a.N = N;
+    a.W = W; a.ldw = ldw;
+    a.dX = want_dx ? on : nullptr; a.dW = want_dw ? on : nullptr;
+    Arena ws{nullptr};
+    return backward(a, ws, false, nullptr) == VQ_OK ? ws.used : 0;
+}
+
+vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, const float* dloss, const void* X, int64_t ldx,
+                                    const void* W, int64_t ldw, const int64_t* labels, int64_t ignore_index, const float* lse,
+                                    void* dX, int64_t lddx, void* dW, int64_t lddw, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_cross_entropy_backward";
+    VQ_TRY(check_sizes(call, T, V, N, dtype));
+    VQ_CHECK(T == 0 || (!dX && !dW) || (dloss && X && W && labels && lse), "vq_cross_entropy_backward: null pointer");
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "W", W, ldw, N));
+    VQ_TRY(check_ld(call, "dX", dX, lddx, N));
+    VQ_TRY(check_ld(call, "dW", dW, lddw, N));
+    VQ_TRY(check_vector(call, "labels", labels, 8));
+    VQ_TRY(check_vector(call, "dloss", dloss, 4));
+    VQ_TRY(check_vector(call, "lse", lse, 4));
+    VQ_TRY(check_apart(call, {dX, dW}, {X, W, labels, dloss, lse}));
+    Loss a{};
+    a.T = T; a.V = V; a.N = N; a.dtype = dtype;
+    a.X = X; a.ldx = ldx; a.W = W; a.ldw = ldw;
+    a.labels = labels; a.ignore = ignore_index;
+    a.dloss = dloss; a.lse_in = lse;
+    a.dX = dX; a.lddx = lddx; a.dW = dW; a.lddw = lddw;
+    Arena count{nullptr};
+    VQ_TRY(backward(a, count, false, as_stream(stream)));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, count.used));
+    if ((T > 0 && dX) || dW) VQ_TRY(check_device());
+    if (dX || dW) {
+        VQ_VALUES(dloss, T, false, call, "dloss");
+        VQ_VALUES(lse, T, false, call, "lse");
+        VQ_MATRIX(X, T, N, ldx, call, "X");
+        VQ_MATRIX(W, V, N, ldw, call, "W");
+    }
+    TimedRegion tr("cross_entropy_backward", 0, as_stream(stream));
+    Arena w{static_cast<char*>(ws)};
+    return backward(a, w, true, as_stream(stream));
+}
+
+}  // extern "C"

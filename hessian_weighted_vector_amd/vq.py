@@ -128,6 +128,11 @@ SIGNATURES = {
     "vq_qlinear": (_I, [_P, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "vq_qgated_workspace_bytes": (_SZ, [_I64, _I64, _I, _I64]),
     "vq_qgated": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "vq_cross_entropy_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _I64]),
+    "vq_cross_entropy": (_I, [_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
+    "vq_cross_entropy_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _I64, _I, _I]),
+    "vq_cross_entropy_backward": (_I, [_I64, _I64, _I64, _I, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64,
+                                       _P, _SZ, _P]),
     "vq_adamw_plan_bytes": (_SZ, [_P, _I64]),
     "vq_adamw_plan": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "vq_adamw": (_I, [_P, _D, _D, _D, _D, _D, _I64, _P, _P, _P, _P]),
@@ -834,6 +839,56 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X, dev)
     _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
     return H
+
+
+# ---- the loss over a vocabulary ---------------------------------------------------
+
+@functools.lru_cache(maxsize=4096)
+def _cross_entropy_need(T, V, N, w, ldw):
+    return load().vq_cross_entropy_workspace_bytes(T, V, N, w, ldw)
+
+
+@functools.lru_cache(maxsize=4096)
+def _cross_entropy_backward_need(*args):
+    return load().vq_cross_entropy_backward_workspace_bytes(*args)
+
+
+def cross_entropy(X, W, labels, ignore_index=-100, ws=None):
+    """(loss, lse), float32 [T] each: loss = lse - z[label], lse = log sum exp z, z = X W^T never kept.
+
+    X [T, N] and W [V, N] are bfloat16 or float16 (one type, rows may be strided), labels int64
+    [T].  Tokens whose label is ignore_index take no part: loss and lse are 0 there, whatever
+    X holds.  Another label outside [0, V) gives a NaN loss.  The reduction is the caller's:
+    loss.sum() / n, with dloss = 1 / n for cross_entropy_backward.
+    """
+    T, V, N = _dims(X, W)
+    dt, dev = _half(X, "X"), _home(X)
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    w, ldw = _matrix(W, V, N, X.dtype, dev, "W")
+    lab = _vector(labels, T, torch.int64, dev, "labels")
+    loss, lse = (torch.empty(T, device=X.device) for _ in range(2))
+    lib = load()
+    p, n, ws = _scratch(_cross_entropy_need(T, V, N, w & 15, ldw), ws, X, dev)
+    _check(lib.vq_cross_entropy(T, V, N, dt, x, ldx, w, ldw, lab, ignore_index, loss.data_ptr(), lse.data_ptr(), p, n, _stream()))
+    return loss, lse
+
+
+def cross_entropy_backward(dloss, X, W, labels, lse, ignore_index=-100, want_dx=True, want_dw=True, ws=None):
+    """(dX, dW) of sum(dloss * loss), dloss float32 [T], for the lse that cross_entropy returned; None where not wanted."""
+    T, V, N = _dims(X, W)
+    dt, dev = _half(X, "X"), _home(X)
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    w, ldw = _matrix(W, V, N, X.dtype, dev, "W")
+    g = _vector(dloss, T, torch.float32, dev, "dloss")
+    lab = _vector(labels, T, torch.int64, dev, "labels")
+    ls = _vector(lse, T, torch.float32, dev, "lse")
+    dX = X.new_empty((T, N)) if want_dx else None
+    dW = X.new_empty((V, N)) if want_dw else None
+    lib = load()
+    p, n, ws = _scratch(_cross_entropy_backward_need(T, V, N, w & 15, ldw, want_dx, want_dw), ws, X, dev)
+    _check(lib.vq_cross_entropy_backward(T, V, N, dt, g, x, ldx, w, ldw, lab, ignore_index, ls, _ptr(dX), N, _ptr(dW), N, p, n,
+                                         _stream()))
+    return dX, dW
 
 
 # ---- the optimizer's step -------------------------------------------------------

@@ -530,6 +530,37 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
                     const void* X, int64_t ldx, const void* bg, const void* bu, void* H, int64_t ldh,
                     void* ws, size_t ws_bytes, void* stream);
 
+/* Softmax cross entropy of a projection onto a vocabulary, the logits never kept:
+ *   z = X W^T,  lse[t] = log sum_v exp z[t,v],  loss[t] = lse[t] - z[t, labels[t]].
+ * X [T x N], W [V x N] (VQ_BF16 or VQ_F16, one type, rows with leading dimensions
+ * in elements, any alignment of elements), labels int64 [T], loss and lse float32
+ * [T].  A token whose label is ignore_index takes no part: its loss and lse are 0,
+ * and nothing that its row of X holds reaches a result.  Any other label outside
+ * [0, V) makes its token's loss NaN.  Sums are float32; the results are bitwise
+ * reproducible for fixed arguments.  0 <= T <= 2^20, 1 <= V, N <= 2^20; T = 0 is a no-op.
+ * Outputs may not overlap inputs or each other.  A reduction (mean over the
+ * learnt tokens, weights) is the caller's, as is dloss below.  Workspaces as in the dense
+ * calls: about T (2 N + 16 + V / 16) bytes. */
+size_t vq_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t N, const void* W, int64_t ldw);
+vq_status vq_cross_entropy(int64_t T, int64_t V, int64_t N, int dtype, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                           const int64_t* labels, int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Gradients of sum_t dloss[t] loss[t]:  dz[t,v] = dloss[t] (exp(z[t,v] - lse[t]) -
+ * [v = labels[t]]) with z formed again and lse as vq_cross_entropy gave it,
+ *   dX = dz W [T x N],  dW = dz^T X [V x N]  (each may be NULL).
+ * dz enters the products rounded to the tensors' type; in fp16 scaled by a power of
+ * two that brings the largest |dloss| to 2^13 (and dX and dW back), so that it
+ * keeps its precision down to 2^-27 of that.  Rows of dX of ignored tokens are zeros.
+ * A label outside [0, V) makes its row of dX and all of dW NaN.  T = 0 writes a zero dW.
+ * The vocabulary is taken in pieces: the workspace holds dz of one piece (about 128
+ * MiB, at least 256 words), the learnt rows of X, and dX in float32, in up to 16 parts. */
+size_t vq_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int64_t N, const void* W, int64_t ldw, int want_dx,
+                                                 int want_dw);
+vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, const float* dloss, const void* X, int64_t ldx,
+                                    const void* W, int64_t ldw, const int64_t* labels, int64_t ignore_index, const float* lse,
+                                    void* dX, int64_t lddx, void* dW, int64_t lddw, void* ws, size_t ws_bytes, void* stream);
+
 /* AdamW (decoupled weight decay) over many tensors in one launch:
  *   g = grad_scale * grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   p = (1 - lr wd) p - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
@@ -593,8 +624,8 @@ double vq_bits_per_weight(int64_t M, int64_t N, int d, int K1, int K2, int64_t n
  * Records are keyed by (step name, K); names: "assign_search" (the matrix-core
  * search kernel alone), "assign" (the whole vq_assign), "update", "objective",
  * "select", "binorm", "residual", "reconstruct", "init", "linear",
- * "linear_backward", "gated", "gated_backward", "qlinear", "qgated", "adamw" (the
- * whole call; K is 0 for these).  vq_timing_count()
+ * "linear_backward", "gated", "gated_backward", "qlinear", "qgated", "cross_entropy",
+ * "cross_entropy_backward", "adamw" (the whole call; K is 0 for these).  vq_timing_count()
  * waits for the recorded events and returns the number of records;
  * vq_timing_get(i, ...) fills record i (name into a caller buffer of
  * name_len bytes): launches, total, min and max milliseconds.  Returns 0 on
