@@ -17,7 +17,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libvq.so")
 SOURCES = ["vq_assign.hip", "vq_update.hip", "vq_select.hip", "vq_elem.hip", "vq_qgemv.hip", "vq_vptq.hip", "vq_hfactor.hip", "vq_groups.hip", "vq_host.hip",
            "vq_timing.hip", "vq_check.hip", "vq_gemm.hip", "vq_ffn.hip",
-           "vq_few.hip", "vq_qffn.hip", "vq_loss.hip", "vq_adamw.hip"]
+           "vq_few.hip", "vq_qffn.hip", "vq_loss.hip", "vq_i8.hip", "vq_adamw.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

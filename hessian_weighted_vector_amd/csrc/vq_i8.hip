@@ -1,0 +1,635 @@
+// Products in 8-bit integers with a scale for each token and each row of the matrix
+// (vq_quantize_rows, vq_linear_i8, vq_gated_i8).
+//
+//   q[t, j] = nearest(127 x[t, j] / top_t), top_t = max_j |x[t, j]|, s_t = top_t / 127
+//   z[t, m] = s_t w_m sum_j q[t, j] Q[m, j] + bias,  Y = act(z) + R, or H = act(g) u
+//
+//   k_i8_rows       the tokens' codes and scales: one read of X
+//   k_i8_gemm       the tiled product: its loop takes pairs of 8-bit elements where the
+//                   16-bit products take one, so tiles, LDS layout and steps are theirs
+//                   and a step is 128 columns
+//   k_i8_few        few tokens: the matrix straight from memory into matrix-core operands
+//   k_i8_finish     adds split sums
+//
+// The sums are exact in 32 bits (127 * 128 * 2^17 < 2^31), whatever the order and the
+// split; they are converted to float32, scaled and go through the epilogue of the dense calls.
+// For 16-bit tokens the codes are those of exact arithmetic: a quotient that is no
+// tie is at least 2^-19 of its value away from one, and the division rounds by 2^-24.
+#include "vq_tile.h"
+
+#include <algorithm>
+
+namespace vq {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// Sixteen 8-bit elements a lane; the tile loop sees eight 16-bit ones.
+struct I8 {
+    typedef i32x4 Acc;
+    typedef i32x4 V8;
+    static __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }
+};
+
+constexpr int64_t kMaxColumns = 1 << 17;      // the sums stay below 2^31
+constexpr int64_t kMaxI8Tokens = 1 << 28;
+constexpr int64_t kRowBytes = 64;             // rows of codes begin and end on these
+
+inline int64_t round64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// ---- codes of rows ------------------------------------------------------------
+struct Rows {
+    const void* X;
+    int64_t rows, ldx;
+    int cols;
+    int8_t* q;
+    int64_t ldq;                 // zeros from cols on
+    float* scale;
+    int odd;
+};
+
+// Eight elements from column c on (those below cols, else 0), in their own type.
+template <class E>
+struct Eight {
+    typedef E V __attribute__((ext_vector_type(8)));
+    V v;
+    __device__ __forceinline__ void load(const E* row, int c, int cols, int odd)
+    {
+        if (c + 8 <= cols) {
+            if (sizeof(E) == 2 && odd) {
+                Words w;
+                w.load(row + c);
+                const uint4 u = w.get(row + c);
+                __builtin_memcpy(&v, &u, 16);
+            } else {
+                __builtin_memcpy(&v, row + c, sizeof(v));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : (E)0.0f;
+        }
+    }
+    // The largest magnitude as bits: NaN and infinities are above every number.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = __float_as_uint((float)v[i]) & 0x7fffffffu;
+            t = b > t ? b : t;
+        }
+        return t;
+    }
+    __device__ __forceinline__ uint2 codes(float top) const
+    {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = top > 0.0f ? __float2int_rn(127.0f * (float)v[i] / top) : 0;
+            w[i >> 2] |= (uint32_t)(k & 0xff) << (8 * (i & 3));
+        }
+        return make_uint2(w[0], w[1]);
+    }
+};
+
+// The largest of a row's bits as a number to divide by; 0 where the row holds none or is not finite.
+__device__ __forceinline__ float divisor(uint32_t bits) { return bits < 0x7f800000u ? __uint_as_float(bits) : 0.0f; }
+__device__ __forceinline__ float scale_of(uint32_t bits) { return bits < 0x7f800000u ? __uint_as_float(bits) / 127.0f : NAN; }
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t t)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t v = (uint32_t)__shfl_xor((int)t, o);
+        t = v > t ? v : t;
+    }
+    return t;
+}
+
+// WAVES waves a row (1 or 4), four waves a workgroup.  The first R chunks of a lane stay
+// in registers, those of longer rows are read again.
+template <class E, int WAVES, int R>
+__global__ __launch_bounds__(256) void k_i8_rows(const Rows a)
+{
+    __shared__ uint32_t tops[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t r = WAVES == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    if (r >= a.rows) return;                                  // whole waves; with four a row, whole workgroups
+    const int first = (WAVES == 1 ? lane : threadIdx.x) * 8, stride = WAVES * 64 * 8;
+    const E* row = static_cast<const E*>(a.X) + r * a.ldx;
+    Eight<E> v[R];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (first + i * stride < a.cols) v[i].load(row, first + i * stride, a.cols, a.odd);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (first + i * stride < a.cols) {
+            const uint32_t t = v[i].top();
+            top = t > top ? t : top;
+        }
+    for (int c = first + R * stride; c < a.cols; c += stride) {
+        Eight<E> w;
+        w.load(row, c, a.cols, a.odd);
+        const uint32_t t = w.top();
+        top = t > top ? t : top;
+    }
+    top = wave_max(top);
+    if (WAVES > 1) {
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = tops[k] > top ? tops[k] : top;
+    }
+    const float d = divisor(top);
+    int8_t* const q = a.q + r * a.ldq;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (first + i * stride < a.cols) *reinterpret_cast<uint2*>(q + first + i * stride) = v[i].codes(d);
+    for (int c = first + R * stride; c < a.cols; c += stride) {
+        Eight<E> w;
+        w.load(row, c, a.cols, a.odd);
+        *reinterpret_cast<uint2*>(q + c) = w.codes(d);
+    }
+    // columns past the last chunk
+    for (int64_t c = (a.cols + 7) / 8 * 8 + first; c < a.ldq; c += stride) *reinterpret_cast<uint2*>(q + c) = make_uint2(0, 0);
+    if (first == 0) a.scale[r] = scale_of(top);
+}
+
+template <class E>
+void rows_launch(const Rows& a, hipStream_t st)
+{
+    // a wave a row up to 4096 columns (eight chunks of 64 lanes)
+    if (a.cols <= 4096) hipLaunchKernelGGL((k_i8_rows<E, 1, 8>), dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_i8_rows<E, 4, 8>), dim3((unsigned)a.rows), dim3(256), 0, st, a);
+}
+
+vq_status rows_codes(const Rows& a, int dtype, hipStream_t st)
+{
+    if (dtype == VQ_BF16) rows_launch<__bf16>(a, st);
+    else if (dtype == VQ_F16) rows_launch<_Float16>(a, st);
+    else rows_launch<float>(a, st);
+    VQ_LAUNCHED("k_i8_rows");
+    return VQ_OK;
+}
+
+// ---- scaled sums ----------------------------------------------------------------
+struct Scales {
+    const float* x;              // a token's
+    const float* w[2];           // a row's of each matrix
+};
+
+// Features m .. m+7 of token t: the epilogue of the dense calls from exact sums.
+template <class T, bool PAIR>
+__device__ __forceinline__ void finish(const Epilogue& e, const Scales& s, int64_t t, int m, int M, const int (&v)[8],
+                                       const int (&u)[8])
+{
+    const float sx = s.x[t];
+    float z[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        z[i] = m + i < M ? (float)v[i] * sx * s.w[0][m + i] : 0.0f;
+        if (PAIR) y[i] = m + i < M ? (float)u[i] * sx * s.w[1][m + i] : 0.0f;
+    }
+    if (PAIR) epilogue_pair<T>(e, t, m, M, z, y);
+    else epilogue_one<T>(e, t, m, M, z);
+}
+
+// ---- the tiled product -------------------------------------------------------------
+struct I8Tile {
+    Tile t;                      // part: int32 sums
+    Scales s;
+};
+
+template <class T, int FP, int FQ, bool PAIR>
+__global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(const I8Tile a)
+{
+    typedef Main<I8, false, false, FP, FQ, PAIR> L;
+    VQ_TILE_BUFFERS(L);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave / kWQ, wq = wave % kWQ, split = blockIdx.y;
+    int tp, tq;
+    pick_tile(blockIdx.x, a.t.ntp * a.t.ntq, a.t.ntp, a.t.ntq, tp, tq);
+    const int p0 = tp * (PAIR ? L::BP / 2 : L::BP), q0 = tq * L::BQ;
+    const int pairs = (a.t.steps + 1) / 2;
+    const int s0 = 2 * (int)((int64_t)pairs * split / a.t.splits), s1 = 2 * (int)((int64_t)pairs * (split + 1) / a.t.splits);
+    i32x4 acc[FP][FQ];
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    L::run(a.t, p0, q0, 0, s0, s1, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
+    if (a.t.part) {
+        constexpr int NI = PAIR ? FP / 2 : FP;
+        const int64_t plane = (int64_t)a.t.nq * a.t.pitch;
+        int* o = reinterpret_cast<int*>(a.t.part) + (int64_t)split * (PAIR ? 2 : 1) * plane;
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const int q = q0 + (wq * FQ + j) * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int p = p0 + (wp * NI + i) * 16 + (lane >> 4) * 4;
+                if (q >= a.t.nq || p >= a.t.np) continue;
+                *reinterpret_cast<i32x4*>(o + (int64_t)q * a.t.pitch + p) = acc[i][j];
+                if (PAIR) *reinterpret_cast<i32x4*>(o + plane + (int64_t)q * a.t.pitch + p) = acc[i + NI][j];
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));           // no load into LDS outlives the workgroup
+        return;
+    }
+    each_row<L>(acc, p0, q0, a.t.np, a.t.nq, wave, lane, pb0, pb1, qb0, qb1,
+                [&](int q, int p, int (&v)[8], int (&u)[8]) { finish<T, PAIR>(a.t.epi, a.s, q, p, a.t.np, v, u); });
+}
+
+// Adds the parts [splits][matrices][T][pitch]; eight features a thread.
+struct Parts {
+    const int* part;
+    int splits, M, T, pitch;
+    Epilogue epi;
+    Scales s;
+};
+
+template <class T, bool PAIR>
+__global__ __launch_bounds__(256) void k_i8_finish(const Parts a)
+{
+    const int64_t per = a.pitch / 8, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= per * a.T) return;
+    const int64_t t = e / per, plane = (int64_t)a.T * a.pitch;
+    const int m = (int)(e - t * per) * 8;
+    const int* o = a.part + t * a.pitch + m;
+    int v[8] = {}, u[8] = {};
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) {
+        const int* oz = o + (int64_t)z * (PAIR ? 2 : 1) * plane;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const i32x4 w = *reinterpret_cast<const i32x4*>(oz + h * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h * 4 + i] += w[i];
+            if (PAIR) {
+                const i32x4 w2 = *reinterpret_cast<const i32x4*>(oz + plane + h * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[h * 4 + i] += w2[i];
+            }
+        }
+    }
+    finish<T, PAIR>(a.epi, a.s, t, m, a.M, v, u);
+}
+
+// ---- few tokens -------------------------------------------------------------------
+// A workgroup owns 16 rows of Q (of both matrices of a pair); its waves take blocks of
+// 64 H columns in turn, a lane's 16 bytes of a row being its operand.
+struct FewI8 {
+    const int8_t* Q[2];
+    int64_t ldq;
+    const int8_t* x;             // codes [T][ldx]
+    int64_t ldx;
+    int M, T, chunks;            // of 64 columns
+    int splits, pitch;
+    int* part;                   // [splits][matrices][T][pitch], or null
+    Scales s;
+    Epilogue epi;
+};
+
+template <class T, int NT, bool PAIR, int H>
+__global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
+{
+    constexpr int NM = PAIR ? 2 : 1;
+    extern __shared__ __align__(16) int red[];                // [waves][NM][NT][64] of four features
+    const int nwaves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int m0 = blockIdx.x * 16;
+    const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;      // rows and tokens past the last repeat it
+    const int8_t* w[NM];
+    const int8_t* x[NT];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) w[m] = a.Q[m] + row * a.ldq + g * 16;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x[n] = a.x + (int64_t)(n * 16 + r < a.T ? n * 16 + r : a.T - 1) * a.ldx + g * 16;
+    i32x4 acc[NM][NT];
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = i32x4{0, 0, 0, 0};
+    const int nfull = a.chunks / H;                           // blocks of H chunks
+    const int f0 = (int)((int64_t)nfull * blockIdx.y / a.splits), f1 = (int)((int64_t)nfull * (blockIdx.y + 1) / a.splits);
+    i32x4 wv[NM][H], xv[NT][H];
+    const auto load = [&](int kb, int j) {
+        const int64_t c = ((int64_t)kb * H + j) * 64;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xv[n][j] = *reinterpret_cast<const i32x4*>(x[n] + c);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) wv[m][j] = *reinterpret_cast<const i32x4*>(w[m] + c);
+    };
+    const auto multiply = [&](int j) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[m][n] = I8::mfma(wv[m][j], xv[n][j], acc[m][n]);
+    };
+    int kb = f0 + wave;
+    if (kb < f1) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            load(kb, j);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll 1
+        for (; kb + nwaves < f1; kb += nwaves) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                multiply(j);
+                __builtin_amdgcn_sched_barrier(0);
+                load(kb + nwaves, j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) multiply(j);
+    }
+    // chunks past the last whole block, dealt to the waves of the last split
+    if (blockIdx.y == a.splits - 1)
+        for (int s = nfull * H + wave; s < a.chunks; s += nwaves) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const i32x4 v = *reinterpret_cast<const i32x4*>(w[m] + (int64_t)s * 64);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[m][n] = I8::mfma(v, *reinterpret_cast<const i32x4*>(x[n] + (int64_t)s * 64), acc[m][n]);
+            }
+        }
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) *reinterpret_cast<i32x4*>(red + (((wave * NM + m) * NT + n) * 64 + lane) * 4) = acc[m][n];
+    __syncthreads();
+    // thread -> token t, features m0 + 8 f .. + 7
+    const int t = threadIdx.x >> 1, f = threadIdx.x & 1;
+    if (t >= a.T || m0 + f * 8 >= a.M) return;
+    int z[2][8] = {};
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            i32x4 v = {0, 0, 0, 0};
+            for (int k = 0; k < nwaves; ++k)
+                v += *reinterpret_cast<const i32x4*>(red + (((k * NM + m) * NT + (t >> 4)) * 64 + (f * 2 + h) * 16 + (t & 15)) * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[m][h * 4 + i] = v[i];
+        }
+    if (a.part) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            int* o = a.part + (((int64_t)blockIdx.y * NM + m) * a.T + t) * a.pitch + m0 + f * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = z[m][i];
+        }
+    } else {
+        finish<T, PAIR>(a.epi, a.s, t, m0 + f * 8, a.M, z[0], z[1]);
+    }
+}
+
+// ---- plan -----------------------------------------------------------------------
+struct Plan {
+    int few, waves;              // few tokens
+    int small, ntp, ntq, steps;  // tiles
+    int splits, pitch;
+    size_t part_bytes;
+};
+
+// The tiled products' model of microseconds with steps of 128 columns.
+Plan make_plan(int64_t T, int64_t M, int64_t N, int nm)
+{
+    Plan p{};
+    p.pitch = (int)((M + 7) / 8 * 8);
+    p.splits = 1;
+    if (T <= 32) {
+        const int64_t groups = (M + 15) / 16, blocks = round64(N) / 512;
+        p.few = 1;
+        p.waves = groups < 512 && blocks >= 16 ? 16 : 8;
+        while (p.splits < 16 && groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+    } else {
+        double least = 1e300;
+        for (int small = 0; small < 2; ++small) {
+            const int bp = (small ? 128 : 256) / nm, bq = small ? 128 : 256;
+            const int ntp = (int)((M + bp - 1) / bp), ntq = (int)((T + bq - 1) / bq);
+            const int steps = (int)((round64(N) + 127) / 128), pairs = (steps + 1) / 2;
+            for (int sp = 1; sp <= 16 && sp <= pairs; ++sp) {
+                const int64_t tiles = (int64_t)ntp * ntq * sp;
+                const double st = 2.0 * ((pairs + sp - 1) / sp);
+                double cost;
+                if (!small) {
+                    cost = (double)((tiles + 255) / 256) * (st * 1.45 + 10.0);
+                } else {
+                    const int64_t rest = tiles % 512;
+                    cost = (double)(tiles / 512) * (st * 1.15 + 4.0) + (rest ? st * (rest <= 256 ? 0.8 : 1.15) + 4.0 : 0.0);
+                }
+                if (sp > 1) cost += 9.5 + 0.8e-6 * (double)M * T * nm * (sp + 1);
+                if (cost < least) {
+                    least = cost;
+                    p.small = small; p.ntp = ntp; p.ntq = ntq; p.steps = steps; p.splits = sp;
+                }
+            }
+        }
+    }
+    p.part_bytes = p.splits > 1 ? (size_t)p.splits * nm * T * p.pitch * sizeof(int) : 0;
+    return p;
+}
+
+struct Call {
+    int64_t T;
+    int dtype, nm;
+    const vq_i8matrix* W[2];
+    const void* X; int64_t ldx;
+    Epilogue epi;
+};
+
+template <class T, int NT, bool PAIR>
+void few_launch(const FewI8& f, int waves, hipStream_t st)
+{
+    const dim3 grid((unsigned)((f.M + 15) / 16), (unsigned)f.splits);
+    const size_t lds = (size_t)waves * (PAIR ? 2 : 1) * NT * 256 * sizeof(int);
+    hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4>), grid, dim3(waves * 64), lds, st, f);
+}
+
+template <class T, bool PAIR>
+vq_status launch(const Call& c, const Plan& p, const int8_t* x, const float* sx, int* part, hipStream_t st)
+{
+    const vq_i8matrix& w = *c.W[0];
+    const Scales s{sx, {w.scale, PAIR ? c.W[1]->scale : nullptr}};
+    const int64_t ldx = round64(w.N);
+    if (p.few) {
+        const FewI8 f{{w.q, PAIR ? c.W[1]->q : nullptr}, w.ldq, x, ldx, (int)w.M, (int)c.T, (int)(ldx / 64), p.splits, p.pitch, part, s, c.epi};
+        if (c.T > 16) few_launch<T, 2, PAIR>(f, p.waves, st);
+        else few_launch<T, 1, PAIR>(f, p.waves, st);
+        VQ_LAUNCHED("k_i8_few");
+    } else {
+        I8Tile a{};
+        a.t.P[0] = reinterpret_cast<const char*>(w.q);
+        a.t.P[1] = PAIR ? reinterpret_cast<const char*>(c.W[1]->q) : a.t.P[0];
+        a.t.Q[0] = a.t.Q[1] = reinterpret_cast<const char*>(x);
+        a.t.ldp = (int)(w.ldq / 2); a.t.ldq = (int)(ldx / 2);
+        a.t.kP = a.t.kQ = (int)(ldx / 2);
+        a.t.np = (int)w.M; a.t.nq = (int)c.T;
+        a.t.ntp = p.ntp; a.t.ntq = p.ntq;
+        a.t.steps = a.t.seg_steps = p.steps;
+        a.t.splits = p.splits; a.t.pitch = p.pitch;
+        a.t.part = reinterpret_cast<float*>(part);
+        a.t.epi = c.epi;
+        a.s = s;
+        const dim3 grid((unsigned)(p.ntp * p.ntq), (unsigned)p.splits);
+        if (p.small) hipLaunchKernelGGL((k_i8_gemm<T, 4, 2, PAIR>), grid, dim3(kThreads), 0, st, a);
+        else hipLaunchKernelGGL((k_i8_gemm<T, 8, 4, PAIR>), grid, dim3(kThreads), 0, st, a);
+        VQ_LAUNCHED("k_i8_gemm");
+    }
+    if (p.splits > 1) {
+        const Parts f{part, p.splits, (int)w.M, (int)c.T, p.pitch, c.epi, s};
+        hipLaunchKernelGGL((k_i8_finish<T, PAIR>), dim3(grid_for(c.T * (p.pitch / 8), 256)), dim3(256), 0, st, f);
+        VQ_LAUNCHED("k_i8_finish");
+    }
+    return VQ_OK;
+}
+
+size_t workspace(int64_t T, int64_t M, int64_t N, int nm)
+{
+    return align_up(T * round64(N)) + align_up(T * sizeof(float)) + align_up(make_plan(T, M, N, nm).part_bytes);
+}
+
+vq_status product(const Call& c, void* ws, hipStream_t st)
+{
+    const int64_t N = c.W[0]->N, ldx = round64(N);
+    const Plan p = make_plan(c.T, c.W[0]->M, N, c.nm);
+    char* at = static_cast<char*>(ws);
+    int8_t* x = reinterpret_cast<int8_t*>(at);
+    float* sx = reinterpret_cast<float*>(at += align_up(c.T * ldx));
+    int* part = p.part_bytes ? reinterpret_cast<int*>(at += align_up(c.T * sizeof(float))) : nullptr;
+    VQ_TRY(rows_codes({c.X, c.T, c.ldx, (int)N, x, ldx, sx, odd_rows(c.X, c.ldx)}, c.dtype, st));
+    if (c.dtype == VQ_BF16) return c.nm > 1 ? launch<Bf16, true>(c, p, x, sx, part, st) : launch<Bf16, false>(c, p, x, sx, part, st);
+    return c.nm > 1 ? launch<F16, true>(c, p, x, sx, part, st) : launch<F16, false>(c, p, x, sx, part, st);
+}
+
+// ---- argument checks ------------------------------------------------------------
+vq_status check_sizes(const std::string& call, int64_t T, int64_t M, int64_t N)
+{
+    VQ_CHECK(T >= 0 && T <= kMaxI8Tokens, call + ": T must be in [0, 2^28]");
+    VQ_CHECK(M >= 1 && M <= kMaxSize, call + ": M must be in [1, 2^20]");
+    VQ_CHECK(N >= 1 && N <= kMaxColumns, call + ": N must be in [1, 2^17]");
+    VQ_CHECK(T * std::max(M, N) <= ((int64_t)1 << 38), call + ": T * max(M, N) must be at most 2^38");
+    return VQ_OK;
+}
+
+vq_status check_codes(const std::string& call, const char* what, const vq_i8matrix* w)
+{
+    VQ_CHECK(w, call + ": " + what + " is null");
+    VQ_CHECK(w->q && w->scale, call + ": " + what + " has a null pointer");
+    VQ_CHECK(aligned16(w->q), call + ": codes of " + what + " are not 16-byte aligned");
+    VQ_CHECK(w->ldq % kRowBytes == 0 && w->ldq >= w->N && w->ldq <= 2 * kMaxLd,
+             call + ": ldq of " + what + " must be a multiple of 64, at least N and at most 2^22");
+    VQ_CHECK(reinterpret_cast<uintptr_t>(w->scale) % 4 == 0, call + ": scale of " + what + " is not aligned to its elements");
+    return VQ_OK;
+}
+
+vq_status check_types(const std::string& call, int dtype, int act)
+{
+    VQ_CHECK(dtype == VQ_BF16 || dtype == VQ_F16, call + ": dtype must be VQ_BF16 or VQ_F16");
+    VQ_CHECK(act >= VQ_ACT_NONE && act <= VQ_ACT_SIGMOID, call + ": unknown activation");
+    return VQ_OK;
+}
+
+}  // namespace
+}  // namespace vq
+
+using namespace vq;
+
+extern "C" {
+
+vq_status vq_quantize_rows(int64_t rows, int64_t cols, int dtype, const void* X, int64_t ldx, int8_t* q, int64_t ldq,
+                           float* scale, void* stream)
+{
+    const std::string call = "vq_quantize_rows";
+    VQ_CHECK(rows >= 0 && rows <= kMaxI8Tokens, call + ": rows must be in [0, 2^28]");
+    VQ_CHECK(cols >= 1 && cols <= kMaxSize, call + ": cols must be in [1, 2^20]");
+    VQ_CHECK(dtype == VQ_BF16 || dtype == VQ_F16 || dtype == VQ_F32, call + ": unknown dtype");
+    if (rows == 0) return VQ_OK;
+    VQ_CHECK(X && q && scale, call + ": null pointer");
+    VQ_TRY(check_ld(call, "X", X, ldx, cols));
+    VQ_CHECK(dtype != VQ_F32 || reinterpret_cast<uintptr_t>(X) % 4 == 0, call + ": X is not aligned to its elements");
+    VQ_CHECK(reinterpret_cast<uintptr_t>(scale) % 4 == 0, call + ": scale is not aligned to its elements");
+    VQ_CHECK(aligned16(q) && ldq % kRowBytes == 0 && ldq >= cols && ldq <= ((int64_t)1 << 40),
+             call + ": q must be 16-byte aligned and ldq a multiple of 64, at least cols");
+    VQ_TRY(check_apart(call, {q, scale}, {X}));
+    VQ_TRY(check_device());
+    VQ_MATRIX(X, rows, cols, ldx, call.c_str(), "X");
+    TimedRegion tr("quantize_rows", 0, as_stream(stream));
+    return rows_codes({X, rows, ldx, (int)cols, q, ldq, scale, dtype != VQ_F32 && odd_rows(X, ldx)}, dtype, as_stream(stream));
+}
+
+size_t vq_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t T)
+{
+    if (check_sizes("vq_linear_i8", T, M, N) != VQ_OK || T == 0) return 0;
+    return workspace(T, M, N, 1);
+}
+
+vq_status vq_linear_i8(const vq_i8matrix* W, int64_t T, int dtype, int act, const void* X, int64_t ldx, const void* bias,
+                       const void* R, int64_t ldr, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_linear_i8";
+    VQ_TRY(check_types(call, dtype, act));
+    VQ_TRY(check_codes(call, "W", W));
+    const int64_t M = W->M, N = W->N;
+    VQ_TRY(check_sizes(call, T, M, N));
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(X && Y, "vq_linear_i8: null pointer");
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "bias", bias, M, M));
+    VQ_TRY(check_ld(call, "R", R, ldr, M));
+    VQ_TRY(check_ld(call, "Y", Y, ldy, M));
+    VQ_TRY(check_apart(call, {Y}, {X, W->q, W->scale, bias}));
+    VQ_CHECK(Y != R || ldy == ldr, "vq_linear_i8: Y in place of R needs R's leading dimension");
+    VQ_TRY(check_workspace(call, ws, ws_bytes, workspace(T, M, N, 1)));
+    VQ_TRY(check_device());
+    VQ_MATRIX(X, T, N, ldx, call, "X");
+    VQ_VALUES(W->scale, M, false, call, "scale of W");
+    VQ_MATRIX(bias, 1, M, M, call, "bias");
+    VQ_MATRIX(R, T, M, ldr, call, "R");
+    TimedRegion tr("linear_i8", 0, as_stream(stream));
+    return product({T, dtype, 1, {W, nullptr}, X, ldx, {act, {bias, nullptr}, R, Y, {nullptr, nullptr}, ldr, ldy, 0}}, ws, as_stream(stream));
+}
+
+size_t vq_gated_i8_workspace_bytes(int64_t M, int64_t N, int64_t T)
+{
+    if (check_sizes("vq_gated_i8", T, M, N) != VQ_OK || T == 0) return 0;
+    return workspace(T, M, N, 2);
+}
+
+vq_status vq_gated_i8(const vq_i8matrix* Wg, const vq_i8matrix* Wu, int64_t T, int dtype, int act, const void* X, int64_t ldx,
+                      const void* bg, const void* bu, void* H, int64_t ldh, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* call = "vq_gated_i8";
+    VQ_TRY(check_types(call, dtype, act));
+    VQ_TRY(check_codes(call, "Wg", Wg));
+    VQ_TRY(check_codes(call, "Wu", Wu));
+    VQ_CHECK(Wg->M == Wu->M && Wg->N == Wu->N && Wg->ldq == Wu->ldq, "vq_gated_i8: Wg and Wu must have the same M, N and ldq");
+    const int64_t M = Wg->M, N = Wg->N;
+    VQ_TRY(check_sizes(call, T, M, N));
+    if (T == 0) return VQ_OK;
+    VQ_CHECK(X && H, "vq_gated_i8: null pointer");
+    VQ_TRY(check_ld(call, "X", X, ldx, N));
+    VQ_TRY(check_ld(call, "bg", bg, M, M));
+    VQ_TRY(check_ld(call, "bu", bu, M, M));
+    VQ_TRY(check_ld(call, "H", H, ldh, M));
+    VQ_TRY(check_apart(call, {H}, {X, Wg->q, Wg->scale, Wu->q, Wu->scale, bg, bu}));
+    VQ_TRY(check_workspace(call, ws, ws_bytes, workspace(T, M, N, 2)));
+    VQ_TRY(check_device());
+    VQ_MATRIX(X, T, N, ldx, call, "X");
+    VQ_VALUES(Wg->scale, M, false, call, "scale of Wg");
+    VQ_VALUES(Wu->scale, M, false, call, "scale of Wu");
+    VQ_MATRIX(bg, 1, M, M, call, "bg");
+    VQ_MATRIX(bu, 1, M, M, call, "bu");
+    TimedRegion tr("gated_i8", 0, as_stream(stream));
+    return product({T, dtype, 2, {Wg, Wu}, X, ldx, {act, {bg, bu}, nullptr, H, {nullptr, nullptr}, 0, ldh, 0}}, ws, as_stream(stream));
+}
+
+}  // extern "C"

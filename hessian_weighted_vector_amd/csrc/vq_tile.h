@@ -142,12 +142,15 @@ __device__ __forceinline__ uint32_t lane_base(int r0, int lane)
 template <class T, int R, bool TR>
 __device__ __forceinline__ typename T::V8 fragment(lds_ptr lds, uint32_t base, int i, int kk)
 {
-    if (!TR) return *(const __attribute__((address_space(3))) typename T::V8*)(lds + (base ^ (kk * 64)) + i * 2048);
-    lds_ptr p = lds + (base ^ (i * 32)) + kk * 32 * R * 2;
-    typedef __attribute__((address_space(3))) typename T::V4* tr_ptr;
-    const typename T::V4 a = T::lds_tr((tr_ptr)p);
-    const typename T::V4 b = T::lds_tr((tr_ptr)(p + 4 * R * 2));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    if constexpr (!TR) {
+        return *(const __attribute__((address_space(3))) typename T::V8*)(lds + (base ^ (kk * 64)) + i * 2048);
+    } else {
+        lds_ptr p = lds + (base ^ (i * 32)) + kk * 32 * R * 2;
+        typedef __attribute__((address_space(3))) typename T::V4* tr_ptr;
+        const typename T::V4 a = T::lds_tr((tr_ptr)p);
+        const typename T::V4 b = T::lds_tr((tr_ptr)(p + 4 * R * 2));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
 }
 
 // Work item -> tile.  Consecutive workgroup ids go to the eight dies in turn;

@@ -68,6 +68,10 @@ class QMatrixStruct(ctypes.Structure):
                 ("idx2", _P), ("rscale", _P), ("cscale", _P), ("row_ptr", _P), ("col", _P), ("delta", _P)]
 
 
+class I8MatrixStruct(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("q", _P), ("ldq", _I64), ("scale", _P)]
+
+
 class AdamWTensor(ctypes.Structure):
     _fields_ = [("param", _P), ("grad", _P), ("master", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P),
                 ("n", _I64)]
@@ -128,6 +132,11 @@ SIGNATURES = {
     "vq_qlinear": (_I, [_P, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "vq_qgated_workspace_bytes": (_SZ, [_I64, _I64, _I, _I64]),
     "vq_qgated": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "vq_linear_i8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "vq_linear_i8": (_I, [_P, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "vq_gated_i8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "vq_gated_i8": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _P, _P, _P, _I64, _P, _SZ, _P]),
+    "vq_quantize_rows": (_I, [_I64, _I64, _I, _P, _I64, _P, _I64, _P, _P]),
     "vq_cross_entropy_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _I64]),
     "vq_cross_entropy": (_I, [_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _SZ, _P]),
     "vq_cross_entropy_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _I64, _I, _I]),
@@ -838,6 +847,108 @@ def qgated(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, 
     lib = load()
     p, n, ws = _scratch(_qgated_need(M, N, Q_gate.d, T), ws, X, dev)
     _check(lib.vq_qgated(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
+    return H
+
+
+# ---- feed-forward calls in 8-bit integers --------------------------------------------
+
+def quantize_rows(X):
+    """(q, scale): int8 [T, N] and float32 [T] with X[t, j] near scale[t] q[t, j], q the integer nearest to 127 X[t, j] / max |X[t]|.
+
+    X [T, N] is bfloat16, float16 or float32; a row that is not finite has a NaN scale.  q's
+    rows begin every multiple of 64 bytes, as Int8Matrix takes them in place.
+    """
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    T, N = X.shape
+    dt, dev = _any_dtype(X, "X"), _home(X)
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    ldq = -(-N // 64) * 64
+    q = torch.empty((T, ldq), dtype=torch.int8, device=X.device)
+    scale = torch.empty(T, device=X.device)
+    _check(load().vq_quantize_rows(T, N, dt, x, ldx, q.data_ptr(), ldq, scale.data_ptr(), _stream()))
+    return q[:, :N], scale
+
+
+class Int8Matrix:
+    """A matrix in 8-bit codes with a scale a row: W[i, j] = scale[i] q[i, j].
+
+    q int8 [M, N], scale float32 [M].  q is kept in place where its rows are laid out as the
+    kernels read them (16-byte aligned, every multiple of 64 bytes, readable to the next one),
+    else copied once on the current stream.
+    """
+
+    def __init__(self, q, scale):
+        if q.dim() != 2 or q.dtype != torch.int8:
+            raise TypeError("q must be an int8 matrix")
+        M, N = q.shape
+        self.index = _home(q, "q")
+        _vector(scale, M, torch.float32, self.index, "scale")
+        ld = q.stride(0) if M > 1 else -(-N // 64) * 64
+        end = q.storage_offset() + (M - 1) * ld + -(-N // 64) * 64
+        if (N > 1 and q.stride(1) != 1) or ld % 64 or ld < N or q.data_ptr() % 16 or end > q.untyped_storage().nbytes():
+            ld = -(-N // 64) * 64
+            copy = torch.empty((M, ld), dtype=torch.int8, device=q.device)
+            copy[:, :N].copy_(q)
+            q = copy[:, :N]
+        self.M, self.N, self.q, self.scale = M, N, q, scale
+        self._struct = I8MatrixStruct(M, N, q.data_ptr(), ld, scale.data_ptr())
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def from_dense(cls, W):
+        """From a dense matrix (bfloat16, float16 or float32), its rows brought to 8 bits."""
+        return cls(*quantize_rows(W))
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_i8_need(M, N, T):
+    return load().vq_linear_i8_workspace_bytes(M, N, T)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_i8_need(M, N, T):
+    return load().vq_gated_i8_workspace_bytes(M, N, T)
+
+
+def linear_i8(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
+    """Y = act(X W^T + bias) + residual with W = the Int8Matrix Q and X brought to 8 bits, a scale a token.
+
+    X [T, N] is bfloat16 or float16; the other tensors have its type.  `out` may be the residual itself.
+    """
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    T, M, N = X.shape[0], Q.M, Q.N
+    dt, a, dev = _half(X, "X"), _act(act), _home(X)
+    if Q.index != dev:
+        _elsewhere(Q.q, "Q")
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    b = _vector(bias, M, X.dtype, dev, "bias")
+    r, ldr = _matrix(residual, T, M, X.dtype, dev, "residual")
+    Y, y, ldy = _output(out, X, T, M, dev)
+    lib = load()
+    p, n, ws = _scratch(_linear_i8_need(M, N, T), ws, X, dev)
+    _check(lib.vq_linear_i8(Q._ref, T, dt, a, x, ldx, b, r, ldr, y, ldy, p, n, _stream()))
+    return Y
+
+
+def gated_i8(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, ws=None):
+    """H = act(X Wg^T + bias_gate) * (X Wu^T + bias_up) with two Int8Matrix of one shape in one launch (tokens as in linear_i8)."""
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    T, M, N = X.shape[0], Q_gate.M, Q_gate.N
+    dt, a, dev = _half(X, "X"), _act(act), _home(X)
+    if Q_gate.index != dev:
+        _elsewhere(Q_gate.q, "Q_gate")
+    if Q_up.index != dev:
+        _elsewhere(Q_up.q, "Q_up")
+    x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
+    bg = _vector(bias_gate, M, X.dtype, dev, "bias_gate")
+    bu = _vector(bias_up, M, X.dtype, dev, "bias_up")
+    H, h, ldh = _output(out, X, T, M, dev)
+    lib = load()
+    p, n, ws = _scratch(_gated_i8_need(M, N, T), ws, X, dev)
+    _check(lib.vq_gated_i8(Q_gate._ref, Q_up._ref, T, dt, a, x, ldx, bg, bu, h, ldh, p, n, _stream()))
     return H
 
 

@@ -530,6 +530,41 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
                     const void* X, int64_t ldx, const void* bg, const void* bu, void* H, int64_t ldh,
                     void* ws, size_t ws_bytes, void* stream);
 
+/* Feed-forward calls in 8-bit integers, for prompts and decoding: a matrix in 8-bit codes
+ * with a float32 scale a row, W[i,j] = scale[i] q[i,j], and tokens brought to 8 bits in the call,
+ *   top_t = max_j |X[t,j]|,  c[t,j] = the integer nearest to 127 X[t,j] / top_t (ties to even),
+ *   (X W^T)[t,i] = (top_t / 127) scale[i] sum_j c[t,j] q[i,j].
+ * The codes of 16-bit tokens are those of exact arithmetic and the sums are exact; top_t / 127,
+ * the two scalings and the epilogue are float32, each stored value is rounded once.
+ * Results are the same bits on every call and for every T.  A token of zeros has zero codes; one that holds a
+ * NaN or an infinity gives NaN in its whole row and changes no other.
+ * q int8 [M x N]: rows begin every ldq bytes, a multiple of 64 and at most 2^22, q is 16-byte aligned, and
+ * the bytes of a row from N to the next multiple of 64 are readable (of any value).
+ * X [T x N], bias, bg, bu [M] (nullable), R [T x M] (nullable), Y, H [T x M] of one type
+ * (VQ_BF16 or VQ_F16) with leading dimensions in elements, any alignment of elements.
+ * 1 <= M <= 2^20, 1 <= N <= 2^17, 0 <= T <= 2^28; T = 0 is a no-op.  Y may be R itself (same address and
+ * leading dimension); other overlaps are not allowed.  The workspace is as in the dense calls. */
+typedef struct {
+    int64_t M, N;
+    const int8_t* q;
+    int64_t ldq;
+    const float* scale;
+} vq_i8matrix;
+
+size_t vq_linear_i8_workspace_bytes(int64_t M, int64_t N, int64_t T);
+vq_status vq_linear_i8(const vq_i8matrix* W, int64_t T, int dtype, int act, const void* X, int64_t ldx, const void* bias,
+                       const void* R, int64_t ldr, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+size_t vq_gated_i8_workspace_bytes(int64_t M, int64_t N, int64_t T);
+vq_status vq_gated_i8(const vq_i8matrix* Wg, const vq_i8matrix* Wu, int64_t T, int dtype, int act, const void* X, int64_t ldx,
+                      const void* bg, const void* bu, void* H, int64_t ldh, void* ws, size_t ws_bytes, void* stream);
+
+/* The codes above of a matrix's rows (VQ_BF16, VQ_F16 or VQ_F32; of VQ_F32 the quotient is
+ * rounded to float32 before it is brought to an integer): q [rows x cols] as in vq_i8matrix, with zeros
+ * from cols to ldq, and scale[r] = top_r / 127 (NaN, with zero codes, where the row is not
+ * finite).  cols <= 2^20. */
+vq_status vq_quantize_rows(int64_t rows, int64_t cols, int dtype, const void* X, int64_t ldx, int8_t* q, int64_t ldq,
+                           float* scale, void* stream);
+
 /* Softmax cross entropy of a projection onto a vocabulary, the logits never kept:
  *   z = X W^T,  lse[t] = log sum_v exp z[t,v],  loss[t] = lse[t] - z[t, labels[t]].
  * X [T x N], W [V x N] (VQ_BF16 or VQ_F16, one type, rows with leading dimensions
@@ -624,7 +659,8 @@ double vq_bits_per_weight(int64_t M, int64_t N, int d, int K1, int K2, int64_t n
  * Records are keyed by (step name, K); names: "assign_search" (the matrix-core
  * search kernel alone), "assign" (the whole vq_assign), "update", "objective",
  * "select", "binorm", "residual", "reconstruct", "init", "linear",
- * "linear_backward", "gated", "gated_backward", "qlinear", "qgated", "cross_entropy",
+ * "linear_backward", "gated", "gated_backward", "qlinear", "qgated",
+ * "linear_i8", "gated_i8", "quantize_rows", "cross_entropy",
  * "cross_entropy_backward", "adamw" (the whole call; K is 0 for these).  vq_timing_count()
  * waits for the recorded events and returns the number of records;
  * vq_timing_get(i, ...) fills record i (name into a caller buffer of
