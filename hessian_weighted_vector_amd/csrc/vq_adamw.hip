@@ -215,6 +215,20 @@ __global__ __launch_bounds__(256) void k_adamw(const Args a)
     }
 }
 
+// New gradients of tensors first .. first + count, taken from the kernel's own arguments, so
+// that nothing on the host has to outlive the call.
+constexpr int kPointers = 448;
+struct GradPointers {
+    const void* grad[kPointers];
+    int64_t first;
+    int count;
+};
+
+__global__ __launch_bounds__(512) void k_adamw_grads(const GradPointers a, vq_adamw_tensor* tensors)
+{
+    if ((int)threadIdx.x < a.count) tensors[a.first + threadIdx.x].grad = a.grad[threadIdx.x];
+}
+
 Coefficients coefficients(double lr, double b1, double b2, double eps, double wd, double power1, double power2)
 {
     Coefficients c;
@@ -405,6 +419,30 @@ vq_status vq_adamw_plan(const vq_adamw_tensor* tensors, int64_t count, int param
     } catch (const std::bad_alloc&) {
         return fail(VQ_ERR_INVALID, "vq_adamw_plan: out of host memory");
     }
+}
+
+vq_status vq_adamw_grads(const vq_adamw_plan_t* plan, const void* const* grads, int64_t count, void* stream)
+{
+    const std::string call = "vq_adamw_grads";
+    VQ_CHECK(plan, call + ": plan is null");
+    VQ_CHECK(count == plan->count, call + ": count must be the plan's");
+    VQ_CHECK(known(plan->grad_dtype) && plan->chunks >= 0 && (plan->chunks == 0 || plan->table), call + ": the plan is not made");
+    if (plan->chunks == 0) return VQ_OK;
+    VQ_CHECK(grads, call + ": grads is null");
+    for (int64_t i = 0; i < count; ++i)
+        VQ_CHECK(!off(grads[i], size_of(plan->grad_dtype)), call + ": gradient " + std::to_string(i) + " is not aligned to its elements");
+    VQ_TRY(check_device());
+    vq_adamw_tensor* const tensors =
+        reinterpret_cast<vq_adamw_tensor*>(static_cast<char*>(plan->table) + align_up(sizeof(Coefficients)));
+    for (int64_t first = 0; first < count; first += kPointers) {
+        GradPointers a{};
+        a.first = first;
+        a.count = (int)std::min<int64_t>(count - first, kPointers);
+        std::copy(grads + first, grads + first + a.count, a.grad);
+        hipLaunchKernelGGL(k_adamw_grads, dim3(1), dim3(512), 0, as_stream(stream), a, tensors);
+        VQ_LAUNCHED("k_adamw_grads");
+    }
+    return VQ_OK;
 }
 
 vq_status vq_adamw(const vq_adamw_plan_t* plan, double lr, double beta1, double beta2, double eps, double weight_decay,

@@ -144,6 +144,7 @@ SIGNATURES = {
                                        _P, _SZ, _P]),
     "vq_adamw_plan_bytes": (_SZ, [_P, _I64]),
     "vq_adamw_plan": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P, _P]),
+    "vq_adamw_grads": (_I, [_P, _P, _I64, _P]),
     "vq_adamw": (_I, [_P, _D, _D, _D, _D, _D, _I64, _P, _P, _P, _P]),
     "vq_timing_enable": (None, [_I]),
     "vq_timing_count": (_I, []),
@@ -1095,13 +1096,17 @@ class AdamW:
                 raise ValueError("%s[%d] must be contiguous" % (name, i))
 
     def _bind(self, grads):
-        """The table of these gradients' tensors on the GPU (waits for the stream)."""
+        """The table on the GPU with these gradients: made once, which waits for the stream, then changed in stream order."""
         grads = list(grads)
         if not grads:
             raise ValueError("grads must have %d tensors" % len(self.params))
         code = _any_dtype(grads[0], "grads[0]")
         self._same(grads, grads[0].dtype, "grads")
         n = len(self.params)
+        if self.grads is not None and code == self._plan.grad_dtype:
+            _check(load().vq_adamw_grads(self._ref, (_P * n)(*[g.data_ptr() for g in grads]), n, _stream()))
+            self.grads = grads
+            return
         none = [None] * n
         s = self.state
         rows = (AdamWTensor * n)(*[
@@ -1118,9 +1123,8 @@ class AdamW:
         self.grads, self._table, self._plan, self._ref, self._bound = grads, table, plan, ctypes.addressof(plan), _stream()
 
     def step(self, grads=None, grad_scale=None):
-        """One step.  grads replace those of the last step (the table is made anew, which waits for
-        the stream); grad_scale: a float32 tensor of one element on the GPU that the gradients are
-        multiplied by."""
+        """One step.  grads replace those of the last step; grad_scale: a float32 tensor of one element on
+        the GPU that the gradients are multiplied by."""
         if self.index != _device():
             _elsewhere(self.params[0], "params[0]")
         if grads is not None:

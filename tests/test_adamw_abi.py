@@ -101,6 +101,23 @@ def test_step_refuses():
     assert step(p=vq.AdamWPlan(None, 0, 0, BF16, BF16, 0, 32))[0] == vq.VQ_OK
 
 
+def test_new_gradients_refuse():
+    lib = vq.load()
+    good = vq.AdamWPlan(FAKE, 2, 2, BF16, F32, 0, 32)
+
+    def grads(ptrs, p=good, count=None):
+        arr = (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs) if ptrs is not None else None
+        st = lib.vq_adamw_grads(ctypes.addressof(p) if p else None, arr, len(ptrs) if count is None else count, None)
+        return st, lib.vq_last_error().decode()
+
+    for args, msg in ((([FAKE, FAKE], None), "null"), (([FAKE],), "count"), (([FAKE, FAKE + 2],), "gradient 1"),
+                      ((None, good, 2), "null"), (([FAKE, FAKE], vq.AdamWPlan(None, 2, 2, BF16, F32, 0, 32)), "not made"),
+                      (([FAKE, FAKE], vq.AdamWPlan(FAKE, 2, 2, BF16, 7, 0, 32)), "not made")):
+        st, text = grads(*args)
+        assert st == vq.VQ_ERR_INVALID and msg in text and text.startswith("vq_adamw_grads"), args
+    assert grads([], vq.AdamWPlan(None, 0, 0, BF16, F32, 0, 32))[0] == vq.VQ_OK
+
+
 def test_python_checks():
     p = torch.zeros(8)
     with pytest.raises(ValueError, match="empty"):

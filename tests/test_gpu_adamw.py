@@ -183,10 +183,10 @@ def test_unaligned_views_and_neighbours(bits, offset):
             bufs.append((buf, view))
         flat[name] = [b for b, _ in bufs]
         opt.state[name] = [v for _, v in bufs]
-    opt.step(opt.grads)                                      # binds the moved moments; one step done
+    opt = vq.AdamW(opt.params, opt.grads, masters=opt.masters, state_bits=bits, state=opt.state, steps=3, **KW)
     before = snapshot(opt)
     opt.step()
-    check_step(opt, before, 5)
+    check_step(opt, before, 4)
     for name in ("m", "v"):
         for i, buf in enumerate(flat[name]):
             n = opt.params[i].numel()
@@ -260,6 +260,36 @@ def test_many_tensors_in_one_call():
     before = snapshot(opt)
     opt.step()
     check_step(opt, before, 4)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_new_gradients_every_step(captured):
+    """Gradients in new tensors at each step, of more tensors than one launch carries; captured too."""
+    sizes = [5 + i % 300 for i in range(1000)]
+    opt = build(sizes, torch.float32, torch.bfloat16, False, 32, 20, capturable=captured)
+    g = torch.Generator().manual_seed(21)
+    for k in range(3):
+        grads = [(1e-2 * torch.randn(n, generator=g)).bfloat16().cuda() for n in sizes]
+        opt_grads = opt.grads
+        opt.grads = grads                                    # what snapshot reads; step() is given them below
+        before = snapshot(opt)
+        opt.grads = opt_grads
+        if captured:
+            st = torch.cuda.Stream()
+            st.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=st):
+                opt.step(grads)
+            graph.replay()
+            torch.cuda.synchronize()
+        else:
+            opt.step(grads)
+        check_step(opt, before, 4 + k)
+    # of another type: the table is made anew
+    if not captured:
+        grads = [x.float() for x in grads]
+        opt.step(grads)
+        assert opt._plan.grad_dtype == 2
 
 
 def test_large_tensor():
