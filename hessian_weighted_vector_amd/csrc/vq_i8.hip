@@ -69,32 +69,87 @@ struct Eight {
             for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : (E)0.0f;
         }
     }
-    // The largest magnitude as bits: NaN and infinities are above every number.
-    __device__ __forceinline__ uint32_t top() const
+};
+
+// The largest magnitude as bits of a float32: NaN and infinities are above every number.
+// Bits without the sign order as the magnitudes do, two of 16 bits at a time.
+template <class E>
+struct Top {
+    typedef unsigned short U2 __attribute__((ext_vector_type(2)));
+    U2 m = {0, 0};
+    __device__ __forceinline__ void add(const Eight<E>& e)
     {
-        uint32_t t = 0;
+        uint32_t w[4];
+        __builtin_memcpy(w, &e.v, 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = __float_as_uint((float)v[i]) & 0x7fffffffu;
-            t = b > t ? b : t;
-        }
-        return t;
+        for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(U2, w[i] & 0x7fff7fffu));
     }
-    __device__ __forceinline__ uint2 codes(float top) const
+    __device__ __forceinline__ uint32_t bits() const
     {
-        uint32_t w[2] = {0, 0};
+        const unsigned short t = m[0] > m[1] ? m[0] : m[1];
+        return __float_as_uint((float)__builtin_bit_cast(E, t));
+    }
+};
+template <>
+struct Top<float> {
+    uint32_t m = 0;
+    __device__ __forceinline__ void add(const Eight<float>& e)
+    {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int k = top > 0.0f ? __float2int_rn(127.0f * (float)v[i] / top) : 0;
-            w[i >> 2] |= (uint32_t)(k & 0xff) << (8 * (i & 3));
+            const uint32_t b = __float_as_uint(e.v[i]) & 0x7fffffffu;
+            m = b > m ? b : m;
+        }
+    }
+    __device__ __forceinline__ uint32_t bits() const { return m; }
+};
+
+// Codes of a row whose largest magnitude has these bits; all zero where that is 0 or not finite.
+//
+// 16-bit elements: y = x (127 / top) in place of 127 x / top, at a fifth of a division's
+// instructions.  y is within 2^-23 of the quotient relatively, two units in its last place.  A
+// tie, k + 1/2 with k < 127, has eight bits, and any other quotient is 2^-19 of itself away from
+// one; so y with its last three bits rounded off is the tie where the quotient is one and on
+// the quotient's side of it elsewhere.  Adding 1.5 2^23 then rounds to an integer, ties to even,
+// whose low byte is the code.  Below 2^-90, where 127 / top could overflow, and for float32
+// elements, each is divided.
+template <class E>
+struct Coder {
+    float top, r;
+    bool divide;
+    __device__ __forceinline__ explicit Coder(uint32_t bits)
+    {
+        top = bits < 0x7f800000u ? __uint_as_float(bits) : 0.0f;
+        divide = sizeof(E) == 4 || (top > 0.0f && top < 0x1p-90f);
+        r = top > 0.0f && !divide ? 127.0f / top : 0.0f;
+    }
+    static __device__ __forceinline__ float scale(uint32_t bits) { return bits < 0x7f800000u ? __uint_as_float(bits) / 127.0f : NAN; }
+    __device__ __forceinline__ uint2 codes(const Eight<E>& e) const
+    {
+        uint32_t k[8];
+        if (divide) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) k[i] = top > 0.0f ? (uint32_t)__float2int_rn(127.0f * (float)e.v[i] / top) : 0u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = (float)e.v[i];
+                // of a row that is not finite: 0, not NaN
+                const uint32_t y = __float_as_uint(r > 0.0f ? x * r : 0.0f);
+                k[i] = __float_as_uint(__uint_as_float((y + 4u) & ~7u) + 0x1.8p23f);
+            }
+        }
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // bytes: v_perm takes the second operand's as 0..3, the first's as 4..7
+            const uint32_t lo = __builtin_amdgcn_perm(k[h * 4 + 1], k[h * 4], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(k[h * 4 + 3], k[h * 4 + 2], 0x04000c0cu);
+            w[h] = lo | hi;
         }
         return make_uint2(w[0], w[1]);
     }
 };
-
-// The largest of a row's bits as a number to divide by; 0 where the row holds none or is not finite.
-__device__ __forceinline__ float divisor(uint32_t bits) { return bits < 0x7f800000u ? __uint_as_float(bits) : 0.0f; }
-__device__ __forceinline__ float scale_of(uint32_t bits) { return bits < 0x7f800000u ? __uint_as_float(bits) / 127.0f : NAN; }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t t)
 {
@@ -118,42 +173,38 @@ __global__ __launch_bounds__(256) void k_i8_rows(const Rows a)
     const int first = (WAVES == 1 ? lane : threadIdx.x) * 8, stride = WAVES * 64 * 8;
     const E* row = static_cast<const E*>(a.X) + r * a.ldx;
     Eight<E> v[R];
-    uint32_t top = 0;
+    Top<E> most;
 #pragma unroll
     for (int i = 0; i < R; ++i)
         if (first + i * stride < a.cols) v[i].load(row, first + i * stride, a.cols, a.odd);
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        if (first + i * stride < a.cols) {
-            const uint32_t t = v[i].top();
-            top = t > top ? t : top;
-        }
+        if (first + i * stride < a.cols) most.add(v[i]);
     for (int c = first + R * stride; c < a.cols; c += stride) {
         Eight<E> w;
         w.load(row, c, a.cols, a.odd);
-        const uint32_t t = w.top();
-        top = t > top ? t : top;
+        most.add(w);
     }
-    top = wave_max(top);
+    uint32_t top = wave_max(most.bits());
     if (WAVES > 1) {
         if (lane == 0) tops[wave] = top;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < 4; ++k) top = tops[k] > top ? tops[k] : top;
     }
-    const float d = divisor(top);
+    const Coder<E> coder(top);
     int8_t* const q = a.q + r * a.ldq;
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        if (first + i * stride < a.cols) *reinterpret_cast<uint2*>(q + first + i * stride) = v[i].codes(d);
+        if (first + i * stride < a.cols) *reinterpret_cast<uint2*>(q + first + i * stride) = coder.codes(v[i]);
     for (int c = first + R * stride; c < a.cols; c += stride) {
         Eight<E> w;
         w.load(row, c, a.cols, a.odd);
-        *reinterpret_cast<uint2*>(q + c) = w.codes(d);
+        *reinterpret_cast<uint2*>(q + c) = coder.codes(w);
     }
     // columns past the last chunk
     for (int64_t c = (a.cols + 7) / 8 * 8 + first; c < a.ldq; c += stride) *reinterpret_cast<uint2*>(q + c) = make_uint2(0, 0);
-    if (first == 0) a.scale[r] = scale_of(top);
+    if (first == 0) a.scale[r] = Coder<E>::scale(top);
 }
 
 template <class E>
@@ -181,10 +232,9 @@ struct Scales {
 
 // Features m .. m+7 of token t: the epilogue of the dense calls from exact sums.
 template <class T, bool PAIR>
-__device__ __forceinline__ void finish(const Epilogue& e, const Scales& s, int64_t t, int m, int M, const int (&v)[8],
+__device__ __forceinline__ void finish(const Epilogue& e, const Scales& s, float sx, int64_t t, int m, int M, const int (&v)[8],
                                        const int (&u)[8])
 {
-    const float sx = s.x[t];
     float z[8], y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -239,7 +289,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(con
         return;
     }
     each_row<L>(acc, p0, q0, a.t.np, a.t.nq, wave, lane, pb0, pb1, qb0, qb1,
-                [&](int q, int p, int (&v)[8], int (&u)[8]) { finish<T, PAIR>(a.t.epi, a.s, q, p, a.t.np, v, u); });
+                [&](int q, int p, int (&v)[8], int (&u)[8]) { finish<T, PAIR>(a.t.epi, a.s, a.s.x[q], q, p, a.t.np, v, u); });
 }
 
 // Adds the parts [splits][matrices][T][pitch]; eight features a thread.
@@ -274,17 +324,20 @@ __global__ __launch_bounds__(256) void k_i8_finish(const Parts a)
             }
         }
     }
-    finish<T, PAIR>(a.epi, a.s, t, m, a.M, v, u);
+    finish<T, PAIR>(a.epi, a.s, a.s.x[t], t, m, a.M, v, u);
 }
 
 // ---- few tokens -------------------------------------------------------------------
 // A workgroup owns 16 rows of Q (of both matrices of a pair); its waves take blocks of
-// 64 H columns in turn, a lane's 16 bytes of a row being its operand.
+// 64 H columns in turn, a lane's 16 bytes of a row being its operand.  OWN: each
+// workgroup makes the codes of the few tokens itself, in LDS, while its first block of Q is on its way: the
+// launch in front (4 to 6 us) is not needed.
 struct FewI8 {
     const int8_t* Q[2];
     int64_t ldq;
     const int8_t* x;             // codes [T][ldx]
     int64_t ldx;
+    Rows rows;                   // OWN: the tokens; scale: written where part is
     int M, T, chunks;            // of 64 columns
     int splits, pitch;
     int* part;                   // [splits][matrices][T][pitch], or null
@@ -292,22 +345,33 @@ struct FewI8 {
     Epilogue epi;
 };
 
-template <class T, int NT, bool PAIR, int H>
+constexpr int kOwnBytes = 60 << 10;      // LDS for codes and the waves' sums
+constexpr int kOwnPad = 16;              // between the codes' rows: other banks
+
+template <class T, int NT, bool PAIR, int H, bool OWN>
 __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
 {
+    typedef typename T::E E;
     constexpr int NM = PAIR ? 2 : 1;
-    extern __shared__ __align__(16) int red[];                // [waves][NM][NT][64] of four features
+    extern __shared__ __align__(16) int red[];                // [waves][NM][NT][64] of four features; OWN: codes [T][ldx + pad]
+    __shared__ uint32_t tops[OWN ? 16 : 1][16];
+    __shared__ float own_scale[16];
     const int nwaves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
     const int m0 = blockIdx.x * 16;
     const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;      // rows and tokens past the last repeat it
+    int8_t* const codes = reinterpret_cast<int8_t*>(red + nwaves * NM * NT * 256);
+    const int ldc = (int)a.ldx + kOwnPad;
     const int8_t* w[NM];
     const int8_t* x[NT];
 #pragma unroll
     for (int m = 0; m < NM; ++m) w[m] = a.Q[m] + row * a.ldq + g * 16;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) x[n] = a.x + (int64_t)(n * 16 + r < a.T ? n * 16 + r : a.T - 1) * a.ldx + g * 16;
+    for (int n = 0; n < NT; ++n) {
+        const int t = n * 16 + r < a.T ? n * 16 + r : a.T - 1;
+        x[n] = (OWN ? codes + t * ldc : a.x + (int64_t)t * a.ldx) + g * 16;
+    }
     i32x4 acc[NM][NT];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
@@ -316,12 +380,15 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
     const int nfull = a.chunks / H;                           // blocks of H chunks
     const int f0 = (int)((int64_t)nfull * blockIdx.y / a.splits), f1 = (int)((int64_t)nfull * (blockIdx.y + 1) / a.splits);
     i32x4 wv[NM][H], xv[NT][H];
-    const auto load = [&](int kb, int j) {
+    const auto load_w = [&](int kb, int j) {
+        const int64_t c = ((int64_t)kb * H + j) * 64;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) wv[m][j] = *reinterpret_cast<const i32x4*>(w[m] + c);
+    };
+    const auto load_x = [&](int kb, int j) {
         const int64_t c = ((int64_t)kb * H + j) * 64;
 #pragma unroll
         for (int n = 0; n < NT; ++n) xv[n][j] = *reinterpret_cast<const i32x4*>(x[n] + c);
-#pragma unroll
-        for (int m = 0; m < NM; ++m) wv[m][j] = *reinterpret_cast<const i32x4*>(w[m] + c);
     };
     const auto multiply = [&](int j) {
 #pragma unroll
@@ -330,19 +397,77 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
             for (int n = 0; n < NT; ++n) acc[m][n] = I8::mfma(wv[m][j], xv[n][j], acc[m][n]);
     };
     int kb = f0 + wave;
-    if (kb < f1) {
+    if (OWN) {
+        // token after token, a thread every blockDim.x-th chunk; the first two of the first token stay in registers
+        const E* const X = static_cast<const E*>(a.rows.X);
+        const int first = threadIdx.x * 8, stride = blockDim.x * 8, cols = a.rows.cols, odd = a.rows.odd;
+        Eight<E> v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (first + i * stride < cols) v[i].load(X, first + i * stride, cols, odd);
+        __builtin_amdgcn_sched_barrier(0);
+        if (kb < f1) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) load_w(kb, j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < a.T; ++t) {
+            Top<E> most;
+            for (int c = first, i = 0; c < cols; c += stride, ++i) {
+                if (t == 0 && i < 2) {
+                    most.add(i ? v[1] : v[0]);
+                } else {
+                    Eight<E> e;
+                    e.load(X + t * a.rows.ldx, c, cols, odd);
+                    most.add(e);
+                }
+            }
+            const uint32_t top = wave_max(most.bits());
+            if (lane == 0) tops[t][wave] = top;
+        }
+        __syncthreads();
+        for (int t = 0; t < a.T; ++t) {
+            uint32_t top = 0;
+            for (int k = 0; k < nwaves; ++k) top = tops[t][k] > top ? tops[t][k] : top;
+            const Coder<E> coder(top);
+            for (int c = first, i = 0; c < cols; c += stride, ++i) {
+                if (t == 0 && i < 2) {
+                    *reinterpret_cast<uint2*>(codes + c) = coder.codes(i ? v[1] : v[0]);
+                } else {
+                    Eight<E> e;
+                    e.load(X + t * a.rows.ldx, c, cols, odd);
+                    *reinterpret_cast<uint2*>(codes + t * ldc + c) = coder.codes(e);
+                }
+            }
+            for (int c = (cols + 7) / 8 * 8 + first; c < (int)a.ldx; c += stride)
+                *reinterpret_cast<uint2*>(codes + t * ldc + c) = make_uint2(0, 0);
+            if (threadIdx.x == 0) {
+                own_scale[t] = Coder<E>::scale(top);
+                if (a.part && blockIdx.x == 0 && blockIdx.y == 0) a.rows.scale[t] = own_scale[t];
+            }
+        }
+        __syncthreads();
+        if (kb < f1) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) load_x(kb, j);
+        }
+    } else if (kb < f1) {
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            load(kb, j);
+            load_x(kb, j);
+            load_w(kb, j);
             __builtin_amdgcn_sched_barrier(0);
         }
+    }
+    if (kb < f1) {
 #pragma unroll 1
         for (; kb + nwaves < f1; kb += nwaves) {
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 multiply(j);
                 __builtin_amdgcn_sched_barrier(0);
-                load(kb + nwaves, j);
+                load_x(kb + nwaves, j);
+                load_w(kb + nwaves, j);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -387,7 +512,7 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
             for (int i = 0; i < 8; ++i) o[i] = z[m][i];
         }
     } else {
-        finish<T, PAIR>(a.epi, a.s, t, m0 + f * 8, a.M, z[0], z[1]);
+        finish<T, PAIR>(a.epi, a.s, OWN ? own_scale[t] : a.s.x[t], t, m0 + f * 8, a.M, z[0], z[1]);
     }
 }
 
@@ -446,24 +571,40 @@ struct Call {
     Epilogue epi;
 };
 
+// Whether a few-token product makes its own codes.
+bool own_codes(int64_t T, int64_t N, int waves, int nm)
+{
+    return T <= 16 && T * (round64(N) + kOwnPad) + waves * nm * 1024 <= kOwnBytes;
+}
+
 template <class T, int NT, bool PAIR>
-void few_launch(const FewI8& f, int waves, hipStream_t st)
+void few_launch(const FewI8& f, int waves, bool own, hipStream_t st)
 {
     const dim3 grid((unsigned)((f.M + 15) / 16), (unsigned)f.splits);
     const size_t lds = (size_t)waves * (PAIR ? 2 : 1) * NT * 256 * sizeof(int);
-    hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4>), grid, dim3(waves * 64), lds, st, f);
+    if constexpr (NT == 1) {
+        if (own) {
+            hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, 4, true>), grid, dim3(waves * 64), lds + f.T * (f.ldx + kOwnPad), st, f);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, false>), grid, dim3(waves * 64), lds, st, f);
 }
 
 template <class T, bool PAIR>
-vq_status launch(const Call& c, const Plan& p, const int8_t* x, const float* sx, int* part, hipStream_t st)
+vq_status launch(const Call& c, const Plan& p, const Rows& rows, int* part, hipStream_t st)
 {
+    const int8_t* const x = rows.q;
+    const float* const sx = rows.scale;
+    const bool own = p.few && own_codes(c.T, rows.cols, p.waves, c.nm);
+    if (!own) VQ_TRY(rows_codes(rows, c.dtype, st));
     const vq_i8matrix& w = *c.W[0];
     const Scales s{sx, {w.scale, PAIR ? c.W[1]->scale : nullptr}};
     const int64_t ldx = round64(w.N);
     if (p.few) {
-        const FewI8 f{{w.q, PAIR ? c.W[1]->q : nullptr}, w.ldq, x, ldx, (int)w.M, (int)c.T, (int)(ldx / 64), p.splits, p.pitch, part, s, c.epi};
-        if (c.T > 16) few_launch<T, 2, PAIR>(f, p.waves, st);
-        else few_launch<T, 1, PAIR>(f, p.waves, st);
+        const FewI8 f{{w.q, PAIR ? c.W[1]->q : nullptr}, w.ldq, x, ldx, rows, (int)w.M, (int)c.T, (int)(ldx / 64), p.splits, p.pitch, part, s, c.epi};
+        if (c.T > 16) few_launch<T, 2, PAIR>(f, p.waves, false, st);
+        else few_launch<T, 1, PAIR>(f, p.waves, own, st);
         VQ_LAUNCHED("k_i8_few");
     } else {
         I8Tile a{};
@@ -505,9 +646,9 @@ vq_status product(const Call& c, void* ws, hipStream_t st)
     int8_t* x = reinterpret_cast<int8_t*>(at);
     float* sx = reinterpret_cast<float*>(at += align_up(c.T * ldx));
     int* part = p.part_bytes ? reinterpret_cast<int*>(at += align_up(c.T * sizeof(float))) : nullptr;
-    VQ_TRY(rows_codes({c.X, c.T, c.ldx, (int)N, x, ldx, sx, odd_rows(c.X, c.ldx)}, c.dtype, st));
-    if (c.dtype == VQ_BF16) return c.nm > 1 ? launch<Bf16, true>(c, p, x, sx, part, st) : launch<Bf16, false>(c, p, x, sx, part, st);
-    return c.nm > 1 ? launch<F16, true>(c, p, x, sx, part, st) : launch<F16, false>(c, p, x, sx, part, st);
+    const Rows rows{c.X, c.T, c.ldx, (int)N, x, ldx, sx, odd_rows(c.X, c.ldx)};
+    if (c.dtype == VQ_BF16) return c.nm > 1 ? launch<Bf16, true>(c, p, rows, part, st) : launch<Bf16, false>(c, p, rows, part, st);
+    return c.nm > 1 ? launch<F16, true>(c, p, rows, part, st) : launch<F16, false>(c, p, rows, part, st);
 }
 
 // ---- argument checks ------------------------------------------------------------

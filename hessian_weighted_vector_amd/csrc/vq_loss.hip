@@ -513,7 +513,7 @@ __global__ __launch_bounds__(256) void k_loss_dx(const TokenGrads a)
     float s[8] = {};
     if (q >= 0) {
         const float* o = a.sums + (int64_t)q * a.pitch + p;
-#pragma unroll 4
+#pragma unroll 8
         for (int z = 0; z < a.splits; ++z) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -561,20 +561,28 @@ GradPlan grad_plan(int64_t Vp, int64_t T, int64_t N, bool with_x, bool with_w)
 {
     GradPlan best{};
     double least = 1e300;
-    const int64_t px = up(up(Vp, kBK), 2), pw = up(up(T, kBK), 2);
+    const int64_t px = up(up(Vp, kBK), 2);
     for (int small = 0; small < 2; ++small) {
         const Shape s = shape(small);
-        const int64_t tx = with_x ? up(N, s.bp) * up(T, s.bq) : 0, tw = with_w ? up(N, s.bp) * up(Vp, s.bq) : 0;
         const int slots = small ? 512 : 256;
-        for (int sx = 1; sx <= 16 && sx <= px; ++sx) {
-            const double per = small ? (tx * sx + tw <= 256 ? 0.8 : 1.15) : 1.45, round = small ? 4.0 : 10.0;
-            const double cx = tx ? 2.0 * up(px, sx) * per + round : 0.0, cw = tw ? 2.0 * pw * per + round : 0.0;
-            // the longer ones first, the shorter ones fill the last round
-            double t = std::max((cx * tx * sx + cw * tw) / slots + 0.5 * std::min(cx, cw), std::max(cx, cw));
-            t += 0.8e-6 * (double)T * N * (with_x ? sx : 0);
-            if (t < least) {
-                least = t;
-                best = {s, sx, cw > cx};
+        const double round = small ? 4.0 : 10.0;
+        for (int sx = 1; sx <= 32 && sx <= px; ++sx) {
+            // half of the tokens may be ignored, which leaves dX's tiles as long and half as many
+            double sum = 0.0;
+            int w_first = 0;
+            for (int64_t n : {T, up(T, 2)}) {
+                const int64_t tx = with_x ? up(N, s.bp) * up(n, s.bq) : 0, tw = with_w ? up(N, s.bp) * up(Vp, s.bq) : 0;
+                const double per = small ? (tx * sx + tw <= 256 ? 0.8 : 1.15) : 1.45;
+                const double cx = tx ? 2.0 * up(px, sx) * per + round : 0.0;
+                const double cw = tw ? 2.0 * up(up(n, kBK), 2) * per + round : 0.0;
+                // the longer ones first, the shorter ones fill the last round
+                sum += std::max((cx * tx * sx + cw * tw) / slots + 0.5 * std::min(cx, cw), std::max(cx, cw));
+                sum += 1.2e-6 * (double)n * N * (with_x ? sx : 0);
+                w_first = cw > cx;
+            }
+            if (sum < least) {
+                least = sum;
+                best = {s, sx, w_first};
             }
             if (!with_x) break;
         }

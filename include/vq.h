@@ -589,7 +589,7 @@ vq_status vq_cross_entropy(int64_t T, int64_t V, int64_t N, int dtype, const voi
  * keeps its precision down to 2^-27 of that.  Rows of dX of ignored tokens are zeros.
  * A label outside [0, V) makes its row of dX and all of dW NaN.  T = 0 writes a zero dW.
  * The vocabulary is taken in pieces: the workspace holds dz of one piece (about 128
- * MiB, at least 256 words), the learnt rows of X, and dX in float32, in up to 16 parts. */
+ * MiB, at least 256 words), the learnt rows of X, and dX in float32, in up to 32 parts. */
 size_t vq_cross_entropy_backward_workspace_bytes(int64_t T, int64_t V, int64_t N, const void* W, int64_t ldw, int want_dx,
                                                  int want_dw);
 vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, const float* dloss, const void* X, int64_t ldx,
