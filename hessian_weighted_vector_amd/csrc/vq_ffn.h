@@ -187,8 +187,9 @@ struct Words {
     uint16_t last;
     __device__ __forceinline__ void load(const void* p)
     {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-        __builtin_memcpy(q, __builtin_assume_aligned(reinterpret_cast<const void*>(at & ~(uintptr_t)3), 4), 16);
+        // by pointer arithmetic: an address made from a number would be loaded as of any memory, not the GPU's alone
+        const char* const at = static_cast<const char*>(p);
+        __builtin_memcpy(q, __builtin_assume_aligned(at - (reinterpret_cast<uintptr_t>(p) & 2), 4), 16);
         last = *reinterpret_cast<const uint16_t*>(at + 14);
     }
     // The elements; p as loaded from, or less by whole words.

@@ -327,17 +327,56 @@ __global__ __launch_bounds__(256) void k_i8_finish(const Parts a)
     finish<T, PAIR>(a.epi, a.s, a.s.x[t], t, m, a.M, v, u);
 }
 
+// The same with the scales, biases and residual of eight whole features read beforehand.
+template <class T, bool PAIR>
+struct Inputs {
+    typedef typename T::E E;
+    typedef typename T::V8 V8;
+    float w[PAIR ? 2 : 1][8];
+    V8 bias[PAIR ? 2 : 1], r;
+    __device__ __forceinline__ void load(const Epilogue& e, const Scales& s, int64_t t, int m)
+    {
+#pragma unroll
+        for (int k = 0; k < (PAIR ? 2 : 1); ++k) {
+            __builtin_memcpy(w[k], s.w[k] + m, 32);
+            if (e.bias[k]) __builtin_memcpy(&bias[k], static_cast<const E*>(e.bias[k]) + m, 16);
+        }
+        if (!PAIR && e.R) __builtin_memcpy(&r, static_cast<const E*>(e.R) + t * e.ldr + m, 16);
+    }
+    __device__ __forceinline__ void finish(const Epilogue& e, float sx, int64_t t, int m, int M, const int (&v)[8], const int (&u)[8]) const
+    {
+        float z[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[i] = (float)v[i] * sx * w[0][i];
+            if (e.bias[0]) z[i] += (float)bias[0][i];
+            if (PAIR) {
+                y[i] = (float)u[i] * sx * w[PAIR ? 1 : 0][i];
+                if (e.bias[1]) y[i] += (float)bias[PAIR ? 1 : 0][i];
+            }
+        }
+        activate(e.act, z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (PAIR) z[i] *= y[i];
+            else if (e.R) z[i] += (float)r[i];
+        }
+        store8<T>(e.Y, e.ldy, t, m, M, z);
+    }
+};
+
 // ---- few tokens -------------------------------------------------------------------
-// A workgroup owns 16 rows of Q (of both matrices of a pair); its waves take blocks of
-// 64 H columns in turn, a lane's 16 bytes of a row being its operand.  OWN: each
-// workgroup makes the codes of the few tokens itself, in LDS, while its first block of Q is on its way: the
-// launch in front (4 to 6 us) is not needed.
+// A workgroup owns 16 rows of Q (of both matrices of a pair); its waves take equal runs of
+// columns, a lane's 16 bytes of a row being its operand, with H chunks of 64 columns in
+// flight.  OWN > 0: each workgroup makes the codes of up to OWN tokens itself, in LDS, while its
+// first chunks of Q are on their way: the launch in front (4 to 6 us) is not needed.  A thread
+// holds all that it reads of the tokens in registers, NX chunks of eight a token.
 struct FewI8 {
     const int8_t* Q[2];
     int64_t ldq;
     const int8_t* x;             // codes [T][ldx]
     int64_t ldx;
-    Rows rows;                   // OWN: the tokens; scale: written where part is
+    Rows rows;                   // OWN: the tokens, at least eight columns; scale: written where part is
     int M, T, chunks;            // of 64 columns
     int splits, pitch;
     int* part;                   // [splits][matrices][T][pitch], or null
@@ -348,16 +387,16 @@ struct FewI8 {
 constexpr int kOwnBytes = 60 << 10;      // LDS for codes and the waves' sums
 constexpr int kOwnPad = 16;              // between the codes' rows: other banks
 
-template <class T, int NT, bool PAIR, int H, bool OWN>
+template <class T, int NT, bool PAIR, int H, int OWN, int NX>
 __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
 {
     typedef typename T::E E;
     constexpr int NM = PAIR ? 2 : 1;
     extern __shared__ __align__(16) int red[];                // [waves][NM][NT][64] of four features; OWN: codes [T][ldx + pad]
-    __shared__ uint32_t tops[OWN ? 16 : 1][16];
-    __shared__ float own_scale[16];
+    __shared__ uint32_t tops[OWN ? OWN : 1][16];
+    __shared__ float own_scale[OWN ? OWN : 1];
     const int nwaves = blockDim.x >> 6;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int m0 = blockIdx.x * 16;
     const int64_t row = m0 + r < a.M ? m0 + r : a.M - 1;      // rows and tokens past the last repeat it
@@ -377,122 +416,112 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
     for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[m][n] = i32x4{0, 0, 0, 0};
-    const int nfull = a.chunks / H;                           // blocks of H chunks
-    const int f0 = (int)((int64_t)nfull * blockIdx.y / a.splits), f1 = (int)((int64_t)nfull * (blockIdx.y + 1) / a.splits);
-    i32x4 wv[NM][H], xv[NT][H];
-    const auto load_w = [&](int kb, int j) {
-        const int64_t c = ((int64_t)kb * H + j) * 64;
+    // the wave's chunks of its split
+    const int c0 = (int)((int64_t)a.chunks * blockIdx.y / a.splits), c1 = (int)((int64_t)a.chunks * (blockIdx.y + 1) / a.splits);
+    const int wb = c0 + (c1 - c0) * wave / nwaves, n = c0 + (c1 - c0) * (wave + 1) / nwaves - wb;
+    i32x4 wv[NM][H], xv[OWN ? 1 : NT][OWN ? 1 : H];
+    const auto load_w = [&](int k, int j) {
+        const int64_t c = (int64_t)(wb + k) * 64;
 #pragma unroll
         for (int m = 0; m < NM; ++m) wv[m][j] = *reinterpret_cast<const i32x4*>(w[m] + c);
     };
-    const auto load_x = [&](int kb, int j) {
-        const int64_t c = ((int64_t)kb * H + j) * 64;
+    const auto load_x = [&](int k, int j) {
+        const int64_t c = (int64_t)(wb + k) * 64;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) xv[n][j] = *reinterpret_cast<const i32x4*>(x[n] + c);
+        for (int t = 0; t < NT; ++t) xv[t][j] = *reinterpret_cast<const i32x4*>(x[t] + c);
     };
-    const auto multiply = [&](int j) {
+    const auto multiply = [&](int k, int j) {
+        const int64_t c = (int64_t)(wb + k) * 64;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int t = 0; t < NT; ++t) {
+            i32x4 v;
+            if constexpr (OWN > 0) v = *reinterpret_cast<const i32x4*>(x[t] + c);
+            else v = xv[t][j];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[m][n] = I8::mfma(wv[m][j], xv[n][j], acc[m][n]);
-    };
-    int kb = f0 + wave;
-    if (OWN) {
-        // token after token, a thread every blockDim.x-th chunk; the first two of the first token stay in registers
-        const E* const X = static_cast<const E*>(a.rows.X);
-        const int first = threadIdx.x * 8, stride = blockDim.x * 8, cols = a.rows.cols, odd = a.rows.odd;
-        Eight<E> v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (first + i * stride < cols) v[i].load(X, first + i * stride, cols, odd);
-        __builtin_amdgcn_sched_barrier(0);
-        if (kb < f1) {
-#pragma unroll
-            for (int j = 0; j < H; ++j) load_w(kb, j);
+            for (int m = 0; m < NM; ++m) acc[m][t] = I8::mfma(wv[m][j], v, acc[m][t]);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        for (int t = 0; t < a.T; ++t) {
-            Top<E> most;
-            for (int c = first, i = 0; c < cols; c += stride, ++i) {
-                if (t == 0 && i < 2) {
-                    most.add(i ? v[1] : v[0]);
-                } else {
-                    Eight<E> e;
-                    e.load(X + t * a.rows.ldx, c, cols, odd);
-                    most.add(e);
-                }
+    };
+    // thread -> token t, features m .. m + 7 of the result; what its epilogue reads is requested now, not behind the sums
+    const int t_out = threadIdx.x >> 1, m_out = m0 + (threadIdx.x & 1) * 8;
+    const bool early = t_out < a.T && m_out + 8 <= a.M && !a.part;
+    Inputs<T, PAIR> in;
+    if (early) in.load(a.epi, a.s, t_out, m_out);
+    const auto prefetch = [&] {
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            if (j < n) {
+                if constexpr (OWN == 0) load_x(j, j);
+                load_w(j, j);
+                __builtin_amdgcn_sched_barrier(0);
             }
+    };
+    if constexpr (OWN > 0) {
+        const E* const X = static_cast<const E*>(a.rows.X);
+        const int cols = a.rows.cols, stride = blockDim.x * 8;
+        Eight<E> v[OWN][NX];
+        // chunks past the end repeat the row's last eight elements
+#pragma unroll
+        for (int t = 0; t < OWN; ++t)
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int c = (int)threadIdx.x * 8 + i * stride;
+                __builtin_memcpy(&v[t][i].v, X + (t < a.T ? t : a.T - 1) * a.rows.ldx + (c < cols - 8 ? c : cols - 8), 16);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        prefetch();
+#pragma unroll
+        for (int t = 0; t < OWN; ++t) {
+            Top<E> most;
+#pragma unroll
+            for (int i = 0; i < NX; ++i) most.add(v[t][i]);
             const uint32_t top = wave_max(most.bits());
             if (lane == 0) tops[t][wave] = top;
         }
         __syncthreads();
-        for (int t = 0; t < a.T; ++t) {
-            uint32_t top = 0;
-            for (int k = 0; k < nwaves; ++k) top = tops[t][k] > top ? tops[t][k] : top;
+#pragma unroll
+        for (int t = 0; t < OWN; ++t) {
+            if (t >= a.T) break;
+            const uint32_t top = wave_max(lane < nwaves ? tops[t][lane & 15] : 0u);
             const Coder<E> coder(top);
-            for (int c = first, i = 0; c < cols; c += stride, ++i) {
-                if (t == 0 && i < 2) {
-                    *reinterpret_cast<uint2*>(codes + c) = coder.codes(i ? v[1] : v[0]);
-                } else {
-                    Eight<E> e;
-                    e.load(X + t * a.rows.ldx, c, cols, odd);
-                    *reinterpret_cast<uint2*>(codes + t * ldc + c) = coder.codes(e);
-                }
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                // the codes from c on, of a chunk read `late` elements too early; zeros behind the row
+                const int c = (int)threadIdx.x * 8 + i * stride, late = c - (c < cols - 8 ? c : cols - 8);
+                uint64_t k = __builtin_bit_cast(uint64_t, coder.codes(v[t][i]));
+                k = late < 8 ? k >> (8 * late) : 0;
+                if (c < (int)a.ldx) *reinterpret_cast<uint64_t*>(codes + t * ldc + c) = k;
             }
-            for (int c = (cols + 7) / 8 * 8 + first; c < (int)a.ldx; c += stride)
-                *reinterpret_cast<uint2*>(codes + t * ldc + c) = make_uint2(0, 0);
             if (threadIdx.x == 0) {
                 own_scale[t] = Coder<E>::scale(top);
                 if (a.part && blockIdx.x == 0 && blockIdx.y == 0) a.rows.scale[t] = own_scale[t];
             }
         }
         __syncthreads();
-        if (kb < f1) {
-#pragma unroll
-            for (int j = 0; j < H; ++j) load_x(kb, j);
-        }
-    } else if (kb < f1) {
+    } else {
+        prefetch();
+    }
+    // a chunk's registers are refilled as soon as they are used
+#pragma unroll 1
+    for (int b = 0; b < n; b += H) {
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            load_x(kb, j);
-            load_w(kb, j);
+            if (b + j >= n) break;
+            multiply(b + j, j);
             __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-    if (kb < f1) {
-#pragma unroll 1
-        for (; kb + nwaves < f1; kb += nwaves) {
-#pragma unroll
-            for (int j = 0; j < H; ++j) {
-                multiply(j);
-                __builtin_amdgcn_sched_barrier(0);
-                load_x(kb + nwaves, j);
-                load_w(kb + nwaves, j);
+            if (b + j + H < n) {
+                if constexpr (OWN == 0) load_x(b + j + H, j);
+                load_w(b + j + H, j);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-#pragma unroll
-        for (int j = 0; j < H; ++j) multiply(j);
     }
-    // chunks past the last whole block, dealt to the waves of the last split
-    if (blockIdx.y == a.splits - 1)
-        for (int s = nfull * H + wave; s < a.chunks; s += nwaves) {
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                const i32x4 v = *reinterpret_cast<const i32x4*>(w[m] + (int64_t)s * 64);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[m][n] = I8::mfma(v, *reinterpret_cast<const i32x4*>(x[n] + (int64_t)s * 64), acc[m][n]);
-            }
-        }
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<i32x4*>(red + (((wave * NM + m) * NT + n) * 64 + lane) * 4) = acc[m][n];
     __syncthreads();
-    // thread -> token t, features m0 + 8 f .. + 7
-    const int t = threadIdx.x >> 1, f = threadIdx.x & 1;
-    if (t >= a.T || m0 + f * 8 >= a.M) return;
+    const int t = t_out, f = threadIdx.x & 1;
+    if (t >= a.T || m_out >= a.M) return;
     int z[2][8] = {};
 #pragma unroll
     for (int m = 0; m < NM; ++m)
@@ -507,13 +536,17 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
     if (a.part) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            int* o = a.part + (((int64_t)blockIdx.y * NM + m) * a.T + t) * a.pitch + m0 + f * 8;
+            int* o = a.part + (((int64_t)blockIdx.y * NM + m) * a.T + t) * a.pitch + m_out;
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = z[m][i];
         }
-    } else {
-        finish<T, PAIR>(a.epi, a.s, OWN ? own_scale[t] : a.s.x[t], t, m0 + f * 8, a.M, z[0], z[1]);
+        return;
     }
+    float sx;
+    if constexpr (OWN > 0) sx = own_scale[t];
+    else sx = a.s.x[t];
+    if (early) in.finish(a.epi, sx, t, m_out, a.M, z[0], z[1]);
+    else finish<T, PAIR>(a.epi, a.s, sx, t, m_out, a.M, z[0], z[1]);
 }
 
 // ---- plan -----------------------------------------------------------------------
@@ -531,10 +564,15 @@ Plan make_plan(int64_t T, int64_t M, int64_t N, int nm)
     p.pitch = (int)((M + 7) / 8 * 8);
     p.splits = 1;
     if (T <= 32) {
+        // Waves a workgroup of 16 rows, one token: 28672 x 8192 44.7 us with four and 47.0 with eight,
+        // 4096 x 11008 14.4 with eight and 15.3 with sixteen, 2048 x 8192 11.0 and 10.1; pairs of 8192 x
+        // 2048 12.3 with four and 11.4 with eight.  The columns are split over workgroups where even
+        // sixteen waves a workgroup leave half of the CUs idle: 1024 x 16384 11.0 over four, 13.1 over two.
         const int64_t groups = (M + 15) / 16, blocks = round64(N) / 512;
         p.few = 1;
-        p.waves = groups < 512 && blocks >= 16 ? 16 : 8;
-        while (p.splits < 16 && groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+        p.waves = groups > (nm > 1 ? 512 : 511) ? 4 : groups >= 128 && groups < 256 && blocks >= 16 ? 16 : 8;
+        while (p.splits < 16 && groups * p.splits < 128 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
+        if (p.splits > 1 && groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
     } else {
         double least = 1e300;
         for (int small = 0; small < 2; ++small) {
@@ -571,10 +609,13 @@ struct Call {
     Epilogue epi;
 };
 
-// Whether a few-token product makes its own codes.
+// Whether a few-token product makes its own codes: one or two tokens that its threads' registers
+// and LDS hold.  Matrices from memory, one token by 4096 x 11008: 14.4 us, 16.9 with the launch in
+// front; 8192 x 2048, 7.6 and 9.4; two by 2048 x 8192, 11.7 and 12.1.  Four are the same either way.
 bool own_codes(int64_t T, int64_t N, int waves, int nm)
 {
-    return T <= 16 && T * (round64(N) + kOwnPad) + waves * nm * 1024 <= kOwnBytes;
+    const int64_t chunks = (round64(N) / 8 + waves * 64 - 1) / (waves * 64);
+    return N >= 8 && T <= 2 && chunks <= 4 && T * (round64(N) + kOwnPad) + waves * nm * 1024 <= kOwnBytes;
 }
 
 template <class T, int NT, bool PAIR>
@@ -584,11 +625,13 @@ void few_launch(const FewI8& f, int waves, bool own, hipStream_t st)
     const size_t lds = (size_t)waves * (PAIR ? 2 : 1) * NT * 256 * sizeof(int);
     if constexpr (NT == 1) {
         if (own) {
-            hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, 4, true>), grid, dim3(waves * 64), lds + f.T * (f.ldx + kOwnPad), st, f);
+            const size_t all = lds + f.T * (f.ldx + kOwnPad);
+            if (f.T == 1) hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, 4, 1, 4>), grid, dim3(waves * 64), all, st, f);
+            else hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, 4, 2, 4>), grid, dim3(waves * 64), all, st, f);
             return;
         }
     }
-    hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, false>), grid, dim3(waves * 64), lds, st, f);
+    hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, 0, 1>), grid, dim3(waves * 64), lds, st, f);
 }
 
 template <class T, bool PAIR>

@@ -274,22 +274,29 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_grad(c
     });
 }
 
-// Few tokens: a wave takes 16 rows of W whole, a workgroup 64, tokens as they come.
+// Few tokens: a wave takes 16 rows of W whole, a workgroup 64, tokens as they come.  Where X
+// fits (LDS), it is staged there: its reads do not queue with those of W, of which sixteen
+// a lane are in flight.
 struct FewLogits {
     const char* W;
     const char* X;
     int64_t ldw, ldx, K;
     int V, T;
+    int ldl;                     // LDS: bytes of a staged row
     const int64_t* labels;
     float2* part;                // [workgroups][T]
     float* picked;
 };
 
-template <class T, int NT, int H, bool ODD>
+constexpr int kStaged = 40 << 10;            // bytes of X in LDS: three workgroups a CU
+
+template <class T, int NT, int H, bool ODD, bool LDS>
 __global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
 {
     typedef typename T::E E;
+    typedef typename T::V8 V8;
     constexpr int B = 32 * H;
+    extern __shared__ __align__(16) char staged[];               // [T][ldl], zeros past K
     __shared__ float2 sh[4][NT * 16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
@@ -297,23 +304,31 @@ __global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
     const int64_t row = m0 + r < a.V ? m0 + r : a.V - 1;         // rows and tokens past the last repeat it
     const E* const w = reinterpret_cast<const E*>(a.W) + row * a.ldw;
     const E* x[NT];
+    const char* xl[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-        x[n] = reinterpret_cast<const E*>(a.X) + (int64_t)(n * 16 + r < a.T ? n * 16 + r : a.T - 1) * a.ldx;
+    for (int n = 0; n < NT; ++n) {
+        const int t = n * 16 + r < a.T ? n * 16 + r : a.T - 1;
+        x[n] = reinterpret_cast<const E*>(a.X) + t * a.ldx;
+        xl[n] = staged + t * a.ldl + g * 16;
+    }
     f32x4 acc[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int nfull = (int)(a.K / B);
-    Ahead<T, ODD> wv[H], xv[NT][H];
+    Ahead<T, ODD> wv[H], xv[LDS ? 1 : NT][LDS ? 1 : H];
     const auto load = [&](int kb, int j) {
         const int64_t c = (int64_t)kb * B + j * 32 + g * 8;
+        if (!LDS)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) xv[n][j].load(x[n], c);
+            for (int n = 0; n < NT; ++n) xv[n][j].load(x[n], c);
         wv[j].load(w, c);
     };
-    const auto multiply = [&](int j) {
+    const auto multiply = [&](int kb, int j) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = T::mfma(wv[j].get(w), xv[n][j].get(x[n]), acc[n]);
+        for (int n = 0; n < NT; ++n) {
+            if (LDS) acc[n] = T::mfma(wv[j].get(w), *reinterpret_cast<const V8*>(xl[n] + ((int64_t)kb * B + j * 32) * 2), acc[n]);
+            else acc[n] = T::mfma(wv[j].get(w), xv[n][j].get(x[n]), acc[n]);
+        }
     };
     if (nfull > 0) {
 #pragma unroll
@@ -321,24 +336,34 @@ __global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
             load(0, j);
             __builtin_amdgcn_sched_barrier(0);
         }
+    }
+    if (LDS) {
+        for (int t = 0; t < a.T; ++t)
+            for (int c = threadIdx.x * 8; c * 2 < a.ldl; c += 256 * 8)
+                *reinterpret_cast<V8*>(staged + t * a.ldl + c * 2) =
+                    chunk_tail<T>(reinterpret_cast<const E*>(a.X) + t * a.ldx, c, a.K);
+        __syncthreads();
+    }
+    if (nfull > 0) {
 #pragma unroll 1
         for (int kb = 0; kb + 1 < nfull; ++kb) {
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                multiply(j);
+                multiply(kb, j);
                 __builtin_amdgcn_sched_barrier(0);
                 load(kb + 1, j);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
-        for (int j = 0; j < H; ++j) multiply(j);
+        for (int j = 0; j < H; ++j) multiply(nfull - 1, j);
     }
     for (int64_t c0 = (int64_t)nfull * B; c0 < a.K; c0 += 32) {
         const int64_t c = c0 + g * 8;
-        const typename T::V8 v = chunk_tail<T>(w, c, a.K);
+        const V8 v = chunk_tail<T>(w, c, a.K);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = T::mfma(v, chunk_tail<T>(x[n], c, a.K), acc[n]);
+        for (int n = 0; n < NT; ++n)
+            acc[n] = T::mfma(v, LDS ? *reinterpret_cast<const V8*>(xl[n] + c0 * 2) : chunk_tail<T>(x[n], c, a.K), acc[n]);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -502,19 +527,22 @@ struct TokenGrads {
     void* dX;
 };
 
-template <class T>
+// G lanes take every G-th part of eight columns and are added in a tree: many parts of few
+// tokens are in flight together.
+template <class T, int G>
 __global__ __launch_bounds__(256) void k_loss_dx(const TokenGrads a)
 {
-    const int per = a.pitch / 8;
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= per * a.T) return;
-    const int64_t t = e / per;
-    const int p = (int)(e - t * per) * 8, q = a.place[t];
+    const int per = a.pitch / 8, lane = threadIdx.x & 63;
+    constexpr int kChunks = 64 / G;                           // of a wave
+    const int64_t e = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * kChunks + lane % kChunks;
+    const bool in = e < per * a.T;
+    const int64_t t = in ? e / per : 0;
+    const int p = in ? (int)(e - t * per) * 8 : 0, q = in ? a.place[t] : -1;
     float s[8] = {};
     if (q >= 0) {
         const float* o = a.sums + (int64_t)q * a.pitch + p;
-#pragma unroll 8
-        for (int z = 0; z < a.splits; ++z) {
+#pragma unroll 4
+        for (int z = lane / kChunks; z < a.splits; z += G) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const f32x4 v = *reinterpret_cast<const f32x4*>(o + z * a.plane + h * 4);
@@ -522,11 +550,24 @@ __global__ __launch_bounds__(256) void k_loss_dx(const TokenGrads a)
                 for (int i = 0; i < 4; ++i) s[h * 4 + i] += v[i];
             }
         }
-        const float scale = a.head->inverse;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] *= scale;
     }
+#pragma unroll
+    for (int o = kChunks; o < 64; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += __shfl_xor(s[i], o);
+    if (!in || lane >= kChunks) return;
+    const float scale = a.head->inverse;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] *= scale;
     store8<T>(a.dX, a.ldx, t, p, a.N, s);
+}
+
+template <class T>
+void dx_launch(const TokenGrads& d, hipStream_t st)
+{
+    const int64_t n = d.T * (d.pitch / 8);
+    if (d.splits > 4) hipLaunchKernelGGL((k_loss_dx<T, 8>), dim3((unsigned)((n + 31) / 32)), dim3(256), 0, st, d);
+    else hipLaunchKernelGGL((k_loss_dx<T, 1>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, d);
 }
 
 // ---- plan -------------------------------------------------------------------
@@ -676,18 +717,21 @@ vq_status words(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, Mat& out, 
 // Whether the vocabulary is read for few tokens straight from memory.
 bool few(const Loss& a) { return a.T <= 32; }
 
-template <class T, int NT, int H>
+template <class T, int NT, int H, bool LDS>
 void few_launch(const FewLogits& f, bool odd, int groups, hipStream_t st)
 {
-    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true>), dim3(groups), dim3(256), 0, st, f);
-    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false>), dim3(groups), dim3(256), 0, st, f);
+    const size_t lds = LDS ? (size_t)f.T * f.ldl : 0;
+    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true, LDS>), dim3(groups), dim3(256), lds, st, f);
+    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false, LDS>), dim3(groups), dim3(256), lds, st, f);
 }
 
 template <class T>
-void few_tokens_launch(const FewLogits& f, bool odd, int groups, hipStream_t st)
+void few_tokens_launch(FewLogits f, bool odd, int groups, hipStream_t st)
 {
-    if (f.T > 16) few_launch<T, 2, 4>(f, odd, groups, st);
-    else few_launch<T, 1, 8>(f, odd, groups, st);
+    f.ldl = (int)std::min<int64_t>(up(f.K, 32) * 64 + 16, 1 << 30);          // 16 more: rows in other banks
+    if (f.T <= 16 && (int64_t)f.T * f.ldl <= kStaged) few_launch<T, 1, 16, true>(f, odd, groups, st);
+    else if (f.T > 16) few_launch<T, 2, 4, false>(f, odd, groups, st);
+    else few_launch<T, 1, 8, false>(f, odd, groups, st);
 }
 
 template <class T>
@@ -716,7 +760,7 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         float2* part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
         float* picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
         if (!run) return VQ_OK;
-        const FewLogits f{static_cast<const char*>(a.W), static_cast<const char*>(a.X), a.ldw, a.ldx, a.N, (int)a.V, (int)a.T,
+        const FewLogits f{static_cast<const char*>(a.W), static_cast<const char*>(a.X), a.ldw, a.ldx, a.N, (int)a.V, (int)a.T, 0,
                           a.labels, part, picked};
         const bool odd = odd_rows(a.W, a.ldw) || odd_rows(a.X, a.ldx);
         if (a.dtype == VQ_BF16) few_tokens_launch<Bf16>(f, odd, j.parts, st);
@@ -844,9 +888,8 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     if (!a.dX) return VQ_OK;
     const TokenGrads d{sums, std::min<int>(plan.splits, (int)up(up(std::min(Vp, a.V), kBK), 2)), (int)N8, (int)a.N, a.T * N8, a.T,
                        a.lddx, tk.head, place, a.dX};
-    const dim3 grid((unsigned)up(a.T * (N8 / 8), 256));
-    if (a.dtype == VQ_BF16) hipLaunchKernelGGL((k_loss_dx<Bf16>), grid, dim3(256), 0, st, d);
-    else hipLaunchKernelGGL((k_loss_dx<F16>), grid, dim3(256), 0, st, d);
+    if (a.dtype == VQ_BF16) dx_launch<Bf16>(d, st);
+    else dx_launch<F16>(d, st);
     VQ_LAUNCHED("k_loss_dx");
     return VQ_OK;
 }
