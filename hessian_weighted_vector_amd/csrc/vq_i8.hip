@@ -230,19 +230,31 @@ struct Scales {
     const float* w[2];           // a row's of each matrix
 };
 
-// Features m .. m+7 of token t: the epilogue of the dense calls from exact sums.
+// Features m .. m+7 of token t: the epilogue of the dense calls from exact sums; w0, w1:
+// these features' scales.
 template <class T, bool PAIR>
-__device__ __forceinline__ void finish(const Epilogue& e, const Scales& s, float sx, int64_t t, int m, int M, const int (&v)[8],
-                                       const int (&u)[8])
+__device__ __forceinline__ void finish(const Epilogue& e, const float (&w0)[8], const float (&w1)[8], float sx, int64_t t, int m,
+                                       int M, const int (&v)[8], const int (&u)[8])
 {
     float z[8], y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        z[i] = m + i < M ? (float)v[i] * sx * s.w[0][m + i] : 0.0f;
-        if (PAIR) y[i] = m + i < M ? (float)u[i] * sx * s.w[1][m + i] : 0.0f;
+        z[i] = (float)v[i] * sx * w0[i];
+        if (PAIR) y[i] = (float)u[i] * sx * w1[i];
     }
     if (PAIR) epilogue_pair<T>(e, t, m, M, z, y);
     else epilogue_one<T>(e, t, m, M, z);
+}
+
+// Scales m .. m+7 (0 from M on).
+__device__ __forceinline__ void eight_scales(const float* s, int m, int M, float (&w)[8])
+{
+    if (m + 8 <= M) {
+        __builtin_memcpy(w, s + m, 32);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = m + i < M ? s[m + i] : 0.0f;
+    }
 }
 
 // ---- the tiled product -------------------------------------------------------------
@@ -255,13 +267,22 @@ template <class T, int FP, int FQ, bool PAIR>
 __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(const I8Tile a)
 {
     typedef Main<I8, false, false, FP, FQ, PAIR> L;
+    constexpr int kP = PAIR ? L::BP / 2 : L::BP;              // features of the tile
     VQ_TILE_BUFFERS(L);
+    // the tile's scales, read while the product runs: in the epilogue a row's would be waited for each time
+    __shared__ __align__(16) float scale_q[L::BQ], scale_p[PAIR ? 2 : 1][kP];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / kWQ, wq = wave % kWQ, split = blockIdx.y;
     int tp, tq;
     pick_tile(blockIdx.x, a.t.ntp * a.t.ntq, a.t.ntp, a.t.ntq, tp, tq);
-    const int p0 = tp * (PAIR ? L::BP / 2 : L::BP), q0 = tq * L::BQ;
+    const int p0 = tp * kP, q0 = tq * L::BQ;
+    if (!a.t.part) {
+        for (int i = threadIdx.x; i < L::BQ; i += kThreads) scale_q[i] = a.s.x[q0 + i < a.t.nq ? q0 + i : a.t.nq - 1];
+#pragma unroll
+        for (int k = 0; k < (PAIR ? 2 : 1); ++k)
+            for (int i = threadIdx.x; i < kP; i += kThreads) scale_p[k][i] = a.s.w[k][p0 + i < a.t.np ? p0 + i : a.t.np - 1];
+    }
     const int pairs = (a.t.steps + 1) / 2;
     const int s0 = 2 * (int)((int64_t)pairs * split / a.t.splits), s1 = 2 * (int)((int64_t)pairs * (split + 1) / a.t.splits);
     i32x4 acc[FP][FQ];
@@ -288,8 +309,12 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(con
         __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));           // no load into LDS outlives the workgroup
         return;
     }
-    each_row<L>(acc, p0, q0, a.t.np, a.t.nq, wave, lane, pb0, pb1, qb0, qb1,
-                [&](int q, int p, int (&v)[8], int (&u)[8]) { finish<T, PAIR>(a.t.epi, a.s, a.s.x[q], q, p, a.t.np, v, u); });
+    each_row<L>(acc, p0, q0, a.t.np, a.t.nq, wave, lane, pb0, pb1, qb0, qb1, [&](int q, int p, int (&v)[8], int (&u)[8]) {
+        float w0[8], w1[8];
+        __builtin_memcpy(w0, __builtin_assume_aligned(scale_p[0] + (p - p0), 16), 32);
+        if (PAIR) __builtin_memcpy(w1, __builtin_assume_aligned(scale_p[PAIR ? 1 : 0] + (p - p0), 16), 32);
+        finish<T, PAIR>(a.t.epi, w0, w1, scale_q[q - q0], q, p, a.t.np, v, u);
+    });
 }
 
 // Adds the parts [splits][matrices][T][pitch]; eight features a thread.
@@ -324,7 +349,10 @@ __global__ __launch_bounds__(256) void k_i8_finish(const Parts a)
             }
         }
     }
-    finish<T, PAIR>(a.epi, a.s, a.s.x[t], t, m, a.M, v, u);
+    float w0[8], w1[8];
+    eight_scales(a.s.w[0], m, a.M, w0);
+    if (PAIR) eight_scales(a.s.w[1], m, a.M, w1);
+    finish<T, PAIR>(a.epi, w0, w1, a.s.x[t], t, m, a.M, v, u);
 }
 
 // The same with the scales, biases and residual of eight whole features read beforehand.
@@ -545,8 +573,11 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
     float sx;
     if constexpr (OWN > 0) sx = own_scale[t];
     else sx = a.s.x[t];
-    if (early) in.finish(a.epi, sx, t, m_out, a.M, z[0], z[1]);
-    else finish<T, PAIR>(a.epi, a.s, sx, t, m_out, a.M, z[0], z[1]);
+    if (early) return in.finish(a.epi, sx, t, m_out, a.M, z[0], z[1]);
+    float w0[8], w1[8];
+    eight_scales(a.s.w[0], m_out, a.M, w0);
+    if (PAIR) eight_scales(a.s.w[1], m_out, a.M, w1);
+    finish<T, PAIR>(a.epi, w0, w1, sx, t, m_out, a.M, z[0], z[1]);
 }
 
 // ---- plan -----------------------------------------------------------------------

@@ -174,10 +174,11 @@ struct Logits {
     int64_t ldz;
 };
 
-// The tile's sums; false where the grid's place holds none.
-template <class L>
+// The tile's sums; false where the grid's place holds none.  before(): what is to be under way
+// while the product runs.
+template <class L, class F>
 __device__ __forceinline__ bool logits_tile(const Tile& full, int n, int& p0, int& q0, int& tp, int wave, int lane, char* pb0,
-                                            char* pb1, char* qb0, char* qb1, f32x4 (&acc)[L::kFP][L::kFQ])
+                                            char* pb1, char* qb0, char* qb1, f32x4 (&acc)[L::kFP][L::kFQ], F before)
 {
     Tile t = full;
     t.nq = n;
@@ -187,6 +188,7 @@ __device__ __forceinline__ bool logits_tile(const Tile& full, int n, int& p0, in
     pick_tile(blockIdx.x, tiles, t.ntp, ntq, tp, tq);
     p0 = tp * L::BP;
     q0 = tq * L::BQ;
+    before();
 #pragma unroll
     for (int i = 0; i < L::kFP; ++i)
 #pragma unroll
@@ -206,7 +208,11 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_logits
     const int n = a.head->count;
     int p0, q0, tp;
     f32x4 acc[FP][FQ];
-    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc)) return;
+    __shared__ int labels[L::BQ];
+    const auto stage = [&] {
+        for (int i = threadIdx.x; i < L::BQ; i += kThreads) labels[i] = a.label[q0 + i < n ? q0 + i : n - 1];
+    };
+    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc, stage)) return;
     __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));               // no load into LDS outlives the workgroup
 
     // lane l: token l%16 of fragment j, words 4*(l/16) .. +3 of fragment i
@@ -223,7 +229,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_logits
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
         const int q = q0 + (wq * FQ + j) * 16 + (lane & 15);
-        const int want = q < n ? a.label[q] - a.v0 - first : -1;
+        const int want = q < n ? labels[q - q0] - a.v0 - first : -1;
         float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < FP; ++i)
@@ -261,10 +267,21 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_grad(c
     const int n = a.head->count;
     int p0, q0, tp;
     f32x4 acc[FP][FQ];
-    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc)) return;
+    // a token's values: read in the epilogue, each row of a tile would wait for them
+    __shared__ int labels[L::BQ];
+    __shared__ float lses[L::BQ], gs[L::BQ];
+    const auto stage = [&] {
+        for (int i = threadIdx.x; i < L::BQ; i += kThreads) {
+            const int q = q0 + i < n ? q0 + i : n - 1;
+            labels[i] = a.label[q];
+            lses[i] = a.lse[q];
+            gs[i] = a.g[q];
+        }
+    };
+    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc, stage)) return;
     each_row<L>(acc, p0, q0, (int)a.ldz, n, wave, lane, pb0, pb1, qb0, qb1, [&](int q, int p, float (&v)[8], float (&)[8]) {
-        const float lse = a.lse[q], g = a.g[q];
-        const int want = a.label[q] - a.v0 - p;
+        const float lse = lses[q - q0], g = gs[q - q0];
+        const int want = labels[q - q0] - a.v0 - p;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float e = exp_of(v[i] - lse);
