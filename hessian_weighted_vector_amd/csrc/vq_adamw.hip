@@ -118,23 +118,55 @@ __device__ __forceinline__ void decode(uint32_t w, float (&v)[4])
     v[0] = lo[0]; v[1] = lo[1]; v[2] = hi[0]; v[3] = hi[1];
 }
 
-// The wave's block in codes, and its scale.  NaN stays NaN (the maximum passes over it).
+// Codes of the quotients by scale, as float32 divides.  ROOT: of the elements' roots.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode_divided(const float (&x)[4], float scale)
+{
+    float y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float v = ROOT ? sqrtf(x[k]) : x[k];
+        y[k] = scale > 0.0f ? v / scale : v;
+        y[k] = y[k] > kTop ? kTop : y[k] < -kTop ? -kTop : y[k];     // the quotient's rounding
+        if (ROOT && x[k] > 0.0f && y[k] < kLeast) y[k] = kLeast;
+    }
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+}
+
+// The wave's block in codes, and its scale; with ROOT of the roots of x.  NaN stays NaN (the
+// maximum passes over it).
+//
+// Four divisions and four exact roots a lane would take as long as the memory.  The hardware's
+// reciprocal and root give the quotients within 2^-22; both ends of an interval of 2^-21 around
+// each are coded, and where they agree the quotient's code is theirs.  The others, a few in a
+// million, and blocks whose largest is so small that a reciprocal or a root could be
+// subnormal, are divided.
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode(const float (&x)[4], float& scale)
 {
     float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    scale = top * (1.0f / kTop);
-    float y[4];
+    scale = (ROOT ? sqrtf(top) : top) * (1.0f / kTop);
+    if (!(top >= 0x1p-90f && top < INFINITY)) return encode_divided<ROOT>(x, scale);
+    const float r = __builtin_amdgcn_rcpf(scale);
+    float lo[4], hi[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        y[k] = scale > 0.0f ? x[k] / scale : x[k];
-        y[k] = y[k] > kTop ? kTop : y[k] < -kTop ? -kTop : y[k];     // the quotient's rounding
-        if (ROOT && y[k] > 0.0f && y[k] < kLeast) y[k] = kLeast;
+        const float y = (ROOT ? __builtin_amdgcn_sqrtf(x[k]) : x[k]) * r;
+        const float least = ROOT && x[k] > 0.0f ? kLeast : -INFINITY;
+        lo[k] = y * (1.0f - 0x1p-21f);
+        hi[k] = __builtin_amdgcn_fmed3f(y * (1.0f + 0x1p-21f), -kTop, kTop);      // a number for NaN: the ends differ
+        if (ROOT) {
+            lo[k] = lo[k] < least ? least : lo[k];
+            hi[k] = hi[k] < least ? least : hi[k];
+        }
     }
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+    int a = __builtin_amdgcn_cvt_pk_fp8_f32(lo[0], lo[1], 0, false), b = __builtin_amdgcn_cvt_pk_fp8_f32(hi[0], hi[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(lo[2], lo[3], a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(hi[2], hi[3], b, true);
+    return a == b ? (uint32_t)a : encode_divided<ROOT>(x, scale);
 }
 
 // P: the parameter's type (the master is float32); G: the gradient's.
@@ -183,14 +215,14 @@ __global__ __launch_bounds__(256) void k_adamw(const Args a)
                 v[b][k] = r * r;
             }
         }
-        float root[4];
+        // the step's root and reciprocal are the hardware's, off by a unit in the last place each; the moments are not
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float gk = g[b][k] * gs;
             m[b][k] = c.b1 * m[b][k] + c.c1 * gk;
             v[b][k] = c.b2 * v[b][k] + c.c2 * (gk * gk);
-            root[k] = sqrtf(v[b][k]);
-            p[b][k] = p[b][k] * c.decay - c.rate * (m[b][k] / (root[k] * c.root + c.eps));
+            const float root = __builtin_amdgcn_sqrtf(v[b][k]);
+            p[b][k] = p[b][k] * c.decay - c.rate * (m[b][k] * __builtin_amdgcn_rcpf(root * c.root + c.eps));
         }
         if (MASTER) store4<float>(t.master, i, n, p[b]);
         store4<P>(t.param, i, n, p[b]);
@@ -201,10 +233,10 @@ __global__ __launch_bounds__(256) void k_adamw(const Args a)
             if (n < 4) {                                      // elements past the tensor's end have no part in the scale
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (k >= n) m[b][k] = root[k] = 0.0f;
+                    if (k >= n) m[b][k] = v[b][k] = 0.0f;
             }
             float s0, s1;
-            const uint32_t w0 = encode<false>(m[b], s0), w1 = encode<true>(root, s1);
+            const uint32_t w0 = encode<false>(m[b], s0), w1 = encode<true>(v[b], s1);
             store_codes(t.m, i, n, w0);
             store_codes(t.v, i, n, w1);
             if (lane == 0) {
