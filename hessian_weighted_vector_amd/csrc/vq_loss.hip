@@ -26,9 +26,11 @@
 // tokens, and workgroups past the count end at once.
 //
 // The logits and the sums of exponentials are float32; dz is rounded to the tensors'
-// type once, because the matrix cores read it in it.  In fp16 it is first multiplied by
-// a power of two that brings the largest |dloss| to 2^13, and dX and dW by its inverse: so
-// probabilities down to 2^-27 keep fp16's full precision.
+// type once, because the matrix cores read it in it.  Before, dloss is divided by its largest
+// magnitude, and dX and dW are multiplied by it: where every token has one weight, 1 / n say, its
+// rounding would otherwise be the same in every label's term, and the gradients' own (1 / 6927
+// in bf16: all of them off by 0.0021).  In fp16 dz is also multiplied by 2^13, so that
+// probabilities down to 2^-27 keep the type's full precision.
 #include "vq_few.h"
 #include "vq_tile.h"
 
@@ -45,7 +47,7 @@ constexpr int64_t kPieceBytes = 128 << 20;      // of dz, or of a packed piece o
 // What the index kernel leaves in front of the workspace.
 struct Head {
     int count;                   // tokens learnt
-    float scale, inverse;        // dz's power of two
+    float inverse;               // what dX and dW are multiplied by
 };
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
@@ -73,7 +75,7 @@ struct Index {
     const float* lse_in;
     float* g;                    // dloss and lse of each place
     float* lse_at;
-    int scaled;                  // whether dz takes a power of two
+    float lift;                  // dz's power of two
 };
 
 // One workgroup; a thread takes a run of consecutive tokens.
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(1024) void k_loss_index(const Index a)
     for (int64_t t = t0; t < t1; ++t) {
         const bool on = a.labels[t] != a.ignore;
         n += on;
-        if (a.scaled && on) top = fmaxf(top, fabsf(a.dloss[t]));
+        if (a.g && on) top = fmaxf(top, fabsf(a.dloss[t]));
     }
     int upto = n;
 #pragma unroll
@@ -106,12 +108,8 @@ __global__ __launch_bounds__(1024) void k_loss_index(const Index a)
         all += sums[w];
         top = fmaxf(top, tops[w]);
     }
-    float scale = 1.0f;
-    if (a.scaled && top > 0.0f && top < INFINITY) {
-        const int e = 13 - ilogbf(top);
-        scale = ldexpf(1.0f, e < -100 ? -100 : e > 100 ? 100 : e);
-    }
-    if (threadIdx.x == 0) *a.head = Head{all, scale, 1.0f / scale};
+    if (!(top > 0.0f && top < INFINITY)) top = 1.0f;
+    if (threadIdx.x == 0) *a.head = Head{all, top / a.lift};
     for (int64_t t = t0; t < t1; ++t) {
         const int64_t l = a.labels[t];
         const bool on = l != a.ignore;
@@ -124,7 +122,7 @@ __global__ __launch_bounds__(1024) void k_loss_index(const Index a)
         a.order[at] = (int)t;
         a.label[at] = known ? (int)l : -1;
         if (a.g) {
-            a.g[at] = known ? a.dloss[t] * scale : NAN;
+            a.g[at] = known ? a.dloss[t] / top * a.lift : NAN;
             a.lse_at[at] = a.lse_in[t];
         }
         ++at;
@@ -863,7 +861,7 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     ix.place = place;
     ix.dloss = a.dloss; ix.lse_in = a.lse_in;
     ix.g = g; ix.lse_at = lse;
-    ix.scaled = a.dtype == VQ_F16;
+    ix.lift = a.dtype == VQ_F16 ? 0x1p13f : 1.0f;
     VQ_TRY(tk.launch(a, ix, st));
     for (int64_t v0 = 0; v0 < a.V; v0 += Vp) {
         const int64_t n = std::min(Vp, a.V - v0), n8 = round8(n);

@@ -584,9 +584,9 @@ vq_status vq_cross_entropy(int64_t T, int64_t V, int64_t N, int dtype, const voi
 /* Gradients of sum_t dloss[t] loss[t]:  dz[t,v] = dloss[t] (exp(z[t,v] - lse[t]) -
  * [v = labels[t]]) with z formed again and lse as vq_cross_entropy gave it,
  *   dX = dz W [T x N],  dW = dz^T X [V x N]  (each may be NULL).
- * dz enters the products rounded to the tensors' type; in fp16 scaled by a power of
- * two that brings the largest |dloss| to 2^13 (and dX and dW back), so that it
- * keeps its precision down to 2^-27 of that.  Rows of dX of ignored tokens are zeros.
+ * dz enters the products divided by the largest |dloss| and rounded to the tensors' type, in fp16
+ * times 2^13, so that it keeps its precision down to 2^-27 of that; dX and dW are multiplied
+ * back in float32.  Rows of dX of ignored tokens are zeros.
  * A label outside [0, V) makes its row of dX and all of dW NaN.  T = 0 writes a zero dW.
  * The vocabulary is taken in pieces: the workspace holds dz of one piece (about 128
  * MiB, at least 256 words), the learnt rows of X, and dX in float32, in up to 32 parts. */

@@ -302,3 +302,19 @@ def test_value_check(monkeypatch):
     W[3, 3] = float("nan")
     with pytest.raises(vq.VQError, match="W holds"):
         vq.cross_entropy(X, W, labels)
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("n", [6927, 683, 1365])
+def test_one_weight_for_every_token(dtype, n):
+    """A dloss of 1 / n that the type does not hold: its rounding must not move the whole gradient one way.
+
+    The coefficient of the result along the exact gradient: independent roundings of u over thousands of terms leave
+    it within u / 4 of 1 (their sum along one direction is that of hundreds of terms at least: u / sqrt(100) and less).
+    """
+    X, W, labels, _ = inputs(800, 2000, 48, dtype, 23, masked=0.0)
+    dloss = torch.full((800,), 1.0 / n, device="cuda")
+    _, lse = vq.cross_entropy(X, W, labels)
+    for got, want in zip(vq.cross_entropy_backward(dloss, X, W, labels, lse), exact_on_gpu(X, W, labels, dloss, lse)):
+        along = float((got.double() * want).sum() / want.square().sum())
+        assert abs(along - 1) <= ref.UNIT[dtype] / 4
