@@ -398,7 +398,8 @@ struct Inputs {
 // columns, a lane's 16 bytes of a row being its operand, with H chunks of 64 columns in
 // flight.  OWN > 0: each workgroup makes the codes of up to OWN tokens itself, in LDS, while its
 // first chunks of Q are on their way: the launch in front (4 to 6 us) is not needed.  A thread
-// holds all that it reads of the tokens in registers, NX chunks of eight a token.
+// holds all that it reads of the tokens in registers, NX chunks of eight a token.  OWN < 0: the
+// same for short rows, a wave a token, up to -OWN tokens each.
 struct FewI8 {
     const int8_t* Q[2];
     int64_t ldq;
@@ -421,8 +422,8 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
     typedef typename T::E E;
     constexpr int NM = PAIR ? 2 : 1;
     extern __shared__ __align__(16) int red[];                // [waves][NM][NT][64] of four features; OWN: codes [T][ldx + pad]
-    __shared__ uint32_t tops[OWN ? OWN : 1][16];
-    __shared__ float own_scale[OWN ? OWN : 1];
+    __shared__ uint32_t tops[OWN > 0 ? OWN : 1][16];
+    __shared__ float own_scale[OWN > 0 ? OWN : OWN < 0 ? 32 : 1];
     const int nwaves = blockDim.x >> 6;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -463,7 +464,7 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             i32x4 v;
-            if constexpr (OWN > 0) v = *reinterpret_cast<const i32x4*>(x[t] + c);
+            if constexpr (OWN != 0) v = *reinterpret_cast<const i32x4*>(x[t] + c);
             else v = xv[t][j];
 #pragma unroll
             for (int m = 0; m < NM; ++m) acc[m][t] = I8::mfma(wv[m][j], v, acc[m][t]);
@@ -525,6 +526,41 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
             }
         }
         __syncthreads();
+    } else if constexpr (OWN < 0) {
+        const E* const X = static_cast<const E*>(a.rows.X);
+        const int cols = a.rows.cols;
+        Eight<E> v[-OWN][NX];
+#pragma unroll
+        for (int k = 0; k < -OWN; ++k)
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int c = lane * 8 + i * 512, t = wave + k * nwaves;
+                __builtin_memcpy(&v[k][i].v, X + (t < a.T ? t : a.T - 1) * a.rows.ldx + (c < cols - 8 ? c : cols - 8), 16);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        prefetch();
+#pragma unroll
+        for (int k = 0; k < -OWN; ++k) {
+            const int t = wave + k * nwaves;
+            if (t >= a.T) break;
+            Top<E> most;
+#pragma unroll
+            for (int i = 0; i < NX; ++i) most.add(v[k][i]);
+            const uint32_t top = wave_max(most.bits());
+            const Coder<E> coder(top);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const int c = lane * 8 + i * 512, late = c - (c < cols - 8 ? c : cols - 8);
+                uint64_t q = __builtin_bit_cast(uint64_t, coder.codes(v[k][i]));
+                q = late < 8 ? q >> (8 * late) : 0;
+                if (c < (int)a.ldx) *reinterpret_cast<uint64_t*>(codes + t * ldc + c) = q;
+            }
+            if (lane == 0) {
+                own_scale[t] = Coder<E>::scale(top);
+                if (a.part && blockIdx.x == 0 && blockIdx.y == 0) a.rows.scale[t] = own_scale[t];
+            }
+        }
+        __syncthreads();
     } else {
         prefetch();
     }
@@ -571,7 +607,7 @@ __global__ __launch_bounds__(1024) void k_i8_few(const FewI8 a)
         return;
     }
     float sx;
-    if constexpr (OWN > 0) sx = own_scale[t];
+    if constexpr (OWN != 0) sx = own_scale[t];
     else sx = a.s.x[t];
     if (early) return in.finish(a.epi, sx, t, m_out, a.M, z[0], z[1]);
     float w0[8], w1[8];
@@ -649,8 +685,18 @@ bool own_codes(int64_t T, int64_t N, int waves, int nm)
     return N >= 8 && T <= 2 && chunks <= 4 && T * (round64(N) + kOwnPad) + waves * nm * 1024 <= kOwnBytes;
 }
 
+// Chunks of eight a lane and token where waves make the codes of a few short rows, four in all;
+// 0 where they do not (8 by a pair of 8192 x 2048: 11.5 us, 14.6 with the launch in front).
+int wave_codes(int64_t T, int64_t N, int waves, int nm)
+{
+    if (N < 8 || T * (round64(N) + kOwnPad) + (int64_t)waves * nm * (T > 16 ? 2 : 1) * 1024 > kOwnBytes) return 0;
+    for (int nx : {1, 2, 4})
+        if (N <= 512 * nx && T <= waves * (4 / nx)) return nx;
+    return 0;
+}
+
 template <class T, int NT, bool PAIR>
-void few_launch(const FewI8& f, int waves, bool own, hipStream_t st)
+void few_launch(const FewI8& f, int waves, bool own, int nx, hipStream_t st)
 {
     const dim3 grid((unsigned)((f.M + 15) / 16), (unsigned)f.splits);
     const size_t lds = (size_t)waves * (PAIR ? 2 : 1) * NT * 256 * sizeof(int);
@@ -658,11 +704,17 @@ void few_launch(const FewI8& f, int waves, bool own, hipStream_t st)
         if (own) {
             const size_t all = lds + f.T * (f.ldx + kOwnPad);
             if (f.T == 1) hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, 4, 1, 4>), grid, dim3(waves * 64), all, st, f);
-            else hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, 4, 2, 4>), grid, dim3(waves * 64), all, st, f);
+            else hipLaunchKernelGGL((k_i8_few<T, 1, PAIR, PAIR ? 2 : 4, 2, 4>), grid, dim3(waves * 64), all, st, f);
             return;
         }
     }
-    hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, 0, 1>), grid, dim3(waves * 64), lds, st, f);
+    const size_t all = lds + f.T * (f.ldx + kOwnPad);
+    switch (nx) {
+    case 1: hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, -4, 1>), grid, dim3(waves * 64), all, st, f); break;
+    case 2: hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, -2, 2>), grid, dim3(waves * 64), all, st, f); break;
+    case 4: hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, -1, 4>), grid, dim3(waves * 64), all, st, f); break;
+    default: hipLaunchKernelGGL((k_i8_few<T, NT, PAIR, 4, 0, 1>), grid, dim3(waves * 64), lds, st, f);
+    }
 }
 
 template <class T, bool PAIR>
@@ -671,14 +723,15 @@ vq_status launch(const Call& c, const Plan& p, const Rows& rows, int* part, hipS
     const int8_t* const x = rows.q;
     const float* const sx = rows.scale;
     const bool own = p.few && own_codes(c.T, rows.cols, p.waves, c.nm);
-    if (!own) VQ_TRY(rows_codes(rows, c.dtype, st));
+    const int nx = p.few && !own ? wave_codes(c.T, rows.cols, p.waves, c.nm) : 0;
+    if (!own && nx == 0) VQ_TRY(rows_codes(rows, c.dtype, st));
     const vq_i8matrix& w = *c.W[0];
     const Scales s{sx, {w.scale, PAIR ? c.W[1]->scale : nullptr}};
     const int64_t ldx = round64(w.N);
     if (p.few) {
         const FewI8 f{{w.q, PAIR ? c.W[1]->q : nullptr}, w.ldq, x, ldx, rows, (int)w.M, (int)c.T, (int)(ldx / 64), p.splits, p.pitch, part, s, c.epi};
-        if (c.T > 16) few_launch<T, 2, PAIR>(f, p.waves, false, st);
-        else few_launch<T, 1, PAIR>(f, p.waves, own, st);
+        if (c.T > 16) few_launch<T, 2, PAIR>(f, p.waves, false, nx, st);
+        else few_launch<T, 1, PAIR>(f, p.waves, own, nx, st);
         VQ_LAUNCHED("k_i8_few");
     } else {
         I8Tile a{};

@@ -10,6 +10,8 @@
 //                   logit, the sum of exponentials below it, and the label's logit
 //   k_loss_few      the same for few tokens, the vocabulary read straight from memory
 //   k_loss_join     joins those pairs (m, s) in a fixed order: lse = m + log s
+//   k_loss_rows     a token's loss from split sums of its logits, where tiles are too few to
+//                   fill the card and N is split over workgroups; k_loss_dz: dz from them
 //   k_loss_grad     the tiled product z again, for one piece of the vocabulary; dz from it
 //   k_loss_two      the piece's rows of dW and its part of dX in one launch
 //   k_loss_dx       dX from the sums, in the caller's order; zeros for the other tokens
@@ -165,6 +167,9 @@ struct Logits {
     float2* part;                // [waves' columns of tiles][tokens]
     int64_t pitch;               // tokens a row of it
     float* picked;               // the labels' logits
+    // split sums: [t.splits][tokens][t.pitch], or null
+    float* sums;
+    int64_t plane;
     // backward
     const float* lse;
     const float* g;
@@ -187,11 +192,13 @@ __device__ __forceinline__ bool logits_tile(const Tile& full, int n, int& p0, in
     p0 = tp * L::BP;
     q0 = tq * L::BQ;
     before();
+    const int pairs = (t.steps + 1) / 2;
+    const int s0 = 2 * (int)((int64_t)pairs * blockIdx.y / t.splits), s1 = 2 * (int)((int64_t)pairs * (blockIdx.y + 1) / t.splits);
 #pragma unroll
     for (int i = 0; i < L::kFP; ++i)
 #pragma unroll
         for (int j = 0; j < L::kFQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    L::run(t, p0, q0, 0, 0, (t.steps + 1) / 2 * 2, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
+    L::run(t, p0, q0, 0, s0, s1, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
     return true;
 }
 
@@ -215,6 +222,19 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_logits
 
     // lane l: token l%16 of fragment j, words 4*(l/16) .. +3 of fragment i
     const int first = p0 + wp * FP * 16, quad = lane >> 4;
+    if (a.sums) {
+        float* const o = a.sums + blockIdx.y * a.plane;
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const int q = q0 + (wq * FQ + j) * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < FP; ++i) {
+                const int p = first + i * 16 + quad * 4;
+                if (q < n && p < a.t.np) *reinterpret_cast<f32x4*>(o + (int64_t)q * a.t.pitch + p) = acc[i][j];
+            }
+        }
+        return;
+    }
     if (first + FP * 16 > a.t.np) {
 #pragma unroll
         for (int i = 0; i < FP; ++i)
@@ -287,6 +307,86 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_grad(c
         }
         store8<T>(a.dz, a.ldz, q, p, (int)a.ldz, v);
     });
+}
+
+// The split sums of words p .. p+3 of a place, in order.
+__device__ __forceinline__ f32x4 joined_sums(const float* sums, int splits, int64_t plane, int64_t at)
+{
+    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) z += *reinterpret_cast<const f32x4*>(sums + k * plane + at);
+    return z;
+}
+
+// A workgroup a token.
+struct RowLoss {
+    const float* sums;
+    int splits, pitch, V;
+    int64_t plane;
+    const Head* head;
+    const int* order;
+    const int* label;
+    float* loss;
+    float* lse;
+};
+
+__global__ __launch_bounds__(256) void k_loss_rows(const RowLoss a)
+{
+    __shared__ float2 sh[4];
+    const int q = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (q >= a.head->count) return;
+    const int64_t row = (int64_t)q * a.pitch;
+    float m = -INFINITY, s = 0.0f;
+    for (int p = threadIdx.x * 4; p < a.V; p += 1024) {
+        const f32x4 z = joined_sums(a.sums, a.splits, a.plane, row + p);
+        float top = z[0], sum = 0.0f;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) top = p + i < a.V ? fmaxf(top, z[i]) : top;
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += p + i < a.V ? exp_of(z[i] - base) : 0.0f;
+        join(m, s, top, sum);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o));
+    if (lane == 0) sh[wave] = make_float2(m, s);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    m = sh[0].x;
+    s = sh[0].y;
+#pragma unroll
+    for (int k = 1; k < 4; ++k) join(m, s, sh[k].x, sh[k].y);
+    const int want = a.label[q];
+    const float lse = m + logf(s);
+    float loss = NAN;
+    if (want >= 0) {
+        const f32x4 z = joined_sums(a.sums, a.splits, a.plane, row + (want & ~3));
+        loss = lse - (want & 2 ? (want & 1 ? z[3] : z[2]) : (want & 1 ? z[1] : z[0]));
+    }
+    a.loss[a.order[q]] = loss;
+    a.lse[a.order[q]] = lse;
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_loss_dz(const Logits a, int64_t places)
+{
+    const int per = (int)(a.ldz / 8);
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, q = e / per;
+    if (q >= places || q >= a.head->count) return;
+    const int p = (int)(e - q * per) * 8;
+    const float lse = a.lse[q], g = a.g[q];
+    const int want = a.label[q] - a.v0 - p;
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x4 z = joined_sums(a.sums, a.t.splits, a.plane, q * a.t.pitch + p + h * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = exp_of(z[i] - lse);
+            v[h * 4 + i] = p + h * 4 + i < a.t.np ? (h * 4 + i == want ? x - 1.0f : x) * g : 0.0f;
+        }
+    }
+    store8<T>(a.dz, a.ldz, q, p, (int)a.ldz, v);
 }
 
 // Few tokens: a wave takes 16 rows of W whole, a workgroup 64, tokens as they come.  Where X
@@ -601,11 +701,30 @@ double tiles_cost(int small, int64_t tiles, double steps)
     return (double)(tiles / 512) * (steps * 1.15 + 4.0) + (rest ? steps * (rest <= 256 ? 0.8 : 1.15) + 4.0 : 0.0);
 }
 
-Shape logits_shape(int64_t V, int64_t T, int64_t N)
+// The logits of V words: the shape, and over how many workgroups N is split where the tiles are few
+// (one more launch where dz comes of it; the forward pass joins parts either way).
+struct LogitsPlan {
+    Shape s;
+    int splits;
+};
+LogitsPlan logits_plan(int64_t V, int64_t T, int64_t N, bool backward, bool may_split)
 {
-    const double st = 2.0 * up(up(N, kBK), 2);
-    const double big = tiles_cost(0, up(V, 256) * up(T, 256), st), little = tiles_cost(1, up(V, 128) * up(T, 128), st);
-    return shape(little < big);
+    LogitsPlan best{};
+    double least = 1e300;
+    const int64_t pairs = up(up(N, kBK), 2);
+    for (int small = 0; small < 2; ++small) {
+        const Shape s = shape(small);
+        const int64_t tiles = up(V, s.bp) * up(T, s.bq);
+        for (int sp = 1; sp <= 16 && sp <= pairs && (sp == 1 || may_split); ++sp) {
+            double t = tiles_cost(small, tiles * sp, 2.0 * up(pairs, sp));
+            if (sp > 1) t += (backward ? 6.0 : 2.0) + 0.9e-6 * (double)T * V * (sp + 1);
+            if (t < least) {
+                least = t;
+                best = {s, sp};
+            }
+        }
+    }
+    return best;
 }
 
 // Both gradients of a piece in one launch: the shape, and how many parts dX's sums are in.
@@ -752,7 +871,8 @@ void few_tokens_launch(FewLogits f, bool odd, int groups, hipStream_t st)
 template <class T>
 void logits_launch(const Logits& g, const Shape& s, bool backward, hipStream_t st)
 {
-    const dim3 grid((unsigned)(g.t.ntp * g.t.ntq));
+    const dim3 grid((unsigned)(g.t.ntp * g.t.ntq), (unsigned)g.t.splits);
+    if (g.sums) backward = false;                             // dz comes of the joined sums
     if (s.small) {
         if (backward) hipLaunchKernelGGL((k_loss_grad<T, 4, 2>), grid, dim3(kThreads), 0, st, g);
         else hipLaunchKernelGGL((k_loss_logits<T, 4, 2>), grid, dim3(kThreads), 0, st, g);
@@ -788,12 +908,20 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         const bool copied = !loads_ok({a.W, a.V, a.N, a.ldw});
         const int64_t Vp = copied ? piece(a.V, 2 * round8(a.N)) : a.V;
         uint16_t* copy = copied ? static_cast<uint16_t*>(ws.take(Vp * round8(a.N) * 2)) : nullptr;
-        const Shape s = logits_shape(Vp, a.T, a.N);
+        const LogitsPlan plan = logits_plan(Vp, a.T, a.N, false, Vp >= a.V);
+        const Shape s = plan.s;
         const int per = kWP * (int)up(Vp, s.bp);              // parts of a piece
-        j.parts = 0;
-        for (int64_t v0 = 0; v0 < a.V; v0 += Vp) j.parts += kWP * (int)up(std::min(Vp, a.V - v0), s.bp);
-        float2* part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
-        float* picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
+        const int64_t pitch = round8(a.V);
+        float2* part = nullptr;
+        float* picked = nullptr;
+        float* sums = nullptr;
+        if (plan.splits > 1) {
+            sums = static_cast<float*>(ws.take(plan.splits * a.T * pitch * sizeof(float)));
+        } else {
+            for (int64_t v0 = 0; v0 < a.V; v0 += Vp) j.parts += kWP * (int)up(std::min(Vp, a.V - v0), s.bp);
+            part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
+            picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
+        }
         if (!run) return VQ_OK;
         Index ix{};
         ix.loss = a.loss; ix.lse = a.lse;
@@ -806,10 +934,23 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
             g.t = tile_of(w.p, w.ld, w.cols, n, 0, tk.x, tk.ldx, tk.ldx, a.T, 0, s);
             g.head = tk.head; g.label = tk.label;
             g.v0 = (int)v0;
-            g.part = part + k * per * a.T; g.pitch = a.T; g.picked = picked;
+            if (sums) {
+                g.t.splits = plan.splits;
+                g.t.pitch = (int)pitch;
+                g.sums = sums;
+                g.plane = a.T * pitch;
+            } else {
+                g.part = part + k * per * a.T; g.pitch = a.T; g.picked = picked;
+            }
             if (a.dtype == VQ_BF16) logits_launch<Bf16>(g, s, false, st);
             else logits_launch<F16>(g, s, false, st);
             VQ_LAUNCHED("k_loss_logits");
+        }
+        if (sums) {
+            const RowLoss r{sums, plan.splits, (int)pitch, (int)a.V, a.T * pitch, tk.head, tk.order, tk.label, a.loss, a.lse};
+            hipLaunchKernelGGL(k_loss_rows, dim3((unsigned)a.T), dim3(256), 0, st, r);
+            VQ_LAUNCHED("k_loss_rows");
+            return VQ_OK;
         }
         j.part = part; j.picked = picked;
         j.head = tk.head; j.order = tk.order;
@@ -825,6 +966,20 @@ void grads_launch(const Grads& g, const GradPlan& p, hipStream_t st)
     const dim3 grid((unsigned)((g.with_x ? g.x.ntp * g.x.ntq * g.x.splits : 0) + (g.with_w ? g.w.ntp * g.w.ntq : 0)));
     if (p.s.small) hipLaunchKernelGGL((k_loss_two<T, 4, 2>), grid, dim3(kThreads), 0, st, g);
     else hipLaunchKernelGGL((k_loss_two<T, 8, 4>), grid, dim3(kThreads), 0, st, g);
+}
+
+template <class T>
+vq_status piece_launch(const Logits& l, const Shape& s, const Grads& g, const GradPlan& plan, int64_t tokens, hipStream_t st)
+{
+    logits_launch<T>(l, s, true, st);
+    VQ_LAUNCHED("k_loss_grad");
+    if (l.sums) {
+        hipLaunchKernelGGL((k_loss_dz<T>), dim3((unsigned)up(tokens * (l.ldz / 8), 256)), dim3(256), 0, st, l, tokens);
+        VQ_LAUNCHED("k_loss_dz");
+    }
+    grads_launch<T>(g, plan, st);
+    VQ_LAUNCHED("k_loss_two");
+    return VQ_OK;
 }
 
 __global__ __launch_bounds__(256) void k_loss_zero(uint16_t* __restrict__ o, int64_t rows, int64_t cols, int64_t ld)
@@ -856,6 +1011,9 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     void* dz = ws.take(a.T * Vp * 2);
     const GradPlan plan = grad_plan(std::min(Vp, a.V), a.T, a.N, a.dX, a.dW);
     float* sums = a.dX ? static_cast<float*>(ws.take(plan.splits * a.T * N8 * sizeof(float))) : nullptr;
+    const LogitsPlan zplan = logits_plan(std::min(Vp, a.V), a.T, a.N, true, true);
+    const int64_t zpitch = round8(std::min(Vp, a.V));
+    float* zsums = zplan.splits > 1 ? static_cast<float*>(ws.take(zplan.splits * a.T * zpitch * sizeof(float))) : nullptr;
     if (!run) return VQ_OK;
     Index ix{};
     ix.place = place;
@@ -867,9 +1025,13 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         const int64_t n = std::min(Vp, a.V - v0), n8 = round8(n);
         Mat w;
         VQ_TRY(words(a, v0, n, copy, w, st));
-        const Shape s = logits_shape(n, a.T, a.N);
+        const Shape s = zplan.s;
         Logits l{};
         l.t = tile_of(w.p, w.ld, w.cols, n, 0, tk.x, tk.ldx, tk.ldx, a.T, 0, s);
+        l.t.splits = zplan.splits;
+        l.t.pitch = (int)zpitch;
+        l.sums = zsums;
+        l.plane = a.T * zpitch;
         l.head = tk.head; l.label = tk.label;
         l.v0 = (int)v0;
         l.lse = lse; l.g = g;
@@ -889,16 +1051,8 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         b.lddw = a.lddw;
         b.with_x = a.dX != nullptr; b.with_w = a.dW != nullptr;
         b.w_first = plan.w_first;
-        if (a.dtype == VQ_BF16) {
-            logits_launch<Bf16>(l, s, true, st);
-            VQ_LAUNCHED("k_loss_grad");
-            grads_launch<Bf16>(b, plan, st);
-        } else {
-            logits_launch<F16>(l, s, true, st);
-            VQ_LAUNCHED("k_loss_grad");
-            grads_launch<F16>(b, plan, st);
-        }
-        VQ_LAUNCHED("k_loss_two");
+        if (a.dtype == VQ_BF16) VQ_TRY(piece_launch<Bf16>(l, s, b, plan, a.T, st));
+        else VQ_TRY(piece_launch<F16>(l, s, b, plan, a.T, st));
     }
     if (!a.dX) return VQ_OK;
     const TokenGrads d{sums, std::min<int>(plan.splits, (int)up(up(std::min(Vp, a.V), kBK), 2)), (int)N8, (int)a.N, a.T * N8, a.T,

@@ -575,7 +575,8 @@ vq_status vq_quantize_rows(int64_t rows, int64_t cols, int dtype, const void* X,
  * reproducible for fixed arguments.  0 <= T <= 2^20, 1 <= V, N <= 2^20; T = 0 is a no-op.
  * Outputs may not overlap inputs or each other.  A reduction (mean over the
  * learnt tokens, weights) is the caller's, as is dloss below.  Workspaces as in the dense
- * calls: about T (2 N + 16 + V / 16) bytes. */
+ * calls: about T (2 N + 16 + V / 16) bytes; where few logits of long rows are split over
+ * workgroups, their float32 parts instead of the last term. */
 size_t vq_cross_entropy_workspace_bytes(int64_t T, int64_t V, int64_t N, const void* W, int64_t ldw);
 vq_status vq_cross_entropy(int64_t T, int64_t V, int64_t N, int dtype, const void* X, int64_t ldx, const void* W, int64_t ldw,
                            const int64_t* labels, int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
