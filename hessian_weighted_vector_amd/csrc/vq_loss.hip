@@ -389,9 +389,9 @@ __global__ __launch_bounds__(256) void k_loss_dz(const Logits a, int64_t places)
     store8<T>(a.dz, a.ldz, q, p, (int)a.ldz, v);
 }
 
-// Few tokens: a wave takes 16 rows of W whole, a workgroup 64, tokens as they come.  Where X
-// fits (LDS), it is staged there: its reads do not queue with those of W, of which sixteen
-// a lane are in flight.
+// Few tokens, as they come: KS waves take 16 rows of W together, blocks of 32 H columns in
+// turn; a workgroup takes 64 rows where a wave takes 16 whole.  Where X fits (LDS), it is staged
+// there: its reads do not queue with those of W.
 struct FewLogits {
     const char* W;
     const char* X;
@@ -405,17 +405,19 @@ struct FewLogits {
 
 constexpr int kStaged = 40 << 10;            // bytes of X in LDS: three workgroups a CU
 
-template <class T, int NT, int H, bool ODD, bool LDS>
-__global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
+template <class T, int NT, int H, bool ODD, bool LDS, int KS>
+__global__ __launch_bounds__(KS > 4 ? KS * 64 : 256) void k_loss_few(const FewLogits a)
 {
     typedef typename T::E E;
     typedef typename T::V8 V8;
     constexpr int B = 32 * H;
     extern __shared__ __align__(16) char staged[];               // [T][ldl], zeros past K
-    __shared__ float2 sh[4][NT * 16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
-    const int m0 = blockIdx.x * 64 + wave * 16;
+    constexpr int kGroups = KS > 1 ? 1 : 4, kThreads = KS > 4 ? KS * 64 : 256;
+    __shared__ float2 sh[kGroups][NT * 16];
+    __shared__ f32x4 red[KS > 1 ? KS - 1 : 1][NT][KS > 1 ? 64 : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4, ks = wave % KS;
+    const int m0 = blockIdx.x * 16 * kGroups + wave / KS * 16;
     const int64_t row = m0 + r < a.V ? m0 + r : a.V - 1;         // rows and tokens past the last repeat it
     const E* const w = reinterpret_cast<const E*>(a.W) + row * a.ldw;
     const E* x[NT];
@@ -445,40 +447,52 @@ __global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
             else acc[n] = T::mfma(wv[j].get(w), xv[n][j].get(x[n]), acc[n]);
         }
     };
-    if (nfull > 0) {
+    if (ks < nfull) {
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            load(0, j);
+            load(ks, j);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (LDS) {
         for (int t = 0; t < a.T; ++t)
-            for (int c = threadIdx.x * 8; c * 2 < a.ldl; c += 256 * 8)
+            for (int c = threadIdx.x * 8; c * 2 < a.ldl; c += kThreads * 8)
                 *reinterpret_cast<V8*>(staged + t * a.ldl + c * 2) =
                     chunk_tail<T>(reinterpret_cast<const E*>(a.X) + t * a.ldx, c, a.K);
         __syncthreads();
     }
-    if (nfull > 0) {
+    if (ks < nfull) {
+        int kb = ks;
 #pragma unroll 1
-        for (int kb = 0; kb + 1 < nfull; ++kb) {
+        for (; kb + KS < nfull; kb += KS) {
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 multiply(kb, j);
                 __builtin_amdgcn_sched_barrier(0);
-                load(kb + 1, j);
+                load(kb + KS, j);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
-        for (int j = 0; j < H; ++j) multiply(nfull - 1, j);
+        for (int j = 0; j < H; ++j) multiply(kb, j);
     }
-    for (int64_t c0 = (int64_t)nfull * B; c0 < a.K; c0 += 32) {
+    for (int64_t c0 = (int64_t)nfull * B + ks * 32; c0 < a.K; c0 += KS * 32) {
         const int64_t c = c0 + g * 8;
         const V8 v = chunk_tail<T>(w, c, a.K);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             acc[n] = T::mfma(v, LDS ? *reinterpret_cast<const V8*>(xl[n] + c0 * 2) : chunk_tail<T>(x[n], c, a.K), acc[n]);
+    }
+    if (KS > 1) {                                                // the first wave adds the others' sums in order
+        if (ks > 0)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) red[ks > 0 ? ks - 1 : 0][n][lane] = acc[n];
+        __syncthreads();
+        if (ks > 0) return;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < KS - 1; ++k) acc[n] += red[k][n][lane];
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -495,7 +509,11 @@ __global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
             if (m0 + g * 4 + i < a.V) s += exp_of(acc[n][i] - base);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        if (g == 0) sh[wave][t] = make_float2(m, s);
+        if (KS > 1) {
+            if (g == 0 && t < a.T) a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(m, s);
+        } else if (g == 0) {
+            sh[wave % kGroups][t] = make_float2(m, s);
+        }
         if (t < a.T) {
             const int64_t want = a.labels[t] - m0 - g * 4;
 #pragma unroll
@@ -503,12 +521,13 @@ __global__ __launch_bounds__(256) void k_loss_few(const FewLogits a)
                 if (want == i && m0 + g * 4 + i < a.V) a.picked[t] = acc[n][i];
         }
     }
+    if (KS > 1) return;
     __syncthreads();
     const int t = threadIdx.x;
     if (t < a.T) {
         float m = sh[0][t].x, s = sh[0][t].y;
 #pragma unroll
-        for (int k = 1; k < 4; ++k) join(m, s, sh[k][t].x, sh[k][t].y);
+        for (int k = 1; k < kGroups; ++k) join(m, s, sh[k][t].x, sh[k][t].y);
         a.part[(int64_t)blockIdx.x * a.T + t] = make_float2(m, s);
     }
 }
@@ -848,24 +867,46 @@ vq_status words(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, Mat& out, 
     return pack_launch(k, st);
 }
 
-// Whether the vocabulary is read for few tokens straight from memory.
-bool few(const Loss& a) { return a.T <= 32; }
+// Whether the vocabulary is read for few tokens straight from memory.  One token by 131072 x 4096
+// 198 us here and 210 in tiles, sixteen 250 and 199; sixteen by 32768 x 4096 69 and 101.
+bool few(const Loss& a) { return a.T <= 8 || (a.T <= 32 && a.V * a.N < (int64_t)1 << 28); }
 
-template <class T, int NT, int H, bool LDS>
-void few_launch(const FewLogits& f, bool odd, int groups, hipStream_t st)
+// Waves that share 16 rows of W.  One token, by one, four and sixteen: 32768 x 4096 64, 58 and 57 us,
+// 32768 x 2048 32, 35 and 34, 2048 x 8192 35, 16 and 15, 8192 x 1024 11, 10 and 10; sixteen tokens by
+// 16384 x 4096 38, 44 and 42, by 8192 x 4096 34, 22 and 22.
+int few_waves(int64_t T, int64_t V, int64_t N)
+{
+    if (N < 512) return 1;
+    const int64_t groups = up(V, 16);
+    if (T > 8) return groups >= 1024 ? 1 : 4;
+    return N >= 4096 ? 16 : groups >= 2048 ? 1 : 4;
+}
+
+template <class T, int NT, int H, bool LDS, int KS>
+void few_launch(const FewLogits& f, bool odd, hipStream_t st)
 {
     const size_t lds = LDS ? (size_t)f.T * f.ldl : 0;
-    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true, LDS>), dim3(groups), dim3(256), lds, st, f);
-    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false, LDS>), dim3(groups), dim3(256), lds, st, f);
+    const dim3 grid((unsigned)up(f.V, KS > 1 ? 16 : 64)), wg(KS > 4 ? KS * 64 : 256);
+    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true, LDS, KS>), grid, wg, lds, st, f);
+    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false, LDS, KS>), grid, wg, lds, st, f);
+}
+
+template <class T, int KS>
+void few_tokens_launch(FewLogits f, bool odd, hipStream_t st)
+{
+    constexpr int H = KS > 1 ? 4 : 8;
+    f.ldl = (int)std::min<int64_t>(up(f.K, 32) * 64 + 16, 1 << 30);          // 16 more: rows in other banks
+    if (f.T <= 16 && (int64_t)f.T * f.ldl <= kStaged) few_launch<T, 1, H, true, KS>(f, odd, st);
+    else if (f.T > 16) few_launch<T, 2, 4, false, KS>(f, odd, st);
+    else few_launch<T, 1, H, false, KS>(f, odd, st);
 }
 
 template <class T>
-void few_tokens_launch(FewLogits f, bool odd, int groups, hipStream_t st)
+void few_logits(const FewLogits& f, bool odd, int waves, hipStream_t st)
 {
-    f.ldl = (int)std::min<int64_t>(up(f.K, 32) * 64 + 16, 1 << 30);          // 16 more: rows in other banks
-    if (f.T <= 16 && (int64_t)f.T * f.ldl <= kStaged) few_launch<T, 1, 16, true>(f, odd, groups, st);
-    else if (f.T > 16) few_launch<T, 2, 4, false>(f, odd, groups, st);
-    else few_launch<T, 1, 8, false>(f, odd, groups, st);
+    if (waves == 1) few_tokens_launch<T, 1>(f, odd, st);
+    else if (waves == 4) few_tokens_launch<T, 4>(f, odd, st);
+    else few_tokens_launch<T, 16>(f, odd, st);
 }
 
 template <class T>
@@ -891,15 +932,16 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     j.loss = a.loss; j.lse = a.lse;
     j.pitch = a.T;
     if (few(a)) {
-        j.parts = (int)up(a.V, 64);
+        const int waves = few_waves(a.T, a.V, a.N);
+        j.parts = (int)up(a.V, waves > 1 ? 16 : 64);
         float2* part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
         float* picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
         if (!run) return VQ_OK;
         const FewLogits f{static_cast<const char*>(a.W), static_cast<const char*>(a.X), a.ldw, a.ldx, a.N, (int)a.V, (int)a.T, 0,
                           a.labels, part, picked};
         const bool odd = odd_rows(a.W, a.ldw) || odd_rows(a.X, a.ldx);
-        if (a.dtype == VQ_BF16) few_tokens_launch<Bf16>(f, odd, j.parts, st);
-        else few_tokens_launch<F16>(f, odd, j.parts, st);
+        if (a.dtype == VQ_BF16) few_logits<Bf16>(f, odd, waves, st);
+        else few_logits<F16>(f, odd, waves, st);
         VQ_LAUNCHED("k_loss_few");
         j.part = part; j.picked = picked;
     } else {

@@ -55,7 +55,8 @@ def check(X, W, labels, dloss):
 @pytest.mark.parametrize("T,V,N", [
     (1, 1, 1), (1, 2, 8), (1, 1000, 64), (2, 63, 15), (3, 64, 136), (15, 65, 32), (16, 257, 513), (17, 255, 7), (31, 4001, 100),
     (32, 256, 256), (33, 256, 64), (33, 1, 3), (64, 129, 1), (100, 1000, 129), (128, 128, 128), (257, 513, 72), (300, 5003, 40),
-    (511, 300, 321), (200, 1088, 2994), (126, 500, 5001), (700, 257, 1500)])
+    (511, 300, 321), (200, 1088, 2994), (126, 500, 5001), (700, 257, 1500), (1, 100, 5000),
+    (5, 333, 4097), (8, 40, 4100), (16, 500, 2049), (30, 700, 1030), (7, 33000, 520)])
 def test_sizes(T, V, N, dtype):
     check(*inputs(T, V, N, dtype, T * 1000 + V))
 
