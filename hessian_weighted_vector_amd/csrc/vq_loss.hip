@@ -5,7 +5,7 @@
 //   dz[t, v] = dloss_t (exp(z[t, v] - lse_t) - [v = label_t]),  dX = dz W,  dW = dz^T X
 //
 //   k_loss_index    the tokens that are learnt, one behind the other, and their labels
-//   k_loss_gather   their rows of X, 16-byte aligned
+//   k_loss_gather   their rows of X, 16-byte aligned (k_loss_index_gather: both)
 //   k_loss_logits   the tiled product z; a wave's tile leaves of each token the largest
 //                   logit, the sum of exponentials below it, and the label's logit
 //   k_loss_few      the same for few tokens, the vocabulary read straight from memory
@@ -43,6 +43,7 @@ namespace vq {
 namespace {
 
 constexpr int64_t kMaxLossTokens = 1 << 20;
+constexpr int64_t kCountedTokens = 2048;        // up to which each token's workgroup counts its place
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kPieceBytes = 128 << 20;      // of dz, or of a packed piece of W
 
@@ -77,7 +78,7 @@ struct Index {
     const float* lse_in;
     float* g;                    // dloss and lse of each place
     float* lse_at;
-    float lift;                  // dz's power of two
+    float lift = 1.0f;           // dz's power of two
 };
 
 // One workgroup; a thread takes a run of consecutive tokens.
@@ -131,13 +132,11 @@ __global__ __launch_bounds__(1024) void k_loss_index(const Index a)
     }
 }
 
-// Row `place` of the learnt tokens' matrix; columns to its pitch are zeros.
-__global__ __launch_bounds__(256) void k_loss_gather(const Head* head, const int* __restrict__ order, const Pack m)
+// A row into the learnt tokens' matrix; columns to its pitch are zeros.
+__device__ __forceinline__ void gather_row(const Pack& m, int64_t from, int64_t to)
 {
-    const int q = blockIdx.x;
-    if (q >= head->count) return;
-    const uint16_t* row = m.s + (int64_t)order[q] * m.ld;
-    uint16_t* o = m.o + (int64_t)q * m.ldp;
+    const uint16_t* row = m.s + from * m.ld;
+    uint16_t* o = m.o + to * m.ldp;
     for (int c = threadIdx.x * 8; c < m.ldp; c += 256 * 8) {
         alignas(16) uint16_t v[8];
         if (c + 8 <= m.cols) {
@@ -155,6 +154,63 @@ __global__ __launch_bounds__(256) void k_loss_gather(const Head* head, const int
         }
         *reinterpret_cast<uint4*>(o + c) = *reinterpret_cast<const uint4*>(v);
     }
+}
+
+__global__ __launch_bounds__(256) void k_loss_gather(const Head* head, const int* __restrict__ order, const Pack m)
+{
+    const int q = blockIdx.x;
+    if (q < head->count) gather_row(m, order[q], q);
+}
+
+// Both at once for fewer tokens: a workgroup a token, which counts the learnt ones before it itself
+// (1260 tokens: a launch and about 4 us less; at 4096 the counting costs as much).
+__global__ __launch_bounds__(256) void k_loss_index_gather(const Index a, const Pack m)
+{
+    __shared__ int counts[4];
+    __shared__ float tops[4];
+    const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, last = (int)a.T - 1;
+    const int64_t l = a.labels[t];
+    const bool on = l != a.ignore;
+    if (!on && threadIdx.x == 0) {
+        if (a.place) a.place[t] = -1;
+        if (a.loss) a.loss[t] = a.lse[t] = 0.0f;
+    }
+    if (!on && t != last) return;                             // the last token's workgroup knows them all
+    int n = 0;
+    float top = 0.0f;
+    const int end = a.g ? (int)a.T : t;                       // the largest |dloss| is that of all
+    for (int i = threadIdx.x; i < end; i += 256) {
+        const bool learnt = a.labels[i] != a.ignore;
+        n += learnt && i < t;
+        if (a.g && learnt) top = fmaxf(top, fabsf(a.dloss[i]));
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        n += __shfl_xor(n, o);
+        top = fmaxf(top, __shfl_xor(top, o));
+    }
+    if (lane == 0) {
+        counts[wave] = n;
+        tops[wave] = top;
+    }
+    __syncthreads();
+    const int at = counts[0] + counts[1] + counts[2] + counts[3];
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    if (!(top > 0.0f && top < INFINITY)) top = 1.0f;
+    if (threadIdx.x == 0) {
+        if (t == last) *a.head = Head{at + on, top / a.lift};
+        if (on) {
+            const bool known = l >= 0 && l < a.V;
+            if (a.place) a.place[t] = at;
+            a.order[at] = t;
+            a.label[at] = known ? (int)l : -1;
+            if (a.g) {
+                a.g[at] = known ? a.dloss[t] / top * a.lift : NAN;
+                a.lse_at[at] = a.lse_in[t];
+            }
+        }
+    }
+    if (on) gather_row(m, t, at);
 }
 
 // The tiled product of a piece of W (rows v0 .. of the vocabulary) and the learnt tokens.
@@ -843,9 +899,14 @@ struct Tokens {
         ix.labels = a.labels;
         ix.T = a.T; ix.V = a.V; ix.ignore = a.ignore;
         ix.head = head; ix.order = order; ix.label = label;
+        const Pack p{static_cast<const uint16_t*>(a.X), x, a.T, a.ldx, ldx, (int)a.N, odd_rows(a.X, a.ldx)};
+        if (a.T <= kCountedTokens) {
+            hipLaunchKernelGGL(k_loss_index_gather, dim3((unsigned)a.T), dim3(256), 0, st, ix, p);
+            VQ_LAUNCHED("k_loss_index_gather");
+            return VQ_OK;
+        }
         hipLaunchKernelGGL(k_loss_index, dim3(1), dim3(1024), 0, st, ix);
         VQ_LAUNCHED("k_loss_index");
-        const Pack p{static_cast<const uint16_t*>(a.X), x, a.T, a.ldx, ldx, (int)a.N, odd_rows(a.X, a.ldx)};
         hipLaunchKernelGGL(k_loss_gather, dim3((unsigned)a.T), dim3(256), 0, st, head, order, p);
         VQ_LAUNCHED("k_loss_gather");
         return VQ_OK;
