@@ -33,6 +33,12 @@
 // rounding would otherwise be the same in every label's term, and the gradients' own (1 / 6927
 // in bf16: all of them off by 0.0021).  In fp16 dz is also multiplied by 2^13, so that
 // probabilities down to 2^-27 keep the type's full precision.
+//
+// What bounds it: power, as the dense products.  4096 tokens of 4096 by 131072 words, bf16, 3.06
+// to 3.16 ms (1.39 to 1.44 PFLOP/s, matrix cores busy 0.78); the gradient of 2048 learnt tokens of
+// 2048, eight pieces of 124 us for dz (busy 0.60: the exponentials and stores of a tile are not
+// hidden) and 223 us for dX and dW (1.23 PFLOP/s).  One token by 32768 x 4096 50 us, bound by W's
+// bytes.
 #include "vq_few.h"
 #include "vq_tile.h"
 

@@ -571,7 +571,7 @@ vq_status vq_quantize_rows(int64_t rows, int64_t cols, int dtype, const void* X,
  * in elements, any alignment of elements), labels int64 [T], loss and lse float32
  * [T].  A token whose label is ignore_index takes no part: its loss and lse are 0,
  * and nothing that its row of X holds reaches a result.  Any other label outside
- * [0, V) makes its token's loss NaN.  Sums are float32; the results are bitwise
+ * [0, V) makes its token's loss NaN.  (VQ_CHECK=1 counts the values of ignored rows too.)  Sums are float32; the results are bitwise
  * reproducible for fixed arguments.  0 <= T <= 2^20, 1 <= V, N <= 2^20; T = 0 is a no-op.
  * Outputs may not overlap inputs or each other.  A reduction (mean over the
  * learnt tokens, weights) is the caller's, as is dloss below.  Workspaces as in the dense
