@@ -380,7 +380,7 @@ __device__ __forceinline__ f32x4 joined_sums(const float* sums, int splits, int6
     return z;
 }
 
-// A workgroup a token.
+// A workgroup a token, of as many threads as its words keep busy.
 struct RowLoss {
     const float* sums;
     int splits, pitch, V;
@@ -392,14 +392,14 @@ struct RowLoss {
     float* lse;
 };
 
-__global__ __launch_bounds__(256) void k_loss_rows(const RowLoss a)
+__global__ __launch_bounds__(1024) void k_loss_rows(const RowLoss a)
 {
-    __shared__ float2 sh[4];
+    __shared__ float2 sh[16];
     const int q = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (q >= a.head->count) return;
     const int64_t row = (int64_t)q * a.pitch;
     float m = -INFINITY, s = 0.0f;
-    for (int p = threadIdx.x * 4; p < a.V; p += 1024) {
+    for (int p = threadIdx.x * 4; p < a.V; p += (int)blockDim.x * 4) {
         const f32x4 z = joined_sums(a.sums, a.splits, a.plane, row + p);
         float top = z[0], sum = 0.0f;
 #pragma unroll
@@ -416,8 +416,7 @@ __global__ __launch_bounds__(256) void k_loss_rows(const RowLoss a)
     if (threadIdx.x != 0) return;
     m = sh[0].x;
     s = sh[0].y;
-#pragma unroll
-    for (int k = 1; k < 4; ++k) join(m, s, sh[k].x, sh[k].y);
+    for (int k = 1; k < (int)blockDim.x >> 6; ++k) join(m, s, sh[k].x, sh[k].y);
     const int want = a.label[q];
     const float lse = m + logf(s);
     float loss = NAN;
@@ -451,9 +450,10 @@ __global__ __launch_bounds__(256) void k_loss_dz(const Logits a, int64_t places)
     store8<T>(a.dz, a.ldz, q, p, (int)a.ldz, v);
 }
 
-// Few tokens, as they come: KS waves take 16 rows of W together, blocks of 32 H columns in
-// turn; a workgroup takes 64 rows where a wave takes 16 whole.  Where X fits (LDS), it is staged
-// there: its reads do not queue with those of W.
+// Few tokens, as they come: KS waves take 16 RG rows of W together, blocks of 32 H columns in
+// turn; a workgroup takes 64 rows where a wave takes 16 whole.  More than 16 tokens share their
+// rows of X among RG groups of rows, which would read it RG times otherwise.  Where X fits (LDS),
+// it is staged there: its reads do not queue with those of W.
 struct FewLogits {
     const char* W;
     const char* X;
@@ -467,7 +467,7 @@ struct FewLogits {
 
 constexpr int kStaged = 40 << 10;            // bytes of X in LDS: three workgroups a CU
 
-template <class T, int NT, int H, bool ODD, bool LDS, int KS>
+template <class T, int NT, int H, bool ODD, bool LDS, int KS, int RG>
 __global__ __launch_bounds__(KS > 4 ? KS * 64 : 256) void k_loss_few(const FewLogits a)
 {
     typedef typename T::E E;
@@ -476,12 +476,16 @@ __global__ __launch_bounds__(KS > 4 ? KS * 64 : 256) void k_loss_few(const FewLo
     extern __shared__ __align__(16) char staged[];               // [T][ldl], zeros past K
     constexpr int kGroups = KS > 1 ? 1 : 4, kThreads = KS > 4 ? KS * 64 : 256;
     __shared__ float2 sh[kGroups][NT * 16];
-    __shared__ f32x4 red[KS > 1 ? KS - 1 : 1][NT][KS > 1 ? 64 : 1];
+    __shared__ f32x4 red[KS > 1 ? KS - 1 : 1][RG][NT][KS > 1 ? 64 : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, ks = wave % KS;
-    const int m0 = blockIdx.x * 16 * kGroups + wave / KS * 16;
-    const int64_t row = m0 + r < a.V ? m0 + r : a.V - 1;         // rows and tokens past the last repeat it
-    const E* const w = reinterpret_cast<const E*>(a.W) + row * a.ldw;
+    const int m0 = (blockIdx.x * kGroups + wave / KS) * 16 * RG;
+    const E* w[RG];
+#pragma unroll
+    for (int i = 0; i < RG; ++i) {
+        const int64_t row = m0 + i * 16 + r < a.V ? m0 + i * 16 + r : a.V - 1;         // rows and tokens past the last repeat it
+        w[i] = reinterpret_cast<const E*>(a.W) + row * a.ldw;
+    }
     const E* x[NT];
     const char* xl[NT];
 #pragma unroll
@@ -490,23 +494,32 @@ __global__ __launch_bounds__(KS > 4 ? KS * 64 : 256) void k_loss_few(const FewLo
         x[n] = reinterpret_cast<const E*>(a.X) + t * a.ldx;
         xl[n] = staged + t * a.ldl + g * 16;
     }
-    f32x4 acc[NT];
+    f32x4 acc[RG][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < RG; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int nfull = (int)(a.K / B);
-    Ahead<T, ODD> wv[H], xv[LDS ? 1 : NT][LDS ? 1 : H];
+    Ahead<T, ODD> wv[RG][H], xv[LDS ? 1 : NT][LDS ? 1 : H];
     const auto load = [&](int kb, int j) {
         const int64_t c = (int64_t)kb * B + j * 32 + g * 8;
         if (!LDS)
 #pragma unroll
             for (int n = 0; n < NT; ++n) xv[n][j].load(x[n], c);
-        wv[j].load(w, c);
+#pragma unroll
+        for (int i = 0; i < RG; ++i) wv[i][j].load(w[i], c);
     };
     const auto multiply = [&](int kb, int j) {
+        V8 wf[RG];
+#pragma unroll
+        for (int i = 0; i < RG; ++i) wf[i] = wv[i][j].get(w[i]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (LDS) acc[n] = T::mfma(wv[j].get(w), *reinterpret_cast<const V8*>(xl[n] + ((int64_t)kb * B + j * 32) * 2), acc[n]);
-            else acc[n] = T::mfma(wv[j].get(w), xv[n][j].get(x[n]), acc[n]);
+            V8 xf;
+            if (LDS) xf = *reinterpret_cast<const V8*>(xl[n] + ((int64_t)kb * B + j * 32) * 2);
+            else xf = xv[LDS ? 0 : n][LDS ? 0 : j].get(x[n]);
+#pragma unroll
+            for (int i = 0; i < RG; ++i) acc[i][n] = T::mfma(wf[i], xf, acc[i][n]);
         }
     };
     if (ks < nfull) {
@@ -540,35 +553,48 @@ __global__ __launch_bounds__(KS > 4 ? KS * 64 : 256) void k_loss_few(const FewLo
     }
     for (int64_t c0 = (int64_t)nfull * B + ks * 32; c0 < a.K; c0 += KS * 32) {
         const int64_t c = c0 + g * 8;
-        const V8 v = chunk_tail<T>(w, c, a.K);
+        V8 wf[RG];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            acc[n] = T::mfma(v, LDS ? *reinterpret_cast<const V8*>(xl[n] + c0 * 2) : chunk_tail<T>(x[n], c, a.K), acc[n]);
+        for (int i = 0; i < RG; ++i) wf[i] = chunk_tail<T>(w[i], c, a.K);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const V8 xf = LDS ? *reinterpret_cast<const V8*>(xl[n] + c0 * 2) : chunk_tail<T>(x[n], c, a.K);
+#pragma unroll
+            for (int i = 0; i < RG; ++i) acc[i][n] = T::mfma(wf[i], xf, acc[i][n]);
+        }
     }
     if (KS > 1) {                                                // the first wave adds the others' sums in order
         if (ks > 0)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) red[ks > 0 ? ks - 1 : 0][n][lane] = acc[n];
+            for (int i = 0; i < RG; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) red[ks > 0 ? ks - 1 : 0][i][n][lane] = acc[i][n];
         __syncthreads();
         if (ks > 0) return;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < RG; ++i)
 #pragma unroll
-            for (int k = 0; k < KS - 1; ++k) acc[n] += red[k][n][lane];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k = 0; k < KS - 1; ++k) acc[i][n] += red[k][i][n][lane];
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int t = n * 16 + r;
         float m = -INFINITY, s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (m0 + g * 4 + i < a.V) m = fmaxf(m, acc[n][i]);
+        for (int j = 0; j < RG; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (m0 + j * 16 + g * 4 + i < a.V) m = fmaxf(m, acc[j][n][i]);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (m0 + g * 4 + i < a.V) s += exp_of(acc[n][i] - base);
+        for (int j = 0; j < RG; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (m0 + j * 16 + g * 4 + i < a.V) s += exp_of(acc[j][n][i] - base);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (KS > 1) {
@@ -579,8 +605,10 @@ __global__ __launch_bounds__(KS > 4 ? KS * 64 : 256) void k_loss_few(const FewLo
         if (t < a.T) {
             const int64_t want = a.labels[t] - m0 - g * 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (want == i && m0 + g * 4 + i < a.V) a.picked[t] = acc[n][i];
+            for (int j = 0; j < RG; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (want == j * 16 + i && m0 + j * 16 + g * 4 + i < a.V) a.picked[t] = acc[j][n][i];
         }
     }
     if (KS > 1) return;
@@ -790,7 +818,7 @@ struct LogitsPlan {
     Shape s;
     int splits;
 };
-LogitsPlan logits_plan(int64_t V, int64_t T, int64_t N, bool backward, bool may_split)
+LogitsPlan logits_plan(int64_t V, int64_t T, int64_t N, bool backward)
 {
     LogitsPlan best{};
     double least = 1e300;
@@ -798,7 +826,7 @@ LogitsPlan logits_plan(int64_t V, int64_t T, int64_t N, bool backward, bool may_
     for (int small = 0; small < 2; ++small) {
         const Shape s = shape(small);
         const int64_t tiles = up(V, s.bp) * up(T, s.bq);
-        for (int sp = 1; sp <= 16 && sp <= pairs && (sp == 1 || may_split); ++sp) {
+        for (int sp = 1; sp <= 16 && sp <= pairs; ++sp) {
             double t = tiles_cost(small, tiles * sp, 2.0 * up(pairs, sp));
             if (sp > 1) t += (backward ? 6.0 : 2.0) + 0.9e-6 * (double)T * V * (sp + 1);
             if (t < least) {
@@ -937,45 +965,60 @@ vq_status words(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, Mat& out, 
 }
 
 // Whether the vocabulary is read for few tokens straight from memory.  One token by 131072 x 4096
-// 198 us here and 210 in tiles, sixteen 250 and 199; sixteen by 32768 x 4096 69 and 101.
-bool few(const Loss& a) { return a.T <= 8 || (a.T <= 32 && a.V * a.N < (int64_t)1 << 28); }
-
-// Waves that share 16 rows of W.  One token, by one, four and sixteen: 32768 x 4096 64, 58 and 57 us,
-// 32768 x 2048 32, 35 and 34, 2048 x 8192 35, 16 and 15, 8192 x 1024 11, 10 and 10; sixteen tokens by
-// 16384 x 4096 38, 44 and 42, by 8192 x 4096 34, 22 and 22.
-int few_waves(int64_t T, int64_t V, int64_t N)
+// 198 us here and 210 in tiles, sixteen 250 and 199; sixteen by 32768 x 4096 69 and 101, 32 74 and 83;
+// 32 by 17513 x 4570 87 and 106 (tiles need a copy of its rows), by 6400 x 7616 44 and 36.
+bool few(const Loss& a)
 {
-    if (N < 512) return 1;
-    const int64_t groups = up(V, 16);
-    if (T > 8) return groups >= 1024 ? 1 : 4;
-    return N >= 4096 ? 16 : groups >= 2048 ? 1 : 4;
+    return a.T <= 8 || (a.V * a.N < (int64_t)1 << 28 && (a.T <= 16 || (a.T <= 32 && a.N <= a.V)));
 }
 
-template <class T, int NT, int H, bool LDS, int KS>
-void few_launch(const FewLogits& f, bool odd, hipStream_t st)
+// Waves that share the rows of W.  One token, by one, four and sixteen: 32768 x 4096 64, 58 and 57 us,
+// 32768 x 2048 32, 35 and 34, 2048 x 8192 35, 16 and 15, 8192 x 1024 11, 10 and 10; sixteen tokens by
+// 16384 x 4096 38, 44 and 42, by 8192 x 4096 34, 22 and 22.  32 tokens by four waves, with one, two and
+// four groups of rows: 4096 x 4096 19, 22 and 30, 8192 x 1024 13, 12 and 14, 32768 x 4096 113, 84 and 74.
+struct FewPlan {
+    int waves, rows;             // groups of 16 rows a wave; a workgroup takes four where its waves share none
+    int parts(int64_t V) const { return (int)up(V, waves > 1 ? 16 * rows : 64 * rows); }
+};
+FewPlan few_plan(int64_t T, int64_t V, int64_t N)
+{
+    const int64_t groups = up(V, 16);
+    if (T > 16) return {4, groups < 512 ? 1 : groups < 2048 ? 2 : 4};
+    if (N < 512) return {1, 1};
+    if (T > 8) return {groups >= 1024 ? 1 : 4, 1};
+    return {N >= 4096 ? 16 : groups >= 2048 ? 1 : 4, 1};
+}
+
+template <class T, int NT, int H, bool LDS, int KS, int RG>
+void few_launch(const FewLogits& f, bool odd, const FewPlan& p, hipStream_t st)
 {
     const size_t lds = LDS ? (size_t)f.T * f.ldl : 0;
-    const dim3 grid((unsigned)up(f.V, KS > 1 ? 16 : 64)), wg(KS > 4 ? KS * 64 : 256);
-    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true, LDS, KS>), grid, wg, lds, st, f);
-    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false, LDS, KS>), grid, wg, lds, st, f);
+    const dim3 grid((unsigned)p.parts(f.V)), wg(KS > 4 ? KS * 64 : 256);
+    if (odd) hipLaunchKernelGGL((k_loss_few<T, NT, H, true, LDS, KS, RG>), grid, wg, lds, st, f);
+    else hipLaunchKernelGGL((k_loss_few<T, NT, H, false, LDS, KS, RG>), grid, wg, lds, st, f);
 }
 
 template <class T, int KS>
-void few_tokens_launch(FewLogits f, bool odd, hipStream_t st)
+void few_tokens_launch(FewLogits f, bool odd, const FewPlan& p, hipStream_t st)
 {
     constexpr int H = KS > 1 ? 4 : 8;
     f.ldl = (int)std::min<int64_t>(up(f.K, 32) * 64 + 16, 1 << 30);          // 16 more: rows in other banks
-    if (f.T <= 16 && (int64_t)f.T * f.ldl <= kStaged) few_launch<T, 1, H, true, KS>(f, odd, st);
-    else if (f.T > 16) few_launch<T, 2, 4, false, KS>(f, odd, st);
-    else few_launch<T, 1, H, false, KS>(f, odd, st);
+    if ((int64_t)f.T * f.ldl <= kStaged) few_launch<T, 1, H, true, KS, 1>(f, odd, p, st);
+    else few_launch<T, 1, H, false, KS, 1>(f, odd, p, st);
 }
 
 template <class T>
-void few_logits(const FewLogits& f, bool odd, int waves, hipStream_t st)
+void few_logits(const FewLogits& f, bool odd, const FewPlan& p, hipStream_t st)
 {
-    if (waves == 1) few_tokens_launch<T, 1>(f, odd, st);
-    else if (waves == 4) few_tokens_launch<T, 4>(f, odd, st);
-    else few_tokens_launch<T, 16>(f, odd, st);
+    if (f.T > 16) {
+        if (p.rows == 1) few_launch<T, 2, 4, false, 4, 1>(f, odd, p, st);
+        else if (p.rows == 2) few_launch<T, 2, 4, false, 4, 2>(f, odd, p, st);
+        else few_launch<T, 2, 2, false, 4, 4>(f, odd, p, st);
+        return;
+    }
+    if (p.waves == 1) few_tokens_launch<T, 1>(f, odd, p, st);
+    else if (p.waves == 4) few_tokens_launch<T, 4>(f, odd, p, st);
+    else few_tokens_launch<T, 16>(f, odd, p, st);
 }
 
 template <class T>
@@ -1001,16 +1044,16 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     j.loss = a.loss; j.lse = a.lse;
     j.pitch = a.T;
     if (few(a)) {
-        const int waves = few_waves(a.T, a.V, a.N);
-        j.parts = (int)up(a.V, waves > 1 ? 16 : 64);
+        const FewPlan plan = few_plan(a.T, a.V, a.N);
+        j.parts = plan.parts(a.V);
         float2* part = static_cast<float2*>(ws.take(j.parts * a.T * sizeof(float2)));
         float* picked = static_cast<float*>(ws.take(a.T * sizeof(float)));
         if (!run) return VQ_OK;
         const FewLogits f{static_cast<const char*>(a.W), static_cast<const char*>(a.X), a.ldw, a.ldx, a.N, (int)a.V, (int)a.T, 0,
                           a.labels, part, picked};
         const bool odd = odd_rows(a.W, a.ldw) || odd_rows(a.X, a.ldx);
-        if (a.dtype == VQ_BF16) few_logits<Bf16>(f, odd, waves, st);
-        else few_logits<F16>(f, odd, waves, st);
+        if (a.dtype == VQ_BF16) few_logits<Bf16>(f, odd, plan, st);
+        else few_logits<F16>(f, odd, plan, st);
         VQ_LAUNCHED("k_loss_few");
         j.part = part; j.picked = picked;
     } else {
@@ -1019,7 +1062,7 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         const bool copied = !loads_ok({a.W, a.V, a.N, a.ldw});
         const int64_t Vp = copied ? piece(a.V, 2 * round8(a.N)) : a.V;
         uint16_t* copy = copied ? static_cast<uint16_t*>(ws.take(Vp * round8(a.N) * 2)) : nullptr;
-        const LogitsPlan plan = logits_plan(Vp, a.T, a.N, false, Vp >= a.V);
+        const LogitsPlan plan = logits_plan(Vp, a.T, a.N, false);
         const Shape s = plan.s;
         const int per = kWP * (int)up(Vp, s.bp);              // parts of a piece
         const int64_t pitch = round8(a.V);
@@ -1048,7 +1091,7 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
             if (sums) {
                 g.t.splits = plan.splits;
                 g.t.pitch = (int)pitch;
-                g.sums = sums;
+                g.sums = sums + v0;
                 g.plane = a.T * pitch;
             } else {
                 g.part = part + k * per * a.T; g.pitch = a.T; g.picked = picked;
@@ -1059,7 +1102,7 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         }
         if (sums) {
             const RowLoss r{sums, plan.splits, (int)pitch, (int)a.V, a.T * pitch, tk.head, tk.order, tk.label, a.loss, a.lse};
-            hipLaunchKernelGGL(k_loss_rows, dim3((unsigned)a.T), dim3(256), 0, st, r);
+            hipLaunchKernelGGL(k_loss_rows, dim3((unsigned)a.T), dim3(a.V > 4096 ? 1024 : 256), 0, st, r);
             VQ_LAUNCHED("k_loss_rows");
             return VQ_OK;
         }
@@ -1124,7 +1167,7 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     void* dz = ws.take(a.T * Vp * 2);
     const GradPlan plan = grad_plan(std::min(Vp, a.V), a.T, a.N, a.dX, a.dW);
     float* sums = a.dX ? static_cast<float*>(ws.take(plan.splits * a.T * N8 * sizeof(float))) : nullptr;
-    const LogitsPlan zplan = logits_plan(std::min(Vp, a.V), a.T, a.N, true, true);
+    const LogitsPlan zplan = logits_plan(std::min(Vp, a.V), a.T, a.N, true);
     const int64_t zpitch = round8(std::min(Vp, a.V));
     float* zsums = zplan.splits > 1 ? static_cast<float*>(ws.take(zplan.splits * a.T * zpitch * sizeof(float))) : nullptr;
     if (!run) return VQ_OK;

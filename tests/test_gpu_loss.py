@@ -56,7 +56,8 @@ def check(X, W, labels, dloss):
     (1, 1, 1), (1, 2, 8), (1, 1000, 64), (2, 63, 15), (3, 64, 136), (15, 65, 32), (16, 257, 513), (17, 255, 7), (31, 4001, 100),
     (32, 256, 256), (33, 256, 64), (33, 1, 3), (64, 129, 1), (100, 1000, 129), (128, 128, 128), (257, 513, 72), (300, 5003, 40),
     (511, 300, 321), (200, 1088, 2994), (126, 500, 5001), (700, 257, 1500), (1, 100, 5000),
-    (5, 333, 4097), (8, 40, 4100), (16, 500, 2049), (30, 700, 1030), (7, 33000, 520)])
+    (5, 333, 4097), (8, 40, 4100), (16, 500, 2049), (30, 700, 1030), (7, 33000, 520),
+    (25, 9001, 131), (32, 33001, 72), (18, 100, 64)])
 def test_sizes(T, V, N, dtype):
     check(*inputs(T, V, N, dtype, T * 1000 + V))
 
@@ -234,6 +235,21 @@ def test_pieces_of_the_vocabulary(dtype, V, ldw):
     for got, ref64 in ((dX[on], wx[on]), (dW, ww)):
         rel = (got.double() - ref64).norm(dim=1) / ref64.norm(dim=1).clamp(min=1e-9)
         assert float(rel.max()) <= 0.05
+
+
+def test_pieces_of_copied_rows_with_split_sums():
+    """Few tokens over a vocabulary whose rows are copied in two pieces, N over several workgroups."""
+    T, V, N = 40, 17513, 4570
+    X, W, labels, _ = inputs(T, V, N, torch.bfloat16, 24, masked=0.2)
+    labels[:4] = torch.tensor([0, V - 1, 8959, 8960], device="cuda")     # first, last, and where the pieces meet
+    loss, lse = vq.cross_entropy(X, W, labels)
+    z = X.double() @ W.double().T
+    on = labels != IGN
+    want = torch.logsumexp(z, 1)
+    tol = ref.sum_error(N) * float((X.double().abs() @ W.double().abs().T).max()) + 64 * 2.0 ** -22
+    picked = z.gather(1, labels.clamp(min=0)[:, None])[:, 0]
+    assert float(((lse.double() - want).abs() * on).max()) <= tol
+    assert float(((loss.double() - (want - picked)).abs() * on).max()) <= 2 * tol
 
 
 def test_same_bits_every_time_and_on_another_stream():
