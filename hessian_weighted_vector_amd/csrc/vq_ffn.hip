@@ -26,33 +26,6 @@ namespace {
 
 constexpr int64_t kMaxTokens = 1 << 28;
 
-// Block `block` of `blocks` of the copy of m.
-__device__ __forceinline__ void pack_rows(const Pack& m, int block, int blocks)
-{
-    const int64_t per = m.ldp / 8;
-    const int64_t n = m.rows * per;
-    for (int64_t e = (int64_t)block * 256 + threadIdx.x; e < n; e += (int64_t)blocks * 256) {
-        const int64_t r = e / per;
-        const int c = (int)(e - r * per) * 8;
-        const uint16_t* p = m.s + r * m.ld + c;
-        alignas(16) uint16_t v[8];
-        if (c + 8 <= m.cols) {
-            if (m.odd) {
-                Words w;
-                w.load(p);
-                const uint4 u = w.get(p);
-                __builtin_memcpy(v, &u, 16);
-            } else {
-                __builtin_memcpy(v, p, 16);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = c + i < m.cols ? p[i] : (uint16_t)0;
-        }
-        *reinterpret_cast<uint4*>(m.o + r * m.ldp + c) = *reinterpret_cast<const uint4*>(v);
-    }
-}
-
 // blockIdx.y: the matrix.
 __global__ __launch_bounds__(256) void k_pack(const Packs a) { pack_rows(a.m[blockIdx.y], blockIdx.x, gridDim.x); }
 

@@ -169,9 +169,14 @@ __global__ __launch_bounds__(256) void k_loss_gather(const Head* head, const int
 }
 
 // Both at once for fewer tokens: a workgroup a token, which counts the learnt ones before it itself
-// (1260 tokens: a launch and about 4 us less; at 4096 the counting costs as much).
-__global__ __launch_bounds__(256) void k_loss_index_gather(const Index a, const Pack m)
+// (1260 tokens: a launch and about 4 us less; at 4096 the counting costs as much).  Workgroups past
+// the tokens copy the first piece of W, where its rows are copied.
+__global__ __launch_bounds__(256) void k_loss_index_gather(const Index a, const Pack m, const Pack w, int wblocks)
 {
+    if ((int)blockIdx.x >= a.T) {
+        pack_rows(w, (int)(blockIdx.x - a.T), wblocks);
+        return;
+    }
     __shared__ int counts[4];
     __shared__ float tops[4];
     const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, last = (int)a.T - 1;
@@ -930,14 +935,23 @@ struct Tokens {
         label = static_cast<int*>(ws.take(a.T * sizeof(int)));
         x = static_cast<uint16_t*>(ws.take(a.T * ldx * 2));
     }
-    vq_status launch(const Loss& a, Index ix, hipStream_t st) const
+    // Rows v0 .. v0 + n of W into `copy`.
+    static Pack piece(const Loss& a, int64_t v0, int64_t n, uint16_t* copy)
+    {
+        const uint16_t* p = static_cast<const uint16_t*>(a.W) + v0 * a.ldw;
+        return {p, copy, n, a.ldw, round8(a.N), (int)a.N, odd_rows(p, a.ldw)};
+    }
+    // Also the first n rows of W into `copy` (where there is one).
+    vq_status launch(const Loss& a, Index ix, int64_t n, uint16_t* copy, hipStream_t st) const
     {
         ix.labels = a.labels;
         ix.T = a.T; ix.V = a.V; ix.ignore = a.ignore;
         ix.head = head; ix.order = order; ix.label = label;
         const Pack p{static_cast<const uint16_t*>(a.X), x, a.T, a.ldx, ldx, (int)a.N, odd_rows(a.X, a.ldx)};
         if (a.T <= kCountedTokens) {
-            hipLaunchKernelGGL(k_loss_index_gather, dim3((unsigned)a.T), dim3(256), 0, st, ix, p);
+            const int blocks = copy ? pack_blocks(n * (round8(a.N) / 8)) : 0;
+            hipLaunchKernelGGL(k_loss_index_gather, dim3((unsigned)(a.T + blocks)), dim3(256), 0, st, ix, p,
+                               copy ? piece(a, 0, n, copy) : Pack{}, blocks);
             VQ_LAUNCHED("k_loss_index_gather");
             return VQ_OK;
         }
@@ -945,23 +959,26 @@ struct Tokens {
         VQ_LAUNCHED("k_loss_index");
         hipLaunchKernelGGL(k_loss_gather, dim3((unsigned)a.T), dim3(256), 0, st, head, order, p);
         VQ_LAUNCHED("k_loss_gather");
-        return VQ_OK;
+        return copy ? copy_piece(a, 0, n, copy, st) : VQ_OK;
+    }
+    static vq_status copy_piece(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, hipStream_t st)
+    {
+        Packs k{};
+        k.m[0] = piece(a, v0, n, copy);
+        k.count = 1;
+        k.blocks = pack_blocks(n * (round8(a.N) / 8));
+        return pack_launch(k, st);
     }
 };
 
-// Rows v0 .. v0 + n of W as the tiles read them: in place, or copied to `copy`.
+// Rows v0 .. v0 + n of W as the tiles read them: in place, or copied to `copy` (the first piece
+// has been).
 vq_status words(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, Mat& out, hipStream_t st)
 {
-    const uint16_t* p = static_cast<const uint16_t*>(a.W) + v0 * a.ldw;
-    out = {p, n, a.N, a.ldw};
+    out = {static_cast<const uint16_t*>(a.W) + v0 * a.ldw, n, a.N, a.ldw};
     if (!copy) return VQ_OK;
-    const int64_t ldp = round8(a.N);
-    Packs k{};
-    k.m[0] = {p, copy, n, a.ldw, ldp, (int)a.N, odd_rows(p, a.ldw)};
-    k.count = 1;
-    k.blocks = pack_blocks(n * (ldp / 8));
-    out = {copy, n, ldp, ldp};
-    return pack_launch(k, st);
+    out = {copy, n, round8(a.N), round8(a.N)};
+    return v0 > 0 ? Tokens::copy_piece(a, v0, n, copy, st) : VQ_OK;
 }
 
 // Whether the vocabulary is read for few tokens straight from memory.  One token by 131072 x 4096
@@ -1079,7 +1096,7 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         if (!run) return VQ_OK;
         Index ix{};
         ix.loss = a.loss; ix.lse = a.lse;
-        VQ_TRY(tk.launch(a, ix, st));
+        VQ_TRY(tk.launch(a, ix, std::min(Vp, a.V), copy, st));
         for (int64_t v0 = 0, k = 0; v0 < a.V; v0 += Vp, ++k) {
             const int64_t n = std::min(Vp, a.V - v0);
             Mat w;
@@ -1176,7 +1193,7 @@ vq_status backward(const Loss& a, Arena& ws, bool run, hipStream_t st)
     ix.dloss = a.dloss; ix.lse_in = a.lse_in;
     ix.g = g; ix.lse_at = lse;
     ix.lift = a.dtype == VQ_F16 ? 0x1p13f : 1.0f;
-    VQ_TRY(tk.launch(a, ix, st));
+    VQ_TRY(tk.launch(a, ix, std::min(Vp, a.V), copy, st));
     for (int64_t v0 = 0; v0 < a.V; v0 += Vp) {
         const int64_t n = std::min(Vp, a.V - v0), n8 = round8(n);
         Mat w;
