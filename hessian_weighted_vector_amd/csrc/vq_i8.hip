@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(con
     typedef Main<I8, false, false, FP, FQ, PAIR> L;
     constexpr int kP = PAIR ? L::BP / 2 : L::BP;              // features of the tile
     VQ_TILE_BUFFERS(L);
-    // the tile's scales, read while the product runs: in the epilogue a row's would be waited for each time
+    // the tile's scales, read in front of the product and kept: in the epilogue a row's would be waited for each time
     __shared__ __align__(16) float scale_q[L::BQ], scale_p[PAIR ? 2 : 1][kP];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -282,12 +282,10 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(con
     int tp, tq;
     pick_tile(blockIdx.x, a.t.ntp * a.t.ntq, a.t.ntp, a.t.ntq, tp, tq);
     const int p0 = tp * kP, q0 = tq * L::BQ;
-    if (!a.t.part) {
-        for (int i = threadIdx.x; i < L::BQ; i += kThreads) scale_q[i] = a.s.x[q0 + i < a.t.nq ? q0 + i : a.t.nq - 1];
-#pragma unroll
-        for (int k = 0; k < (PAIR ? 2 : 1); ++k)
-            for (int i = threadIdx.x; i < kP; i += kThreads) scale_p[k][i] = a.s.w[k][p0 + i < a.t.np ? p0 + i : a.t.np - 1];
-    }
+    static_assert(L::BQ <= kThreads && kP <= kThreads, "a scale a thread");
+    const int i_q = q0 + (int)threadIdx.x < a.t.nq ? q0 + (int)threadIdx.x : a.t.nq - 1;
+    const int i_p = p0 + (int)threadIdx.x < a.t.np ? p0 + (int)threadIdx.x : a.t.np - 1;
+    const float my_q = a.s.x[i_q], my_p = a.s.w[0][i_p], my_p2 = PAIR ? a.s.w[1][i_p] : 0.0f;
     const int pairs = (a.t.steps + 1) / 2;
     const int s0 = 2 * (int)((int64_t)pairs * split / a.t.splits), s1 = 2 * (int)((int64_t)pairs * (split + 1) / a.t.splits);
     i32x4 acc[FP][FQ];
@@ -314,6 +312,12 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_i8_gemm(con
         __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));           // no load into LDS outlives the workgroup
         return;
     }
+    if (threadIdx.x < L::BQ) scale_q[threadIdx.x] = my_q;
+    if (threadIdx.x < kP) {
+        scale_p[0][threadIdx.x] = my_p;
+        if (PAIR) scale_p[PAIR ? 1 : 0][threadIdx.x] = my_p2;
+    }
+    // behind each_row's barrier every scale is there
     each_row<L>(acc, p0, q0, a.t.np, a.t.nq, wave, lane, pb0, pb1, qb0, qb1, [&](int q, int p, int (&v)[8], int (&u)[8]) {
         float w0[8], w1[8];
         __builtin_memcpy(w0, __builtin_assume_aligned(scale_p[0] + (p - p0), 16), 32);
