@@ -212,12 +212,21 @@ __global__ __launch_bounds__(256) void k_i8_rows(const Rows a)
     if (first == 0) a.scale[r] = Coder<E>::scale(top);
 }
 
+// A launch takes fewer than 2^32 threads.
 template <class E>
-void rows_launch(const Rows& a, hipStream_t st)
+void rows_launch(const Rows& all, hipStream_t st)
 {
-    // a wave a row up to 4096 columns (eight chunks of 64 lanes)
-    if (a.cols <= 4096) hipLaunchKernelGGL((k_i8_rows<E, 1, 8>), dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((k_i8_rows<E, 4, 8>), dim3((unsigned)a.rows), dim3(256), 0, st, a);
+    constexpr int64_t kRows = 1 << 23;
+    for (int64_t r = 0; r < all.rows; r += kRows) {
+        Rows a = all;
+        a.X = static_cast<const E*>(all.X) + r * all.ldx;
+        a.rows = std::min(all.rows - r, kRows);
+        a.q += r * all.ldq;
+        a.scale += r;
+        // a wave a row up to 4096 columns (eight chunks of 64 lanes)
+        if (a.cols <= 4096) hipLaunchKernelGGL((k_i8_rows<E, 1, 8>), dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_i8_rows<E, 4, 8>), dim3((unsigned)a.rows), dim3(256), 0, st, a);
+    }
 }
 
 vq_status rows_codes(const Rows& a, int dtype, hipStream_t st)
@@ -655,6 +664,7 @@ Plan make_plan(int64_t T, int64_t M, int64_t N, int nm)
             const int bp = (small ? 128 : 256) / nm, bq = small ? 128 : 256;
             const int ntp = (int)((M + bp - 1) / bp), ntq = (int)((T + bq - 1) / bq);
             const int steps = (int)((round64(N) + 127) / 128), pairs = (steps + 1) / 2;
+            if (small && (int64_t)ntp * ntq >= 1 << 22) continue;     // a launch takes fewer than 2^32 threads
             for (int sp = 1; sp <= 16 && sp <= pairs; ++sp) {
                 const int64_t tiles = (int64_t)ntp * ntq * sp;
                 const double st = 2.0 * ((pairs + sp - 1) / sp);

@@ -54,6 +54,30 @@ def test_int8_rows_past_4_gb(T):
     assert bool((H[:, V - 1] == 2500.0).all()) and not bool(H[:, :V - 2].any())
 
 
+def test_more_tokens_than_one_launch_has_threads():
+    """2^32 threads: of the codes from 2^26 rows on, of small tiles from 2^23."""
+    T = (1 << 26) + 5
+    X = torch.ones((T, 2), dtype=torch.float16, device="cuda")
+    X[T - 1, 1], X[1 << 23, 0] = 0.5, -1.0
+    Q = vq.Int8Matrix(torch.tensor([[3, 4]], dtype=torch.int8, device="cuda"), torch.full((1,), 0.5, device="cuda"))
+    Y = vq.linear_i8(Q, X)[:, 0]
+    # the code of 0.5 beside 1 is 64 (63.5 to even): 127 * 3 + 64 * 4 over 127, halved
+    assert float(Y[T - 1]) == pytest.approx((127 * 3 + 64 * 4) / 254, rel=2.0 ** -10) and float(Y[1 << 23]) == 0.5
+    Y[T - 1], Y[1 << 23] = 3.5, 3.5
+    assert bool((Y == 3.5).all())
+
+
+def test_more_small_tiles_than_one_launch_takes():
+    T, M = 1 << 28, 193                                       # 104 GB of results
+    X = torch.ones((T, 1), dtype=torch.float16, device="cuda")
+    X[T - 1, 0], X[T // 2, 0] = 2.0, -2.0
+    q = torch.ones((M, 1), dtype=torch.int8, device="cuda")
+    Q = vq.Int8Matrix(q, torch.ones(M, device="cuda"))
+    H = vq.gated_i8(Q, Q, X, act="none")
+    assert bool((H[T - 1] == 4.0).all()) and bool((H[T // 2] == 4.0).all())
+    assert bool((H[:1 << 20] == 1.0).all()) and bool((H[T - 1 - (1 << 20):T - 1] == 1.0).all())
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_past_2_31_elements(bits):
     n = (1 << 31) + 4099
