@@ -888,6 +888,9 @@ int64_t piece(int64_t V, int64_t bytes_a_word)
     return std::min(up(up(V, n), 256) * 256, up(V, 8) * 8);
 }
 
+// Words of one launch: fewer than 2^32 threads also in small tiles.
+int64_t most_words(int64_t T) { return ((int64_t)1 << 22) / up(T, 128) * 128; }
+
 Tile tile_of(const void* P, int64_t ldp, int64_t kP, int64_t np, int64_t wp, const void* Q, int64_t ldq, int64_t kQ, int64_t nq,
              int64_t wq, const Shape& s)
 {
@@ -1077,7 +1080,7 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         Tokens tk;
         tk.take(ws, a);
         const bool copied = !loads_ok({a.W, a.V, a.N, a.ldw});
-        const int64_t Vp = copied ? piece(a.V, 2 * round8(a.N)) : a.V;
+        const int64_t Vp = copied ? std::min(piece(a.V, 2 * round8(a.N)), most_words(a.T)) : std::min(a.V, most_words(a.T));
         uint16_t* copy = copied ? static_cast<uint16_t*>(ws.take(Vp * round8(a.N) * 2)) : nullptr;
         const LogitsPlan plan = logits_plan(Vp, a.T, a.N, false);
         const Shape s = plan.s;

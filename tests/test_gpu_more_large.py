@@ -54,6 +54,28 @@ def test_int8_rows_past_4_gb(T):
     assert bool((H[:, V - 1] == 2500.0).all()) and not bool(H[:, :V - 2].any())
 
 
+def test_cross_entropy_of_the_most_tokens():
+    """2^20 tokens by more than 2^19 words: more tiles than one launch takes."""
+    T, words, n = 1 << 20, (1 << 19) + 1000, 8
+    g = torch.Generator().manual_seed(70)
+    X = torch.randn((T, n), generator=g).bfloat16().cuda()
+    W = torch.randn((words, n), generator=g).bfloat16().cuda()
+    labels = torch.randint(0, words, (T,), generator=g).cuda()
+    labels[::5] = -100
+    loss, lse = vq.cross_entropy(X, W, labels)
+    at = torch.tensor([0, 1, 2, 127, 128, T // 2 + 1, T - 2, T - 1])
+    z = X[at.cuda()].cpu().double() @ W.cpu().double().T
+    want = torch.logsumexp(z, 1)
+    for i, t in enumerate(at.tolist()):
+        if t % 5 == 0:
+            assert float(loss[t]) == 0.0 and float(lse[t]) == 0.0
+            continue
+        # products exact in float32 but for 8 additions of at most 128, exponents rounded to 2^-24 of at most 256
+        assert abs(float(lse[t]) - float(want[i])) <= 1e-4
+        assert abs(float(loss[t]) - float(want[i] - z[i, int(labels[t])])) <= 1e-4
+    assert bool(torch.isfinite(loss).all()) and bool((loss[labels != -100] > 0).all())
+
+
 def test_more_tokens_than_one_launch_has_threads():
     """2^32 threads: of the codes from 2^26 rows on, of small tiles from 2^23."""
     T = (1 << 26) + 5
