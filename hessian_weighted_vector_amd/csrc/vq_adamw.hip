@@ -417,7 +417,7 @@ static vq_status make_plan(const vq_adamw_tensor* tensors, int64_t count, int pa
             add(t.v_scale, blocks * 4, true);
         }
     }
-    VQ_CHECK(chunks < ((int64_t)1 << 31), call + ": more than 2^31 chunks of 4096 elements");
+    VQ_CHECK(chunks < ((int64_t)1 << 24), call + ": more than 2^24 chunks of 4096 elements");      // 2^32 threads
     // a tensor given twice, or two that overlap, would be stepped twice at once
     std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.a < y.a; });
     uintptr_t any = 0, written = 0;                           // ends of the ranges so far

@@ -1018,7 +1018,10 @@ class AdamW:
     elements.  `state` (a dict of lists m, v and, in 8 bits, m_scale, v_scale, as the
     attribute of that name holds them) and `steps` continue an earlier run; `state` is used
     in place.  capturable keeps the step's number (`steps`, int64) and the learning rate
-    (`lr`, float32) on the GPU: a captured step() replays as consecutive steps.
+    (`lr`, float32) on the GPU: a captured step() replays as consecutive steps, with the
+    gradients that it was given when captured, or without any with those of the last step.
+    Outside of a graph step() without gradients takes the last ones given outside of one.
+    The first gradients of a type are given outside of a capture.
     """
 
     BLOCK = 256
@@ -1058,8 +1061,8 @@ class AdamW:
         else:
             self.steps, self.lr = int(steps), float(lr)
         self.grads = None
-        self._plan = AdamWPlan()
-        self._ref = ctypes.addressof(self._plan)
+        self._tables = {}                                     # by the gradients' type: plan, table, its stream, gradients
+        self._captured = []                                   # gradients that graphs put into the tables
         if grads is not None:
             self._bind(grads)
 
@@ -1096,17 +1099,31 @@ class AdamW:
                 raise ValueError("%s[%d] must be contiguous" % (name, i))
 
     def _bind(self, grads):
-        """The table on the GPU with these gradients: made once, which waits for the stream, then changed in stream order."""
+        """A type's table on the GPU with these gradients: made once, which waits for the stream, then changed in stream order.
+
+        A graph may have been captured with any table: they stay, and what they point to.
+        """
         grads = list(grads)
         if not grads:
             raise ValueError("grads must have %d tensors" % len(self.params))
         code = _any_dtype(grads[0], "grads[0]")
         self._same(grads, grads[0].dtype, "grads")
+        n, captured = len(self.params), torch.cuda.is_current_stream_capturing()
+        if code in self._tables:
+            plan = self._tables[code][0]
+            _check(load().vq_adamw_grads(ctypes.addressof(plan), (_P * n)(*[g.data_ptr() for g in grads]), n, _stream()))
+        elif captured:
+            raise ValueError("the first gradients of a type must be given outside of a capture")
+        else:
+            plan = self._table(grads, code)
+        self._plan, self._ref = plan, ctypes.addressof(plan)
+        if captured:
+            self._captured.append(grads)
+        else:
+            self.grads = self._tables[code][3] = grads
+
+    def _table(self, grads, code):
         n = len(self.params)
-        if self.grads is not None and code == self._plan.grad_dtype:
-            _check(load().vq_adamw_grads(self._ref, (_P * n)(*[g.data_ptr() for g in grads]), n, _stream()))
-            self.grads = grads
-            return
         none = [None] * n
         s = self.state
         rows = (AdamWTensor * n)(*[
@@ -1120,7 +1137,8 @@ class AdamW:
         plan = AdamWPlan()
         _check(lib.vq_adamw_plan(rows, n, self.dtype, code, self.masters is not None, self.state_bits, table.data_ptr(), need,
                                  ctypes.addressof(plan), _stream()))
-        self.grads, self._table, self._plan, self._ref, self._bound = grads, table, plan, ctypes.addressof(plan), _stream()
+        self._tables[code] = [plan, table, _stream(), grads]
+        return plan
 
     def step(self, grads=None, grad_scale=None):
         """One step.  grads replace those of the last step; grad_scale: a float32 tensor of one element on
@@ -1129,14 +1147,17 @@ class AdamW:
             _elsewhere(self.params[0], "params[0]")
         if grads is not None:
             self._bind(grads)
-        if self.grads is None:
+        elif self.grads is None:
             raise ValueError("grads are needed")
+        elif self._captured:                                  # a replay may have put its own into the table
+            self._bind(self.grads)
         gs = None
         if grad_scale is not None:
             gs = _vector(grad_scale.reshape(-1), 1, torch.float32, self.index, "grad_scale")
         st = _stream()
-        if st != self._bound:                                 # the table's memory waits for this stream too
-            self._table.record_stream(torch.cuda.current_stream())
+        _, table, made_on, _ = self._tables[self._plan.grad_dtype]
+        if st != made_on:                                     # the table's memory waits for this stream too
+            table.record_stream(torch.cuda.current_stream())
         b1, b2 = self.betas
         if self.capturable:
             _check(load().vq_adamw(self._ref, 0.0, b1, b2, self.eps, self.weight_decay, 0, self.steps.data_ptr(),

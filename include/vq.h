@@ -617,7 +617,7 @@ vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, 
  * (device, vq_adamw_plan_bytes, 16-byte aligned) and the plan; it waits for the
  * stream, so it is made outside of a capture.  The plan is valid while
  * the tensors and the table stay where they are; several may be alive.  Tensors may not overlap, gradients
- * may overlap each other.  n = 0 is allowed.
+ * may overlap each other.  n = 0 is allowed; all chunks of 4096 elements together must be fewer than 2^24.
  *
  * vq_adamw_grads puts other gradients (host array of count device pointers, of the
  * tensors' sizes and the plan's type) into the table, in stream order and without waiting; it may

@@ -60,6 +60,11 @@ def test_plan_refuses_overlaps():
     assert st == vq.VQ_ERR_WORKSPACE
 
 
+def test_plan_refuses_too_many_elements():
+    st, text = plan([tensor(0, n=1 << 36)])
+    assert st == vq.VQ_ERR_INVALID and "chunks" in text
+
+
 def test_plan_sizes():
     lib = vq.load()
 

@@ -292,6 +292,70 @@ def test_new_gradients_every_step(captured):
         assert opt._plan.grad_dtype == 2
 
 
+def capture(step):
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        step()
+    return graph
+
+
+def signed(opt, f):
+    """The sign of a fresh element's step in f(): its gradient's, with moments of nothing."""
+    for k in ("m", "v"):
+        opt.state[k][0].zero_()
+    before = opt.params[0].clone()
+    f()
+    torch.cuda.synchronize()
+    return torch.sign(before - opt.params[0]).tolist()
+
+
+def test_eager_steps_beside_a_captured_one_with_its_own_gradients():
+    """The graph's gradients are the graph's: before and after replays step() takes those given outside of it."""
+    p = torch.zeros(2, device="cuda")
+    opt = vq.AdamW([p], [torch.tensor([1.0, -1.0], device="cuda")], weight_decay=0.0, capturable=True)
+    own = torch.tensor([-1.0, -1.0], device="cuda")
+    graph = capture(lambda: opt.step([own]))
+    assert signed(opt, opt.step) == [1, -1]
+    for _ in range(3):
+        assert signed(opt, graph.replay) == [-1, -1]
+        assert signed(opt, opt.step) == [1, -1]
+    opt.step([torch.tensor([1.0, 1.0], device="cuda")])
+    assert signed(opt, graph.replay) == [-1, -1]
+    assert signed(opt, opt.step) == [1, 1]
+
+
+def test_captured_step_keeps_its_table():
+    """Gradients of another type outside of the graph leave the table that it reads, and what that points to."""
+    p = torch.zeros(2, device="cuda")
+    opt = vq.AdamW([p], [torch.tensor([1.0, -1.0], device="cuda").bfloat16()], weight_decay=0.0, capturable=True)
+    graph = capture(opt.step)
+    for _ in range(3):
+        assert signed(opt, lambda: opt.step([torch.tensor([-1.0, 1.0], device="cuda")])) == [-1, 1]
+        # memory that a freed table or gradient would have left
+        junk = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in (16, 512, 1024, 2048) for _ in range(8)]
+        assert signed(opt, graph.replay) == [1, -1]
+        del junk
+
+
+def test_first_gradients_in_a_capture_are_refused():
+    opt = vq.AdamW([torch.zeros(2, device="cuda")], capturable=True)
+    x = torch.zeros(1, device="cuda")
+    g = torch.ones(2, device="cuda")
+
+    def step():
+        x.add_(1.0)
+        with pytest.raises(ValueError, match="outside of a capture"):
+            opt.step([g])
+
+    capture(step).replay()
+    torch.cuda.synchronize()
+    assert float(x) == 1.0 and int(opt.steps) == 0
+    opt.step([g])
+    assert int(opt.steps) == 1
+
+
 def test_large_tensor():
     """Past 2^24 elements: chunks and blocks keep their places."""
     n = (1 << 25) + 77
