@@ -5,7 +5,8 @@
 //   dz[t, v] = dloss_t (exp(z[t, v] - lse_t) - [v = label_t]),  dX = dz W,  dW = dz^T X
 //
 //   k_loss_index    the tokens that are learnt, one behind the other, and their labels
-//   k_loss_gather   their rows of X, 16-byte aligned (k_loss_index_gather: both)
+//   k_loss_gather   their rows of X, 16-byte aligned (k_loss_index_gather: both, and the copied rows
+//                   of W's first piece)
 //   k_loss_logits   the tiled product z; a wave's tile leaves of each token the largest
 //                   logit, the sum of exponentials below it, and the label's logit
 //   k_loss_few      the same for few tokens, the vocabulary read straight from memory
@@ -34,10 +35,10 @@
 // in bf16: all of them off by 0.0021).  In fp16 dz is also multiplied by 2^13, so that
 // probabilities down to 2^-27 keep the type's full precision.
 //
-// What bounds it: power, as the dense products.  4096 tokens of 4096 by 131072 words, bf16, 3.06
-// to 3.16 ms (1.39 to 1.44 PFLOP/s, matrix cores busy 0.78); the gradient of 2048 learnt tokens of
-// 2048, eight pieces of 124 us for dz (busy 0.60: the exponentials and stores of a tile are not
-// hidden) and 223 us for dX and dW (1.23 PFLOP/s).  One token by 32768 x 4096 50 us, bound by W's
+// What bounds it: power, as the dense products.  4096 tokens of 4096 by 131072 words, bf16, 3.04
+// to 3.16 ms (1.39 to 1.45 PFLOP/s, matrix cores busy 0.78); the gradient of 2048 learnt tokens of
+// 2048, eight pieces of 120 us for dz (busy 0.60: the exponentials and stores of a tile are not
+// hidden) and 211 us for dX and dW (1.30 PFLOP/s).  One token by 32768 x 4096 50 us, bound by W's
 // bytes.
 #include "vq_few.h"
 #include "vq_tile.h"

@@ -1116,7 +1116,7 @@ class AdamW:
             raise ValueError("the first gradients of a type must be given outside of a capture")
         else:
             plan = self._table(grads, code)
-        self._plan, self._ref = plan, ctypes.addressof(plan)
+        self._plan, self._ref, self._memory, self._made_on = plan, ctypes.addressof(plan), *self._tables[code][1:3]
         if captured:
             self._captured.append(grads)
         else:
@@ -1145,6 +1145,8 @@ class AdamW:
         the GPU that the gradients are multiplied by."""
         if self.index != _device():
             _elsewhere(self.params[0], "params[0]")
+        if not self.capturable and torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured step would replay as one and the same: capturable is needed")
         if grads is not None:
             self._bind(grads)
         elif self.grads is None:
@@ -1155,9 +1157,8 @@ class AdamW:
         if grad_scale is not None:
             gs = _vector(grad_scale.reshape(-1), 1, torch.float32, self.index, "grad_scale")
         st = _stream()
-        _, table, made_on, _ = self._tables[self._plan.grad_dtype]
-        if st != made_on:                                     # the table's memory waits for this stream too
-            table.record_stream(torch.cuda.current_stream())
+        if st != self._made_on:                               # the table's memory waits for this stream too
+            self._memory.record_stream(torch.cuda.current_stream())
         b1, b2 = self.betas
         if self.capturable:
             _check(load().vq_adamw(self._ref, 0.0, b1, b2, self.eps, self.weight_decay, 0, self.steps.data_ptr(),

@@ -356,6 +356,20 @@ def test_first_gradients_in_a_capture_are_refused():
     assert int(opt.steps) == 1
 
 
+def test_capture_without_capturable_is_refused():
+    p, x = torch.zeros(2, device="cuda"), torch.zeros(1, device="cuda")
+    opt = vq.AdamW([p], [torch.ones(2, device="cuda")])
+
+    def step():
+        x.add_(1.0)
+        with pytest.raises(ValueError, match="capturable"):
+            opt.step()
+
+    capture(step).replay()
+    torch.cuda.synchronize()
+    assert float(x) == 1.0 and opt.steps == 0 and not bool(p.any())
+
+
 def test_large_tensor():
     """Past 2^24 elements: chunks and blocks keep their places."""
     n = (1 << 25) + 77
