@@ -404,34 +404,51 @@ __global__ __launch_bounds__(1024) void k_loss_rows(const RowLoss a)
     const int q = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (q >= a.head->count) return;
     const int64_t row = (int64_t)q * a.pitch;
+    const int want = a.label[q], t = a.order[q];
+    const f32x4 zl = joined_sums(a.sums, a.splits, a.plane, row + (want < 0 ? 0 : want & ~3));       // the label's logit is among them
     float m = -INFINITY, s = 0.0f;
-    for (int p = threadIdx.x * 4; p < a.V; p += (int)blockDim.x * 4) {
-        const f32x4 z = joined_sums(a.sums, a.splits, a.plane, row + p);
-        float top = z[0], sum = 0.0f;
+    // four chunks of words in flight: one by one, each would wait for memory
+    constexpr int kAhead = 4;
+    const int stride = (int)blockDim.x * 4;
+    for (int p0 = threadIdx.x * 4; p0 < a.V; p0 += kAhead * stride) {
+        const float* at[kAhead];
+        f32x4 z[kAhead];
 #pragma unroll
-        for (int i = 1; i < 4; ++i) top = p + i < a.V ? fmaxf(top, z[i]) : top;
-        const float base = top == -INFINITY ? 0.0f : top;
+        for (int j = 0; j < kAhead; ++j) {
+            at[j] = a.sums + row + (p0 + j * stride < a.V ? p0 + j * stride : p0);
+            z[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll 2
+        for (int k = 0; k < a.splits; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += p + i < a.V ? exp_of(z[i] - base) : 0.0f;
-        join(m, s, top, sum);
+            for (int j = 0; j < kAhead; ++j) z[j] += *reinterpret_cast<const f32x4*>(at[j] + k * a.plane);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int p = p0 + j * stride;
+            if (p >= a.V) break;
+            float top = z[j][0], sum = 0.0f;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) top = p + i < a.V ? fmaxf(top, z[j][i]) : top;
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += p + i < a.V ? exp_of(z[j][i] - base) : 0.0f;
+            join(m, s, top, sum);
+        }
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o));
     if (lane == 0) sh[wave] = make_float2(m, s);
     __syncthreads();
-    if (threadIdx.x != 0) return;
-    m = sh[0].x;
-    s = sh[0].y;
-    for (int k = 1; k < (int)blockDim.x >> 6; ++k) join(m, s, sh[k].x, sh[k].y);
-    const int want = a.label[q];
+    if (wave != 0) return;
+    const bool in = lane < (int)blockDim.x >> 6;
+    m = in ? sh[lane & 15].x : -INFINITY;
+    s = in ? sh[lane & 15].y : 0.0f;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) join(m, s, __shfl_xor(m, o), __shfl_xor(s, o));
+    if (lane != 0) return;
     const float lse = m + logf(s);
-    float loss = NAN;
-    if (want >= 0) {
-        const f32x4 z = joined_sums(a.sums, a.splits, a.plane, row + (want & ~3));
-        loss = lse - (want & 2 ? (want & 1 ? z[3] : z[2]) : (want & 1 ? z[1] : z[0]));
-    }
-    a.loss[a.order[q]] = loss;
-    a.lse[a.order[q]] = lse;
+    a.loss[t] = want < 0 ? NAN : lse - (want & 2 ? (want & 1 ? zl[3] : zl[2]) : (want & 1 ? zl[1] : zl[0]));
+    a.lse[t] = lse;
 }
 
 template <class T>
@@ -1130,8 +1147,11 @@ vq_status forward(const Loss& a, Arena& ws, bool run, hipStream_t st)
         j.part = part; j.picked = picked;
         j.head = tk.head; j.order = tk.order;
     }
-    // one token by 32768 x 4096 (2048 parts): the call takes 49.8 us, 53.5 with 64 threads a token
+    // one token by 32768 x 4096 (2048 parts): the call takes 49.8 us, 53.5 with 64 threads a token; 48 and
+    // 128 tokens by 131072 words 9.4 and 9.2 us with 256 threads a token, 11.9 and 11.0 with 64; 512 by 32000 4.9
+    // and 5.4, 2048 by 131072 15.7 and 6.1
     if (few(a)) hipLaunchKernelGGL((k_loss_join<1>), dim3((unsigned)a.T), dim3(1024), 0, st, j);
+    else if (a.T <= 128) hipLaunchKernelGGL((k_loss_join<4>), dim3((unsigned)up(a.T, 4)), dim3(1024), 0, st, j);
     else hipLaunchKernelGGL((k_loss_join<16>), dim3((unsigned)up(a.T, 16)), dim3(1024), 0, st, j);
     VQ_LAUNCHED("k_loss_join");
     return VQ_OK;
