@@ -642,13 +642,23 @@ struct Plan {
     size_t part_bytes;
 };
 
+// Whether tokens are few: while the codes' products stay below 1.2e9 (one or two, which need no launch
+// in front, always).  Matrices from memory, few and tiles: 8192 x 8192 by 8 tokens 20.5 and 23.6 us,
+// by 17 26.2 and 24.4, by 32 32.7 and 25.6; pairs of it by 3 32.4 and 34.9, by 16 39.2 and 35.7;
+// 28672 x 8192 by 3 48.2 and 56.3, by 8 56.0 and 56.4, by 32 97 and 59; 8192 x 4096 by 32 21.9 and 21.0.
+// The rule is wrong for pairs of 11008 x 4096 by 16 (32.0, 37.9) and 2048 x 16384 by 16 (25.7, 20.7).
+bool few_tokens(int64_t T, int64_t M, int64_t N, int nm)
+{
+    return T <= 2 || (T <= 32 && (double)T * (double)M * (double)N * nm < 1.2e9);
+}
+
 // The tiled products' model of microseconds with steps of 128 columns.
 Plan make_plan(int64_t T, int64_t M, int64_t N, int nm)
 {
     Plan p{};
     p.pitch = (int)((M + 7) / 8 * 8);
     p.splits = 1;
-    if (T <= 32) {
+    if (few_tokens(T, M, N, nm)) {
         // Waves a workgroup of 16 rows, one token: 28672 x 8192 44.7 us with four and 47.0 with eight,
         // 4096 x 11008 14.4 with eight and 15.3 with sixteen, 2048 x 8192 11.0 and 10.1; pairs of 8192 x
         // 2048 12.3 with four and 11.4 with eight.  The columns are split over workgroups where even

@@ -201,6 +201,20 @@ def test_same_tokens_in_every_batch(M, N):
     within(whole[:64, rows], want, "rows")
 
 
+@pytest.mark.parametrize("T", [2, 3, 5, 17, 31])
+def test_few_tokens_of_large_matrices(T):
+    """Past the size at which few tokens go through tiles; odd sizes."""
+    M, N = 50001, 4099
+    g = torch.Generator().manual_seed(80)
+    Q, q, s = matrix(M, N, g)
+    X = values((T, N), torch.float16, g, scale=0.05)
+    Y, H = vq.linear_i8(Q, X), vq.gated_i8(Q, Q, X, act="none")
+    rows = torch.cat([torch.arange(5), torch.randint(0, M, (100,), generator=g), torch.arange(M - 20, M)]).cuda()
+    within(Y[:, rows], ref.linear(X, q[rows], s[rows], None, None, "none", torch.float16), "linear")
+    within(H[:, rows], ref.gated(X, q[rows], s[rows], q[rows], s[rows], None, None, "none", torch.float16), "gated")
+    assert torch.equal(vq.linear_i8(Q, X[:1]), Y[:1]) and torch.equal(vq.gated_i8(Q, Q, X[T - 1:], act="none"), H[T - 1:])
+
+
 @pytest.mark.parametrize("T", [1, 80])
 def test_captured_graphs_and_streams(T):
     g = torch.Generator().manual_seed(9)
