@@ -231,6 +231,7 @@ struct Logits {
     const Head* head;
     const int* label;
     int v0;
+    int turn;                    // workgroups begin at different steps
     // forward
     float2* part;                // [waves' columns of tiles][tokens]
     int64_t pitch;               // tokens a row of it
@@ -248,7 +249,7 @@ struct Logits {
 // The tile's sums; false where the grid's place holds none.  before(): what is to be under way
 // while the product runs.
 template <class L, class F>
-__device__ __forceinline__ bool logits_tile(const Tile& full, int n, int& p0, int& q0, int& tp, int wave, int lane, char* pb0,
+__device__ __forceinline__ bool logits_tile(const Tile& full, int turn, int n, int& p0, int& q0, int& tp, int wave, int lane, char* pb0,
                                             char* pb1, char* qb0, char* qb1, f32x4 (&acc)[L::kFP][L::kFQ], F before)
 {
     Tile t = full;
@@ -261,11 +262,20 @@ __device__ __forceinline__ bool logits_tile(const Tile& full, int n, int& p0, in
     q0 = tq * L::BQ;
     before();
     const int pairs = (t.steps + 1) / 2;
-    const int s0 = 2 * (int)((int64_t)pairs * blockIdx.y / t.splits), s1 = 2 * (int)((int64_t)pairs * (blockIdx.y + 1) / t.splits);
+    const int s0 = 2 * (int)((int64_t)pairs * blockIdx.y / t.splits);
+    int s1 = 2 * (int)((int64_t)pairs * (blockIdx.y + 1) / t.splits);
 #pragma unroll
     for (int i = 0; i < L::kFP; ++i)
 #pragma unroll
         for (int j = 0; j < L::kFQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (L::kFP * L::kFQ < 32) {
+        const int at = turn ? turned(s0, s1) : s0;
+        if (at > s0) {
+            L::run(t, p0, q0, 0, at, s1, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
+            run_again();
+            s1 = at;
+        }
+    }
     L::run(t, p0, q0, 0, s0, s1, wave, lane, (lds_ptr)pb0, (lds_ptr)pb1, (lds_ptr)qb0, (lds_ptr)qb1, acc);
     return true;
 }
@@ -285,7 +295,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_logits
     const auto stage = [&] {
         for (int i = threadIdx.x; i < L::BQ; i += kThreads) labels[i] = a.label[q0 + i < n ? q0 + i : n - 1];
     };
-    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc, stage)) return;
+    if (!logits_tile<L>(a.t, a.turn, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc, stage)) return;
     __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));               // no load into LDS outlives the workgroup
 
     // lane l: token l%16 of fragment j, words 4*(l/16) .. +3 of fragment i
@@ -364,7 +374,7 @@ __global__ __launch_bounds__(kThreads, FP * FQ >= 32 ? 2 : 4) void k_loss_grad(c
             gs[i] = a.g[q];
         }
     };
-    if (!logits_tile<L>(a.t, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc, stage)) return;
+    if (!logits_tile<L>(a.t, a.turn, n, p0, q0, tp, wave, lane, pb0, pb1, qb0, qb1, acc, stage)) return;
     each_row<L>(acc, p0, q0, (int)a.ldz, n, wave, lane, pb0, pb1, qb0, qb1, [&](int q, int p, float (&v)[8], float (&)[8]) {
         const float lse = lses[q - q0], g = gs[q - q0];
         const int want = labels[q - q0] - a.v0 - p;
@@ -1002,12 +1012,16 @@ vq_status words(const Loss& a, int64_t v0, int64_t n, uint16_t* copy, Mat& out, 
     return v0 > 0 ? Tokens::copy_piece(a, v0, n, copy, st) : VQ_OK;
 }
 
-// Whether the vocabulary is read for few tokens straight from memory.  One token by 131072 x 4096
-// 198 us here and 210 in tiles, sixteen 250 and 199; sixteen by 32768 x 4096 69 and 101, 32 74 and 83;
-// 32 by 17513 x 4570 87 and 106 (tiles need a copy of its rows), by 6400 x 7616 44 and 36.
+// Whether the vocabulary is read for few tokens straight from memory: while the products stay below
+// 1.6e9, and where tiles would need a copy of its rows.  Rows from memory, straight and in tiles: 131072 x
+// 4096 by two tokens 174 and 183 us, by eight 212 and 183; 65536 x 4096 by four 99 and 106, by sixteen 125 and
+// 106; 32768 x 4096 by nine 61 and 63, by 32 73 and 65; 32768 x 2048 by 32 40 and 41; 4096 x 4096 by 32 20
+// and 24; 2048 x 8192 by sixteen 21 and 24, by 32 32 and 25; 17513 x 4570 by 32 86 and 100.
 bool few(const Loss& a)
 {
-    return a.T <= 8 || (a.V * a.N < (int64_t)1 << 28 && (a.T <= 16 || (a.T <= 32 && a.N <= a.V)));
+    if (a.T <= 2 || a.T > 32) return a.T <= 2;
+    if (a.T > 16 && a.N > a.V) return false;
+    return !loads_ok({a.W, a.V, a.N, a.ldw}) || (double)a.T * (double)a.V * (double)a.N < 1.6e9;
 }
 
 // Waves that share the rows of W.  One token, by one, four and sixteen: 32768 x 4096 64, 58 and 57 us,
@@ -1059,10 +1073,13 @@ void few_logits(const FewLogits& f, bool odd, const FewPlan& p, hipStream_t st)
     else few_tokens_launch<T, 16>(f, odd, p, st);
 }
 
+// 64 tokens by 32768 x 4096, from memory, 80.4 us and 68.4 in turns, by 65536 x 4096 131 and 107; two rounds
+// of tiles, 131072 x 4096, 188 and 209.
 template <class T>
-void logits_launch(const Logits& g, const Shape& s, bool backward, hipStream_t st)
+void logits_launch(Logits g, const Shape& s, bool backward, hipStream_t st)
 {
     const dim3 grid((unsigned)(g.t.ntp * g.t.ntq), (unsigned)g.t.splits);
+    g.turn = s.small && in_turn(g.t);
     if (g.sums) backward = false;                             // dz comes of the joined sums
     if (s.small) {
         if (backward) hipLaunchKernelGGL((k_loss_grad<T, 4, 2>), grid, dim3(kThreads), 0, st, g);

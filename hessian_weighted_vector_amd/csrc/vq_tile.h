@@ -272,6 +272,26 @@ struct Main {
     }
 };
 
+// Few tokens against a matrix that is read once, by one round of workgroups (two small tiles a CU): all
+// of them walk its rows in step and ask a few memory channels at a time.  They begin at one of eight
+// places of their steps instead and come to the steps before it last.  The second start costs about as
+// much as a step or two, so runs of less than 16 steps are left as they are.
+__device__ __forceinline__ int turned(int s0, int s1)
+{
+    return s0 + 2 * ((s1 - s0) / 2 * (int)(((blockIdx.x + blockIdx.y * 3) / 8 + blockIdx.x) & 7) / 8);
+}
+inline bool in_turn(const Tile& t)
+{
+    return t.ntq == 1 && (int64_t)t.ntp * t.splits <= 512 && t.steps >= 16 * t.splits;
+}
+
+// Between two runs: every wave has read the buffers, and its last loads into them are there.
+__device__ __forceinline__ void run_again()
+{
+    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+    asm volatile("s_barrier" ::: "memory");
+}
+
 // The finished sums, eight consecutive features of a row at a time: f(q, p, v, u) for
 // features p .. p+7 of output row q (u: the second matrix's, of a pair), rows and
 // features past the last left out.  The wave turns two columns of fragments at a time

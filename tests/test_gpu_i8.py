@@ -215,6 +215,21 @@ def test_few_tokens_of_large_matrices(T):
     assert torch.equal(vq.linear_i8(Q, X[:1]), Y[:1]) and torch.equal(vq.gated_i8(Q, Q, X[T - 1:], act="none"), H[T - 1:])
 
 
+@pytest.mark.parametrize("T", [33, 100, 128])
+def test_one_round_of_tiles(T):
+    """Workgroups that begin at different steps: the sums of a token are those of it alone."""
+    M, N = 20001, 2100
+    g = torch.Generator().manual_seed(81)
+    Q, q, s = matrix(M, N, g)
+    X, R = values((T, N), torch.bfloat16, g), values((T, M), torch.bfloat16, g)
+    Y, H = vq.linear_i8(Q, X, residual=R), vq.gated_i8(Q, Q, X)
+    for t in (0, 31, T - 1):
+        assert torch.equal(vq.linear_i8(Q, X[t:t + 1], residual=R[t:t + 1]), Y[t:t + 1])
+        assert torch.equal(vq.gated_i8(Q, Q, X[t:t + 1]), H[t:t + 1])
+    rows = torch.cat([torch.randint(0, M, (100,), generator=g), torch.arange(M - 20, M)]).cuda()
+    within(Y[:, rows], ref.linear(X, q[rows], s[rows], None, R[:, rows], "none", torch.bfloat16), "linear")
+
+
 @pytest.mark.parametrize("T", [1, 80])
 def test_captured_graphs_and_streams(T):
     g = torch.Generator().manual_seed(9)

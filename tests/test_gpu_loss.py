@@ -62,6 +62,17 @@ def test_sizes(T, V, N, dtype):
     check(*inputs(T, V, N, dtype, T * 1000 + V))
 
 
+@pytest.mark.parametrize("T,V,N,dtype", [
+    (40, 40000, 1040, torch.bfloat16), (128, 33000, 2056, torch.float16), (70, 17000, 3000, torch.bfloat16),
+    (16, 40000, 2600, torch.float16), (9, 45000, 4096, torch.bfloat16), (20, 40001, 2601, torch.bfloat16)])
+def test_few_tokens_of_large_vocabularies(T, V, N, dtype):
+    """Where a round of workgroups reads the whole vocabulary, and where few tokens go through tiles."""
+    X, W, labels, dloss = inputs(T, V, N, dtype, V + T)
+    first = check(X, W, labels, dloss)
+    again = (*vq.cross_entropy(X, W, labels, ignore_index=IGN),)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 @pytest.mark.parametrize("ldx,ldw,offset", [(0, 1, 0), (1, 0, 0), (3, 5, 1), (8, 8, 8), (16, 0, 3)])
 @pytest.mark.parametrize("T", [5, 20, 70])
 def test_strides_and_alignment(T, ldx, ldw, offset):
