@@ -89,7 +89,7 @@ class Head:
     def backward(self, kept, scale=1.0):
         """(dX, dW) of scale times the mean loss; fp16 callers take a scale that keeps the gradients in range."""
         X, labels, lse, n, ignore_index = kept
-        dloss = torch.full((X.shape[0],), float(scale), device=X.device) / n
+        dloss = torch.full((X.shape[0],), float(scale), dtype=torch.float32, device=X.device) / n
         return vq.cross_entropy_backward(dloss, X, self.W, labels, lse, ignore_index)
 
 
@@ -143,7 +143,7 @@ def fine_tune(block, master, X, want, a, g):
     matrices; block's are their copies, and AdamW writes both.
     """
     N = X.shape[1]
-    teacher = torch.randn((a.vocab, N), generator=g, device="cuda") * N ** -0.5
+    teacher = torch.randn((a.vocab, N), generator=g, dtype=torch.float32, device="cuda") * N ** -0.5
     labels = (want.float() @ teacher.T).argmax(1)
     labels[:X.shape[0] // 4] = -100
     master["head"] = 0.5 * teacher
@@ -179,7 +179,7 @@ def main(argv=None):
     g = torch.Generator(device="cuda").manual_seed(0)
 
     def normal(scale, *shape):
-        return scale * torch.randn(shape, generator=g, device="cuda")
+        return scale * torch.randn(shape, generator=g, dtype=torch.float32, device="cuda")
 
     N, M, T = a.model, a.hidden, a.tokens
     names = ("Wg", "Wu", "Wd")

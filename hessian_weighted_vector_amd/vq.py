@@ -866,7 +866,7 @@ def quantize_rows(X):
     x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
     ldq = -(-N // 64) * 64
     q = torch.empty((T, ldq), dtype=torch.int8, device=X.device)
-    scale = torch.empty(T, device=X.device)
+    scale = torch.empty(T, dtype=torch.float32, device=X.device)
     _check(load().vq_quantize_rows(T, N, dt, x, ldx, q.data_ptr(), ldq, scale.data_ptr(), _stream()))
     return q[:, :N], scale
 
@@ -978,7 +978,7 @@ def cross_entropy(X, W, labels, ignore_index=-100, ws=None):
     x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
     w, ldw = _matrix(W, V, N, X.dtype, dev, "W")
     lab = _vector(labels, T, torch.int64, dev, "labels")
-    loss, lse = (torch.empty(T, device=X.device) for _ in range(2))
+    loss, lse = (torch.empty(T, dtype=torch.float32, device=X.device) for _ in range(2))
     lib = load()
     p, n, ws = _scratch(_cross_entropy_need(T, V, N, w & 15, ldw), ws, X, dev)
     _check(lib.vq_cross_entropy(T, V, N, dt, x, ldx, w, ldw, lab, ignore_index, loss.data_ptr(), lse.data_ptr(), p, n, _stream()))
@@ -1057,7 +1057,7 @@ class AdamW:
         self.capturable = bool(capturable)
         if capturable:
             self.steps = torch.full((1,), int(steps), dtype=torch.int64, device=dev)
-            self.lr = torch.full((1,), float(lr), device=dev)
+            self.lr = torch.full((1,), float(lr), dtype=torch.float32, device=dev)
         else:
             self.steps, self.lr = int(steps), float(lr)
         self.grads = None
@@ -1079,7 +1079,7 @@ class AdamW:
             flat = flat if self.state_bits == 32 else flat.view(torch.float8_e4m3fn)
             out[k] = [flat[s * self.BLOCK:s * self.BLOCK + p.numel()].view(p.shape) for s, p in zip(starts, self.params)]
             if self.state_bits == 8:
-                scale = torch.zeros(at, device=dev)
+                scale = torch.zeros(at, dtype=torch.float32, device=dev)
                 out[k + "_scale"] = [scale[s:s - (-p.numel() // self.BLOCK)] for s, p in zip(starts, self.params)]
         return out
 
