@@ -117,14 +117,17 @@ struct Top<float> {
 // one; so y with its last three bits rounded off is the tie where the quotient is one and on
 // the quotient's side of it elsewhere.  Adding 1.5 2^23 then rounds to an integer, ties to even,
 // whose low byte is the code.  Below 2^-90, where 127 / top could overflow, and for float32
-// elements, each is divided.
+// elements, each is divided: 127 x rounded, then the quotient rounded.  Rows above 2^120, where 127 x
+// could overflow, are taken 2^-7 times as large, which changes no code.
 template <class E>
 struct Coder {
-    float top, r;
+    float top, r, shrink;
     bool divide;
     __device__ __forceinline__ explicit Coder(uint32_t bits)
     {
         top = bits < 0x7f800000u ? __uint_as_float(bits) : 0.0f;
+        shrink = sizeof(E) == 4 && top > 0x1p120f ? 0x1p-7f : 1.0f;
+        top *= shrink;
         divide = sizeof(E) == 4 || (top > 0.0f && top < 0x1p-90f);
         r = top > 0.0f && !divide ? 127.0f / top : 0.0f;
     }
@@ -134,7 +137,7 @@ struct Coder {
         uint32_t k[8];
         if (divide) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) k[i] = top > 0.0f ? (uint32_t)__float2int_rn(127.0f * (float)e.v[i] / top) : 0u;
+            for (int i = 0; i < 8; ++i) k[i] = top > 0.0f ? (uint32_t)__float2int_rn(127.0f * ((float)e.v[i] * shrink) / top) : 0u;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

@@ -558,8 +558,8 @@ size_t vq_gated_i8_workspace_bytes(int64_t M, int64_t N, int64_t T);
 vq_status vq_gated_i8(const vq_i8matrix* Wg, const vq_i8matrix* Wu, int64_t T, int dtype, int act, const void* X, int64_t ldx,
                       const void* bg, const void* bu, void* H, int64_t ldh, void* ws, size_t ws_bytes, void* stream);
 
-/* The codes above of a matrix's rows (VQ_BF16, VQ_F16 or VQ_F32; of VQ_F32 the quotient is
- * rounded to float32 before it is brought to an integer): q [rows x cols] as in vq_i8matrix, with zeros
+/* The codes above of a matrix's rows (VQ_BF16, VQ_F16 or VQ_F32; of VQ_F32 127 X and then the
+ * quotient are rounded to float32 before it is brought to an integer): q [rows x cols] as in vq_i8matrix, with zeros
  * from cols to ldq, and scale[r] = top_r / 127 (NaN, with zero codes, where the row is not
  * finite).  cols <= 2^20. */
 vq_status vq_quantize_rows(int64_t rows, int64_t cols, int dtype, const void* X, int64_t ldx, int8_t* q, int64_t ldq,
