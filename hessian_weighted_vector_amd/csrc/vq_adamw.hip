@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <memory>
 #include <new>
 #include <type_traits>
 #include <vector>
@@ -332,6 +333,17 @@ struct Range {
     bool written;
 };
 
+// What new gradients are checked against: the tensors' sizes, and what a step writes, in order and apart.
+struct Known {
+    std::vector<int64_t> n;
+    std::vector<Range> written;
+    bool writes(uintptr_t a, uintptr_t b) const
+    {
+        const auto r = std::upper_bound(written.begin(), written.end(), a, [](uintptr_t at, const Range& w) { return at < w.b; });
+        return r != written.end() && r->a < b;
+    }
+};
+
 // VQ_CHECK=1: the values of n elements, in rows for the counting kernel.
 vq_status check_elements(const void* p, int64_t n, int dtype, const char* what, hipStream_t st)
 {
@@ -426,13 +438,17 @@ static vq_status make_plan(const vq_adamw_tensor* tensors, int64_t count, int pa
         any = std::max(any, r.b);
         if (r.written) written = std::max(written, r.b);
     }
-    *plan = vq_adamw_plan_t{nullptr, count, 0, param_dtype, grad_dtype, has_master ? 1 : 0, state_bits};
+    *plan = vq_adamw_plan_t{nullptr, count, 0, param_dtype, grad_dtype, has_master ? 1 : 0, state_bits, nullptr};
     if (chunks == 0) return VQ_OK;
     const size_t need = vq_adamw_plan_bytes(tensors, count);
     VQ_WS(table && table_bytes >= need, call + ": table too small");
     VQ_CHECK(aligned16(table), call + ": table is not 16-byte aligned");
     VQ_TRY(check_device());
     const size_t at_tensors = align_up(sizeof(Coefficients)), at_chunks = at_tensors + tensors_bytes(count);
+    std::unique_ptr<Known> known(new Known);
+    for (int64_t i = 0; i < count; ++i) known->n.push_back(tensors[i].n);
+    for (const Range& r : ranges)
+        if (r.written) known->written.push_back(r);
     std::vector<char> host(need);
     std::copy(tensors, tensors + count, reinterpret_cast<vq_adamw_tensor*>(host.data() + at_tensors));
     Chunk* c = reinterpret_cast<Chunk*>(host.data() + at_chunks);
@@ -442,6 +458,7 @@ static vq_status make_plan(const vq_adamw_tensor* tensors, int64_t count, int pa
     VQ_HIP(hipStreamSynchronize(as_stream(stream)));
     plan->table = table;
     plan->chunks = chunks;
+    plan->known = known.release();
     return VQ_OK;
 }
 
@@ -455,6 +472,13 @@ vq_status vq_adamw_plan(const vq_adamw_tensor* tensors, int64_t count, int param
     }
 }
 
+void vq_adamw_plan_free(vq_adamw_plan_t* plan)
+{
+    if (!plan) return;
+    delete static_cast<Known*>(plan->known);
+    plan->known = nullptr;
+}
+
 vq_status vq_adamw_grads(const vq_adamw_plan_t* plan, const void* const* grads, int64_t count, void* stream)
 {
     const std::string call = "vq_adamw_grads";
@@ -463,8 +487,17 @@ vq_status vq_adamw_grads(const vq_adamw_plan_t* plan, const void* const* grads, 
     VQ_CHECK(known(plan->grad_dtype) && plan->chunks >= 0 && (plan->chunks == 0 || plan->table), call + ": the plan is not made");
     if (plan->chunks == 0) return VQ_OK;
     VQ_CHECK(grads, call + ": grads is null");
+    const size_t size = size_of(plan->grad_dtype);
     for (int64_t i = 0; i < count; ++i)
-        VQ_CHECK(!off(grads[i], size_of(plan->grad_dtype)), call + ": gradient " + std::to_string(i) + " is not aligned to its elements");
+        VQ_CHECK(!off(grads[i], size), call + ": gradient " + std::to_string(i) + " is not aligned to its elements");
+    const Known* const known = static_cast<const Known*>(plan->known);
+    VQ_CHECK(known, call + ": the plan is not made, or was freed");
+    for (int64_t i = 0; i < count; ++i) {
+        if (known->n[i] == 0) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(grads[i]);
+        VQ_CHECK(at, call + ": gradient " + std::to_string(i) + " is null");
+        VQ_CHECK(!known->writes(at, at + known->n[i] * size), call + ": gradient " + std::to_string(i) + " overlaps what a step writes");
+    }
     VQ_TRY(check_device());
     vq_adamw_tensor* const tensors =
         reinterpret_cast<vq_adamw_tensor*>(static_cast<char*>(plan->table) + align_up(sizeof(Coefficients)));

@@ -10,6 +10,7 @@ import ctypes
 import functools
 import math
 import os
+import weakref
 
 import numpy as np
 import torch
@@ -79,7 +80,7 @@ class AdamWTensor(ctypes.Structure):
 
 class AdamWPlan(ctypes.Structure):
     _fields_ = [("table", _P), ("count", _I64), ("chunks", _I64), ("param_dtype", _I), ("grad_dtype", _I),
-                ("has_master", _I), ("state_bits", _I)]
+                ("has_master", _I), ("state_bits", _I), ("known", _P)]
 
 
 # name -> (restype, argtypes); every symbol declared in include/vq.h
@@ -144,6 +145,7 @@ SIGNATURES = {
                                        _P, _SZ, _P]),
     "vq_adamw_plan_bytes": (_SZ, [_P, _I64]),
     "vq_adamw_plan": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P, _P]),
+    "vq_adamw_plan_free": (None, [_P]),
     "vq_adamw_grads": (_I, [_P, _P, _I64, _P]),
     "vq_adamw": (_I, [_P, _D, _D, _D, _D, _D, _I64, _P, _P, _P, _P]),
     "vq_timing_enable": (None, [_I]),
@@ -1005,6 +1007,10 @@ def cross_entropy_backward(dloss, X, W, labels, lse, ignore_index=-100, want_dx=
 
 # ---- the optimizer's step -------------------------------------------------------
 
+def _free_plan(plan):
+    load().vq_adamw_plan_free(ctypes.addressof(plan))
+
+
 class AdamW:
     """AdamW over many tensors in one launch, in place.
 
@@ -1012,7 +1018,8 @@ class AdamW:
         p = (1 - lr wd) p - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 
     params: contiguous tensors of one type (bfloat16, float16 or float32); grads: of the same
-    sizes and of one type, kept by the caller and filled before each step, or given to step().
+    sizes and of one type, kept by the caller and filled before each step, or given to step();
+    they share no memory with what a step writes.
     masters: float32 tensors that hold the values of 16-bit params.  state_bits 8 keeps the
     moments as float8_e4m3fn codes of m and sqrt(v) with a float32 scale for each 256
     elements.  `state` (a dict of lists m, v and, in 8 bits, m_scale, v_scale, as the
@@ -1137,6 +1144,7 @@ class AdamW:
         plan = AdamWPlan()
         _check(lib.vq_adamw_plan(rows, n, self.dtype, code, self.masters is not None, self.state_bits, table.data_ptr(), need,
                                  ctypes.addressof(plan), _stream()))
+        weakref.finalize(self, _free_plan, plan)
         self._tables[code] = [plan, table, _stream(), grads]
         return plan
 

@@ -618,10 +618,13 @@ vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, 
  * stream, so it is made outside of a capture.  The plan is valid while
  * the tensors and the table stay where they are; several may be alive.  Tensors may not overlap, gradients
  * may overlap each other.  n = 0 is allowed; all chunks of 4096 elements together must be fewer than 2^24.
+ * The plan also holds the tensors' sizes and ranges in host memory, which vq_adamw_plan_free gives back (of a
+ * plan filled with zeros, nothing); steps read the table alone.
  *
  * vq_adamw_grads puts other gradients (host array of count device pointers, of the
  * tensors' sizes and the plan's type) into the table, in stream order and without waiting; it may
- * be captured.  A tensor of no elements may have NULL, others may not; gradients may not overlap what a step writes.
+ * be captured.  A tensor of no elements may have NULL; NULL for another and a gradient that overlaps what a step
+ * writes are refused, and nothing is changed then.
  *
  * vq_adamw is one step.  step counts from 1.  step_from (device int64, nullable)
  * holds the number of steps done, in place of step: the call adds one to it and takes
@@ -642,11 +645,13 @@ typedef struct {
     void* table;
     int64_t count, chunks;
     int param_dtype, grad_dtype, has_master, state_bits;
+    void* known;
 } vq_adamw_plan_t;
 
 size_t vq_adamw_plan_bytes(const vq_adamw_tensor* tensors, int64_t count);
 vq_status vq_adamw_plan(const vq_adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype, int has_master,
                         int state_bits, void* table, size_t table_bytes, vq_adamw_plan_t* plan, void* stream);
+void vq_adamw_plan_free(vq_adamw_plan_t* plan);
 vq_status vq_adamw_grads(const vq_adamw_plan_t* plan, const void* const* grads, int64_t count, void* stream);
 vq_status vq_adamw(const vq_adamw_plan_t* plan, double lr, double beta1, double beta2, double eps, double weight_decay,
                    int64_t step, int64_t* step_from, const float* lr_from, const float* grad_scale, void* stream);
