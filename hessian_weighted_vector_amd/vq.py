@@ -1028,7 +1028,8 @@ class AdamW:
     (`lr`, float32) on the GPU: a captured step() replays as consecutive steps, with the
     gradients that it was given when captured, or without any with those of the last step.
     Outside of a graph step() without gradients takes the last ones given outside of one.
-    The first gradients of a type are given outside of a capture.
+    The first gradients of a type are given outside of a capture.  Those of captured steps are
+    kept until release().
     """
 
     BLOCK = 256
@@ -1147,6 +1148,18 @@ class AdamW:
         weakref.finalize(self, _free_plan, plan)
         self._tables[code] = [plan, table, _stream(), grads]
         return plan
+
+    def release(self):
+        """Drops the gradients that captured steps were given: for when none of their graphs will replay again.
+
+        Until then each capture keeps its own, and a step() without gradients outside of a graph
+        puts the last ones given there back into the table first, one launch for each 448 tensors.
+        """
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("gradients are released outside of a capture")
+        if self._captured:
+            self._bind(self.grads)                            # the table may hold what is dropped
+            self._captured = []
 
     def step(self, grads=None, grad_scale=None):
         """One step.  grads replace those of the last step; grad_scale: a float32 tensor of one element on
