@@ -99,6 +99,8 @@ class Int8Block:
     def __init__(self, gate, up, down, act="silu"):
         if (up.M, up.N) != (gate.M, gate.N) or (down.M, down.N) != (gate.N, gate.M):
             raise ValueError("gate and up must be [M x N] and down [N x M]")
+        if gate._struct.ldq != up._struct.ldq:                # the pair's rows are read together
+            gate, up = gate.compact(), up.compact()
         self.gate, self.up, self.down, self.act = gate, up, down, act
 
     def forward(self, X):

@@ -898,6 +898,15 @@ class Int8Matrix:
         self._struct = I8MatrixStruct(M, N, q.data_ptr(), ld, scale.data_ptr())
         self._ref = ctypes.addressof(self._struct)
 
+    def compact(self):
+        """The matrix with its codes' rows as near as they can be (each begins at the next multiple of 64 bytes): itself, or a copy."""
+        ld = -(-self.N // 64) * 64
+        if self._struct.ldq == ld:
+            return self
+        copy = torch.empty((self.M, ld), dtype=torch.int8, device=self.q.device)
+        copy[:, :self.N].copy_(self.q)
+        return type(self)(copy[:, :self.N], self.scale)
+
     @classmethod
     def from_dense(cls, W):
         """From a dense matrix (bfloat16, float16 or float32), its rows brought to 8 bits."""
@@ -936,7 +945,10 @@ def linear_i8(Q, X, bias=None, residual=None, act="none", out=None, ws=None):
 
 
 def gated_i8(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None, ws=None):
-    """H = act(X Wg^T + bias_gate) * (X Wu^T + bias_up) with two Int8Matrix of one shape in one launch (tokens as in linear_i8)."""
+    """H = act(X Wg^T + bias_gate) * (X Wu^T + bias_up) with two Int8Matrix of one shape in one launch (tokens as in linear_i8).
+
+    Their codes' rows are equally far apart: with one kept in place in wider rows, take compact() of both.
+    """
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     T, M, N = X.shape[0], Q_gate.M, Q_gate.N
@@ -945,6 +957,8 @@ def gated_i8(Q_gate, Q_up, X, bias_gate=None, bias_up=None, act="silu", out=None
         _elsewhere(Q_gate.q, "Q_gate")
     if Q_up.index != dev:
         _elsewhere(Q_up.q, "Q_up")
+    if Q_gate._struct.ldq != Q_up._struct.ldq and (Q_up.M, Q_up.N) == (M, N):
+        raise ValueError("Q_gate and Q_up must have rows that are equally far apart: take compact() of both")
     x, ldx = _matrix(X, T, N, X.dtype, dev, "X")
     bg = _vector(bias_gate, M, X.dtype, dev, "bias_gate")
     bu = _vector(bias_up, M, X.dtype, dev, "bias_up")

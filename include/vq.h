@@ -540,6 +540,7 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
  * NaN or an infinity gives NaN in its whole row and changes no other.
  * q int8 [M x N]: rows begin every ldq bytes, a multiple of 64 and at most 2^22, q is 16-byte aligned, and
  * the bytes of a row from N to the next multiple of 64 are readable (of any value).
+ * Wg and Wu have the same M, N and ldq.
  * X [T x N], bias, bg, bu [M] (nullable), R [T x M] (nullable), Y, H [T x M] of one type
  * (VQ_BF16 or VQ_F16) with leading dimensions in elements, any alignment of elements.
  * 1 <= M <= 2^20, 1 <= N <= 2^17, 0 <= T <= 2^28; T = 0 is a no-op.  Y may be R itself (same address and
