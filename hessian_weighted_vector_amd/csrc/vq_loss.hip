@@ -30,7 +30,7 @@
 //
 // The logits and the sums of exponentials are float32; dz is rounded to the tensors'
 // type once, because the matrix cores read it in it.  Before, dloss is divided by its largest
-// magnitude, and dX and dW are multiplied by it: where every token has one weight, 1 / n say, its
+// finite magnitude, and dX and dW are multiplied by it: where every token has one weight, 1 / n say, its
 // rounding would otherwise be the same in every label's term, and the gradients' own (1 / 6927
 // in bf16: all of them off by 0.0021).  In fp16 dz is also multiplied by 2^13, so that
 // probabilities down to 2^-27 keep the type's full precision.
@@ -70,6 +70,13 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2)
     m = top;
 }
 
+// The magnitude where it is finite.  A dloss that is not has no part in what all are divided by.
+__device__ __forceinline__ float finite_size(float x)
+{
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.0f;
+}
+
 struct Index {
     const int64_t* labels;
     int64_t T, V, ignore;
@@ -100,7 +107,7 @@ __global__ __launch_bounds__(1024) void k_loss_index(const Index a)
     for (int64_t t = t0; t < t1; ++t) {
         const bool on = a.labels[t] != a.ignore;
         n += on;
-        if (a.g && on) top = fmaxf(top, fabsf(a.dloss[t]));
+        if (a.g && on) top = fmaxf(top, finite_size(a.dloss[t]));
     }
     int upto = n;
 #pragma unroll
@@ -118,7 +125,7 @@ __global__ __launch_bounds__(1024) void k_loss_index(const Index a)
         all += sums[w];
         top = fmaxf(top, tops[w]);
     }
-    if (!(top > 0.0f && top < INFINITY)) top = 1.0f;
+    if (top == 0.0f) top = 1.0f;
     if (threadIdx.x == 0) *a.head = Head{all, top / a.lift};
     for (int64_t t = t0; t < t1; ++t) {
         const int64_t l = a.labels[t];
@@ -194,7 +201,7 @@ __global__ __launch_bounds__(256) void k_loss_index_gather(const Index a, const 
     for (int i = threadIdx.x; i < end; i += 256) {
         const bool learnt = a.labels[i] != a.ignore;
         n += learnt && i < t;
-        if (a.g && learnt) top = fmaxf(top, fabsf(a.dloss[i]));
+        if (a.g && learnt) top = fmaxf(top, finite_size(a.dloss[i]));
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -208,7 +215,7 @@ __global__ __launch_bounds__(256) void k_loss_index_gather(const Index a, const 
     __syncthreads();
     const int at = counts[0] + counts[1] + counts[2] + counts[3];
     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    if (!(top > 0.0f && top < INFINITY)) top = 1.0f;
+    if (top == 0.0f) top = 1.0f;
     if (threadIdx.x == 0) {
         if (t == last) *a.head = Head{at + on, top / a.lift};
         if (on) {

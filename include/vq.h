@@ -586,7 +586,7 @@ vq_status vq_cross_entropy(int64_t T, int64_t V, int64_t N, int dtype, const voi
 /* Gradients of sum_t dloss[t] loss[t]:  dz[t,v] = dloss[t] (exp(z[t,v] - lse[t]) -
  * [v = labels[t]]) with z formed again and lse as vq_cross_entropy gave it,
  *   dX = dz W [T x N],  dW = dz^T X [V x N]  (each may be NULL).
- * dz enters the products divided by the largest |dloss| and rounded to the tensors' type, in fp16
+ * dz enters the products divided by the largest finite |dloss| and rounded to the tensors' type, in fp16
  * times 2^13, so that it keeps its precision down to 2^-27 of that; dX and dW are multiplied
  * back in float32.  Rows of dX of ignored tokens are zeros.
  * A label outside [0, V) makes its row of dX and all of dW NaN.  T = 0 writes a zero dW.
