@@ -223,6 +223,9 @@ Plan make_shape(GemmKind kind, int small, int64_t np, int64_t nq, int64_t K, int
     return p;
 }
 
+// A launch takes fewer than 2^32 threads; 256 x 256 tiles of what fits the memory stay below it.
+constexpr int64_t kMostTiles = (int64_t)1 << 23;
+
 size_t part_bytes(const Plan& p, int64_t nq, int nout)
 {
     return p.splits > 1 ? align_up((size_t)p.splits * nout * nq * p.pitch * sizeof(float)) : 0;
@@ -236,6 +239,7 @@ Plan make_plan(GemmKind kind, int64_t np, int64_t nq, int64_t K, int nseg, int n
     for (int small = 0; small < 2; ++small) {
         Plan p = make_shape(kind, small, np, nq, K, nseg);
         const int pairs = (p.steps + 1) / 2;
+        if (small && (int64_t)p.ntp * p.ntq >= kMostTiles) continue;
         for (int sp = 1; sp <= 16 && sp <= pairs; ++sp) {
             const int64_t tiles = (int64_t)p.ntp * p.ntq * nbatch * sp;
             const double st = 2.0 * ((pairs + sp - 1) / sp);
@@ -296,6 +300,7 @@ bool make_plans(const GemmSize& x, const GemmSize& w, Plan& px, Plan& pw)
         Plan b = make_shape(w.kind, small, w.np, w.nq, w.K, w.nseg);
         const int64_t ta = (int64_t)a.ntp * a.ntq, tb = (int64_t)b.ntp * b.ntq * w.nbatch;
         const int slots = small ? 512 : 256;
+        if (small && ta + tb >= kMostTiles - (1 << 20)) continue;     // the bias gradients' workgroups ride along
         for (int sa : kSplits) {
             if (sa > (a.steps + 1) / 2 || (sa > 1 && ta * sa > 2 * slots)) break;
             a.splits = sa;
