@@ -672,13 +672,17 @@ Plan make_plan(int64_t T, int64_t M, int64_t N, int nm)
     p.pitch = (int)((M + 7) / 8 * 8);
     p.splits = 1;
     if (few_tokens(T, M, N, nm)) {
-        // Waves a workgroup of 16 rows, one token: 28672 x 8192 44.7 us with four and 47.0 with eight,
-        // 4096 x 11008 14.4 with eight and 15.3 with sixteen, 2048 x 8192 11.0 and 10.1; pairs of 8192 x
-        // 2048 12.3 with four and 11.4 with eight.  The columns are split over workgroups where even
-        // sixteen waves a workgroup leave half of the CUs idle: 1024 x 16384 11.0 over four, 13.1 over two.
+        // Waves a workgroup of 16 rows, one token, matrices from memory.  At 512 groups of rows one matrix
+        // takes four and a pair eight: 8192 x 2048, 4096, 8192 and 28672 8.2, 11.2, 16.5 and 51.2 us with four,
+        // 8.5, 10.5, 16.4 and 53.5 with eight; pairs of 8192 x 2048, 4096 and 8192 12.2, 17.6 and 28.3 with four,
+        // 11.4, 17.3 and 28.5 with eight.  Above, both take four (28672 x 8192 44.7 and 47.0; pairs of 9216 x 4096
+        // 20.9 and 23.7); below, eight (7168 x 8192 15.3 and 15.6, pairs of it 26.5 and 26.3; 4096 x 11008 14.4
+        // with eight and 15.3 with sixteen) or, for few groups of long rows, sixteen (2048 x 8192 11.0 with eight
+        // and 10.1).  The columns are split over workgroups where even sixteen waves a workgroup leave half of the
+        // CUs idle: 1024 x 16384 11.0 over four, 13.1 over two.
         const int64_t groups = (M + 15) / 16, blocks = round64(N) / 512;
         p.few = 1;
-        p.waves = groups > (nm > 1 ? 512 : 511) ? 4 : groups >= 128 && groups < 256 && blocks >= 16 ? 16 : 8;
+        p.waves = groups >= (nm > 1 ? 513 : 512) ? 4 : groups >= 128 && groups < 256 && blocks >= 16 ? 16 : 8;
         while (p.splits < 16 && groups * p.splits < 128 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
         if (p.splits > 1 && groups * p.splits < 256 && blocks >= (int64_t)p.waves * p.splits * 2) p.splits *= 2;
     } else {
