@@ -337,10 +337,13 @@ struct Range {
 struct Known {
     std::vector<int64_t> n;
     std::vector<Range> written;
-    bool writes(uintptr_t a, uintptr_t b) const
+    // Whether a step writes between a and b.  `at` is the first range that ends behind a: where the last one
+    // asked for lay near, it is still that (searched for each of 1000 gradients, a step's call took 15 us more).
+    bool writes(uintptr_t a, uintptr_t b, size_t& at) const
     {
-        const auto r = std::upper_bound(written.begin(), written.end(), a, [](uintptr_t at, const Range& w) { return at < w.b; });
-        return r != written.end() && r->a < b;
+        if ((at > 0 && written[at - 1].b > a) || (at < written.size() && written[at].b <= a))
+            at = std::upper_bound(written.begin(), written.end(), a, [](uintptr_t x, const Range& w) { return x < w.b; }) - written.begin();
+        return at < written.size() && written[at].a < b;
     }
 };
 
@@ -492,11 +495,12 @@ vq_status vq_adamw_grads(const vq_adamw_plan_t* plan, const void* const* grads, 
         VQ_CHECK(!off(grads[i], size), call + ": gradient " + std::to_string(i) + " is not aligned to its elements");
     const Known* const known = static_cast<const Known*>(plan->known);
     VQ_CHECK(known, call + ": the plan is not made, or was freed");
+    size_t at = 0;
     for (int64_t i = 0; i < count; ++i) {
         if (known->n[i] == 0) continue;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(grads[i]);
-        VQ_CHECK(at, call + ": gradient " + std::to_string(i) + " is null");
-        VQ_CHECK(!known->writes(at, at + known->n[i] * size), call + ": gradient " + std::to_string(i) + " overlaps what a step writes");
+        const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+        VQ_CHECK(g, call + ": gradient " + std::to_string(i) + " is null");
+        VQ_CHECK(!known->writes(g, g + known->n[i] * size, at), call + ": gradient " + std::to_string(i) + " overlaps what a step writes");
     }
     VQ_TRY(check_device());
     vq_adamw_tensor* const tensors =
