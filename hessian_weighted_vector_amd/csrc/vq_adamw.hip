@@ -10,7 +10,7 @@
 // The plan is a table on the GPU: one entry a tensor and one a chunk of 4096
 // elements, so a workgroup finds its work in two dependent loads, however many
 // tensors there are, and no tensor's end leaves more than a part of one chunk idle.
-// Three tensors of 45.1 M elements (bf16, masters): 702 us (5.4 TB/s; a large copy reaches 4.9),
+// Three tensors of 45.1 M elements (bf16, masters): 700 us (5.4 TB/s; a large read reaches 6.2, a copy 4.9),
 // 411 us with 8-bit moments (5.3 TB/s); 256 of up to 8192 elements 5.8 to 6.2 us.
 //
 // 8-bit moments.  256 consecutive elements of a tensor share a float32 scale: m is kept

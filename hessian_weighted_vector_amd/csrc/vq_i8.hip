@@ -17,8 +17,8 @@
 // tie is at least 2^-19 of its value away from one, and the arithmetic rounds by 2^-23.
 //
 // What bounds it: a step of the tile loop takes as many cycles of LDS as of the matrix cores.
-// 4096 tokens by a pair of 28672 x 8192 1.38 to 1.45 ms (2.7 POP/s, matrix cores busy 0.72 at 1.8
-// GHz; 1.29 ms with zeros, so power is a tenth of it); 2048 by 4096 x 11008 101 to 110 us, 14 of
+// 4096 tokens by a pair of 28672 x 8192 1.38 to 1.46 ms (2.6 to 2.8 POP/s, matrix cores busy 0.72 at 1.8
+// GHz; 1.29 ms with zeros, so power is a tenth of it); 2048 by 4096 x 11008 101 to 111 us, 14 of
 // them the codes; one token 12 us, matrices from memory 14.4 (45 MB at the rate of a large read: 7.3).
 #include "vq_tile.h"
 

@@ -32,11 +32,11 @@
 // type once, because the matrix cores read it in it.  Before, dloss is divided by its largest
 // finite magnitude, and dX and dW are multiplied by it: where every token has one weight, 1 / n say, its
 // rounding would otherwise be the same in every label's term, and the gradients' own (1 / 6927
-// in bf16: all of them off by 0.0021).  In fp16 dz is also multiplied by 2^13, so that
+// in bf16: all of them off by 0.0025).  In fp16 dz is also multiplied by 2^13, so that
 // probabilities down to 2^-27 keep the type's full precision.
 //
 // What bounds it: power, as the dense products.  4096 tokens of 4096 by 131072 words, bf16, 3.04
-// to 3.16 ms (1.39 to 1.45 PFLOP/s, matrix cores busy 0.78); the gradient of 2048 learnt tokens of
+// to 3.22 ms (1.37 to 1.45 PFLOP/s, matrix cores busy 0.78); the gradient of 2048 learnt tokens of
 // 2048, eight pieces of 120 us for dz (busy 0.60: the exponentials and stores of a tile are not
 // hidden) and 211 us for dX and dW (1.30 PFLOP/s).  One token by 32768 x 4096 50 us, bound by W's
 // bytes.

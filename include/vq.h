@@ -543,8 +543,8 @@ vq_status vq_qgated(const vq_qmatrix* Qg, const vq_qmatrix* Qu, int64_t T, int d
  * Wg and Wu have the same M, N and ldq.
  * X [T x N], bias, bg, bu [M] (nullable), R [T x M] (nullable), Y, H [T x M] of one type
  * (VQ_BF16 or VQ_F16) with leading dimensions in elements, any alignment of elements.
- * 1 <= M <= 2^20, 1 <= N <= 2^17, 0 <= T <= 2^28; T = 0 is a no-op.  Y may be R itself (same address and
- * leading dimension); other overlaps are not allowed.  The workspace is as in the dense calls. */
+ * 1 <= M <= 2^20, 1 <= N <= 2^17, 0 <= T <= 2^28, T max(M, N) <= 2^38; T = 0 is a no-op.  Y may be R itself
+ * (same address and leading dimension); other overlaps are not allowed.  The workspace is as in the dense calls. */
 typedef struct {
     int64_t M, N;
     const int8_t* q;
@@ -630,7 +630,7 @@ vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, 
  * vq_adamw is one step.  step counts from 1.  step_from (device int64, nullable)
  * holds the number of steps done, in place of step: the call adds one to it and takes
  * the learning rate from lr_from (device, nullable) or lr, so that a captured
- * graph replays as consecutive steps.  grad_scale: device float32 or NULL (1). */
+ * graph replays as consecutive steps; it needs a plan with elements.  grad_scale: device float32 or NULL (1). */
 typedef struct {
     void* param;
     const void* grad;
