@@ -1169,6 +1169,8 @@ class AdamW:
         Until then each capture keeps its own, and a step() without gradients outside of a graph
         puts the last ones given there back into the table first, one launch for each 448 tensors.
         """
+        if self.index != _device():
+            _elsewhere(self.params[0], "params[0]")
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("gradients are released outside of a capture")
         if self._captured:

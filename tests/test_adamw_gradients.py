@@ -73,3 +73,14 @@ def test_a_freed_plan_takes_no_gradients():
     assert st == vq.VQ_ERR_INVALID and "freed" in text
     opt.step()                                                # the table is still there
     assert bool((opt.params[0] < -0.9).all())
+
+
+def test_release_on_another_gpu(monkeypatch):
+    """Like step(), refused before anything is launched."""
+    opt = object.__new__(vq.AdamW)
+    opt.params, opt.index, opt._captured, opt.grads = [torch.zeros(2)], 1, [[torch.zeros(2)]], [torch.zeros(2)]
+    monkeypatch.setattr(vq, "_device", lambda: 0)
+    monkeypatch.setattr(opt, "_bind", lambda grads: pytest.fail("launched"), raising=False)
+    with pytest.raises(ValueError, match="GPU"):
+        opt.release()
+    assert len(opt._captured) == 1
