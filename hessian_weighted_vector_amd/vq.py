@@ -1040,7 +1040,9 @@ class AdamW:
     attribute of that name holds them) and `steps` continue an earlier run; `state` is used
     in place.  capturable keeps the step's number (`steps`, int64) and the learning rate
     (`lr`, float32) on the GPU: a captured step() replays as consecutive steps, with the
-    gradients that it was given when captured, or without any with those of the last step.
+    gradients that it was given when captured, or without any with those of the last step before
+    each replay (captured after a step that was given its own: with the last ones given outside of
+    a graph until then).
     Outside of a graph step() without gradients takes the last ones given outside of one.
     The first gradients of a type are given outside of a capture.  Those of captured steps are
     kept until release().
@@ -1130,10 +1132,10 @@ class AdamW:
             raise ValueError("grads must have %d tensors" % len(self.params))
         code = _any_dtype(grads[0], "grads[0]")
         self._same(grads, grads[0].dtype, "grads")
-        n, captured = len(self.params), torch.cuda.is_current_stream_capturing()
+        captured = torch.cuda.is_current_stream_capturing()
         if code in self._tables:
             plan = self._tables[code][0]
-            _check(load().vq_adamw_grads(ctypes.addressof(plan), (_P * n)(*[g.data_ptr() for g in grads]), n, _stream()))
+            self._put(plan, grads)
         elif captured:
             raise ValueError("the first gradients of a type must be given outside of a capture")
         else:
@@ -1143,6 +1145,10 @@ class AdamW:
             self._captured.append(grads)
         else:
             self.grads = self._tables[code][3] = grads
+
+    def _put(self, plan, grads):
+        """Gradients into a plan's table, in stream order."""
+        _check(load().vq_adamw_grads(ctypes.addressof(plan), (_P * len(grads))(*[g.data_ptr() for g in grads]), len(grads), _stream()))
 
     def _table(self, grads, code):
         n = len(self.params)
@@ -1174,7 +1180,9 @@ class AdamW:
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("gradients are released outside of a capture")
         if self._captured:
-            self._bind(self.grads)                            # the table may hold what is dropped
+            for plan, _, _, grads in self._tables.values():   # each may hold what is dropped
+                self._put(plan, grads)
+            self._bind(self.grads)
             self._captured = []
 
     def step(self, grads=None, grad_scale=None):

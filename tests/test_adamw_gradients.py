@@ -84,3 +84,41 @@ def test_release_on_another_gpu(monkeypatch):
     with pytest.raises(ValueError, match="GPU"):
         opt.release()
     assert len(opt._captured) == 1
+
+
+def test_release_puts_back_the_gradients_of_every_type(monkeypatch):
+    """A graph of one type's table may replay when gradients of another type were the last ones."""
+    put = []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                if name == "vq_adamw_grads":
+                    put.append((args[0], list(args[1])))
+                return 0
+            return call
+
+    capturing = [False]
+    monkeypatch.setattr(vq, "load", Library)
+    monkeypatch.setattr(vq, "_home", lambda X, name="X": -1)
+    monkeypatch.setattr(vq, "_device", lambda: -1)
+    monkeypatch.setattr(vq, "_stream", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: None)
+    wide, half, own = (torch.zeros(300, dtype=t) for t in (torch.float32, torch.bfloat16, torch.float32))
+    opt = vq.AdamW([torch.zeros(300)], [wide], capturable=True)
+    plan_wide = opt._ref
+    opt.step([half])
+    plan_half = opt._ref
+    capturing[0] = True
+    opt.step([own])
+    capturing[0] = False
+    assert put == [(plan_wide, [own.data_ptr()])]
+    del put[:]
+    opt.release()
+    assert (plan_wide, [wide.data_ptr()]) in put and put[-1] == (plan_half, [half.data_ptr()])
+    assert opt._captured == [] and opt._ref == plan_half
+    del put[:]
+    opt.step()
+    opt.release()
+    assert put == []

@@ -76,3 +76,21 @@ def test_release_in_a_capture_is_refused():
     assert float(x) == 1.0
     opt.release()
     opt.step()
+
+
+def test_a_graph_that_stays_takes_the_gradients_of_its_type():
+    """Released beside a graph without gradients of its own, of another type than the last eager ones."""
+    opt = vq.AdamW([torch.zeros(2, device="cuda")], [torch.tensor([1.0, -1.0], device="cuda")], weight_decay=0.0, capturable=True)
+    stays = capture(opt.step)
+    own = torch.tensor([-1.0, 1.0], device="cuda")
+    goes = capture(lambda: opt.step([own]))
+    assert moved(opt, goes.replay) == [-1, 1] and moved(opt, stays.replay) == [-1, 1]
+    assert moved(opt, lambda: opt.step([torch.tensor([1.0, 1.0], device="cuda").bfloat16()])) == [1, 1]
+    del goes, own
+    opt.release()
+    gc.collect()
+    junk = [torch.full((2,), -1.0, device="cuda") for _ in range(64)]
+    for _ in range(2):
+        assert moved(opt, stays.replay) == [1, -1]
+        assert moved(opt, opt.step) == [1, 1]
+    assert len(junk) == 64
