@@ -619,8 +619,8 @@ vq_status vq_cross_entropy_backward(int64_t T, int64_t V, int64_t N, int dtype, 
  * stream, so it is made outside of a capture.  The plan is valid while
  * the tensors and the table stay where they are; several may be alive.  Tensors may not overlap, gradients
  * may overlap each other.  n = 0 is allowed; all chunks of 4096 elements together must be fewer than 2^24.
- * The plan also holds the tensors' sizes and ranges in host memory, which vq_adamw_plan_free gives back (of a
- * plan filled with zeros, nothing); steps read the table alone.
+ * The plan also holds the tensors' sizes and ranges in host memory (copies of a plan share it), which
+ * vq_adamw_plan_free gives back (of a plan filled with zeros, nothing); steps read the table alone.
  *
  * vq_adamw_grads puts other gradients (host array of count device pointers, of the
  * tensors' sizes and the plan's type) into the table, in stream order and without waiting; it may
